@@ -307,6 +307,7 @@ def measure_l2_gbs(torch, nbytes=32 << 20, reps=10, trials=5):
 # traffic figure is keyed by their digest, so it stays valid while that
 # kernel's code is unchanged.
 _COMMON = ["tma.cuh", "exact_math.cuh", "io_types.cuh", "rnn_internal.h"]
+_SSM = ["ssm_math.cuh", "ssm_internal.h"]
 KERNEL_SOURCES = {
     "rnn_recurrent_kernel": ["k_recur.cuh", "k_recur_rnn.cu", "k_recur_gru.cu", "k_recur_lstm.cu"] + _COMMON,
     "rnn_dataflow_kernel": ["k_recur.cuh", "k_recur2.cuh", "k_recur_rnn.cu", "k_recur_gru.cu", "k_recur_lstm.cu",
@@ -317,6 +318,9 @@ KERNEL_SOURCES = {
     "proj_tma_kernel": ["k_proj.cu", "exact_math.cuh", "tma.cuh", "rnn_internal.h"],
     "proj_tc_kernel": ["k_proj_tc.cu", "tma.cuh", "rnn_internal.h"],
     "rnn_cell_kernel": ["k_cell.cu", "exact_math.cuh", "rnn_internal.h"],
+    "ssm_conv_kernel": ["k_ssm_conv.cu", "ssm_api.cpp"] + _SSM,
+    "ssm_scan_kernel": ["k_ssm_scan.cu", "ssm_api.cpp"] + _SSM,
+    "scores_kernel": ["k_scores.cu", "ssm_api.cpp"] + _SSM,
 }
 
 

@@ -1,6 +1,7 @@
 /*
  * onnx_recurrent.h -- C ABI of the GB300 (sm_103a) ONNX RNN / GRU / LSTM
- * sequence operator.
+ * sequence operator, and of the state space and token score operators of
+ * recurrent language models (their own sections below).
  *
  * The operator is the one defined by the page "Recurrent operators: RNN, GRU,
  * LSTM" (sections Support, Computation, Activations, Choices the specification
@@ -385,6 +386,232 @@ rnn_status rnn_cell_plan_create(rnn_plan_t* out, int64_t hidden_size, int64_t in
                                 const char* activation, float clip);
 rnn_status rnn_cell_run(rnn_plan_t plan, int64_t batch_size, const float* X, const float* H,
                         const float* W, const float* R, const float* B, float* Ho, void* stream);
+
+/* ------------------------------------------------- state space layers
+ * Operators of a gated state space layer: a short causal convolution over
+ * time, the selective scan behind it, their gradients, and their forms for
+ * single tokens.  With D channels, M states per channel, G groups of D / G
+ * neighbouring channels that share B and C, and K taps, every row n of the
+ * batch runs steps t = 0 .. len_n - 1 (len_n = seq_length without
+ * sequence_lens):
+ *
+ *   conv   Y[t,d]   = f(bias[d] + sum_k W[d,k] * X[t-K+1+k,d])
+ *          where X[-K+1 .. -1] is the carried state (zeros without one) and
+ *          f is the identity or silu(v) = v / (1 + exp(-v));
+ *   scan   delta    = softplus(dt[t,d] + dt_bias[d])   (or the sum itself)
+ *          h[t,d,m] = exp(delta * A[d,m]) * h[t-1,d,m] + delta * B[t,g,m] * X[t,d]
+ *          y[t,d]   = sum_m C[t,g,m] * h[t,d,m] + Dskip[d] * X[t,d]
+ *          Y[t,d]   = y[t,d] * silu(Z[t,d])             (or y itself)
+ *          where h[-1] is initial_h (zeros without one).
+ *
+ * Steps t >= len_n of a row write zeros to Y (and to every gradient of a
+ * step) and leave the state as it was.  All sums, states and gradients are
+ * held in fp32; X, dt, B, C, Z, the convolution's state, Y and their
+ * gradients are stored in the plan's io type (RNN_IO_*, default F32), each
+ * rounded to nearest even once; A, Dskip, dt_bias, W, bias, h and their
+ * gradients are fp32.
+ *
+ * rnn_view: a tensor [seq, batch, ...] whose innermost part (the D channels,
+ * or the G x M values of B and C) is dense; the strides of a step and of a
+ * batch row are in elements, so a view may be a part of a wider tensor.  Both
+ * strides zero: dense, in the plan's layout (0: [seq, batch, ...], 1:
+ * [batch, seq, ...]).  Output views must not overlap themselves or an input.
+ *
+ * Calls are stream-ordered and asynchronous and allocate nothing but the
+ * plan's scratch (grown with cudaMalloc when a call needs more, so make a
+ * call of that size before a stream capture).  A plan is not re-entrant; its
+ * calls may use different streams (a call that needs the scratch waits for
+ * the previous one's use of it).  A length outside [0, seq_length] or a slot
+ * outside its range is found by the kernels: the length is clamped, the slot
+ * skipped, and rnn_ssm_sync reports RNN_ERR_INVALID_INPUT.  This differs from
+ * rnn_run, which reads the lengths back first: a layer's calls follow one
+ * another without a wait. */
+typedef struct rnn_ssm* rnn_ssm_t;
+typedef struct {
+    void* data;
+    int64_t seq_stride, batch_stride;
+} rnn_view;
+
+/* Create a plan (no device work; callable without a GPU).
+ *   channels      D > 0;  state_size M in [1, 128];  groups G > 0 divides D;
+ *   conv_width    K in [1, 8];
+ *   layout        0 or 1 (dense views only);
+ *   conv_silu     1: f is silu, 0: the identity;
+ *   dt_softplus   1: delta is the softplus, 0: the sum itself.
+ * Anything else is RNN_ERR_INVALID_ARGUMENT. */
+rnn_status rnn_ssm_create(rnn_ssm_t* out, int64_t channels, int64_t state_size, int64_t groups, int64_t conv_width,
+                          int layout, int conv_silu, int dt_softplus);
+void rnn_ssm_destroy(rnn_ssm_t plan);
+rnn_status rnn_ssm_set_io_type(rnn_ssm_t plan, int io);
+/* Wait for the device and report (and clear) the status that the plan's calls
+ * left: RNN_OK, or RNN_ERR_INVALID_INPUT (see above). */
+rnn_status rnn_ssm_sync(rnn_ssm_t plan);
+/* Kernels that the plan's last call queued. */
+int rnn_ssm_last_launch_count(rnn_ssm_t plan);
+
+/* Arguments are plain structures whose fields are all 8 bytes wide. */
+typedef struct {
+    int64_t seq_length, batch_size;
+    rnn_view X;
+    const float* W;                /* [D, K] */
+    const float* bias;             /* [D], or NULL */
+    const int32_t* sequence_lens;  /* [N], or NULL */
+    const void* initial_state;     /* [N, K-1, D] oldest first, io type, or NULL */
+    rnn_view Y;                    /* out */
+    void* final_state;             /* out [N, K-1, D]: the last K-1 inputs of each row, or NULL */
+    void* stream;
+} rnn_ssm_conv_args;
+rnn_status rnn_ssm_conv(rnn_ssm_t plan, const rnn_ssm_conv_args* args);
+
+/* Gradients of the convolution: dY (required) and d_final_state (or NULL) are
+ * the loss's slopes in the outputs; dX, dW, dbias and d_initial_state (each
+ * may be NULL, dX by its data) are overwritten.  Sums over steps and rows are taken in a
+ * fixed order: the same inputs give the same bits. */
+typedef struct {
+    int64_t seq_length, batch_size;
+    rnn_view dY, X;
+    const float* W;
+    const float* bias;
+    const int32_t* sequence_lens;
+    const void* initial_state;
+    const void* d_final_state;
+    rnn_view dX;
+    float* dW;
+    float* dbias;
+    void* d_initial_state;
+    void* stream;
+} rnn_ssm_conv_grad_args;
+rnn_status rnn_ssm_conv_grad(rnn_ssm_t plan, const rnn_ssm_conv_grad_args* args);
+
+/* One token of each row: X and Y [N, D] (rows a batch_stride apart, 0: dense;
+ * seq_stride is not used).  Row n's state is state[slots[n]] ([slots, K-1, D];
+ * without slots state[n]); the new one goes to the same slot of state_out,
+ * which may be state itself.  A row of slot -1 is padding: its Y is zero and
+ * no state is touched.  Slots of one call must differ from one another (two
+ * rows on one slot race). */
+typedef struct {
+    int64_t batch_size, n_slots;   /* n_slots: slots of state (read with slots only) */
+    rnn_view X;
+    const float* W;
+    const float* bias;
+    const void* state;
+    void* state_out;
+    const int32_t* slots;          /* [N], or NULL */
+    rnn_view Y;
+    void* stream;
+} rnn_ssm_conv_step_args;
+rnn_status rnn_ssm_conv_step(rnn_ssm_t plan, const rnn_ssm_conv_step_args* args);
+
+typedef struct {
+    int64_t seq_length, batch_size;
+    rnn_view X, dt, B, C, Z;       /* Z.data may be NULL: no gate */
+    const float* A;                /* [D, M] */
+    const float* Dskip;            /* [D], or NULL */
+    const float* dt_bias;          /* [D], or NULL */
+    const int32_t* sequence_lens;  /* [N], or NULL */
+    const float* initial_h;        /* [N, D, M], or NULL */
+    rnn_view Y;                    /* out */
+    float* Y_h;                    /* out [N, D, M]: the state after each row's last step, or NULL */
+    float* saved;                  /* out, rnn_ssm_saved_size floats for rnn_ssm_scan_grad, or NULL */
+    void* stream;
+} rnn_ssm_scan_args;
+rnn_status rnn_ssm_scan(rnn_ssm_t plan, const rnn_ssm_scan_args* args);
+/* Floats of `saved` for a run of this size (-1 for invalid arguments). */
+int64_t rnn_ssm_saved_size(rnn_ssm_t plan, int64_t seq_length, int64_t batch_size);
+
+/* Gradients of the scan: dY (required) and dY_h (or NULL) are the loss's
+ * slopes in the outputs, `saved` comes from rnn_ssm_scan on the same inputs.
+ * dX, ddt, dB, dC, dZ (views; dZ only with Z) and dA, dDskip, ddt_bias,
+ * d_initial_h are overwritten; each may be NULL.  dB and dC sum over the
+ * channels of a group, dA, dDskip and ddt_bias over steps and rows, all in a
+ * fixed order: the same inputs give the same bits. */
+typedef struct {
+    int64_t seq_length, batch_size;
+    rnn_view dY, X, dt, B, C, Z;
+    const float* A;
+    const float* Dskip;
+    const float* dt_bias;
+    const int32_t* sequence_lens;
+    const float* initial_h;
+    const float* saved;
+    const float* dY_h;
+    rnn_view dX, ddt, dB, dC, dZ;
+    float* dA;
+    float* dDskip;
+    float* ddt_bias;
+    float* d_initial_h;
+    void* stream;
+} rnn_ssm_scan_grad_args;
+rnn_status rnn_ssm_scan_grad(rnn_ssm_t plan, const rnn_ssm_scan_grad_args* args);
+
+/* One token of each row: views hold [N, ...] (batch_stride, 0: dense).  Row
+ * n's state is H[slots[n]] ([slots, D, M]; without slots H[n]), the new one
+ * goes to the same slot of H_out, which may be H itself; slots as in
+ * rnn_ssm_conv_step. */
+typedef struct {
+    int64_t batch_size, n_slots;
+    rnn_view X, dt, B, C, Z;
+    const float* A;
+    const float* Dskip;
+    const float* dt_bias;
+    const float* H;
+    float* H_out;
+    const int32_t* slots;
+    rnn_view Y;
+    void* stream;
+} rnn_ssm_scan_step_args;
+rnn_status rnn_ssm_scan_step(rnn_ssm_t plan, const rnn_ssm_scan_step_args* args);
+
+/* ----------------------------------------------------- token scores
+ * Scores of rows of logits x[V] (one row per position; io type RNN_IO_*, rows
+ * row_stride elements apart, 0: V): with lse = log sum_i exp(x_i),
+ *   logp     = x[id] - lse           of the given token id,
+ *   entropy  = -sum_i p_i log p_i    with p_i = exp(x_i - lse),
+ *   top      the `top` (0 .. 32, at most V) largest logits' places, largest
+ *            first, ties to the lowest place, and their log probabilities.
+ * A negative id stands for no token: logp is 0 (and gives no gradient); an id
+ * >= V gives logp NaN.  A logit of -inf has probability 0 and adds nothing to
+ * the entropy; a row of nothing but -inf has lse = -inf, every log
+ * probability -inf, entropy 0 and zero gradients; a row with a NaN or +inf
+ * has NaN scores (a NaN ranks above +inf, +0 and -0 tie).
+ * ids (with logp), logp, entropy, lse, top_ids and top_logp (with top > 0)
+ * are each optional. */
+typedef struct {
+    int64_t rows, vocab, row_stride, io;
+    const void* logits;
+    const int32_t* ids;            /* [rows] */
+    int64_t top;
+    float* logp;                   /* out [rows] */
+    float* entropy;                /* out [rows] */
+    float* lse;                    /* out [rows] */
+    int32_t* top_ids;              /* out [rows, top] */
+    float* top_logp;               /* out [rows, top] */
+    void* stream;
+} rnn_scores_args;
+rnn_status rnn_scores(const rnn_scores_args* args);
+
+/* Gradient of the scores in the logits, from the slopes d_logp [rows],
+ * d_entropy [rows] and d_top [rows, top] (each may be NULL) and what
+ * rnn_scores wrote (lse; entropy with d_entropy; top_ids with d_top):
+ *   dlogits[i] = d_logp * (i == id) + sum_j d_top[j] * (i == top_ids[j])
+ *              - (d_logp + sum_j d_top[j]) * p_i - d_entropy * p_i * (log p_i + entropy).
+ * dlogits (io type, its own row stride, 0: V) may be the logits themselves. */
+typedef struct {
+    int64_t rows, vocab, row_stride, io;
+    const void* logits;
+    const int32_t* ids;
+    const float* lse;
+    const float* entropy;
+    const float* d_logp;
+    const float* d_entropy;
+    int64_t top;
+    const int32_t* top_ids;
+    const float* d_top;
+    void* dlogits;
+    int64_t d_row_stride;
+    void* stream;
+} rnn_scores_grad_args;
+rnn_status rnn_scores_grad(const rnn_scores_grad_args* args);
 
 /* Message of the last failing call on this thread ("" if none). */
 const char* rnn_last_error(void);

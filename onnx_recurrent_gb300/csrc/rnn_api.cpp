@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "rnn_internal.h"
+#include "ssm_internal.h"
 
 namespace rnngb {
 cudaError_t launch_recurrent_rnn(const RecParams&, bool, int, size_t, cudaStream_t);
@@ -2101,6 +2102,8 @@ rnn_status rnn_run_static_scratch(rnn_plan_t pl, int64_t S, int64_t N, const flo
 }  // extern "C"
 
 namespace rnngb {
+
+void set_last_error(const char* message) { g_error = message; }
 
 bool encode_tensor_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
                        const cuuint64_t* strides, const cuuint32_t* box, bool swizzle128, int dtype)

@@ -1,0 +1,127 @@
+// Shared by the state space and token score entry points (ssm_api.cpp) and
+// their kernels.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace rnngb {
+
+void set_last_error(const char* message);   // rnn_last_error's text (this thread)
+
+// A [seq, batch, ...] tensor with a dense innermost part; strides in elements.
+struct View {
+    void* data = nullptr;
+    int64_t ss = 0, bs = 0;
+};
+
+// One state per kSsmTile steps is saved by the scan for its gradient, and
+// the gradient works through a row in tiles of that many steps.
+constexpr int kSsmTile = 16;
+constexpr int kSsmMaxState = 128;
+constexpr int kSsmMaxTaps = 8;
+constexpr int kMaxTop = 32;
+
+struct ConvParams {
+    int64_t S, N, D;
+    int K, io, silu;
+    View X, Y;
+    const float *W, *bias;
+    const int32_t* lens;
+    const void* h0;         // [N, K-1, D]
+    void* hT;
+    int* status;
+};
+
+struct ConvGradParams {
+    ConvParams f;           // Y and hT unused
+    View dY, dX;
+    const void* dhT;
+    void* dh0;
+    float *dW, *dbias;
+    float* part;            // [parts, D * K + D]
+    int64_t parts;
+};
+
+struct ConvStepParams {
+    int64_t N, D, slots_n;
+    int K, io, silu;
+    View X, Y;
+    const float *W, *bias;
+    const void* state;
+    void* state_out;
+    const int32_t* slots;
+    int* status;
+};
+
+struct ScanParams {
+    int64_t S, N, D;
+    int M, G, io, softplus;
+    View X, dt, B, C, Z, Y;
+    const float *A, *Dskip, *dt_bias;
+    const int32_t* lens;
+    const float* h0;
+    float* hT;
+    float* saved;
+    int* status;
+};
+
+struct ScanGradParams {
+    ScanParams f;           // Y and hT unused
+    View dY, dX, ddt, dB, dC, dZ;
+    const float* dhT;
+    float *dA, *dDskip, *ddt_bias, *dh0;
+    float* part;            // scratch (scan_grad_scratch)
+};
+
+struct ScanStepParams {
+    int64_t N, D, slots_n;
+    int M, G, io, softplus;
+    View X, dt, B, C, Z, Y;
+    const float *A, *Dskip, *dt_bias, *H;
+    float* H_out;
+    const int32_t* slots;
+    int* status;
+};
+
+struct ScoreParams {
+    int64_t rows, V, stride;
+    int io, top;
+    const void* x;
+    const int32_t* ids;
+    float *logp, *entropy, *lse;
+    int32_t* top_ids;
+    float* top_logp;
+};
+
+struct ScoreGradParams {
+    int64_t rows, V, stride, d_stride;
+    int io, top;
+    const void* x;
+    const int32_t* ids;
+    const float *lse, *entropy, *d_logp, *d_entropy;
+    const int32_t* top_ids;
+    const float* d_top;
+    void* dx;
+};
+
+// Each launcher queues its kernels on `s` and adds their number to *launches.
+cudaError_t launch_ssm_conv(const ConvParams& p, cudaStream_t s, int* launches);
+int64_t ssm_conv_grad_parts(const ConvGradParams& p);
+cudaError_t launch_ssm_conv_grad(const ConvGradParams& p, cudaStream_t s, int* launches);
+cudaError_t launch_ssm_conv_step(const ConvStepParams& p, cudaStream_t s, int* launches);
+int64_t ssm_saved_floats(int64_t S, int64_t N, int64_t D, int64_t M);
+cudaError_t launch_ssm_scan(const ScanParams& p, cudaStream_t s, int* launches);
+size_t ssm_scan_grad_scratch(const ScanGradParams& p);
+cudaError_t launch_ssm_scan_grad(const ScanGradParams& p, cudaStream_t s, int* launches);
+cudaError_t launch_ssm_scan_step(const ScanStepParams& p, cudaStream_t s, int* launches);
+cudaError_t launch_scores(const ScoreParams& p, cudaStream_t s, int* launches);
+cudaError_t launch_scores_grad(const ScoreGradParams& p, cudaStream_t s, int* launches);
+
+// Sums of `parts` partial results, in order: out0 takes the first n0 values
+// of each, out1 the next n1, out2 the last n2 (a NULL output is skipped).
+cudaError_t launch_sum_parts(const float* part, int64_t parts, float* out0, int64_t n0, float* out1, int64_t n1,
+                             float* out2, int64_t n2, cudaStream_t s, int* launches);
+
+}  // namespace rnngb
