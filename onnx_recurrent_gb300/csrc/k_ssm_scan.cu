@@ -1,387 +1,507 @@
-// Selective state space scan, its gradients and its single-token form (the
-// formulas stand in include/onnx_recurrent.h).
+// Selective state space scan (the formulas stand in include/onnx_recurrent.h).
 //
-// A channel's M states are spread over L lanes (L a power of two), E = 4
-// states a lane; states past M have A = B = C = 0 and stay 0.  Every lane
-// walks the row's steps in order; y[t] is summed over the channel's lanes.
+// Work of one state update h = exp(delta A) h + delta X B, y += C h: one
+// exponential (32 lanes a clock and SM, measured) and four fp32 operations
+// (128 lanes a clock and SM): both pipes take 4/128 of a clock, so 152 SMs at
+// 1.92 GHz need 107 ns for a million updates; the bytes of X, dt, Z and Y
+// (8 a channel and step in 16-bit types, 16 updates with M = 16) need 74 ns.
+// What the kernel adds to the four operations is kept small:
+//   - a lane holds four states of four neighbouring channels: a step's B and C
+//     are read once for four channels, delta and delta X once for four states
+//     (shared memory returns 128 bytes a clock, whoever asks for the same);
+//   - channels are packed in pairs (ssm_tile.cuh): half the issue slots;
+//   - delta and delta X are formed once per channel and step, and Y's gate
+//     and rounding applied once, by elementwise passes over tiles of kSsmTile
+//     steps; the passes and the loop in between share a warp's own part of
+//     shared memory, so a tile costs the block two barriers;
+//   - the sum over a channel's lanes goes with the channels, halving the
+//     values each time; in the first exchange each lane sends its second pair
+//     of channels, which for odd lanes is the first in memory, so nothing is
+//     selected.
+// The next tile's inputs are copied while a tile is computed.
 //
-// Gradient, for one channel with g[t,m] the loss's slope in h[t,m],
-// a = exp(delta A), p = a h[t-1] and e = dY silu(Z):
-//     g[t]   = C e + a[t+1] g[t+1]
-//     dX     = delta sum_m g B + Dskip e       dC = e h,  dB = delta X g
-//     ddelta = sum_m g (A p + B X)             dA = sum_t delta g p
-// The forward run saves h before each tile of kSsmTile steps; the gradient
-// takes the tiles from the last to the first, forms a tile's a and p again
-// from the saved state and then goes through its steps backwards.
-#include "ssm_math.cuh"
+// Measured (38 rows of 512 steps, 2048 channels, M = 16, bf16: all SMs full):
+// 206 us, 3.1 updates a ns, a third of the pipes' bound.  Counters: issue slots
+// 59 % busy, fp32 pipe 60 %, shared memory 57 %, exponentials 40 %; with parts
+// left out, the loop over steps takes 64 % of the time (its loads and
+// exchanges half of that), softplus and gate 9 %, copies 7 %, the rest goes to
+// the passes' shared memory and barriers.  Tried at the same size and no faster:
+// 8 channels a lane (252 us, fewer warps), 2 (337 us), scalar instead of
+// packed operations, 8 or 32 steps a tile, 5 to 8 blocks an SM.
+//
+// When rows and channels are too few for the SMs, the steps are split in
+// chunks: one launch finds each chunk's end state from zero and the sum of
+// its delta (the product of its decays is exp(A sum delta)), a small one
+// chains them to every chunk's first state, and the scan runs over all chunks
+// at once.  That costs another exponential and three operations per update.
+#include "ssm_tile.cuh"
+
+#pragma nv_diag_suppress 128   // loops that a launch for end states leaves out
 
 namespace rnngb {
 namespace {
 
-constexpr int kThreads = 128;
 constexpr int E = 4;              // states of a lane
-constexpr int T = kSsmTile;
+constexpr int CH = 4;             // channels of a lane
+constexpr int T = 16;             // steps of a tile in shared memory
+constexpr int U = 4;              // steps of the inner loop's body
+struct ScanLaunch {
+    int cblocks;          // blocks of channels in a group
+    int64_t chunk;        // steps of a chunk (a multiple of T)
+    int chunks;
+    bool fast_x, fast_dt, fast_z, fast_b, fast_c, vec_y, vec_h, vec_s;
+    float* ends;          // [chunks - 1][N][D][M]: end states, then first states of chunks 1 ..
+    float* deltas;        // [chunks - 1][N][D]
+};
 
-// Lanes of a channel of M states: the power of two that holds them.
-int lanes_of(int M)
-{
-    int l = 1;
-    while (l * E < M) l *= 2;
-    return l;
-}
-
-template <typename V>
-__device__ __forceinline__ float ld(const View& v, int64_t t, int64_t n, int64_t i)
-{
-    return to_f(static_cast<const V*>(v.data)[t * v.ss + n * v.bs + i]);
-}
-
-template <int L>
-__device__ __forceinline__ float sum_lanes(float v)
-{
-#pragma unroll
-    for (int o = L / 2; o > 0; o /= 2) v += __shfl_xor_sync(~0u, v, o);
-    return v;
-}
-
-// Blocks take whole channels of one group: kThreads / L of them.
+// A block's shape and its shared memory.
 template <typename V, int L>
-__global__ void __launch_bounds__(kThreads) ssm_scan_kernel(const ScanParams p, int cblocks)
+struct Tile {
+    static constexpr int W = L >= 4 ? 4 : L;               // warps
+    static constexpr int THREADS = 32 * W;
+    static constexpr int WC = 32 / L * CH;                 // channels of a warp
+    static constexpr int ME = L * E;                       // states, padded
+    static constexpr int PW = WC + 4;                      // pitch of delta and delta X
+    static constexpr int NV = WC < 4 ? WC : 4;             // channels of an elementwise access
+    using Rows = Stager<V, T, W * WC, THREADS>;            // of X, dt, Z
+    using Pairs = Stager<V, T, ME, THREADS>;               // of B, C
+    static constexpr int RX = T * Rows::PITCH, RB = T * Pairs::PITCH;
+    static constexpr size_t bytes(int raws)
+    {
+        return sizeof(V) * 2 * (size_t)(raws * RX + 2 * RB) + sizeof(float) * 2 * T * ME + sizeof(float) * 2 * W * (T * PW + WC);
+    }
+};
+
+template <typename V, int L, bool ENDS>
+__global__ void __launch_bounds__(Tile<V, L>::THREADS, 16 / Tile<V, L>::W)
+    ssm_scan_kernel(const ScanParams p, const ScanLaunch q)
 {
-    constexpr int CH = kThreads / L;
-    const int lane = threadIdx.x % L;
-    const int64_t n = blockIdx.x / (cblocks * p.G);
-    const int g = blockIdx.x / cblocks % p.G;
+    using K = Tile<V, L>;
+    constexpr int RAWS = ENDS ? 2 : 3, PAIRS = CH / 2, NP = K::NV / 2;
+    extern __shared__ __align__(16) char smem[];
+    V* raw = reinterpret_cast<V*>(smem);                          // [2][RAWS][T][..]: dt, X, Z
+    V* rawbc = raw + 2 * RAWS * K::RX;                            // [2][2][T][..]: B, C
+    float* bc = reinterpret_cast<float*>(rawbc + 2 * 2 * K::RB);  // [T][2][ME]: B, C
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    float* sd = bc + 2 * T * K::ME + warp * 2 * (T * K::PW + K::WC);   // the warp's delta
+    float* sx = sd + T * K::PW;                                   // delta X, then y
+    float* sb = sx + T * K::PW;                                   // dt_bias and Dskip of its channels
+
+    unsigned blk = blockIdx.x;
+    const int cb = blk % q.cblocks;
+    blk /= q.cblocks;
+    const int g = blk % p.G;
+    blk /= p.G;
+    const int64_t n = blk % (unsigned)p.N;
+    const int chunk = blk / (unsigned)p.N;
     const int64_t dg = p.D / p.G;
-    const int64_t c = (int64_t)(blockIdx.x % cblocks) * CH + threadIdx.x / L;
-    const bool on = c < dg;
-    const int64_t d = g * dg + (on ? c : 0);
+    const int64_t c0 = (int64_t)cb * K::W * K::WC;                // first channel in the group
+    const int valid = dg - c0 < K::W * K::WC ? (int)(dg - c0) : K::W * K::WC;
+    const int64_t d0 = g * dg + c0;
     const int64_t len = row_length(p.lens, n, p.S, p.status);
-    const int64_t tiles = (p.S + T - 1) / T;
-    float A[E], h[E];
-#pragma unroll
-    for (int j = 0; j < E; ++j) {
-        const int m = lane * E + j;
-        A[j] = m < p.M ? p.A[d * p.M + m] : 0.0f;
-        h[j] = m < p.M && p.h0 ? p.h0[(n * p.D + d) * p.M + m] : 0.0f;
-    }
-    const float skip = p.Dskip ? p.Dskip[d] : 0.0f, bias = p.dt_bias ? p.dt_bias[d] : 0.0f;
-    V* y = static_cast<V*>(p.Y.data) + n * p.Y.bs + d;
-    for (int64_t t = 0; t < len; ++t) {
-        if (p.saved && t % T == 0 && on)
-#pragma unroll
-            for (int j = 0; j < E; ++j)
-                if (lane * E + j < p.M) p.saved[((n * tiles + t / T) * p.D + d) * p.M + lane * E + j] = h[j];
-        const float x = ld<V>(p.X, t, n, d);
-        float delta = ld<V>(p.dt, t, n, d) + bias;
-        if (p.softplus) delta = softplus_f(delta);
-        float s = 0.0f;
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-            const int m = lane * E + j;
-            const float b = m < p.M ? ld<V>(p.B, t, n, g * p.M + m) : 0.0f;
-            const float cc = m < p.M ? ld<V>(p.C, t, n, g * p.M + m) : 0.0f;
-            h[j] = fmaf(expf(delta * A[j]), h[j], delta * x * b);
-            s = fmaf(cc, h[j], s);
-        }
-        s = sum_lanes<L>(s) + skip * x;
-        if (p.Z.data) s *= silu_f(ld<V>(p.Z, t, n, d));
-        if (lane == 0 && on) y[t * p.Y.ss] = from_f<V>(s);
-    }
-    if (!on) return;
-    if (lane == 0)
-        for (int64_t t = len; t < p.S; ++t) y[t * p.Y.ss] = from_f<V>(0.0f);
-    if (p.hT)
-#pragma unroll
-        for (int j = 0; j < E; ++j)
-            if (lane * E + j < p.M) p.hT[(n * p.D + d) * p.M + lane * E + j] = h[j];
-}
+    const int64_t t_first = chunk * q.chunk;
+    const int64_t t_end = t_first + q.chunk < p.S ? t_first + q.chunk : p.S;
+    const int64_t live = len < t_end ? len : t_end;               // steps of the row end here
 
-// Scratch of the gradient: for each row the sums over its steps of dA, dDskip
-// and ddt_bias, and for each channel block the sums over its channels of dB
-// and dC at every step.
-template <typename V, int L>
-__global__ void __launch_bounds__(kThreads) ssm_scan_grad_kernel(const ScanGradParams q, int cblocks, float* steps)
-{
-    constexpr int CH = kThreads / L, W = kThreads / 32;
-    const ScanParams& p = q.f;
-    __shared__ float bc[W][T][2][L * E];
-    const int lane = threadIdx.x % L, warp = threadIdx.x / 32;
-    const int cb = blockIdx.x % cblocks;
-    const int64_t n = blockIdx.x / (cblocks * p.G);
-    const int g = blockIdx.x / cblocks % p.G;
-    const int64_t dg = p.D / p.G;
-    const int64_t c = (int64_t)cb * CH + threadIdx.x / L;
-    const bool on = c < dg;
-    const int64_t d = g * dg + (on ? c : 0);
-    const int64_t len = row_length(p.lens, n, p.S, p.status);
-    const int64_t tiles = (p.S + T - 1) / T;
-    const float some = on ? 1.0f : 0.0f;     // channels past the group add nothing
-    float A[E], ahead[E], dA[E];
+    // this lane's channels (of the warp's) and states
+    const int sg = lane % L, cg = lane / L;
+    // Exchanges over a channel's lanes that halve the pairs: SPLIT of them; then
+    // one that halves the last pair (HALVE), if there are lanes left for it.
+    constexpr int SPLIT = PAIRS >= 4 && L >= 4 ? 2 : PAIRS >= 2 && L >= 2 ? 1 : 0, LEFT = PAIRS >> SPLIT;
+    constexpr bool HALVE = LEFT == 1 && L > (1 << SPLIT);
+    const bool up = HALVE && (sg >> SPLIT & 1);
+    int ch[PAIRS];                                                // first channel of each pair
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-        const int m = lane * E + j;
-        A[j] = m < p.M ? p.A[d * p.M + m] : 0.0f;
-        ahead[j] = m < p.M && q.dhT && on ? q.dhT[(n * p.D + d) * p.M + m] : 0.0f;
-        dA[j] = 0.0f;
+    for (int r = 0; r < PAIRS; ++r) {
+        int at = r;                                               // where the lane keeps and sends differs by its bits
+        if (SPLIT >= 1 && sg & 1) at ^= PAIRS / 2;
+        if (SPLIT >= 2 && sg & 2) at ^= PAIRS / 4;
+        ch[r] = cg * CH + 2 * at;
     }
-    const float skip = p.Dskip ? p.Dskip[d] : 0.0f, bias = p.dt_bias ? p.dt_bias[d] : 0.0f;
-    float dskip = 0.0f, dbias = 0.0f;
-    for (int64_t k = (len + T - 1) / T - 1; k >= 0; --k) {
-        float a[T][E], past[T][E], h[E];
+    f2 A[E][PAIRS], h[E][PAIRS];
+    {
+        const float* first = ENDS ? nullptr : chunk == 0 ? p.h0 : q.ends + (int64_t)(chunk - 1) * p.N * p.D * p.M;
 #pragma unroll
-        for (int j = 0; j < E; ++j)
-            h[j] = lane * E + j < p.M ? p.saved[((n * tiles + k) * p.D + d) * p.M + lane * E + j] : 0.0f;
+        for (int r = 0; r < PAIRS; ++r) {
+            float a[2][E], s[2][E];
 #pragma unroll
-        for (int i = 0; i < T; ++i) {
-            const int64_t t = k * T + i;
-            float x = 0.0f, delta = 0.0f;
-            if (t < len) {
-                x = ld<V>(p.X, t, n, d);
-                delta = ld<V>(p.dt, t, n, d) + bias;
-                if (p.softplus) delta = softplus_f(delta);
-            }
+            for (int i = 0; i < 2; ++i) {
+                const int c = warp * K::WC + ch[r] + i;
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                const int m = lane * E + j;
-                const float b = m < p.M && t < len ? ld<V>(p.B, t, n, g * p.M + m) : 0.0f;
-                a[i][j] = expf(delta * A[j]);
-                past[i][j] = a[i][j] * h[j];
-                h[j] = fmaf(delta * x, b, past[i][j]);
-            }
-        }
-#pragma unroll
-        for (int i = T - 1; i >= 0; --i) {
-            const int64_t t = k * T + i;
-            float db[E], dc[E];
-            float x = 0.0f, v = 0.0f, delta = 0.0f, e = 0.0f, z = 0.0f, dy = 0.0f;
-            if (t < len) {
-                x = ld<V>(p.X, t, n, d);
-                v = ld<V>(p.dt, t, n, d) + bias;
-                delta = p.softplus ? softplus_f(v) : v;
-                dy = some * ld<V>(q.dY, t, n, d);
-                e = dy;
-                if (p.Z.data) {
-                    z = ld<V>(p.Z, t, n, d);
-                    e = dy * silu_f(z);
+                for (int j = 0; j < E; ++j) {
+                    const int m = sg * E + j;
+                    const bool on = c < valid && m < p.M;
+                    a[i][j] = on ? p.A[(d0 + c) * p.M + m] * kLog2e : 0.0f;
+                    s[i][j] = on && first ? first[(n * p.D + d0 + c) * p.M + m] : 0.0f;
                 }
             }
-            float y = 0.0f, driven = 0.0f, decayed = 0.0f;
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                const int m = lane * E + j;
-                const float b = m < p.M && t < len ? ld<V>(p.B, t, n, g * p.M + m) : 0.0f;
-                const float cc = m < p.M && t < len ? ld<V>(p.C, t, n, g * p.M + m) : 0.0f;
-                const float hj = fmaf(delta * x, b, past[i][j]);
-                const float slope = fmaf(cc, e, ahead[j]);
-                const float sp = slope * past[i][j];
-                y = fmaf(cc, hj, y);
-                driven = fmaf(slope, b, driven);
-                decayed = fmaf(sp, A[j], decayed);
-                dA[j] = fmaf(sp, delta, dA[j]);
-                db[j] = delta * x * slope;
-                dc[j] = e * hj;
-                ahead[j] = a[i][j] * slope;
+            for (int j = 0; j < E; ++j) A[j][r] = pack2(a[0][j], a[1][j]), h[j][r] = pack2(s[0][j], s[1][j]);
+        }
+    }
+
+    // elementwise accesses: NV channels from ec on, steps er, er + ROWS, ..
+    constexpr int PER_ROW = K::WC / K::NV, ROWS = 32 / PER_ROW;
+    const int ev = lane % PER_ROW * K::NV, er = lane / PER_ROW;
+    const int ec = warp * K::WC + ev;                             // channel in the block
+    const int some = valid - ec < K::NV ? (valid - ec > 0 ? valid - ec : 0) : K::NV;
+    f2 total[ENDS ? NP : 1];
+#pragma unroll
+    for (int e = 0; e < (ENDS ? NP : 1); ++e) total[e] = 0;
+    for (int i = lane; i < 2 * K::WC; i += 32) {
+        const int c = warp * K::WC + i % K::WC;
+        const float* from = i < K::WC ? p.dt_bias : p.Dskip;
+        sb[i] = from && c < valid ? from[d0 + c] : 0.0f;
+    }
+    __syncwarp();
+
+    const bool gate = !ENDS && p.Z.data;
+    auto stage = [&](int k) {
+        const int64_t t0 = t_first + (int64_t)k * T, left = live - t0, row = anew(n);
+        const int steps = left < T ? (int)left : T;
+        V* r = raw + (k & 1) * RAWS * K::RX;
+        V* b = rawbc + (k & 1) * 2 * K::RB;
+        K::Rows::copy(r, p.dt, row, t0, d0, steps, valid, q.fast_dt);
+        K::Rows::copy(r + K::RX, p.X, row, t0, d0, steps, valid, q.fast_x);
+        if (gate) K::Rows::copy(r + 2 * K::RX, p.Z, row, t0, d0, steps, valid, q.fast_z);
+        K::Pairs::copy(b, p.B, row, t0, (int64_t)g * p.M, steps, p.M, q.fast_b);
+        if (!ENDS) K::Pairs::copy(b + K::RB, p.C, row, t0, (int64_t)g * p.M, steps, p.M, q.fast_c);
+        cp_async_commit();
+    };
+    const int tiles = live > t_first ? (int)((live - t_first + T - 1) / T) : 0;
+    if (tiles) stage(0);
+    for (int k = 0; k < tiles; ++k) {
+        const int64_t left = live - t_first - (int64_t)k * T;
+        const int steps = left < T ? (int)left : T;
+        const int buf = k & 1;
+        cp_async_wait<0>();
+        __syncthreads();                       // tile k has landed; tile k-1's buffers are free
+        if (k + 1 < tiles) stage(k + 1);
+        const V* r = raw + buf * RAWS * K::RX + ec;
+        const V* b = rawbc + buf * 2 * K::RB;
+        for (int i = threadIdx.x; i < T * K::ME; i += K::THREADS) {
+            const int t = i / K::ME, m = i % K::ME;
+            bc[t * 2 * K::ME + m] = to_f(b[t * K::Pairs::PITCH + m]);
+            if (!ENDS) bc[(t * 2 + 1) * K::ME + m] = to_f(b[K::RB + t * K::Pairs::PITCH + m]);
+        }
+        constexpr int TURNS = (T + ROWS - 1) / ROWS, BATCH = TURNS < 4 ? TURNS : 4;
+#pragma unroll
+        for (int i0 = 0; i0 < TURNS; i0 += BATCH) {
+            f2 d[BATCH * NP];
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                f2 v[NP];
+                load_pairs<V, K::NV>(r + (er + (i0 + i) * ROWS) % T * K::Rows::PITCH, v);
+#pragma unroll
+                for (int e = 0; e < NP; ++e) d[i * NP + e] = add2(v[e], *reinterpret_cast<const f2*>(sb + ev + 2 * e));
             }
-            y = sum_lanes<L>(y) + skip * x;
-            driven = sum_lanes<L>(driven);
-            decayed = sum_lanes<L>(decayed);
-            // over the warp's channels, which share B and C
+            if (p.softplus) softplus_pairs(d);
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
+            for (int i = 0; i < BATCH; ++i) {
+                const int t = er + (i0 + i) * ROWS;
+                if (ROWS > T && t >= T) break;
+                f2 x[NP];
+                load_pairs<V, K::NV>(r + K::RX + t * K::Rows::PITCH, x);
 #pragma unroll
-                for (int o = 16; o >= L; o /= 2) {
-                    db[j] += __shfl_xor_sync(~0u, db[j], o);
-                    dc[j] += __shfl_xor_sync(~0u, dc[j], o);
+                for (int e = 0; e < NP; ++e) {
+                    f2& v = d[i * NP + e];
+                    if (t >= steps) v = 0;
+                    if (ENDS) total[ENDS ? e : 0] = add2(total[ENDS ? e : 0], v);
+                    *reinterpret_cast<f2*>(sd + t * K::PW + ev + 2 * e) = v;
+                    *reinterpret_cast<f2*>(sx + t * K::PW + ev + 2 * e) = mul2(v, x[e]);
                 }
-                if (threadIdx.x % 32 < L) {
-                    bc[warp][i][0][lane * E + j] = db[j];
-                    bc[warp][i][1][lane * E + j] = dc[j];
+            }
+        }
+        __syncthreads();                       // B and C are in place (and each warp's own delta)
+        if (warp * K::WC >= valid) continue;
+        // Four steps at a time: their y are stored together, because the loads
+        // of a step cannot pass a store before them.
+#pragma unroll 1
+        for (int t4 = 0; t4 < T; t4 += U) {
+            if (!ENDS && p.saved && t4 % kSsmTile == 0 && t4 < steps) {
+                const int64_t at = anew(n) * ((p.S + kSsmTile - 1) / kSsmTile) + (t_first + (int64_t)k * T + t4) / kSsmTile;
+                float* saved = p.saved + (at * p.D + d0) * p.M + sg * E;
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) {
+                    float s[2][E];
+#pragma unroll
+                    for (int j = 0; j < E; ++j) unpack2(h[j][i], s[0][j], s[1][j]);
+#pragma unroll
+                    for (int o = 0; o < 2; ++o) {
+                        const int c = warp * K::WC + ch[i] + o;
+                        if (c < valid && sg * E < p.M)
+                            store_vec<float, E>(saved + (int64_t)c * p.M, s[o], p.M - sg * E < E ? p.M - sg * E : E, q.vec_h);
+                    }
                 }
             }
-            if (t < len && on && lane == 0) {
-                float ddt = fmaf(x, driven, decayed);
-                if (p.softplus) ddt *= sigmoid_f(v);
-                dbias += ddt;
-                dskip = fmaf(e, x, dskip);
-                if (q.dX.data) static_cast<V*>(q.dX.data)[t * q.dX.ss + n * q.dX.bs + d] = from_f<V>(fmaf(delta, driven, skip * e));
-                if (q.ddt.data) static_cast<V*>(q.ddt.data)[t * q.ddt.ss + n * q.ddt.bs + d] = from_f<V>(ddt);
-                if (q.dZ.data) static_cast<V*>(q.dZ.data)[t * q.dZ.ss + n * q.dZ.bs + d] = from_f<V>(dy * y * silu_slope(z));
+            f2 ys[U][LEFT];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int t = t4 + u;
+                f2 d[PAIRS], dx[PAIRS], y[PAIRS];
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) {
+                    d[i] = *reinterpret_cast<const f2*>(sd + t * K::PW + ch[i]);
+                    dx[i] = *reinterpret_cast<const f2*>(sx + t * K::PW + ch[i]);
+                }
+                const float4 vb = *reinterpret_cast<const float4*>(bc + t * 2 * K::ME + sg * E);
+                float4 vc = vb;
+                if (!ENDS) vc = *reinterpret_cast<const float4*>(bc + (t * 2 + 1) * K::ME + sg * E);
+                const f2 B[E] = {dup2(vb.x), dup2(vb.y), dup2(vb.z), dup2(vb.w)};
+                const f2 C[E] = {dup2(vc.x), dup2(vc.y), dup2(vc.z), dup2(vc.w)};
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i)
+#pragma unroll
+                    for (int j = 0; j < E; ++j) {
+                        h[j][i] = fma2(ex2_2(mul2(d[i], A[j][i])), h[j][i], mul2(dx[i], B[j]));
+                        if (!ENDS) y[i] = j == 0 ? mul2(C[j], h[j][i]) : fma2(C[j], h[j][i], y[i]);
+                    }
+                if (ENDS) continue;
+                // over the channel's lanes
+#pragma unroll
+                for (int k = 0; k < SPLIT; ++k)
+#pragma unroll
+                    for (int i = 0; i < PAIRS >> (k + 1); ++i)
+                        y[i] = add2(y[i], __shfl_xor_sync(~0u, y[i + (PAIRS >> (k + 1))], 1 << k));
+                if (HALVE) {
+                    float a, b2;
+                    unpack2(y[0], a, b2);
+                    float one = (up ? b2 : a) + __shfl_xor_sync(~0u, up ? a : b2, 1 << SPLIT);
+#pragma unroll
+                    for (int o = 2 << SPLIT; o < L; o *= 2) one += __shfl_xor_sync(~0u, one, o);
+                    y[0] = pack2(one, one);
+                }
+#pragma unroll
+                for (int i = 0; i < LEFT; ++i) ys[u][i] = y[i];
+            }
+            if (ENDS) continue;
+            // y takes delta X's place
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float* to = sx + (t4 + u) * K::PW;
+                if (HALVE) {
+                    float a, b2;
+                    unpack2(ys[u][0], a, b2);
+                    if (sg < (2 << SPLIT)) to[ch[0] + (up ? 1 : 0)] = a;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < LEFT; ++i) *reinterpret_cast<f2*>(to + ch[i]) = ys[u][i];
+                }
             }
         }
-        __syncthreads();
-        for (int i = threadIdx.x; i < T * 2 * p.M; i += kThreads) {
-            const int m = i % p.M, w = i / p.M % 2, at = i / p.M / 2;
-            float s = 0.0f;
+        if (ENDS) continue;
+        __syncwarp();
+        V* y_row = static_cast<V*>(p.Y.data) + anew(n) * p.Y.bs + d0 + ec + (t_first + (int64_t)k * T + er) * p.Y.ss;
 #pragma unroll
-            for (int r = 0; r < W; ++r) s += bc[r][at][w][m];
-            const int64_t t = k * T + at;
-            if (t < len) steps[((((int64_t)cb * p.N + n) * p.S + t) * p.G + g) * 2 * p.M + w * p.M + m] = s;
-        }
-        __syncthreads();
-    }
-    if (!on) return;
-    if (lane == 0) {
-        const V zero = from_f<V>(0.0f);
-        for (int64_t t = len; t < p.S; ++t) {
-            if (q.dX.data) static_cast<V*>(q.dX.data)[t * q.dX.ss + n * q.dX.bs + d] = zero;
-            if (q.ddt.data) static_cast<V*>(q.ddt.data)[t * q.ddt.ss + n * q.ddt.bs + d] = zero;
-            if (q.dZ.data) static_cast<V*>(q.dZ.data)[t * q.dZ.ss + n * q.dZ.bs + d] = zero;
-        }
-    }
-    float* part = q.part + n * p.D * (p.M + 2);
+        for (int i = 0; i < (T + ROWS - 1) / ROWS; ++i) {
+            const int t = er + i * ROWS;
+            if (ROWS > T && t >= T) break;
+            f2 x[NP], z[NP];
+            float v[K::NV];
+            load_pairs<V, K::NV>(r + K::RX + t * K::Rows::PITCH, x);
+            if (gate) load_pairs<V, K::NV>(r + 2 * K::RX + t * K::Rows::PITCH, z);
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-        const int m = lane * E + j;
-        if (m < p.M) {
-            part[d * p.M + m] = dA[j];
-            if (q.dh0) q.dh0[(n * p.D + d) * p.M + m] = ahead[j];
+            for (int e = 0; e < NP; ++e) {
+                f2 s = fma2(*reinterpret_cast<const f2*>(sb + K::WC + ev + 2 * e), x[e], *reinterpret_cast<const f2*>(sx + t * K::PW + ev + 2 * e));
+                if (gate && p.saved) unpack2(s, v[2 * e], v[2 * e + 1]);
+                if (gate) z[e] = s = mul2(s, silu_fast2(z[e]));
+                if (!(gate && p.saved)) unpack2(s, v[2 * e], v[2 * e + 1]);
+            }
+            if (gate && p.saved) {             // y before the gate, for the gate's gradient
+                const int64_t at = (anew(n) * p.S + t_first + (int64_t)k * T + t) * p.D + d0 + ec;
+                store_vec<float, K::NV>(p.saved + ssm_saved_states(p.S, p.N, p.D, p.M) + at, v, t < steps ? some : 0, q.vec_s);
+#pragma unroll
+                for (int e = 0; e < NP; ++e) unpack2(z[e], v[2 * e], v[2 * e + 1]);
+            }
+            store_vec<V, K::NV>(y_row + i * ROWS * p.Y.ss, v, t < steps ? some : 0, q.vec_y);
         }
     }
-    if (lane == 0) {
-        part[p.D * p.M + d] = dskip;
-        part[p.D * p.M + p.D + d] = dbias;
+    if (ENDS) {
+        // the chunk's sum of delta, over the steps that the lanes took
+#pragma unroll
+        for (int e = 0; e < NP; ++e) {
+#pragma unroll
+            for (int o = PER_ROW; o < 32; o *= 2) total[ENDS ? e : 0] = add2(total[ENDS ? e : 0], __shfl_xor_sync(~0u, total[ENDS ? e : 0], o));
+            float v[2];
+            unpack2(total[ENDS ? e : 0], v[0], v[1]);
+            if (er == 0) store_vec<float, 2>(q.deltas + ((int64_t)chunk * p.N + n) * p.D + d0 + ec + 2 * e, v, some - 2 * e < 2 ? some - 2 * e : 2, false);
+        }
+    } else {
+        const float zero[K::NV] = {};
+        V* y = static_cast<V*>(p.Y.data) + n * p.Y.bs + d0 + ec;
+        for (int64_t t = (live > t_first ? live : t_first) + er; t < t_end; t += ROWS)
+            store_vec<V, K::NV>(y + t * p.Y.ss, zero, some, q.vec_y);
+        const bool last = len > 0 ? len > t_first && len <= t_end : chunk == 0;
+        if (!p.hT || !last) return;
+    }
+    float* to = ENDS ? q.ends + (int64_t)chunk * p.N * p.D * p.M : p.hT;
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+        float s[2][E];
+#pragma unroll
+        for (int j = 0; j < E; ++j) unpack2(h[j][i], s[0][j], s[1][j]);
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+            const int c = warp * K::WC + ch[i] + o;
+            if (c < valid && sg * E < p.M)
+                store_vec<float, E>(to + (n * p.D + d0 + c) * p.M + sg * E, s[o], p.M - sg * E < E ? p.M - sg * E : E, q.vec_h);
+        }
     }
 }
 
-// dB and dC of every step: the channel blocks' sums in order, zero past a
-// row's end.
-template <typename V>
-__global__ void __launch_bounds__(256) ssm_scan_bc_kernel(const ScanGradParams q, int cblocks, const float* steps)
+// First states of chunks 1 .. from the chunks' end states: one state a thread.
+__global__ void __launch_bounds__(256) ssm_scan_chain_kernel(const ScanParams p, const ScanLaunch q)
 {
-    const ScanParams& p = q.f;
-    const int64_t per = (int64_t)p.G * 2 * p.M, count = p.N * p.S * per;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256) {
-        const int64_t t = i / per % p.S, n = i / per / p.S;
-        const int r = (int)(i % per), g = r / (2 * p.M), w = r / p.M % 2, m = r % p.M;
-        float s = 0.0f;
-        if (t < row_length(p.lens, n, p.S, p.status))
-            for (int cb = 0; cb < cblocks; ++cb) s += steps[cb * count + i];
-        const View& v = w ? q.dC : q.dB;
-        if (v.data) static_cast<V*>(v.data)[t * v.ss + n * v.bs + g * p.M + m] = from_f<V>(s);
-    }
-}
-
-template <typename V, int L>
-__global__ void __launch_bounds__(kThreads) ssm_scan_step_kernel(const ScanStepParams p, int cblocks)
-{
-    const int lane = threadIdx.x % L;
-    const int64_t n = blockIdx.x / cblocks;
-    const int64_t c = (int64_t)(blockIdx.x % cblocks) * (kThreads / L) + threadIdx.x / L;
-    const bool on = c < p.D;
-    const int64_t d = on ? c : 0;
-    V* y = static_cast<V*>(p.Y.data) + n * p.Y.bs + d;
-    int64_t slot = n;
-    if (p.slots) {
-        slot = p.slots[n];
-        if (slot < 0 || slot >= p.slots_n) {      // the same for the whole block
-            if (slot != -1) *p.status = 2;        // RNN_ERR_INVALID_INPUT
-            if (on && lane == 0) *y = from_f<V>(0.0f);
-            return;
-        }
-    }
-    const int64_t g = d / (p.D / p.G);
-    const float x = ld<V>(p.X, 0, n, d);
-    float delta = ld<V>(p.dt, 0, n, d) + (p.dt_bias ? p.dt_bias[d] : 0.0f);
-    if (p.softplus) delta = softplus_f(delta);
-    float s = 0.0f;
+    const int64_t per = p.N * p.D * p.M, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= per) return;
+    const int64_t nd = i / p.M;
+    const float a = p.A[nd % p.D * p.M + i % p.M] * kLog2e;
+    float h = p.h0 ? p.h0[i] : 0.0f;
+    constexpr int B = 8;
+    for (int c0 = 0; c0 < q.chunks - 1; c0 += B) {
+        float e[B], d[B];
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-        const int m = lane * E + j;
-        if (m < p.M && on) {
-            const int64_t at = (slot * p.D + d) * p.M + m;
-            const float h = fmaf(expf(delta * p.A[d * p.M + m]), p.H[at], delta * x * ld<V>(p.B, 0, n, g * p.M + m));
-            p.H_out[at] = h;
-            s = fmaf(ld<V>(p.C, 0, n, g * p.M + m), h, s);
+        for (int k = 0; k < B; ++k) {
+            const bool on = c0 + k < q.chunks - 1;
+            e[k] = on ? q.ends[(c0 + k) * per + i] : 0.0f;
+            d[k] = on ? q.deltas[(int64_t)(c0 + k) * p.N * p.D + nd] : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            h = fmaf(ex2(a * d[k]), h, e[k]);
+            if (c0 + k < q.chunks - 1) q.ends[(c0 + k) * per + i] = h;
         }
     }
-    s = sum_lanes<L>(s) + (p.Dskip ? p.Dskip[d] : 0.0f) * x;
-    if (p.Z.data) s *= silu_f(ld<V>(p.Z, 0, n, d));
-    if (lane == 0 && on) *y = from_f<V>(s);
 }
 
 constexpr int64_t kMaxGrid = 0x7fffffff;
 
+// Measured times of a step (M = 16, bf16, gate, in ns) with 1 .. 4 warps on
+// every scheduler: 239, 342, 375, 402; the chunks' end states cost another 0.72
+// of a pass.  With few warps the latency of a step's chain shows, so splitting
+// pays: 8 rows of 2048 steps x 2048 channels take 490 us unsplit and 295 us in
+// 14 chunks, one row of 16384 steps 292 us in 38; 64 rows of 512 steps fill
+// the SMs and take 356 us unsplit, 488 us in two.
+constexpr ScanCost kCost{4, {0, 239, 342, 375, 402}, 2500, 0.72};
+
 template <typename V, int L>
-cudaError_t scan_l(const ScanParams& p, cudaStream_t s)
+cudaError_t run(const ScanParams& p, const ScanChoice& c, cudaStream_t s, int* launches)
 {
-    const int64_t cb = (p.D / p.G + kThreads / L - 1) / (kThreads / L);
-    if (cb * p.G > kMaxGrid / p.N) return cudaErrorInvalidConfiguration;
-    ssm_scan_kernel<V, L><<<(unsigned)(cb * p.G * p.N), kThreads, 0, s>>>(p, (int)cb);
-    return cudaGetLastError();
-}
-template <typename V, int L>
-cudaError_t scan_grad_l(const ScanGradParams& q, cudaStream_t s)
-{
-    const ScanParams& p = q.f;
-    const int64_t cb = (p.D / p.G + kThreads / L - 1) / (kThreads / L);
-    if (cb * p.G > kMaxGrid / p.N) return cudaErrorInvalidConfiguration;
-    float* steps = q.part + p.N * p.D * (p.M + 2);
-    ssm_scan_grad_kernel<V, L><<<(unsigned)(cb * p.G * p.N), kThreads, 0, s>>>(q, (int)cb, steps);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.S == 0) return e;
-    const int64_t count = p.N * p.S * p.G * 2 * p.M, blocks = (count + 255) / 256;
-    ssm_scan_bc_kernel<V><<<(unsigned)(blocks < 65536 ? blocks : 65536), 256, 0, s>>>(q, (int)cb, steps);
-    return cudaGetLastError();
-}
-template <typename V, int L>
-cudaError_t scan_step_l(const ScanStepParams& p, cudaStream_t s)
-{
-    const int64_t cb = (p.D + kThreads / L - 1) / (kThreads / L);
-    if (cb > kMaxGrid / p.N) return cudaErrorInvalidConfiguration;
-    ssm_scan_step_kernel<V, L><<<(unsigned)(cb * p.N), kThreads, 0, s>>>(p, (int)cb);
+    using K = Tile<V, L>;
+    const int elem = (int)sizeof(V);
+    const int64_t dg = p.D / p.G, block = K::W * K::WC, group = p.G > 1 ? dg : 0;
+    ScanLaunch q{};
+    q.cblocks = (int)c.cblocks;
+    q.chunk = c.chunk;
+    q.chunks = c.chunks;
+    q.fast_x = rows_aligned(p.X, elem, block, group);
+    q.fast_dt = rows_aligned(p.dt, elem, block, group);
+    q.fast_z = rows_aligned(p.Z, elem, block, group);
+    q.fast_b = rows_aligned(p.B, elem, 0, p.G > 1 ? p.M : 0);
+    q.fast_c = rows_aligned(p.C, elem, 0, p.G > 1 ? p.M : 0);
+    const int64_t bytes = elem * K::NV;
+    q.vec_y = (uintptr_t)p.Y.data % bytes == 0 && p.Y.ss * elem % bytes == 0 && p.Y.bs * elem % bytes == 0 &&
+              group * elem % bytes == 0;
+    q.vec_h = p.M % E == 0 && ((uintptr_t)p.hT | (uintptr_t)p.saved) % 16 == 0;
+    q.vec_s = p.D % K::NV == 0 && group % K::NV == 0 && ssm_saved_states(p.S, p.N, p.D, p.M) % 4 == 0 && (uintptr_t)p.saved % 16 == 0;
+    q.ends = p.scratch;
+    q.deltas = p.scratch + (int64_t)(c.chunks - 1) * p.N * p.D * p.M;
+    const int64_t blocks = c.cblocks * p.G * p.N;
+    if (blocks > kMaxGrid / c.chunks) return cudaErrorInvalidConfiguration;
+    if (c.chunks > 1) {
+        auto* f = ssm_scan_kernel<V, L, true>;
+        const size_t smem = K::bytes(2);
+        cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        f<<<(unsigned)(blocks * (c.chunks - 1)), K::THREADS, smem, s>>>(p, q);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        const int64_t states = p.N * p.D * p.M;
+        if ((states + 255) / 256 > kMaxGrid) return cudaErrorInvalidConfiguration;
+        ssm_scan_chain_kernel<<<(unsigned)((states + 255) / 256), 256, 0, s>>>(p, q);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        *launches += 2;
+    }
+    auto* f = ssm_scan_kernel<V, L, false>;
+    const size_t smem = K::bytes(3);
+    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    f<<<(unsigned)(blocks * c.chunks), K::THREADS, smem, s>>>(p, q);
+    ++*launches;
     return cudaGetLastError();
 }
 
-#define BY_LANES(F, V, M, ...)                       \
-    switch (lanes_of(M)) {                           \
-    case 1: return F<V, 1>(__VA_ARGS__);             \
-    case 2: return F<V, 2>(__VA_ARGS__);             \
-    case 4: return F<V, 4>(__VA_ARGS__);             \
-    case 8: return F<V, 8>(__VA_ARGS__);             \
-    case 16: return F<V, 16>(__VA_ARGS__);           \
-    default: return F<V, 32>(__VA_ARGS__);           \
+template <typename V>
+cudaError_t by_lanes(const ScanParams& p, const ScanChoice& c, cudaStream_t s, int* launches)
+{
+    switch (ssm_lanes(p.M)) {
+    case 1: return run<V, 1>(p, c, s, launches);
+    case 2: return run<V, 2>(p, c, s, launches);
+    case 4: return run<V, 4>(p, c, s, launches);
+    case 8: return run<V, 8>(p, c, s, launches);
+    case 16: return run<V, 16>(p, c, s, launches);
+    default: return run<V, 32>(p, c, s, launches);
     }
-template <typename V>
-cudaError_t scan_t(const ScanParams& p, cudaStream_t s) { BY_LANES(scan_l, V, p.M, p, s) }
-template <typename V>
-cudaError_t scan_grad_t(const ScanGradParams& p, cudaStream_t s) { BY_LANES(scan_grad_l, V, p.f.M, p, s) }
-template <typename V>
-cudaError_t scan_step_t(const ScanStepParams& p, cudaStream_t s) { BY_LANES(scan_step_l, V, p.M, p, s) }
+}
 
 }  // namespace
 
-int64_t ssm_saved_floats(int64_t S, int64_t N, int64_t D, int64_t M) { return (S + T - 1) / T * N * D * M; }
+int64_t ssm_saved_floats(int64_t S, int64_t N, int64_t D, int64_t M) { return ssm_saved_states(S, N, D, M) + S * N * D; }
+
+ScanChoice ssm_split(const ScanParams& p, int tile, const ScanCost& cost, int sms)
+{
+    const int L = ssm_lanes(p.M), W = L >= 4 ? 4 : L, WC = 32 / L * CH;
+    const int64_t dg = p.D / p.G, tiles = (p.S + tile - 1) / tile, blocks = (dg + W * WC - 1) / (W * WC);
+    const double all = (double)blocks * W * p.G * p.N / (4.0 * sms);       // warps per scheduler
+    auto pass = [&](double w, double steps) {
+        const int waves = (int)(w / cost.warps);
+        const double rest = w - (double)cost.warps * waves;
+        const int r = (int)rest + (rest > (int)rest ? 1 : 0);
+        return waves * (cost.begin_ns + steps * cost.step_ns[cost.warps]) + (r ? cost.begin_ns + steps * cost.step_ns[r] : 0.0);
+    };
+    ScanChoice best{1, blocks, (tiles > 0 ? tiles : 1) * tile};
+    double least = pass(all, (double)tiles * tile);
+    for (int64_t k = 2; k <= tiles && k <= 512; ++k) {
+        const int64_t per = (tiles + k - 1) / k;
+        if ((tiles + per - 1) / per != k) continue;
+        const double steps = (double)per * tile;
+        // 5 us for two launches more, and a chunk's part of their chain
+        const double t = pass(all * (double)k, steps) + cost.ends * pass(all * (double)(k - 1), steps) + 5000.0 + 50.0 * (double)k;
+        if (t < least) {
+            least = t;
+            best.chunks = (int)k;
+            best.chunk = per * tile;
+        }
+    }
+    return best;
+}
+
+cudaError_t ssm_sm_count(int* sms)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    return e == cudaSuccess ? cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) : e;
+}
+
+cudaError_t ssm_scan_scratch(const ScanParams& p, size_t* bytes)
+{
+    int sms = 0;
+    cudaError_t e = ssm_sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    *bytes = sizeof(float) * (size_t)(ssm_split(p, T, kCost, sms).chunks - 1) * (size_t)(p.N * p.D * (p.M + 1));
+    return cudaSuccess;
+}
 
 cudaError_t launch_ssm_scan(const ScanParams& p, cudaStream_t s, int* launches)
 {
-    ++*launches;
-    return p.io == 1 ? scan_t<__half>(p, s) : p.io == 2 ? scan_t<__nv_bfloat16>(p, s) : scan_t<float>(p, s);
-}
-
-size_t ssm_scan_grad_scratch(const ScanGradParams& q)
-{
-    const ScanParams& p = q.f;
-    const int64_t per = kThreads / lanes_of(p.M), cb = (p.D / p.G + per - 1) / per;
-    return sizeof(float) * (size_t)(p.N * p.D * (p.M + 2) + cb * p.N * p.S * p.G * 2 * p.M);
-}
-
-cudaError_t launch_ssm_scan_grad(const ScanGradParams& q, cudaStream_t s, int* launches)
-{
-    if (q.f.N > 0) {
-        *launches += q.f.S > 0 ? 2 : 1;
-        cudaError_t e = q.f.io == 1 ? scan_grad_t<__half>(q, s) : q.f.io == 2 ? scan_grad_t<__nv_bfloat16>(q, s)
-                                                                              : scan_grad_t<float>(q, s);
-        if (e != cudaSuccess) return e;
-    }
-    const int64_t D = q.f.D;
-    return launch_sum_parts(q.part, q.f.N, q.dA, D * q.f.M, q.dDskip, D, q.ddt_bias, D, s, launches);
-}
-
-cudaError_t launch_ssm_scan_step(const ScanStepParams& p, cudaStream_t s, int* launches)
-{
-    ++*launches;
-    return p.io == 1 ? scan_step_t<__half>(p, s) : p.io == 2 ? scan_step_t<__nv_bfloat16>(p, s) : scan_step_t<float>(p, s);
+    int sms = 0;
+    cudaError_t e = ssm_sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    const ScanChoice c = ssm_split(p, T, kCost, sms);
+    return p.io == 1   ? by_lanes<__half>(p, c, s, launches)
+           : p.io == 2 ? by_lanes<__nv_bfloat16>(p, c, s, launches)
+                       : by_lanes<float>(p, c, s, launches);
 }
 
 }  // namespace rnngb

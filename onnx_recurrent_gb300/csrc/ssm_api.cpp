@@ -411,8 +411,16 @@ rnn_status rnn_ssm_scan(rnn_ssm_t pl, const rnn_ssm_scan_args* a)
     p.h0 = a->initial_h;
     p.hT = a->Y_h;
     p.saved = a->saved;
-    cudaError_t e = launch_ssm_scan(p, (cudaStream_t)a->stream, &pl->launches);
-    return e == cudaSuccess ? RNN_OK : cuda_fail(e, "scan launch");
+    cudaStream_t st = (cudaStream_t)a->stream;
+    size_t bytes = 0;
+    cudaError_t e = ssm_scan_scratch(p, &bytes);
+    if (e != cudaSuccess) return cuda_fail(e, "reading the device's attributes");
+    rs = claim_scratch(pl, bytes, st);
+    if (rs != RNN_OK) return rs;
+    p.scratch = (float*)pl->scratch;
+    e = launch_ssm_scan(p, st, &pl->launches);
+    if (e != cudaSuccess) return cuda_fail(e, "scan launch");
+    return release_scratch(pl, bytes, st);
 }
 
 rnn_status rnn_ssm_scan_grad(rnn_ssm_t pl, const rnn_ssm_scan_grad_args* a)
@@ -456,11 +464,13 @@ rnn_status rnn_ssm_scan_grad(rnn_ssm_t pl, const rnn_ssm_scan_grad_args* a)
     p.ddt_bias = a->ddt_bias;
     p.dh0 = a->d_initial_h;
     cudaStream_t st = (cudaStream_t)a->stream;
-    const size_t bytes = ssm_scan_grad_scratch(p);
+    size_t bytes = 0;
+    cudaError_t e = ssm_scan_grad_scratch(p, &bytes);
+    if (e != cudaSuccess) return cuda_fail(e, "reading the device's attributes");
     rs = claim_scratch(pl, bytes, st);
     if (rs != RNN_OK) return rs;
     p.part = (float*)pl->scratch;
-    cudaError_t e = launch_ssm_scan_grad(p, st, &pl->launches);
+    e = launch_ssm_scan_grad(p, st, &pl->launches);
     if (e != cudaSuccess) return cuda_fail(e, "scan gradient launch");
     return release_scratch(pl, bytes, st);
 }

@@ -16,9 +16,14 @@ struct View {
     int64_t ss = 0, bs = 0;
 };
 
-// One state per kSsmTile steps is saved by the scan for its gradient, and
-// the gradient works through a row in tiles of that many steps.
-constexpr int kSsmTile = 16;
+// What the scan saves for its gradient: the state before every kSsmTile-th
+// step, [N][ceil(S / kSsmTile)][D][M] (from which the gradient, in tiles of that many
+// steps, forms the others again), then y before its gate, [N][S][D].
+constexpr int kSsmTile = 8;
+__host__ __device__ inline int64_t ssm_saved_states(int64_t S, int64_t N, int64_t D, int64_t M)
+{
+    return (S + kSsmTile - 1) / kSsmTile * N * D * M;
+}
 constexpr int kSsmMaxState = 128;
 constexpr int kSsmMaxTaps = 8;
 constexpr int kMaxTop = 32;
@@ -64,6 +69,7 @@ struct ScanParams {
     const float* h0;
     float* hT;
     float* saved;
+    float* scratch;         // ssm_scan_scratch
     int* status;
 };
 
@@ -106,14 +112,37 @@ struct ScoreGradParams {
     void* dx;
 };
 
+// How a scan is split: blocks of channels in a group, and chunks of `chunk`
+// steps.  Chosen by a model of the time: `warps` warps fit a scheduler, a step
+// takes step_ns[w] with w of them on each, a block begin_ns to begin and end, and the
+// launch that finds the chunks' end states the part `ends` of the scan's time.
+struct ScanChoice {
+    int chunks;
+    int64_t cblocks, chunk;
+};
+struct ScanCost {
+    int warps;
+    double step_ns[5], begin_ns, ends;
+};
+ScanChoice ssm_split(const ScanParams& p, int tile, const ScanCost& cost, int sms);
+cudaError_t ssm_sm_count(int* sms);
+// Lanes of a channel of M states, four a lane: a power of two.
+inline int ssm_lanes(int M)
+{
+    int l = 1;
+    while (l * 4 < M) l *= 2;
+    return l;
+}
+
 // Each launcher queues its kernels on `s` and adds their number to *launches.
 cudaError_t launch_ssm_conv(const ConvParams& p, cudaStream_t s, int* launches);
 int64_t ssm_conv_grad_parts(const ConvGradParams& p);
 cudaError_t launch_ssm_conv_grad(const ConvGradParams& p, cudaStream_t s, int* launches);
 cudaError_t launch_ssm_conv_step(const ConvStepParams& p, cudaStream_t s, int* launches);
 int64_t ssm_saved_floats(int64_t S, int64_t N, int64_t D, int64_t M);
+cudaError_t ssm_scan_scratch(const ScanParams& p, size_t* bytes);
 cudaError_t launch_ssm_scan(const ScanParams& p, cudaStream_t s, int* launches);
-size_t ssm_scan_grad_scratch(const ScanGradParams& p);
+cudaError_t ssm_scan_grad_scratch(const ScanGradParams& p, size_t* bytes);
 cudaError_t launch_ssm_scan_grad(const ScanGradParams& p, cudaStream_t s, int* launches);
 cudaError_t launch_ssm_scan_step(const ScanStepParams& p, cudaStream_t s, int* launches);
 cudaError_t launch_scores(const ScoreParams& p, cudaStream_t s, int* launches);
