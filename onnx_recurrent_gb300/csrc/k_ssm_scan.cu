@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(Tile<V, L>::THREADS, 16 / Tile<V, L>::W)
                 for (int i = 0; i < PAIRS; ++i)
 #pragma unroll
                     for (int j = 0; j < E; ++j) {
-                        h[j][i] = fma2(ex2_2(mul2(d[i], A[j][i])), h[j][i], mul2(dx[i], B[j]));
+                        h[j][i] = fma2(decay2(d[i], A[j][i]), h[j][i], mul2(dx[i], B[j]));
                         if (!ENDS) y[i] = j == 0 ? mul2(C[j], h[j][i]) : fma2(C[j], h[j][i], y[i]);
                     }
                 if (ENDS) continue;

@@ -33,6 +33,8 @@
 // latencies, and more do not fit the registers (three with 168 and a few spills:
 // 837 us for 8 rows of 2048 steps; two with 240: 873 us; four with 128: 919 us).
 // Scalar instead of packed operations: 5 to 15 % slower.
+#include <type_traits>
+
 #include "ssm_tile.cuh"
 
 #pragma nv_diag_suppress 128   // loops that some lane counts leave out
@@ -70,7 +72,7 @@ struct Tile {
     using Sums = Stager<float, T, W * WC, THREADS>;        // of y
     using Pairs = Stager<V, T, ME, THREADS>;               // of B, C
     static constexpr int RX = T * Rows::PITCH, RB = T * Pairs::PITCH, RY = T * Sums::PITCH;
-    static constexpr int WARP = 3 * T * PW + 2 * WC;       // floats of a warp
+    static constexpr int WARP = 3 * T * PW + 2 * WC;             // floats of a warp
     static constexpr size_t bytes()
     {
         return sizeof(V) * 2 * (4 * RX + 2 * RB) + sizeof(float) * (2 * RY + 2 * T * ME + W * WARP + W * T * 2 * ME);
@@ -105,30 +107,39 @@ struct Place {
     }
     __device__ __forceinline__ int state(int j) const { return j < 2 ? m0 + j : m1 + j - 2; }
 
-    // Sums of v over the channel's lanes, stored for the warp's channels.
-    __device__ __forceinline__ void sum_states(f2 (&v)[PAIRS], float* to) const
+    static constexpr int SV = HALVE ? 1 : 2 * LEFT;                       // sums over states that a lane ends with
+    static constexpr int CV = GROUPS >= 8 ? 1 : 8 / GROUPS;               // and sums over channels
+
+    // Sums of v over the channel's lanes; each lane ends with those of some channels.
+    __device__ __forceinline__ void sum_states(f2 (&v)[PAIRS], float (&r)[SV]) const
     {
-        if (GROUPS == 1) __syncwarp();   // `to` has been read by all
-        if (SPLIT) v[0] = add2(v[0], __shfl_xor_sync(~0u, v[1], 1));
-        if (HALVE) {
+        if constexpr (SPLIT == 1) v[0] = add2(v[0], __shfl_xor_sync(~0u, v[1], 1));
+        if constexpr (HALVE) {
             float a, b;
             unpack2(v[0], a, b);
-            float one = (up ? b : a) + __shfl_xor_sync(~0u, up ? a : b, 2);
+            r[0] = (up ? b : a) + __shfl_xor_sync(~0u, up ? a : b, 2);
 #pragma unroll
-            for (int o = 4; o < L; o *= 2) one += __shfl_xor_sync(~0u, one, o);
-            if (L == 4 || sg < 4) to[ch[0] + (up ? 1 : 0)] = one;
+            for (int o = 4; o < L; o *= 2) r[0] += __shfl_xor_sync(~0u, r[0], o);
         } else {
 #pragma unroll
-            for (int i = 0; i < LEFT; ++i) *reinterpret_cast<f2*>(to + ch[i]) = v[i];
+            for (int i = 0; i < LEFT; ++i) unpack2(v[i], r[2 * i], r[2 * i + 1]);
         }
     }
-    // Sums of b and c over the warp's channels, stored as [2][ME].
-    __device__ __forceinline__ void sum_channels(float (&b)[E], float (&c)[E], float* to) const
+    __device__ __forceinline__ void store_states_sum(const float (&r)[SV], float* to) const
     {
-        constexpr int ME = L * E;
+        if constexpr (HALVE) {
+            if (L == 4 || sg < 4) to[ch[0] + (up ? 1 : 0)] = r[0];
+        } else {
+#pragma unroll
+            for (int i = 0; i < LEFT; ++i) *reinterpret_cast<float2*>(to + ch[i]) = make_float2(r[2 * i], r[2 * i + 1]);
+        }
+    }
+    // Sums of b and c over the warp's channels; each lane ends with those of some states.
+    __device__ __forceinline__ void sum_channels(float (&b)[E], float (&c)[E], float (&r)[CV]) const
+    {
         if constexpr (GROUPS == 1) {
-            *reinterpret_cast<float4*>(to + sg * E) = make_float4(b[0], b[1], b[2], b[3]);
-            *reinterpret_cast<float4*>(to + ME + sg * E) = make_float4(c[0], c[1], c[2], c[3]);
+#pragma unroll
+            for (int j = 0; j < E; ++j) r[j] = b[j], r[E + j] = c[j];
         } else {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -136,21 +147,34 @@ struct Place {
                 c[j] += __shfl_xor_sync(~0u, c[j + 2], L);
             }
             if constexpr (GROUPS == 2) {
-                *reinterpret_cast<float2*>(to + m0) = make_float2(b[0], b[1]);
-                *reinterpret_cast<float2*>(to + ME + m0) = make_float2(c[0], c[1]);
+                r[0] = b[0], r[1] = b[1], r[2] = c[0], r[3] = c[1];
             } else {
-                float r[2];
+                float w[2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) r[j] = (up2 ? c[j] : b[j]) + __shfl_xor_sync(~0u, up2 ? b[j] : c[j], 2 * L);
+                for (int j = 0; j < 2; ++j) w[j] = (up2 ? c[j] : b[j]) + __shfl_xor_sync(~0u, up2 ? b[j] : c[j], 2 * L);
                 if constexpr (GROUPS == 4) {
-                    *reinterpret_cast<float2*>(to + (up2 ? ME : 0) + m0) = make_float2(r[0], r[1]);
+                    r[0] = w[0], r[1] = w[1];
                 } else {
-                    float one = (up4 ? r[1] : r[0]) + __shfl_xor_sync(~0u, up4 ? r[0] : r[1], 4 * L);
+                    r[0] = (up4 ? w[1] : w[0]) + __shfl_xor_sync(~0u, up4 ? w[0] : w[1], 4 * L);
 #pragma unroll
-                    for (int o = 8 * L; o < 32; o *= 2) one += __shfl_xor_sync(~0u, one, o);
-                    if (GROUPS == 8 || cg < 8) to[(up2 ? ME : 0) + m0 + (up4 ? 1 : 0)] = one;
+                    for (int o = 8 * L; o < 32; o *= 2) r[0] += __shfl_xor_sync(~0u, r[0], o);
                 }
             }
+        }
+    }
+    __device__ __forceinline__ void store_channels_sum(const float (&r)[CV], float* to) const      // [2][ME]
+    {
+        constexpr int ME = L * E;
+        if constexpr (GROUPS >= 8) {
+            if (GROUPS == 8 || cg < 8) to[(up2 ? ME : 0) + m0 + (up4 ? 1 : 0)] = r[0];
+        } else if constexpr (GROUPS == 4) {
+            *reinterpret_cast<float2*>(to + (up2 ? ME : 0) + m0) = make_float2(r[0], r[1]);
+        } else if constexpr (GROUPS == 2) {
+            *reinterpret_cast<float2*>(to + m0) = make_float2(r[0], r[1]);
+            *reinterpret_cast<float2*>(to + ME + m0) = make_float2(r[2], r[3]);
+        } else {
+            *reinterpret_cast<float4*>(to + sg * E) = make_float4(r[0], r[1], r[2], r[3]);
+            *reinterpret_cast<float4*>(to + ME + sg * E) = make_float4(r[4], r[5], r[6], r[7]);
         }
     }
 };
@@ -264,11 +288,19 @@ __global__ void __launch_bounds__(Tile<V, L>::THREADS, 12 / Tile<V, L>::W)
         const float* from = b.chunk + 1 < q.chunks ? q.ends + (int64_t)b.chunk * p.N * p.D * p.M : pp.dhT;
         load_states<L>(carry, from ? from + (b.n * p.D + b.d0) * p.M : nullptr, at, c0, b.valid, p.M, false, 1.0f);
     }
+    float most_a = 0.0f;
 #pragma unroll
-    for (int j = 0; j < E; ++j)
+    for (int j = 0; j < E; ++j) {
 #pragma unroll
-        for (int i = 0; i < PAIRS; ++i) dA[j][i] = 0;
+        for (int i = 0; i < PAIRS; ++i) {
+            dA[j][i] = 0;
+            float x, y;
+            unpack2(A[j][i], x, y);
+            most_a = fmaxf(most_a, fmaxf(fabsf(x), fabsf(y)));
+        }
+    }
 
+    most_a = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(most_a)));      // of the warp
     constexpr int PER_ROW = K::WC / NV, ROWS = 32 / PER_ROW, TURNS = (T + ROWS - 1) / ROWS;
     const int ev = lane % PER_ROW * NV, er = lane / PER_ROW, ec = c0 + ev;
     const int some = b.valid - ec < NV ? (b.valid - ec > 0 ? b.valid - ec : 0) : NV;
@@ -320,6 +352,10 @@ __global__ void __launch_bounds__(Tile<V, L>::THREADS, 12 / Tile<V, L>::W)
             bc[t * 2 * K::ME + m] = to_f(rb[t * K::Pairs::PITCH + m]);
             bc[(t * 2 + 1) * K::ME + m] = to_f(rb[K::RB + t * K::Pairs::PITCH + m]);
         }
+        // Whether decays below 2^-126 occur, which the exponential flushes but dA may
+        // consist of: then they are formed as squares, by a copy of the code (a branch
+        // around the squares in one copy cost 10 %).
+        bool deep;
         {
             f2 d[TURNS * NP];
 #pragma unroll
@@ -330,6 +366,14 @@ __global__ void __launch_bounds__(Tile<V, L>::THREADS, 12 / Tile<V, L>::W)
                 for (int e = 0; e < NP; ++e) d[i * NP + e] = add2(v[e], *reinterpret_cast<const f2*>(sb + ev + 2 * e));
             }
             if (p.softplus) softplus_pairs(d);
+            float most_d = 0.0f;
+#pragma unroll
+            for (int i = 0; i < TURNS * NP; ++i) {
+                float x, y;
+                unpack2(d[i], x, y);
+                most_d = fmaxf(most_d, fmaxf(fabsf(x), fabsf(y)));
+            }
+            deep = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(most_d))) * most_a > 125.0f;
 #pragma unroll
             for (int i = 0; i < TURNS; ++i) {
                 const int t = er + i * ROWS;
@@ -359,10 +403,12 @@ __global__ void __launch_bounds__(Tile<V, L>::THREADS, 12 / Tile<V, L>::W)
                 const f2 d = *reinterpret_cast<const f2*>(sd + t * K::PW + at.ch[i]);
                 const f2 dx = *reinterpret_cast<const f2*>(sx + t * K::PW + at.ch[i]);
 #pragma unroll
-                for (int j = 0; j < E; ++j) to[j][i] = fma2(ex2_2(mul2(d, A[j][i])), from[j][i], mul2(dx, B[j]));
+                for (int j = 0; j < E; ++j) to[j][i] = fma2(decay2(d, A[j][i]), from[j][i], mul2(dx, B[j]));
             }
         };
-        if (c0 < b.valid) {
+        // The tile's steps backwards.
+        auto back = [&](auto is_deep) {
+            constexpr bool DEEP = decltype(is_deep)::value;
             if (steps > U) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) ahead(H[0], H[0], u);
@@ -387,11 +433,16 @@ __global__ void __launch_bounds__(Tile<V, L>::THREADS, 12 / Tile<V, L>::W)
                         const f2 d = *reinterpret_cast<const f2*>(sd + t * K::PW + at.ch[i]);
                         const f2 dx = *reinterpret_cast<const f2*>(sx + t * K::PW + at.ch[i]);
                         const f2 e = *reinterpret_cast<const f2*>(se + t * K::PW + at.ch[i]);
-                        const f2 half = mul2(d, dup2(0.5f));
+                        f2 a[E];
+#pragma unroll
+                        for (int j = 0; j < E; ++j) a[j] = decay2(DEEP ? mul2(d, dup2(0.5f)) : d, A[j][i]);
+                        if (DEEP) {
+#pragma unroll
+                            for (int j = 0; j < E; ++j) a[j] = mul2(a[j], a[j]);
+                        }
 #pragma unroll
                         for (int j = 0; j < E; ++j) {
-                            // as a square: a keeps its digits below 2^-126, which dA may consist of
-                            const f2 root = ex2_2(mul2(half, A[j][i])), a = mul2(root, root), past = mul2(a, H[u][j][i]);
+                            const f2 past = mul2(a[j], H[u][j][i]);
                             const f2 now = u + 1 < U ? H[u + 1 < U ? u + 1 : 0][j][i] : fma2(dx, B[j], past);
                             const f2 g = fma2(C[j], e, carry[j][i]), gp = mul2(g, past);
                             driven[i] = j == 0 ? mul2(g, B[0]) : fma2(g, B[j], driven[i]);
@@ -399,7 +450,7 @@ __global__ void __launch_bounds__(Tile<V, L>::THREADS, 12 / Tile<V, L>::W)
                             dA[j][i] = fma2(gp, d, dA[j][i]);
                             db[j] = i == 0 ? mul2(g, dx) : fma2(g, dx, db[j]);
                             dc[j] = i == 0 ? mul2(e, now) : fma2(e, now, dc[j]);
-                            carry[j][i] = mul2(a, g);
+                            carry[j][i] = mul2(a[j], g);
                         }
                     }
                     float vb[E], vc[E];
@@ -411,11 +462,20 @@ __global__ void __launch_bounds__(Tile<V, L>::THREADS, 12 / Tile<V, L>::W)
                         unpack2(dc[j], x, y);
                         vc[j] = x + y;
                     }
-                    at.sum_channels(vb, vc, sums + ((warp * T + t) * 2) * K::ME);
-                    at.sum_states(driven, sx + t * K::PW);
-                    at.sum_states(decayed, se + t * K::PW);
+                    float over_channels[Place<L>::CV], over_states[2][Place<L>::SV];
+                    at.sum_channels(vb, vc, over_channels);
+                    at.sum_states(driven, over_states[0]);
+                    at.sum_states(decayed, over_states[1]);
+                    if (Place<L>::GROUPS == 1) __syncwarp();       // every lane has read the step's values
+                    at.store_channels_sum(over_channels, sums + (warp * T + t) * 2 * K::ME);
+                    at.store_states_sum(over_states[0], sx + t * K::PW);
+                    at.store_states_sum(over_states[1], se + t * K::PW);
                 }
             }
+        };
+        if (c0 < b.valid) {
+            if (deep) back(std::true_type{});
+            else back(std::false_type{});
         } else {
             for (int i = lane; i < T * 2 * K::ME; i += 32) sums[warp * T * 2 * K::ME + i] = 0.0f;
         }
@@ -590,7 +650,7 @@ __global__ void __launch_bounds__(Tile<V, L>::THREADS, 16 / Tile<V, L>::W)
                 const f2 dd = *reinterpret_cast<const f2*>(sd + t * K::PW + at.ch[i]);
                 const f2 e = *reinterpret_cast<const f2*>(se + t * K::PW + at.ch[i]);
 #pragma unroll
-                for (int j = 0; j < E; ++j) carry[j][i] = mul2(ex2_2(mul2(dd, A[j][i])), fma2(C[j], e, carry[j][i]));
+                for (int j = 0; j < E; ++j) carry[j][i] = mul2(decay2(dd, A[j][i]), fma2(C[j], e, carry[j][i]));
             }
         }
     }
