@@ -322,7 +322,7 @@ KERNEL_SOURCES = {
     "ssm_scan_kernel": ["k_ssm_scan.cu", "ssm_tile.cuh", "ssm_api.cpp"] + _SSM,
     "ssm_scan_grad_kernel": ["k_ssm_scan_grad.cu", "ssm_tile.cuh", "ssm_api.cpp"] + _SSM,
     "ssm_scan_step_kernel": ["k_ssm_step.cu", "ssm_tile.cuh", "ssm_api.cpp"] + _SSM,
-    "scores_kernel": ["k_scores.cu", "ssm_api.cpp"] + _SSM,
+    "scores_kernel": ["k_scores.cu", "ssm_tile.cuh", "tma.cuh", "ssm_api.cpp"] + _SSM,
 }
 
 

@@ -2,25 +2,41 @@
 // include/onnx_recurrent.h).
 //
 // One pass over a row keeps, per thread, the largest logit m so far and, with
-// d_i = x_i - m <= 0,
-//     s = sum_i exp(d_i),   u = sum_i d_i exp(d_i)
-// (when m grows by g: u = (u - g s) exp(-g), s = s exp(-g)), from which
-//     lse = m + log s,      entropy = log s - u / s:
-// both parts of the entropy are >= 0, so nothing cancels.
+// d_i = (x_i - m) log2 e <= 0,
+//     s = sum_i 2^d_i,   u = sum_i d_i 2^d_i
+// (when m grows by g, in the same unit: u = (u - g s) 2^-g, s = s 2^-g), from which
+//     lse = m + log s,      entropy = log s - u / s log 2:
+// both parts of the entropy are >= 0, so nothing cancels.  A -inf adds 0 to
+// both sums (u takes d no lower than -150, where 2^d is 0); a NaN or +inf makes s NaN.
 //
-// Alternatives: each warp keeps the 32 largest logits it has seen, one per
-// lane and sorted, as whole numbers that sort like (logit, lowest place
-// first); a logit is compared with the last one wanted and inserted if it is
-// above it, which after the first few hundred is rare.
-#include "ssm_math.cuh"
+// Alternatives: the pass leaves every thread its largest logit.  With j = top /
+// warps, rounded up, the smallest of the warps' j-th largest is a bound that at
+// least `top` logits reach; only threads whose own largest reaches it look at their
+// logits again and put those that do in a list, which is sorted: keys are whole numbers that sort like (logit, lowest place
+// first).  If too many reach it (many equal logits), each warp keeps a sorted list of the 32
+// largest keys instead, one per lane, and inserts what is above the last one wanted
+// (done for every row, that took 677 us for 8192 rows of 32000 bf16 logits,
+// top 20).  Sorted lists are joined by taking the larger of one and the other reversed,
+// and sorting that.
+//
+// The bytes bound it: a logit is read once (twice with the gradient, which
+// writes it once); about 5 instructions a logit, of 11 that the SMs have
+// time for at 16-bit logits.  A row is a block's; with fewer rows than fill the
+// SMs it is a cluster's, whose blocks' results the first joins through
+// distributed shared memory, so no launch and no memory is needed for that.
+#include <type_traits>
+
+#include "ssm_tile.cuh"
+#include "tma.cuh"
 
 namespace rnngb {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+__device__ __forceinline__ float a_nan() { return __int_as_float(0x7fc00000); }
 
 // Whole numbers that sort like the logits: NaN above +inf, +0 like -0.
 __device__ __forceinline__ unsigned order_of(float x)
@@ -29,177 +45,504 @@ __device__ __forceinline__ unsigned order_of(float x)
     const unsigned b = __float_as_uint(x + 0.0f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
-__device__ __forceinline__ unsigned long long key_of(float x, unsigned i)
-{
-    return (unsigned long long)order_of(x) << 32 | (unsigned)~i;
-}
-__device__ __forceinline__ float logit_of(unsigned long long key)
+using Key = unsigned long long;
+__device__ __forceinline__ Key key_of(float x, unsigned i) { return (Key)order_of(x) << 32 | (unsigned)~i; }
+__device__ __forceinline__ float logit_of(Key key)
 {
     const unsigned o = (unsigned)(key >> 32);
     return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
 }
 
 // Insert key c (the same in all lanes) into the warp's sorted list.
-__device__ __forceinline__ void insert(unsigned long long& list, unsigned long long c)
+__device__ __forceinline__ void insert(Key& list, Key c)
 {
     const int lane = threadIdx.x % 32;
     const int at = __popc(__ballot_sync(~0u, list > c));
-    const unsigned long long up = __shfl_up_sync(~0u, list, 1);
+    const Key up = __shfl_up_sync(~0u, list, 1);
     list = lane < at ? list : lane == at ? c : up;
+}
+// The 32 largest of two sorted lists, sorted.
+__device__ __forceinline__ void merge(Key& list, Key other)
+{
+    const int lane = threadIdx.x % 32;
+    const Key back = __shfl_sync(~0u, other, 31 - lane);
+    list = list > back ? list : back;
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) {
+        const Key far = __shfl_xor_sync(~0u, list, o);
+        list = (lane & o) == 0 ? (list > far ? list : far) : (list > far ? far : list);
+    }
+}
+
+// The warp's values, sorted, largest in lane 0.
+template <typename T>
+__device__ __forceinline__ T sorted(T v)
+{
+    const int lane = threadIdx.x % 32;
+#pragma unroll
+    for (int k = 2; k <= 32; k *= 2)
+#pragma unroll
+        for (int o = k / 2; o > 0; o /= 2) {
+            const T far = __shfl_xor_sync(~0u, v, o);
+            const bool larger = ((lane & k) == 0) == ((lane & o) == 0);
+            v = larger ? (v > far ? v : far) : (v > far ? far : v);
+        }
+    return v;
 }
 
 struct Sums {
     float m, s, u;
 };
-__device__ __forceinline__ void add_logit(Sums& a, float x)
+// What is taken from a logit before 2^..; an empty set's is 0.
+__device__ __forceinline__ float base_of(float m) { return m == neg_inf() ? 0.0f : m; }
+__device__ __forceinline__ void raise_to(Sums& a, float m)
 {
-    if (x > a.m) {
-        const float g = x - a.m, f = expf(-g);   // the first one: f = 0
-        a.u = a.s > 0.0f ? (a.u - g * a.s) * f : 0.0f;
-        a.s *= f;
-        a.m = x;
-    }
-    const float d = x - a.m, e = expf(d);
-    if (e > 0.0f) {                               // so -inf adds nothing
-        a.s += e;
-        a.u = fmaf(d, e, a.u);
-    }
-}
-__device__ __forceinline__ void join(Sums& a, const Sums& b)
-{
-    if (b.s == 0.0f) return;
-    if (a.s == 0.0f) {
-        a = b;
-        return;
-    }
-    const float m = fmaxf(a.m, b.m), ga = m - a.m, gb = m - b.m, fa = expf(-ga), fb = expf(-gb);
-    const float ua = fa > 0.0f ? (a.u - ga * a.s) * fa : 0.0f, ub = fb > 0.0f ? (b.u - gb * b.s) * fb : 0.0f;
+    const float g = (base_of(m) - base_of(a.m)) * kLog2e, f = a.s > 0.0f ? ex2(-g) : 0.0f;
+    a.u = f > 0.0f ? (a.u - g * a.s) * f : 0.0f;
+    a.s = a.s != a.s ? a.s : a.s * f;
     a.m = m;
-    a.s = a.s * fa + b.s * fb;
-    a.u = ua + ub;
+}
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float v;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ void join(Sums& a, Sums b)
+{
+    const float m = max_nan(a.m, b.m);
+    raise_to(a, m);
+    raise_to(b, m);
+    a.s += b.s;
+    a.u += b.u;
 }
 
+// The elements of [lo, hi) of a row before its first 16-byte boundary.
 template <typename V>
-__global__ void __launch_bounds__(kThreads) scores_kernel(const ScoreParams p)
+__device__ __forceinline__ int64_t to_boundary(const V* x, int64_t lo, int64_t hi)
 {
-    __shared__ Sums sums[kWarps];
-    __shared__ unsigned long long lists[kWarps][32];
-    __shared__ int bad;
-    const int64_t row = blockIdx.x;
+    const int64_t n = (16 - (int64_t)((uintptr_t)(x + lo) % 16)) % 16 / (int64_t)sizeof(V);
+    return n < hi - lo ? n : hi - lo;
+}
+template <typename V, int N>
+__device__ __forceinline__ void unpack_vec(const uint4& raw, float (&v)[N])
+{
+    __align__(16) V e[N];
+    *reinterpret_cast<uint4*>(e) = raw;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = to_f(e[i]);
+}
+
+// N neighbouring logits.
+template <int N>
+__device__ __forceinline__ void take(Sums& a, const float (&x)[N])
+{
+    float most = x[0];
+#pragma unroll
+    for (int e = 1; e < N; ++e) most = max_nan(most, x[e]);
+    if (!(most <= a.m)) raise_to(a, max_nan(a.m, most));
+    const float base = base_of(a.m);
+    if constexpr (N % 2 == 0) {
+        const f2 minus = dup2(-base), scale = dup2(kLog2e);
+        f2 s = pack2(a.s, 0.0f), u = pack2(a.u, 0.0f);
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+            const f2 d = mul2(add2(pack2(x[e], x[e + 1]), minus), scale), p = ex2_2(d);
+            float d0, d1;
+            unpack2(d, d0, d1);
+            s = add2(s, p);
+            u = fma2(p, pack2(fmaxf(d0, -150.0f), fmaxf(d1, -150.0f)), u);
+        }
+        float v0, v1;
+        unpack2(s, v0, v1);
+        a.s = v0 + v1;
+        unpack2(u, v0, v1);
+        a.u = v0 + v1;
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float d = (x[e] - base) * kLog2e, p = ex2(d);
+            a.s += p;
+            a.u = fmaf(p, fmaxf(d, -150.0f), a.u);
+        }
+    }
+}
+
+// A row's part [lo, hi): single logits at its ends, 16 bytes at a time between.
+template <typename V>
+struct Part {
+    static constexpr int N = 16 / (int)sizeof(V);
+    const V* x;
+    int64_t lo, hi, first;      // first: where the 16-byte pieces begin
+    int vecs;
+
+    __device__ __forceinline__ Part(const V* row, int64_t V_, int part, int blocks) : x(row)
+    {
+        const int64_t per = ((V_ + blocks - 1) / blocks + N - 1) / N * N;
+        lo = part * per < V_ ? part * per : V_;
+        hi = lo + per < V_ ? lo + per : V_;
+        first = lo + to_boundary(x, lo, hi);
+        vecs = (int)((hi - first) / N);
+    }
+    // This thread's single logit's place, or -1: at most 14 threads have one.
+    __device__ __forceinline__ int64_t single() const
+    {
+        const int64_t i = lo + threadIdx.x;
+        const int64_t at = i < first ? i : i + (int64_t)vecs * N;      // the tail's threads come after the head's
+        return at < hi && threadIdx.x < 2 * N ? at : -1;
+    }
+    __device__ __forceinline__ const uint4* body() const { return reinterpret_cast<const uint4*>(x + first); }
+};
+
+constexpr int kCandidates = 512;
+struct Found {
+    Sums sums;
+    Key list[32];
+};
+// Shared memory of a row's alternatives.
+template <int WARPS>
+struct Shared {
+    Found found[WARPS];
+    Found mine;
+    unsigned most[WARPS], count;
+    Key candidates[kCandidates];
+};
+
+// The part's 32 largest keys (at least its `top` largest), sorted over the lanes of warp 0.
+// `most`: this thread's largest logit.
+template <typename V, int THREADS>
+__device__ __forceinline__ Key largest(const Part<V>& r, float most, int top, Shared<THREADS / 32>& sh)
+{
+    constexpr int N = Part<V>::N, WARPS = THREADS / 32, AHEAD = 4;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const V* x = static_cast<const V*>(p.x) + row * p.stride;
-    if (threadIdx.x == 0) bad = 0;
+    const unsigned own = order_of(most);
+    const unsigned in_order = sorted(own);
+    if (lane == (top + WARPS - 1) / WARPS - 1) sh.most[warp] = in_order;
+    if (threadIdx.x == 0) sh.count = 0;
     __syncthreads();
-    Sums a{neg_inf(), 0.0f, 0.0f};
-    unsigned long long list = 0;
-    bool odd = false;
-    for (int64_t i0 = 0; i0 < p.V; i0 += kThreads) {
-        const int64_t i = i0 + threadIdx.x;
-        const float v = i < p.V ? to_f(x[i]) : neg_inf();
-        odd |= v != v || v == -neg_inf();
-        add_logit(a, v);
-        if (p.top) {
-            const unsigned long long key = i < p.V ? key_of(v, (unsigned)i) : 0;
-            unsigned todo = __ballot_sync(~0u, key > __shfl_sync(~0u, list, p.top - 1));
-            while (todo) {
-                insert(list, __shfl_sync(~0u, key, __ffs(todo) - 1));
-                todo &= todo - 1;
+    unsigned bound = sh.most[0];
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) bound = bound < sh.most[w] ? bound : sh.most[w];
+    auto put = [&](float v, int64_t i) {
+        if (order_of(v) < bound) return;
+        const unsigned at = atomicAdd(&sh.count, 1u);      // their order does not matter: they are sorted
+        if (at < kCandidates) sh.candidates[at] = key_of(v, (unsigned)i);
+    };
+    if (own >= bound) {
+        const int64_t one = r.single();
+        if (one >= 0) put(to_f(r.x[one]), one);
+        for (int v = threadIdx.x; v < r.vecs; v += AHEAD * THREADS) {
+            uint4 raw[AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                if (v + k * THREADS < r.vecs) raw[k] = r.body()[v + k * THREADS];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                if (v + k * THREADS >= r.vecs) break;
+                float e[N];
+                unpack_vec<V, N>(raw[k], e);
+                float of = e[0];
+#pragma unroll
+                for (int i = 1; i < N; ++i) of = max_nan(of, e[i]);
+                if (order_of(of) < bound) continue;
+#pragma unroll
+                for (int i = 0; i < N; ++i) put(e[i], r.first + (int64_t)(v + k * THREADS) * N + i);
             }
         }
     }
-    if (odd) bad = 1;
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) {
-        const Sums b{__shfl_xor_sync(~0u, a.m, o), __shfl_xor_sync(~0u, a.s, o), __shfl_xor_sync(~0u, a.u, o)};
-        join(a, b);
-    }
-    if (lane == 0) sums[warp] = a;
-    lists[warp][lane] = list;
     __syncthreads();
-    if (warp != 0) return;
-    a = sums[0];
-    for (int w = 1; w < kWarps; ++w) join(a, sums[w]);
-    const float nan = __int_as_float(0x7fc00000);
-    const float total = a.s > 0.0f ? logf(a.s) : 0.0f;
-    const float lse = bad ? nan : a.s > 0.0f ? a.m + total : neg_inf();
-    const bool empty = !bad && a.s == 0.0f;
-    if (lane == 0) {
-        if (p.lse) p.lse[row] = lse;
-        if (p.entropy) p.entropy[row] = bad ? nan : empty ? 0.0f : total - a.u / a.s;
-        if (p.logp) {
-            const int id = p.ids[row];
-            p.logp[row] = id < 0 ? 0.0f : id >= p.V ? nan : empty ? neg_inf() : to_f(x[id]) - lse;
+    const unsigned count = sh.count;
+    Key list = 0;
+    if (count <= kCandidates) {
+        for (unsigned i = warp * 32; i < count; i += THREADS)
+            sh.candidates[i + lane] = sorted(i + lane < count ? sh.candidates[i + lane] : 0);
+        __syncthreads();
+        if (warp == 0 && count > 0) {
+            list = sh.candidates[lane];
+            for (unsigned i = 32; i < count; i += 32) merge(list, sh.candidates[i + lane]);
+        }
+        return list;
+    }
+    // too many: sorted lists of the warps' own
+    for (int64_t i0 = r.lo; i0 < r.hi; i0 += THREADS) {
+        const int64_t i = i0 + threadIdx.x;
+        const Key key = i < r.hi ? key_of(to_f(r.x[i]), (unsigned)i) : 0;
+        unsigned todo = __ballot_sync(~0u, key > __shfl_sync(~0u, list, top - 1));
+        while (todo) {
+            const Key c = __shfl_sync(~0u, key, __ffs(todo) - 1);
+            if (c > __shfl_sync(~0u, list, top - 1)) insert(list, c);
+            todo &= todo - 1;
         }
     }
-    if (!p.top) return;
-    list = lists[0][lane];
-    for (int w = 1; w < kWarps; ++w)
-        for (int j = 0; j < p.top; ++j) insert(list, lists[w][j]);
-    if (lane < p.top) {
+    sh.found[warp].list[lane] = list;
+    __syncthreads();
+    if (warp == 0)
+        for (int w = 1; w < WARPS; ++w) merge(list, sh.found[w].list[lane]);
+    return list;
+}
+
+template <typename V, int THREADS, bool TOP>
+__global__ void __launch_bounds__(THREADS, TOP ? 0 : 2048 / THREADS) scores_kernel(const ScoreParams p, int blocks)
+{
+    constexpr int N = Part<V>::N, AHEAD = 2, WARPS = THREADS / 32;
+    __shared__ std::conditional_t<TOP, Shared<WARPS>, Found[WARPS + 1]> shared;
+    const int part = blockIdx.x % blocks, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    Found *found, *mine;
+    if constexpr (TOP) found = shared.found, mine = &shared.mine;
+    else found = shared, mine = shared + WARPS;
+    const int64_t row = blockIdx.x / blocks;
+    const V* x = static_cast<const V*>(p.x) + row * p.stride;
+    const Part<V> r(x, p.V, part, blocks);
+    Sums a{neg_inf(), 0.0f, 0.0f};
+    const int64_t one = r.single();
+    if (one >= 0) {
+        const float v[1] = {to_f(x[one])};
+        take<1>(a, v);
+    }
+    for (int v = threadIdx.x; v < r.vecs; v += AHEAD * THREADS) {
+        uint4 raw[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (v + k * THREADS < r.vecs) raw[k] = r.body()[v + k * THREADS];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (v + k * THREADS < r.vecs) {
+                float e[N];
+                unpack_vec<V, N>(raw[k], e);
+                take<N>(a, e);
+            }
+    }
+    Key list = 0;
+    if constexpr (TOP) list = largest<V, THREADS>(r, a.m, p.top, shared);
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2)
+        join(a, Sums{__shfl_xor_sync(~0u, a.m, o), __shfl_xor_sync(~0u, a.s, o), __shfl_xor_sync(~0u, a.u, o)});
+    if (lane == 0) found[warp].sums = a;
+    __syncthreads();
+    if (warp == 0) {
+        a = found[lane % WARPS].sums;
+#pragma unroll
+        for (int o = WARPS / 2; o > 0; o /= 2)
+            join(a, Sums{__shfl_xor_sync(~0u, a.m, o), __shfl_xor_sync(~0u, a.s, o), __shfl_xor_sync(~0u, a.u, o)});
+    }
+    if (blocks > 1) {
+        if (warp == 0) {
+            if (lane == 0) mine->sums = a;
+            if (TOP) mine->list[lane] = list;
+        }
+        cluster_sync_all();
+        if (part == 0 && warp == 0) {
+            for (int k = 1; k < blocks; ++k) {
+                const unsigned at = cluster_map(smem_addr(mine), k);
+                Sums b;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.m) : "r"(at));
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.s) : "r"(at + 4));
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.u) : "r"(at + 8));
+                join(a, b);
+                if (TOP) {
+                    Key other;
+                    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(other) : "r"(at + (unsigned)offsetof(Found, list) + 8 * lane));
+                    merge(list, other);
+                }
+            }
+        }
+        cluster_sync_all();      // no block leaves before its results are read
+        if (part != 0) return;
+    }
+    if (warp != 0) return;
+    const bool bad = a.s != a.s, empty = a.s == 0.0f;
+    const float total = empty ? 0.0f : logf(a.s);
+    const float lse = bad ? a_nan() : empty ? neg_inf() : a.m + total;
+    if (lane == 0) {
+        if (p.lse) p.lse[row] = lse;
+        if (p.entropy) p.entropy[row] = bad ? a_nan() : empty ? 0.0f : total - a.u * kLn2 / a.s;
+        if (p.logp) {
+            const int id = p.ids[row];
+            p.logp[row] = id < 0 ? 0.0f : id >= p.V ? a_nan() : empty ? neg_inf() : to_f(x[id]) - lse;
+        }
+    }
+    if (TOP && lane < p.top) {
         if (p.top_ids) p.top_ids[row * p.top + lane] = (int)~(unsigned)list;
         if (p.top_logp) p.top_logp[row * p.top + lane] = empty ? neg_inf() : logit_of(list) - lse;
     }
 }
 
-// dlogits of one row.  Places that are the given token or an alternative get
-// a term of their own; the row's other places share
-//     -(d_logp + sum d_top) p - d_entropy p (log p + entropy).
-template <typename V>
-__global__ void __launch_bounds__(kThreads) scores_grad_kernel(const ScoreGradParams p)
+// dlogits of a row, with d_i = (x_i - lse) log2 e and p_i = 2^d_i:
+//     g_i = p_i (k0 + k1 d_i),  k0 = -(d_logp + sum d_top + d_entropy entropy),
+//                               k1 = -d_entropy log 2,
+// plus a term of its own at the given token and at each alternative.  Those
+// places are taken out before the block writes and put in after it: the
+// gradient may overwrite the logits.
+template <typename V, int THREADS>
+__global__ void __launch_bounds__(THREADS) scores_grad_kernel(const ScoreGradParams p, int blocks)
 {
+    constexpr int N = 16 / (int)sizeof(V);
     __shared__ int at[kMaxTop + 1];
     __shared__ float extra[kMaxTop + 1];
-    const int64_t row = blockIdx.x;
+    const int64_t row = blockIdx.x / blocks;
+    const int part = blockIdx.x % blocks;
     const V* x = static_cast<const V*>(p.x) + row * p.stride;
     V* dx = static_cast<V*>(p.dx) + row * p.d_stride;
+    const int64_t per = ((p.V + blocks - 1) / blocks + N - 1) / N * N;
+    const int64_t lo = part * per < p.V ? part * per : p.V, hi = lo + per < p.V ? lo + per : p.V;
     const float lse = p.lse[row];
-    const float h = p.d_entropy ? p.entropy[row] : 0.0f, dh = p.d_entropy ? p.d_entropy[row] : 0.0f;
+    const float dh = p.d_entropy ? p.d_entropy[row] : 0.0f, h = p.d_entropy ? p.entropy[row] : 0.0f;
     const int id = p.ids ? p.ids[row] : -1;
     const float dl = p.d_logp && id >= 0 ? p.d_logp[row] : 0.0f;
-    const int terms = p.top + 1;
-    if (threadIdx.x < terms) {
-        const int j = threadIdx.x;
-        at[j] = j < p.top ? p.top_ids[row * p.top + j] : id;
-        extra[j] = j < p.top ? p.d_top[row * p.top + j] : dl;
+    const bool empty = lse == neg_inf();
+    float all = dl;
+    for (int j = 0; j < p.top; ++j) all += p.d_top[row * p.top + j];
+    const float k0 = empty ? 0.0f : -fmaf(dh, h, all), k1 = empty ? 0.0f : -dh * kLn2;
+    auto slope = [&](float v) {
+        const float d = empty ? neg_inf() : (v - lse) * kLog2e;
+        return ex2(d) * fmaf(k1, fmaxf(d, -150.0f), k0);
+    };
+    float special = 0.0f;
+    int64_t place = -1;
+    if (p.top > 0) {
+        if (threadIdx.x <= p.top) {
+            const int j = threadIdx.x;
+            at[j] = j < p.top ? p.top_ids[row * p.top + j] : id;
+            extra[j] = j < p.top ? p.d_top[row * p.top + j] : dl;
+        }
+        __syncthreads();
+        if (threadIdx.x <= p.top) place = at[threadIdx.x];
+    } else if (threadIdx.x == 0) {
+        place = id;
+    }
+    if (place >= lo && place < hi) {
+        special = slope(to_f(x[place]));
+        if (!empty) {
+            if (p.top > 0) {
+                for (int j = 0; j <= p.top; ++j)
+                    if (at[j] == place) special += extra[j];
+            } else {
+                special += dl;
+            }
+        }
+    } else {
+        place = -1;
     }
     __syncthreads();
-    float all = 0.0f;
-    for (int j = 0; j < terms; ++j) all += extra[j];
-    const bool empty = lse == neg_inf();
-    for (int64_t i = threadIdx.x; i < p.V; i += kThreads) {
-        float g = 0.0f;
-        if (!empty) {
-            const float l = to_f(x[i]) - lse, pr = expf(l);
-            g = -all * pr;
-            if (pr > 0.0f) g -= dh * pr * (l + h);
-            if (pr != pr) g = pr;
-            for (int j = 0; j < terms; ++j)
-                if (at[j] == i) g += extra[j];
-        }
-        dx[i] = from_f<V>(g);
+
+    const int64_t head = to_boundary(dx, lo, hi), vecs = (hi - lo - head) / N, tail = lo + head + vecs * N;
+    const bool same = (uintptr_t)(x + lo + head) % 16 == 0;      // 16-byte loads as well as stores
+    {
+        const int64_t i = threadIdx.x < head ? lo + threadIdx.x : tail + threadIdx.x - head;
+        if (threadIdx.x < head || i < hi) dx[i] = from_f<V>(slope(to_f(x[i])));
     }
+    const f2 scale = dup2(kLog2e), k0_2 = dup2(k0), k1_2 = dup2(k1), minus = dup2(-lse);
+    auto body = [&](const uint4& raw, int64_t v) {
+        float e[N];
+        unpack_vec<V, N>(raw, e);
+        __align__(16) V out[N];
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const f2 d = mul2(add2(pack2(e[i], e[i + 1]), minus), scale);
+            float d0, d1;
+            unpack2(d, d0, d1);
+            const f2 g = mul2(ex2_2(d), fma2(k1_2, pack2(fmaxf(d0, -150.0f), fmaxf(d1, -150.0f)), k0_2));
+            unpack2(g, d0, d1);
+            out[i] = from_f<V>(d0);
+            out[i + 1] = from_f<V>(d1);
+        }
+        __stcs(reinterpret_cast<uint4*>(dx + lo + head) + v, *reinterpret_cast<uint4*>(out));
+    };
+    auto load = [&](int64_t v) {
+        const V* from = x + lo + head + v * N;
+        if (same) return __ldcs(reinterpret_cast<const uint4*>(from));
+        __align__(16) V e[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) e[i] = from[i];
+        return *reinterpret_cast<uint4*>(e);
+    };
+    if (empty) {
+        for (int64_t v = threadIdx.x; v < vecs; v += THREADS)
+            reinterpret_cast<uint4*>(dx + lo + head)[v] = make_uint4(0, 0, 0, 0);
+    } else {
+        for (int64_t v = threadIdx.x; v < vecs; v += 2 * THREADS) {
+            const bool two = v + THREADS < vecs;
+            const uint4 a = load(v);
+            uint4 b = a;
+            if (two) b = load(v + THREADS);
+            body(a, v);
+            if (two) body(b, v + THREADS);
+        }
+    }
+    __syncthreads();
+    if (place >= 0) dx[place] = from_f<V>(special);
+}
+
+// Blocks of a row.  One while the rows give every SM four blocks (2048
+// threads hold enough loads in flight); fewer rows are split, down to 2048
+// logits a block.
+int blocks_of(int64_t rows, int64_t V, int sms, int most)
+{
+    int b = 1;
+    while (b < most && rows * b < 4 * (int64_t)sms && V / (2 * b) >= 2048) b *= 2;
+    return b;
+}
+
+// Threads of a block with `per` logits: enough 16-byte pieces for each.
+int threads_of(int64_t per) { return per < 4096 ? 64 : 256; }
+
+template <typename V, int THREADS, bool TOP>
+cudaError_t run(const ScoreParams& p, int blocks, cudaStream_t s)
+{
+    if (blocks == 1) {
+        scores_kernel<V, THREADS, TOP><<<(unsigned)p.rows, THREADS, 0, s>>>(p, 1);
+        return cudaGetLastError();
+    }
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)(p.rows * blocks));
+    c.blockDim = dim3(THREADS);
+    c.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = blocks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    c.attrs = attr;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, scores_kernel<V, THREADS, TOP>, p, blocks);
+}
+template <typename V>
+cudaError_t run(const ScoreParams& p, int blocks, cudaStream_t s)
+{
+    const bool few = threads_of(p.V / blocks) == 64;
+    if (p.top) return few ? run<V, 64, true>(p, blocks, s) : run<V, 256, true>(p, blocks, s);
+    return few ? run<V, 64, false>(p, blocks, s) : run<V, 256, false>(p, blocks, s);
+}
+template <typename V>
+cudaError_t run_grad(const ScoreGradParams& p, int blocks, cudaStream_t s)
+{
+    const unsigned grid = (unsigned)(p.rows * blocks);
+    if (threads_of(p.V / blocks) == 64) scores_grad_kernel<V, 64><<<grid, 64, 0, s>>>(p, blocks);
+    else scores_grad_kernel<V, 256><<<grid, 256, 0, s>>>(p, blocks);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_scores(const ScoreParams& p, cudaStream_t s, int* launches)
 {
+    int sms = 0;
+    cudaError_t e = ssm_sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    const int blocks = blocks_of(p.rows, p.V, sms, kMaxCluster);
     ++*launches;
-    const unsigned grid = (unsigned)p.rows;
-    if (p.io == 1) scores_kernel<__half><<<grid, kThreads, 0, s>>>(p);
-    else if (p.io == 2) scores_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(p);
-    else scores_kernel<float><<<grid, kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return p.io == 1 ? run<__half>(p, blocks, s) : p.io == 2 ? run<__nv_bfloat16>(p, blocks, s) : run<float>(p, blocks, s);
 }
 
 cudaError_t launch_scores_grad(const ScoreGradParams& p, cudaStream_t s, int* launches)
 {
+    int sms = 0;
+    cudaError_t e = ssm_sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    const int blocks = blocks_of(p.rows, p.V, sms, 64);
     ++*launches;
-    const unsigned grid = (unsigned)p.rows;
-    if (p.io == 1) scores_grad_kernel<__half><<<grid, kThreads, 0, s>>>(p);
-    else if (p.io == 2) scores_grad_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(p);
-    else scores_grad_kernel<float><<<grid, kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return p.io == 1   ? run_grad<__half>(p, blocks, s)
+           : p.io == 2 ? run_grad<__nv_bfloat16>(p, blocks, s)
+                       : run_grad<float>(p, blocks, s);
 }
 
 }  // namespace rnngb
