@@ -318,7 +318,7 @@ KERNEL_SOURCES = {
     "proj_tma_kernel": ["k_proj.cu", "exact_math.cuh", "tma.cuh", "rnn_internal.h"],
     "proj_tc_kernel": ["k_proj_tc.cu", "tma.cuh", "rnn_internal.h"],
     "rnn_cell_kernel": ["k_cell.cu", "exact_math.cuh", "rnn_internal.h"],
-    "ssm_conv_kernel": ["k_ssm_conv.cu", "ssm_api.cpp"] + _SSM,
+    "ssm_conv_kernel": ["k_ssm_conv.cu", "ssm_tile.cuh", "ssm_api.cpp"] + _SSM,
     "ssm_scan_kernel": ["k_ssm_scan.cu", "ssm_tile.cuh", "ssm_api.cpp"] + _SSM,
     "ssm_scan_grad_kernel": ["k_ssm_scan_grad.cu", "ssm_tile.cuh", "ssm_api.cpp"] + _SSM,
     "ssm_scan_step_kernel": ["k_ssm_step.cu", "ssm_tile.cuh", "ssm_api.cpp"] + _SSM,

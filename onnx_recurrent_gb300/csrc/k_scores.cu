@@ -9,15 +9,17 @@
 // both parts of the entropy are >= 0, so nothing cancels.  A -inf adds 0 to
 // both sums (u takes d no lower than -150, where 2^d is 0); a NaN or +inf makes s NaN.
 //
-// Alternatives: the pass leaves every thread its largest logit.  With j = top /
-// warps, rounded up, the smallest of the warps' j-th largest is a bound that at
-// least `top` logits reach; only threads whose own largest reaches it look at their
-// logits again and put those that do in a list, which is sorted: keys are whole numbers that sort like (logit, lowest place
-// first).  If too many reach it (many equal logits), each warp keeps a sorted list of the 32
-// largest keys instead, one per lane, and inserts what is above the last one wanted
-// (done for every row, that took 677 us for 8192 rows of 32000 bf16 logits,
-// top 20).  Sorted lists are joined by taking the larger of one and the other reversed,
-// and sorting that.
+// Alternatives: the pass leaves every thread its largest logit.  The `top`-th
+// largest of these is a bound that at least `top` logits reach, and logits that reach it
+// are few: they belong to threads whose own largest does.  Warps read such threads'
+// logits again, all lanes one thread's, and put those that reach the bound in a
+// list, which is sorted: keys are whole numbers that sort like (logit, lowest place
+// first).  If many logits equal the bound (a masked row, say), only those above it and the
+// first equal ones are taken; if even those above it are too many, each warp
+// keeps a sorted list of the 32 largest keys, one per lane, and inserts what is above the
+// last one wanted (done for every row, that took 677 us for 8192 rows of
+// 32000 bf16 logits, top 20, against 163 us this way).  Sorted lists are joined by
+// taking the larger of one and the other reversed, and sorting that.
 //
 // The bytes bound it: a logit is read once (twice with the gradient, which
 // writes it once); about 5 instructions a logit, of 11 that the SMs have
@@ -62,14 +64,15 @@ __device__ __forceinline__ void insert(Key& list, Key c)
     list = lane < at ? list : lane == at ? c : up;
 }
 // The 32 largest of two sorted lists, sorted.
-__device__ __forceinline__ void merge(Key& list, Key other)
+template <typename T>
+__device__ __forceinline__ void merge(T& list, T other)
 {
     const int lane = threadIdx.x % 32;
-    const Key back = __shfl_sync(~0u, other, 31 - lane);
+    const T back = __shfl_sync(~0u, other, 31 - lane);
     list = list > back ? list : back;
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) {
-        const Key far = __shfl_xor_sync(~0u, list, o);
+        const T far = __shfl_xor_sync(~0u, list, o);
         list = (lane & o) == 0 ? (list > far ? list : far) : (list > far ? far : list);
     }
 }
@@ -184,12 +187,12 @@ struct Part {
         first = lo + to_boundary(x, lo, hi);
         vecs = (int)((hi - first) / N);
     }
-    // This thread's single logit's place, or -1: at most 14 threads have one.
-    __device__ __forceinline__ int64_t single() const
+    // The place of thread t's single logit, or -1: at most 14 threads have one.
+    __device__ __forceinline__ int64_t single(int t) const
     {
-        const int64_t i = lo + threadIdx.x;
+        const int64_t i = lo + t;
         const int64_t at = i < first ? i : i + (int64_t)vecs * N;      // the tail's threads come after the head's
-        return at < hi && threadIdx.x < 2 * N ? at : -1;
+        return at < hi && t < 2 * N ? at : -1;
     }
     __device__ __forceinline__ const uint4* body() const { return reinterpret_cast<const uint4*>(x + first); }
 };
@@ -204,7 +207,8 @@ template <int WARPS>
 struct Shared {
     Found found[WARPS];
     Found mine;
-    unsigned most[WARPS], count;
+    unsigned most[WARPS][32], bound, threads, count;
+    unsigned short again[32 * WARPS];
     Key candidates[kCandidates];
 };
 
@@ -213,45 +217,92 @@ struct Shared {
 template <typename V, int THREADS>
 __device__ __forceinline__ Key largest(const Part<V>& r, float most, int top, Shared<THREADS / 32>& sh)
 {
-    constexpr int N = Part<V>::N, WARPS = THREADS / 32, AHEAD = 4;
+    constexpr int N = Part<V>::N, WARPS = THREADS / 32;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const unsigned own = order_of(most);
-    const unsigned in_order = sorted(own);
-    if (lane == (top + WARPS - 1) / WARPS - 1) sh.most[warp] = in_order;
-    if (threadIdx.x == 0) sh.count = 0;
+    sh.most[warp][lane] = sorted(own);
+    if (threadIdx.x == 0) sh.count = sh.threads = 0;
     __syncthreads();
-    unsigned bound = sh.most[0];
+    if (warp == 0) {
+        unsigned v = sh.most[0][lane];
 #pragma unroll
-    for (int w = 1; w < WARPS; ++w) bound = bound < sh.most[w] ? bound : sh.most[w];
-    auto put = [&](float v, int64_t i) {
-        if (order_of(v) < bound) return;
-        const unsigned at = atomicAdd(&sh.count, 1u);      // their order does not matter: they are sorted
-        if (at < kCandidates) sh.candidates[at] = key_of(v, (unsigned)i);
-    };
-    if (own >= bound) {
-        const int64_t one = r.single();
-        if (one >= 0) put(to_f(r.x[one]), one);
-        for (int v = threadIdx.x; v < r.vecs; v += AHEAD * THREADS) {
-            uint4 raw[AHEAD];
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k)
-                if (v + k * THREADS < r.vecs) raw[k] = r.body()[v + k * THREADS];
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k) {
-                if (v + k * THREADS >= r.vecs) break;
-                float e[N];
-                unpack_vec<V, N>(raw[k], e);
-                float of = e[0];
-#pragma unroll
-                for (int i = 1; i < N; ++i) of = max_nan(of, e[i]);
-                if (order_of(of) < bound) continue;
-#pragma unroll
-                for (int i = 0; i < N; ++i) put(e[i], r.first + (int64_t)(v + k * THREADS) * N + i);
-            }
-        }
+        for (int w = 1; w < WARPS; ++w) merge(v, sh.most[w][lane]);
+        if (lane == top - 1) sh.bound = v;
     }
     __syncthreads();
-    const unsigned count = sh.count;
+    const unsigned bound = sh.bound;
+    if (own >= bound) sh.again[atomicAdd(&sh.threads, 1u)] = threadIdx.x;
+    __syncthreads();
+    // Logits of at least `from` go into the list (their order there does not matter).
+    auto put = [&](float v, int64_t i, unsigned long long from) {
+        if (order_of(v) < from) return;
+        const unsigned at = atomicAdd(&sh.count, 1u);
+        if (at < kCandidates) sh.candidates[at] = key_of(v, (unsigned)i);
+    };
+    auto look = [&](int v, unsigned long long from) {
+        float e[N];
+        unpack_vec<V, N>(r.body()[v], e);
+        float of = e[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) of = max_nan(of, e[i]);
+        if (order_of(of) < from) return;
+#pragma unroll
+        for (int i = 0; i < N; ++i) put(e[i], r.first + (int64_t)v * N + i, from);
+    };
+    const unsigned threads = sh.threads;
+    auto again = [&](unsigned long long from) {
+        if (threads <= THREADS / 4) {
+            for (unsigned k = warp; k < threads; k += WARPS) {
+                const int t = sh.again[k];
+                const int64_t one = r.single(t);
+                if (lane == 0 && one >= 0) put(to_f(r.x[one]), one, from);
+                for (int v = t + lane * THREADS; v < r.vecs; v += 32 * THREADS) look(v, from);
+            }
+        } else if (own >= bound) {
+            const int64_t one = r.single(threadIdx.x);
+            if (one >= 0) put(to_f(r.x[one]), one, from);
+#pragma unroll 2
+            for (int v = threadIdx.x; v < r.vecs; v += THREADS) look(v, from);
+        }
+    };
+    again(bound);
+    __syncthreads();
+    unsigned count = sh.count;
+    __syncthreads();
+    if (count > kCandidates) {
+        // Many logits equal the bound: those above it, and the first `top` equal ones.
+        if (threadIdx.x == 0) sh.count = 0;
+        __syncthreads();
+        again((unsigned long long)bound + 1);
+        __syncthreads();
+        count = sh.count;
+        __syncthreads();
+        if (count <= kCandidates - 32 * 4 && warp == 0) {
+            unsigned found = 0;
+            for (int64_t i0 = r.lo; i0 < r.hi && found < top; i0 += 32 * 4) {
+                bool same[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int64_t i = i0 + k * 32 + lane;
+                    same[k] = i < r.hi && order_of(to_f(r.x[i])) == bound;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const unsigned hits = __ballot_sync(~0u, same[k]);
+                    const unsigned at = count + found + __popc(hits & ((1u << lane) - 1));
+                    const int64_t i = i0 + k * 32 + lane;
+                    // (a NaN's key says so whatever the NaN, and -0's is +0's)
+                    if (same[k] && at < kCandidates) sh.candidates[at] = (Key)bound << 32 | (unsigned)~(unsigned)i;
+                    found += __popc(hits);
+                }
+            }
+            if (lane == 0) sh.count = count + found < kCandidates ? count + found : kCandidates;
+        } else if (count > kCandidates - 32 * 4 && threadIdx.x == 0) {
+            sh.count = kCandidates + 1;
+        }
+        __syncthreads();
+        count = sh.count;
+    }
     Key list = 0;
     if (count <= kCandidates) {
         for (unsigned i = warp * 32; i < count; i += THREADS)
@@ -282,7 +333,7 @@ __device__ __forceinline__ Key largest(const Part<V>& r, float most, int top, Sh
 }
 
 template <typename V, int THREADS, bool TOP>
-__global__ void __launch_bounds__(THREADS, TOP ? 0 : 2048 / THREADS) scores_kernel(const ScoreParams p, int blocks)
+__global__ void __launch_bounds__(THREADS, 2048 / THREADS) scores_kernel(const ScoreParams p, int blocks)
 {
     constexpr int N = Part<V>::N, AHEAD = 2, WARPS = THREADS / 32;
     __shared__ std::conditional_t<TOP, Shared<WARPS>, Found[WARPS + 1]> shared;
@@ -294,7 +345,7 @@ __global__ void __launch_bounds__(THREADS, TOP ? 0 : 2048 / THREADS) scores_kern
     const V* x = static_cast<const V*>(p.x) + row * p.stride;
     const Part<V> r(x, p.V, part, blocks);
     Sums a{neg_inf(), 0.0f, 0.0f};
-    const int64_t one = r.single();
+    const int64_t one = r.single(threadIdx.x);
     if (one >= 0) {
         const float v[1] = {to_f(x[one])};
         take<1>(a, v);

@@ -1,126 +1,304 @@
 // Short causal convolution over time for each channel (the formulas stand in
 // include/onnx_recurrent.h), its gradients and its single-token form.
 //
-// A thread takes one channel of one row and walks along a run of steps with
-// the last K inputs in registers, so each input is read once (and K - 1 again
-// at the start of a run).  The gradient's walk keeps the last K slopes of the
-// sums as well: with pre[t] = bias + sum_j W[j] X[t-K+1+j] and
-// e[t] = dY[t] f'(pre[t]),
+// The bytes bound it: 2 (4 with the gradient) 16-bit values an element, 12 (30)
+// instructions, of which the SMs have time for 40.  A thread takes NV
+// neighbouring channels of one row (four where the tensors allow it) and
+// walks along a run of steps with the next K sums in registers, so each
+// input is read once (and K - 1 again at the start of a run).  The thread's
+// inputs of the next kRing steps are on their way to its own places in shared memory,
+// so no barrier is needed and loads in flight cost no registers (with the
+// next four steps' in registers instead: 51 to 76 us for 8 rows of 2048 steps x 2048
+// bf16 channels, 32 us this way).  The gradient's walk
+// keeps the last K inputs and slopes of the sums: with pre[t] = bias + sum_j W[j]
+// X[t-K+1+j] and e[t] = dY[t] f'(pre[t]),
 //     dX[u] = sum_j W[j] e[u+K-1-j],   dW[j] = sum_t e[t] X[t-K+1+j],
-// so after step t the walk can write dX[t-K+1].
-#include "ssm_math.cuh"
+// so after step t the walk can write dX[t-K+1].  dW and dbias are summed over
+// a run in registers, then over runs and rows in order by a kernel of their own.
+#include <initializer_list>
+
+#include "ssm_tile.cuh"
 
 namespace rnngb {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kRun = 32;          // steps of one thread's walk
+constexpr int kRing = 8;          // steps whose inputs are in flight
+constexpr int kUnroll = 4;        // steps of a loop's body: the K values in registers then rotate without moves
 
-template <typename T, int K>
-__device__ __forceinline__ float conv_input(const ConvParams& p, int64_t n, int64_t t, int64_t d)
+template <typename T, int NV>
+struct __align__(sizeof(T) * NV) Vec {
+    T v[NV];
+};
+
+// The NV channels from d on of step t (a carried one for t < 0), or zeros.
+template <typename T, int K, int NV>
+__device__ __forceinline__ Vec<T, NV> conv_input(const ConvParams& p, int64_t n, int64_t t, int64_t d)
 {
-    if (t >= 0) return to_f(static_cast<const T*>(p.X.data)[t * p.X.ss + n * p.X.bs + d]);
-    if (!p.h0) return 0.0f;
-    return to_f(static_cast<const T*>(p.h0)[(n * (K - 1) + (t + K - 1)) * p.D + d]);
+    const T* from;
+    if (t >= 0) from = static_cast<const T*>(p.X.data) + t * p.X.ss + n * p.X.bs + d;
+    else from = p.h0 ? static_cast<const T*>(p.h0) + (n * (K - 1) + (t + K - 1)) * p.D + d : nullptr;
+    Vec<T, NV> r;
+    if (from) {
+        r = *reinterpret_cast<const Vec<T, NV>*>(from);
+    } else {
+#pragma unroll
+        for (int e = 0; e < NV; ++e) r.v[e] = from_f<T>(0.0f);
+    }
+    return r;
 }
 
-template <typename T, int K>
-__global__ void __launch_bounds__(kThreads) ssm_conv_kernel(const ConvParams p, int dblocks, int runs)
+// N floats, in 16-byte pieces where they allow it.
+template <int N>
+__device__ __forceinline__ void load_floats(const float* from, float (&to)[N])
 {
-    const int64_t d = (int64_t)(blockIdx.x % dblocks) * kThreads + threadIdx.x;
-    const int64_t t0 = (int64_t)(blockIdx.x / dblocks % runs) * kRun;
-    const int64_t n = blockIdx.x / dblocks / runs;
-    if (d >= p.D) return;
-    const int64_t len = row_length(p.lens, n, p.S, p.status);
-    const int64_t t1 = t0 + kRun < p.S ? t0 + kRun : p.S;
-    float w[K], x[K];
+    if (N % 4 == 0 && (uintptr_t)from % 16 == 0) {
 #pragma unroll
-    for (int j = 0; j < K; ++j) w[j] = p.W[d * K + j];
-    const float b = p.bias ? p.bias[d] : 0.0f;
-#pragma unroll
-    for (int j = 1; j < K; ++j) x[j] = t0 < len ? conv_input<T, K>(p, n, t0 - K + j, d) : 0.0f;
-    T* y = static_cast<T*>(p.Y.data) + n * p.Y.bs + d;
-    for (int64_t t = t0; t < t1; ++t) {
-        float v = 0.0f;
-        if (t < len) {
-#pragma unroll
-            for (int j = 0; j + 1 < K; ++j) x[j] = x[j + 1];
-            x[K - 1] = conv_input<T, K>(p, n, t, d);
-            v = b;
-#pragma unroll
-            for (int j = 0; j < K; ++j) v = fmaf(w[j], x[j], v);
-            if (p.silu) v = silu_f(v);
+        for (int i = 0; i < N / 4; ++i) {
+            const float4 v = reinterpret_cast<const float4*>(from)[i];
+            to[4 * i] = v.x, to[4 * i + 1] = v.y, to[4 * i + 2] = v.z, to[4 * i + 3] = v.w;
         }
-        y[t * p.Y.ss] = from_f<T>(v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) to[i] = from[i];
     }
+}
+// A thread's own ring of inputs.
+template <typename T, int NV>
+struct Ring {
+    using V = Vec<T, NV>;
+    static constexpr bool ASYNC = sizeof(V) >= 4;      // a single 16-bit value is too small to copy
+    V* at;                                             // this thread's place in each slot, kThreads apart
+
+    // Step's values to the slot, or zeros.
+    __device__ __forceinline__ void start(int slot, const T* from, bool on, const void* valid) const
+    {
+        if constexpr (ASYNC) {
+            const unsigned d = (unsigned)__cvta_generic_to_shared(at + slot * kThreads);
+            const void* src = on ? from : valid;
+            const int bytes = on ? (int)sizeof(V) : 0;
+            if constexpr (sizeof(V) == 16)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(d), "l"(src), "r"(bytes) : "memory");
+            else
+                asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;\n" ::"r"(d), "l"(src), "r"(bytes), "n"((int)sizeof(V)) : "memory");
+        } else {
+            at[slot * kThreads].v[0] = on ? *from : from_f<T>(0.0f);
+        }
+    }
+    // Without asynchronous copies: a body's steps at once, so that their loads overlap.
+    __device__ __forceinline__ void refill(int slot, const T* from, int64_t ss, int left) const
+    {
+        T v[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) v[i] = i < left ? from[i * ss] : from_f<T>(0.0f);
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) at[(slot + i) % kRing * kThreads].v[0] = v[i];
+    }
+    __device__ __forceinline__ V get(int slot) const { return at[slot * kThreads]; }
+};
+
+template <int K, int NV>
+struct Weights {
+    float w[NV * K], bias[NV];
+    __device__ __forceinline__ Weights(const ConvParams& p, int64_t d)
+    {
+        load_floats(p.W + d * K, w);
+        if (p.bias) {
+            load_floats(p.bias + d, bias);
+        } else {
+#pragma unroll
+            for (int e = 0; e < NV; ++e) bias[e] = 0.0f;
+        }
+    }
+    __device__ __forceinline__ float of(int tap, int e) const { return w[e * K + tap]; }
+};
+
+// What a thread has: channels d .., row n, steps t0 .. t1-1; false: nothing.
+template <int NV>
+__device__ __forceinline__ bool find(const ConvParams& p, unsigned dblocks, unsigned runs, int run, int64_t& d, int64_t& n,
+                                     int64_t& t0, int64_t& t1)
+{
+    d = ((int64_t)(blockIdx.x % dblocks) * kThreads + threadIdx.x) * NV;
+    t0 = (int64_t)(blockIdx.x / dblocks % runs) * run;
+    n = blockIdx.x / dblocks / runs;
+    t1 = t0 + run < p.S ? t0 + run : p.S;
+    return d < p.D;
+}
+
+template <typename T, int K, int NV>
+__global__ void __launch_bounds__(kThreads, K <= 4 ? 8 : 4) ssm_conv_kernel(const ConvParams p, unsigned dblocks, unsigned runs, int run)
+{
+    __shared__ Vec<T, NV> ring_mem[kRing][kThreads];
+    int64_t d, n, t0, t1;
+    if (!find<NV>(p, dblocks, runs, run, d, n, t0, t1)) return;
+    const int64_t len = row_length(p.lens, n, p.S, p.status);
+    const int64_t live = len < t1 ? len : t1;
+    T* y = static_cast<T*>(p.Y.data) + n * p.Y.bs + d;
+    if (t0 < live) {
+        const Weights<K, NV> w(p, d);
+        // sums[i]: what the inputs so far give to the sum i steps ahead, taps in order from the bias
+        float sums[K][NV];
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+#pragma unroll
+            for (int e = 0; e < NV; ++e) sums[j][e] = w.bias[e];
+        // takes the next input, returns the sum that it completes
+        auto next = [&](float x, int e) {
+            const float done = fmaf(w.of(K - 1, e), x, sums[0][e]);
+#pragma unroll
+            for (int j = 0; j + 1 < K; ++j) sums[j][e] = fmaf(w.of(K - 2 - j, e), x, sums[j + 1][e]);
+            return done;
+        };
+#pragma unroll
+        for (int j = 0; j + 1 < K; ++j) {
+            const Vec<T, NV> r = conv_input<T, K, NV>(p, n, t0 - K + 1 + j, d);
+#pragma unroll
+            for (int e = 0; e < NV; ++e) next(to_f(r.v[e]), e);
+        }
+        const Ring<T, NV> ring{ring_mem[0] + threadIdx.x};
+        const T* x = static_cast<const T*>(p.X.data) + n * p.X.bs + d;
+#pragma unroll
+        for (int i = 0; i < kRing; ++i) {
+            ring.start(i, x + (t0 + i) * p.X.ss, t0 + i < live, p.X.data);
+            cp_async_commit();
+        }
+        const int steps = (int)(live - t0);
+        for (int i0 = 0; i0 < steps; i0 += kUnroll) {
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) {
+                const int slot = (i0 + i) % kRing;
+                cp_async_wait<kRing - 1>();
+                const Vec<T, NV> r = ring.get(slot);
+                Vec<T, NV> out;
+#pragma unroll
+                for (int e = 0; e < NV; ++e) {
+                    const float v = next(to_f(r.v[e]), e);
+                    out.v[e] = from_f<T>(p.silu ? silu_fast(v) : v);
+                }
+                if (i0 + i < steps) *reinterpret_cast<Vec<T, NV>*>(y + (t0 + i0 + i) * p.Y.ss) = out;
+                if (ring.ASYNC) ring.start(slot, x + (t0 + i0 + i + kRing) * p.X.ss, i0 + i + kRing < steps, p.X.data);
+                cp_async_commit();
+            }
+            if (!ring.ASYNC) ring.refill(i0, x + (t0 + i0 + kRing) * p.X.ss, p.X.ss, steps - i0 - kRing);
+        }
+        cp_async_wait<0>();
+    }
+    Vec<T, NV> zero;
+#pragma unroll
+    for (int e = 0; e < NV; ++e) zero.v[e] = from_f<T>(0.0f);
+    for (int64_t t = live > t0 ? live : t0; t < t1; ++t) *reinterpret_cast<Vec<T, NV>*>(y + t * p.Y.ss) = zero;
     if (t0 == 0 && p.hT) {   // the last K-1 inputs, reaching back into the carried ones
 #pragma unroll
         for (int j = 0; j + 1 < K; ++j)
-            static_cast<T*>(p.hT)[(n * (K - 1) + j) * p.D + d] = from_f<T>(conv_input<T, K>(p, n, len - K + 1 + j, d));
+            *reinterpret_cast<Vec<T, NV>*>(static_cast<T*>(p.hT) + (n * (K - 1) + j) * p.D + d) =
+                conv_input<T, K, NV>(p, n, len - K + 1 + j, d);
     }
 }
 
-template <typename T, int K>
-__global__ void __launch_bounds__(kThreads) ssm_conv_grad_kernel(const ConvGradParams q, int dblocks, int runs)
+template <typename T, int K, int NV>
+__global__ void __launch_bounds__(kThreads, K <= 4 ? 5 : 3) ssm_conv_grad_kernel(const ConvGradParams q, unsigned dblocks, unsigned runs, int run)
 {
     const ConvParams& p = q.f;
-    const int64_t d = (int64_t)(blockIdx.x % dblocks) * kThreads + threadIdx.x;
-    const int64_t run = blockIdx.x / dblocks % runs;
-    const int64_t n = blockIdx.x / dblocks / runs;
-    if (d >= p.D) return;
-    const int64_t t0 = run * kRun;
+    __shared__ Vec<T, NV> ring_mem[2][kRing][kThreads];
+    int64_t d, n, t0, t1;
+    if (!find<NV>(p, dblocks, runs, run, d, n, t0, t1)) return;
     const int64_t len = row_length(p.lens, n, p.S, p.status);
-    const int64_t t1 = t0 + kRun < p.S ? t0 + kRun : p.S;
-    float w[K], x[K], e[K], dw[K];
+    const Weights<K, NV> w(p, d);
+    float x[K][NV], s[K][NV], dw[K][NV], db[NV];
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-        w[j] = p.W[d * K + j];
-        dw[j] = e[j] = 0.0f;
-        x[j] = j > 0 && t0 < len ? conv_input<T, K>(p, n, t0 - K + j, d) : 0.0f;
+        Vec<T, NV> r;
+        const bool on = j > 0 && t0 < len;
+        if (on) r = conv_input<T, K, NV>(p, n, t0 - K + j, d);
+#pragma unroll
+        for (int e = 0; e < NV; ++e) {
+            x[j][e] = on ? to_f(r.v[e]) : 0.0f;
+            s[j][e] = dw[j][e] = db[e] = 0.0f;
+        }
     }
-    const float b = p.bias ? p.bias[d] : 0.0f;
-    float db = 0.0f;
     const T* dy = static_cast<const T*>(q.dY.data) + n * q.dY.bs + d;
     const T* dhT = static_cast<const T*>(q.dhT);
+    const Ring<T, NV> ring_x{ring_mem[0][0] + threadIdx.x}, ring_y{ring_mem[1][0] + threadIdx.x};
+    const T* xs = static_cast<const T*>(p.X.data) + n * p.X.bs + d;
     // slopes of the run's steps, and of the K-1 after it that its inputs reach
-    for (int64_t t = t0; t < t1 + K - 1; ++t) {
+    const int steps = (int)(t1 - t0) + K - 1, known = len - t0 < steps ? (int)(len > t0 ? len - t0 : 0) : steps;
+    auto start = [&](int i) {
+        ring_x.start(i % kRing, xs + (t0 + i) * p.X.ss, i < known, p.X.data);
+        ring_y.start(i % kRing, dy + (t0 + i) * q.dY.ss, i < known, p.X.data);
+        cp_async_commit();
+    };
 #pragma unroll
-        for (int j = 0; j + 1 < K; ++j) {
-            x[j] = x[j + 1];
-            e[j] = e[j + 1];
-        }
-        x[K - 1] = e[K - 1] = 0.0f;
-        if (t < len) {
-            x[K - 1] = conv_input<T, K>(p, n, t, d);
-            float v = b;
+    for (int i = 0; i < kRing; ++i) start(i);
+    for (int i0 = 0; i0 < steps; i0 += kUnroll) {
 #pragma unroll
-            for (int j = 0; j < K; ++j) v = fmaf(w[j], x[j], v);
-            const float s = to_f(dy[t * q.dY.ss]);
-            e[K - 1] = p.silu ? s * silu_slope(v) : s;
-            if (t < t1) {
-                db += e[K - 1];
+        for (int i = 0; i < kUnroll; ++i) {
+            const int k = i0 + i;
+            cp_async_wait<kRing - 1>();
+            const Vec<T, NV> rx = ring_x.get(k % kRing), ry = ring_y.get(k % kRing);
+            const bool own = k < known && k < (int)(t1 - t0);
 #pragma unroll
-                for (int j = 0; j < K; ++j) dw[j] = fmaf(e[K - 1], x[j], dw[j]);
+            for (int e = 0; e < NV; ++e) {
+#pragma unroll
+                for (int j = 0; j + 1 < K; ++j) {
+                    x[j][e] = x[j + 1][e];
+                    s[j][e] = s[j + 1][e];
+                }
+                x[K - 1][e] = to_f(rx.v[e]);           // zero past the row's end, as is dY
+                float v = w.bias[e];
+#pragma unroll
+                for (int j = 0; j < K; ++j) v = fmaf(w.of(j, e), x[j][e], v);
+                float g = to_f(ry.v[e]);
+                if (p.silu) {
+                    const float o = sigmoid_fast(v);
+                    g *= o * fmaf(v, 1.0f - o, 1.0f);
+                }
+                s[K - 1][e] = k < known ? g : 0.0f;
+                const float mine = own ? g : 0.0f;
+                db[e] += mine;
+#pragma unroll
+                for (int j = 0; j < K; ++j) dw[j][e] = fmaf(mine, x[j][e], dw[j][e]);
             }
-        }
-        const int64_t u = t - K + 1;   // the input whose slopes are complete: e[0] belongs to step u
-        if (u >= t0 || t0 == 0) {
-            float g = 0.0f;
+            const int64_t u = t0 + k - K + 1;   // the input whose slopes are complete: s[0] belongs to step u
+            if (k < steps && (u >= t0 || t0 == 0)) {
+                float g[NV];
 #pragma unroll
-            for (int j = 0; j < K; ++j) g = fmaf(w[K - 1 - j], e[j], g);
-            if (dhT && u >= len - (K - 1) && u < len) g += to_f(dhT[(n * (K - 1) + (u - len + K - 1)) * p.D + d]);
-            if (u >= 0) {
-                if (q.dX.data) static_cast<T*>(q.dX.data)[u * q.dX.ss + n * q.dX.bs + d] = from_f<T>(g);
-            } else if (q.dh0) {
-                static_cast<T*>(q.dh0)[(n * (K - 1) + (u + K - 1)) * p.D + d] = from_f<T>(g);
+                for (int e = 0; e < NV; ++e) {
+                    g[e] = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < K; ++j) g[e] = fmaf(w.of(K - 1 - j, e), s[j][e], g[e]);
+                }
+                if (dhT && u >= len - (K - 1) && u < len) {
+                    const Vec<T, NV> more = *reinterpret_cast<const Vec<T, NV>*>(dhT + (n * (K - 1) + (u - len + K - 1)) * p.D + d);
+#pragma unroll
+                    for (int e = 0; e < NV; ++e) g[e] += to_f(more.v[e]);
+                }
+                Vec<T, NV> out;
+#pragma unroll
+                for (int e = 0; e < NV; ++e) out.v[e] = from_f<T>(g[e]);
+                T* to = nullptr;
+                if (u >= 0) {
+                    if (q.dX.data) to = static_cast<T*>(q.dX.data) + u * q.dX.ss + n * q.dX.bs + d;
+                } else if (q.dh0) {
+                    to = static_cast<T*>(q.dh0) + (n * (K - 1) + (u + K - 1)) * p.D + d;
+                }
+                if (to) *reinterpret_cast<Vec<T, NV>*>(to) = out;
             }
+            if (ring_x.ASYNC) start(k + kRing);
+        }
+        if (!ring_x.ASYNC) {
+            ring_x.refill(i0, xs + (t0 + i0 + kRing) * p.X.ss, p.X.ss, known - i0 - kRing);
+            ring_y.refill(i0, dy + (t0 + i0 + kRing) * q.dY.ss, q.dY.ss, known - i0 - kRing);
         }
     }
+    cp_async_wait<0>();
     if (q.part) {
-        float* part = q.part + (n * runs + run) * p.D * (K + 1);
+        float* part = q.part + (n * runs + t0 / run) * p.D * (K + 1);
 #pragma unroll
-        for (int j = 0; j < K; ++j) part[d * K + j] = dw[j];
-        part[p.D * K + d] = db;
+        for (int e = 0; e < NV; ++e) {
+#pragma unroll
+            for (int j = 0; j < K; ++j) part[(d + e) * K + j] = dw[j][e];
+            part[p.D * K + d + e] = db[e];
+        }
     }
 }
 
@@ -149,7 +327,7 @@ __global__ void __launch_bounds__(kThreads) ssm_conv_step_kernel(const ConvStepP
     float v = p.bias ? p.bias[d] : 0.0f;
 #pragma unroll
     for (int j = 0; j < K; ++j) v = fmaf(p.W[d * K + j], to_f(x[j]), v);
-    *y = from_f<T>(p.silu ? silu_f(v) : v);
+    *y = from_f<T>(p.silu ? silu_fast(v) : v);
 #pragma unroll
     for (int j = 0; j + 1 < K; ++j) so[j * p.D] = x[j + 1];
 }
@@ -163,8 +341,10 @@ __global__ void __launch_bounds__(512) sum_parts_kernel(const float* part, int64
     const int64_t n = n0 + n1 + n2;
     const int64_t i = (int64_t)blockIdx.x * 32 + threadIdx.x;
     float s = 0.0f;
-    if (i < n)
+    if (i < n) {
+#pragma unroll 8
         for (int64_t r = threadIdx.y; r < parts; r += 16) s += part[r * n + i];
+    }
     sums[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.y != 0 || i >= n) return;
@@ -203,22 +383,84 @@ cudaError_t by_type(int io, int K, A... a)
     return by_taps<F, float>(K, a...);
 }
 
+// Channels of a thread: four (two where the gradient's K taps of four would not fit
+// the registers; eight 16-bit ones take twice the registers and no less time), two
+// for 16-bit types of even sizes, else one.
+template <typename T, int K, bool GRAD>
+constexpr int widest()
+{
+    constexpr int full = 16 / (int)sizeof(T), fits = GRAD && K > 4 ? 2 : 4;
+    return full < fits ? full : fits;
+}
+bool views_fit(std::initializer_list<View> views, std::initializer_list<const void*> states, int64_t D, int elem, int nv)
+{
+    const int64_t bytes = (int64_t)elem * nv;
+    if (D % nv) return false;
+    for (const View& v : views)
+        if (v.data && ((uintptr_t)v.data % bytes || v.ss * elem % bytes || v.bs * elem % bytes)) return false;
+    for (const void* s : states)
+        if ((uintptr_t)s % bytes) return false;
+    return true;
+}
+
+// Steps of a run: the longest that leaves the SMs enough threads (each run
+// reads K - 1 inputs again, and writes a partial dW).
+int run_of(int64_t S, int64_t threads_a_run)
+{
+    int run = 128;
+    while (run > 16 && (S + run - 1) / run * threads_a_run < 152 * 1024) run /= 2;
+    return run;
+}
+int64_t run_count(int64_t S, int run) { return S > 0 ? (S + run - 1) / run : 1; }
+constexpr int64_t kMaxGrid = 0x7fffffff;
+
 template <typename T, int K>
 struct RunConv {
-    static cudaError_t go(const ConvParams* p, unsigned grid, int db, int runs, cudaStream_t s)
+    template <int NV>
+    static cudaError_t with(const ConvParams& p, cudaStream_t s)
     {
-        ssm_conv_kernel<T, K><<<grid, kThreads, 0, s>>>(*p, db, runs);
+        const int64_t threads = (p.D + NV - 1) / NV, db = (threads + kThreads - 1) / kThreads;
+        const int run = run_of(p.S, threads * p.N);
+        const int64_t runs = run_count(p.S, run);
+        if (db * runs > kMaxGrid / p.N) return cudaErrorInvalidConfiguration;
+        ssm_conv_kernel<T, K, NV><<<(unsigned)(db * runs * p.N), kThreads, 0, s>>>(p, (unsigned)db, (unsigned)runs, run);
         return cudaGetLastError();
+    }
+    static cudaError_t go(const ConvParams* p, cudaStream_t s)
+    {
+        constexpr int W = widest<T, K, false>();
+        auto fit = [&](int nv) { return views_fit({p->X, p->Y}, {p->h0, p->hT}, p->D, sizeof(T), nv); };
+        if (fit(W)) return with<W>(*p, s);
+        if constexpr (sizeof(T) == 2 && W > 2)
+            if (fit(2)) return with<2>(*p, s);
+        return with<1>(*p, s);
     }
 };
 template <typename T, int K>
 struct RunConvGrad {
-    static cudaError_t go(const ConvGradParams* p, unsigned grid, int db, int runs, cudaStream_t s)
+    template <int NV>
+    static cudaError_t with(const ConvGradParams& q, int run, cudaStream_t s)
     {
-        ssm_conv_grad_kernel<T, K><<<grid, kThreads, 0, s>>>(*p, db, runs);
+        const ConvParams& p = q.f;
+        const int64_t threads = (p.D + NV - 1) / NV, db = (threads + kThreads - 1) / kThreads, runs = run_count(p.S, run);
+        if (db * runs > kMaxGrid / p.N) return cudaErrorInvalidConfiguration;
+        ssm_conv_grad_kernel<T, K, NV><<<(unsigned)(db * runs * p.N), kThreads, 0, s>>>(q, (unsigned)db, (unsigned)runs, run);
         return cudaGetLastError();
     }
+    static cudaError_t go(const ConvGradParams* q, int run, cudaStream_t s)
+    {
+        constexpr int W = widest<T, K, true>();
+        auto fit = [&](int nv) {
+            return views_fit({q->f.X, q->dY, q->dX}, {q->f.h0, q->dhT, q->dh0}, q->f.D, sizeof(T), nv);
+        };
+        if (fit(W)) return with<W>(*q, run, s);
+        if constexpr (sizeof(T) == 2 && W > 2)
+            if (fit(2)) return with<2>(*q, run, s);
+        return with<1>(*q, run, s);
+    }
 };
+int grad_run(const ConvParams& p) { return run_of(p.S, (p.D + 1) / 2 * p.N); }
+
 template <typename T, int K>
 struct RunConvStep {
     static cudaError_t go(const ConvStepParams* p, unsigned grid, int db, cudaStream_t s)
@@ -228,32 +470,25 @@ struct RunConvStep {
     }
 };
 
-int64_t run_count(int64_t S) { return S > 0 ? (S + kRun - 1) / kRun : 1; }
-constexpr int64_t kMaxGrid = 0x7fffffff;
-
 }  // namespace
 
 cudaError_t launch_ssm_conv(const ConvParams& p, cudaStream_t s, int* launches)
 {
-    const int64_t db = (p.D + kThreads - 1) / kThreads, runs = run_count(p.S);
-    if (db * runs > kMaxGrid / p.N) return cudaErrorInvalidConfiguration;
     ++*launches;
-    return by_type<RunConv>(p.io, p.K, &p, (unsigned)(db * runs * p.N), (int)db, (int)runs, s);
+    return by_type<RunConv>(p.io, p.K, &p, s);
 }
 
-int64_t ssm_conv_grad_parts(const ConvGradParams& p) { return p.f.N * run_count(p.f.S); }
+int64_t ssm_conv_grad_parts(const ConvGradParams& q) { return q.f.N * run_count(q.f.S, grad_run(q.f)); }
 
-cudaError_t launch_ssm_conv_grad(const ConvGradParams& p, cudaStream_t s, int* launches)
+cudaError_t launch_ssm_conv_grad(const ConvGradParams& q, cudaStream_t s, int* launches)
 {
-    const int64_t db = (p.f.D + kThreads - 1) / kThreads, runs = run_count(p.f.S);
-    if (p.f.N > 0) {
-        if (db * runs > kMaxGrid / p.f.N) return cudaErrorInvalidConfiguration;
+    if (q.f.N > 0) {
         ++*launches;
-        cudaError_t e = by_type<RunConvGrad>(p.f.io, p.f.K, &p, (unsigned)(db * runs * p.f.N), (int)db, (int)runs, s);
+        cudaError_t e = by_type<RunConvGrad>(q.f.io, q.f.K, &q, grad_run(q.f), s);
         if (e != cudaSuccess) return e;
     }
-    if (!p.dW && !p.dbias) return cudaSuccess;
-    return launch_sum_parts(p.part, p.parts, p.dW, p.f.D * p.f.K, p.dbias, p.f.D, nullptr, 0, s, launches);
+    if (!q.dW && !q.dbias) return cudaSuccess;
+    return launch_sum_parts(q.part, q.parts, q.dW, q.f.D * q.f.K, q.dbias, q.f.D, nullptr, 0, s, launches);
 }
 
 cudaError_t launch_ssm_conv_step(const ConvStepParams& p, cudaStream_t s, int* launches)

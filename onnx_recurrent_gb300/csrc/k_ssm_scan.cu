@@ -34,6 +34,8 @@
 // its delta (the product of its decays is exp(A sum delta)), a small one
 // chains them to every chunk's first state, and the scan runs over all chunks
 // at once.  That costs another exponential and three operations per update.
+#include <cmath>
+
 #include "ssm_tile.cuh"
 
 #pragma nv_diag_suppress 128   // loops that a launch for end states leaves out
@@ -385,8 +387,10 @@ constexpr int64_t kMaxGrid = 0x7fffffff;
 constexpr ScanCost kCost{4, {0, 239, 342, 375, 402}, 2500, 0.72};
 
 template <typename V, int L>
-cudaError_t run(const ScanParams& p, const ScanChoice& c, cudaStream_t s, int* launches)
+cudaError_t run(const ScanParams& p, cudaStream_t s, int* launches)
 {
+    const ScanChoice& c = p.split;
+    static std::atomic<uint64_t> ready_ends{0}, ready{0};
     using K = Tile<V, L>;
     const int elem = (int)sizeof(V);
     const int64_t dg = p.D / p.G, block = K::W * K::WC, group = p.G > 1 ? dg : 0;
@@ -411,7 +415,7 @@ cudaError_t run(const ScanParams& p, const ScanChoice& c, cudaStream_t s, int* l
     if (c.chunks > 1) {
         auto* f = ssm_scan_kernel<V, L, true>;
         const size_t smem = K::bytes(2);
-        cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaError_t e = allow_shared(f, smem, ready_ends);
         if (e != cudaSuccess) return e;
         f<<<(unsigned)(blocks * (c.chunks - 1)), K::THREADS, smem, s>>>(p, q);
         e = cudaGetLastError();
@@ -425,7 +429,7 @@ cudaError_t run(const ScanParams& p, const ScanChoice& c, cudaStream_t s, int* l
     }
     auto* f = ssm_scan_kernel<V, L, false>;
     const size_t smem = K::bytes(3);
-    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_shared(f, smem, ready);
     if (e != cudaSuccess) return e;
     f<<<(unsigned)(blocks * c.chunks), K::THREADS, smem, s>>>(p, q);
     ++*launches;
@@ -433,15 +437,15 @@ cudaError_t run(const ScanParams& p, const ScanChoice& c, cudaStream_t s, int* l
 }
 
 template <typename V>
-cudaError_t by_lanes(const ScanParams& p, const ScanChoice& c, cudaStream_t s, int* launches)
+cudaError_t by_lanes(const ScanParams& p, cudaStream_t s, int* launches)
 {
     switch (ssm_lanes(p.M)) {
-    case 1: return run<V, 1>(p, c, s, launches);
-    case 2: return run<V, 2>(p, c, s, launches);
-    case 4: return run<V, 4>(p, c, s, launches);
-    case 8: return run<V, 8>(p, c, s, launches);
-    case 16: return run<V, 16>(p, c, s, launches);
-    default: return run<V, 32>(p, c, s, launches);
+    case 1: return run<V, 1>(p, s, launches);
+    case 2: return run<V, 2>(p, s, launches);
+    case 4: return run<V, 4>(p, s, launches);
+    case 8: return run<V, 8>(p, s, launches);
+    case 16: return run<V, 16>(p, s, launches);
+    default: return run<V, 32>(p, s, launches);
     }
 }
 
@@ -455,16 +459,16 @@ ScanChoice ssm_split(const ScanParams& p, int tile, const ScanCost& cost, int sm
     const int64_t dg = p.D / p.G, tiles = (p.S + tile - 1) / tile, blocks = (dg + W * WC - 1) / (W * WC);
     const double all = (double)blocks * W * p.G * p.N / (4.0 * sms);       // warps per scheduler
     auto pass = [&](double w, double steps) {
-        const int waves = (int)(w / cost.warps);
-        const double rest = w - (double)cost.warps * waves;
-        const int r = (int)rest + (rest > (int)rest ? 1 : 0);
+        const double waves = std::floor(w / cost.warps);
+        const int r = (int)std::ceil(w - cost.warps * waves);
         return waves * (cost.begin_ns + steps * cost.step_ns[cost.warps]) + (r ? cost.begin_ns + steps * cost.step_ns[r] : 0.0);
     };
     ScanChoice best{1, blocks, (tiles > 0 ? tiles : 1) * tile};
     double least = pass(all, (double)tiles * tile);
-    for (int64_t k = 2; k <= tiles && k <= 512; ++k) {
-        const int64_t per = (tiles + k - 1) / k;
-        if ((tiles + per - 1) / per != k) continue;
+    // chunks of fewer and fewer tiles, each number of chunks once
+    for (int64_t per = (tiles + 1) / 2; per > 0 && tiles > 1;) {
+        const int64_t k = (tiles + per - 1) / per, next = (tiles + k) / (k + 1);      // `per` of k + 1 chunks
+        if (k > 512) break;
         const double steps = (double)per * tile;
         // 5 us for two launches more, and a chunk's part of their chain
         const double t = pass(all * (double)k, steps) + cost.ends * pass(all * (double)(k - 1), steps) + 5000.0 + 50.0 * (double)k;
@@ -473,6 +477,7 @@ ScanChoice ssm_split(const ScanParams& p, int tile, const ScanCost& cost, int sm
             best.chunks = (int)k;
             best.chunk = per * tile;
         }
+        per = next < per ? next : per - 1;
     }
     return best;
 }
@@ -484,24 +489,21 @@ cudaError_t ssm_sm_count(int* sms)
     return e == cudaSuccess ? cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) : e;
 }
 
-cudaError_t ssm_scan_scratch(const ScanParams& p, size_t* bytes)
+cudaError_t ssm_scan_plan(ScanParams& p, size_t* bytes)
 {
     int sms = 0;
     cudaError_t e = ssm_sm_count(&sms);
     if (e != cudaSuccess) return e;
-    *bytes = sizeof(float) * (size_t)(ssm_split(p, T, kCost, sms).chunks - 1) * (size_t)(p.N * p.D * (p.M + 1));
+    p.split = ssm_split(p, T, kCost, sms);
+    *bytes = sizeof(float) * (size_t)(p.split.chunks - 1) * (size_t)(p.N * p.D * (p.M + 1));
     return cudaSuccess;
 }
 
 cudaError_t launch_ssm_scan(const ScanParams& p, cudaStream_t s, int* launches)
 {
-    int sms = 0;
-    cudaError_t e = ssm_sm_count(&sms);
-    if (e != cudaSuccess) return e;
-    const ScanChoice c = ssm_split(p, T, kCost, sms);
-    return p.io == 1   ? by_lanes<__half>(p, c, s, launches)
-           : p.io == 2 ? by_lanes<__nv_bfloat16>(p, c, s, launches)
-                       : by_lanes<float>(p, c, s, launches);
+    return p.io == 1   ? by_lanes<__half>(p, s, launches)
+           : p.io == 2 ? by_lanes<__nv_bfloat16>(p, s, launches)
+                       : by_lanes<float>(p, s, launches);
 }
 
 }  // namespace rnngb

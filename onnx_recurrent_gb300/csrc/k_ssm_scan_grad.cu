@@ -722,10 +722,12 @@ constexpr int64_t kMaxGrid = 0x7fffffff;
 constexpr ScanCost kCost{3, {0, 687, 807, 1120}, 3000, 0.25};
 
 template <typename V, int L>
-cudaError_t run(const ScanGradParams& pp, const ScanChoice& c, cudaStream_t s, int* launches)
+cudaError_t run(const ScanGradParams& pp, cudaStream_t s, int* launches)
 {
     using K = Tile<V, L>;
     const ScanParams& p = pp.f;
+    const ScanChoice& c = p.split;
+    static std::atomic<uint64_t> ready_ends{0}, ready{0};
     const int elem = (int)sizeof(V);
     const int64_t dg = p.D / p.G, block = K::W * K::WC, group = p.G > 1 ? dg : 0;
     GradLaunch q{};
@@ -748,7 +750,7 @@ cudaError_t run(const ScanGradParams& pp, const ScanChoice& c, cudaStream_t s, i
     q.vec_dz = vec(pp.dZ);
     q.vec_h = p.M % 2 == 0 && (uintptr_t)p.saved % 8 == 0;
     const int64_t states = p.N * p.D * p.M;
-    q.ends = pp.part;
+    q.ends = p.scratch;
     q.deltas = q.ends + (c.chunks - 1) * states;
     q.part = q.deltas + (c.chunks - 1) * p.N * p.D;
     q.steps = q.part + c.chunks * p.N * p.D * (p.M + 2);
@@ -756,7 +758,7 @@ cudaError_t run(const ScanGradParams& pp, const ScanChoice& c, cudaStream_t s, i
     if (blocks > kMaxGrid / c.chunks) return cudaErrorInvalidConfiguration;
     if (c.chunks > 1) {
         auto* f = ssm_scan_grad_ends_kernel<V, L>;
-        cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::bytes_ends());
+        cudaError_t e = allow_shared(f, K::bytes_ends(), ready_ends);
         if (e != cudaSuccess) return e;
         f<<<(unsigned)(blocks * (c.chunks - 1)), K::THREADS, K::bytes_ends(), s>>>(pp, q);
         e = cudaGetLastError();
@@ -768,7 +770,7 @@ cudaError_t run(const ScanGradParams& pp, const ScanChoice& c, cudaStream_t s, i
         *launches += 2;
     }
     auto* f = ssm_scan_grad_kernel<V, L>;
-    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::bytes());
+    cudaError_t e = allow_shared(f, K::bytes(), ready);
     if (e != cudaSuccess) return e;
     f<<<(unsigned)(blocks * c.chunks), K::THREADS, K::bytes(), s>>>(pp, q);
     e = cudaGetLastError();
@@ -785,27 +787,28 @@ cudaError_t run(const ScanGradParams& pp, const ScanChoice& c, cudaStream_t s, i
 }
 
 template <typename V>
-cudaError_t by_lanes(const ScanGradParams& p, const ScanChoice& c, cudaStream_t s, int* launches)
+cudaError_t by_lanes(const ScanGradParams& p, cudaStream_t s, int* launches)
 {
     switch (ssm_lanes(p.f.M)) {
-    case 1: return run<V, 1>(p, c, s, launches);
-    case 2: return run<V, 2>(p, c, s, launches);
-    case 4: return run<V, 4>(p, c, s, launches);
-    case 8: return run<V, 8>(p, c, s, launches);
-    case 16: return run<V, 16>(p, c, s, launches);
-    default: return run<V, 32>(p, c, s, launches);
+    case 1: return run<V, 1>(p, s, launches);
+    case 2: return run<V, 2>(p, s, launches);
+    case 4: return run<V, 4>(p, s, launches);
+    case 8: return run<V, 8>(p, s, launches);
+    case 16: return run<V, 16>(p, s, launches);
+    default: return run<V, 32>(p, s, launches);
     }
 }
 
 }  // namespace
 
-cudaError_t ssm_scan_grad_scratch(const ScanGradParams& pp, size_t* bytes)
+cudaError_t ssm_scan_grad_plan(ScanGradParams& pp, size_t* bytes)
 {
     int sms = 0;
     cudaError_t e = ssm_sm_count(&sms);
     if (e != cudaSuccess) return e;
-    const ScanParams& p = pp.f;
-    const ScanChoice c = ssm_split(p, T, kCost, sms);
+    ScanParams& p = pp.f;
+    p.split = ssm_split(p, T, kCost, sms);
+    const ScanChoice& c = p.split;
     *bytes = sizeof(float) * (size_t)((c.chunks - 1) * p.N * p.D * (p.M + 1) + c.chunks * p.N * p.D * (p.M + 2) +
                                       c.cblocks * p.N * p.S * p.G * 2 * p.M);
     return cudaSuccess;
@@ -814,13 +817,9 @@ cudaError_t ssm_scan_grad_scratch(const ScanGradParams& pp, size_t* bytes)
 cudaError_t launch_ssm_scan_grad(const ScanGradParams& p, cudaStream_t s, int* launches)
 {
     if (p.f.N == 0) return launch_sum_parts(nullptr, 0, p.dA, p.f.D * p.f.M, p.dDskip, p.f.D, p.ddt_bias, p.f.D, s, launches);
-    int sms = 0;
-    cudaError_t e = ssm_sm_count(&sms);
-    if (e != cudaSuccess) return e;
-    const ScanChoice c = ssm_split(p.f, T, kCost, sms);
-    return p.f.io == 1   ? by_lanes<__half>(p, c, s, launches)
-           : p.f.io == 2 ? by_lanes<__nv_bfloat16>(p, c, s, launches)
-                         : by_lanes<float>(p, c, s, launches);
+    return p.f.io == 1   ? by_lanes<__half>(p, s, launches)
+           : p.f.io == 2 ? by_lanes<__nv_bfloat16>(p, s, launches)
+                         : by_lanes<float>(p, s, launches);
 }
 
 }  // namespace rnngb

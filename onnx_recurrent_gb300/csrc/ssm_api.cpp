@@ -413,7 +413,7 @@ rnn_status rnn_ssm_scan(rnn_ssm_t pl, const rnn_ssm_scan_args* a)
     p.saved = a->saved;
     cudaStream_t st = (cudaStream_t)a->stream;
     size_t bytes = 0;
-    cudaError_t e = ssm_scan_scratch(p, &bytes);
+    cudaError_t e = ssm_scan_plan(p, &bytes);
     if (e != cudaSuccess) return cuda_fail(e, "reading the device's attributes");
     rs = claim_scratch(pl, bytes, st);
     if (rs != RNN_OK) return rs;
@@ -465,11 +465,11 @@ rnn_status rnn_ssm_scan_grad(rnn_ssm_t pl, const rnn_ssm_scan_grad_args* a)
     p.dh0 = a->d_initial_h;
     cudaStream_t st = (cudaStream_t)a->stream;
     size_t bytes = 0;
-    cudaError_t e = ssm_scan_grad_scratch(p, &bytes);
+    cudaError_t e = ssm_scan_grad_plan(p, &bytes);
     if (e != cudaSuccess) return cuda_fail(e, "reading the device's attributes");
     rs = claim_scratch(pl, bytes, st);
     if (rs != RNN_OK) return rs;
-    p.part = (float*)pl->scratch;
+    p.f.scratch = (float*)pl->scratch;
     e = launch_ssm_scan_grad(p, st, &pl->launches);
     if (e != cudaSuccess) return cuda_fail(e, "scan gradient launch");
     return release_scratch(pl, bytes, st);

@@ -2,6 +2,7 @@
 // their kernels.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -60,6 +61,13 @@ struct ConvStepParams {
     int* status;
 };
 
+// How a scan is split: blocks of channels in a group, and chunks of `chunk`
+// steps.
+struct ScanChoice {
+    int chunks;
+    int64_t cblocks, chunk;
+};
+
 struct ScanParams {
     int64_t S, N, D;
     int M, G, io, softplus;
@@ -69,7 +77,8 @@ struct ScanParams {
     const float* h0;
     float* hT;
     float* saved;
-    float* scratch;         // ssm_scan_scratch
+    ScanChoice split;       // ssm_scan_plan, ssm_scan_grad_plan
+    float* scratch;
     int* status;
 };
 
@@ -78,7 +87,6 @@ struct ScanGradParams {
     View dY, dX, ddt, dB, dC, dZ;
     const float* dhT;
     float *dA, *dDskip, *ddt_bias, *dh0;
-    float* part;            // scratch (scan_grad_scratch)
 };
 
 struct ScanStepParams {
@@ -112,14 +120,9 @@ struct ScoreGradParams {
     void* dx;
 };
 
-// How a scan is split: blocks of channels in a group, and chunks of `chunk`
-// steps.  Chosen by a model of the time: `warps` warps fit a scheduler, a step
-// takes step_ns[w] with w of them on each, a block begin_ns to begin and end, and the
-// launch that finds the chunks' end states the part `ends` of the scan's time.
-struct ScanChoice {
-    int chunks;
-    int64_t cblocks, chunk;
-};
+// A split is chosen by a model of the time: `warps` warps fit a scheduler, a
+// step takes step_ns[w] with w of them on each, a block begin_ns to begin and end, and
+// the launch that finds the chunks' end states the part `ends` of the scan's time.
 struct ScanCost {
     int warps;
     double step_ns[5], begin_ns, ends;
@@ -134,15 +137,30 @@ inline int ssm_lanes(int M)
     return l;
 }
 
+// Lets a kernel have more than 48 KB of dynamic shared memory: once on each device.
+template <typename F>
+cudaError_t allow_shared(F* kernel, size_t bytes, std::atomic<uint64_t>& done)
+{
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 // Each launcher queues its kernels on `s` and adds their number to *launches.
 cudaError_t launch_ssm_conv(const ConvParams& p, cudaStream_t s, int* launches);
 int64_t ssm_conv_grad_parts(const ConvGradParams& p);
 cudaError_t launch_ssm_conv_grad(const ConvGradParams& p, cudaStream_t s, int* launches);
 cudaError_t launch_ssm_conv_step(const ConvStepParams& p, cudaStream_t s, int* launches);
 int64_t ssm_saved_floats(int64_t S, int64_t N, int64_t D, int64_t M);
-cudaError_t ssm_scan_scratch(const ScanParams& p, size_t* bytes);
+cudaError_t ssm_scan_plan(ScanParams& p, size_t* bytes);            // the split, and the scratch's size
 cudaError_t launch_ssm_scan(const ScanParams& p, cudaStream_t s, int* launches);
-cudaError_t ssm_scan_grad_scratch(const ScanGradParams& p, size_t* bytes);
+cudaError_t ssm_scan_grad_plan(ScanGradParams& p, size_t* bytes);
 cudaError_t launch_ssm_scan_grad(const ScanGradParams& p, cudaStream_t s, int* launches);
 cudaError_t launch_ssm_scan_step(const ScanStepParams& p, cudaStream_t s, int* launches);
 cudaError_t launch_scores(const ScoreParams& p, cudaStream_t s, int* launches);

@@ -18,12 +18,15 @@ from .rnn import IO_TYPES, _check
 ACTIVATIONS = {None: 0, "silu": 1}
 _TORCH_IO = None
 _lib = None
+# torch and what the calls below use of it, set by _load: a token's call takes a
+# few microseconds in all, so each look-up counts.
+torch = _f32 = _i32 = _empty = _raw_stream = None
 
 Scores = namedtuple("Scores", "logp entropy lse top_ids top_logp")
 
 
 def _load():
-    global _lib, _TORCH_IO
+    global _lib, _TORCH_IO, torch, _f32, _i32, _empty, _raw_stream
     if _lib is None:
         import torch
         lib = _rnn.load()
@@ -41,6 +44,9 @@ def _load():
         lib.rnn_scores.argtypes = [ctypes.c_char_p]
         lib.rnn_scores_grad.argtypes = [ctypes.c_char_p]
         _TORCH_IO = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+        _f32, _i32, _empty = torch.float32, torch.int32, torch.empty
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
         _lib = lib
     return _lib
 
@@ -49,7 +55,6 @@ class SSM:
     """A state space plan's handle plus the attributes it was created with."""
 
     def __init__(self, handle, channels, state_size, groups, conv_width, layout):
-        import torch
         self.handle = handle
         self.channels = channels
         self.state_size = state_size
@@ -85,7 +90,6 @@ def rnn_ssm_destroy(plan: SSM):
 
 def rnn_ssm_set_io_type(plan: SSM, io):
     """Element type of X, dt, B, C, Z, Y, the convolution's state and their gradients: "f32", "f16" or "bf16"."""
-    import torch
     _check(_load().rnn_ssm_set_io_type(plan.handle, IO_TYPES[io] if isinstance(io, str) else int(io)))
     plan.io = io if isinstance(io, str) else {v: k for k, v in IO_TYPES.items()}[int(io)]
     plan.dtype = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[plan.io]
@@ -100,60 +104,81 @@ def rnn_ssm_last_launch_count(plan: SSM) -> int:
     return int(_load().rnn_ssm_last_launch_count(plan.handle))
 
 
-def _stream(stream, device):
+def _stream(stream, dev):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream(device).cuda_stream
+        return _raw_stream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _bad(t, shape, dtype, device, name):
+def _bad(t, shape, dtype, dev, name):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
     raise ValueError(f"{name} has shape {tuple(t.shape)}, strides {t.stride()}; expected {tuple(shape)}")
 
 
-def _dense(t, shape, dtype, device, name):
+def _device(t, name):
+    """Index of the GPU that the call's first tensor is on."""
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _dense(t, shape, dtype, dev, name):
     """Address of a dense tensor of this shape and type, 0 for None."""
     if t is None:
         return 0
-    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
-        _bad(t, shape, dtype, device, name)
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        _bad(t, shape, dtype, dev, name)
     return t.data_ptr()
 
 
 _NO_VIEW = (0, 0, 0)
 
 
-def _view(t, shape, dtype, device, name, layout, step=False):
-    """(address, step stride, row stride) of a [seq, batch, ...] (layout 0),
-    [batch, seq, ...] (layout 1) or, with step, [batch, ...] tensor whose
-    innermost part is dense."""
+def _view(t, shape, dtype, dev, name, layout):
+    """(address, step stride, row stride) of a [seq, batch, ...] (layout 0) or
+    [batch, seq, ...] (layout 1) tensor whose innermost part is dense."""
     if t is None:
         return _NO_VIEW
-    if t.dtype != dtype or t.device != device or t.shape != shape:
-        _bad(t, shape, dtype, device, name)
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _bad(t, shape, dtype, dev, name)
+    if t.is_contiguous():
+        return t.data_ptr(), 0, 0                  # dense
     st = t.stride()
-    lead = 1 if step else 2
     inner = 1
-    for i in range(len(shape) - 1, lead - 1, -1):
+    for i in range(len(shape) - 1, 1, -1):
         if shape[i] != 1:
             if st[i] != inner:
-                _bad(t, shape, dtype, device, name + " (dense innermost part)")
+                _bad(t, shape, dtype, dev, name + " (dense innermost part)")
             inner *= shape[i]
-    if step:
-        # a stride of 0 reads as dense: for one row it is
-        if st[0] == 0 and shape[0] > 1:
-            raise ValueError(f"{name}: rows must not share memory")
-        return t.data_ptr(), 0, st[0]
     ss, bs = (st[0], st[1]) if layout == 0 else (st[1], st[0])
-    if ss == 0 and bs == 0 and shape[0] * shape[1] > 1:
+    if ss == 0 and bs == 0:
         raise ValueError(f"{name}: steps and rows must not all share memory")
     return t.data_ptr(), ss, bs
+
+
+def _rows(t, shape, dtype, dev, name):
+    """The same of a [batch, ...] tensor."""
+    if t is None:
+        return _NO_VIEW
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _bad(t, shape, dtype, dev, name)
+    if t.is_contiguous():
+        return t.data_ptr(), 0, 0
+    st = t.stride()
+    inner = 1
+    for i in range(len(shape) - 1, 0, -1):
+        if shape[i] != 1:
+            if st[i] != inner:
+                _bad(t, shape, dtype, dev, name + " (dense innermost part)")
+            inner *= shape[i]
+    if st[0] == 0 and shape[0] > 1:
+        raise ValueError(f"{name}: rows must not share memory")
+    return t.data_ptr(), 0, st[0]
 
 
 def _sizes(plan, X):
@@ -170,14 +195,13 @@ def _shapes(plan, S, N):
 def rnn_ssm_conv(plan: SSM, X, W, bias=None, sequence_lens=None, initial_state=None, Y=None, final_state=None,
                  stream=None):
     """Y = f(causal convolution of X); every output is optional but Y."""
-    import torch
     S, N = _sizes(plan, X)
-    D, K, dt, dev, lay = plan.channels, plan.conv_width, plan.dtype, X.device, plan.layout
+    D, K, dt, dev, lay = plan.channels, plan.conv_width, plan.dtype, _device(X, "X"), plan.layout
     full, _ = _shapes(plan, S, N)
-    f32 = torch.float32
+    f32 = _f32
     args = struct.pack(
         "14q", S, N, *_view(X, full, dt, dev, "X", lay), _dense(W, (D, K), f32, dev, "W"),
-        _dense(bias, (D,), f32, dev, "bias"), _dense(sequence_lens, (N,), torch.int32, dev, "sequence_lens"),
+        _dense(bias, (D,), f32, dev, "bias"), _dense(sequence_lens, (N,), _i32, dev, "sequence_lens"),
         _dense(initial_state, (N, K - 1, D), dt, dev, "initial_state"), *_view(Y, full, dt, dev, "Y", lay),
         _dense(final_state, (N, K - 1, D), dt, dev, "final_state"), _stream(stream, dev))
     _check(_load().rnn_ssm_conv(plan.handle, args))
@@ -185,10 +209,9 @@ def rnn_ssm_conv(plan: SSM, X, W, bias=None, sequence_lens=None, initial_state=N
 
 def ssm_conv(plan: SSM, X, W, bias=None, sequence_lens=None, initial_state=None, stream=None):
     """Returns (Y, final_state)."""
-    import torch
     S, N = _sizes(plan, X)
     full, _ = _shapes(plan, S, N)
-    Y = torch.empty(full, dtype=plan.dtype, device=X.device)
+    Y = _empty(full, dtype=plan.dtype, device=X.device)
     state = torch.empty((N, plan.conv_width - 1, plan.channels), dtype=plan.dtype, device=X.device)
     rnn_ssm_conv(plan, X, W, bias, sequence_lens, initial_state, Y, state, stream)
     return Y, state
@@ -196,15 +219,14 @@ def ssm_conv(plan: SSM, X, W, bias=None, sequence_lens=None, initial_state=None,
 
 def rnn_ssm_conv_grad(plan: SSM, dY, X, W, bias=None, sequence_lens=None, initial_state=None, d_final_state=None,
                       dX=None, dW=None, dbias=None, d_initial_state=None, stream=None):
-    import torch
     S, N = _sizes(plan, X)
-    D, K, dt, dev, lay = plan.channels, plan.conv_width, plan.dtype, X.device, plan.layout
+    D, K, dt, dev, lay = plan.channels, plan.conv_width, plan.dtype, _device(X, "X"), plan.layout
     full, _ = _shapes(plan, S, N)
-    f32, state = torch.float32, (N, K - 1, D)
+    f32, state = _f32, (N, K - 1, D)
     args = struct.pack(
         "20q", S, N, *_view(dY, full, dt, dev, "dY", lay), *_view(X, full, dt, dev, "X", lay),
         _dense(W, (D, K), f32, dev, "W"), _dense(bias, (D,), f32, dev, "bias"),
-        _dense(sequence_lens, (N,), torch.int32, dev, "sequence_lens"),
+        _dense(sequence_lens, (N,), _i32, dev, "sequence_lens"),
         _dense(initial_state, state, dt, dev, "initial_state"), _dense(d_final_state, state, dt, dev, "d_final_state"),
         *_view(dX, full, dt, dev, "dX", lay), _dense(dW, (D, K), f32, dev, "dW"),
         _dense(dbias, (D,), f32, dev, "dbias"), _dense(d_initial_state, state, dt, dev, "d_initial_state"),
@@ -215,10 +237,9 @@ def rnn_ssm_conv_grad(plan: SSM, dY, X, W, bias=None, sequence_lens=None, initia
 def ssm_conv_grad(plan: SSM, dY, X, W, bias=None, sequence_lens=None, initial_state=None, d_final_state=None,
                   stream=None):
     """Returns a dict of dX and dW, of dbias where bias is given, and of d_initial_state where initial_state is."""
-    import torch
     S, N = _sizes(plan, X)
     full, _ = _shapes(plan, S, N)
-    out = {"dX": torch.empty(full, dtype=plan.dtype, device=X.device), "dW": torch.empty_like(W)}
+    out = {"dX": _empty(full, dtype=plan.dtype, device=X.device), "dW": torch.empty_like(W)}
     if bias is not None:
         out["dbias"] = torch.empty_like(bias)
     if initial_state is not None:
@@ -230,17 +251,16 @@ def ssm_conv_grad(plan: SSM, dY, X, W, bias=None, sequence_lens=None, initial_st
 def rnn_ssm_conv_step(plan: SSM, X, W, bias, state, Y, state_out=None, slots=None, stream=None):
     """One token of each row: X and Y [batch, channels], state [slots or batch,
     conv_width - 1, channels]; state_out None updates state in place."""
-    import torch
-    D, K, dt, dev = plan.channels, plan.conv_width, plan.dtype, X.device
+    D, K, dt, dev = plan.channels, plan.conv_width, plan.dtype, _device(X, "X")
     N = X.shape[0]
     n_slots = N if slots is None else state.shape[0]
     shape = (n_slots, K - 1, D)
     at = _dense(state, shape, dt, dev, "state")
     args = struct.pack(
-        "14q", N, n_slots, *_view(X, (N, D), dt, dev, "X", 0, True), _dense(W, (D, K), torch.float32, dev, "W"),
-        _dense(bias, (D,), torch.float32, dev, "bias"), at,
+        "14q", N, n_slots, *_rows(X, (N, D), dt, dev, "X"), _dense(W, (D, K), _f32, dev, "W"),
+        _dense(bias, (D,), _f32, dev, "bias"), at,
         at if state_out is None else _dense(state_out, shape, dt, dev, "state_out"),
-        _dense(slots, (N,), torch.int32, dev, "slots"), *_view(Y, (N, D), dt, dev, "Y", 0, True), _stream(stream, dev))
+        _dense(slots, (N,), _i32, dev, "slots"), *_rows(Y, (N, D), dt, dev, "Y"), _stream(stream, dev))
     _check(_load().rnn_ssm_conv_step(plan.handle, args))
 
 
@@ -250,29 +270,27 @@ def rnn_ssm_saved_size(plan: SSM, seq_length, batch_size) -> int:
 
 
 def _scan_inputs(plan, S, N, X, dt_, A, B, C, Dskip, Z, dt_bias, lens, h0):
-    import torch
-    D, M, io, dev, lay = plan.channels, plan.state_size, plan.dtype, X.device, plan.layout
+    D, M, io, dev, lay = plan.channels, plan.state_size, plan.dtype, X.get_device(), plan.layout
     full, bc = _shapes(plan, S, N)
-    f32 = torch.float32
+    f32 = _f32
     return (*_view(X, full, io, dev, "X", lay), *_view(dt_, full, io, dev, "dt", lay),
             *_view(B, bc, io, dev, "B", lay), *_view(C, bc, io, dev, "C", lay), *_view(Z, full, io, dev, "Z", lay),
             _dense(A, (D, M), f32, dev, "A"), _dense(Dskip, (D,), f32, dev, "D"),
-            _dense(dt_bias, (D,), f32, dev, "dt_bias"), _dense(lens, (N,), torch.int32, dev, "sequence_lens"),
+            _dense(dt_bias, (D,), f32, dev, "dt_bias"), _dense(lens, (N,), _i32, dev, "sequence_lens"),
             _dense(h0, (N, D, M), f32, dev, "initial_h"))
 
 
 def rnn_ssm_scan(plan: SSM, X, dt, A, B, C, D=None, Z=None, dt_bias=None, sequence_lens=None, initial_h=None,
                  Y=None, Y_h=None, saved=None, stream=None):
     """The scan; X, dt, Z, Y [seq, batch, channels] and B, C [seq, batch, groups, state] in the plan's layout."""
-    import torch
     S, N = _sizes(plan, X)
-    dev = X.device
+    dev = _device(X, "X")
     full, _ = _shapes(plan, S, N)
     args = struct.pack(
         "28q", S, N, *_scan_inputs(plan, S, N, X, dt, A, B, C, D, Z, dt_bias, sequence_lens, initial_h),
         *_view(Y, full, plan.dtype, dev, "Y", plan.layout),
-        _dense(Y_h, (N, plan.channels, plan.state_size), torch.float32, dev, "Y_h"),
-        0 if saved is None else _dense(saved, (rnn_ssm_saved_size(plan, S, N),), torch.float32, dev, "saved"),
+        _dense(Y_h, (N, plan.channels, plan.state_size), _f32, dev, "Y_h"),
+        0 if saved is None else _dense(saved, (rnn_ssm_saved_size(plan, S, N),), _f32, dev, "saved"),
         _stream(stream, dev))
     _check(_load().rnn_ssm_scan(plan.handle, args))
 
@@ -280,10 +298,9 @@ def rnn_ssm_scan(plan: SSM, X, dt, A, B, C, D=None, Z=None, dt_bias=None, sequen
 def ssm_scan(plan: SSM, X, dt, A, B, C, D=None, Z=None, dt_bias=None, sequence_lens=None, initial_h=None, save=False,
              stream=None):
     """Returns (Y, Y_h, saved); saved is None unless save."""
-    import torch
     S, N = _sizes(plan, X)
     full, _ = _shapes(plan, S, N)
-    dev, f32 = X.device, torch.float32
+    dev, f32 = X.device, _f32
     Y = torch.empty(full, dtype=plan.dtype, device=dev)
     Y_h = torch.empty((N, plan.channels, plan.state_size), dtype=f32, device=dev)
     saved = torch.empty((rnn_ssm_saved_size(plan, S, N),), dtype=f32, device=dev) if save else None
@@ -294,9 +311,8 @@ def ssm_scan(plan: SSM, X, dt, A, B, C, D=None, Z=None, dt_bias=None, sequence_l
 def rnn_ssm_scan_grad(plan: SSM, dY, saved, X, dt, A, B, C, D=None, Z=None, dt_bias=None, sequence_lens=None,
                       initial_h=None, dY_h=None, dX=None, ddt=None, dB=None, dC=None, dZ=None, dA=None, dD=None,
                       ddt_bias=None, d_initial_h=None, stream=None):
-    import torch
     S, N = _sizes(plan, X)
-    io, dev, lay, f32 = plan.dtype, X.device, plan.layout, torch.float32
+    io, dev, lay, f32 = plan.dtype, _device(X, "X"), plan.layout, _f32
     full, bc = _shapes(plan, S, N)
     ch, st = (plan.channels,), (N, plan.channels, plan.state_size)
     args = struct.pack(
@@ -314,7 +330,6 @@ def rnn_ssm_scan_grad(plan: SSM, dY, saved, X, dt, A, B, C, D=None, Z=None, dt_b
 def ssm_scan_grad(plan: SSM, dY, saved, X, dt, A, B, C, D=None, Z=None, dt_bias=None, sequence_lens=None,
                   initial_h=None, dY_h=None, stream=None):
     """Returns a dict of dX, ddt, dA, dB, dC and of dD, dZ, ddt_bias, d_initial_h for those of the inputs given."""
-    import torch
     S, N = _sizes(plan, X)
     full, bc = _shapes(plan, S, N)
     new = lambda shape: torch.empty(shape, dtype=plan.dtype, device=X.device)  # noqa: E731
@@ -336,19 +351,18 @@ def rnn_ssm_scan_step(plan: SSM, X, dt, A, B, C, H, Y, D=None, Z=None, dt_bias=N
                       stream=None):
     """One token of each row: X, dt, Z, Y [batch, channels], B, C [batch, groups,
     state], H [slots or batch, channels, state]; H_out None updates H in place."""
-    import torch
-    dev, io, f32 = X.device, plan.dtype, torch.float32
+    dev, io, f32 = _device(X, "X"), plan.dtype, _f32
     N, ch, M = X.shape[0], plan.channels, plan.state_size
     full, bc = (N, ch), (N, plan.groups, M)
     n_slots = N if slots is None else H.shape[0]
     at = _dense(H, (n_slots, ch, M), f32, dev, "H")
     args = struct.pack(
-        "27q", N, n_slots, *_view(X, full, io, dev, "X", 0, True), *_view(dt, full, io, dev, "dt", 0, True),
-        *_view(B, bc, io, dev, "B", 0, True), *_view(C, bc, io, dev, "C", 0, True),
-        *_view(Z, full, io, dev, "Z", 0, True), _dense(A, (ch, M), f32, dev, "A"), _dense(D, (ch,), f32, dev, "D"),
+        "27q", N, n_slots, *_rows(X, full, io, dev, "X"), *_rows(dt, full, io, dev, "dt"),
+        *_rows(B, bc, io, dev, "B"), *_rows(C, bc, io, dev, "C"),
+        *_rows(Z, full, io, dev, "Z"), _dense(A, (ch, M), f32, dev, "A"), _dense(D, (ch,), f32, dev, "D"),
         _dense(dt_bias, (ch,), f32, dev, "dt_bias"), at,
         at if H_out is None else _dense(H_out, (n_slots, ch, M), f32, dev, "H_out"),
-        _dense(slots, (N,), torch.int32, dev, "slots"), *_view(Y, full, io, dev, "Y", 0, True), _stream(stream, dev))
+        _dense(slots, (N,), _i32, dev, "slots"), *_rows(Y, full, io, dev, "Y"), _stream(stream, dev))
     _check(_load().rnn_ssm_scan_step(plan.handle, args))
 
 
@@ -368,11 +382,10 @@ def _logits(t, name, dtype=None, shape=None, device=None):
 
 def rnn_scores(logits, ids=None, top=0, logp=None, entropy=None, lse=None, top_ids=None, top_logp=None, stream=None):
     """Scores of rows of logits [rows, vocab] into the outputs given."""
-    import torch
     lib = _load()
     at, stride = _logits(logits, "logits")
     rows, vocab = logits.shape
-    dev, f32, i32, top = logits.device, torch.float32, torch.int32, int(top)
+    dev, f32, i32, top = logits.get_device(), _f32, _i32, int(top)
     args = struct.pack(
         "13q", rows, vocab, stride, _TORCH_IO[logits.dtype], at, _dense(ids, (rows,), i32, dev, "ids"), top,
         _dense(logp, (rows,), f32, dev, "logp"), _dense(entropy, (rows,), f32, dev, "entropy"),
@@ -384,38 +397,37 @@ def rnn_scores(logits, ids=None, top=0, logp=None, entropy=None, lse=None, top_i
 def scores(logits, ids=None, top=0, stream=None) -> Scores:
     """Scores(logp, entropy, lse, top_ids, top_logp) of rows of logits; logp is
     None without ids, top_ids and top_logp are None for top = 0."""
-    import torch
-    new = lambda shape, t=torch.float32: torch.empty(shape, dtype=t, device=logits.device)  # noqa: E731
+    _load()
+    new = lambda shape, t=_f32: _empty(shape, dtype=t, device=logits.device)  # noqa: E731
     rows, top = logits.shape[0], int(top)
     if top < 0:
         raise ValueError(f"top must not be negative, got {top}")
     r = Scores(None if ids is None else new(rows), new(rows), new(rows),
-               new((rows, top), torch.int32) if top else None, new((rows, top)) if top else None)
+               new((rows, top), _i32) if top else None, new((rows, top)) if top else None)
     rnn_scores(logits, ids, top, *r, stream=stream)
     return r
 
 
 def rnn_scores_grad(logits, ids, result: Scores, d_logp=None, d_entropy=None, d_top=None, dlogits=None, stream=None):
     """Gradient of the scores in the logits into dlogits (which may be logits); ``result`` is their Scores."""
-    import torch
     lib = _load()
     at, stride = _logits(logits, "logits")
     rows, vocab = logits.shape
     d_at, d_stride = _logits(dlogits, "dlogits", logits.dtype, logits.shape, logits.device)
-    dev, f32 = logits.device, torch.float32
+    dev, f32 = logits.get_device(), _f32
     top = 0 if d_top is None else d_top.shape[1]
     args = struct.pack(
-        "16q", rows, vocab, stride, _TORCH_IO[logits.dtype], at, _dense(ids, (rows,), torch.int32, dev, "ids"),
+        "16q", rows, vocab, stride, _TORCH_IO[logits.dtype], at, _dense(ids, (rows,), _i32, dev, "ids"),
         _dense(result.lse, (rows,), f32, dev, "lse"), _dense(result.entropy, (rows,), f32, dev, "entropy"),
         _dense(d_logp, (rows,), f32, dev, "d_logp"), _dense(d_entropy, (rows,), f32, dev, "d_entropy"), top,
-        _dense(result.top_ids, (rows, top), torch.int32, dev, "top_ids") if top else 0,
+        _dense(result.top_ids, (rows, top), _i32, dev, "top_ids") if top else 0,
         _dense(d_top, (rows, top), f32, dev, "d_top"), d_at, d_stride, _stream(stream, dev))
     _check(lib.rnn_scores_grad(args))
 
 
 def scores_grad(logits, ids, result: Scores, d_logp=None, d_entropy=None, d_top=None, stream=None):
     """Returns dlogits, in the logits' type."""
-    import torch
-    dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    _load()
+    dlogits = _empty(logits.shape, dtype=logits.dtype, device=logits.device)
     rnn_scores_grad(logits, ids, result, d_logp, d_entropy, d_top, dlogits, stream)
     return dlogits

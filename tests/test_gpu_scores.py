@@ -191,3 +191,17 @@ def test_no_rows_and_refusals():
         orc.scores_grad(x, None, s, torch.ones(2, device="cuda"))
     with pytest.raises(orc.RNNError):
         orc.rnn_scores_grad(x, ids, s._replace(lse=None), torch.ones(2, device="cuda"), dlogits=torch.empty_like(x))
+
+
+@pytest.mark.parametrize("rows,V", [(2, 3000), (3, 50001), (700, 9000)])
+def test_many_equal_logits(rows, V):
+    """Rows in which hundreds of logits tie at the last place wanted, with larger ones among and after them."""
+    g = torch.Generator().manual_seed(8)
+    x = torch.randint(-3, 4, (rows, V), generator=g).float()       # seven values: a seventh of the row ties at the top
+    x[0] = -INF
+    x[0, V - 7:V - 2] = torch.arange(5).float()                    # five allowed, at the row's end; the rest tie at -inf
+    x[1, torch.randperm(V, generator=g)[:900]] = torch.rand(900, generator=g) + 10.0
+    for io in ("bf16", "f32"):
+        v = x.to(DT[io])
+        got = orc.scores(v.cuda(), top=32)
+        assert torch.equal(got.top_ids[:3].cpu(), ref.scores(v[:3].double(), None, 32)["top_ids"])
