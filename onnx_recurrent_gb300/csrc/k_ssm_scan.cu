@@ -31,9 +31,10 @@
 //
 // When rows and channels are too few for the SMs, the steps are split in
 // chunks: one launch finds each chunk's end state from zero and the sum of
-// its delta (the product of its decays is exp(A sum delta)), a small one
-// chains them to every chunk's first state, and the scan runs over all chunks
-// at once.  That costs another exponential and three operations per update.
+// its delta (the product of its decays is exp(A sum delta)), and the scan runs over
+// all chunks at once, each from its first state: with up to kFold chunks the
+// block chains the end states before its own, with more a small launch in between
+// chains them for all.  That costs another exponential and three operations per update.
 #include <cmath>
 
 #include "ssm_tile.cuh"
@@ -47,6 +48,7 @@ constexpr int E = 4;              // states of a lane
 constexpr int CH = 4;             // channels of a lane
 constexpr int T = 16;             // steps of a tile in shared memory
 constexpr int U = 4;              // steps of the inner loop's body
+constexpr int kFold = 16;         // chunks whose states a block chains itself
 struct ScanLaunch {
     int cblocks;          // blocks of channels in a group
     int64_t chunk;        // steps of a chunk (a multiple of T)
@@ -121,24 +123,46 @@ __global__ void __launch_bounds__(Tile<V, L>::THREADS, 16 / Tile<V, L>::W)
         ch[r] = cg * CH + 2 * at;
     }
     f2 A[E][PAIRS], h[E][PAIRS];
-    {
-        const float* first = ENDS ? nullptr : chunk == 0 ? p.h0 : q.ends + (int64_t)(chunk - 1) * p.N * p.D * p.M;
+    // the lane's part of an [.., D, M] table's row n
+    auto table = [&](f2 (&v)[E][PAIRS], const float* from, bool vec, float scale) {
 #pragma unroll
         for (int r = 0; r < PAIRS; ++r) {
-            float a[2][E], s[2][E];
+            float s[2][E];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int c = warp * K::WC + ch[r] + i;
+                const float* at = from + (d0 + c) * p.M + sg * E;
+                if (vec && from && c < valid && sg * E < p.M) {
+                    load_vec<float, E>(at, s[i]);
+                } else {
 #pragma unroll
-                for (int j = 0; j < E; ++j) {
-                    const int m = sg * E + j;
-                    const bool on = c < valid && m < p.M;
-                    a[i][j] = on ? p.A[(d0 + c) * p.M + m] * kLog2e : 0.0f;
-                    s[i][j] = on && first ? first[(n * p.D + d0 + c) * p.M + m] : 0.0f;
+                    for (int j = 0; j < E; ++j) s[i][j] = from && c < valid && sg * E + j < p.M ? at[j] : 0.0f;
                 }
             }
 #pragma unroll
-            for (int j = 0; j < E; ++j) A[j][r] = pack2(a[0][j], a[1][j]), h[j][r] = pack2(s[0][j], s[1][j]);
+            for (int j = 0; j < E; ++j) v[j][r] = pack2(s[0][j] * scale, s[1][j] * scale);
+        }
+    };
+    table(A, p.A, false, kLog2e);
+    {
+        const int64_t states = p.N * p.D * p.M, row = n * p.D * p.M;
+        const bool fold = q.chunks <= kFold;
+        const float* first = ENDS ? nullptr : chunk == 0 || fold ? p.h0 : q.ends + (chunk - 1) * states;
+        table(h, first ? first + row : nullptr, false, 1.0f);
+        if (!ENDS && fold) {
+#pragma unroll 2
+            for (int k = 0; k < chunk; ++k) {
+                f2 end[E][PAIRS];
+                table(end, q.ends + k * states + row, q.vec_h, 1.0f);
+                const float* delta = q.deltas + (k * p.N + n) * p.D + d0 + warp * K::WC;
+#pragma unroll
+                for (int r = 0; r < PAIRS; ++r) {
+                    const bool on = warp * K::WC + ch[r] < valid, both = warp * K::WC + ch[r] + 1 < valid;
+                    const f2 d = pack2(on ? delta[ch[r]] : 0.0f, both ? delta[ch[r] + 1] : 0.0f);
+#pragma unroll
+                    for (int j = 0; j < E; ++j) h[j][r] = fma2(ex2_2(mul2(d, A[j][r])), h[j][r], end[j][r]);
+                }
+            }
         }
     }
 
@@ -420,12 +444,15 @@ cudaError_t run(const ScanParams& p, cudaStream_t s, int* launches)
         f<<<(unsigned)(blocks * (c.chunks - 1)), K::THREADS, smem, s>>>(p, q);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        const int64_t states = p.N * p.D * p.M;
-        if ((states + 255) / 256 > kMaxGrid) return cudaErrorInvalidConfiguration;
-        ssm_scan_chain_kernel<<<(unsigned)((states + 255) / 256), 256, 0, s>>>(p, q);
-        e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-        *launches += 2;
+        ++*launches;
+        if (c.chunks > kFold) {
+            const int64_t states = p.N * p.D * p.M;
+            if ((states + 255) / 256 > kMaxGrid) return cudaErrorInvalidConfiguration;
+            ssm_scan_chain_kernel<<<(unsigned)((states + 255) / 256), 256, 0, s>>>(p, q);
+            e = cudaGetLastError();
+            if (e != cudaSuccess) return e;
+            ++*launches;
+        }
     }
     auto* f = ssm_scan_kernel<V, L, false>;
     const size_t smem = K::bytes(3);

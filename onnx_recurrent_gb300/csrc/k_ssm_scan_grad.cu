@@ -19,12 +19,13 @@
 // The sums over a channel's states (for dX, ddelta) go over L lanes, those
 // over channels (dB, dC) over the other 32 / L, each halving the values at
 // every exchange; what a lane sends first is chosen by its place in memory,
-// so nothing is selected.  dB and dC are then summed over the block's warps,
-// written for each block of channels, and added up in order by a kernel of
-// their own; dA, dDskip and ddt_bias likewise over rows and chunks of steps.
+// so nothing is selected.  dB and dC are then summed over the block's warps and
+// written for each block of channels, dA, dDskip and ddt_bias for each row and
+// chunk of steps; a last launch adds both up in order.
 //
 // Steps are split in chunks as in the forward run, from the end: one launch
-// finds the q that each chunk passes on when none enters, another chains them.
+// finds the q that each chunk passes on when none enters; with up to kFold
+// chunks a block chains those after its own, with more another launch does.
 //
 // Measured (38 rows of 512 steps, 2048 channels, M = 16, bf16, SMs full): 838 us,
 // 0.76 updates a ns; 390 instructions for 512 updates, 140 of them packed fp32
@@ -47,6 +48,7 @@ constexpr int CH = 4;             // channels of a lane
 constexpr int PAIRS = CH / 2;
 constexpr int T = kSsmTile;       // steps of a tile
 constexpr int U = 4;              // steps of half a tile
+constexpr int kFold = 16;         // chunks whose q a block chains itself
 constexpr int NV = 4, NP = 2;     // channels of an elementwise access
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -285,8 +287,25 @@ __global__ void __launch_bounds__(Tile<V, L>::THREADS, 12 / Tile<V, L>::W)
     f2 A[E][PAIRS], carry[E][PAIRS], dA[E][PAIRS];
     load_states<L>(A, p.A + b.d0 * p.M, at, c0, b.valid, p.M, false, kLog2e);
     {
-        const float* from = b.chunk + 1 < q.chunks ? q.ends + (int64_t)b.chunk * p.N * p.D * p.M : pp.dhT;
-        load_states<L>(carry, from ? from + (b.n * p.D + b.d0) * p.M : nullptr, at, c0, b.valid, p.M, false, 1.0f);
+        const int64_t states = p.N * p.D * p.M, row = (b.n * p.D + b.d0) * p.M;
+        const bool fold = q.chunks <= kFold;
+        const float* from = b.chunk + 1 < q.chunks && !fold ? q.ends + b.chunk * states : pp.dhT;
+        load_states<L>(carry, from ? from + row : nullptr, at, c0, b.valid, p.M, false, 1.0f);
+        if (fold) {
+#pragma unroll 2
+            for (int k = q.chunks - 2; k >= b.chunk; --k) {
+                f2 end[E][PAIRS];
+                load_states<L>(end, q.ends + k * states + row, at, c0, b.valid, p.M, p.M % 2 == 0, 1.0f);
+                const float* delta = q.deltas + (k * p.N + b.n) * p.D + b.d0 + c0;
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) {
+                    const bool on = c0 + at.ch[i] < b.valid, both = c0 + at.ch[i] + 1 < b.valid;
+                    const f2 d = pack2(on ? delta[at.ch[i]] : 0.0f, both ? delta[at.ch[i] + 1] : 0.0f);
+#pragma unroll
+                    for (int j = 0; j < E; ++j) carry[j][i] = fma2(ex2_2(mul2(d, A[j][i])), carry[j][i], end[j][i]);
+                }
+            }
+        }
     }
     float most_a = 0.0f;
 #pragma unroll
@@ -692,16 +711,41 @@ __global__ void __launch_bounds__(256) ssm_scan_grad_chain_kernel(const ScanGrad
     }
 }
 
-// dB and dC of every step: the channel blocks' sums in order, zero past a
-// row's end.
+// The sums over blocks, in order.  Blocks below `parts_blocks`: dA, dDskip and
+// ddt_bias over rows and chunks (32 values a block, 8 threads' sums each); the others: dB and
+// dC of every step over the blocks of channels, zero past a row's end.
 template <typename V>
-__global__ void __launch_bounds__(256) ssm_scan_bc_kernel(const ScanGradParams pp, const GradLaunch q)
+__global__ void __launch_bounds__(256) ssm_scan_grad_sums_kernel(const ScanGradParams pp, const GradLaunch q, int64_t parts_blocks)
 {
     const ScanParams& p = pp.f;
+    if (blockIdx.x < parts_blocks) {
+        __shared__ float sums[8][33];
+        const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+        const int64_t n0 = p.D * p.M, n = n0 + 2 * p.D, i = (int64_t)blockIdx.x * 32 + lane, parts = q.chunks * p.N;
+        float s = 0.0f;
+        if (i < n) {
+#pragma unroll 8
+            for (int64_t r = w; r < parts; r += 8) s += q.part[r * n + i];
+        }
+        sums[w][lane] = s;
+        __syncthreads();
+        if (w != 0 || i >= n) return;
+        s = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) s += sums[r][lane];
+        if (i < n0) {
+            if (pp.dA) pp.dA[i] = s;
+        } else if (i < n0 + p.D) {
+            if (pp.dDskip) pp.dDskip[i - n0] = s;
+        } else if (pp.ddt_bias) {
+            pp.ddt_bias[i - n0 - p.D] = s;
+        }
+        return;
+    }
     const int64_t per = (int64_t)p.G * 2 * p.M, count = p.N * p.S * per;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256) {
-        const int64_t t = i / per % p.S, n = i / per / p.S;
-        const int r = (int)(i % per), g = r / (2 * p.M), w = r / p.M % 2, m = r % p.M;
+    for (int64_t i = (blockIdx.x - parts_blocks) * 256 + threadIdx.x; i < count; i += (gridDim.x - parts_blocks) * 256) {
+        const int64_t step = i / per, t = step % p.S, n = step / p.S;
+        const int r = (int)(i - step * per), g = r / (2 * p.M), w = r / p.M % 2, m = r % p.M;
         float s = 0.0f;
         if (t < row_length(p.lens, n, p.S, p.status)) {
 #pragma unroll 4
@@ -763,11 +807,14 @@ cudaError_t run(const ScanGradParams& pp, cudaStream_t s, int* launches)
         f<<<(unsigned)(blocks * (c.chunks - 1)), K::THREADS, K::bytes_ends(), s>>>(pp, q);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        if ((states + 255) / 256 > kMaxGrid) return cudaErrorInvalidConfiguration;
-        ssm_scan_grad_chain_kernel<<<(unsigned)((states + 255) / 256), 256, 0, s>>>(pp, q);
-        e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-        *launches += 2;
+        ++*launches;
+        if (c.chunks > kFold) {
+            if ((states + 255) / 256 > kMaxGrid) return cudaErrorInvalidConfiguration;
+            ssm_scan_grad_chain_kernel<<<(unsigned)((states + 255) / 256), 256, 0, s>>>(pp, q);
+            e = cudaGetLastError();
+            if (e != cudaSuccess) return e;
+            ++*launches;
+        }
     }
     auto* f = ssm_scan_grad_kernel<V, L>;
     cudaError_t e = allow_shared(f, K::bytes(), ready);
@@ -776,14 +823,12 @@ cudaError_t run(const ScanGradParams& pp, cudaStream_t s, int* launches)
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     ++*launches;
-    if (p.S > 0) {
-        const int64_t count = p.N * p.S * p.G * 2 * p.M, grid = (count + 255) / 256;
-        ssm_scan_bc_kernel<V><<<(unsigned)(grid < 65536 ? grid : 65536), 256, 0, s>>>(pp, q);
-        e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-        ++*launches;
-    }
-    return launch_sum_parts(q.part, c.chunks * p.N, pp.dA, p.D * p.M, pp.dDskip, p.D, pp.ddt_bias, p.D, s, launches);
+    const int64_t parts_blocks = (p.D * (p.M + 2) + 31) / 32, steps_blocks = (p.N * p.S * p.G * 2 * p.M + 255) / 256;
+    if (parts_blocks > kMaxGrid - 65536) return cudaErrorInvalidConfiguration;
+    const unsigned grid = (unsigned)(parts_blocks + (steps_blocks < 65536 ? steps_blocks : 65536));
+    ssm_scan_grad_sums_kernel<V><<<grid, 256, 0, s>>>(pp, q, parts_blocks);
+    ++*launches;
+    return cudaGetLastError();
 }
 
 template <typename V>

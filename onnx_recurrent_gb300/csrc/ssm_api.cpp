@@ -17,8 +17,10 @@ struct rnn_ssm {
     int* status = nullptr;        // device word the kernels report through
     char* scratch = nullptr;
     size_t scratch_bytes = 0;
-    cudaEvent_t used = nullptr;   // after the last call that used the scratch
-    bool pending = false;
+    cudaEvent_t used = nullptr;   // after the last call that used the scratch,
+    bool pending = false;         // if there is one,
+    unsigned long long user = 0;  // on the stream of this id
+    bool capturing = false;       // the call at hand is being captured
     int launches = 0;
 };
 
@@ -142,25 +144,24 @@ rnn_status claim_scratch(rnn_ssm* pl, size_t bytes, cudaStream_t st)
             return cuda_fail(e, "cudaEventCreate");
         }
     }
-    if (pl->pending) {
-        cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-        cudaError_t e = cudaStreamIsCapturing(st, &cs);
-        // an event recorded outside a capture cannot be waited on inside one
-        if (e == cudaSuccess && cs == cudaStreamCaptureStatusNone) e = cudaStreamWaitEvent(st, pl->used, 0);
-        if (e != cudaSuccess) return cuda_fail(e, "ordering the scratch");
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    cudaError_t e = cudaStreamIsCapturing(st, &cs);
+    pl->capturing = cs != cudaStreamCaptureStatusNone;
+    // an event recorded outside a capture cannot be waited on inside one
+    if (e == cudaSuccess && !pl->capturing) {
+        e = cudaStreamGetId(st, &id);
+        if (e == cudaSuccess && pl->pending && id != pl->user) e = cudaStreamWaitEvent(st, pl->used, 0);
+        pl->user = id;
     }
-    return RNN_OK;
+    return e == cudaSuccess ? RNN_OK : cuda_fail(e, "ordering the scratch");
 }
 
 rnn_status release_scratch(rnn_ssm* pl, size_t bytes, cudaStream_t st)
 {
-    if (!bytes) return RNN_OK;
-    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-    cudaError_t e = cudaStreamIsCapturing(st, &cs);
-    if (e == cudaSuccess && cs == cudaStreamCaptureStatusNone) {
-        e = cudaEventRecord(pl->used, st);
-        pl->pending = true;
-    }
+    if (!bytes || pl->capturing) return RNN_OK;
+    cudaError_t e = cudaEventRecord(pl->used, st);
+    pl->pending = true;
     return e == cudaSuccess ? RNN_OK : cuda_fail(e, "cudaEventRecord");
 }
 
