@@ -1,0 +1,78 @@
+"""The state space operators and token scores as differentiable functions.
+
+Thin torch.autograd wrappers of ``ssm``: each forward and each gradient is one
+entry point of the CUDA library.  Gradients are those of one backward pass
+(they are not differentiable again).
+"""
+from __future__ import annotations
+
+import torch
+
+from . import ssm
+
+
+class _Conv(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, plan, X, W, bias, sequence_lens, initial_state):
+        Y, state = ssm.ssm_conv(plan, X, W, bias, sequence_lens, initial_state)
+        ctx.plan = plan
+        ctx.save_for_backward(X, W, bias, sequence_lens, initial_state)
+        return Y, state
+
+    @staticmethod
+    def backward(ctx, dY, d_state):
+        X, W, bias, lens, h0 = ctx.saved_tensors
+        g = ssm.ssm_conv_grad(ctx.plan, dY.contiguous(), X, W, bias, lens, h0, d_state.contiguous())
+        return None, g["dX"], g["dW"], g.get("dbias"), None, g.get("d_initial_state")
+
+
+class _Scan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, plan, X, dt, A, B, C, D, Z, dt_bias, sequence_lens, initial_h):
+        args = (X, dt, A, B, C, D, Z, dt_bias, sequence_lens, initial_h)
+        Y, Y_h, saved = ssm.ssm_scan(plan, *args, save=True)
+        ctx.plan = plan
+        ctx.save_for_backward(saved, *args)
+        return Y, Y_h
+
+    @staticmethod
+    def backward(ctx, dY, dY_h):
+        saved, *args = ctx.saved_tensors
+        g = ssm.ssm_scan_grad(ctx.plan, dY.contiguous(), saved, *args, dY_h=dY_h.contiguous())
+        return (None, g["dX"], g["ddt"], g["dA"], g["dB"], g["dC"], g.get("dD"), g.get("dZ"), g.get("ddt_bias"), None,
+                g.get("d_initial_h"))
+
+
+class _Scores(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, ids, top):
+        r = ssm.scores(logits, ids, top=top)
+        ctx.top = top
+        ctx.save_for_backward(logits, ids, *r)
+        if r.top_ids is None:
+            return r.logp, r.entropy
+        ctx.mark_non_differentiable(r.top_ids)
+        return r.logp, r.entropy, r.top_ids, r.top_logp
+
+    @staticmethod
+    def backward(ctx, d_logp, d_entropy, d_ids=None, d_top=None):
+        logits, ids, *r = ctx.saved_tensors
+        dlogits = ssm.scores_grad(logits, ids, ssm.Scores(*r), d_logp.contiguous(), d_entropy.contiguous(),
+                                  None if d_top is None else d_top.contiguous())
+        return dlogits, None, None
+
+
+def conv(plan, X, W, bias=None, sequence_lens=None, initial_state=None):
+    """(Y, final_state) of the causal convolution, as ``ssm_conv``."""
+    return _Conv.apply(plan, X, W, bias, sequence_lens, initial_state)
+
+
+def scan(plan, X, dt, A, B, C, D=None, Z=None, dt_bias=None, sequence_lens=None, initial_h=None):
+    """(Y, Y_h) of the selective scan, as ``ssm_scan``."""
+    return _Scan.apply(plan, X, dt, A, B, C, D, Z, dt_bias, sequence_lens, initial_h)
+
+
+def scores(logits, ids, top=0):
+    """(logp, entropy), and (top_ids, top_logp) with top > 0, as ``scores``;
+    -logp is the cross entropy of the token."""
+    return _Scores.apply(logits, ids, top)

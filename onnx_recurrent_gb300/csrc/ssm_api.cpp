@@ -103,6 +103,25 @@ rnn_status check_views(const rnn_ssm* pl, const Named* views, int n)
     return RNN_OK;
 }
 
+struct NamedF32 {
+    const void* p;
+    const char* name;
+};
+// fp32 and int32 arrays: whether they are aligned to their elements.
+template <int N>
+rnn_status check_arrays(const NamedF32 (&arrays)[N])
+{
+    for (const NamedF32& a : arrays)
+        if ((uintptr_t)a.p % 4) return fail(RNN_ERR_INVALID_ARGUMENT, "%s is not aligned to its elements", a.name);
+    return RNN_OK;
+}
+// Arrays of the plan's io type.
+rnn_status check_state(const rnn_ssm* pl, const void* p, const char* name)
+{
+    if ((uintptr_t)p % element(pl->io)) return fail(RNN_ERR_INVALID_ARGUMENT, "%s is not aligned to its elements", name);
+    return RNN_OK;
+}
+
 rnn_status ensure_status(rnn_ssm* pl)
 {
     if (pl->status) return RNN_OK;
@@ -294,6 +313,10 @@ rnn_status rnn_ssm_conv(rnn_ssm_t pl, const rnn_ssm_conv_args* a)
     rs = check_views(pl, views, 2);
     if (rs != RNN_OK) return rs;
     NEED(a->W, "W");
+    rs = check_arrays({{a->W, "W"}, {a->bias, "bias"}, {a->sequence_lens, "sequence_lens"}});
+    if (rs == RNN_OK) rs = check_state(pl, a->initial_state, "initial_state");
+    if (rs == RNN_OK) rs = check_state(pl, a->final_state, "final_state");
+    if (rs != RNN_OK) return rs;
     rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
     ConvParams p = conv_params(pl, a->seq_length, a->batch_size);
@@ -317,6 +340,11 @@ rnn_status rnn_ssm_conv_grad(rnn_ssm_t pl, const rnn_ssm_conv_grad_args* a)
     rs = check_views(pl, views, 3);
     if (rs != RNN_OK) return rs;
     NEED(a->W, "W");
+    rs = check_arrays({{a->W, "W"}, {a->bias, "bias"}, {a->sequence_lens, "sequence_lens"}, {a->dW, "dW"}, {a->dbias, "dbias"}});
+    if (rs == RNN_OK) rs = check_state(pl, a->initial_state, "initial_state");
+    if (rs == RNN_OK) rs = check_state(pl, a->d_final_state, "d_final_state");
+    if (rs == RNN_OK) rs = check_state(pl, a->d_initial_state, "d_initial_state");
+    if (rs != RNN_OK) return rs;
     rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
     ConvGradParams p{};
@@ -357,6 +385,9 @@ rnn_status rnn_ssm_conv_step(rnn_ssm_t pl, const rnn_ssm_conv_step_args* a)
         NEED(a->state_out, "state_out");
     }
     rs = check_slots(a->slots, a->n_slots);
+    if (rs == RNN_OK) rs = check_arrays({{a->W, "W"}, {a->bias, "bias"}, {a->slots, "slots"}});
+    if (rs == RNN_OK) rs = check_state(pl, a->state, "state");
+    if (rs == RNN_OK) rs = check_state(pl, a->state_out, "state_out");
     if (rs == RNN_OK) rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
     ConvStepParams p{};
@@ -395,6 +426,9 @@ rnn_status rnn_ssm_scan(rnn_ssm_t pl, const rnn_ssm_scan_args* a)
     rs = check_views(pl, views, 6);
     if (rs != RNN_OK) return rs;
     NEED(a->A, "A");
+    rs = check_arrays({{a->A, "A"}, {a->Dskip, "Dskip"}, {a->dt_bias, "dt_bias"}, {a->sequence_lens, "sequence_lens"},
+                       {a->initial_h, "initial_h"}, {a->Y_h, "Y_h"}, {a->saved, "saved"}});
+    if (rs != RNN_OK) return rs;
     rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
     ScanParams p = scan_params(pl, a->seq_length, a->batch_size);
@@ -437,6 +471,10 @@ rnn_status rnn_ssm_scan_grad(rnn_ssm_t pl, const rnn_ssm_scan_grad_args* a)
     NEED(a->A, "A");
     if (steps) NEED(a->saved, "saved");
     if (a->dZ.data && !a->Z.data && steps) return fail(RNN_ERR_INVALID_ARGUMENT, "dZ without Z");
+    rs = check_arrays({{a->A, "A"}, {a->Dskip, "Dskip"}, {a->dt_bias, "dt_bias"}, {a->sequence_lens, "sequence_lens"},
+                       {a->initial_h, "initial_h"}, {a->saved, "saved"}, {a->dY_h, "dY_h"}, {a->dA, "dA"}, {a->dDskip, "dDskip"},
+                       {a->ddt_bias, "ddt_bias"}, {a->d_initial_h, "d_initial_h"}});
+    if (rs != RNN_OK) return rs;
     rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
     ScanGradParams p{};
@@ -489,6 +527,8 @@ rnn_status rnn_ssm_scan_step(rnn_ssm_t pl, const rnn_ssm_scan_step_args* a)
     NEED(a->H, "H");
     NEED(a->H_out, "H_out");
     rs = check_slots(a->slots, a->n_slots);
+    if (rs == RNN_OK)
+        rs = check_arrays({{a->A, "A"}, {a->Dskip, "Dskip"}, {a->dt_bias, "dt_bias"}, {a->H, "H"}, {a->H_out, "H_out"}, {a->slots, "slots"}});
     if (rs == RNN_OK) rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
     ScanStepParams p{};
@@ -523,6 +563,9 @@ rnn_status rnn_scores(const rnn_scores_args* a)
     rnn_status rs = check_scores(a->rows, a->vocab, a->row_stride, a->io, a->top, a->logits);
     if (rs != RNN_OK) return rs;
     if (a->rows == 0) return RNN_OK;
+    rs = check_arrays({{a->ids, "ids"}, {a->logp, "logp"}, {a->entropy, "entropy"}, {a->lse, "lse"}, {a->top_ids, "top_ids"},
+                       {a->top_logp, "top_logp"}});
+    if (rs != RNN_OK) return rs;
     if (a->logp && !a->ids) return fail(RNN_ERR_INVALID_ARGUMENT, "logp without ids");
     if (a->top > 0 && !a->top_ids && !a->top_logp) return fail(RNN_ERR_INVALID_ARGUMENT, "top without top_ids and top_logp");
     ScoreParams p{};
@@ -555,6 +598,9 @@ rnn_status rnn_scores_grad(const rnn_scores_grad_args* a)
     NEED(a->dlogits, "dlogits");
     if ((uintptr_t)a->dlogits % element((int)a->io))
         return fail(RNN_ERR_INVALID_ARGUMENT, "dlogits are not aligned to their elements");
+    rs = check_arrays({{a->ids, "ids"}, {a->lse, "lse"}, {a->entropy, "entropy"}, {a->d_logp, "d_logp"}, {a->d_entropy, "d_entropy"},
+                       {a->top_ids, "top_ids"}, {a->d_top, "d_top"}});
+    if (rs != RNN_OK) return rs;
     if (a->d_logp && !a->ids) return fail(RNN_ERR_INVALID_ARGUMENT, "d_logp without ids");
     if (a->d_entropy && !a->entropy) return fail(RNN_ERR_INVALID_ARGUMENT, "d_entropy without entropy");
     if (a->d_top && (!a->top_ids || a->top == 0)) return fail(RNN_ERR_INVALID_ARGUMENT, "d_top without top_ids");
