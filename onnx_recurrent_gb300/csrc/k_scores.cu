@@ -136,39 +136,60 @@ __device__ __forceinline__ void unpack_vec(const uint4& raw, float (&v)[N])
     for (int i = 0; i < N; ++i) v[i] = to_f(e[i]);
 }
 
-// N neighbouring logits.
+// N neighbouring logits, of which the largest and the smallest are given.
+// Ordinary ones (|m| < 2^60, none more than 2^6 below m, so no -inf) need one
+// operation for d and no lower bound on it.
 template <int N>
-__device__ __forceinline__ void take(Sums& a, const float (&x)[N])
+__device__ __forceinline__ void take(Sums& a, f2& s2, f2& u2, const float (&x)[N], float most, float least)
 {
-    float most = x[0];
-#pragma unroll
-    for (int e = 1; e < N; ++e) most = max_nan(most, x[e]);
-    if (!(most <= a.m)) raise_to(a, max_nan(a.m, most));
+    if (!(most <= a.m)) {
+        float v0, v1, w0, w1;
+        unpack2(s2, v0, v1);
+        unpack2(u2, w0, w1);
+        a.s = v0 + v1;
+        a.u = w0 + w1;
+        raise_to(a, max_nan(a.m, most));
+        s2 = pack2(a.s, 0.0f);
+        u2 = pack2(a.u, 0.0f);
+    }
     const float base = base_of(a.m);
-    if constexpr (N % 2 == 0) {
-        const f2 minus = dup2(-base), scale = dup2(kLog2e);
-        f2 s = pack2(a.s, 0.0f), u = pack2(a.u, 0.0f);
+    const f2 scale = dup2(kLog2e);
+    if (least > base - 64.0f && fabsf(base) < 1e18f) {
+        const f2 minus = dup2(-base * kLog2e);
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+            const f2 d = fma2(pack2(x[e], x[e + 1]), scale, minus), p = ex2_2(d);
+            s2 = add2(s2, p);
+            u2 = fma2(p, d, u2);
+        }
+    } else {
+        const f2 minus = dup2(-base);
 #pragma unroll
         for (int e = 0; e < N; e += 2) {
             const f2 d = mul2(add2(pack2(x[e], x[e + 1]), minus), scale), p = ex2_2(d);
             float d0, d1;
             unpack2(d, d0, d1);
-            s = add2(s, p);
-            u = fma2(p, pack2(fmaxf(d0, -150.0f), fmaxf(d1, -150.0f)), u);
-        }
-        float v0, v1;
-        unpack2(s, v0, v1);
-        a.s = v0 + v1;
-        unpack2(u, v0, v1);
-        a.u = v0 + v1;
-    } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const float d = (x[e] - base) * kLog2e, p = ex2(d);
-            a.s += p;
-            a.u = fmaf(p, fmaxf(d, -150.0f), a.u);
+            s2 = add2(s2, p);
+            u2 = fma2(p, pack2(fmaxf(d0, -150.0f), fmaxf(d1, -150.0f)), u2);
         }
     }
+}
+// The largest (a NaN counts as one) and smallest of 16 bytes of logits.
+__device__ __forceinline__ void extremes(const uint4& raw, const float (&x)[4], float& most, float& least, float)
+{
+    most = max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3]));
+    least = fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
+}
+template <typename V>
+__device__ __forceinline__ void extremes(const uint4& raw, const float (&x)[8], float& most, float& least, V)
+{
+    using V2 = std::conditional_t<std::is_same_v<V, __half>, __half2, __nv_bfloat162>;
+    __align__(16) V2 v[4];
+    *reinterpret_cast<uint4*>(v) = raw;
+    const V2 hi = __hmax2_nan(__hmax2_nan(v[0], v[1]), __hmax2_nan(v[2], v[3]));
+    const V2 lo = __hmin2(__hmin2(v[0], v[1]), __hmin2(v[2], v[3]));
+    most = max_nan(to_f(hi.x), to_f(hi.y));
+    least = fminf(to_f(lo.x), to_f(lo.y));
 }
 
 // A row's part [lo, hi): single logits at its ends, 16 bytes at a time between.
@@ -346,9 +367,10 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) scores_kernel(const S
     const Part<V> r(x, p.V, part, blocks);
     Sums a{neg_inf(), 0.0f, 0.0f};
     const int64_t one = r.single(threadIdx.x);
+    f2 s2 = 0, u2 = 0;
     if (one >= 0) {
-        const float v[1] = {to_f(x[one])};
-        take<1>(a, v);
+        const float v = to_f(x[one]), two[2] = {v, neg_inf()};
+        take<2>(a, s2, u2, two, v, neg_inf());
     }
     for (int v = threadIdx.x; v < r.vecs; v += AHEAD * THREADS) {
         uint4 raw[AHEAD];
@@ -358,10 +380,18 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) scores_kernel(const S
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k)
             if (v + k * THREADS < r.vecs) {
-                float e[N];
+                float e[N], most, least;
                 unpack_vec<V, N>(raw[k], e);
-                take<N>(a, e);
+                extremes(raw[k], e, most, least, V{});
+                take<N>(a, s2, u2, e, most, least);
             }
+    }
+    {
+        float v0, v1;
+        unpack2(s2, v0, v1);
+        a.s = v0 + v1;
+        unpack2(u2, v0, v1);
+        a.u = v0 + v1;
     }
     Key list = 0;
     if constexpr (TOP) list = largest<V, THREADS>(r, a.m, p.top, shared);

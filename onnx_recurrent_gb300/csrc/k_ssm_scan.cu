@@ -47,7 +47,7 @@ namespace {
 constexpr int E = 4;              // states of a lane
 constexpr int CH = 4;             // channels of a lane
 constexpr int T = 16;             // steps of a tile in shared memory
-constexpr int U = 4;              // steps of the inner loop's body
+constexpr int U = 8;              // steps of the inner loop's body
 constexpr int kFold = 16;         // chunks whose states a block chains itself
 struct ScanLaunch {
     int cblocks;          // blocks of channels in a group
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(Tile<V, L>::THREADS, 16 / Tile<V, L>::W)
         }
         __syncthreads();                       // B and C are in place (and each warp's own delta)
         if (warp * K::WC >= valid) continue;
-        // Four steps at a time: their y are stored together, because the loads
+        // U steps at a time: their y are stored together, because the loads
         // of a step cannot pass a store before them.
 #pragma unroll 1
         for (int t4 = 0; t4 < T; t4 += U) {
