@@ -1,21 +1,23 @@
 // Short causal convolution over time for each channel (the formulas stand in
 // include/onnx_recurrent.h), its gradients and its single-token form.
 //
-// The bytes bound it: 2 (4 with the gradient) 16-bit values an element, 12 (30)
-// instructions, of which the SMs have time for 40.  A thread takes NV
-// neighbouring channels of one row (four where the tensors allow it) and
-// walks along a run of steps with the next K sums in registers, so each
-// input is read once (and K - 1 again at the start of a run).  The thread's
-// inputs of the next kRing steps are on their way to its own places in shared memory,
-// so no barrier is needed and loads in flight cost no registers (with the
-// next four steps' in registers instead: 51 to 76 us for 8 rows of 2048 steps x 2048
-// bf16 channels, 32 us this way).  The gradient's walk
-// keeps the last K inputs and slopes of the sums: with pre[t] = bias + sum_j W[j]
-// X[t-K+1+j] and e[t] = dY[t] f'(pre[t]),
+// Little is computed for an element's bytes (2 values, 3 with the gradient), but
+// at 16 bits the instructions weigh as much.  A thread takes NV neighbouring
+// channels of one row (four where the tensors allow it), whose sums it forms in
+// packed pairs, and walks along a run of steps with the next K sums in
+// registers, so each input is read once (and K - 1 again at the start of a run).
+// The thread's inputs of the next kRing steps are on their way to its own places
+// in shared memory, so no barrier is needed and loads in flight cost no registers.
+// 8 rows of 2048 steps x 2048 bf16 channels, 4 taps, take 29 us (4.6 TB/s; 5.6 TB/s
+// with 32-bit values) and their gradient 66 us; with single arithmetic 32 us and
+// 79 us, with the next four steps' inputs in registers 51 to 76 us.
+// The gradient's walk keeps the last K inputs and slopes of the sums: with
+// pre[t] = bias + sum_j W[j] X[t-K+1+j] and e[t] = dY[t] f'(pre[t]),
 //     dX[u] = sum_j W[j] e[u+K-1-j],   dW[j] = sum_t e[t] X[t-K+1+j],
 // so after step t the walk can write dX[t-K+1].  dW and dbias are summed over
 // a run in registers, then over runs and rows in order by a kernel of their own.
 #include <initializer_list>
+#include <type_traits>
 
 #include "ssm_tile.cuh"
 
@@ -97,20 +99,108 @@ struct Ring {
     __device__ __forceinline__ V get(int slot) const { return at[slot * kThreads]; }
 };
 
+// NV channels' values: packed pairs, or the one channel's (packed arithmetic with
+// a half idle takes 156 us for the gradient of 8 rows of 2048 steps x 2047
+// bf16 channels, single arithmetic 110 us).
+template <int NV>
+struct Pairs {
+    using V = std::conditional_t<NV == 1, float, f2>;
+    static constexpr int N = (NV + 1) / 2;
+    V v[N];
+};
+__device__ __forceinline__ f2 plus(f2 a, f2 b) { return add2(a, b); }
+__device__ __forceinline__ float plus(float a, float b) { return a + b; }
+__device__ __forceinline__ f2 times_plus(f2 a, f2 b, f2 c) { return fma2(a, b, c); }
+__device__ __forceinline__ float times_plus(float a, float b, float c) { return fmaf(a, b, c); }
+// x f'(v) of silu
+__device__ __forceinline__ f2 silu_slope(f2 x, f2 v)
+{
+    const f2 o = sigmoid_fast2(v), one = dup2(1.0f);
+    return mul2(x, mul2(o, fma2(v, fma2(o, dup2(-1.0f), one), one)));
+}
+__device__ __forceinline__ float silu_slope(float x, float v)
+{
+    const float o = sigmoid_fast(v);
+    return x * (o * fmaf(v, 1.0f - o, 1.0f));
+}
+template <int NV>
+__device__ __forceinline__ Pairs<NV> make_pairs(const float (&x)[NV])
+{
+    Pairs<NV> r;
+    if constexpr (NV == 1) {
+        r.v[0] = x[0];
+    } else {
+#pragma unroll
+        for (int e = 0; e < NV / 2; ++e) r.v[e] = pack2(x[2 * e], x[2 * e + 1]);
+    }
+    return r;
+}
+template <typename T, int NV>
+__device__ __forceinline__ Pairs<NV> pairs_of(const Vec<T, NV>& x)
+{
+    float f[NV];
+#pragma unroll
+    for (int e = 0; e < NV; ++e) f[e] = to_f(x.v[e]);
+    return make_pairs<NV>(f);
+}
+template <int NV>
+__device__ __forceinline__ void floats_of(const Pairs<NV>& x, float (&f)[NV])
+{
+    if constexpr (NV == 1) {
+        f[0] = x.v[0];
+    } else {
+#pragma unroll
+        for (int e = 0; e < NV / 2; ++e) unpack2(x.v[e], f[2 * e], f[2 * e + 1]);
+    }
+}
+template <typename T, int NV>
+__device__ __forceinline__ Vec<T, NV> vec_of(const Pairs<NV>& x)
+{
+    Vec<T, NV> r;
+    float f[NV];
+    floats_of(x, f);
+#pragma unroll
+    for (int e = 0; e < NV; ++e) r.v[e] = from_f<T>(f[e]);
+    return r;
+}
+template <int NV>
+__device__ __forceinline__ Pairs<NV> fma_pairs(const Pairs<NV>& a, const Pairs<NV>& b, const Pairs<NV>& c)
+{
+    Pairs<NV> r;
+#pragma unroll
+    for (int e = 0; e < Pairs<NV>::N; ++e) r.v[e] = times_plus(a.v[e], b.v[e], c.v[e]);
+    return r;
+}
+template <int NV>
+__device__ __forceinline__ Pairs<NV> silu_pairs(const Pairs<NV>& v)
+{
+    Pairs<NV> r;
+#pragma unroll
+    for (int e = 0; e < Pairs<NV>::N; ++e)
+        if constexpr (NV == 1) r.v[e] = silu_fast(v.v[e]);
+        else r.v[e] = silu_fast2(v.v[e]);
+    return r;
+}
+
 template <int K, int NV>
 struct Weights {
-    float w[NV * K], bias[NV];
+    Pairs<NV> w[K], bias;
     __device__ __forceinline__ Weights(const ConvParams& p, int64_t d)
     {
-        load_floats(p.W + d * K, w);
-        if (p.bias) {
-            load_floats(p.bias + d, bias);
-        } else {
+        float all[NV * K], b[NV];
+        load_floats(p.W + d * K, all);
 #pragma unroll
-            for (int e = 0; e < NV; ++e) bias[e] = 0.0f;
+        for (int j = 0; j < K; ++j) {
+            float tap[NV];
+#pragma unroll
+            for (int e = 0; e < NV; ++e) tap[e] = all[e * K + j];
+            w[j] = make_pairs<NV>(tap);
         }
+#pragma unroll
+        for (int e = 0; e < NV; ++e) b[e] = 0.0f;
+        if (p.bias) load_floats(p.bias + d, b);
+        bias = make_pairs<NV>(b);
     }
-    __device__ __forceinline__ float of(int tap, int e) const { return w[e * K + tap]; }
 };
 
 // What a thread has: channels d .., row n, steps t0 .. t1-1; false: nothing.
@@ -137,49 +227,47 @@ __global__ void __launch_bounds__(kThreads, K <= 4 ? 8 : 4) ssm_conv_kernel(cons
     if (t0 < live) {
         const Weights<K, NV> w(p, d);
         // sums[i]: what the inputs so far give to the sum i steps ahead, taps in order from the bias
-        float sums[K][NV];
+        Pairs<NV> sums[K];
 #pragma unroll
-        for (int j = 0; j < K; ++j)
-#pragma unroll
-            for (int e = 0; e < NV; ++e) sums[j][e] = w.bias[e];
+        for (int j = 0; j < K; ++j) sums[j] = w.bias;
         // takes the next input, returns the sum that it completes
-        auto next = [&](float x, int e) {
-            const float done = fmaf(w.of(K - 1, e), x, sums[0][e]);
+        auto next = [&](const Pairs<NV>& x) {
+            const Pairs<NV> done = fma_pairs(w.w[K - 1], x, sums[0]);
 #pragma unroll
-            for (int j = 0; j + 1 < K; ++j) sums[j][e] = fmaf(w.of(K - 2 - j, e), x, sums[j + 1][e]);
+            for (int j = 0; j + 1 < K; ++j) sums[j] = fma_pairs(w.w[K - 2 - j], x, j + 2 < K ? sums[j + 1] : w.bias);
             return done;
         };
 #pragma unroll
-        for (int j = 0; j + 1 < K; ++j) {
-            const Vec<T, NV> r = conv_input<T, K, NV>(p, n, t0 - K + 1 + j, d);
-#pragma unroll
-            for (int e = 0; e < NV; ++e) next(to_f(r.v[e]), e);
-        }
+        for (int j = 0; j + 1 < K; ++j) next(pairs_of(conv_input<T, K, NV>(p, n, t0 - K + 1 + j, d)));
         const Ring<T, NV> ring{ring_mem[0] + threadIdx.x};
-        const T* x = static_cast<const T*>(p.X.data) + n * p.X.bs + d;
+        const int steps = (int)(live - t0);
+        const T* x = static_cast<const T*>(p.X.data) + n * p.X.bs + d + t0 * p.X.ss;      // the next input to start
 #pragma unroll
         for (int i = 0; i < kRing; ++i) {
-            ring.start(i, x + (t0 + i) * p.X.ss, t0 + i < live, p.X.data);
+            ring.start(i, x, i < steps, p.X.data);
             cp_async_commit();
+            x += p.X.ss;
         }
-        const int steps = (int)(live - t0);
+        T* to = y + t0 * p.Y.ss;
         for (int i0 = 0; i0 < steps; i0 += kUnroll) {
 #pragma unroll
             for (int i = 0; i < kUnroll; ++i) {
                 const int slot = (i0 + i) % kRing;
                 cp_async_wait<kRing - 1>();
-                const Vec<T, NV> r = ring.get(slot);
-                Vec<T, NV> out;
-#pragma unroll
-                for (int e = 0; e < NV; ++e) {
-                    const float v = next(to_f(r.v[e]), e);
-                    out.v[e] = from_f<T>(p.silu ? silu_fast(v) : v);
+                Pairs<NV> v = next(pairs_of(ring.get(slot)));
+                if (p.silu) v = silu_pairs(v);
+                if (i0 + i < steps) *reinterpret_cast<Vec<T, NV>*>(to) = vec_of<T>(v);
+                to += p.Y.ss;
+                if (ring.ASYNC) {
+                    ring.start(slot, x, i0 + i + kRing < steps, p.X.data);
+                    x += p.X.ss;
                 }
-                if (i0 + i < steps) *reinterpret_cast<Vec<T, NV>*>(y + (t0 + i0 + i) * p.Y.ss) = out;
-                if (ring.ASYNC) ring.start(slot, x + (t0 + i0 + i + kRing) * p.X.ss, i0 + i + kRing < steps, p.X.data);
                 cp_async_commit();
             }
-            if (!ring.ASYNC) ring.refill(i0, x + (t0 + i0 + kRing) * p.X.ss, p.X.ss, steps - i0 - kRing);
+            if (!ring.ASYNC) {
+                ring.refill(i0, x, p.X.ss, steps - i0 - kRing);
+                x += kUnroll * p.X.ss;
+            }
         }
         cp_async_wait<0>();
     }
@@ -204,100 +292,96 @@ __global__ void __launch_bounds__(kThreads, K <= 4 ? 5 : 3) ssm_conv_grad_kernel
     if (!find<NV>(p, dblocks, runs, run, d, n, t0, t1)) return;
     const int64_t len = row_length(p.lens, n, p.S, p.status);
     const Weights<K, NV> w(p, d);
-    float x[K][NV], s[K][NV], dw[K][NV], db[NV];
+    Pairs<NV> zeros;
+#pragma unroll
+    for (int e = 0; e < Pairs<NV>::N; ++e) zeros.v[e] = 0;
+    Pairs<NV> x[K], s[K], dw[K], db = zeros;
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-        Vec<T, NV> r;
-        const bool on = j > 0 && t0 < len;
-        if (on) r = conv_input<T, K, NV>(p, n, t0 - K + j, d);
-#pragma unroll
-        for (int e = 0; e < NV; ++e) {
-            x[j][e] = on ? to_f(r.v[e]) : 0.0f;
-            s[j][e] = dw[j][e] = db[e] = 0.0f;
-        }
+        x[j] = j > 0 && t0 < len ? pairs_of(conv_input<T, K, NV>(p, n, t0 - K + j, d)) : zeros;
+        s[j] = dw[j] = zeros;
     }
-    const T* dy = static_cast<const T*>(q.dY.data) + n * q.dY.bs + d;
     const T* dhT = static_cast<const T*>(q.dhT);
     const Ring<T, NV> ring_x{ring_mem[0][0] + threadIdx.x}, ring_y{ring_mem[1][0] + threadIdx.x};
-    const T* xs = static_cast<const T*>(p.X.data) + n * p.X.bs + d;
     // slopes of the run's steps, and of the K-1 after it that its inputs reach
-    const int steps = (int)(t1 - t0) + K - 1, known = len - t0 < steps ? (int)(len > t0 ? len - t0 : 0) : steps;
+    const int owned = (int)(t1 - t0), steps = owned + K - 1, known = len - t0 < steps ? (int)(len > t0 ? len - t0 : 0) : steps;
+    const T* xs = static_cast<const T*>(p.X.data) + n * p.X.bs + d + t0 * p.X.ss;         // the next ones to start
+    const T* ys = static_cast<const T*>(q.dY.data) + n * q.dY.bs + d + t0 * q.dY.ss;
     auto start = [&](int i) {
-        ring_x.start(i % kRing, xs + (t0 + i) * p.X.ss, i < known, p.X.data);
-        ring_y.start(i % kRing, dy + (t0 + i) * q.dY.ss, i < known, p.X.data);
-        cp_async_commit();
+        ring_x.start(i % kRing, xs, i < known, p.X.data);
+        ring_y.start(i % kRing, ys, i < known, p.X.data);
+        xs += p.X.ss;
+        ys += q.dY.ss;
     };
 #pragma unroll
-    for (int i = 0; i < kRing; ++i) start(i);
+    for (int i = 0; i < kRing; ++i) {
+        start(i);
+        cp_async_commit();
+    }
+    T* to = static_cast<T*>(q.dX.data) + n * q.dX.bs + d + (t0 - K + 1) * q.dX.ss;       // of step u below
+    const int last = dhT && len - (K - 1) - t0 < steps ? (int)(len - (K - 1) - t0) : steps;      // u - t0 from which dhT reaches
     for (int i0 = 0; i0 < steps; i0 += kUnroll) {
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
-            const int k = i0 + i;
+            const int k = i0 + i, u = k - K + 1;     // the input whose slopes are complete, from t0
             cp_async_wait<kRing - 1>();
-            const Vec<T, NV> rx = ring_x.get(k % kRing), ry = ring_y.get(k % kRing);
-            const bool own = k < known && k < (int)(t1 - t0);
 #pragma unroll
-            for (int e = 0; e < NV; ++e) {
-#pragma unroll
-                for (int j = 0; j + 1 < K; ++j) {
-                    x[j][e] = x[j + 1][e];
-                    s[j][e] = s[j + 1][e];
-                }
-                x[K - 1][e] = to_f(rx.v[e]);           // zero past the row's end, as is dY
-                float v = w.bias[e];
-#pragma unroll
-                for (int j = 0; j < K; ++j) v = fmaf(w.of(j, e), x[j][e], v);
-                float g = to_f(ry.v[e]);
-                if (p.silu) {
-                    const float o = sigmoid_fast(v);
-                    g *= o * fmaf(v, 1.0f - o, 1.0f);
-                }
-                s[K - 1][e] = k < known ? g : 0.0f;
-                const float mine = own ? g : 0.0f;
-                db[e] += mine;
-#pragma unroll
-                for (int j = 0; j < K; ++j) dw[j][e] = fmaf(mine, x[j][e], dw[j][e]);
+            for (int j = 0; j + 1 < K; ++j) {
+                x[j] = x[j + 1];
+                s[j] = s[j + 1];
             }
-            const int64_t u = t0 + k - K + 1;   // the input whose slopes are complete: s[0] belongs to step u
-            if (k < steps && (u >= t0 || t0 == 0)) {
-                float g[NV];
+            x[K - 1] = pairs_of(ring_x.get(k % kRing));          // zero past the row's end, as is dY
+            Pairs<NV> g = pairs_of(ring_y.get(k % kRing));
+            if (p.silu) {
+                Pairs<NV> v = w.bias;
 #pragma unroll
-                for (int e = 0; e < NV; ++e) {
-                    g[e] = 0.0f;
+                for (int j = 0; j < K; ++j) v = fma_pairs(w.w[j], x[j], v);
 #pragma unroll
-                    for (int j = 0; j < K; ++j) g[e] = fmaf(w.of(K - 1 - j, e), s[j][e], g[e]);
+                for (int e = 0; e < Pairs<NV>::N; ++e) g.v[e] = silu_slope(g.v[e], v.v[e]);
+            }
+            s[K - 1] = k < known ? g : zeros;
+            if (k < known && k < owned) {
+#pragma unroll
+                for (int e = 0; e < Pairs<NV>::N; ++e) db.v[e] = plus(db.v[e], g.v[e]);
+#pragma unroll
+                for (int j = 0; j < K; ++j) dw[j] = fma_pairs(g, x[j], dw[j]);
+            }
+            if (k < steps && (u >= 0 || t0 == 0)) {
+                Pairs<NV> sum = zeros;
+#pragma unroll
+                for (int j = 0; j < K; ++j) sum = fma_pairs(w.w[K - 1 - j], s[j], sum);
+                if (u >= last && u < known && t0 + u < len) {
+                    const int64_t at = (n * (K - 1) + (t0 + u - len + K - 1)) * p.D + d;
+                    const Pairs<NV> more = pairs_of(*reinterpret_cast<const Vec<T, NV>*>(dhT + at));
+#pragma unroll
+                    for (int e = 0; e < Pairs<NV>::N; ++e) sum.v[e] = plus(sum.v[e], more.v[e]);
                 }
-                if (dhT && u >= len - (K - 1) && u < len) {
-                    const Vec<T, NV> more = *reinterpret_cast<const Vec<T, NV>*>(dhT + (n * (K - 1) + (u - len + K - 1)) * p.D + d);
-#pragma unroll
-                    for (int e = 0; e < NV; ++e) g[e] += to_f(more.v[e]);
-                }
-                Vec<T, NV> out;
-#pragma unroll
-                for (int e = 0; e < NV; ++e) out.v[e] = from_f<T>(g[e]);
-                T* to = nullptr;
                 if (u >= 0) {
-                    if (q.dX.data) to = static_cast<T*>(q.dX.data) + u * q.dX.ss + n * q.dX.bs + d;
+                    if (q.dX.data) *reinterpret_cast<Vec<T, NV>*>(to) = vec_of<T>(sum);
                 } else if (q.dh0) {
-                    to = static_cast<T*>(q.dh0) + (n * (K - 1) + (u + K - 1)) * p.D + d;
+                    *reinterpret_cast<Vec<T, NV>*>(static_cast<T*>(q.dh0) + (n * (K - 1) + (u + K - 1)) * p.D + d) = vec_of<T>(sum);
                 }
-                if (to) *reinterpret_cast<Vec<T, NV>*>(to) = out;
             }
+            to += q.dX.ss;
             if (ring_x.ASYNC) start(k + kRing);
+            cp_async_commit();
         }
         if (!ring_x.ASYNC) {
-            ring_x.refill(i0, xs + (t0 + i0 + kRing) * p.X.ss, p.X.ss, known - i0 - kRing);
-            ring_y.refill(i0, dy + (t0 + i0 + kRing) * q.dY.ss, q.dY.ss, known - i0 - kRing);
+            ring_x.refill(i0, xs, p.X.ss, known - i0 - kRing);
+            ring_y.refill(i0, ys, q.dY.ss, known - i0 - kRing);
+            xs += kUnroll * p.X.ss;
+            ys += kUnroll * q.dY.ss;
         }
     }
     cp_async_wait<0>();
     if (q.part) {
         float* part = q.part + (n * runs + t0 / run) * p.D * (K + 1);
 #pragma unroll
-        for (int e = 0; e < NV; ++e) {
+        for (int j = 0; j <= K; ++j) {
+            float v[NV];
+            floats_of(j < K ? dw[j < K ? j : 0] : db, v);
 #pragma unroll
-            for (int j = 0; j < K; ++j) part[(d + e) * K + j] = dw[j][e];
-            part[p.D * K + d + e] = db[e];
+            for (int e = 0; e < NV; ++e) part[j < K ? (d + e) * K + j : p.D * K + d + e] = v[e];
         }
     }
 }
