@@ -1,12 +1,15 @@
 // Scores of rows of logits and their gradient (the formulas stand in
 // include/onnx_recurrent.h).
 //
-// One pass over a row keeps, per thread, the largest logit m so far and, with
-// d_i = (x_i - m) log2 e <= 0,
+// One pass over a row keeps, per thread, a logit m that none so far exceeds by
+// more than kSlack and, with d_i = (x_i - m) log2 e,
 //     s = sum_i 2^d_i,   u = sum_i d_i 2^d_i
 // (when m grows by g, in the same unit: u = (u - g s) 2^-g, s = s 2^-g), from which
-//     lse = m + log s,      entropy = log s - u / s log 2:
-// both parts of the entropy are >= 0, so nothing cancels.  A -inf adds 0 to
+//     lse = m + log s,      entropy = log s - u / s log 2.
+// With kSlack = 0 both parts of the entropy are >= 0 and nothing cancels; the
+// slack of 4 lets at most 4 units of them cancel (an error of 4 * 2^-24), and spares a
+// warp, one of whose 32 threads finds a larger logit nearly every time, the
+// growing (8192 rows of 32000 bf16 logits: 107 us without the slack, 101 us with it).  A -inf adds 0 to
 // both sums (u takes d no lower than -150, where 2^d is 0); a NaN or +inf makes s NaN.
 //
 // Alternatives: the pass leaves every thread its largest logit.  The `top`-th
@@ -18,12 +21,14 @@
 // first equal ones are taken; if even those above it are too many, each warp
 // keeps a sorted list of the 32 largest keys, one per lane, and inserts what is above the
 // last one wanted (done for every row, that took 677 us for 8192 rows of
-// 32000 bf16 logits, top 20, against 163 us this way).  Sorted lists are joined by
+// 32000 bf16 logits, top 20, against 149 us this way).  Sorted lists are joined by
 // taking the larger of one and the other reversed, and sorting that.
 //
-// The bytes bound it: a logit is read once (twice with the gradient, which
-// writes it once); about 5 instructions a logit, of 11 that the SMs have
-// time for at 16-bit logits.  A row is a block's; with fewer rows than fill the
+// A logit is read once (once more by the gradient, which writes it once).  At 16
+// bits the SMs' issue slots bind before the bytes do: about 12 instructions a
+// logit (conversion, d, 2^d, two sums, the extremes), four fifths of the slots.
+// The rows above take 101 us (5.2 TB/s; a copy's rate is 6.8 TB/s), their gradient 180 us
+// (5.8 TB/s), and as many bytes of 32-bit logits, top 8, 108 us (4.8 TB/s).  A row is a block's; with fewer rows than fill the
 // SMs it is a cluster's, whose blocks' results the first joins through
 // distributed shared memory, so no launch and no memory is needed for that.
 #include <type_traits>
@@ -35,6 +40,7 @@ namespace rnngb {
 namespace {
 
 constexpr int kMaxCluster = 8;
+constexpr float kSlack = 4.0f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
@@ -142,7 +148,7 @@ __device__ __forceinline__ void unpack_vec(const uint4& raw, float (&v)[N])
 template <int N>
 __device__ __forceinline__ void take(Sums& a, f2& s2, f2& u2, const float (&x)[N], float most, float least)
 {
-    if (!(most <= a.m)) {
+    if (!(most <= a.m + kSlack)) {
         float v0, v1, w0, w1;
         unpack2(s2, v0, v1);
         unpack2(u2, w0, w1);
@@ -372,6 +378,7 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) scores_kernel(const S
         const float v = to_f(x[one]), two[2] = {v, neg_inf()};
         take<2>(a, s2, u2, two, v, neg_inf());
     }
+    float most_here = one >= 0 ? to_f(x[one]) : neg_inf();       // this thread's largest
     for (int v = threadIdx.x; v < r.vecs; v += AHEAD * THREADS) {
         uint4 raw[AHEAD];
 #pragma unroll
@@ -383,6 +390,7 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) scores_kernel(const S
                 float e[N], most, least;
                 unpack_vec<V, N>(raw[k], e);
                 extremes(raw[k], e, most, least, V{});
+                if (TOP) most_here = max_nan(most_here, most);
                 take<N>(a, s2, u2, e, most, least);
             }
     }
@@ -394,7 +402,7 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) scores_kernel(const S
         a.u = v0 + v1;
     }
     Key list = 0;
-    if constexpr (TOP) list = largest<V, THREADS>(r, a.m, p.top, shared);
+    if constexpr (TOP) list = largest<V, THREADS>(r, most_here, p.top, shared);
 #pragma unroll
     for (int o = 16; o > 0; o /= 2)
         join(a, Sums{__shfl_xor_sync(~0u, a.m, o), __shfl_xor_sync(~0u, a.s, o), __shfl_xor_sync(~0u, a.u, o)});
