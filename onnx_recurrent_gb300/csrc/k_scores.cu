@@ -7,10 +7,11 @@
 // (when m grows by g, in the same unit: u = (u - g s) 2^-g, s = s 2^-g), from which
 //     lse = m + log s,      entropy = log s - u / s log 2.
 // With kSlack = 0 both parts of the entropy are >= 0 and nothing cancels; the
-// slack of 4 lets at most 4 units of them cancel (an error of 4 * 2^-24), and spares a
-// warp, one of whose 32 threads finds a larger logit nearly every time, the
-// growing (8192 rows of 32000 bf16 logits: 107 us without the slack, 101 us with it).  A -inf adds 0 to
-// both sums (u takes d no lower than -150, where 2^d is 0); a NaN or +inf makes s NaN.
+// slack of 4 lets at most 4 units of them cancel (an error of 4 * 2^-24, kept from
+// making an entropy negative), and spares a warp, one of whose 32 threads finds a
+// larger logit nearly every time, the growing (8192 rows of 32000 bf16 logits: 107 us
+// without the slack, 101 us with it).  A -inf adds 0 to both sums (u takes d no
+// lower than -150, where 2^d is 0); a NaN or +inf makes s NaN.
 //
 // Alternatives: the pass leaves every thread its largest logit.  The `top`-th
 // largest of these is a bound that at least `top` logits reach, and logits that reach it
@@ -28,9 +29,11 @@
 // bits the SMs' issue slots bind before the bytes do: about 12 instructions a
 // logit (conversion, d, 2^d, two sums, the extremes), four fifths of the slots.
 // The rows above take 101 us (5.2 TB/s; a copy's rate is 6.8 TB/s), their gradient 180 us
-// (5.8 TB/s), and as many bytes of 32-bit logits, top 8, 108 us (4.8 TB/s).  A row is a block's; with fewer rows than fill the
-// SMs it is a cluster's, whose blocks' results the first joins through
-// distributed shared memory, so no launch and no memory is needed for that.
+// (5.8 TB/s), and as many bytes of 32-bit logits, top 8, 108 us (4.8 TB/s).  Tried and
+// no faster: one, three or four 16-byte loads ahead instead of two, copies to a
+// ring in shared memory.  A row is a block's; with fewer rows than fill the SMs it is
+// a cluster's, whose blocks' results the first joins through distributed
+// shared memory, so no launch and no memory is needed for that.
 #include <type_traits>
 
 #include "ssm_tile.cuh"
@@ -444,7 +447,7 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) scores_kernel(const S
     const float lse = bad ? a_nan() : empty ? neg_inf() : a.m + total;
     if (lane == 0) {
         if (p.lse) p.lse[row] = lse;
-        if (p.entropy) p.entropy[row] = bad ? a_nan() : empty ? 0.0f : total - a.u * kLn2 / a.s;
+        if (p.entropy) p.entropy[row] = bad ? a_nan() : empty ? 0.0f : fmaxf(total - a.u * kLn2 / a.s, 0.0f);
         if (p.logp) {
             const int id = p.ids[row];
             p.logp[row] = id < 0 ? 0.0f : id >= p.V ? a_nan() : empty ? neg_inf() : to_f(x[id]) - lse;

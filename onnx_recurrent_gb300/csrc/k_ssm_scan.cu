@@ -20,14 +20,15 @@
 //     selected.
 // The next tile's inputs are copied while a tile is computed.
 //
-// Measured (38 rows of 512 steps, 2048 channels, M = 16, bf16: all SMs full):
-// 206 us, 3.1 updates a ns, a third of the pipes' bound.  Counters: issue slots
-// 59 % busy, fp32 pipe 60 %, shared memory 57 %, exponentials 40 %; with parts
-// left out, the loop over steps takes 64 % of the time (its loads and
+// Measured (38 rows of 1024 steps, 2048 channels, M = 16, bf16: all SMs full):
+// 395 us, 3.2 updates a ns, a third of the pipes' bound.  Counters: issue slots
+// 59 % busy, fp32 pipe 58 %, shared memory 52 %, exponentials 38 %, DRAM 17 %; with
+// parts left out, the loop over steps takes 64 % of the time (its loads and
 // exchanges half of that), softplus and gate 9 %, copies 7 %, the rest goes to
-// the passes' shared memory and barriers.  Tried at the same size and no faster:
-// 8 channels a lane (252 us, fewer warps), 2 (337 us), scalar instead of
-// packed operations, 8 or 32 steps a tile, 5 to 8 blocks an SM.
+// the passes' shared memory and barriers.  Four steps a loop body instead of U: 4 %
+// slower.  Tried (512 steps, 206 us then) and no faster: 8 channels a lane (252 us, fewer
+// warps), 2 (337 us), scalar instead of packed operations, 8 or 32 steps a tile,
+// 5 to 8 blocks an SM.
 //
 // When rows and channels are too few for the SMs, the steps are split in
 // chunks: one launch finds each chunk's end state from zero and the sum of
@@ -406,8 +407,8 @@ constexpr int64_t kMaxGrid = 0x7fffffff;
 // every scheduler: 239, 342, 375, 402; the chunks' end states cost another 0.72
 // of a pass.  With few warps the latency of a step's chain shows, so splitting
 // pays: 8 rows of 2048 steps x 2048 channels take 490 us unsplit and 295 us in
-// 14 chunks, one row of 16384 steps 292 us in 38; 64 rows of 512 steps fill
-// the SMs and take 356 us unsplit, 488 us in two.
+// 14 chunks, one row of 16384 steps 288 us in 38; 64 rows of 512 steps fill
+// the SMs and take 343 us unsplit, 488 us in two.
 constexpr ScanCost kCost{4, {0, 239, 342, 375, 402}, 2500, 0.72};
 
 template <typename V, int L>

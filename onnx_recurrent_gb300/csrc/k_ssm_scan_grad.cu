@@ -27,13 +27,14 @@
 // finds the q that each chunk passes on when none enters; with up to kFold
 // chunks a block chains those after its own, with more another launch does.
 //
-// Measured (38 rows of 512 steps, 2048 channels, M = 16, bf16, SMs full): 838 us,
-// 0.76 updates a ns; 390 instructions for 512 updates, 140 of them packed fp32
-// ones, 43 exponentials.  Issue slots are 47 % busy, the fp32 pipe 46 %, shared
-// memory 36 %, DRAM 16 %: two or three warps a scheduler do not hide a step's
-// latencies, and more do not fit the registers (three with 168 and a few spills:
-// 837 us for 8 rows of 2048 steps; two with 240: 873 us; four with 128: 919 us).
-// Scalar instead of packed operations: 5 to 15 % slower.
+// Measured (8 rows of 2048 steps, 2048 channels, M = 16, bf16): 832 us, 0.65 updates
+// a ns with the launch for the chunks' q; 390 instructions for 512 updates, 140 of
+// them packed fp32 ones, 43 exponentials.  Counters with the SMs full: issue slots 38 to
+// 47 % busy, the fp32 pipe 29 to 46 %, shared memory 30 to 36 %, DRAM 11 to 16 %: three warps
+// a scheduler do not hide a step's latencies, and more do not fit the registers
+// (three blocks an SM with 168; two with 240: 873 us; four with 128: 919 us).
+// Scalar instead of packed operations: 5 to 15 % slower; dA summed in shared memory
+// to free registers: no faster.
 #include <type_traits>
 
 #include "ssm_tile.cuh"
@@ -760,9 +761,9 @@ constexpr int64_t kMaxGrid = 0x7fffffff;
 
 // Measured times of a step (M = 16, bf16, gate, in ns) with 1 .. 3 warps on
 // every scheduler: 687, 807, 1120; finding the chunks' q costs another quarter
-// of a pass.  8 rows of 2048 steps x 2048 channels take 1408 us unsplit, 837 us in 7
-// chunks; one row of 16384 steps 840 us in 57; 64 rows of 512 steps fill the SMs
-// and take 1505 us unsplit, 1553 us in two.
+// of a pass.  8 rows of 2048 steps x 2048 channels take 1408 us unsplit, 832 us in 7
+// chunks; one row of 16384 steps 845 us in 57; 64 rows of 512 steps fill the SMs
+// and take 1501 us unsplit, 1553 us in two.
 constexpr ScanCost kCost{3, {0, 687, 807, 1120}, 3000, 0.25};
 
 template <typename V, int L>

@@ -7,7 +7,11 @@
 // delta X, the gate) is formed first, once for a channel and row, in shared memory; then a
 // lane keeps its part of A, and its states of the next AHEAD rows are on their way to
 // its own places in shared memory: loads in flight are what bandwidth needs,
-// and cost no registers there.
+// and cost no registers there.  256 rows x 4096 channels x 16 states take 29 us (4.6 TB/s
+// of states), 256 x 2048 x 64 56 us (4.8 TB/s); with the next rows' states in registers
+// 50 to 81 us.  Also measured for the former: 4 blocks an SM 32 us, 6 32 us, 8 38 us;
+// 4 rows a block 36 us, 16 34 us; 2 rows ahead 32 us, 8 35 us (6 blocks an SM).  A block's
+// first loads and the last, partly filled wave of blocks hold back the rest.
 #include "ssm_tile.cuh"
 
 namespace rnngb {
@@ -39,10 +43,10 @@ __device__ __forceinline__ void load4(const V* from, int m, int M, bool vec, flo
 constexpr int kAhead = 4;
 
 template <typename V, int L, int ROWS>
-__global__ void __launch_bounds__(kThreads) ssm_scan_step_kernel(const ScanStepParams p, int cblocks, bool vec)
+__global__ void __launch_bounds__(kThreads, 5) ssm_scan_step_kernel(const ScanStepParams p, int cblocks, bool vec)
 {
     constexpr int CB = kThreads / L, ME = L * E, AHEAD = ROWS < kAhead ? ROWS : kAhead;
-    __shared__ int64_t slots[ROWS];                   // -1: no state
+    __shared__ int64_t slots[ROWS], first[ROWS];      // -1: no state; its first value
     __shared__ float4 ring[AHEAD][kThreads];
     __shared__ float4 pre[ROWS][CB];                  // delta, delta X, Dskip X, gate
     __shared__ __align__(16) float bc[ROWS][2][ME];
@@ -64,13 +68,15 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_step_kernel(const ScanStepP
             }
         }
         slots[threadIdx.x] = slot;
+        first[threadIdx.x] = slot * p.D * p.M;
     }
     if (threadIdx.x == 0) groups = (int)(((c0 + CB < p.D ? c0 + CB : p.D) - 1) / dg - g0) + 1;
     __syncthreads();
     // with vec, states come through the ring
+    const float* from = p.H + d * p.M + m;
+    float* to = p.H_out + d * p.M + m;
     auto start = [&](int r) {
-        if (r < rows && slots[r] >= 0 && m < p.M)
-            cp_async16(&ring[r % AHEAD][threadIdx.x], p.H + (slots[r] * p.D + d) * p.M + m, 16);
+        if (r < rows && first[r] >= 0 && m < p.M) cp_async16(&ring[r % AHEAD][threadIdx.x], from + first[r], 16);
         cp_async_commit();
     };
     if (vec) {
@@ -97,9 +103,38 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_step_kernel(const ScanStepP
             bc[r][w][k] = k < p.M ? ld<V>(w ? p.C : p.B, n0 + r, g0 * p.M + k) : 0.0f;
         }
     __syncthreads();
+    V* y = static_cast<V*>(p.Y.data) + n0 * p.Y.bs + d;
+    if (vec && shared_bc) {       // the ordinary case, in packed pairs and without the others' choices
+        const f2 a0 = pack2(a[0], a[1]), a1 = pack2(a[2], a[3]);
+        const bool mine = on && m < p.M;
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            if (r >= rows) break;
+            const int64_t at = first[r];
+            const float4 v = pre[r][on ? ch : 0];
+            const ulonglong2 vb = *reinterpret_cast<const ulonglong2*>(&bc[r][0][m]), vc = *reinterpret_cast<const ulonglong2*>(&bc[r][1][m]);
+            cp_async_wait<AHEAD - 1>();
+            ulonglong2 h = *reinterpret_cast<const ulonglong2*>(&ring[r % AHEAD][threadIdx.x]);
+            const f2 delta = dup2(v.x), dx = dup2(v.y);
+            h.x = fma2(ex2_2(mul2(delta, a0)), h.x, mul2(dx, vb.x));
+            h.y = fma2(ex2_2(mul2(delta, a1)), h.y, mul2(dx, vb.y));
+            if (r + AHEAD < ROWS) start(r + AHEAD);
+            else cp_async_commit();
+            if (mine && at >= 0) *reinterpret_cast<ulonglong2*>(to + at) = h;
+            float s0, s1;
+            unpack2(fma2(vc.y, h.y, mul2(vc.x, h.x)), s0, s1);
+            float s = m < p.M ? s0 + s1 : 0.0f;
+#pragma unroll
+            for (int o = L / 2; o > 0; o /= 2) s += __shfl_xor_sync(~0u, s, o);
+            if (lane == 0 && on) *y = from_f<V>(at >= 0 ? (s + v.z) * v.w : 0.0f);
+            y += p.Y.bs;
+        }
+        cp_async_wait<0>();
+        return;
+    }
 #pragma unroll 1
     for (int r = 0; r < rows; ++r) {
-        const int64_t n = n0 + r, slot = slots[r], at = (slot * p.D + d) * p.M + m;
+        const int64_t n = n0 + r, slot = slots[r];
         float h[E] = {}, vb[E], vc[E];
         if (shared_bc) {
             load_vec<float, E>(&bc[r][0][m], vb);
@@ -113,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_step_kernel(const ScanStepP
             cp_async_wait<AHEAD - 1>();
             if (m < p.M) load_vec<float, E>(reinterpret_cast<const float*>(&ring[r % AHEAD][threadIdx.x]), h);
         } else if (slot >= 0) {
-            load4(p.H + at, m, p.M, false, h);
+            load4(from + first[r], m, p.M, false, h);
         }
         float s = 0.0f;
 #pragma unroll
@@ -122,10 +157,10 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_step_kernel(const ScanStepP
             s = fmaf(vc[j], h[j], s);
         }
         if (vec) start(r + AHEAD);
-        if (on && m < p.M && slot >= 0) store_vec<float, E>(p.H_out + at, h, p.M - m < E ? p.M - m : E, vec);
+        if (on && m < p.M && slot >= 0) store_vec<float, E>(to + first[r], h, p.M - m < E ? p.M - m : E, vec);
 #pragma unroll
         for (int o = L / 2; o > 0; o /= 2) s += __shfl_xor_sync(~0u, s, o);
-        if (lane == 0 && on) static_cast<V*>(p.Y.data)[n * p.Y.bs + d] = from_f<V>(slot >= 0 ? (s + v.z) * v.w : 0.0f);
+        if (lane == 0 && on) y[r * p.Y.bs] = from_f<V>(slot >= 0 ? (s + v.z) * v.w : 0.0f);
     }
     if (vec) cp_async_wait<0>();
 }
