@@ -26,8 +26,8 @@
 // taking the larger of one and the other reversed, and sorting that.
 //
 // A logit is read once (once more by the gradient, which writes it once).  At 16
-// bits the SMs' issue slots bind before the bytes do: about 12 instructions a
-// logit (conversion, d, 2^d, two sums, the extremes), four fifths of the slots.
+// bits the SMs' issue slots bind before the bytes do: about 11 instructions a
+// logit (conversion, d, 2^d, two sums, the extremes), three quarters of the slots.
 // The rows above take 101 us (5.2 TB/s; a copy's rate is 6.8 TB/s), their gradient 180 us
 // (5.8 TB/s), and as many bytes of 32-bit logits, top 8, 108 us (4.8 TB/s).  Tried and
 // no faster: one, three or four 16-byte loads ahead instead of two, copies to a
