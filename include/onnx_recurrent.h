@@ -564,7 +564,8 @@ rnn_status rnn_ssm_scan_step(rnn_ssm_t plan, const rnn_ssm_scan_step_args* args)
 
 /* ----------------------------------------------------- token scores
  * Scores of rows of logits x[V] (one row per position; io type RNN_IO_*, rows
- * row_stride elements apart, 0: V): with lse = log sum_i exp(x_i),
+ * row_stride elements apart, 0: V, RNN_SHARED_ROW: every row is the one at
+ * `logits`): with lse = log sum_i exp(x_i),
  *   logp     = x[id] - lse           of the given token id,
  *   entropy  = -sum_i p_i log p_i    with p_i = exp(x_i - lse),
  *   top      the `top` (0 .. 32, at most V) largest logits' places, largest
@@ -576,6 +577,7 @@ rnn_status rnn_ssm_scan_step(rnn_ssm_t plan, const rnn_ssm_scan_step_args* args)
  * has NaN scores (a NaN ranks above +inf, +0 and -0 tie).
  * ids (with logp), logp, entropy, lse, top_ids and top_logp (with top > 0)
  * are each optional. */
+#define RNN_SHARED_ROW (-1)
 typedef struct {
     int64_t rows, vocab, row_stride, io;
     const void* logits;
@@ -595,7 +597,8 @@ rnn_status rnn_scores(const rnn_scores_args* args);
  * rnn_scores wrote (lse; entropy with d_entropy; top_ids with d_top):
  *   dlogits[i] = d_logp * (i == id) + sum_j d_top[j] * (i == top_ids[j])
  *              - (d_logp + sum_j d_top[j]) * p_i - d_entropy * p_i * (log p_i + entropy).
- * dlogits (io type, its own row stride, 0: V) may be the logits themselves. */
+ * dlogits (io type, its own row stride, 0: V) may be the logits themselves,
+ * unless these are one shared row. */
 typedef struct {
     int64_t rows, vocab, row_stride, io;
     const void* logits;

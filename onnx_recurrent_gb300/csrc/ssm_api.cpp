@@ -197,7 +197,7 @@ rnn_status check_scores(int64_t rows, int64_t vocab, int64_t stride, int64_t io,
     if (rows > 0x7fffff00LL || vocab > 0x7fffff00LL) return fail(RNN_ERR_UNSUPPORTED, "a size of 2^31 or more");
     if (io != RNN_IO_F32 && io != RNN_IO_F16 && io != RNN_IO_BF16)
         return fail(RNN_ERR_INVALID_ARGUMENT, "unknown io type %lld", (long long)io);
-    if (stride != 0 && stride < vocab)
+    if (stride != 0 && stride != RNN_SHARED_ROW && stride < vocab)
         return fail(RNN_ERR_INVALID_ARGUMENT, "row_stride %lld is below vocab %lld", (long long)stride, (long long)vocab);
     if (top < 0 || top > kMaxTop || top > vocab)
         return fail(RNN_ERR_INVALID_ARGUMENT, "top %lld outside [0, min(%d, vocab)]", (long long)top, kMaxTop);
@@ -207,6 +207,8 @@ rnn_status check_scores(int64_t rows, int64_t vocab, int64_t stride, int64_t io,
     }
     return RNN_OK;
 }
+
+int64_t logits_stride(int64_t stride, int64_t vocab) { return stride == RNN_SHARED_ROW ? 0 : stride ? stride : vocab; }
 
 ConvParams conv_params(const rnn_ssm* pl, int64_t S, int64_t N)
 {
@@ -571,7 +573,7 @@ rnn_status rnn_scores(const rnn_scores_args* a)
     ScoreParams p{};
     p.rows = a->rows;
     p.V = a->vocab;
-    p.stride = a->row_stride ? a->row_stride : a->vocab;
+    p.stride = logits_stride(a->row_stride, a->vocab);
     p.io = (int)a->io;
     p.top = (int)a->top;
     p.x = a->logits;
@@ -607,7 +609,7 @@ rnn_status rnn_scores_grad(const rnn_scores_grad_args* a)
     ScoreGradParams p{};
     p.rows = a->rows;
     p.V = a->vocab;
-    p.stride = a->row_stride ? a->row_stride : a->vocab;
+    p.stride = logits_stride(a->row_stride, a->vocab);
     p.d_stride = a->d_row_stride ? a->d_row_stride : a->vocab;
     p.io = (int)a->io;
     p.top = a->d_top ? (int)a->top : 0;

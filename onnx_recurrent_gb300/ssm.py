@@ -366,8 +366,12 @@ def rnn_ssm_scan_step(plan: SSM, X, dt, A, B, C, H, Y, D=None, Z=None, dt_bias=N
     _check(_load().rnn_ssm_scan_step(plan.handle, args))
 
 
+_SHARED_ROW = -1        # RNN_SHARED_ROW: every row is the same one
+
+
 def _logits(t, name, dtype=None, shape=None, device=None):
-    """(address, row stride) of a [rows, vocab] tensor with dense rows."""
+    """(address, row stride) of a [rows, vocab] tensor with dense rows; rows
+    that are all one row (an expanded tensor's) have no stride of their own."""
     if not t.is_cuda or (device is not None and t.device != device):
         raise TypeError(f"{name} must be a CUDA tensor on one device with the others")
     if t.dim() != 2 or (shape is not None and t.shape != shape) or (dtype is not None and t.dtype != dtype):
@@ -377,7 +381,7 @@ def _logits(t, name, dtype=None, shape=None, device=None):
     rows, vocab = t.shape
     if vocab > 1 and t.stride(1) != 1:
         raise ValueError(f"{name}: a row must be dense")
-    return t.data_ptr(), (t.stride(0) if rows > 1 else vocab)
+    return t.data_ptr(), (t.stride(0) or _SHARED_ROW) if rows > 1 else vocab
 
 
 def rnn_scores(logits, ids=None, top=0, logp=None, entropy=None, lse=None, top_ids=None, top_logp=None, stream=None):
@@ -409,11 +413,14 @@ def scores(logits, ids=None, top=0, stream=None) -> Scores:
 
 
 def rnn_scores_grad(logits, ids, result: Scores, d_logp=None, d_entropy=None, d_top=None, dlogits=None, stream=None):
-    """Gradient of the scores in the logits into dlogits (which may be logits); ``result`` is their Scores."""
+    """Gradient of the scores in the logits into dlogits (which may be logits of rows of their own); ``result`` is
+    their Scores."""
     lib = _load()
     at, stride = _logits(logits, "logits")
     rows, vocab = logits.shape
     d_at, d_stride = _logits(dlogits, "dlogits", logits.dtype, logits.shape, logits.device)
+    if d_stride == _SHARED_ROW:
+        raise ValueError("dlogits: rows must not share memory")
     dev, f32 = logits.get_device(), _f32
     top = 0 if d_top is None else d_top.shape[1]
     args = struct.pack(

@@ -1,0 +1,53 @@
+"""Which memory the state space operators and token scores use: tensors whose
+rows share memory, states updated in place, scratch kept by captured graphs,
+streams and devices that are not the current ones."""
+import pytest
+import torch
+
+import onnx_recurrent_gb300 as orc
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    orc.build()
+
+
+def _rand(seed):
+    g = torch.Generator().manual_seed(seed)
+    return lambda *s, scale=1.0: (torch.randn(*s, generator=g) * scale).cuda()
+
+
+# ------------------------------------------------- rows that share memory
+
+@pytest.mark.parametrize("rows,V,top,dtype", [(2, 1, 1, torch.float32), (5, 33, 4, torch.float32), (7, 9001, 20, torch.bfloat16),
+                                              (900, 300, 0, torch.float16)])
+def test_scores_of_one_row_for_several_tokens(rows, V, top, dtype):
+    """An expanded row of logits: the scores and gradients of as many copies of it, bit for bit (the copies start on
+    16-byte boundaries as the row does: the order of a row's sums goes by its alignment)."""
+    r = _rand(1)
+    row = (r(1, V) * 3).to(dtype)
+    ids = (torch.arange(rows, device="cuda", dtype=torch.int32) * 7) % V
+    d_logp, d_entropy = r(rows), r(rows)
+    d_top = r(rows, top) if top else None
+    one, copies = row.expand(rows, V), torch.zeros(rows, (V + 7) // 8 * 8, device="cuda", dtype=dtype)[:, :V]
+    copies.copy_(one)
+    assert one.stride(0) == 0
+    got, want = orc.scores(one, ids, top=top), orc.scores(copies, ids, top=top)
+    for a, b in zip(got, want):
+        assert (a is None and b is None) or torch.equal(a, b)
+    assert torch.equal(orc.scores_grad(one, ids, got, d_logp, d_entropy, d_top),
+                       orc.scores_grad(copies, ids, want, d_logp, d_entropy, d_top))
+
+
+def test_gradients_refuse_rows_that_share_memory():
+    x = torch.randn(1, 40, device="cuda")
+    ids = torch.zeros(3, dtype=torch.int32, device="cuda")
+    s = orc.scores(x.expand(3, 40), ids)
+    one = torch.ones(3, device="cuda")
+    for logits, out in ((x.expand(3, 40), x.expand(3, 40)), (x.repeat(3, 1), x.expand(3, 40))):
+        with pytest.raises(ValueError):
+            orc.rnn_scores_grad(logits, ids, s, one, dlogits=out)
+    with pytest.raises(orc.RNNError):      # rows that overlap in part
+        orc.scores(torch.zeros(100, device="cuda").as_strided((3, 40), (20, 1)), ids)
