@@ -415,7 +415,8 @@ rnn_status rnn_cell_run(rnn_plan_t plan, int64_t batch_size, const float* X, con
  * or the G x M values of B and C) is dense; the strides of a step and of a
  * batch row are in elements, so a view may be a part of a wider tensor.  Both
  * strides zero: dense, in the plan's layout (0: [seq, batch, ...], 1:
- * [batch, seq, ...]).  Output views must not overlap themselves or an input.
+ * [batch, seq, ...]).  Output views must not overlap an input, nor may their
+ * own steps or rows (the latter is refused).
  *
  * Calls are stream-ordered and asynchronous and allocate nothing but the
  * plan's scratch (grown with cudaMalloc when a call needs more, so make a

@@ -103,6 +103,21 @@ rnn_status check_views(const rnn_ssm* pl, const Named* views, int n)
     return RNN_OK;
 }
 
+// Output views: one whose steps or rows share memory would be written by blocks that run in any order.
+struct OutView {
+    View v;
+    int64_t inner;
+    const char* name;
+};
+template <int K>
+rnn_status check_outputs(int64_t S, int64_t N, const OutView (&views)[K])
+{
+    for (const OutView& o : views)
+        if (o.v.data && ((S > 1 && o.v.ss < o.inner) || (N > 1 && o.v.bs < o.inner) || (S > 1 && N > 1 && o.v.ss == o.v.bs)))
+            return fail(RNN_ERR_INVALID_ARGUMENT, "%s: its steps or rows share memory", o.name);
+    return RNN_OK;
+}
+
 struct NamedF32 {
     const void* p;
     const char* name;
@@ -316,14 +331,15 @@ rnn_status rnn_ssm_conv(rnn_ssm_t pl, const rnn_ssm_conv_args* a)
     if (rs != RNN_OK) return rs;
     NEED(a->W, "W");
     rs = check_arrays({{a->W, "W"}, {a->bias, "bias"}, {a->sequence_lens, "sequence_lens"}});
+    const View Y = dense(a->Y, pl, a->seq_length, a->batch_size, pl->D);
+    if (rs == RNN_OK) rs = check_outputs(a->seq_length, a->batch_size, {{Y, pl->D, "Y"}});
     if (rs == RNN_OK) rs = check_state(pl, a->initial_state, "initial_state");
     if (rs == RNN_OK) rs = check_state(pl, a->final_state, "final_state");
-    if (rs != RNN_OK) return rs;
-    rs = ensure_status(pl);
+    if (rs == RNN_OK) rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
     ConvParams p = conv_params(pl, a->seq_length, a->batch_size);
     p.X = dense(a->X, pl, p.S, p.N, p.D);
-    p.Y = dense(a->Y, pl, p.S, p.N, p.D);
+    p.Y = Y;
     p.W = a->W;
     p.bias = a->bias;
     p.lens = a->sequence_lens;
@@ -346,8 +362,9 @@ rnn_status rnn_ssm_conv_grad(rnn_ssm_t pl, const rnn_ssm_conv_grad_args* a)
     if (rs == RNN_OK) rs = check_state(pl, a->initial_state, "initial_state");
     if (rs == RNN_OK) rs = check_state(pl, a->d_final_state, "d_final_state");
     if (rs == RNN_OK) rs = check_state(pl, a->d_initial_state, "d_initial_state");
-    if (rs != RNN_OK) return rs;
-    rs = ensure_status(pl);
+    const View dX = dense(a->dX, pl, a->seq_length, a->batch_size, pl->D);
+    if (rs == RNN_OK) rs = check_outputs(a->seq_length, a->batch_size, {{dX, pl->D, "dX"}});
+    if (rs == RNN_OK) rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
     ConvGradParams p{};
     p.f = conv_params(pl, a->seq_length, a->batch_size);
@@ -357,7 +374,7 @@ rnn_status rnn_ssm_conv_grad(rnn_ssm_t pl, const rnn_ssm_conv_grad_args* a)
     p.f.lens = a->sequence_lens;
     p.f.h0 = a->initial_state;
     p.dY = dense(a->dY, pl, p.f.S, p.f.N, p.f.D);
-    p.dX = dense(a->dX, pl, p.f.S, p.f.N, p.f.D);
+    p.dX = dX;
     p.dhT = a->d_final_state;
     p.dh0 = a->d_initial_state;
     p.dW = a->dW;
@@ -390,6 +407,8 @@ rnn_status rnn_ssm_conv_step(rnn_ssm_t pl, const rnn_ssm_conv_step_args* a)
     if (rs == RNN_OK) rs = check_arrays({{a->W, "W"}, {a->bias, "bias"}, {a->slots, "slots"}});
     if (rs == RNN_OK) rs = check_state(pl, a->state, "state");
     if (rs == RNN_OK) rs = check_state(pl, a->state_out, "state_out");
+    const View Y = dense_row(a->Y, pl->D);
+    if (rs == RNN_OK) rs = check_outputs(1, a->batch_size, {{Y, pl->D, "Y"}});
     if (rs == RNN_OK) rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
     ConvStepParams p{};
@@ -400,7 +419,7 @@ rnn_status rnn_ssm_conv_step(rnn_ssm_t pl, const rnn_ssm_conv_step_args* a)
     p.io = pl->io;
     p.silu = pl->silu;
     p.X = dense_row(a->X, p.D);
-    p.Y = dense_row(a->Y, p.D);
+    p.Y = Y;
     p.W = a->W;
     p.bias = a->bias;
     p.state = a->state;
@@ -430,8 +449,9 @@ rnn_status rnn_ssm_scan(rnn_ssm_t pl, const rnn_ssm_scan_args* a)
     NEED(a->A, "A");
     rs = check_arrays({{a->A, "A"}, {a->Dskip, "Dskip"}, {a->dt_bias, "dt_bias"}, {a->sequence_lens, "sequence_lens"},
                        {a->initial_h, "initial_h"}, {a->Y_h, "Y_h"}, {a->saved, "saved"}});
-    if (rs != RNN_OK) return rs;
-    rs = ensure_status(pl);
+    const View Y = dense(a->Y, pl, a->seq_length, a->batch_size, pl->D);
+    if (rs == RNN_OK) rs = check_outputs(a->seq_length, a->batch_size, {{Y, pl->D, "Y"}});
+    if (rs == RNN_OK) rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
     ScanParams p = scan_params(pl, a->seq_length, a->batch_size);
     const int64_t gm = (int64_t)p.G * p.M;
@@ -440,7 +460,7 @@ rnn_status rnn_ssm_scan(rnn_ssm_t pl, const rnn_ssm_scan_args* a)
     p.B = dense(a->B, pl, p.S, p.N, gm);
     p.C = dense(a->C, pl, p.S, p.N, gm);
     p.Z = dense(a->Z, pl, p.S, p.N, p.D);
-    p.Y = dense(a->Y, pl, p.S, p.N, p.D);
+    p.Y = Y;
     p.A = a->A;
     p.Dskip = a->Dskip;
     p.dt_bias = a->dt_bias;
@@ -477,11 +497,17 @@ rnn_status rnn_ssm_scan_grad(rnn_ssm_t pl, const rnn_ssm_scan_grad_args* a)
                        {a->initial_h, "initial_h"}, {a->saved, "saved"}, {a->dY_h, "dY_h"}, {a->dA, "dA"}, {a->dDskip, "dDskip"},
                        {a->ddt_bias, "ddt_bias"}, {a->d_initial_h, "d_initial_h"}});
     if (rs != RNN_OK) return rs;
-    rs = ensure_status(pl);
-    if (rs != RNN_OK) return rs;
+    const int64_t S = a->seq_length, N = a->batch_size, D = pl->D, gm = (int64_t)pl->G * pl->M;
     ScanGradParams p{};
-    p.f = scan_params(pl, a->seq_length, a->batch_size);
-    const int64_t S = p.f.S, N = p.f.N, D = p.f.D, gm = (int64_t)p.f.G * p.f.M;
+    p.dX = dense(a->dX, pl, S, N, D);
+    p.ddt = dense(a->ddt, pl, S, N, D);
+    p.dB = dense(a->dB, pl, S, N, gm);
+    p.dC = dense(a->dC, pl, S, N, gm);
+    p.dZ = dense(a->dZ, pl, S, N, D);
+    rs = check_outputs(S, N, {{p.dX, D, "dX"}, {p.ddt, D, "ddt"}, {p.dB, gm, "dB"}, {p.dC, gm, "dC"}, {p.dZ, D, "dZ"}});
+    if (rs == RNN_OK) rs = ensure_status(pl);
+    if (rs != RNN_OK) return rs;
+    p.f = scan_params(pl, S, N);
     p.f.X = dense(a->X, pl, S, N, D);
     p.f.dt = dense(a->dt, pl, S, N, D);
     p.f.B = dense(a->B, pl, S, N, gm);
@@ -494,11 +520,6 @@ rnn_status rnn_ssm_scan_grad(rnn_ssm_t pl, const rnn_ssm_scan_grad_args* a)
     p.f.h0 = a->initial_h;
     p.f.saved = const_cast<float*>(a->saved);
     p.dY = dense(a->dY, pl, S, N, D);
-    p.dX = dense(a->dX, pl, S, N, D);
-    p.ddt = dense(a->ddt, pl, S, N, D);
-    p.dB = dense(a->dB, pl, S, N, gm);
-    p.dC = dense(a->dC, pl, S, N, gm);
-    p.dZ = dense(a->dZ, pl, S, N, D);
     p.dhT = a->dY_h;
     p.dA = a->dA;
     p.dDskip = a->dDskip;
@@ -531,6 +552,8 @@ rnn_status rnn_ssm_scan_step(rnn_ssm_t pl, const rnn_ssm_scan_step_args* a)
     rs = check_slots(a->slots, a->n_slots);
     if (rs == RNN_OK)
         rs = check_arrays({{a->A, "A"}, {a->Dskip, "Dskip"}, {a->dt_bias, "dt_bias"}, {a->H, "H"}, {a->H_out, "H_out"}, {a->slots, "slots"}});
+    const View Y = dense_row(a->Y, pl->D);
+    if (rs == RNN_OK) rs = check_outputs(1, a->batch_size, {{Y, pl->D, "Y"}});
     if (rs == RNN_OK) rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
     ScanStepParams p{};
@@ -547,7 +570,7 @@ rnn_status rnn_ssm_scan_step(rnn_ssm_t pl, const rnn_ssm_scan_step_args* a)
     p.B = dense_row(a->B, gm);
     p.C = dense_row(a->C, gm);
     p.Z = dense_row(a->Z, p.D);
-    p.Y = dense_row(a->Y, p.D);
+    p.Y = Y;
     p.A = a->A;
     p.Dskip = a->Dskip;
     p.dt_bias = a->dt_bias;

@@ -51,3 +51,23 @@ def test_gradients_refuse_rows_that_share_memory():
             orc.rnn_scores_grad(logits, ids, s, one, dlogits=out)
     with pytest.raises(orc.RNNError):      # rows that overlap in part
         orc.scores(torch.zeros(100, device="cuda").as_strided((3, 40), (20, 1)), ids)
+
+
+def test_outputs_refuse_steps_or_rows_that_share_memory():
+    N, S, D = 3, 4, 8
+    r = _rand(2)
+    plan = orc.rnn_ssm_create(D, state_size=4, layout=1)
+    X, W, one = r(N, S, D), r(D, 4), torch.zeros(1, S, D, device="cuda")
+    with pytest.raises(orc.RNNError) as e:
+        orc.rnn_ssm_conv(plan, X, W, Y=one.expand(N, S, D))
+    assert e.value.status == 1
+    with pytest.raises(orc.RNNError):
+        orc.rnn_ssm_conv_grad(plan, X, X, W, dX=one.expand(N, S, D))
+    with pytest.raises(orc.RNNError):
+        orc.rnn_ssm_conv(plan, X, W, Y=torch.zeros(N, 1, D, device="cuda").expand(N, S, D))
+    B = r(N, S, 1, 4)
+    with pytest.raises(orc.RNNError):
+        orc.rnn_ssm_scan(plan, X, X, -torch.ones(D, 4, device="cuda"), B, B, Y=one.expand(N, S, D))
+    # inputs may: a broadcast row gives what its copies give
+    x = r(1, S, D).expand(N, S, D)
+    assert torch.equal(orc.ssm_conv(plan, x, W)[0], orc.ssm_conv(plan, x.contiguous(), W)[0])

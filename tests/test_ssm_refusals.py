@@ -27,3 +27,39 @@ def test_gradients_of_a_shared_row_need_memory_of_their_own(lib):
     grad[14] = -1                                   # nor can the gradients be one row
     grad[13] = 8192
     assert _run(lib.rnn_scores_grad, grad) == 1 and "d_row_stride" in orc.rnn_last_error()
+
+
+def test_outputs_whose_steps_or_rows_share_memory(lib):
+    p = orc.rnn_ssm_create(8, state_size=4, conv_width=3, groups=2)
+    S, N, D, at = 5, 2, 8, 4096
+    bad = [(0, 64), (64, 0), (4, 64), (64, 4), (16, 16)]         # step and row strides
+    dense = (at, 0, 0)
+    for ss, bs in bad:
+        out = (at, ss, bs)
+        conv = [S, N, *dense, at, 0, 0, 0, *out, 0, 0]
+        conv_grad = [S, N, *dense, *dense, at, 0, 0, 0, 0, *out, 0, 0, 0, 0]
+        scan = [S, N, *dense, *dense, *dense, *dense, 0, 0, 0, at, 0, 0, 0, 0, *out, 0, 0, 0]
+        assert (len(conv), len(conv_grad), len(scan)) == (14, 20, 28)
+        for name, fields in (("conv", conv), ("conv_grad", conv_grad), ("scan", scan)):
+            assert _run(getattr(lib, "rnn_ssm_" + name), fields, p) == 1, (name, ss, bs)
+            assert "share memory" in orc.rnn_last_error()
+        for which in range(5):                       # dX, ddt, dB, dC, dZ
+            outs = [0] * 15
+            outs[3 * which:3 * which + 3] = out
+            fields = [S, N] + [*dense] * 6 + [at, 0, 0, 0, 0, at, 0] + outs + [0] * 5
+            assert len(fields) == 47 and _run(lib.rnn_ssm_scan_grad, fields, p) == 1, which
+            assert "share memory" in orc.rnn_last_error()
+    row = (at, 0, 4)
+    step = [N, 0, *dense, at, 0, at, at, 0, *row, 0]
+    assert _run(lib.rnn_ssm_conv_step, step, p) == 1 and "share memory" in orc.rnn_last_error()
+    step = [N, 0] + [*dense] * 4 + [0, 0, 0, at, 0, 0, at, at, 0, *row, 0]
+    assert len(step) == 27 and _run(lib.rnn_ssm_scan_step, step, p) == 1 and "share memory" in orc.rnn_last_error()
+
+
+def test_outputs_that_do_not_share_memory_pass_the_check(lib):
+    """Strides of a part of a wider tensor, either dimension first; a stride of a dimension of one value is not read.
+    (The next refusal shows that the check was passed.)"""
+    p = orc.rnn_ssm_create(8, state_size=4, conv_width=3)
+    for S, N, ss, bs in ((5, 2, 16, 8), (5, 2, 8, 40), (1, 2, 0, 8), (5, 1, 8, 0), (1, 1, 3, 3)):
+        conv = [S, N, 4096, 0, 0, 4096, 0, 0, 0, 4096, ss, bs, 2, 0]        # final_state not aligned
+        assert _run(lib.rnn_ssm_conv, conv, p) == 1 and "final_state" in orc.rnn_last_error()
