@@ -512,7 +512,8 @@ typedef struct {
     const int32_t* sequence_lens;  /* [N], or NULL */
     const float* initial_h;        /* [N, D, M], or NULL */
     rnn_view Y;                    /* out */
-    float* Y_h;                    /* out [N, D, M]: the state after each row's last step, or NULL */
+    float* Y_h;                    /* out [N, D, M]: the state after each row's last step, or NULL; may be
+                                      initial_h itself (an overlap in part is refused) */
     float* saved;                  /* out, rnn_ssm_saved_size floats for rnn_ssm_scan_grad, or NULL */
     void* stream;
 } rnn_ssm_scan_args;

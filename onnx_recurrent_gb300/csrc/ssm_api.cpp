@@ -130,6 +130,14 @@ rnn_status check_arrays(const NamedF32 (&arrays)[N])
         if ((uintptr_t)a.p % 4) return fail(RNN_ERR_INVALID_ARGUMENT, "%s is not aligned to its elements", a.name);
     return RNN_OK;
 }
+// A state and where it goes: the same memory, or memory apart.
+rnn_status check_in_place(const void* in, const void* out, size_t bytes, const char* names)
+{
+    const uintptr_t a = (uintptr_t)in, b = (uintptr_t)out;
+    if (in && out && a != b && (a < b ? b - a : a - b) < bytes)
+        return fail(RNN_ERR_INVALID_ARGUMENT, "%s overlap in part", names);
+    return RNN_OK;
+}
 // Arrays of the plan's io type.
 rnn_status check_state(const rnn_ssm* pl, const void* p, const char* name)
 {
@@ -451,6 +459,8 @@ rnn_status rnn_ssm_scan(rnn_ssm_t pl, const rnn_ssm_scan_args* a)
                        {a->initial_h, "initial_h"}, {a->Y_h, "Y_h"}, {a->saved, "saved"}});
     const View Y = dense(a->Y, pl, a->seq_length, a->batch_size, pl->D);
     if (rs == RNN_OK) rs = check_outputs(a->seq_length, a->batch_size, {{Y, pl->D, "Y"}});
+    const size_t states = sizeof(float) * (size_t)(a->batch_size * pl->D * pl->M);
+    if (rs == RNN_OK) rs = check_in_place(a->initial_h, a->Y_h, states, "initial_h and Y_h");
     if (rs == RNN_OK) rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
     ScanParams p = scan_params(pl, a->seq_length, a->batch_size);
@@ -472,12 +482,20 @@ rnn_status rnn_ssm_scan(rnn_ssm_t pl, const rnn_ssm_scan_args* a)
     size_t bytes = 0;
     cudaError_t e = ssm_scan_plan(p, &bytes);
     if (e != cudaSuccess) return cuda_fail(e, "reading the device's attributes");
-    rs = claim_scratch(pl, bytes, st);
+    // In place, the last chunk's block would write states that other chunks' blocks
+    // still read: they read a copy.  (Unsplit, the thread that writes a state has read it.)
+    const size_t copy = p.split.chunks > 1 && p.h0 && p.h0 == p.hT ? states : 0;
+    rs = claim_scratch(pl, bytes + copy, st);
     if (rs != RNN_OK) return rs;
     p.scratch = (float*)pl->scratch;
+    if (copy) {
+        e = cudaMemcpyAsync(pl->scratch + bytes, p.h0, copy, cudaMemcpyDeviceToDevice, st);
+        if (e != cudaSuccess) return cuda_fail(e, "copying initial_h");
+        p.h0 = (const float*)(pl->scratch + bytes);
+    }
     e = launch_ssm_scan(p, st, &pl->launches);
     if (e != cudaSuccess) return cuda_fail(e, "scan launch");
-    return release_scratch(pl, bytes, st);
+    return release_scratch(pl, bytes + copy, st);
 }
 
 rnn_status rnn_ssm_scan_grad(rnn_ssm_t pl, const rnn_ssm_scan_grad_args* a)

@@ -71,3 +71,31 @@ def test_outputs_refuse_steps_or_rows_that_share_memory():
     # inputs may: a broadcast row gives what its copies give
     x = r(1, S, D).expand(N, S, D)
     assert torch.equal(orc.ssm_conv(plan, x, W)[0], orc.ssm_conv(plan, x.contiguous(), W)[0])
+
+
+# --------------------------------------------------- states updated in place
+
+def _scan_inputs(N, S, D, M, G, seed, gate=True):
+    r = _rand(seed)
+    return dict(X=r(N, S, D), dt=r(N, S, D, scale=0.5), A=-torch.exp(r(D, M, scale=0.5)), B=r(N, S, G, M), C=r(N, S, G, M),
+                D=r(D), Z=r(N, S, D) if gate else None, dt_bias=r(D, scale=0.5) - 2.0), r(N, D, M)
+
+
+# unsplit, split with the blocks' own chain, split with the chain's launch: so many launches
+IN_PLACE = [((3, 9, 40, 16, 1), 1), ((1, 150, 136, 16, 1), 2), ((2, 300, 64, 16, 2), 3), ((2, 500, 40, 32, 1), 3)]
+
+
+@pytest.mark.parametrize("size,launches", IN_PLACE, ids=lambda v: str(v))
+@pytest.mark.parametrize("ragged", [False, True])
+def test_scan_updates_its_state_in_place(size, launches, ragged):
+    N, S, D, M, G = size
+    v, h0 = _scan_inputs(*size, seed=3)
+    lens = torch.tensor([S, 0, S // 2][:N], dtype=torch.int32, device="cuda") if ragged else None
+    plan = orc.rnn_ssm_create(D, state_size=M, groups=G, layout=1)
+    Y, Y_h, _ = orc.ssm_scan(plan, **v, sequence_lens=lens, initial_h=h0)
+    assert orc.rnn_ssm_last_launch_count(plan) == launches
+    for _ in range(3):
+        h, y = h0.clone(), torch.empty_like(Y)
+        orc.rnn_ssm_scan(plan, **v, sequence_lens=lens, initial_h=h, Y=y, Y_h=h)
+        assert torch.equal(y, Y) and torch.equal(h, Y_h)
+    orc.rnn_ssm_sync(plan)

@@ -63,3 +63,11 @@ def test_outputs_that_do_not_share_memory_pass_the_check(lib):
     for S, N, ss, bs in ((5, 2, 16, 8), (5, 2, 8, 40), (1, 2, 0, 8), (5, 1, 8, 0), (1, 1, 3, 3)):
         conv = [S, N, 4096, 0, 0, 4096, 0, 0, 0, 4096, ss, bs, 2, 0]        # final_state not aligned
         assert _run(lib.rnn_ssm_conv, conv, p) == 1 and "final_state" in orc.rnn_last_error()
+
+
+def test_states_that_overlap_in_part(lib):
+    p = orc.rnn_ssm_create(8, state_size=4, conv_width=3)
+    at, h, bytes_ = 4096, 1 << 20, 2 * 8 * 4 * 4
+    for other in (h + 4, h - 4, h + bytes_ - 4, h - bytes_ + 4):
+        scan = [5, 2] + [at, 0, 0] * 4 + [0, 0, 0, at, 0, 0, 0, h, at, 0, 0, other, 0, 0]
+        assert _run(lib.rnn_ssm_scan, scan, p) == 1 and "overlap" in orc.rnn_last_error()
