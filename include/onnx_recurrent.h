@@ -526,7 +526,8 @@ int64_t rnn_ssm_saved_size(rnn_ssm_t plan, int64_t seq_length, int64_t batch_siz
  * dX, ddt, dB, dC, dZ (views; dZ only with Z) and dA, dDskip, ddt_bias,
  * d_initial_h are overwritten; each may be NULL.  dB and dC sum over the
  * channels of a group, dA, dDskip and ddt_bias over steps and rows, all in a
- * fixed order: the same inputs give the same bits. */
+ * fixed order: the same inputs give the same bits.  d_initial_h may be dY_h
+ * itself (an overlap in part is refused). */
 typedef struct {
     int64_t seq_length, batch_size;
     rnn_view dY, X, dt, B, C, Z;

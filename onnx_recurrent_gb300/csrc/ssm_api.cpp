@@ -523,6 +523,8 @@ rnn_status rnn_ssm_scan_grad(rnn_ssm_t pl, const rnn_ssm_scan_grad_args* a)
     p.dC = dense(a->dC, pl, S, N, gm);
     p.dZ = dense(a->dZ, pl, S, N, D);
     rs = check_outputs(S, N, {{p.dX, D, "dX"}, {p.ddt, D, "ddt"}, {p.dB, gm, "dB"}, {p.dC, gm, "dC"}, {p.dZ, D, "dZ"}});
+    const size_t states = sizeof(float) * (size_t)(N * D * pl->M);
+    if (rs == RNN_OK) rs = check_in_place(a->dY_h, a->d_initial_h, states, "dY_h and d_initial_h");
     if (rs == RNN_OK) rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
     p.f = scan_params(pl, S, N);
@@ -547,12 +549,19 @@ rnn_status rnn_ssm_scan_grad(rnn_ssm_t pl, const rnn_ssm_scan_grad_args* a)
     size_t bytes = 0;
     cudaError_t e = ssm_scan_grad_plan(p, &bytes);
     if (e != cudaSuccess) return cuda_fail(e, "reading the device's attributes");
-    rs = claim_scratch(pl, bytes, st);
+    // in place, as in the forward run: the first chunk's block would write what the others read
+    const size_t copy = p.f.split.chunks > 1 && p.dhT && p.dhT == p.dh0 ? states : 0;
+    rs = claim_scratch(pl, bytes + copy, st);
     if (rs != RNN_OK) return rs;
     p.f.scratch = (float*)pl->scratch;
+    if (copy) {
+        e = cudaMemcpyAsync(pl->scratch + bytes, p.dhT, copy, cudaMemcpyDeviceToDevice, st);
+        if (e != cudaSuccess) return cuda_fail(e, "copying dY_h");
+        p.dhT = (const float*)(pl->scratch + bytes);
+    }
     e = launch_ssm_scan_grad(p, st, &pl->launches);
     if (e != cudaSuccess) return cuda_fail(e, "scan gradient launch");
-    return release_scratch(pl, bytes, st);
+    return release_scratch(pl, bytes + copy, st);
 }
 
 rnn_status rnn_ssm_scan_step(rnn_ssm_t pl, const rnn_ssm_scan_step_args* a)

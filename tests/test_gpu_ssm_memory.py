@@ -99,3 +99,28 @@ def test_scan_updates_its_state_in_place(size, launches, ragged):
         orc.rnn_ssm_scan(plan, **v, sequence_lens=lens, initial_h=h, Y=y, Y_h=h)
         assert torch.equal(y, Y) and torch.equal(h, Y_h)
     orc.rnn_ssm_sync(plan)
+
+
+# launches of the gradient: as above, and one that adds up the sums
+GRAD_IN_PLACE = [((3, 9, 40, 16, 1), 2), ((1, 100, 136, 16, 1), 3), ((2, 300, 64, 16, 2), 4), ((2, 500, 40, 32, 1), 4)]
+
+
+@pytest.mark.parametrize("size,launches", GRAD_IN_PLACE, ids=lambda v: str(v))
+@pytest.mark.parametrize("ragged", [False, True])
+def test_scan_gradient_updates_its_states_slope_in_place(size, launches, ragged):
+    N, S, D, M, G = size
+    v, h0 = _scan_inputs(*size, seed=4)
+    r = _rand(5)
+    dY, dY_h = r(N, S, D), r(N, D, M)
+    lens = torch.tensor([S, 0, S // 2][:N], dtype=torch.int32, device="cuda") if ragged else None
+    plan = orc.rnn_ssm_create(D, state_size=M, groups=G, layout=1)
+    _, _, saved = orc.ssm_scan(plan, **v, sequence_lens=lens, initial_h=h0, save=True)
+    want = orc.ssm_scan_grad(plan, dY, saved, **v, sequence_lens=lens, initial_h=h0, dY_h=dY_h)
+    assert orc.rnn_ssm_last_launch_count(plan) == launches
+    for _ in range(3):
+        d = dY_h.clone()
+        out = {k: d if k == "d_initial_h" else torch.empty_like(t) for k, t in want.items()}
+        orc.rnn_ssm_scan_grad(plan, dY, saved, **v, sequence_lens=lens, initial_h=h0, dY_h=d, **out)
+        for k in want:
+            assert torch.equal(out[k], want[k]), k
+    orc.rnn_ssm_sync(plan)
