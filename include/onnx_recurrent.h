@@ -467,7 +467,8 @@ rnn_status rnn_ssm_conv(rnn_ssm_t plan, const rnn_ssm_conv_args* args);
 /* Gradients of the convolution: dY (required) and d_final_state (or NULL) are
  * the loss's slopes in the outputs; dX, dW, dbias and d_initial_state (each
  * may be NULL, dX by its data) are overwritten.  Sums over steps and rows are taken in a
- * fixed order: the same inputs give the same bits. */
+ * fixed order: the same inputs give the same bits.  d_initial_state may be
+ * d_final_state itself (an overlap in part is refused). */
 typedef struct {
     int64_t seq_length, batch_size;
     rnn_view dY, X;

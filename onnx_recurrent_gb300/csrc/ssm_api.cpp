@@ -372,6 +372,8 @@ rnn_status rnn_ssm_conv_grad(rnn_ssm_t pl, const rnn_ssm_conv_grad_args* a)
     if (rs == RNN_OK) rs = check_state(pl, a->d_initial_state, "d_initial_state");
     const View dX = dense(a->dX, pl, a->seq_length, a->batch_size, pl->D);
     if (rs == RNN_OK) rs = check_outputs(a->seq_length, a->batch_size, {{dX, pl->D, "dX"}});
+    const size_t states = element(pl->io) * (size_t)(a->batch_size * (pl->K - 1) * pl->D);
+    if (rs == RNN_OK) rs = check_in_place(a->d_final_state, a->d_initial_state, states, "d_final_state and d_initial_state");
     if (rs == RNN_OK) rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
     ConvGradParams p{};
@@ -390,12 +392,21 @@ rnn_status rnn_ssm_conv_grad(rnn_ssm_t pl, const rnn_ssm_conv_grad_args* a)
     cudaStream_t st = (cudaStream_t)a->stream;
     p.parts = ssm_conv_grad_parts(p);
     const size_t bytes = a->dW || a->dbias ? sizeof(float) * (size_t)p.parts * (size_t)(p.f.D * (p.f.K + 1)) : 0;
-    rs = claim_scratch(pl, bytes, st);
+    // In place, the blocks of a row's first steps would write what those of its last
+    // steps still read: they read a copy, on a 16-byte boundary as the slopes may be.
+    const size_t copy = p.dhT && p.dhT == p.dh0 ? states : 0, at = (bytes + 15) / 16 * 16;
+    rs = claim_scratch(pl, copy ? at + copy : bytes, st);
     if (rs != RNN_OK) return rs;
     p.part = bytes ? (float*)pl->scratch : nullptr;
-    cudaError_t e = launch_ssm_conv_grad(p, st, &pl->launches);
+    cudaError_t e = cudaSuccess;
+    if (copy) {
+        e = cudaMemcpyAsync(pl->scratch + at, p.dhT, copy, cudaMemcpyDeviceToDevice, st);
+        if (e != cudaSuccess) return cuda_fail(e, "copying d_final_state");
+        p.dhT = pl->scratch + at;
+    }
+    e = launch_ssm_conv_grad(p, st, &pl->launches);
     if (e != cudaSuccess) return cuda_fail(e, "convolution gradient launch");
-    return release_scratch(pl, bytes, st);
+    return release_scratch(pl, bytes + copy, st);
 }
 
 rnn_status rnn_ssm_conv_step(rnn_ssm_t pl, const rnn_ssm_conv_step_args* a)

@@ -124,3 +124,22 @@ def test_scan_gradient_updates_its_states_slope_in_place(size, launches, ragged)
         for k in want:
             assert torch.equal(out[k], want[k]), k
     orc.rnn_ssm_sync(plan)
+
+
+@pytest.mark.parametrize("N,S,D,K,io", [(3, 1, 40, 4, "f32"), (3, 2, 33, 8, "bf16"), (4, 300, 72, 4, "f16"), (2, 40, 8, 1, "f32")])
+def test_convolution_gradient_updates_its_states_slope_in_place(N, S, D, K, io):
+    """Runs shorter than the taps, where the first state takes slopes of the last one, and runs of several blocks."""
+    r, t = _rand(6), {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[io]
+    plan = orc.rnn_ssm_create(D, conv_width=K, layout=1)
+    orc.rnn_ssm_set_io_type(plan, io)
+    X, dY, W, b = r(N, S, D).to(t), r(N, S, D).to(t), r(D, K), r(D)
+    h0, d_state = r(N, K - 1, D).to(t), r(N, K - 1, D).to(t)
+    lens = torch.tensor([S, 0, max(S - 1, 0), S // 2][:N], dtype=torch.int32, device="cuda")
+    want = orc.ssm_conv_grad(plan, dY, X, W, b, lens, h0, d_state)
+    for with_weights in (True, False):
+        d = d_state.clone()
+        dX, dW, db = torch.empty_like(X), torch.empty_like(W), torch.empty_like(b)
+        orc.rnn_ssm_conv_grad(plan, dY, X, W, b, lens, h0, d, dX, dW if with_weights else None, db if with_weights else None, d)
+        assert torch.equal(dX, want["dX"]) and torch.equal(d, want["d_initial_state"])
+        assert not with_weights or (torch.equal(dW, want["dW"]) and torch.equal(db, want["dbias"]))
+    orc.rnn_ssm_sync(plan)

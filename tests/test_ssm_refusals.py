@@ -79,3 +79,11 @@ def test_slopes_of_the_scans_states_that_overlap_in_part(lib):
     for other in (h + 4, h - 4, h + bytes_ - 4, h - bytes_ + 4):
         grad = [5, 2] + [at, 0, 0] * 6 + [at, 0, 0, 0, 0, at, h] + [0] * 15 + [0, 0, 0, other, 0]
         assert len(grad) == 47 and _run(lib.rnn_ssm_scan_grad, grad, p) == 1 and "overlap" in orc.rnn_last_error()
+
+
+def test_slopes_of_the_convolutions_states_that_overlap_in_part(lib):
+    p = orc.rnn_ssm_create(8, state_size=4, conv_width=3)
+    at, h, bytes_ = 4096, 1 << 20, 2 * 2 * 8 * 4
+    for other in (h + 4, h - 4, h + bytes_ - 4, h - bytes_ + 4):
+        grad = [5, 2, at, 0, 0, at, 0, 0, at, 0, 0, 0, h, 0, 0, 0, 0, 0, other, 0]
+        assert len(grad) == 20 and _run(lib.rnn_ssm_conv_grad, grad, p) == 1 and "overlap" in orc.rnn_last_error()
