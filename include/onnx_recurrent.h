@@ -459,7 +459,8 @@ typedef struct {
     const int32_t* sequence_lens;  /* [N], or NULL */
     const void* initial_state;     /* [N, K-1, D] oldest first, io type, or NULL */
     rnn_view Y;                    /* out */
-    void* final_state;             /* out [N, K-1, D]: the last K-1 inputs of each row, or NULL */
+    void* final_state;             /* out [N, K-1, D]: the last K-1 inputs of each row, or NULL; may be
+                                      initial_state itself (an overlap in part is refused) */
     void* stream;
 } rnn_ssm_conv_args;
 rnn_status rnn_ssm_conv(rnn_ssm_t plan, const rnn_ssm_conv_args* args);
@@ -488,7 +489,7 @@ rnn_status rnn_ssm_conv_grad(rnn_ssm_t plan, const rnn_ssm_conv_grad_args* args)
 /* One token of each row: X and Y [N, D] (rows a batch_stride apart, 0: dense;
  * seq_stride is not used).  Row n's state is state[slots[n]] ([slots, K-1, D];
  * without slots state[n]); the new one goes to the same slot of state_out,
- * which may be state itself.  A row of slot -1 is padding: its Y is zero and
+ * which may be state itself (an overlap in part is refused).  A row of slot -1 is padding: its Y is zero and
  * no state is touched.  Slots of one call must differ from one another (two
  * rows on one slot race). */
 typedef struct {

@@ -343,6 +343,9 @@ rnn_status rnn_ssm_conv(rnn_ssm_t pl, const rnn_ssm_conv_args* a)
     if (rs == RNN_OK) rs = check_outputs(a->seq_length, a->batch_size, {{Y, pl->D, "Y"}});
     if (rs == RNN_OK) rs = check_state(pl, a->initial_state, "initial_state");
     if (rs == RNN_OK) rs = check_state(pl, a->final_state, "final_state");
+    // the same memory needs no copy: a row's first run alone reads it, and its threads have read a value before they write it
+    const size_t states = element(pl->io) * (size_t)(a->batch_size * (pl->K - 1) * pl->D);
+    if (rs == RNN_OK) rs = check_in_place(a->initial_state, a->final_state, states, "initial_state and final_state");
     if (rs == RNN_OK) rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
     ConvParams p = conv_params(pl, a->seq_length, a->batch_size);
@@ -426,6 +429,8 @@ rnn_status rnn_ssm_conv_step(rnn_ssm_t pl, const rnn_ssm_conv_step_args* a)
     if (rs == RNN_OK) rs = check_arrays({{a->W, "W"}, {a->bias, "bias"}, {a->slots, "slots"}});
     if (rs == RNN_OK) rs = check_state(pl, a->state, "state");
     if (rs == RNN_OK) rs = check_state(pl, a->state_out, "state_out");
+    const size_t states = element(pl->io) * (size_t)((a->slots ? a->n_slots : a->batch_size) * (pl->K - 1) * pl->D);
+    if (rs == RNN_OK) rs = check_in_place(a->state, a->state_out, states, "state and state_out");
     const View Y = dense_row(a->Y, pl->D);
     if (rs == RNN_OK) rs = check_outputs(1, a->batch_size, {{Y, pl->D, "Y"}});
     if (rs == RNN_OK) rs = ensure_status(pl);
@@ -590,6 +595,8 @@ rnn_status rnn_ssm_scan_step(rnn_ssm_t pl, const rnn_ssm_scan_step_args* a)
     rs = check_slots(a->slots, a->n_slots);
     if (rs == RNN_OK)
         rs = check_arrays({{a->A, "A"}, {a->Dskip, "Dskip"}, {a->dt_bias, "dt_bias"}, {a->H, "H"}, {a->H_out, "H_out"}, {a->slots, "slots"}});
+    const size_t states = sizeof(float) * (size_t)((a->slots ? a->n_slots : a->batch_size) * pl->D * pl->M);
+    if (rs == RNN_OK) rs = check_in_place(a->H, a->H_out, states, "H and H_out");
     const View Y = dense_row(a->Y, pl->D);
     if (rs == RNN_OK) rs = check_outputs(1, a->batch_size, {{Y, pl->D, "Y"}});
     if (rs == RNN_OK) rs = ensure_status(pl);

@@ -143,3 +143,16 @@ def test_convolution_gradient_updates_its_states_slope_in_place(N, S, D, K, io):
         assert torch.equal(dX, want["dX"]) and torch.equal(d, want["d_initial_state"])
         assert not with_weights or (torch.equal(dW, want["dW"]) and torch.equal(db, want["dbias"]))
     orc.rnn_ssm_sync(plan)
+
+
+@pytest.mark.parametrize("N,S,D,K,io", [(3, 1, 40, 4, "f32"), (3, 2, 33, 8, "bf16"), (4, 300, 72, 4, "f16"), (3, 0, 8, 5, "f32")])
+def test_convolution_updates_its_state_in_place(N, S, D, K, io):
+    r, t = _rand(7), {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[io]
+    plan = orc.rnn_ssm_create(D, conv_width=K, layout=1)
+    orc.rnn_ssm_set_io_type(plan, io)
+    X, W, h0 = r(N, S, D).to(t), r(D, K), r(N, K - 1, D).to(t)
+    lens = torch.tensor([S, 0, max(S - 1, 0), S // 2][:N], dtype=torch.int32, device="cuda")
+    Y, state = orc.ssm_conv(plan, X, W, None, lens, h0)
+    y = torch.empty_like(Y)
+    orc.rnn_ssm_conv(plan, X, W, None, lens, h0, y, h0)
+    assert torch.equal(y, Y) and torch.equal(h0, state)

@@ -87,3 +87,20 @@ def test_slopes_of_the_convolutions_states_that_overlap_in_part(lib):
     for other in (h + 4, h - 4, h + bytes_ - 4, h - bytes_ + 4):
         grad = [5, 2, at, 0, 0, at, 0, 0, at, 0, 0, 0, h, 0, 0, 0, 0, 0, other, 0]
         assert len(grad) == 20 and _run(lib.rnn_ssm_conv_grad, grad, p) == 1 and "overlap" in orc.rnn_last_error()
+
+
+def test_the_convolutions_and_single_tokens_states_that_overlap_in_part(lib):
+    p = orc.rnn_ssm_create(8, state_size=4, conv_width=3)
+    at, h = 4096, 1 << 20
+    for slots, n in ((0, 2), (at, 7)):
+        for step, size in (("conv", 2 * 8 * 4), ("scan", 8 * 4 * 4)):
+            for other in (h + 4, h - 4, h + n * size - 4, h - n * size + 4):
+                if step == "conv":
+                    fields = [2, n, at, 0, 0, at, 0, h, other, slots, at, 0, 0, 0]
+                else:
+                    fields = [2, n] + [at, 0, 0] * 4 + [0, 0, 0, at, 0, 0, h, other, slots, at, 0, 0, 0]
+                assert _run(getattr(lib, f"rnn_ssm_{step}_step"), fields, p) == 1, (step, other)
+                assert "overlap" in orc.rnn_last_error()
+    for other in (h + 4, h - 4, h + 124, h - 124):
+        conv = [5, 2, at, 0, 0, at, 0, 0, h, at, 0, 0, other, 0]
+        assert _run(lib.rnn_ssm_conv, conv, p) == 1 and "overlap" in orc.rnn_last_error()
