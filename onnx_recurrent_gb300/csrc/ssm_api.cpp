@@ -42,6 +42,17 @@ rnn_status cuda_fail(cudaError_t e, const char* what)
     return fail(e == cudaErrorMemoryAllocation ? RNN_ERR_OOM : RNN_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// Lets this thread allocate and free while a stream is being captured, which
+// would otherwise spoil the capture.
+struct AmidCapture {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    const cudaError_t status = cudaThreadExchangeStreamCaptureMode(&mode);
+    ~AmidCapture()
+    {
+        if (status == cudaSuccess) cudaThreadExchangeStreamCaptureMode(&mode);
+    }
+};
+
 size_t element(int io) { return io == RNN_IO_F32 ? 4 : 2; }
 
 // A caller's view; both strides 0 stand for a dense tensor in the plan's
@@ -295,6 +306,8 @@ rnn_status rnn_ssm_create(rnn_ssm_t* out, int64_t channels, int64_t state_size, 
 void rnn_ssm_destroy(rnn_ssm_t pl)
 {
     if (!pl) return;
+    // a plan may be collected at any time, amid another's capture too
+    AmidCapture amid;
     if (pl->scratch) cudaFree(pl->scratch);   // synchronises with outstanding work
     if (pl->status) cudaFree(pl->status);
     if (pl->used) cudaEventDestroy(pl->used);

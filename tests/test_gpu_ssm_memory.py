@@ -1,6 +1,8 @@
 """Which memory the state space operators and token scores use: tensors whose
 rows share memory, states updated in place, scratch kept by captured graphs,
 streams and devices that are not the current ones."""
+import gc
+
 import pytest
 import torch
 
@@ -156,3 +158,25 @@ def test_convolution_updates_its_state_in_place(N, S, D, K, io):
     y = torch.empty_like(Y)
     orc.rnn_ssm_conv(plan, X, W, None, lens, h0, y, h0)
     assert torch.equal(y, Y) and torch.equal(h0, state)
+
+
+# ------------------------------------------------------- captured calls
+
+def test_a_plan_that_goes_amid_a_capture():
+    """As the garbage collector may have it: the capture goes on, and its graph replays."""
+    size = (1, 150, 136, 16, 1)
+    v, h0 = _scan_inputs(*size, seed=8)
+    N, S, D, M, G = size
+    old = orc.rnn_ssm_create(D, state_size=M, groups=G, layout=1)
+    orc.ssm_scan(old, **v, initial_h=h0)             # takes scratch, a status word and an event
+    plan, W = orc.rnn_ssm_create(D, layout=1), torch.ones(D, 4, device="cuda")
+    want, _ = orc.ssm_conv(plan, v["X"], W)
+    gc.collect()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        orc.rnn_ssm_destroy(old)
+        Y, _ = orc.ssm_conv(plan, v["X"], W)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(Y, want)
