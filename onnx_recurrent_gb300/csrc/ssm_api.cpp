@@ -11,6 +11,13 @@
 
 using namespace rnngb;
 
+namespace {
+struct Kept {
+    char* data;
+    Kept* next;
+};
+}  // namespace
+
 struct rnn_ssm {
     int64_t D = 0;
     int M = 0, G = 0, K = 0, layout = 0, silu = 0, softplus = 0, io = RNN_IO_F32;
@@ -21,6 +28,9 @@ struct rnn_ssm {
     bool pending = false;         // if there is one,
     unsigned long long user = 0;  // on the stream of this id
     bool capturing = false;       // the call at hand is being captured
+    char* graph_scratch = nullptr;   // the scratch of captured calls
+    size_t graph_bytes = 0;
+    Kept* kept = nullptr;         // it and what it grew from: graphs hold their addresses
     int launches = 0;
 };
 
@@ -172,10 +182,44 @@ rnn_status ensure_status(rnn_ssm* pl)
     return RNN_OK;
 }
 
-// The plan's scratch of at least `bytes`, after the previous call's use of it.
-rnn_status claim_scratch(rnn_ssm* pl, size_t bytes, cudaStream_t st)
+// Scratch of at least `bytes` for a call that is being captured.  A graph keeps
+// the address and runs at times that no event of this plan knows, so it is not the
+// plain calls' scratch, and not freed before the plan.
+rnn_status claim_graph_scratch(rnn_ssm* pl, size_t bytes)
 {
+    if (bytes <= pl->graph_bytes) return RNN_OK;
+    Kept* k = new (std::nothrow) Kept;
+    if (!k) return fail(RNN_ERR_OOM, "host allocation failed");
+    cudaError_t e;
+    {
+        AmidCapture amid;
+        e = amid.status == cudaSuccess ? cudaMalloc((void**)&k->data, bytes) : amid.status;
+    }
+    if (e != cudaSuccess) {
+        delete k;
+        return cuda_fail(e, "cudaMalloc(scratch of captured calls)");
+    }
+    k->next = pl->kept;
+    pl->kept = k;
+    pl->graph_scratch = k->data;
+    pl->graph_bytes = bytes;
+    return RNN_OK;
+}
+
+// The plan's scratch of at least `bytes`, after the previous call's use of it.
+rnn_status claim_scratch(rnn_ssm* pl, size_t bytes, cudaStream_t st, char** scratch)
+{
+    *scratch = nullptr;
     if (!bytes) return RNN_OK;
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(st, &cs);
+    if (e != cudaSuccess) return cuda_fail(e, "asking whether the stream is being captured");
+    pl->capturing = cs != cudaStreamCaptureStatusNone;
+    if (pl->capturing) {
+        rnn_status rs = claim_graph_scratch(pl, bytes);
+        *scratch = pl->graph_scratch;
+        return rs;
+    }
     if (bytes > pl->scratch_bytes) {
         if (pl->scratch) {
             cudaFree(pl->scratch);   // synchronises with outstanding work
@@ -183,7 +227,7 @@ rnn_status claim_scratch(rnn_ssm* pl, size_t bytes, cudaStream_t st)
             pl->scratch_bytes = 0;
             pl->pending = false;
         }
-        cudaError_t e = cudaMalloc((void**)&pl->scratch, bytes);
+        e = cudaMalloc((void**)&pl->scratch, bytes);
         if (e != cudaSuccess) {
             pl->scratch = nullptr;
             return cuda_fail(e, "cudaMalloc(scratch)");
@@ -191,22 +235,17 @@ rnn_status claim_scratch(rnn_ssm* pl, size_t bytes, cudaStream_t st)
         pl->scratch_bytes = bytes;
     }
     if (!pl->used) {
-        cudaError_t e = cudaEventCreateWithFlags(&pl->used, cudaEventDisableTiming);
+        e = cudaEventCreateWithFlags(&pl->used, cudaEventDisableTiming);
         if (e != cudaSuccess) {
             pl->used = nullptr;
             return cuda_fail(e, "cudaEventCreate");
         }
     }
-    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
     unsigned long long id = 0;
-    cudaError_t e = cudaStreamIsCapturing(st, &cs);
-    pl->capturing = cs != cudaStreamCaptureStatusNone;
-    // an event recorded outside a capture cannot be waited on inside one
-    if (e == cudaSuccess && !pl->capturing) {
-        e = cudaStreamGetId(st, &id);
-        if (e == cudaSuccess && pl->pending && id != pl->user) e = cudaStreamWaitEvent(st, pl->used, 0);
-        pl->user = id;
-    }
+    e = cudaStreamGetId(st, &id);
+    if (e == cudaSuccess && pl->pending && id != pl->user) e = cudaStreamWaitEvent(st, pl->used, 0);
+    pl->user = id;
+    *scratch = pl->scratch;
     return e == cudaSuccess ? RNN_OK : cuda_fail(e, "ordering the scratch");
 }
 
@@ -309,6 +348,11 @@ void rnn_ssm_destroy(rnn_ssm_t pl)
     // a plan may be collected at any time, amid another's capture too
     AmidCapture amid;
     if (pl->scratch) cudaFree(pl->scratch);   // synchronises with outstanding work
+    while (Kept* k = pl->kept) {
+        pl->kept = k->next;
+        cudaFree(k->data);
+        delete k;
+    }
     if (pl->status) cudaFree(pl->status);
     if (pl->used) cudaEventDestroy(pl->used);
     delete pl;
@@ -411,14 +455,15 @@ rnn_status rnn_ssm_conv_grad(rnn_ssm_t pl, const rnn_ssm_conv_grad_args* a)
     // In place, the blocks of a row's first steps would write what those of its last
     // steps still read: they read a copy, on a 16-byte boundary as the slopes may be.
     const size_t copy = p.dhT && p.dhT == p.dh0 ? states : 0, at = (bytes + 15) / 16 * 16;
-    rs = claim_scratch(pl, copy ? at + copy : bytes, st);
+    char* scratch = nullptr;
+    rs = claim_scratch(pl, copy ? at + copy : bytes, st, &scratch);
     if (rs != RNN_OK) return rs;
-    p.part = bytes ? (float*)pl->scratch : nullptr;
+    p.part = bytes ? (float*)scratch : nullptr;
     cudaError_t e = cudaSuccess;
     if (copy) {
-        e = cudaMemcpyAsync(pl->scratch + at, p.dhT, copy, cudaMemcpyDeviceToDevice, st);
+        e = cudaMemcpyAsync(scratch + at, p.dhT, copy, cudaMemcpyDeviceToDevice, st);
         if (e != cudaSuccess) return cuda_fail(e, "copying d_final_state");
-        p.dhT = pl->scratch + at;
+        p.dhT = scratch + at;
     }
     e = launch_ssm_conv_grad(p, st, &pl->launches);
     if (e != cudaSuccess) return cuda_fail(e, "convolution gradient launch");
@@ -514,13 +559,14 @@ rnn_status rnn_ssm_scan(rnn_ssm_t pl, const rnn_ssm_scan_args* a)
     // In place, the last chunk's block would write states that other chunks' blocks
     // still read: they read a copy.  (Unsplit, the thread that writes a state has read it.)
     const size_t copy = p.split.chunks > 1 && p.h0 && p.h0 == p.hT ? states : 0;
-    rs = claim_scratch(pl, bytes + copy, st);
+    char* scratch = nullptr;
+    rs = claim_scratch(pl, bytes + copy, st, &scratch);
     if (rs != RNN_OK) return rs;
-    p.scratch = (float*)pl->scratch;
+    p.scratch = (float*)scratch;
     if (copy) {
-        e = cudaMemcpyAsync(pl->scratch + bytes, p.h0, copy, cudaMemcpyDeviceToDevice, st);
+        e = cudaMemcpyAsync(scratch + bytes, p.h0, copy, cudaMemcpyDeviceToDevice, st);
         if (e != cudaSuccess) return cuda_fail(e, "copying initial_h");
-        p.h0 = (const float*)(pl->scratch + bytes);
+        p.h0 = (const float*)(scratch + bytes);
     }
     e = launch_ssm_scan(p, st, &pl->launches);
     if (e != cudaSuccess) return cuda_fail(e, "scan launch");
@@ -580,13 +626,14 @@ rnn_status rnn_ssm_scan_grad(rnn_ssm_t pl, const rnn_ssm_scan_grad_args* a)
     if (e != cudaSuccess) return cuda_fail(e, "reading the device's attributes");
     // in place, as in the forward run: the first chunk's block would write what the others read
     const size_t copy = p.f.split.chunks > 1 && p.dhT && p.dhT == p.dh0 ? states : 0;
-    rs = claim_scratch(pl, bytes + copy, st);
+    char* scratch = nullptr;
+    rs = claim_scratch(pl, bytes + copy, st, &scratch);
     if (rs != RNN_OK) return rs;
-    p.f.scratch = (float*)pl->scratch;
+    p.f.scratch = (float*)scratch;
     if (copy) {
-        e = cudaMemcpyAsync(pl->scratch + bytes, p.dhT, copy, cudaMemcpyDeviceToDevice, st);
+        e = cudaMemcpyAsync(scratch + bytes, p.dhT, copy, cudaMemcpyDeviceToDevice, st);
         if (e != cudaSuccess) return cuda_fail(e, "copying dY_h");
-        p.dhT = (const float*)(pl->scratch + bytes);
+        p.dhT = (const float*)(scratch + bytes);
     }
     e = launch_ssm_scan_grad(p, st, &pl->launches);
     if (e != cudaSuccess) return cuda_fail(e, "scan gradient launch");

@@ -180,3 +180,67 @@ def test_a_plan_that_goes_amid_a_capture():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(Y, want)
+
+
+def test_a_graph_outlives_the_scratch_of_later_calls():
+    """A split scan, its gradient and a convolution's captured, then plain calls that need much more scratch, then
+    replays: the graph's outputs are those of plain calls on its inputs."""
+    size = (1, 150, 136, 16, 1)
+    N, S, D, M, G = size
+    v, h0 = _scan_inputs(*size, seed=8)
+    r = _rand(9)
+    dY, dY_h, W, b = r(N, S, D), r(N, D, M), r(D, 4), r(D)
+    plan = orc.rnn_ssm_create(D, state_size=M, groups=G, layout=1)
+
+    def calls():
+        Y, Y_h, saved = orc.ssm_scan(plan, **v, initial_h=h0, save=True)
+        g = orc.ssm_scan_grad(plan, dY, saved, **v, initial_h=h0, dY_h=dY_h)
+        c = orc.ssm_conv_grad(plan, dY, v["X"], W, b)
+        return [Y, Y_h, *g.values(), *c.values()]
+    orc.rnn_ssm_conv(plan, v["X"], W, Y=torch.empty_like(v["X"]))          # the plan's first call: no scratch
+    gc.collect()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = calls()
+    want = [t.clone() for t in calls()]
+    big, H0 = _scan_inputs(4, 1500, D, M, G, seed=10)
+    for _ in range(3):
+        for t in outs:
+            t.fill_(float("nan"))
+        graph.replay()
+        Y, _, saved = orc.ssm_scan(plan, **big, initial_h=H0, save=True)
+        orc.ssm_scan_grad(plan, Y, saved, **big, initial_h=H0)
+        # whatever took the place of freed memory is not written either
+        other = [torch.full((1 << 20,), 3.0, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        for t, w in zip(outs, want):
+            assert torch.equal(t, w)
+        assert all((o == 3.0).all() for o in other)
+    orc.rnn_ssm_sync(plan)
+
+
+def test_plain_calls_beside_a_replay():
+    """Plain calls of the plan on another stream while its graph replays: neither uses the other's scratch."""
+    size = (2, 300, 64, 16, 2)
+    N, S, D, M, G = size
+    v, h0 = _scan_inputs(*size, seed=11)
+    w, k0 = _scan_inputs(*size, seed=12)
+    plan = orc.rnn_ssm_create(D, state_size=M, groups=G, layout=1)
+    want_v = [t.clone() for t in orc.ssm_scan(plan, **v, initial_h=h0)[:2]]
+    want_w = [t.clone() for t in orc.ssm_scan(plan, **w, initial_h=k0)[:2]]
+    gc.collect()
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        Y, Y_h, _ = orc.ssm_scan(plan, **v, initial_h=h0)
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        graph.replay()
+        with torch.cuda.stream(side):
+            outs.append(orc.ssm_scan(plan, **w, initial_h=k0)[:2])
+    torch.cuda.synchronize()
+    assert torch.equal(Y, want_v[0]) and torch.equal(Y_h, want_v[1])
+    for y, h in outs:
+        assert torch.equal(y, want_w[0]) and torch.equal(h, want_w[1])
