@@ -419,18 +419,18 @@ rnn_status rnn_cell_run(rnn_plan_t plan, int64_t batch_size, const float* X, con
  * own steps or rows (the latter is refused).
  *
  * Calls are stream-ordered and asynchronous and allocate nothing but the
- * plan's scratch (grown with cudaMalloc when a call needs more).  A plan is
- * not re-entrant; its calls may use different streams (a call that needs the
- * scratch waits for the previous one's use of it).  Make a plan's first call
- * before a stream capture.  Captured calls have scratch of their own, kept for
- * their graphs until the plan is destroyed: plain calls of any size may run
- * between replays and beside them, but replays of graphs with calls of one
- * plan must not run side by side, nor such branches of one graph, and the
- * plan must outlive them.  A length outside [0, seq_length] or a slot
- * outside its range is found by the kernels: the length is clamped, the slot
- * skipped, and rnn_ssm_sync reports RNN_ERR_INVALID_INPUT.  This differs from
- * rnn_run, which reads the lengths back first: a layer's calls follow one
- * another without a wait. */
+ * plan's scratch (grown with cudaMalloc when a call needs more) and, with its
+ * first call, a status word.  A plan is not re-entrant; its calls may use
+ * different streams (a call that needs the scratch waits for the previous
+ * one's use of it).  Captured calls have scratch of their own, kept for their
+ * graphs until the plan is destroyed: plain calls of any size may run between
+ * replays and beside them, but replays of graphs with calls of one plan must
+ * not run side by side, nor such branches of one graph, and the plan must
+ * outlive them.  A length outside [0, seq_length] or a slot outside its range
+ * is found by the kernels: the length is clamped, the slot skipped, and
+ * rnn_ssm_sync reports RNN_ERR_INVALID_INPUT.  This differs from rnn_run,
+ * which reads the lengths back first: a layer's calls follow one another
+ * without a wait. */
 typedef struct rnn_ssm* rnn_ssm_t;
 typedef struct {
     void* data;

@@ -169,11 +169,19 @@ rnn_status check_state(const rnn_ssm* pl, const void* p, const char* name)
 rnn_status ensure_status(rnn_ssm* pl)
 {
     if (pl->status) return RNN_OK;
+    // Cleared on a stream of its own, which alone is waited for: no other work is, and
+    // the plan's first call may be a captured one.
+    AmidCapture amid;
     int* p = nullptr;
-    cudaError_t e = cudaMalloc((void**)&p, 256);
+    cudaError_t e = amid.status == cudaSuccess ? cudaMalloc((void**)&p, 256) : amid.status;
     if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(status)");
-    e = cudaMemset(p, 0, 256);
-    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    cudaStream_t own = nullptr;
+    e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
+    if (e == cudaSuccess) {
+        e = cudaMemsetAsync(p, 0, 256, own);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(own);
+        cudaStreamDestroy(own);
+    }
     if (e != cudaSuccess) {
         cudaFree(p);
         return cuda_fail(e, "cudaMemset(status)");

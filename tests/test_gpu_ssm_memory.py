@@ -244,3 +244,45 @@ def test_plain_calls_beside_a_replay():
     assert torch.equal(Y, want_v[0]) and torch.equal(Y_h, want_v[1])
     for y, h in outs:
         assert torch.equal(y, want_w[0]) and torch.equal(h, want_w[1])
+
+
+def test_a_plans_first_call_does_not_wait_for_other_work():
+    D = 32
+    r = _rand(13)
+    X, W = r(2, 5, D), r(D, 4)
+    Y = torch.empty_like(X)
+    orc.rnn_ssm_conv(orc.rnn_ssm_create(D, layout=1), X, W, Y=Y)           # loads the kernel
+    a = torch.randn(8192, 8192, device="cuda", dtype=torch.bfloat16)
+    out, done, side = torch.empty_like(a), torch.cuda.Event(), torch.cuda.Stream()
+    torch.mm(a, a, out=out)
+    torch.cuda.synchronize()
+    for _ in range(200):                                                   # over 100 ms
+        torch.mm(a, a, out=out)
+    done.record()
+    plan = orc.rnn_ssm_create(D, layout=1)
+    orc.rnn_ssm_conv(plan, X, W, Y=Y, stream=side)
+    assert not done.query()
+    torch.cuda.synchronize()
+    orc.rnn_ssm_sync(plan)
+
+
+def test_a_plans_first_call_may_be_captured():
+    size = (1, 150, 136, 16, 1)
+    N, S, D, M, G = size
+    v, h0 = _scan_inputs(*size, seed=14)
+    want = orc.ssm_scan(orc.rnn_ssm_create(D, state_size=M, layout=1), **v, initial_h=h0)
+    plan = orc.rnn_ssm_create(D, state_size=M, layout=1)
+    lens = torch.tensor([S], dtype=torch.int32, device="cuda")
+    gc.collect()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Y, Y_h, _ = orc.ssm_scan(plan, **v, sequence_lens=lens, initial_h=h0)
+    graph.replay()
+    assert torch.equal(Y, want[0]) and torch.equal(Y_h, want[1])
+    orc.rnn_ssm_sync(plan)
+    lens.fill_(S + 1)                                                      # a length that the kernels report
+    graph.replay()
+    with pytest.raises(orc.RNNError):
+        orc.rnn_ssm_sync(plan)
+    orc.rnn_ssm_sync(plan)
