@@ -418,10 +418,12 @@ rnn_status rnn_cell_run(rnn_plan_t plan, int64_t batch_size, const float* X, con
  * [batch, seq, ...]).  Output views must not overlap an input, nor may their
  * own steps or rows (the latter is refused).
  *
- * Calls are stream-ordered and asynchronous and allocate nothing but the
- * plan's scratch (grown with cudaMalloc when a call needs more) and, with its
- * first call, a status word.  A plan is not re-entrant; its calls may use
- * different streams (a call that needs the scratch waits for the previous
+ * Calls run on the current device, which must be that of their tensors and
+ * stream, and the same for all calls of a plan (its memory lies there; another
+ * is refused).  They are stream-ordered and asynchronous and allocate nothing
+ * but the plan's scratch (grown with cudaMalloc when a call needs more) and,
+ * with its first call, a status word.  A plan is not re-entrant; its calls may
+ * use different streams (a call that needs the scratch waits for the previous
  * one's use of it).  Captured calls have scratch of their own, kept for their
  * graphs until the plan is destroyed: plain calls of any size may run between
  * replays and beside them, but replays of graphs with calls of one plan must

@@ -21,6 +21,7 @@ struct Kept {
 struct rnn_ssm {
     int64_t D = 0;
     int M = 0, G = 0, K = 0, layout = 0, silu = 0, softplus = 0, io = RNN_IO_F32;
+    int device = -1;              // of the first call: what follows lies there
     int* status = nullptr;        // device word the kernels report through
     char* scratch = nullptr;
     size_t scratch_bytes = 0;
@@ -166,14 +167,21 @@ rnn_status check_state(const rnn_ssm* pl, const void* p, const char* name)
     return RNN_OK;
 }
 
+// The plan's status word, on the device of its calls: the current one, which
+// must be the same every time.
 rnn_status ensure_status(rnn_ssm* pl)
 {
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if (pl->status && device != pl->device)
+        return fail(RNN_ERR_INVALID_ARGUMENT, "the plan's memory is on device %d, the current device is %d", pl->device, device);
     if (pl->status) return RNN_OK;
     // Cleared on a stream of its own, which alone is waited for: no other work is, and
     // the plan's first call may be a captured one.
     AmidCapture amid;
     int* p = nullptr;
-    cudaError_t e = amid.status == cudaSuccess ? cudaMalloc((void**)&p, 256) : amid.status;
+    e = amid.status == cudaSuccess ? cudaMalloc((void**)&p, 256) : amid.status;
     if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(status)");
     cudaStream_t own = nullptr;
     e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
@@ -187,6 +195,7 @@ rnn_status ensure_status(rnn_ssm* pl)
         return cuda_fail(e, "cudaMemset(status)");
     }
     pl->status = p;
+    pl->device = device;
     return RNN_OK;
 }
 
@@ -379,13 +388,16 @@ rnn_status rnn_ssm_sync(rnn_ssm_t pl)
 {
     if (!pl) return fail(RNN_ERR_INVALID_ARGUMENT, "plan is NULL");
     if (!pl->status) return RNN_OK;   // nothing has run
-    int word = 0;
-    cudaError_t e = cudaDeviceSynchronize();
+    int word = 0, current = 0;
+    cudaError_t e = cudaGetDevice(&current);
+    if (e == cudaSuccess && current != pl->device) e = cudaSetDevice(pl->device);
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e == cudaSuccess) e = cudaMemcpy(&word, pl->status, sizeof word, cudaMemcpyDeviceToHost);
     if (e == cudaSuccess && word) {
         e = cudaMemset(pl->status, 0, sizeof word);
         if (e == cudaSuccess) e = cudaDeviceSynchronize();
     }
+    if (current != pl->device) cudaSetDevice(current);
     if (e != cudaSuccess) return cuda_fail(e, "reading the status");
     if (word) return fail(RNN_ERR_INVALID_INPUT, "a sequence length outside [0, seq_length] or a slot outside its range");
     return RNN_OK;

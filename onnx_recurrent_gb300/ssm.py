@@ -20,13 +20,13 @@ _TORCH_IO = None
 _lib = None
 # torch and what the calls below use of it, set by _load: a token's call takes a
 # few microseconds in all, so each look-up counts.
-torch = _f32 = _i32 = _empty = _raw_stream = None
+torch = _f32 = _i32 = _empty = _raw_stream = _current_device = None
 
 Scores = namedtuple("Scores", "logp entropy lse top_ids top_logp")
 
 
 def _load():
-    global _lib, _TORCH_IO, torch, _f32, _i32, _empty, _raw_stream
+    global _lib, _TORCH_IO, torch, _f32, _i32, _empty, _raw_stream, _current_device
     if _lib is None:
         import torch
         lib = _rnn.load()
@@ -47,6 +47,7 @@ def _load():
         _f32, _i32, _empty = torch.float32, torch.int32, torch.empty
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _lib = lib
     return _lib
 
@@ -108,6 +109,15 @@ def _stream(stream, dev):
     if stream is None:
         return _raw_stream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _call(dev, entry, *args):
+    """An entry point, on the GPU that the call's tensors are on."""
+    if dev == _current_device():
+        _check(entry(*args))
+    else:
+        with torch.cuda.device(dev):
+            _check(entry(*args))
 
 
 def _bad(t, shape, dtype, dev, name):
@@ -204,7 +214,7 @@ def rnn_ssm_conv(plan: SSM, X, W, bias=None, sequence_lens=None, initial_state=N
         _dense(bias, (D,), f32, dev, "bias"), _dense(sequence_lens, (N,), _i32, dev, "sequence_lens"),
         _dense(initial_state, (N, K - 1, D), dt, dev, "initial_state"), *_view(Y, full, dt, dev, "Y", lay),
         _dense(final_state, (N, K - 1, D), dt, dev, "final_state"), _stream(stream, dev))
-    _check(_load().rnn_ssm_conv(plan.handle, args))
+    _call(dev, _load().rnn_ssm_conv, plan.handle, args)
 
 
 def ssm_conv(plan: SSM, X, W, bias=None, sequence_lens=None, initial_state=None, stream=None):
@@ -231,7 +241,7 @@ def rnn_ssm_conv_grad(plan: SSM, dY, X, W, bias=None, sequence_lens=None, initia
         *_view(dX, full, dt, dev, "dX", lay), _dense(dW, (D, K), f32, dev, "dW"),
         _dense(dbias, (D,), f32, dev, "dbias"), _dense(d_initial_state, state, dt, dev, "d_initial_state"),
         _stream(stream, dev))
-    _check(_load().rnn_ssm_conv_grad(plan.handle, args))
+    _call(dev, _load().rnn_ssm_conv_grad, plan.handle, args)
 
 
 def ssm_conv_grad(plan: SSM, dY, X, W, bias=None, sequence_lens=None, initial_state=None, d_final_state=None,
@@ -261,7 +271,7 @@ def rnn_ssm_conv_step(plan: SSM, X, W, bias, state, Y, state_out=None, slots=Non
         _dense(bias, (D,), _f32, dev, "bias"), at,
         at if state_out is None else _dense(state_out, shape, dt, dev, "state_out"),
         _dense(slots, (N,), _i32, dev, "slots"), *_rows(Y, (N, D), dt, dev, "Y"), _stream(stream, dev))
-    _check(_load().rnn_ssm_conv_step(plan.handle, args))
+    _call(dev, _load().rnn_ssm_conv_step, plan.handle, args)
 
 
 def rnn_ssm_saved_size(plan: SSM, seq_length, batch_size) -> int:
@@ -292,7 +302,7 @@ def rnn_ssm_scan(plan: SSM, X, dt, A, B, C, D=None, Z=None, dt_bias=None, sequen
         _dense(Y_h, (N, plan.channels, plan.state_size), _f32, dev, "Y_h"),
         0 if saved is None else _dense(saved, (rnn_ssm_saved_size(plan, S, N),), _f32, dev, "saved"),
         _stream(stream, dev))
-    _check(_load().rnn_ssm_scan(plan.handle, args))
+    _call(dev, _load().rnn_ssm_scan, plan.handle, args)
 
 
 def ssm_scan(plan: SSM, X, dt, A, B, C, D=None, Z=None, dt_bias=None, sequence_lens=None, initial_h=None, save=False,
@@ -324,7 +334,7 @@ def rnn_ssm_scan_grad(plan: SSM, dY, saved, X, dt, A, B, C, D=None, Z=None, dt_b
         _dense(dA, ch + (plan.state_size,), f32, dev, "dA"), _dense(dD, ch, f32, dev, "dD"),
         _dense(ddt_bias, ch, f32, dev, "ddt_bias"), _dense(d_initial_h, st, f32, dev, "d_initial_h"),
         _stream(stream, dev))
-    _check(_load().rnn_ssm_scan_grad(plan.handle, args))
+    _call(dev, _load().rnn_ssm_scan_grad, plan.handle, args)
 
 
 def ssm_scan_grad(plan: SSM, dY, saved, X, dt, A, B, C, D=None, Z=None, dt_bias=None, sequence_lens=None,
@@ -363,7 +373,7 @@ def rnn_ssm_scan_step(plan: SSM, X, dt, A, B, C, H, Y, D=None, Z=None, dt_bias=N
         _dense(dt_bias, (ch,), f32, dev, "dt_bias"), at,
         at if H_out is None else _dense(H_out, (n_slots, ch, M), f32, dev, "H_out"),
         _dense(slots, (N,), _i32, dev, "slots"), *_rows(Y, full, io, dev, "Y"), _stream(stream, dev))
-    _check(_load().rnn_ssm_scan_step(plan.handle, args))
+    _call(dev, _load().rnn_ssm_scan_step, plan.handle, args)
 
 
 _SHARED_ROW = -1        # RNN_SHARED_ROW: every row is the same one
@@ -395,7 +405,7 @@ def rnn_scores(logits, ids=None, top=0, logp=None, entropy=None, lse=None, top_i
         _dense(logp, (rows,), f32, dev, "logp"), _dense(entropy, (rows,), f32, dev, "entropy"),
         _dense(lse, (rows,), f32, dev, "lse"), _dense(top_ids, (rows, top), i32, dev, "top_ids"),
         _dense(top_logp, (rows, top), f32, dev, "top_logp"), _stream(stream, dev))
-    _check(lib.rnn_scores(args))
+    _call(dev, lib.rnn_scores, args)
 
 
 def scores(logits, ids=None, top=0, stream=None) -> Scores:
@@ -429,7 +439,7 @@ def rnn_scores_grad(logits, ids, result: Scores, d_logp=None, d_entropy=None, d_
         _dense(d_logp, (rows,), f32, dev, "d_logp"), _dense(d_entropy, (rows,), f32, dev, "d_entropy"), top,
         _dense(result.top_ids, (rows, top), _i32, dev, "top_ids") if top else 0,
         _dense(d_top, (rows, top), f32, dev, "d_top"), d_at, d_stride, _stream(stream, dev))
-    _check(lib.rnn_scores_grad(args))
+    _call(dev, lib.rnn_scores_grad, args)
 
 
 def scores_grad(logits, ids, result: Scores, d_logp=None, d_entropy=None, d_top=None, stream=None):
