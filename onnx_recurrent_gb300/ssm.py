@@ -111,6 +111,14 @@ def _stream(stream, dev):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _onto(stream, device):
+    """`stream` as the current one: what a call allocates belongs to the stream that it runs on (memory of another
+    stream's may still be in use by work queued there)."""
+    if isinstance(stream, int):
+        stream = torch.cuda.default_stream(device) if stream < 2 else torch.cuda.ExternalStream(stream, device)
+    return torch.cuda.stream(stream)
+
+
 def _call(dev, entry, *args):
     """An entry point, on the GPU that the call's tensors are on."""
     if dev == _current_device():
@@ -219,11 +227,14 @@ def rnn_ssm_conv(plan: SSM, X, W, bias=None, sequence_lens=None, initial_state=N
 
 def ssm_conv(plan: SSM, X, W, bias=None, sequence_lens=None, initial_state=None, stream=None):
     """Returns (Y, final_state)."""
+    if stream is not None:
+        with _onto(stream, X.device):
+            return ssm_conv(plan, X, W, bias, sequence_lens, initial_state)
     S, N = _sizes(plan, X)
     full, _ = _shapes(plan, S, N)
     Y = _empty(full, dtype=plan.dtype, device=X.device)
     state = torch.empty((N, plan.conv_width - 1, plan.channels), dtype=plan.dtype, device=X.device)
-    rnn_ssm_conv(plan, X, W, bias, sequence_lens, initial_state, Y, state, stream)
+    rnn_ssm_conv(plan, X, W, bias, sequence_lens, initial_state, Y, state)
     return Y, state
 
 
@@ -247,6 +258,9 @@ def rnn_ssm_conv_grad(plan: SSM, dY, X, W, bias=None, sequence_lens=None, initia
 def ssm_conv_grad(plan: SSM, dY, X, W, bias=None, sequence_lens=None, initial_state=None, d_final_state=None,
                   stream=None):
     """Returns a dict of dX and dW, of dbias where bias is given, and of d_initial_state where initial_state is."""
+    if stream is not None:
+        with _onto(stream, X.device):
+            return ssm_conv_grad(plan, dY, X, W, bias, sequence_lens, initial_state, d_final_state)
     S, N = _sizes(plan, X)
     full, _ = _shapes(plan, S, N)
     out = {"dX": _empty(full, dtype=plan.dtype, device=X.device), "dW": torch.empty_like(W)}
@@ -254,7 +268,7 @@ def ssm_conv_grad(plan: SSM, dY, X, W, bias=None, sequence_lens=None, initial_st
         out["dbias"] = torch.empty_like(bias)
     if initial_state is not None:
         out["d_initial_state"] = torch.empty_like(initial_state)
-    rnn_ssm_conv_grad(plan, dY, X, W, bias, sequence_lens, initial_state, d_final_state, stream=stream, **out)
+    rnn_ssm_conv_grad(plan, dY, X, W, bias, sequence_lens, initial_state, d_final_state, **out)
     return out
 
 
@@ -308,13 +322,16 @@ def rnn_ssm_scan(plan: SSM, X, dt, A, B, C, D=None, Z=None, dt_bias=None, sequen
 def ssm_scan(plan: SSM, X, dt, A, B, C, D=None, Z=None, dt_bias=None, sequence_lens=None, initial_h=None, save=False,
              stream=None):
     """Returns (Y, Y_h, saved); saved is None unless save."""
+    if stream is not None:
+        with _onto(stream, X.device):
+            return ssm_scan(plan, X, dt, A, B, C, D, Z, dt_bias, sequence_lens, initial_h, save)
     S, N = _sizes(plan, X)
     full, _ = _shapes(plan, S, N)
     dev, f32 = X.device, _f32
     Y = torch.empty(full, dtype=plan.dtype, device=dev)
     Y_h = torch.empty((N, plan.channels, plan.state_size), dtype=f32, device=dev)
     saved = torch.empty((rnn_ssm_saved_size(plan, S, N),), dtype=f32, device=dev) if save else None
-    rnn_ssm_scan(plan, X, dt, A, B, C, D, Z, dt_bias, sequence_lens, initial_h, Y, Y_h, saved, stream)
+    rnn_ssm_scan(plan, X, dt, A, B, C, D, Z, dt_bias, sequence_lens, initial_h, Y, Y_h, saved)
     return Y, Y_h, saved
 
 
@@ -340,6 +357,9 @@ def rnn_ssm_scan_grad(plan: SSM, dY, saved, X, dt, A, B, C, D=None, Z=None, dt_b
 def ssm_scan_grad(plan: SSM, dY, saved, X, dt, A, B, C, D=None, Z=None, dt_bias=None, sequence_lens=None,
                   initial_h=None, dY_h=None, stream=None):
     """Returns a dict of dX, ddt, dA, dB, dC and of dD, dZ, ddt_bias, d_initial_h for those of the inputs given."""
+    if stream is not None:
+        with _onto(stream, X.device):
+            return ssm_scan_grad(plan, dY, saved, X, dt, A, B, C, D, Z, dt_bias, sequence_lens, initial_h, dY_h)
     S, N = _sizes(plan, X)
     full, bc = _shapes(plan, S, N)
     new = lambda shape: torch.empty(shape, dtype=plan.dtype, device=X.device)  # noqa: E731
@@ -352,8 +372,7 @@ def ssm_scan_grad(plan: SSM, dY, saved, X, dt, A, B, C, D=None, Z=None, dt_bias=
         out["ddt_bias"] = torch.empty_like(dt_bias)
     if initial_h is not None:
         out["d_initial_h"] = torch.empty_like(initial_h)
-    rnn_ssm_scan_grad(plan, dY, saved, X, dt, A, B, C, D, Z, dt_bias, sequence_lens, initial_h, dY_h, stream=stream,
-                      **out)
+    rnn_ssm_scan_grad(plan, dY, saved, X, dt, A, B, C, D, Z, dt_bias, sequence_lens, initial_h, dY_h, **out)
     return out
 
 
@@ -412,13 +431,16 @@ def scores(logits, ids=None, top=0, stream=None) -> Scores:
     """Scores(logp, entropy, lse, top_ids, top_logp) of rows of logits; logp is
     None without ids, top_ids and top_logp are None for top = 0."""
     _load()
+    if stream is not None:
+        with _onto(stream, logits.device):
+            return scores(logits, ids, top)
     new = lambda shape, t=_f32: _empty(shape, dtype=t, device=logits.device)  # noqa: E731
     rows, top = logits.shape[0], int(top)
     if top < 0:
         raise ValueError(f"top must not be negative, got {top}")
     r = Scores(None if ids is None else new(rows), new(rows), new(rows),
                new((rows, top), _i32) if top else None, new((rows, top)) if top else None)
-    rnn_scores(logits, ids, top, *r, stream=stream)
+    rnn_scores(logits, ids, top, *r)
     return r
 
 
@@ -445,6 +467,9 @@ def rnn_scores_grad(logits, ids, result: Scores, d_logp=None, d_entropy=None, d_
 def scores_grad(logits, ids, result: Scores, d_logp=None, d_entropy=None, d_top=None, stream=None):
     """Returns dlogits, in the logits' type."""
     _load()
+    if stream is not None:
+        with _onto(stream, logits.device):
+            return scores_grad(logits, ids, result, d_logp, d_entropy, d_top)
     dlogits = _empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    rnn_scores_grad(logits, ids, result, d_logp, d_entropy, d_top, dlogits, stream)
+    rnn_scores_grad(logits, ids, result, d_logp, d_entropy, d_top, dlogits)
     return dlogits

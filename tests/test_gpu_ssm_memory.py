@@ -286,3 +286,45 @@ def test_a_plans_first_call_may_be_captured():
     with pytest.raises(orc.RNNError):
         orc.rnn_ssm_sync(plan)
     orc.rnn_ssm_sync(plan)
+
+
+# ------------------------------------------------------------- streams
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_outputs_belong_to_the_stream_of_the_call(handle):
+    """Memory that was freed on the current stream, where work queued earlier may still use it, is not what a call on
+    another stream writes."""
+    N, S, D, M, V = 2, 600, 512, 16, 4096
+    v, h0 = _scan_inputs(N, S, D, M, 1, seed=15)
+    r = _rand(16)
+    W, b, x = r(D, 4), r(D), r(N * S, V)
+    plan = orc.rnn_ssm_create(D, state_size=M, layout=1)
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if handle else side
+    torch.cuda.synchronize()
+
+    def freed(*shapes):
+        kept = [torch.empty(s, device="cuda") for s in shapes for _ in range(4)]
+        return {t.data_ptr() for t in kept}
+
+    def check(outs, spots):
+        assert not {t.data_ptr() for t in outs} & spots
+    full, state = (N, S, D), (N, D, M)
+    spots = freed(full, (N, 3, D))
+    check(orc.ssm_conv(plan, v["X"], W, b, stream=stream), spots)
+    spots = freed(full, (D, 4), (D,))
+    check(orc.ssm_conv_grad(plan, v["X"], v["X"], W, b, stream=stream).values(), spots)
+    side.synchronize()
+    spots = freed(full, state, (orc.rnn_ssm_saved_size(plan, S, N),))
+    Y, Y_h, saved = orc.ssm_scan(plan, **v, initial_h=h0, save=True, stream=stream)
+    check((Y, Y_h, saved), spots)
+    side.synchronize()
+    spots = freed(full, state, (N, S, 1, M), (D, M), (D,))
+    check(orc.ssm_scan_grad(plan, Y, saved, **v, initial_h=h0, stream=stream).values(), spots)
+    spots = freed((N * S, V), (N * S,), (N * S, 5))
+    s = orc.scores(x, torch.zeros(N * S, dtype=torch.int32, device="cuda"), top=5, stream=stream)
+    check(s, spots)
+    check([orc.scores_grad(x, None, s, d_top=s.top_logp, stream=stream)], spots)
+    torch.cuda.synchronize()
+    want = orc.ssm_scan(plan, **v, initial_h=h0)
+    assert torch.equal(Y, want[0]) and torch.equal(Y_h, want[1])
