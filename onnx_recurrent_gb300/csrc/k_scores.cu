@@ -1,17 +1,27 @@
 // Scores of rows of logits and their gradient (the formulas stand in
 // include/onnx_recurrent.h).
 //
-// One pass over a row keeps, per thread, a logit m that none so far exceeds by
-// more than kSlack and, with d_i = (x_i - m) log2 e,
+// One pass over a row keeps, per thread, a whole number R and, with
+// d_i = x_i log2 e - R, none so far larger than kSlack,
 //     s = sum_i 2^d_i,   u = sum_i d_i 2^d_i
-// (when m grows by g, in the same unit: u = (u - g s) 2^-g, s = s 2^-g), from which
-//     lse = m + log s,      entropy = log s - u / s log 2.
+// (when R grows by g: u = (u - g s) 2^-g, s = s 2^-g), from which
+//     logp_i = d_i log 2 - log s,   entropy = log s - u / s log 2.
+// d_i is one fused operation, rounded once; R is exact, and so is g, whatever a
+// row's offset from zero: sums of different R are joined without an error of their
+// own.  (A logit m times log2 e, rounded to fp32, is off by half a unit in its
+// last place, by another in each thread: 4 % of a row's weights around 10^6.)  And
+// logp does not go through lse, which at an offset of 30 is rounded by 10^-6.
 // With kSlack = 0 both parts of the entropy are >= 0 and nothing cancels; the
-// slack of 4 lets at most 4 units of them cancel (an error of 4 * 2^-24, kept from
-// making an entropy negative), and spares a warp, one of whose 32 threads finds a
-// larger logit nearly every time, the growing (8192 rows of 32000 bf16 logits: 107 us
-// without the slack, 101 us with it).  A -inf adds 0 to both sums (u takes d no
-// lower than -150, where 2^d is 0); a NaN or +inf makes s NaN.
+// slack of 6 lets at most 6 units of them cancel (an error of 4 * 2^-24 in units of log 2,
+// kept from making an entropy negative), and spares a warp, one of whose 32 threads finds
+// a larger logit nearly every time, the growing (8192 rows of 32000 bf16 logits took 107 us
+// without a slack and 101 us with one, before R was a whole number).  A -inf adds 0 to both sums (u takes d no
+// lower than -150, where 2^d is 0).
+//
+// R begins at that of -2^21, which logits of a mask's -10^38 leave where it is, and
+// is a NaN, as s then is, past 2^21, where whole numbers in fp32 would give out soon.  So
+// a row whose largest logit is a NaN, infinite or not within 2^21 of zero ends with s
+// = 0 or a NaN, and is read again with that logit taken from the others: d_i = (x_i - m) log2 e.
 //
 // Alternatives: the pass leaves every thread its largest logit.  The `top`-th
 // largest of these is a bound that at least `top` logits reach, and logits that reach it
@@ -22,14 +32,14 @@
 // first equal ones are taken; if even those above it are too many, each warp
 // keeps a sorted list of the 32 largest keys, one per lane, and inserts what is above the
 // last one wanted (done for every row, that took 677 us for 8192 rows of
-// 32000 bf16 logits, top 20, against 149 us this way).  Sorted lists are joined by
+// 32000 bf16 logits, top 20, against 137 us this way).  Sorted lists are joined by
 // taking the larger of one and the other reversed, and sorting that.
 //
 // A logit is read once (once more by the gradient, which writes it once).  At 16
 // bits the SMs' issue slots bind before the bytes do: about 11 instructions a
 // logit (conversion, d, 2^d, two sums, the extremes), three quarters of the slots.
-// The rows above take 101 us (5.2 TB/s; a copy's rate is 6.8 TB/s), their gradient 180 us
-// (5.8 TB/s), and as many bytes of 32-bit logits, top 8, 108 us (4.8 TB/s).  Tried and
+// The rows above take 88 us (6.0 TB/s; a copy's rate is 6.8 TB/s), their gradient 178 us
+// (5.9 TB/s), and as many bytes of 32-bit logits, top 8, 102 us (5.1 TB/s).  Tried and
 // no faster: one, three or four 16-byte loads ahead instead of two, copies to a
 // ring in shared memory.  A row is a block's; with fewer rows than fill the SMs it is
 // a cluster's, whose blocks' results the first joins through distributed
@@ -43,8 +53,9 @@ namespace rnngb {
 namespace {
 
 constexpr int kMaxCluster = 8;
-constexpr float kSlack = 4.0f;
-constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 6.0f;
+constexpr float kNear = 2097152.0f;                     // 2^21
+constexpr float kLn2 = 0.6931471805599453f, kLn2Rest = 7.348693209507928e-09f;      // 1 / kLog2e = kLn2 + kLn2Rest
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 __device__ __forceinline__ float a_nan() { return __int_as_float(0x7fc00000); }
@@ -102,31 +113,34 @@ __device__ __forceinline__ T sorted(T v)
     return v;
 }
 
-struct Sums {
-    float m, s, u;
-};
-// What is taken from a logit before 2^..; an empty set's is 0.
-__device__ __forceinline__ float base_of(float m) { return m == neg_inf() ? 0.0f : m; }
-__device__ __forceinline__ void raise_to(Sums& a, float m)
-{
-    const float g = (base_of(m) - base_of(a.m)) * kLog2e, f = a.s > 0.0f ? ex2(-g) : 0.0f;
-    a.u = f > 0.0f ? (a.u - g * a.s) * f : 0.0f;
-    a.s = a.s != a.s ? a.s : a.s * f;
-    a.m = m;
-}
 __device__ __forceinline__ float max_nan(float a, float b)
 {
     float v;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(v) : "f"(a), "f"(b));
     return v;
 }
-__device__ __forceinline__ void join(Sums& a, Sums b)
+// R of a near logit: v log2 e, rounded to a whole number where 1.5 * 2^23 has its last place.
+__device__ __forceinline__ float whole(float v) { return fmaf(v, kLog2e, 12582912.0f) - 12582912.0f; }
+struct Sums {
+    float r, s, u;
+};
+// The sums of groups of `width` lanes, in every lane.
+__device__ __forceinline__ Sums join(Sums a, int width)
 {
-    const float m = max_nan(a.m, b.m);
-    raise_to(a, m);
-    raise_to(b, m);
-    a.s += b.s;
-    a.u += b.u;
+    float r = a.r;
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2)
+        if (o < width) r = max_nan(r, __shfl_xor_sync(~0u, r, o));
+    const float g = r - a.r, f = ex2(-g);
+    a.u = fmaf(-g, a.s, a.u) * f;
+    a.s *= f;
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2)
+        if (o < width) {
+            a.s += __shfl_xor_sync(~0u, a.s, o);
+            a.u += __shfl_xor_sync(~0u, a.u, o);
+        }
+    return Sums{r, a.s, a.u};
 }
 
 // The elements of [lo, hi) of a row before its first 16-byte boundary.
@@ -145,41 +159,39 @@ __device__ __forceinline__ void unpack_vec(const uint4& raw, float (&v)[N])
     for (int i = 0; i < N; ++i) v[i] = to_f(e[i]);
 }
 
+// A thread's sums, in two halves; minus_r is -R.
+struct Running {
+    float minus_r;
+    f2 s, u;
+};
 // N neighbouring logits, of which the largest and the smallest are given.
-// Ordinary ones (|m| < 2^60, none more than 2^6 below m, so no -inf) need one
-// operation for d and no lower bound on it.
+// Ordinary ones (none of a d below -92, so no -inf) need no lower bound on d.
 template <int N>
-__device__ __forceinline__ void take(Sums& a, f2& s2, f2& u2, const float (&x)[N], float most, float least)
+__device__ __forceinline__ void take(Running& run, const float (&x)[N], float most, float least)
 {
-    if (!(most <= a.m + kSlack)) {
-        float v0, v1, w0, w1;
-        unpack2(s2, v0, v1);
-        unpack2(u2, w0, w1);
-        a.s = v0 + v1;
-        a.u = w0 + w1;
-        raise_to(a, max_nan(a.m, most));
-        s2 = pack2(a.s, 0.0f);
-        u2 = pack2(a.u, 0.0f);
+    if (!(fmaf(most, kLog2e, run.minus_r) <= kSlack)) {
+        const float r = most < kNear ? whole(most) : a_nan(), g = r + run.minus_r;
+        const f2 f = dup2(ex2(-g));
+        run.u = mul2(fma2(run.s, dup2(-g), run.u), f);
+        run.s = mul2(run.s, f);
+        run.minus_r = -r;
     }
-    const float base = base_of(a.m);
-    const f2 scale = dup2(kLog2e);
-    if (least > base - 64.0f && fabsf(base) < 1e18f) {
-        const f2 minus = dup2(-base * kLog2e);
+    const f2 scale = dup2(kLog2e), minus = dup2(run.minus_r);
+    if (fmaf(least, kLog2e, run.minus_r) > -92.0f) {
 #pragma unroll
         for (int e = 0; e < N; e += 2) {
             const f2 d = fma2(pack2(x[e], x[e + 1]), scale, minus), p = ex2_2(d);
-            s2 = add2(s2, p);
-            u2 = fma2(p, d, u2);
+            run.s = add2(run.s, p);
+            run.u = fma2(p, d, run.u);
         }
     } else {
-        const f2 minus = dup2(-base);
 #pragma unroll
         for (int e = 0; e < N; e += 2) {
-            const f2 d = mul2(add2(pack2(x[e], x[e + 1]), minus), scale), p = ex2_2(d);
+            const f2 d = fma2(pack2(x[e], x[e + 1]), scale, minus), p = ex2_2(d);
             float d0, d1;
             unpack2(d, d0, d1);
-            s2 = add2(s2, p);
-            u2 = fma2(p, pack2(fmaxf(d0, -150.0f), fmaxf(d1, -150.0f)), u2);
+            run.s = add2(run.s, p);
+            run.u = fma2(p, pack2(fmaxf(d0, -150.0f), fmaxf(d1, -150.0f)), run.u);
         }
     }
 }
@@ -362,6 +374,88 @@ __device__ __forceinline__ Key largest(const Part<V>& r, float most, int top, Sh
     return list;
 }
 
+// f(logits, their number) of this thread's pieces of the part.
+template <typename V, int THREADS, typename F>
+__device__ __forceinline__ void each(const Part<V>& r, F f)
+{
+    const int64_t one = r.single(threadIdx.x);
+    if (one >= 0) {
+        const float v = to_f(r.x[one]);
+        f(&v, 1);
+    }
+    for (int v = threadIdx.x; v < r.vecs; v += THREADS) {
+        float e[Part<V>::N];
+        unpack_vec<V, Part<V>::N>(r.body()[v], e);
+        f(e, Part<V>::N);
+    }
+}
+
+// What another block of the cluster has at an address of this one's.
+__device__ __forceinline__ float remote(const float* mine, int block)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_map(smem_addr(mine), block)) : "memory");
+    return v;
+}
+__device__ __forceinline__ Key remote(const Key* mine, int block)
+{
+    Key v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(cluster_map(smem_addr(mine), block)) : "memory");
+    return v;
+}
+
+// The largest logit m of a row read before (as r), and its sums with d_i = (x_i - m) log2 e:
+// in all threads of warp 0 of the row's first block.  `most`: this thread's largest, if KNOWN.
+template <typename V, int THREADS, bool KNOWN>
+__device__ __noinline__ Sums read_again(const V* x, int64_t V_, int part, int blocks, float most, Found* found, Found* mine)
+{
+    constexpr int WARPS = THREADS / 32;
+    const Part<V> r(x, V_, part, blocks);
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    if (!KNOWN) {
+        most = neg_inf();
+        each<V, THREADS>(r, [&](const float* x, int n) {
+            for (int i = 0; i < n; ++i) most = max_nan(most, x[i]);
+        });
+    }
+    for (int o = 16; o > 0; o /= 2) most = max_nan(most, __shfl_xor_sync(~0u, most, o));
+    __syncthreads();                     // all have read the first sums
+    if (blocks > 1) cluster_sync_all();
+    if (lane == 0) found[warp].sums.r = most;
+    __syncthreads();
+    float m = found[0].sums.r;
+    for (int w = 1; w < WARPS; ++w) m = max_nan(m, found[w].sums.r);
+    if (blocks > 1) {
+        if (threadIdx.x == 0) mine->sums.r = m;
+        cluster_sync_all();
+        for (int k = 0; k < blocks; ++k) m = max_nan(m, remote(&mine->sums.r, k));
+    }
+    float s = 0.0f, u = 0.0f;
+    if (m != neg_inf())
+        each<V, THREADS>(r, [&](const float* x, int n) {
+            for (int i = 0; i < n; ++i) {
+                const float d = (x[i] - m) * kLog2e, p = ex2(d);
+                s += p;
+                u = fmaf(p, fmaxf(d, -150.0f), u);
+            }
+        });
+    for (int o = 16; o > 0; o /= 2) {
+        s += __shfl_xor_sync(~0u, s, o);
+        u += __shfl_xor_sync(~0u, u, o);
+    }
+    if (lane == 0) found[warp].sums.s = s, found[warp].sums.u = u;
+    __syncthreads();
+    s = u = 0.0f;
+    for (int w = 0; w < WARPS; ++w) s += found[w].sums.s, u += found[w].sums.u;
+    if (blocks > 1) {
+        if (threadIdx.x == 0) mine->sums.s = s, mine->sums.u = u;
+        cluster_sync_all();
+        s = u = 0.0f;
+        for (int k = 0; k < blocks; ++k) s += remote(&mine->sums.s, k), u += remote(&mine->sums.u, k);
+    }
+    return Sums{m, s, u};
+}
+
 template <typename V, int THREADS, bool TOP>
 __global__ void __launch_bounds__(THREADS, 2048 / THREADS) scores_kernel(const ScoreParams p, int blocks)
 {
@@ -374,12 +468,11 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) scores_kernel(const S
     const int64_t row = blockIdx.x / blocks;
     const V* x = static_cast<const V*>(p.x) + row * p.stride;
     const Part<V> r(x, p.V, part, blocks);
-    Sums a{neg_inf(), 0.0f, 0.0f};
+    Running run{-whole(-kNear), 0, 0};
     const int64_t one = r.single(threadIdx.x);
-    f2 s2 = 0, u2 = 0;
     if (one >= 0) {
         const float v = to_f(x[one]), two[2] = {v, neg_inf()};
-        take<2>(a, s2, u2, two, v, neg_inf());
+        take<2>(run, two, v, neg_inf());
     }
     float most_here = one >= 0 ? to_f(x[one]) : neg_inf();       // this thread's largest
     for (int v = threadIdx.x; v < r.vecs; v += AHEAD * THREADS) {
@@ -394,68 +487,71 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) scores_kernel(const S
                 unpack_vec<V, N>(raw[k], e);
                 extremes(raw[k], e, most, least, V{});
                 if (TOP) most_here = max_nan(most_here, most);
-                take<N>(a, s2, u2, e, most, least);
+                take<N>(run, e, most, least);
             }
     }
+    Sums a;
     {
-        float v0, v1;
-        unpack2(s2, v0, v1);
-        a.s = v0 + v1;
-        unpack2(u2, v0, v1);
-        a.u = v0 + v1;
+        float v0, v1, w0, w1;
+        unpack2(run.s, v0, v1);
+        unpack2(run.u, w0, w1);
+        a = join(Sums{-run.minus_r, v0 + v1, w0 + w1}, 32);
     }
+    if (lane == 0) found[warp].sums = a;
     Key list = 0;
     if constexpr (TOP) list = largest<V, THREADS>(r, most_here, p.top, shared);
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2)
-        join(a, Sums{__shfl_xor_sync(~0u, a.m, o), __shfl_xor_sync(~0u, a.s, o), __shfl_xor_sync(~0u, a.u, o)});
-    if (lane == 0) found[warp].sums = a;
     __syncthreads();
-    if (warp == 0) {
-        a = found[lane % WARPS].sums;
-#pragma unroll
-        for (int o = WARPS / 2; o > 0; o /= 2)
-            join(a, Sums{__shfl_xor_sync(~0u, a.m, o), __shfl_xor_sync(~0u, a.s, o), __shfl_xor_sync(~0u, a.u, o)});
-    }
-    if (blocks > 1) {
+    Key next = 0;
+    a = found[lane % WARPS].sums;        // over the lanes: of the block's warps,
+    if (blocks > 1) {                    // then of the row's blocks
         if (warp == 0) {
+            a = join(a, WARPS);
             if (lane == 0) mine->sums = a;
             if (TOP) mine->list[lane] = list;
         }
         cluster_sync_all();
-        if (part == 0 && warp == 0) {
+        const int k = lane % blocks;
+        const bool joins = part == 0 && warp == 0;       // the others look at s alone
+        if (TOP && joins) next = remote(&mine->list[lane], 1);
+        a = Sums{joins ? remote(&mine->sums.r, k) : 0.0f, remote(&mine->sums.s, k), joins ? remote(&mine->sums.u, k) : 0.0f};
+    }
+    // (where R is a logit's, that one's 2^d is above 0.7); the same in all threads
+    const bool near = !__any_sync(~0u, a.s != a.s) && __any_sync(~0u, a.s > 0.5f);
+    if (!near) a = read_again<V, THREADS, TOP>(x, p.V, part, blocks, most_here, found, mine);
+    else if (warp == 0 && part == 0) a = join(a, blocks == 1 ? WARPS : blocks);
+    if (blocks > 1) {
+        if (TOP && part == 0 && warp == 0) {
             for (int k = 1; k < blocks; ++k) {
-                const unsigned at = cluster_map(smem_addr(mine), k);
-                Sums b;
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.m) : "r"(at));
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.s) : "r"(at + 4));
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.u) : "r"(at + 8));
-                join(a, b);
-                if (TOP) {
-                    Key other;
-                    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(other) : "r"(at + (unsigned)offsetof(Found, list) + 8 * lane));
-                    merge(list, other);
-                }
+                const Key other = next;
+                if (k + 1 < blocks) next = remote(&mine->list[lane], k + 1);
+                merge(list, other);
             }
         }
         cluster_sync_all();      // no block leaves before its results are read
         if (part != 0) return;
     }
     if (warp != 0) return;
+    // a.r is R, or the row's largest logit
     const bool bad = a.s != a.s, empty = a.s == 0.0f;
     const float total = empty ? 0.0f : logf(a.s);
-    const float lse = bad ? a_nan() : empty ? neg_inf() : a.m + total;
+    const float lse = bad ? a_nan() : empty ? neg_inf() : near ? fmaf(a.r, kLn2, fmaf(a.r, kLn2Rest, total)) : a.r + total;
+    auto log_p = [&](float v) {
+        if (bad || empty) return bad ? a_nan() : neg_inf();
+        // (past 10^30, a mask's value, the product would leave fp32's range)
+        const float lp = !near ? v - a.r - total : fabsf(v) < 1e30f ? fmaf(fmaf(v, kLog2e, -a.r), kLn2, -total) : v - lse;
+        return lp > 0.0f ? 0.0f : lp;          // a certain token's, rounded up
+    };
     if (lane == 0) {
         if (p.lse) p.lse[row] = lse;
         if (p.entropy) p.entropy[row] = bad ? a_nan() : empty ? 0.0f : fmaxf(total - a.u * kLn2 / a.s, 0.0f);
         if (p.logp) {
             const int id = p.ids[row];
-            p.logp[row] = id < 0 ? 0.0f : id >= p.V ? a_nan() : empty ? neg_inf() : to_f(x[id]) - lse;
+            p.logp[row] = id < 0 ? 0.0f : id >= p.V ? a_nan() : log_p(to_f(x[id]));
         }
     }
     if (TOP && lane < p.top) {
         if (p.top_ids) p.top_ids[row * p.top + lane] = (int)~(unsigned)list;
-        if (p.top_logp) p.top_logp[row * p.top + lane] = empty ? neg_inf() : logit_of(list) - lse;
+        if (p.top_logp) p.top_logp[row * p.top + lane] = log_p(logit_of(list));
     }
 }
 
