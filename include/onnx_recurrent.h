@@ -589,6 +589,10 @@ rnn_status rnn_ssm_scan_step(rnn_ssm_t plan, const rnn_ssm_scan_step_args* args)
  * ids (with logp), logp, entropy, lse, top_ids and top_logp (with top > 0)
  * are each optional. */
 #define RNN_SHARED_ROW (-1)
+/* Added to io: lse is [2, rows], the rows' lse and, after them, what its
+ * rounding to fp32 left off.  The gradient is then exact at any offset of the
+ * logits (without it, probabilities are off by as much as lse is). */
+#define RNN_SCORES_LSE_PAIR 256
 typedef struct {
     int64_t rows, vocab, row_stride, io;
     const void* logits;
@@ -596,7 +600,7 @@ typedef struct {
     int64_t top;
     float* logp;                   /* out [rows] */
     float* entropy;                /* out [rows] */
-    float* lse;                    /* out [rows] */
+    float* lse;                    /* out [rows], or [2, rows] */
     int32_t* top_ids;              /* out [rows, top] */
     float* top_logp;               /* out [rows, top] */
     void* stream;
@@ -614,7 +618,7 @@ typedef struct {
     int64_t rows, vocab, row_stride, io;
     const void* logits;
     const int32_t* ids;
-    const float* lse;
+    const float* lse;              /* [rows], or [2, rows] */
     const float* entropy;
     const float* d_logp;
     const float* d_entropy;

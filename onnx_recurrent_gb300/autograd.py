@@ -48,7 +48,7 @@ class _Scores(torch.autograd.Function):
     def forward(ctx, logits, ids, top):
         r = ssm.scores(logits, ids, top=top)
         ctx.top = top
-        ctx.save_for_backward(logits, ids, *r)
+        ctx.save_for_backward(logits, ids, r.lse._pair[0], *r)
         if r.top_ids is None:
             return r.logp, r.entropy
         ctx.mark_non_differentiable(r.top_ids)
@@ -56,8 +56,8 @@ class _Scores(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, d_logp, d_entropy, d_ids=None, d_top=None):
-        logits, ids, *r = ctx.saved_tensors
-        dlogits = ssm.scores_grad(logits, ids, ssm.Scores(*r), d_logp.contiguous(), d_entropy.contiguous(),
+        logits, ids, pair, *r = ctx.saved_tensors
+        dlogits = ssm.scores_grad(logits, ids, ssm.Scores(*r)._replace(lse=pair), d_logp.contiguous(), d_entropy.contiguous(),
                                   None if d_top is None else d_top.contiguous())
         return dlogits, None, None
 

@@ -534,7 +534,8 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) scores_kernel(const S
     // a.r is R, or the row's largest logit
     const bool bad = a.s != a.s, empty = a.s == 0.0f;
     const float total = empty ? 0.0f : logf(a.s);
-    const float lse = bad ? a_nan() : empty ? neg_inf() : near ? fmaf(a.r, kLn2, fmaf(a.r, kLn2Rest, total)) : a.r + total;
+    const float small = near ? fmaf(a.r, kLn2Rest, total) : total;         // lse without the large part
+    const float lse = bad ? a_nan() : empty ? neg_inf() : near ? fmaf(a.r, kLn2, small) : a.r + small;
     auto log_p = [&](float v) {
         if (bad || empty) return bad ? a_nan() : neg_inf();
         // (past 10^30, a mask's value, the product would leave fp32's range)
@@ -543,6 +544,7 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) scores_kernel(const S
     };
     if (lane == 0) {
         if (p.lse) p.lse[row] = lse;
+        if (p.lse_rest) p.lse_rest[row] = bad || empty ? 0.0f : (near ? fmaf(a.r, kLn2, -lse) : a.r - lse) + small;
         if (p.entropy) p.entropy[row] = bad ? a_nan() : empty ? 0.0f : fmaxf(total - a.u * kLn2 / a.s, 0.0f);
         if (p.logp) {
             const int id = p.ids[row];
@@ -555,7 +557,9 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) scores_kernel(const S
     }
 }
 
-// dlogits of a row, with d_i = (x_i - lse) log2 e and p_i = 2^d_i:
+// dlogits of a row, with d_i = (x_i - lse) log2 e and p_i = 2^d_i (lse in two parts where
+// the caller has the second: rounded to fp32 alone, it is off by 10^-6 at 30, and by all of
+// log V in an even row of a mask's -10^38, whose p_i would each be 1):
 //     g_i = p_i (k0 + k1 d_i),  k0 = -(d_logp + sum d_top + d_entropy entropy),
 //                               k1 = -d_entropy log 2,
 // plus a term of its own at the given token and at each alternative.  Those
@@ -573,7 +577,7 @@ __global__ void __launch_bounds__(THREADS) scores_grad_kernel(const ScoreGradPar
     V* dx = static_cast<V*>(p.dx) + row * p.d_stride;
     const int64_t per = ((p.V + blocks - 1) / blocks + N - 1) / N * N;
     const int64_t lo = part * per < p.V ? part * per : p.V, hi = lo + per < p.V ? lo + per : p.V;
-    const float lse = p.lse[row];
+    const float lse = p.lse[row], minus_rest = p.lse_rest ? -p.lse_rest[row] * kLog2e : 0.0f;
     const float dh = p.d_entropy ? p.d_entropy[row] : 0.0f, h = p.d_entropy ? p.entropy[row] : 0.0f;
     const int id = p.ids ? p.ids[row] : -1;
     const float dl = p.d_logp && id >= 0 ? p.d_logp[row] : 0.0f;
@@ -582,7 +586,7 @@ __global__ void __launch_bounds__(THREADS) scores_grad_kernel(const ScoreGradPar
     for (int j = 0; j < p.top; ++j) all += p.d_top[row * p.top + j];
     const float k0 = empty ? 0.0f : -fmaf(dh, h, all), k1 = empty ? 0.0f : -dh * kLn2;
     auto slope = [&](float v) {
-        const float d = empty ? neg_inf() : (v - lse) * kLog2e;
+        const float d = empty ? neg_inf() : fmaf(v - lse, kLog2e, minus_rest);
         return ex2(d) * fmaf(k1, fmaxf(d, -150.0f), k0);
     };
     float special = 0.0f;
@@ -619,14 +623,14 @@ __global__ void __launch_bounds__(THREADS) scores_grad_kernel(const ScoreGradPar
         const int64_t i = threadIdx.x < head ? lo + threadIdx.x : tail + threadIdx.x - head;
         if (threadIdx.x < head || i < hi) dx[i] = from_f<V>(slope(to_f(x[i])));
     }
-    const f2 scale = dup2(kLog2e), k0_2 = dup2(k0), k1_2 = dup2(k1), minus = dup2(-lse);
+    const f2 scale = dup2(kLog2e), k0_2 = dup2(k0), k1_2 = dup2(k1), minus = dup2(-lse), rest2 = dup2(minus_rest);
     auto body = [&](const uint4& raw, int64_t v) {
         float e[N];
         unpack_vec<V, N>(raw, e);
         __align__(16) V out[N];
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
-            const f2 d = mul2(add2(pack2(e[i], e[i + 1]), minus), scale);
+            const f2 d = fma2(add2(pack2(e[i], e[i + 1]), minus), scale, rest2);
             float d0, d1;
             unpack2(d, d0, d1);
             const f2 g = mul2(ex2_2(d), fma2(k1_2, pack2(fmaxf(d0, -150.0f), fmaxf(d1, -150.0f)), k0_2));

@@ -285,6 +285,7 @@ rnn_status check_scores(int64_t rows, int64_t vocab, int64_t stride, int64_t io,
 {
     if (rows < 0 || vocab <= 0) return fail(RNN_ERR_INVALID_ARGUMENT, "rows %lld, vocab %lld", (long long)rows, (long long)vocab);
     if (rows > 0x7fffff00LL || vocab > 0x7fffff00LL) return fail(RNN_ERR_UNSUPPORTED, "a size of 2^31 or more");
+    io &= ~(int64_t)RNN_SCORES_LSE_PAIR;
     if (io != RNN_IO_F32 && io != RNN_IO_F16 && io != RNN_IO_BF16)
         return fail(RNN_ERR_INVALID_ARGUMENT, "unknown io type %lld", (long long)io);
     if (stride != 0 && stride != RNN_SHARED_ROW && stride < vocab)
@@ -722,13 +723,14 @@ rnn_status rnn_scores(const rnn_scores_args* a)
     p.rows = a->rows;
     p.V = a->vocab;
     p.stride = logits_stride(a->row_stride, a->vocab);
-    p.io = (int)a->io;
+    p.io = (int)(a->io & ~RNN_SCORES_LSE_PAIR);
     p.top = (int)a->top;
     p.x = a->logits;
     p.ids = a->ids;
     p.logp = a->logp;
     p.entropy = a->entropy;
     p.lse = a->lse;
+    p.lse_rest = a->io & RNN_SCORES_LSE_PAIR && a->lse ? a->lse + a->rows : nullptr;
     p.top_ids = a->top_ids;
     p.top_logp = a->top_logp;
     int launches = 0;
@@ -746,7 +748,7 @@ rnn_status rnn_scores_grad(const rnn_scores_grad_args* a)
     if (a->rows == 0) return RNN_OK;
     NEED(a->lse, "lse");
     NEED(a->dlogits, "dlogits");
-    if ((uintptr_t)a->dlogits % element((int)a->io))
+    if ((uintptr_t)a->dlogits % element((int)(a->io & ~RNN_SCORES_LSE_PAIR)))
         return fail(RNN_ERR_INVALID_ARGUMENT, "dlogits are not aligned to their elements");
     rs = check_arrays({{a->ids, "ids"}, {a->lse, "lse"}, {a->entropy, "entropy"}, {a->d_logp, "d_logp"}, {a->d_entropy, "d_entropy"},
                        {a->top_ids, "top_ids"}, {a->d_top, "d_top"}});
@@ -759,11 +761,12 @@ rnn_status rnn_scores_grad(const rnn_scores_grad_args* a)
     p.V = a->vocab;
     p.stride = logits_stride(a->row_stride, a->vocab);
     p.d_stride = a->d_row_stride ? a->d_row_stride : a->vocab;
-    p.io = (int)a->io;
+    p.io = (int)(a->io & ~RNN_SCORES_LSE_PAIR);
     p.top = a->d_top ? (int)a->top : 0;
     p.x = a->logits;
     p.ids = a->ids;
     p.lse = a->lse;
+    p.lse_rest = a->io & RNN_SCORES_LSE_PAIR && a->lse ? a->lse + a->rows : nullptr;
     p.entropy = a->entropy;
     p.d_logp = a->d_logp;
     p.d_entropy = a->d_entropy;

@@ -104,7 +104,7 @@ struct ScoreParams {
     int io, top;
     const void* x;
     const int32_t* ids;
-    float *logp, *entropy, *lse;
+    float *logp, *entropy, *lse, *lse_rest;
     int32_t* top_ids;
     float* top_logp;
 };
@@ -114,7 +114,7 @@ struct ScoreGradParams {
     int io, top;
     const void* x;
     const int32_t* ids;
-    const float *lse, *entropy, *d_logp, *d_entropy;
+    const float *lse, *lse_rest, *entropy, *d_logp, *d_entropy;
     const int32_t* top_ids;
     const float* d_top;
     void* dx;

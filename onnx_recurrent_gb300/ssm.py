@@ -396,6 +396,31 @@ def rnn_ssm_scan_step(plan: SSM, X, dt, A, B, C, H, Y, D=None, Z=None, dt_bias=N
 
 
 _SHARED_ROW = -1        # RNN_SHARED_ROW: every row is the same one
+_LSE_PAIR = 256         # RNN_SCORES_LSE_PAIR: lse is [2, rows]
+
+
+def _version(t):
+    return None if t.is_inference() else t._version
+
+
+def _lse(t, rows, dev):
+    """(address, flag of io) of an lse: [rows], or [2, rows] with what its rounding leaves off.  ``scores`` makes the
+    former as the first half of the latter; the other half goes with it until a torch operation writes to it."""
+    if t is None:
+        return 0, 0
+    if t.dim() == 2:
+        return _dense(t, (2, rows), _f32, dev, "lse"), _LSE_PAIR
+    pair, version = getattr(t, "_pair", (None, None))
+    if pair is None or version != _version(t):
+        return _dense(t, (rows,), _f32, dev, "lse"), 0
+    return _dense(pair, (2, rows), _f32, dev, "lse"), _LSE_PAIR
+
+
+def _with_rest(pair):
+    """The lse of a new [2, rows]."""
+    lse = pair[0]
+    lse._pair = pair, _version(lse)
+    return lse
 
 
 def _logits(t, name, dtype=None, shape=None, device=None):
@@ -414,15 +439,15 @@ def _logits(t, name, dtype=None, shape=None, device=None):
 
 
 def rnn_scores(logits, ids=None, top=0, logp=None, entropy=None, lse=None, top_ids=None, top_logp=None, stream=None):
-    """Scores of rows of logits [rows, vocab] into the outputs given."""
+    """Scores of rows of logits [rows, vocab] into the outputs given; an lse of [2, rows] takes its rounding's rest too."""
     lib = _load()
     at, stride = _logits(logits, "logits")
     rows, vocab = logits.shape
     dev, f32, i32, top = logits.get_device(), _f32, _i32, int(top)
+    lse, pair = _lse(lse, rows, dev)
     args = struct.pack(
-        "13q", rows, vocab, stride, _TORCH_IO[logits.dtype], at, _dense(ids, (rows,), i32, dev, "ids"), top,
-        _dense(logp, (rows,), f32, dev, "logp"), _dense(entropy, (rows,), f32, dev, "entropy"),
-        _dense(lse, (rows,), f32, dev, "lse"), _dense(top_ids, (rows, top), i32, dev, "top_ids"),
+        "13q", rows, vocab, stride, _TORCH_IO[logits.dtype] + pair, at, _dense(ids, (rows,), i32, dev, "ids"), top,
+        _dense(logp, (rows,), f32, dev, "logp"), _dense(entropy, (rows,), f32, dev, "entropy"), lse, _dense(top_ids, (rows, top), i32, dev, "top_ids"),
         _dense(top_logp, (rows, top), f32, dev, "top_logp"), _stream(stream, dev))
     _call(dev, lib.rnn_scores, args)
 
@@ -438,7 +463,7 @@ def scores(logits, ids=None, top=0, stream=None) -> Scores:
     rows, top = logits.shape[0], int(top)
     if top < 0:
         raise ValueError(f"top must not be negative, got {top}")
-    r = Scores(None if ids is None else new(rows), new(rows), new(rows),
+    r = Scores(None if ids is None else new(rows), new(rows), _with_rest(new((2, rows))),
                new((rows, top), _i32) if top else None, new((rows, top)) if top else None)
     rnn_scores(logits, ids, top, *r)
     return r
@@ -455,9 +480,10 @@ def rnn_scores_grad(logits, ids, result: Scores, d_logp=None, d_entropy=None, d_
         raise ValueError("dlogits: rows must not share memory")
     dev, f32 = logits.get_device(), _f32
     top = 0 if d_top is None else d_top.shape[1]
+    lse, pair = _lse(result.lse, rows, dev)
     args = struct.pack(
-        "16q", rows, vocab, stride, _TORCH_IO[logits.dtype], at, _dense(ids, (rows,), _i32, dev, "ids"),
-        _dense(result.lse, (rows,), f32, dev, "lse"), _dense(result.entropy, (rows,), f32, dev, "entropy"),
+        "16q", rows, vocab, stride, _TORCH_IO[logits.dtype] + pair, at, _dense(ids, (rows,), _i32, dev, "ids"),
+        lse, _dense(result.entropy, (rows,), f32, dev, "entropy"),
         _dense(d_logp, (rows,), f32, dev, "d_logp"), _dense(d_entropy, (rows,), f32, dev, "d_entropy"), top,
         _dense(result.top_ids, (rows, top), _i32, dev, "top_ids") if top else 0,
         _dense(d_top, (rows, top), f32, dev, "d_top"), d_at, d_stride, _stream(stream, dev))

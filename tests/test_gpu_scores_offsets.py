@@ -104,3 +104,66 @@ def test_certain_tokens(io, V):
     sure = logp > -0.5
     assert sure.any() and float((got.logp.cpu() - logp).abs()[sure].max()) <= 16 * ref.U
     assert float((got.entropy.cpu() - entropy).abs()[sure].max()) <= 48 * ref.U
+
+
+def _exact_grad(x, ids, dl, dh):
+    x = x.double().requires_grad_(True)
+    logp = torch.log_softmax(x, 1)
+    entropy = -(logp.exp() * logp).nan_to_num(0.0).sum(1)
+    loss = (logp.gather(1, ids.long()[:, None])[:, 0] * dl.double()).sum() + (entropy * dh.double()).sum()
+    return torch.autograd.grad(loss, x)[0]
+
+
+@pytest.mark.parametrize("V", [40, 700, 5000])
+@pytest.mark.parametrize("offset", [0.0, 30.0, -100.0, 1e3, 1e5, -1e7, -1497613952.0])
+def test_gradient_of_offset_rows(V, offset):
+    """As norms: d's rounding (below 4 u times log 2, as most weight has |d| < 16), 2^x within 2 units in the last place
+    (4 u) and three products give a probability within 8 u, the factor beside it another 8 u of its terms."""
+    g = torch.Generator().manual_seed(V)
+    rows = 64
+    x = (torch.randn(rows, V, generator=g) * max(2.0, 2e-7 * abs(offset))).double().add(offset).float().cuda()
+    ids = torch.randint(0, V, (rows,), generator=g, dtype=torch.int32).cuda()
+    dl, dh = torch.randn(rows, generator=g).cuda(), torch.randn(rows, generator=g).cuda() * 0.3
+    got = orc.scores_grad(x, ids, orc.scores(x, ids), dl, dh).double()
+    want = _exact_grad(x, ids, dl, dh)
+    want_p = want - torch.zeros_like(want).scatter_(1, ids.long()[:, None], dl.double()[:, None])     # without the tokens' ones
+    assert float((got - want).norm() / want_p.norm()) <= 16 * ref.U
+
+
+@pytest.mark.parametrize("io", list(DT))
+@pytest.mark.parametrize("V", [1, 7, 300, 9000])
+def test_gradient_of_rows_masked_by_the_lowest_value(io, V):
+    """An even row: every probability is 1 / V, and the entropy, at its largest, has no slope."""
+    x = torch.full((3, V), torch.finfo(DT[io]).min, dtype=DT[io], device="cuda")
+    ids = torch.tensor([0, V // 2, V - 1], dtype=torch.int32, device="cuda")
+    one = torch.ones(3, device="cuda")
+    got = orc.scores_grad(x, ids, orc.scores(x, ids), one, one).double()
+    want = torch.full((3, V), -1.0 / V, dtype=torch.float64, device="cuda").scatter_add_(1, ids.long()[:, None], one.double()[:, None])
+    want = want.float().double()                # as any fp32 result is, at best
+    tol = 48 * ref.U / V + want.abs() * ref.IO_U[io] + ref.IO_TINY[io]
+    assert bool(((got - want).abs() <= tol).all())
+
+
+def test_scores_made_elsewhere_have_an_lse_alone():
+    """The gradient then takes that; it takes the rounding's rest again where the buffers are filled once more."""
+    x = torch.randn(5, 300, device="cuda")
+    even = torch.full((5, 300), torch.finfo(torch.float32).min, device="cuda")
+    ids = torch.arange(5, dtype=torch.int32, device="cuda")
+    one = torch.ones(5, device="cuda")
+    s, t = orc.scores(x, ids), orc.scores(even, ids)
+    logp, entropy, lse, top_ids, top_logp = s
+    assert lse.shape == (5,) and top_ids is None and top_logp is None
+    want = orc.scores_grad(x, ids, s, one)
+    bare = [s._replace(lse=lse.clone()), t._replace(lse=t.lse.copy_(lse))]       # no rest; one that is not lse's any more
+    orc.rnn_scores(x, ids, lse=torch.empty_like(lse))
+    for other in bare:
+        assert float((orc.scores_grad(x, ids, other, one) - want).abs().max()) <= 16 * ref.U
+    u = orc.scores(even, ids)
+    orc.rnn_scores(x, ids, 0, *u)
+    assert torch.equal(u.lse, lse) and torch.equal(orc.scores_grad(x, ids, u, one), want)
+    pair = torch.empty(2, 5, device="cuda")
+    orc.rnn_scores(x, ids, lse=pair)
+    assert torch.equal(pair[0], lse) and torch.equal(orc.scores_grad(x, ids, s._replace(lse=pair), one), want)
+    with torch.inference_mode():
+        v = orc.scores(x, ids)
+        assert torch.equal(orc.scores_grad(x, ids, v, one), want)
