@@ -116,8 +116,8 @@ __global__ void __launch_bounds__(kThreads, 5) ssm_scan_step_kernel(const ScanSt
             cp_async_wait<AHEAD - 1>();
             ulonglong2 h = *reinterpret_cast<const ulonglong2*>(&ring[r % AHEAD][threadIdx.x]);
             const f2 delta = dup2(v.x), dx = dup2(v.y);
-            h.x = fma2(ex2_2(mul2(delta, a0)), h.x, mul2(dx, vb.x));
-            h.y = fma2(ex2_2(mul2(delta, a1)), h.y, mul2(dx, vb.y));
+            h.x = fma2(decay2(delta, a0), h.x, mul2(dx, vb.x));
+            h.y = fma2(decay2(delta, a1), h.y, mul2(dx, vb.y));
             if (r + AHEAD < ROWS) start(r + AHEAD);
             else cp_async_commit();
             if (mine && at >= 0) *reinterpret_cast<ulonglong2*>(to + at) = h;
@@ -152,9 +152,10 @@ __global__ void __launch_bounds__(kThreads, 5) ssm_scan_step_kernel(const ScanSt
         }
         float s = 0.0f;
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            h[j] = fmaf(ex2(v.x * a[j]), h[j], v.y * vb[j]);
-            s = fmaf(vc[j], h[j], s);
+        for (int j = 0; j < E; j += 2) {
+            unpack2(fma2(decay2(dup2(v.x), pack2(a[j], a[j + 1])), pack2(h[j], h[j + 1]), mul2(dup2(v.y), pack2(vb[j], vb[j + 1]))), h[j],
+                    h[j + 1]);
+            s = fmaf(vc[j + 1], h[j + 1], fmaf(vc[j], h[j], s));
         }
         if (vec) start(r + AHEAD);
         if (on && m < p.M && slot >= 0) store_vec<float, E>(to + first[r], h, p.M - m < E ? p.M - m : E, vec);

@@ -49,12 +49,15 @@ __device__ __forceinline__ f2 ex2_2(f2 x)
     unpack2(x, a, b);
     return pack2(ex2(a), ex2(b));
 }
-// exp(d A) of a pair, A carrying log2 e.  The hardware's 2^x is low by 0.3 of
-// 2^-24 on average for x in [-0.1, -0.001] (measured; 0.5 in [-1, 0]), always
-// to the same side, which a state that remembers hundreds of steps sums up; a
-// nudge of the argument, rounded with the product, takes that out (relative
-// error of dA, 1024 steps: 1.1e-6 without it).  2^nudge rounds to 1, so d = 0 leaves a state as it is.
-__device__ __forceinline__ f2 decay2(f2 d, f2 A) { return ex2_2(fma2(d, A, pack2(2.7e-8f, 2.7e-8f))); }
+// exp(d A) of a pair, A carrying log2 e.  The hardware's 2^x is low, measured as
+// means over neighbouring d A, by 0.08 to 0.13 of 2^-24 where -d A is below 0.002 and by 0.3
+// to 0.5 from 0.003 on, always to the same side, and a state, which remembers
+// 1 / (-d A) steps, sums that up.  A nudge of the argument, rounded with the product,
+// adds 0.1 of 2^-24 back: what is left then sums up to at most 65 of 2^-24 for all -d A
+// above 0.0003 (without a nudge 250 of 2^-24, at 0.0003; with three times this one,
+// right for -d A around 0.1, 230 at 0.001 and 700 at 0.0003).  2^nudge rounds to 1, so
+// d = 0 leaves a state as it is.
+__device__ __forceinline__ f2 decay2(f2 d, f2 A) { return ex2_2(fma2(d, A, pack2(8.6e-9f, 8.6e-9f))); }
 __device__ __forceinline__ float rcp(float x)
 {
     float v;
