@@ -1,12 +1,13 @@
 """The state space operators and token scores as differentiable functions.
 
 Thin torch.autograd wrappers of ``ssm``: each forward and each gradient is one
-entry point of the CUDA library.  Gradients are those of one backward pass
-(they are not differentiable again).
+entry point of the CUDA library.  Gradients are those of one backward pass:
+differentiating them again raises an error.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import ssm
 
@@ -20,6 +21,7 @@ class _Conv(torch.autograd.Function):
         return Y, state
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY, d_state):
         X, W, bias, lens, h0 = ctx.saved_tensors
         g = ssm.ssm_conv_grad(ctx.plan, dY.contiguous(), X, W, bias, lens, h0, d_state.contiguous())
@@ -36,6 +38,7 @@ class _Scan(torch.autograd.Function):
         return Y, Y_h
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY, dY_h):
         saved, *args = ctx.saved_tensors
         g = ssm.ssm_scan_grad(ctx.plan, dY.contiguous(), saved, *args, dY_h=dY_h.contiguous())
@@ -55,6 +58,7 @@ class _Scores(torch.autograd.Function):
         return r.logp, r.entropy, r.top_ids, r.top_logp
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_logp, d_entropy, d_ids=None, d_top=None):
         logits, ids, pair, *r = ctx.saved_tensors
         dlogits = ssm.scores_grad(logits, ids, ssm.Scores(*r)._replace(lse=pair), d_logp.contiguous(), d_entropy.contiguous(),

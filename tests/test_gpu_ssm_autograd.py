@@ -1,0 +1,47 @@
+"""What the differentiable functions do besides a first gradient: second
+derivatives, outputs that a loss leaves out, inputs that need no gradient."""
+import pytest
+import torch
+
+import onnx_recurrent_gb300 as orc
+from onnx_recurrent_gb300 import autograd
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    orc.build()
+
+
+def _rand(seed):
+    g = torch.Generator().manual_seed(seed)
+    return lambda *s, scale=1.0: (torch.randn(*s, generator=g) * scale).cuda()
+
+
+def _layer(seed=0, N=2, S=9, D=8, M=4):
+    r = _rand(seed)
+    plan = orc.rnn_ssm_create(D, state_size=M, layout=1)
+    v = dict(X=r(N, S, D), dt=r(N, S, D, scale=0.5), A=-torch.exp(r(D, M)), B=r(N, S, 1, M), C=r(N, S, 1, M), D=r(D),
+             Z=r(N, S, D), dt_bias=r(D) - 2, initial_h=r(N, D, M))
+    return plan, v, dict(W=r(D, 4), bias=r(D), initial_state=r(N, 3, D))
+
+
+def _leaves(v):
+    return {k: t.clone().requires_grad_(True) for k, t in v.items()}
+
+
+@pytest.mark.parametrize("which", ["conv", "scan", "scores"])
+def test_second_derivatives_are_refused(which):
+    plan, v, c = _layer()
+    x = v["X"].clone().requires_grad_(True)
+    if which == "conv":
+        out = autograd.conv(plan, x ** 3, **c)[0]
+    elif which == "scan":
+        out = autograd.scan(plan, x ** 3, **{k: t for k, t in v.items() if k != "X"})[0]
+    else:
+        ids = torch.zeros(18, dtype=torch.int32, device="cuda")
+        out = autograd.scores((x ** 3).reshape(18, 8), ids)[0]
+    g, = torch.autograd.grad(out.square().sum(), x, create_graph=True)      # a gradient penalty's first half
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.square().sum().backward()
