@@ -12,6 +12,10 @@ from torch.autograd.function import once_differentiable
 from . import ssm
 
 
+def _dense(slope):
+    return None if slope is None else slope.contiguous()
+
+
 class _Conv(torch.autograd.Function):
     @staticmethod
     def forward(ctx, plan, X, W, bias, sequence_lens, initial_state):
@@ -61,8 +65,8 @@ class _Scores(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, d_logp, d_entropy, d_ids=None, d_top=None):
         logits, ids, pair, *r = ctx.saved_tensors
-        dlogits = ssm.scores_grad(logits, ids, ssm.Scores(*r)._replace(lse=pair), d_logp.contiguous(), d_entropy.contiguous(),
-                                  None if d_top is None else d_top.contiguous())
+        dlogits = ssm.scores_grad(logits, ids, ssm.Scores(*r)._replace(lse=pair), _dense(d_logp), d_entropy.contiguous(),
+                                  _dense(d_top))
         return dlogits, None, None
 
 
@@ -76,7 +80,7 @@ def scan(plan, X, dt, A, B, C, D=None, Z=None, dt_bias=None, sequence_lens=None,
     return _Scan.apply(plan, X, dt, A, B, C, D, Z, dt_bias, sequence_lens, initial_h)
 
 
-def scores(logits, ids, top=0):
-    """(logp, entropy), and (top_ids, top_logp) with top > 0, as ``scores``;
-    -logp is the cross entropy of the token."""
+def scores(logits, ids=None, top=0):
+    """(logp, entropy), and (top_ids, top_logp) with top > 0, as ``ssm.scores``;
+    -logp is the cross entropy of the token (None without ids)."""
     return _Scores.apply(logits, ids, top)

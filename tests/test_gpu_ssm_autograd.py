@@ -45,3 +45,23 @@ def test_second_derivatives_are_refused(which):
     g, = torch.autograd.grad(out.square().sum(), x, create_graph=True)      # a gradient penalty's first half
     with pytest.raises(RuntimeError, match="once_differentiable"):
         g.square().sum().backward()
+
+
+@pytest.mark.parametrize("top", [0, 3])
+def test_scores_without_tokens(top):
+    """A loss of the entropy and the alternatives alone."""
+    r = _rand(1)
+    x = r(7, 50).requires_grad_(True)
+    out = autograd.scores(x, top=top)
+    assert out[0] is None and len(out) == (4 if top else 2)
+    w = r(7), r(7, 3)
+    loss = (out[1] * w[0]).sum() + ((out[3] * w[1]).sum() if top else 0)
+    loss.backward()
+    y = x.detach().double().requires_grad_(True)
+    logp = torch.log_softmax(y, 1)
+    want = (-(logp.exp() * logp).sum(1) * w[0]).sum()
+    if top:
+        want = want + (logp.topk(3).values * w[1]).sum()
+    want.backward()
+    # products of a few roundings each, of terms below 4 in all: as a norm
+    assert float((x.grad - y.grad).norm() / y.grad.norm()) <= 1e-6
