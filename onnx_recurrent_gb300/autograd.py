@@ -2,7 +2,8 @@
 
 Thin torch.autograd wrappers of ``ssm``: each forward and each gradient is one
 entry point of the CUDA library.  Gradients are those of one backward pass:
-differentiating them again raises an error.
+differentiating them again raises an error.  Only the gradients that are asked
+for are formed, and a scan that needs none saves nothing for them.
 """
 from __future__ import annotations
 
@@ -16,9 +17,17 @@ def _dense(slope):
     return None if slope is None else slope.contiguous()
 
 
+def _wanted(ctx, inputs):
+    """New tensors for the gradients that are needed, under their names: inputs are (name, tensor) in the order of
+    forward's arguments after the plan, with no name for what has no gradient."""
+    return {name: torch.empty_like(t, memory_format=torch.contiguous_format)
+            for (name, t), needed in zip(inputs, ctx.needs_input_grad[1:]) if name and needed}
+
+
 class _Conv(torch.autograd.Function):
     @staticmethod
     def forward(ctx, plan, X, W, bias, sequence_lens, initial_state):
+        ctx.set_materialize_grads(False)
         Y, state = ssm.ssm_conv(plan, X, W, bias, sequence_lens, initial_state)
         ctx.plan = plan
         ctx.save_for_backward(X, W, bias, sequence_lens, initial_state)
@@ -28,13 +37,16 @@ class _Conv(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dY, d_state):
         X, W, bias, lens, h0 = ctx.saved_tensors
-        g = ssm.ssm_conv_grad(ctx.plan, dY.contiguous(), X, W, bias, lens, h0, d_state.contiguous())
-        return None, g["dX"], g["dW"], g.get("dbias"), None, g.get("d_initial_state")
+        dY = torch.zeros_like(X, memory_format=torch.contiguous_format) if dY is None else dY.contiguous()
+        g = _wanted(ctx, (("dX", X), ("dW", W), ("dbias", bias), (None, lens), ("d_initial_state", h0)))
+        ssm.rnn_ssm_conv_grad(ctx.plan, dY, X, W, bias, lens, h0, _dense(d_state), **g)
+        return None, g.get("dX"), g.get("dW"), g.get("dbias"), None, g.get("d_initial_state")
 
 
 class _Scan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, plan, X, dt, A, B, C, D, Z, dt_bias, sequence_lens, initial_h):
+        ctx.set_materialize_grads(False)
         args = (X, dt, A, B, C, D, Z, dt_bias, sequence_lens, initial_h)
         Y, Y_h, saved = ssm.ssm_scan(plan, *args, save=True)
         ctx.plan = plan
@@ -45,16 +57,19 @@ class _Scan(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dY, dY_h):
         saved, *args = ctx.saved_tensors
-        g = ssm.ssm_scan_grad(ctx.plan, dY.contiguous(), saved, *args, dY_h=dY_h.contiguous())
-        return (None, g["dX"], g["ddt"], g["dA"], g["dB"], g["dC"], g.get("dD"), g.get("dZ"), g.get("ddt_bias"), None,
-                g.get("d_initial_h"))
+        X = args[0]
+        dY = torch.zeros_like(X, memory_format=torch.contiguous_format) if dY is None else dY.contiguous()
+        names = ("dX", "ddt", "dA", "dB", "dC", "dD", "dZ", "ddt_bias", None, "d_initial_h")
+        g = _wanted(ctx, zip(names, args))
+        ssm.rnn_ssm_scan_grad(ctx.plan, dY, saved, *args, dY_h=_dense(dY_h), **g)
+        return (None, *(g.get(name) for name in names))
 
 
 class _Scores(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, ids, top):
+        ctx.set_materialize_grads(False)
         r = ssm.scores(logits, ids, top=top)
-        ctx.top = top
         ctx.save_for_backward(logits, ids, r.lse._pair[0], *r)
         if r.top_ids is None:
             return r.logp, r.entropy
@@ -65,7 +80,7 @@ class _Scores(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, d_logp, d_entropy, d_ids=None, d_top=None):
         logits, ids, pair, *r = ctx.saved_tensors
-        dlogits = ssm.scores_grad(logits, ids, ssm.Scores(*r)._replace(lse=pair), _dense(d_logp), d_entropy.contiguous(),
+        dlogits = ssm.scores_grad(logits, ids, ssm.Scores(*r)._replace(lse=pair), _dense(d_logp), _dense(d_entropy),
                                   _dense(d_top))
         return dlogits, None, None
 
@@ -77,7 +92,10 @@ def conv(plan, X, W, bias=None, sequence_lens=None, initial_state=None):
 
 def scan(plan, X, dt, A, B, C, D=None, Z=None, dt_bias=None, sequence_lens=None, initial_h=None):
     """(Y, Y_h) of the selective scan, as ``ssm_scan``."""
-    return _Scan.apply(plan, X, dt, A, B, C, D, Z, dt_bias, sequence_lens, initial_h)
+    args = (X, dt, A, B, C, D, Z, dt_bias, sequence_lens, initial_h)
+    if not torch.is_grad_enabled() or not any(t is not None and t.requires_grad for t in args):
+        return ssm.ssm_scan(plan, *args)[:2]
+    return _Scan.apply(plan, *args)
 
 
 def scores(logits, ids=None, top=0):

@@ -65,3 +65,67 @@ def test_scores_without_tokens(top):
     want.backward()
     # products of a few roundings each, of terms below 4 in all: as a norm
     assert float((x.grad - y.grad).norm() / y.grad.norm()) <= 1e-6
+
+
+def _grads(fn, plan, v, use):
+    leaf = _leaves(v)
+    outs = fn(plan, **leaf)
+    r = _rand(3)
+    sum((o * r(*o.shape)).sum() * u for o, u in zip(outs, use)).backward()
+    return {k: t.grad for k, t in leaf.items()}
+
+
+@pytest.mark.parametrize("used", [0, 1])
+def test_a_loss_of_one_output(used):
+    """The other's slopes are zeros, whether a tensor holds them or none does."""
+    plan, v, c = _layer(4)
+    c["X"] = v["X"]
+    for fn, inputs in ((autograd.scan, v), (autograd.conv, c)):
+        leaf = _leaves(inputs)
+        outs = fn(plan, **leaf)
+        w = _rand(5)(*outs[used].shape)
+        (outs[used] * w).sum().backward()
+        full = _leaves(inputs)
+        outs = fn(plan, **full)
+        ((outs[used] * w).sum() + (outs[1 - used] * 0).sum()).backward()
+        for k in inputs:
+            assert torch.equal(leaf[k].grad, full[k].grad), k
+
+
+@pytest.mark.parametrize("which", ["scan", "conv"])
+def test_only_the_gradients_asked_for(which):
+    plan, v, c = _layer(6)
+    c["X"] = v["X"]
+    fn, inputs = (autograd.scan, v) if which == "scan" else (autograd.conv, c)
+    want = _grads(fn, plan, inputs, (1, 1))
+    for name in inputs:
+        one = {k: t.clone().requires_grad_(k == name) for k, t in inputs.items()}
+        outs = fn(plan, **one)
+        r = _rand(3)
+        sum((o * r(*o.shape)).sum() for o in outs).backward()
+        assert torch.equal(one[name].grad, want[name]), name
+        assert all(t.grad is None for k, t in one.items() if k != name)
+
+
+@pytest.mark.parametrize("off", ["no_grad", "inference_mode", "no leaf"])
+def test_a_scan_without_gradients_saves_nothing(off):
+    """What the states and y would take on top of the outputs is not allocated."""
+    N, S, D, M = 2, 512, 256, 16
+    plan, v, _ = _layer(7, N, S, D, M)
+    if off != "no leaf":
+        v = _leaves(v)
+    saved = orc.rnn_ssm_saved_size(plan, S, N) * 4
+    outputs = 4 * (N * S * D + N * D * M)
+
+    def peak():
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        with torch.no_grad() if off == "no_grad" else torch.inference_mode(off == "inference_mode"):
+            Y, Y_h = autograd.scan(plan, **v)
+        assert not Y.requires_grad
+        return torch.cuda.max_memory_allocated() - before, Y, Y_h
+    taken, Y, Y_h = peak()
+    assert saved > outputs and taken < outputs + saved // 2
+    want = orc.ssm_scan(plan, **{k: t.detach() for k, t in v.items()})
+    assert torch.equal(Y, want[0]) and torch.equal(Y_h, want[1])
