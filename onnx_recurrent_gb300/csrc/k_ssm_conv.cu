@@ -489,10 +489,10 @@ bool views_fit(std::initializer_list<View> views, std::initializer_list<const vo
 
 // Steps of a run: the longest that leaves the SMs enough threads (each run
 // reads K - 1 inputs again, and writes a partial dW).
-int run_of(int64_t S, int64_t threads_a_run)
+int run_of(int64_t S, int64_t threads_a_run, int sms)
 {
     int run = 128;
-    while (run > 16 && (S + run - 1) / run * threads_a_run < 152 * 1024) run /= 2;
+    while (run > 16 && (S + run - 1) / run * threads_a_run < (int64_t)sms * 1024) run /= 2;
     return run;
 }
 int64_t run_count(int64_t S, int run) { return S > 0 ? (S + run - 1) / run : 1; }
@@ -501,50 +501,49 @@ constexpr int64_t kMaxGrid = 0x7fffffff;
 template <typename T, int K>
 struct RunConv {
     template <int NV>
-    static cudaError_t with(const ConvParams& p, cudaStream_t s)
+    static cudaError_t with(const ConvParams& p, int sms, cudaStream_t s)
     {
         const int64_t threads = (p.D + NV - 1) / NV, db = (threads + kThreads - 1) / kThreads;
-        const int run = run_of(p.S, threads * p.N);
+        const int run = run_of(p.S, threads * p.N, sms);
         const int64_t runs = run_count(p.S, run);
         if (db * runs > kMaxGrid / p.N) return cudaErrorInvalidConfiguration;
         ssm_conv_kernel<T, K, NV><<<(unsigned)(db * runs * p.N), kThreads, 0, s>>>(p, (unsigned)db, (unsigned)runs, run);
         return cudaGetLastError();
     }
-    static cudaError_t go(const ConvParams* p, cudaStream_t s)
+    static cudaError_t go(const ConvParams* p, int sms, cudaStream_t s)
     {
         constexpr int W = widest<T, K, false>();
         auto fit = [&](int nv) { return views_fit({p->X, p->Y}, {p->h0, p->hT}, p->D, sizeof(T), nv); };
-        if (fit(W)) return with<W>(*p, s);
+        if (fit(W)) return with<W>(*p, sms, s);
         if constexpr (sizeof(T) == 2 && W > 2)
-            if (fit(2)) return with<2>(*p, s);
-        return with<1>(*p, s);
+            if (fit(2)) return with<2>(*p, sms, s);
+        return with<1>(*p, sms, s);
     }
 };
 template <typename T, int K>
 struct RunConvGrad {
     template <int NV>
-    static cudaError_t with(const ConvGradParams& q, int run, cudaStream_t s)
+    static cudaError_t with(const ConvGradParams& q, cudaStream_t s)
     {
         const ConvParams& p = q.f;
+        const int run = q.run;
         const int64_t threads = (p.D + NV - 1) / NV, db = (threads + kThreads - 1) / kThreads, runs = run_count(p.S, run);
         if (db * runs > kMaxGrid / p.N) return cudaErrorInvalidConfiguration;
         ssm_conv_grad_kernel<T, K, NV><<<(unsigned)(db * runs * p.N), kThreads, 0, s>>>(q, (unsigned)db, (unsigned)runs, run);
         return cudaGetLastError();
     }
-    static cudaError_t go(const ConvGradParams* q, int run, cudaStream_t s)
+    static cudaError_t go(const ConvGradParams* q, cudaStream_t s)
     {
         constexpr int W = widest<T, K, true>();
         auto fit = [&](int nv) {
             return views_fit({q->f.X, q->dY, q->dX}, {q->f.h0, q->dhT, q->dh0}, q->f.D, sizeof(T), nv);
         };
-        if (fit(W)) return with<W>(*q, run, s);
+        if (fit(W)) return with<W>(*q, s);
         if constexpr (sizeof(T) == 2 && W > 2)
-            if (fit(2)) return with<2>(*q, run, s);
-        return with<1>(*q, run, s);
+            if (fit(2)) return with<2>(*q, s);
+        return with<1>(*q, s);
     }
 };
-int grad_run(const ConvParams& p) { return run_of(p.S, (p.D + 1) / 2 * p.N); }
-
 template <typename T, int K>
 struct RunConvStep {
     static cudaError_t go(const ConvStepParams* p, unsigned grid, int db, cudaStream_t s)
@@ -558,17 +557,28 @@ struct RunConvStep {
 
 cudaError_t launch_ssm_conv(const ConvParams& p, cudaStream_t s, int* launches)
 {
+    int sms = 0;
+    cudaError_t e = ssm_sm_count(&sms);
+    if (e != cudaSuccess) return e;
     ++*launches;
-    return by_type<RunConv>(p.io, p.K, &p, s);
+    return by_type<RunConv>(p.io, p.K, &p, sms, s);
 }
 
-int64_t ssm_conv_grad_parts(const ConvGradParams& q) { return q.f.N * run_count(q.f.S, grad_run(q.f)); }
+cudaError_t ssm_conv_grad_plan(ConvGradParams& q)
+{
+    int sms = 0;
+    cudaError_t e = ssm_sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    q.run = run_of(q.f.S, (q.f.D + 1) / 2 * q.f.N, sms);
+    q.parts = q.f.N * run_count(q.f.S, q.run);
+    return cudaSuccess;
+}
 
 cudaError_t launch_ssm_conv_grad(const ConvGradParams& q, cudaStream_t s, int* launches)
 {
     if (q.f.N > 0) {
         ++*launches;
-        cudaError_t e = by_type<RunConvGrad>(q.f.io, q.f.K, &q, grad_run(q.f), s);
+        cudaError_t e = by_type<RunConvGrad>(q.f.io, q.f.K, &q, s);
         if (e != cudaSuccess) return e;
     }
     if (!q.dW && !q.dbias) return cudaSuccess;

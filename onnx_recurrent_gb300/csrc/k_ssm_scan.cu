@@ -512,9 +512,15 @@ ScanChoice ssm_split(const ScanParams& p, int tile, const ScanCost& cost, int sm
 
 cudaError_t ssm_sm_count(int* sms)
 {
+    static std::atomic<int> known[64];          // a call's host time counts
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    return e == cudaSuccess ? cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) : e;
+    if (e != cudaSuccess) return e;
+    const bool keep = dev >= 0 && dev < 64;
+    if (keep && (*sms = known[dev].load(std::memory_order_relaxed))) return cudaSuccess;
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && keep) known[dev].store(*sms, std::memory_order_relaxed);
+    return e;
 }
 
 cudaError_t ssm_scan_plan(ScanParams& p, size_t* bytes)

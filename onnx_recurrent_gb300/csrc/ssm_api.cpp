@@ -471,7 +471,8 @@ rnn_status rnn_ssm_conv_grad(rnn_ssm_t pl, const rnn_ssm_conv_grad_args* a)
     p.dW = a->dW;
     p.dbias = a->dbias;
     cudaStream_t st = (cudaStream_t)a->stream;
-    p.parts = ssm_conv_grad_parts(p);
+    cudaError_t e = ssm_conv_grad_plan(p);
+    if (e != cudaSuccess) return cuda_fail(e, "reading the device's attributes");
     const size_t bytes = a->dW || a->dbias ? sizeof(float) * (size_t)p.parts * (size_t)(p.f.D * (p.f.K + 1)) : 0;
     // In place, the blocks of a row's first steps would write what those of its last
     // steps still read: they read a copy, on a 16-byte boundary as the slopes may be.
@@ -480,7 +481,6 @@ rnn_status rnn_ssm_conv_grad(rnn_ssm_t pl, const rnn_ssm_conv_grad_args* a)
     rs = claim_scratch(pl, copy ? at + copy : bytes, st, &scratch);
     if (rs != RNN_OK) return rs;
     p.part = bytes ? (float*)scratch : nullptr;
-    cudaError_t e = cudaSuccess;
     if (copy) {
         e = cudaMemcpyAsync(scratch + at, p.dhT, copy, cudaMemcpyDeviceToDevice, st);
         if (e != cudaSuccess) return cuda_fail(e, "copying d_final_state");

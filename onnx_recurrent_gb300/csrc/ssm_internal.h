@@ -46,6 +46,7 @@ struct ConvGradParams {
     const void* dhT;
     void* dh0;
     float *dW, *dbias;
+    int run;                // steps of a run (ssm_conv_grad_plan, as parts)
     float* part;            // [parts, D * K + D]
     int64_t parts;
 };
@@ -154,7 +155,7 @@ cudaError_t allow_shared(F* kernel, size_t bytes, std::atomic<uint64_t>& done)
 
 // Each launcher queues its kernels on `s` and adds their number to *launches.
 cudaError_t launch_ssm_conv(const ConvParams& p, cudaStream_t s, int* launches);
-int64_t ssm_conv_grad_parts(const ConvGradParams& p);
+cudaError_t ssm_conv_grad_plan(ConvGradParams& p);
 cudaError_t launch_ssm_conv_grad(const ConvGradParams& p, cudaStream_t s, int* launches);
 cudaError_t launch_ssm_conv_step(const ConvStepParams& p, cudaStream_t s, int* launches);
 int64_t ssm_saved_floats(int64_t S, int64_t N, int64_t D, int64_t M);
