@@ -70,7 +70,7 @@ class _Scores(torch.autograd.Function):
     def forward(ctx, logits, ids, top):
         ctx.set_materialize_grads(False)
         r = ssm.scores(logits, ids, top=top)
-        ctx.save_for_backward(logits, ids, r.lse._pair[0], *r)
+        ctx.save_for_backward(logits, ids, *r)
         if r.top_ids is None:
             return r.logp, r.entropy
         ctx.mark_non_differentiable(r.top_ids)
@@ -79,8 +79,10 @@ class _Scores(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, d_logp, d_entropy, d_ids=None, d_top=None):
-        logits, ids, pair, *r = ctx.saved_tensors
-        dlogits = ssm.scores_grad(logits, ids, ssm.Scores(*r)._replace(lse=pair), _dense(d_logp), _dense(d_entropy),
+        logits, ids, *r = ctx.saved_tensors
+        r = ssm.Scores(*r)
+        r.lse._rest = True             # as it was made, whether or not the tensor came back as the same object
+        dlogits = ssm.scores_grad(logits, ids, r, _dense(d_logp), _dense(d_entropy),
                                   _dense(d_top))
         return dlogits, None, None
 

@@ -428,17 +428,18 @@ __device__ __noinline__ Sums read_again(const V* x, int64_t V_, int part, int bl
     if (blocks > 1) {
         if (threadIdx.x == 0) mine->sums.r = m;
         cluster_sync_all();
-        for (int k = 0; k < blocks; ++k) m = max_nan(m, remote(&mine->sums.r, k));
+        m = remote(&mine->sums.r, lane % blocks);
+        for (int o = blocks / 2; o > 0; o /= 2) m = max_nan(m, __shfl_xor_sync(~0u, m, o));
     }
     float s = 0.0f, u = 0.0f;
-    if (m != neg_inf())
-        each<V, THREADS>(r, [&](const float* x, int n) {
-            for (int i = 0; i < n; ++i) {
-                const float d = (x[i] - m) * kLog2e, p = ex2(d);
-                s += p;
-                u = fmaf(p, fmaxf(d, -150.0f), u);
-            }
-        });
+    if (m == neg_inf()) return Sums{m, s, u};
+    each<V, THREADS>(r, [&](const float* x, int n) {
+        for (int i = 0; i < n; ++i) {
+            const float d = (x[i] - m) * kLog2e, p = ex2(d);
+            s += p;
+            u = fmaf(p, fmaxf(d, -150.0f), u);
+        }
+    });
     for (int o = 16; o > 0; o /= 2) {
         s += __shfl_xor_sync(~0u, s, o);
         u += __shfl_xor_sync(~0u, u, o);
@@ -450,8 +451,12 @@ __device__ __noinline__ Sums read_again(const V* x, int64_t V_, int part, int bl
     if (blocks > 1) {
         if (threadIdx.x == 0) mine->sums.s = s, mine->sums.u = u;
         cluster_sync_all();
-        s = u = 0.0f;
-        for (int k = 0; k < blocks; ++k) s += remote(&mine->sums.s, k), u += remote(&mine->sums.u, k);
+        s = remote(&mine->sums.s, lane % blocks);
+        u = remote(&mine->sums.u, lane % blocks);
+        for (int o = blocks / 2; o > 0; o /= 2) {
+            s += __shfl_xor_sync(~0u, s, o);
+            u += __shfl_xor_sync(~0u, u, o);
+        }
     }
     return Sums{m, s, u};
 }

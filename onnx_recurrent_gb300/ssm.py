@@ -20,13 +20,13 @@ _TORCH_IO = None
 _lib = None
 # torch and what the calls below use of it, set by _load: a token's call takes a
 # few microseconds in all, so each look-up counts.
-torch = _f32 = _i32 = _empty = _raw_stream = _current_device = None
+torch = _f32 = _i32 = _empty = _empty_like = _raw_stream = _current_device = None
 
 Scores = namedtuple("Scores", "logp entropy lse top_ids top_logp")
 
 
 def _load():
-    global _lib, _TORCH_IO, torch, _f32, _i32, _empty, _raw_stream, _current_device
+    global _lib, _TORCH_IO, torch, _f32, _i32, _empty, _empty_like, _raw_stream, _current_device
     if _lib is None:
         import torch
         lib = _rnn.load()
@@ -44,7 +44,7 @@ def _load():
         lib.rnn_scores.argtypes = [ctypes.c_char_p]
         lib.rnn_scores_grad.argtypes = [ctypes.c_char_p]
         _TORCH_IO = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
-        _f32, _i32, _empty = torch.float32, torch.int32, torch.empty
+        _f32, _i32, _empty, _empty_like = torch.float32, torch.int32, torch.empty, torch.empty_like
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
         _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -122,10 +122,12 @@ def _onto(stream, device):
 def _call(dev, entry, *args):
     """An entry point, on the GPU that the call's tensors are on."""
     if dev == _current_device():
-        _check(entry(*args))
+        status = entry(*args)
     else:
         with torch.cuda.device(dev):
-            _check(entry(*args))
+            status = entry(*args)
+    if status:
+        _check(status)
 
 
 def _bad(t, shape, dtype, dev, name):
@@ -222,7 +224,7 @@ def rnn_ssm_conv(plan: SSM, X, W, bias=None, sequence_lens=None, initial_state=N
         _dense(bias, (D,), f32, dev, "bias"), _dense(sequence_lens, (N,), _i32, dev, "sequence_lens"),
         _dense(initial_state, (N, K - 1, D), dt, dev, "initial_state"), *_view(Y, full, dt, dev, "Y", lay),
         _dense(final_state, (N, K - 1, D), dt, dev, "final_state"), _stream(stream, dev))
-    _call(dev, _load().rnn_ssm_conv, plan.handle, args)
+    _call(dev, _lib.rnn_ssm_conv, plan.handle, args)
 
 
 def ssm_conv(plan: SSM, X, W, bias=None, sequence_lens=None, initial_state=None, stream=None):
@@ -252,7 +254,7 @@ def rnn_ssm_conv_grad(plan: SSM, dY, X, W, bias=None, sequence_lens=None, initia
         *_view(dX, full, dt, dev, "dX", lay), _dense(dW, (D, K), f32, dev, "dW"),
         _dense(dbias, (D,), f32, dev, "dbias"), _dense(d_initial_state, state, dt, dev, "d_initial_state"),
         _stream(stream, dev))
-    _call(dev, _load().rnn_ssm_conv_grad, plan.handle, args)
+    _call(dev, _lib.rnn_ssm_conv_grad, plan.handle, args)
 
 
 def ssm_conv_grad(plan: SSM, dY, X, W, bias=None, sequence_lens=None, initial_state=None, d_final_state=None,
@@ -285,7 +287,7 @@ def rnn_ssm_conv_step(plan: SSM, X, W, bias, state, Y, state_out=None, slots=Non
         _dense(bias, (D,), _f32, dev, "bias"), at,
         at if state_out is None else _dense(state_out, shape, dt, dev, "state_out"),
         _dense(slots, (N,), _i32, dev, "slots"), *_rows(Y, (N, D), dt, dev, "Y"), _stream(stream, dev))
-    _call(dev, _load().rnn_ssm_conv_step, plan.handle, args)
+    _call(dev, _lib.rnn_ssm_conv_step, plan.handle, args)
 
 
 def rnn_ssm_saved_size(plan: SSM, seq_length, batch_size) -> int:
@@ -316,7 +318,7 @@ def rnn_ssm_scan(plan: SSM, X, dt, A, B, C, D=None, Z=None, dt_bias=None, sequen
         _dense(Y_h, (N, plan.channels, plan.state_size), _f32, dev, "Y_h"),
         0 if saved is None else _dense(saved, (rnn_ssm_saved_size(plan, S, N),), _f32, dev, "saved"),
         _stream(stream, dev))
-    _call(dev, _load().rnn_ssm_scan, plan.handle, args)
+    _call(dev, _lib.rnn_ssm_scan, plan.handle, args)
 
 
 def ssm_scan(plan: SSM, X, dt, A, B, C, D=None, Z=None, dt_bias=None, sequence_lens=None, initial_h=None, save=False,
@@ -351,7 +353,7 @@ def rnn_ssm_scan_grad(plan: SSM, dY, saved, X, dt, A, B, C, D=None, Z=None, dt_b
         _dense(dA, ch + (plan.state_size,), f32, dev, "dA"), _dense(dD, ch, f32, dev, "dD"),
         _dense(ddt_bias, ch, f32, dev, "ddt_bias"), _dense(d_initial_h, st, f32, dev, "d_initial_h"),
         _stream(stream, dev))
-    _call(dev, _load().rnn_ssm_scan_grad, plan.handle, args)
+    _call(dev, _lib.rnn_ssm_scan_grad, plan.handle, args)
 
 
 def ssm_scan_grad(plan: SSM, dY, saved, X, dt, A, B, C, D=None, Z=None, dt_bias=None, sequence_lens=None,
@@ -392,35 +394,35 @@ def rnn_ssm_scan_step(plan: SSM, X, dt, A, B, C, H, Y, D=None, Z=None, dt_bias=N
         _dense(dt_bias, (ch,), f32, dev, "dt_bias"), at,
         at if H_out is None else _dense(H_out, (n_slots, ch, M), f32, dev, "H_out"),
         _dense(slots, (N,), _i32, dev, "slots"), *_rows(Y, full, io, dev, "Y"), _stream(stream, dev))
-    _call(dev, _load().rnn_ssm_scan_step, plan.handle, args)
+    _call(dev, _lib.rnn_ssm_scan_step, plan.handle, args)
 
 
 _SHARED_ROW = -1        # RNN_SHARED_ROW: every row is the same one
 _LSE_PAIR = 256         # RNN_SCORES_LSE_PAIR: lse is [2, rows]
 
 
-def _version(t):
-    return None if t.is_inference() else t._version
+def _untouched(t):
+    """Whether no torch operation has written to an lse of ``_new_lse``."""
+    try:
+        return t._version == 1
+    except RuntimeError:                    # made in inference mode, which does not count
+        return True
+
+
+def _new_lse(rows, device):
+    """An lse of [rows] with room behind it for what its rounding leaves off."""
+    t = _empty(2 * rows, dtype=_f32, device=device).resize_(rows)
+    t._rest = True
+    return t
 
 
 def _lse(t, rows, dev):
-    """(address, flag of io) of an lse: [rows], or [2, rows] with what its rounding leaves off.  ``scores`` makes the
-    former as the first half of the latter; the other half goes with it until a torch operation writes to it."""
+    """(address, flag of io) of an lse: [rows], or [2, rows] with its rounding's rest, which ``_new_lse``'s have too."""
     if t is None:
         return 0, 0
     if t.dim() == 2:
         return _dense(t, (2, rows), _f32, dev, "lse"), _LSE_PAIR
-    pair, version = getattr(t, "_pair", (None, None))
-    if pair is None or version != _version(t):
-        return _dense(t, (rows,), _f32, dev, "lse"), 0
-    return _dense(pair, (2, rows), _f32, dev, "lse"), _LSE_PAIR
-
-
-def _with_rest(pair):
-    """The lse of a new [2, rows]."""
-    lse = pair[0]
-    lse._pair = pair, _version(lse)
-    return lse
+    return _dense(t, (rows,), _f32, dev, "lse"), _LSE_PAIR if getattr(t, "_rest", False) and _untouched(t) else 0
 
 
 def _logits(t, name, dtype=None, shape=None, device=None):
@@ -433,6 +435,8 @@ def _logits(t, name, dtype=None, shape=None, device=None):
     if t.dtype not in _TORCH_IO:
         raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
     rows, vocab = t.shape
+    if t.is_contiguous():
+        return t.data_ptr(), vocab
     if vocab > 1 and t.stride(1) != 1:
         raise ValueError(f"{name}: a row must be dense")
     return t.data_ptr(), (t.stride(0) or _SHARED_ROW) if rows > 1 else vocab
@@ -455,17 +459,24 @@ def rnn_scores(logits, ids=None, top=0, logp=None, entropy=None, lse=None, top_i
 def scores(logits, ids=None, top=0, stream=None) -> Scores:
     """Scores(logp, entropy, lse, top_ids, top_logp) of rows of logits; logp is
     None without ids, top_ids and top_logp are None for top = 0."""
-    _load()
+    lib = _load()
     if stream is not None:
         with _onto(stream, logits.device):
             return scores(logits, ids, top)
-    new = lambda shape, t=_f32: _empty(shape, dtype=t, device=logits.device)  # noqa: E731
-    rows, top = logits.shape[0], int(top)
+    at, stride = _logits(logits, "logits")
+    device, rows, top = logits.device, logits.shape[0], int(top)
     if top < 0:
         raise ValueError(f"top must not be negative, got {top}")
-    r = Scores(None if ids is None else new(rows), new(rows), _with_rest(new((2, rows))),
-               new((rows, top), _i32) if top else None, new((rows, top)) if top else None)
-    rnn_scores(logits, ids, top, *r)
+    dev, entropy = logits.get_device(), _empty(rows, dtype=_f32, device=device)
+    top_logp = _empty((rows, top), dtype=_f32, device=device) if top else None
+    r = Scores(None if ids is None else _empty_like(entropy), entropy, _new_lse(rows, device),
+               _empty_like(top_logp, dtype=_i32) if top else None, top_logp)
+    ids_at = _dense(ids, (rows,), _i32, dev, "ids")
+    args = struct.pack(
+        "13q", rows, logits.shape[1], stride, _TORCH_IO[logits.dtype] + _LSE_PAIR, at, ids_at, top,
+        r.logp.data_ptr() if ids_at else 0, entropy.data_ptr(), r.lse.data_ptr(), r.top_ids.data_ptr() if top else 0,
+        top_logp.data_ptr() if top else 0, _raw_stream(dev))
+    _call(dev, lib.rnn_scores, args)
     return r
 
 
