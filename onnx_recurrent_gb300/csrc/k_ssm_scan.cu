@@ -110,17 +110,16 @@ __global__ void __launch_bounds__(Tile<V, L>::THREADS, 16 / Tile<V, L>::W)
 
     // this lane's channels (of the warp's) and states
     const int sg = lane % L, cg = lane / L;
-    // Exchanges over a channel's lanes that halve the pairs: SPLIT of them; then
-    // one that halves the last pair (HALVE), if there are lanes left for it.
-    constexpr int SPLIT = PAIRS >= 4 && L >= 4 ? 2 : PAIRS >= 2 && L >= 2 ? 1 : 0, LEFT = PAIRS >> SPLIT;
+    // Exchanges over a channel's lanes: one that halves the pairs (SPLIT), then
+    // one that halves the last pair (HALVE), if there are lanes for them.
+    constexpr int SPLIT = L >= 2 ? 1 : 0, LEFT = PAIRS >> SPLIT;
     constexpr bool HALVE = LEFT == 1 && L > (1 << SPLIT);
     const bool up = HALVE && (sg >> SPLIT & 1);
+    static_assert(PAIRS == 2, "the exchanges are those of two pairs");
     int ch[PAIRS];                                                // first channel of each pair
 #pragma unroll
     for (int r = 0; r < PAIRS; ++r) {
-        int at = r;                                               // where the lane keeps and sends differs by its bits
-        if (SPLIT >= 1 && sg & 1) at ^= PAIRS / 2;
-        if (SPLIT >= 2 && sg & 2) at ^= PAIRS / 4;
+        const int at = SPLIT && sg & 1 ? r ^ 1 : r;               // what the lane keeps, and what it sends
         ch[r] = cg * CH + 2 * at;
     }
     f2 A[E][PAIRS], h[E][PAIRS];
@@ -285,11 +284,7 @@ __global__ void __launch_bounds__(Tile<V, L>::THREADS, 16 / Tile<V, L>::W)
                     }
                 if (ENDS) continue;
                 // over the channel's lanes
-#pragma unroll
-                for (int k = 0; k < SPLIT; ++k)
-#pragma unroll
-                    for (int i = 0; i < PAIRS >> (k + 1); ++i)
-                        y[i] = add2(y[i], __shfl_xor_sync(~0u, y[i + (PAIRS >> (k + 1))], 1 << k));
+                if (SPLIT) y[0] = add2(y[0], __shfl_xor_sync(~0u, y[1], 1));
                 if (HALVE) {
                     float a, b2;
                     unpack2(y[0], a, b2);

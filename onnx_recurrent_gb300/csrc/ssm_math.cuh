@@ -1,5 +1,4 @@
-// Device helpers of the state space and token score kernels: element types,
-// row lengths, and the softplus and silu of the formulas with their slopes.
+// Device helpers of the state space and token score kernels: element types and row lengths.
 #pragma once
 
 #include <cstdint>
@@ -34,16 +33,5 @@ __device__ __forceinline__ int64_t row_length(const int32_t* lens, int64_t n, in
     }
     return len;
 }
-
-__device__ __forceinline__ float sigmoid_f(float v) { return 1.0f / (1.0f + expf(-v)); }
-__device__ __forceinline__ float silu_f(float v) { return v / (1.0f + expf(-v)); }
-// silu's slope: s + v s (1 - s) with s = sigmoid(v).
-__device__ __forceinline__ float silu_slope(float v)
-{
-    const float s = sigmoid_f(v);
-    return s + v * s * (1.0f - s);
-}
-// log(1 + exp(v)) without overflow and without cancellation for v << 0.
-__device__ __forceinline__ float softplus_f(float v) { return fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v))); }
 
 }  // namespace rnngb

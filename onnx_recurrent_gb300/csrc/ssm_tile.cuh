@@ -146,11 +146,10 @@ struct Stager {
     static constexpr int EP = 16 / (int)sizeof(V);
     static constexpr int PIECES = (COLS + EP - 1) / EP;
     static constexpr int PITCH = PIECES * EP;                  // of a step in shared memory
-    static constexpr int EACH = THREADS >= PIECES ? THREADS / PIECES : 1;       // steps a pass
-    static constexpr int TURNS = THREADS >= PIECES ? 1 : PIECES / THREADS;      // pieces a thread and step
+    static constexpr int EACH = THREADS / PIECES;              // steps a pass
     static constexpr int PASSES = (T + EACH - 1) / EACH;
-    static_assert(THREADS % PIECES == 0 || PIECES % THREADS == 0, "pieces are a power of two");
-    __device__ __forceinline__ static int row() { return TURNS > 1 ? 0 : threadIdx.x / PIECES; }
+    static_assert(THREADS % PIECES == 0, "every thread has one piece of a step");
+    __device__ __forceinline__ static int row() { return threadIdx.x / PIECES; }
     __device__ __forceinline__ static int col() { return threadIdx.x % PIECES * EP; }
     __device__ __forceinline__ static void piece(V* to, const V* src, int count, bool fast, const View& v)
     {
@@ -167,7 +166,7 @@ struct Stager {
     {
         V* to = dst + row() * PITCH + col();
         const V* src = static_cast<const V*>(v.data) + (t0 + row()) * v.ss + n * v.bs + c0 + col();
-        if (fast && live == T && valid >= PITCH && TURNS == 1) {       // a whole tile
+        if (fast && live == T && valid >= PITCH) {       // a whole tile
 #pragma unroll
             for (int i = 0; i < PASSES; ++i) {
                 if (EACH <= T || row() < T) cp_async16(to + i * EACH * PITCH, src, 16);
@@ -175,11 +174,7 @@ struct Stager {
             }
         } else {
             for (int i = 0; i < PASSES; ++i) {
-                if (EACH <= T || row() < T)
-                    for (int k = 0; k < TURNS; ++k) {
-                        const int at = k * THREADS * EP;
-                        piece(to + i * EACH * PITCH + at, src + at, row() + i * EACH < live ? valid - col() - at : 0, fast, v);
-                    }
+                if (EACH <= T || row() < T) piece(to + i * EACH * PITCH, src, row() + i * EACH < live ? valid - col() : 0, fast, v);
                 src += EACH * v.ss;
             }
         }
