@@ -416,7 +416,7 @@ rnn_status rnn_cell_run(rnn_plan_t plan, int64_t batch_size, const float* X, con
  * batch row are in elements, so a view may be a part of a wider tensor.  Both
  * strides zero: dense, in the plan's layout (0: [seq, batch, ...], 1:
  * [batch, seq, ...]).  Output views must not overlap an input, nor may their
- * own steps or rows (the latter is refused).
+ * own steps or rows (the latter is refused, as is the convolution in place).
  *
  * Calls run on the current device, which must be that of their tensors and
  * stream, and the same for all calls of a plan (its memory lies there; another

@@ -140,6 +140,15 @@ rnn_status check_outputs(int64_t S, int64_t N, const OutView (&views)[K])
     return RNN_OK;
 }
 
+// The convolution in place: a run of steps begins with the K - 1 inputs before it
+// (its gradient ends with the slopes after it), which another block overwrites.
+rnn_status check_not_input(const rnn_ssm* pl, int64_t S, const rnn_view& out, const char* name, const rnn_view& in, const char* input)
+{
+    if (out.data && out.data == in.data && S > 1 && pl->K > 1)
+        return fail(RNN_ERR_INVALID_ARGUMENT, "%s must not be %s", name, input);
+    return RNN_OK;
+}
+
 struct NamedF32 {
     const void* p;
     const char* name;
@@ -424,6 +433,7 @@ rnn_status rnn_ssm_conv(rnn_ssm_t pl, const rnn_ssm_conv_args* a)
     // the same memory needs no copy: a row's first run alone reads it, and its threads have read a value before they write it
     const size_t states = element(pl->io) * (size_t)(a->batch_size * (pl->K - 1) * pl->D);
     if (rs == RNN_OK) rs = check_in_place(a->initial_state, a->final_state, states, "initial_state and final_state");
+    if (rs == RNN_OK) rs = check_not_input(pl, a->seq_length, a->Y, "Y", a->X, "X");
     if (rs == RNN_OK) rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
     ConvParams p = conv_params(pl, a->seq_length, a->batch_size);
@@ -455,6 +465,8 @@ rnn_status rnn_ssm_conv_grad(rnn_ssm_t pl, const rnn_ssm_conv_grad_args* a)
     if (rs == RNN_OK) rs = check_outputs(a->seq_length, a->batch_size, {{dX, pl->D, "dX"}});
     const size_t states = element(pl->io) * (size_t)(a->batch_size * (pl->K - 1) * pl->D);
     if (rs == RNN_OK) rs = check_in_place(a->d_final_state, a->d_initial_state, states, "d_final_state and d_initial_state");
+    if (rs == RNN_OK) rs = check_not_input(pl, a->seq_length, a->dX, "dX", a->X, "X");
+    if (rs == RNN_OK) rs = check_not_input(pl, a->seq_length, a->dX, "dX", a->dY, "dY");
     if (rs == RNN_OK) rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
     ConvGradParams p{};

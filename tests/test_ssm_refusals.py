@@ -104,3 +104,12 @@ def test_the_convolutions_and_single_tokens_states_that_overlap_in_part(lib):
     for other in (h + 4, h - 4, h + 124, h - 124):
         conv = [5, 2, at, 0, 0, at, 0, 0, h, at, 0, 0, other, 0]
         assert _run(lib.rnn_ssm_conv, conv, p) == 1 and "overlap" in orc.rnn_last_error()
+
+
+def test_the_convolution_in_place(lib):
+    p = orc.rnn_ssm_create(8, state_size=4, conv_width=3)
+    x, y, w = (1 << 20, 0, 0), (2 << 20, 0, 0), 4096
+    assert _run(lib.rnn_ssm_conv, [50, 2, *x, w, 0, 0, 0, *x, 0, 0], p) == 1 and "Y must not be X" in orc.rnn_last_error()
+    for dX in (x, y):
+        assert _run(lib.rnn_ssm_conv_grad, [50, 2, *y, *x, w, 0, 0, 0, 0, *dX, 0, 0, 0, 0], p) == 1
+        assert "dX must not be" in orc.rnn_last_error()
