@@ -501,23 +501,23 @@ constexpr int64_t kMaxGrid = 0x7fffffff;
 template <typename T, int K>
 struct RunConv {
     template <int NV>
-    static cudaError_t with(const ConvParams& p, int sms, cudaStream_t s)
+    static cudaError_t with(const ConvParams& p, cudaStream_t s)
     {
         const int64_t threads = (p.D + NV - 1) / NV, db = (threads + kThreads - 1) / kThreads;
-        const int run = run_of(p.S, threads * p.N, sms);
+        const int run = run_of(p.S, threads * p.N, p.sms);
         const int64_t runs = run_count(p.S, run);
         if (db * runs > kMaxGrid / p.N) return cudaErrorInvalidConfiguration;
         ssm_conv_kernel<T, K, NV><<<(unsigned)(db * runs * p.N), kThreads, 0, s>>>(p, (unsigned)db, (unsigned)runs, run);
         return cudaGetLastError();
     }
-    static cudaError_t go(const ConvParams* p, int sms, cudaStream_t s)
+    static cudaError_t go(const ConvParams* p, cudaStream_t s)
     {
         constexpr int W = widest<T, K, false>();
         auto fit = [&](int nv) { return views_fit({p->X, p->Y}, {p->h0, p->hT}, p->D, sizeof(T), nv); };
-        if (fit(W)) return with<W>(*p, sms, s);
+        if (fit(W)) return with<W>(*p, s);
         if constexpr (sizeof(T) == 2 && W > 2)
-            if (fit(2)) return with<2>(*p, sms, s);
-        return with<1>(*p, sms, s);
+            if (fit(2)) return with<2>(*p, s);
+        return with<1>(*p, s);
     }
 };
 template <typename T, int K>
@@ -557,21 +557,14 @@ struct RunConvStep {
 
 cudaError_t launch_ssm_conv(const ConvParams& p, cudaStream_t s, int* launches)
 {
-    int sms = 0;
-    cudaError_t e = ssm_sm_count(&sms);
-    if (e != cudaSuccess) return e;
     ++*launches;
-    return by_type<RunConv>(p.io, p.K, &p, sms, s);
+    return by_type<RunConv>(p.io, p.K, &p, s);
 }
 
-cudaError_t ssm_conv_grad_plan(ConvGradParams& q)
+void ssm_conv_grad_plan(ConvGradParams& q)
 {
-    int sms = 0;
-    cudaError_t e = ssm_sm_count(&sms);
-    if (e != cudaSuccess) return e;
-    q.run = run_of(q.f.S, (q.f.D + 1) / 2 * q.f.N, sms);
+    q.run = run_of(q.f.S, (q.f.D + 1) / 2 * q.f.N, q.f.sms);
     q.parts = q.f.N * run_count(q.f.S, q.run);
-    return cudaSuccess;
 }
 
 cudaError_t launch_ssm_conv_grad(const ConvGradParams& q, cudaStream_t s, int* launches)

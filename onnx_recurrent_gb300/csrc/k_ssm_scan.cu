@@ -476,11 +476,11 @@ cudaError_t by_lanes(const ScanParams& p, cudaStream_t s, int* launches)
 
 int64_t ssm_saved_floats(int64_t S, int64_t N, int64_t D, int64_t M) { return ssm_saved_states(S, N, D, M) + S * N * D; }
 
-ScanChoice ssm_split(const ScanParams& p, int tile, const ScanCost& cost, int sms)
+ScanChoice ssm_split(const ScanParams& p, int tile, const ScanCost& cost)
 {
     const int L = ssm_lanes(p.M), W = L >= 4 ? 4 : L, WC = 32 / L * CH;
     const int64_t dg = p.D / p.G, tiles = (p.S + tile - 1) / tile, blocks = (dg + W * WC - 1) / (W * WC);
-    const double all = (double)blocks * W * p.G * p.N / (4.0 * sms);       // warps per scheduler
+    const double all = (double)blocks * W * p.G * p.N / (4.0 * p.sms);       // warps per scheduler
     auto pass = [&](double w, double steps) {
         const double waves = std::floor(w / cost.warps);
         const int r = (int)std::ceil(w - cost.warps * waves);
@@ -518,14 +518,10 @@ cudaError_t ssm_sm_count(int* sms)
     return e;
 }
 
-cudaError_t ssm_scan_plan(ScanParams& p, size_t* bytes)
+void ssm_scan_plan(ScanParams& p, size_t* bytes)
 {
-    int sms = 0;
-    cudaError_t e = ssm_sm_count(&sms);
-    if (e != cudaSuccess) return e;
-    p.split = ssm_split(p, T, kCost, sms);
+    p.split = ssm_split(p, T, kCost);
     *bytes = sizeof(float) * (size_t)(p.split.chunks - 1) * (size_t)(p.N * p.D * (p.M + 1));
-    return cudaSuccess;
 }
 
 cudaError_t launch_ssm_scan(const ScanParams& p, cudaStream_t s, int* launches)

@@ -847,17 +847,13 @@ cudaError_t by_lanes(const ScanGradParams& p, cudaStream_t s, int* launches)
 
 }  // namespace
 
-cudaError_t ssm_scan_grad_plan(ScanGradParams& pp, size_t* bytes)
+void ssm_scan_grad_plan(ScanGradParams& pp, size_t* bytes)
 {
-    int sms = 0;
-    cudaError_t e = ssm_sm_count(&sms);
-    if (e != cudaSuccess) return e;
     ScanParams& p = pp.f;
-    p.split = ssm_split(p, T, kCost, sms);
+    p.split = ssm_split(p, T, kCost);
     const ScanChoice& c = p.split;
     *bytes = sizeof(float) * (size_t)((c.chunks - 1) * p.N * p.D * (p.M + 1) + c.chunks * p.N * p.D * (p.M + 2) +
                                       c.cblocks * p.N * p.S * p.G * 2 * p.M);
-    return cudaSuccess;
 }
 
 cudaError_t launch_ssm_scan_grad(const ScanGradParams& p, cudaStream_t s, int* launches)

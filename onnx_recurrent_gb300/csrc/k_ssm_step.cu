@@ -183,11 +183,8 @@ template <typename V, int L>
 cudaError_t scan_step_l(const ScanStepParams& p, cudaStream_t s)
 {
     constexpr int ROWS = L >= 4 ? 8 : 4;
-    int sms = 0;
-    const cudaError_t e = ssm_sm_count(&sms);
-    if (e != cudaSuccess) return e;
     const int64_t cb = (p.D + kThreads / L - 1) / (kThreads / L);
-    return cb * (p.N / ROWS) >= sms * 3 ? scan_step_rows<V, L, ROWS>(p, s) : scan_step_rows<V, L, 1>(p, s);
+    return cb * (p.N / ROWS) >= p.sms * 3 ? scan_step_rows<V, L, ROWS>(p, s) : scan_step_rows<V, L, 1>(p, s);
 }
 
 #define BY_LANES(F, V, M, ...)                       \

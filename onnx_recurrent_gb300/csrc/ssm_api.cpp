@@ -22,6 +22,7 @@ struct rnn_ssm {
     int64_t D = 0;
     int M = 0, G = 0, K = 0, layout = 0, silu = 0, softplus = 0, io = RNN_IO_F32;
     int device = -1;              // of the first call: what follows lies there
+    int sms = 0;
     int* status = nullptr;        // device word the kernels report through
     char* scratch = nullptr;
     size_t scratch_bytes = 0;
@@ -203,6 +204,11 @@ rnn_status ensure_status(rnn_ssm* pl)
         cudaFree(p);
         return cuda_fail(e, "cudaMemset(status)");
     }
+    e = ssm_sm_count(&pl->sms);
+    if (e != cudaSuccess) {
+        cudaFree(p);
+        return cuda_fail(e, "reading the device's attributes");
+    }
     pl->status = p;
     pl->device = device;
     return RNN_OK;
@@ -319,6 +325,7 @@ ConvParams conv_params(const rnn_ssm* pl, int64_t S, int64_t N)
     p.K = pl->K;
     p.io = pl->io;
     p.silu = pl->silu;
+    p.sms = pl->sms;
     p.status = pl->status;
     return p;
 }
@@ -333,6 +340,7 @@ ScanParams scan_params(const rnn_ssm* pl, int64_t S, int64_t N)
     p.G = pl->G;
     p.io = pl->io;
     p.softplus = pl->softplus;
+    p.sms = pl->sms;
     p.status = pl->status;
     return p;
 }
@@ -483,8 +491,7 @@ rnn_status rnn_ssm_conv_grad(rnn_ssm_t pl, const rnn_ssm_conv_grad_args* a)
     p.dW = a->dW;
     p.dbias = a->dbias;
     cudaStream_t st = (cudaStream_t)a->stream;
-    cudaError_t e = ssm_conv_grad_plan(p);
-    if (e != cudaSuccess) return cuda_fail(e, "reading the device's attributes");
+    ssm_conv_grad_plan(p);
     const size_t bytes = a->dW || a->dbias ? sizeof(float) * (size_t)p.parts * (size_t)(p.f.D * (p.f.K + 1)) : 0;
     // In place, the blocks of a row's first steps would write what those of its last
     // steps still read: they read a copy, on a 16-byte boundary as the slopes may be.
@@ -493,6 +500,7 @@ rnn_status rnn_ssm_conv_grad(rnn_ssm_t pl, const rnn_ssm_conv_grad_args* a)
     rs = claim_scratch(pl, copy ? at + copy : bytes, st, &scratch);
     if (rs != RNN_OK) return rs;
     p.part = bytes ? (float*)scratch : nullptr;
+    cudaError_t e = cudaSuccess;
     if (copy) {
         e = cudaMemcpyAsync(scratch + at, p.dhT, copy, cudaMemcpyDeviceToDevice, st);
         if (e != cudaSuccess) return cuda_fail(e, "copying d_final_state");
@@ -587,8 +595,8 @@ rnn_status rnn_ssm_scan(rnn_ssm_t pl, const rnn_ssm_scan_args* a)
     p.saved = a->saved;
     cudaStream_t st = (cudaStream_t)a->stream;
     size_t bytes = 0;
-    cudaError_t e = ssm_scan_plan(p, &bytes);
-    if (e != cudaSuccess) return cuda_fail(e, "reading the device's attributes");
+    cudaError_t e = cudaSuccess;
+    ssm_scan_plan(p, &bytes);
     // In place, the last chunk's block would write states that other chunks' blocks
     // still read: they read a copy.  (Unsplit, the thread that writes a state has read it.)
     const size_t copy = p.split.chunks > 1 && p.h0 && p.h0 == p.hT ? states : 0;
@@ -655,8 +663,8 @@ rnn_status rnn_ssm_scan_grad(rnn_ssm_t pl, const rnn_ssm_scan_grad_args* a)
     p.dh0 = a->d_initial_h;
     cudaStream_t st = (cudaStream_t)a->stream;
     size_t bytes = 0;
-    cudaError_t e = ssm_scan_grad_plan(p, &bytes);
-    if (e != cudaSuccess) return cuda_fail(e, "reading the device's attributes");
+    cudaError_t e = cudaSuccess;
+    ssm_scan_grad_plan(p, &bytes);
     // in place, as in the forward run: the first chunk's block would write what the others read
     const size_t copy = p.f.split.chunks > 1 && p.dhT && p.dhT == p.dh0 ? states : 0;
     char* scratch = nullptr;
@@ -702,6 +710,7 @@ rnn_status rnn_ssm_scan_step(rnn_ssm_t pl, const rnn_ssm_scan_step_args* a)
     p.G = pl->G;
     p.io = pl->io;
     p.softplus = pl->softplus;
+    p.sms = pl->sms;
     const int64_t gm = (int64_t)p.G * p.M;
     p.X = dense_row(a->X, p.D);
     p.dt = dense_row(a->dt, p.D);

@@ -31,7 +31,7 @@ constexpr int kMaxTop = 32;
 
 struct ConvParams {
     int64_t S, N, D;
-    int K, io, silu;
+    int K, io, silu, sms;   // sms: the device's multiprocessors, here and below
     View X, Y;
     const float *W, *bias;
     const int32_t* lens;
@@ -71,7 +71,7 @@ struct ScanChoice {
 
 struct ScanParams {
     int64_t S, N, D;
-    int M, G, io, softplus;
+    int M, G, io, softplus, sms;
     View X, dt, B, C, Z, Y;
     const float *A, *Dskip, *dt_bias;
     const int32_t* lens;
@@ -92,7 +92,7 @@ struct ScanGradParams {
 
 struct ScanStepParams {
     int64_t N, D, slots_n;
-    int M, G, io, softplus;
+    int M, G, io, softplus, sms;
     View X, dt, B, C, Z, Y;
     const float *A, *Dskip, *dt_bias, *H;
     float* H_out;
@@ -128,7 +128,7 @@ struct ScanCost {
     int warps;
     double step_ns[5], begin_ns, ends;
 };
-ScanChoice ssm_split(const ScanParams& p, int tile, const ScanCost& cost, int sms);
+ScanChoice ssm_split(const ScanParams& p, int tile, const ScanCost& cost);
 cudaError_t ssm_sm_count(int* sms);
 // Lanes of a channel of M states, four a lane: a power of two.
 inline int ssm_lanes(int M)
@@ -155,13 +155,13 @@ cudaError_t allow_shared(F* kernel, size_t bytes, std::atomic<uint64_t>& done)
 
 // Each launcher queues its kernels on `s` and adds their number to *launches.
 cudaError_t launch_ssm_conv(const ConvParams& p, cudaStream_t s, int* launches);
-cudaError_t ssm_conv_grad_plan(ConvGradParams& p);
+void ssm_conv_grad_plan(ConvGradParams& p);
 cudaError_t launch_ssm_conv_grad(const ConvGradParams& p, cudaStream_t s, int* launches);
 cudaError_t launch_ssm_conv_step(const ConvStepParams& p, cudaStream_t s, int* launches);
 int64_t ssm_saved_floats(int64_t S, int64_t N, int64_t D, int64_t M);
-cudaError_t ssm_scan_plan(ScanParams& p, size_t* bytes);            // the split, and the scratch's size
+void ssm_scan_plan(ScanParams& p, size_t* bytes);            // the split, and the scratch's size
 cudaError_t launch_ssm_scan(const ScanParams& p, cudaStream_t s, int* launches);
-cudaError_t ssm_scan_grad_plan(ScanGradParams& p, size_t* bytes);
+void ssm_scan_grad_plan(ScanGradParams& p, size_t* bytes);
 cudaError_t launch_ssm_scan_grad(const ScanGradParams& p, cudaStream_t s, int* launches);
 cudaError_t launch_ssm_scan_step(const ScanStepParams& p, cudaStream_t s, int* launches);
 cudaError_t launch_scores(const ScoreParams& p, cudaStream_t s, int* launches);

@@ -20,13 +20,13 @@ _TORCH_IO = None
 _lib = None
 # torch and what the calls below use of it, set by _load: a token's call takes a
 # few microseconds in all, so each look-up counts.
-torch = _f32 = _i32 = _empty = _empty_like = _raw_stream = _current_device = None
+torch = _f32 = _i32 = _empty = _empty_like = _raw_stream = _current_device = _one_device = None
 
 Scores = namedtuple("Scores", "logp entropy lse top_ids top_logp")
 
 
 def _load():
-    global _lib, _TORCH_IO, torch, _f32, _i32, _empty, _empty_like, _raw_stream, _current_device
+    global _lib, _TORCH_IO, torch, _f32, _i32, _empty, _empty_like, _raw_stream, _current_device, _one_device
     if _lib is None:
         import torch
         lib = _rnn.load()
@@ -48,6 +48,7 @@ def _load():
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
         _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        _one_device = torch.cuda.device_count() == 1
         _lib = lib
     return _lib
 
@@ -105,9 +106,7 @@ def rnn_ssm_last_launch_count(plan: SSM) -> int:
     return int(_load().rnn_ssm_last_launch_count(plan.handle))
 
 
-def _stream(stream, dev):
-    if stream is None:
-        return _raw_stream(dev)
+def _handle(stream):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -119,13 +118,13 @@ def _onto(stream, device):
     return torch.cuda.stream(stream)
 
 
-def _call(dev, entry, *args):
+def _call(dev, entry, handle, args):
     """An entry point, on the GPU that the call's tensors are on."""
-    if dev == _current_device():
-        status = entry(*args)
+    if _one_device or dev == _current_device():
+        status = entry(handle, args)
     else:
         with torch.cuda.device(dev):
-            status = entry(*args)
+            status = entry(handle, args)
     if status:
         _check(status)
 
@@ -142,9 +141,10 @@ def _bad(t, shape, dtype, dev, name):
 
 def _device(t, name):
     """Index of the GPU that the call's first tensor is on."""
-    if not t.is_cuda:
+    dev = t.get_device()            # negative for the host's
+    if dev < 0:
         raise TypeError(f"{name} must be a CUDA tensor")
-    return t.get_device()
+    return dev
 
 
 def _dense(t, shape, dtype, dev, name):
@@ -223,7 +223,7 @@ def rnn_ssm_conv(plan: SSM, X, W, bias=None, sequence_lens=None, initial_state=N
         "14q", S, N, *_view(X, full, dt, dev, "X", lay), _dense(W, (D, K), f32, dev, "W"),
         _dense(bias, (D,), f32, dev, "bias"), _dense(sequence_lens, (N,), _i32, dev, "sequence_lens"),
         _dense(initial_state, (N, K - 1, D), dt, dev, "initial_state"), *_view(Y, full, dt, dev, "Y", lay),
-        _dense(final_state, (N, K - 1, D), dt, dev, "final_state"), _stream(stream, dev))
+        _dense(final_state, (N, K - 1, D), dt, dev, "final_state"), _raw_stream(dev) if stream is None else _handle(stream))
     _call(dev, _lib.rnn_ssm_conv, plan.handle, args)
 
 
@@ -253,7 +253,7 @@ def rnn_ssm_conv_grad(plan: SSM, dY, X, W, bias=None, sequence_lens=None, initia
         _dense(initial_state, state, dt, dev, "initial_state"), _dense(d_final_state, state, dt, dev, "d_final_state"),
         *_view(dX, full, dt, dev, "dX", lay), _dense(dW, (D, K), f32, dev, "dW"),
         _dense(dbias, (D,), f32, dev, "dbias"), _dense(d_initial_state, state, dt, dev, "d_initial_state"),
-        _stream(stream, dev))
+        _raw_stream(dev) if stream is None else _handle(stream))
     _call(dev, _lib.rnn_ssm_conv_grad, plan.handle, args)
 
 
@@ -286,7 +286,8 @@ def rnn_ssm_conv_step(plan: SSM, X, W, bias, state, Y, state_out=None, slots=Non
         "14q", N, n_slots, *_rows(X, (N, D), dt, dev, "X"), _dense(W, (D, K), _f32, dev, "W"),
         _dense(bias, (D,), _f32, dev, "bias"), at,
         at if state_out is None else _dense(state_out, shape, dt, dev, "state_out"),
-        _dense(slots, (N,), _i32, dev, "slots"), *_rows(Y, (N, D), dt, dev, "Y"), _stream(stream, dev))
+        _dense(slots, (N,), _i32, dev, "slots"), *_rows(Y, (N, D), dt, dev, "Y"),
+        _raw_stream(dev) if stream is None else _handle(stream))
     _call(dev, _lib.rnn_ssm_conv_step, plan.handle, args)
 
 
@@ -317,7 +318,7 @@ def rnn_ssm_scan(plan: SSM, X, dt, A, B, C, D=None, Z=None, dt_bias=None, sequen
         *_view(Y, full, plan.dtype, dev, "Y", plan.layout),
         _dense(Y_h, (N, plan.channels, plan.state_size), _f32, dev, "Y_h"),
         0 if saved is None else _dense(saved, (rnn_ssm_saved_size(plan, S, N),), _f32, dev, "saved"),
-        _stream(stream, dev))
+        _raw_stream(dev) if stream is None else _handle(stream))
     _call(dev, _lib.rnn_ssm_scan, plan.handle, args)
 
 
@@ -352,7 +353,7 @@ def rnn_ssm_scan_grad(plan: SSM, dY, saved, X, dt, A, B, C, D=None, Z=None, dt_b
         *_view(dB, bc, io, dev, "dB", lay), *_view(dC, bc, io, dev, "dC", lay), *_view(dZ, full, io, dev, "dZ", lay),
         _dense(dA, ch + (plan.state_size,), f32, dev, "dA"), _dense(dD, ch, f32, dev, "dD"),
         _dense(ddt_bias, ch, f32, dev, "ddt_bias"), _dense(d_initial_h, st, f32, dev, "d_initial_h"),
-        _stream(stream, dev))
+        _raw_stream(dev) if stream is None else _handle(stream))
     _call(dev, _lib.rnn_ssm_scan_grad, plan.handle, args)
 
 
@@ -393,7 +394,8 @@ def rnn_ssm_scan_step(plan: SSM, X, dt, A, B, C, H, Y, D=None, Z=None, dt_bias=N
         *_rows(Z, full, io, dev, "Z"), _dense(A, (ch, M), f32, dev, "A"), _dense(D, (ch,), f32, dev, "D"),
         _dense(dt_bias, (ch,), f32, dev, "dt_bias"), at,
         at if H_out is None else _dense(H_out, (n_slots, ch, M), f32, dev, "H_out"),
-        _dense(slots, (N,), _i32, dev, "slots"), *_rows(Y, full, io, dev, "Y"), _stream(stream, dev))
+        _dense(slots, (N,), _i32, dev, "slots"), *_rows(Y, full, io, dev, "Y"),
+        _raw_stream(dev) if stream is None else _handle(stream))
     _call(dev, _lib.rnn_ssm_scan_step, plan.handle, args)
 
 
@@ -442,24 +444,33 @@ def _logits(t, name, dtype=None, shape=None, device=None):
     return t.data_ptr(), (t.stride(0) or _SHARED_ROW) if rows > 1 else vocab
 
 
+def _scores(_, args):
+    return _lib.rnn_scores(args)
+
+
+def _scores_grad(_, args):
+    return _lib.rnn_scores_grad(args)
+
+
 def rnn_scores(logits, ids=None, top=0, logp=None, entropy=None, lse=None, top_ids=None, top_logp=None, stream=None):
     """Scores of rows of logits [rows, vocab] into the outputs given; an lse of [2, rows] takes its rounding's rest too."""
-    lib = _load()
+    _load()
     at, stride = _logits(logits, "logits")
     rows, vocab = logits.shape
     dev, f32, i32, top = logits.get_device(), _f32, _i32, int(top)
     lse, pair = _lse(lse, rows, dev)
     args = struct.pack(
         "13q", rows, vocab, stride, _TORCH_IO[logits.dtype] + pair, at, _dense(ids, (rows,), i32, dev, "ids"), top,
-        _dense(logp, (rows,), f32, dev, "logp"), _dense(entropy, (rows,), f32, dev, "entropy"), lse, _dense(top_ids, (rows, top), i32, dev, "top_ids"),
-        _dense(top_logp, (rows, top), f32, dev, "top_logp"), _stream(stream, dev))
-    _call(dev, lib.rnn_scores, args)
+        _dense(logp, (rows,), f32, dev, "logp"), _dense(entropy, (rows,), f32, dev, "entropy"), lse,
+        _dense(top_ids, (rows, top), i32, dev, "top_ids"), _dense(top_logp, (rows, top), f32, dev, "top_logp"),
+        _raw_stream(dev) if stream is None else _handle(stream))
+    _call(dev, _scores, None, args)
 
 
 def scores(logits, ids=None, top=0, stream=None) -> Scores:
     """Scores(logp, entropy, lse, top_ids, top_logp) of rows of logits; logp is
     None without ids, top_ids and top_logp are None for top = 0."""
-    lib = _load()
+    _load()
     if stream is not None:
         with _onto(stream, logits.device):
             return scores(logits, ids, top)
@@ -476,14 +487,14 @@ def scores(logits, ids=None, top=0, stream=None) -> Scores:
         "13q", rows, logits.shape[1], stride, _TORCH_IO[logits.dtype] + _LSE_PAIR, at, ids_at, top,
         r.logp.data_ptr() if ids_at else 0, entropy.data_ptr(), r.lse.data_ptr(), r.top_ids.data_ptr() if top else 0,
         top_logp.data_ptr() if top else 0, _raw_stream(dev))
-    _call(dev, lib.rnn_scores, args)
+    _call(dev, _scores, None, args)
     return r
 
 
 def rnn_scores_grad(logits, ids, result: Scores, d_logp=None, d_entropy=None, d_top=None, dlogits=None, stream=None):
     """Gradient of the scores in the logits into dlogits (which may be logits of rows of their own); ``result`` is
     their Scores."""
-    lib = _load()
+    _load()
     at, stride = _logits(logits, "logits")
     rows, vocab = logits.shape
     d_at, d_stride = _logits(dlogits, "dlogits", logits.dtype, logits.shape, logits.device)
@@ -497,8 +508,9 @@ def rnn_scores_grad(logits, ids, result: Scores, d_logp=None, d_entropy=None, d_
         lse, _dense(result.entropy, (rows,), f32, dev, "entropy"),
         _dense(d_logp, (rows,), f32, dev, "d_logp"), _dense(d_entropy, (rows,), f32, dev, "d_entropy"), top,
         _dense(result.top_ids, (rows, top), _i32, dev, "top_ids") if top else 0,
-        _dense(d_top, (rows, top), f32, dev, "d_top"), d_at, d_stride, _stream(stream, dev))
-    _call(dev, lib.rnn_scores_grad, args)
+        _dense(d_top, (rows, top), f32, dev, "d_top"), d_at, d_stride,
+        _raw_stream(dev) if stream is None else _handle(stream))
+    _call(dev, _scores_grad, None, args)
 
 
 def scores_grad(logits, ids, result: Scores, d_logp=None, d_entropy=None, d_top=None, stream=None):

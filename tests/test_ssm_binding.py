@@ -54,6 +54,7 @@ def calls(monkeypatch):
         current[0] = before
     monkeypatch.setattr(ssm, "_lib", Library())
     monkeypatch.setattr(ssm, "_current_device", lambda: current[0])
+    monkeypatch.setattr(ssm, "_one_device", False)
     monkeypatch.setattr(ssm, "_raw_stream", lambda index: 1000 + index)
     monkeypatch.setattr(torch.cuda, "device", device)
     return seen
