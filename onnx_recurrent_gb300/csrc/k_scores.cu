@@ -36,8 +36,8 @@
 // taking the larger of one and the other reversed, and sorting that.
 //
 // A logit is read once (once more by the gradient, which writes it once).  At 16
-// bits the SMs' issue slots bind before the bytes do: about 11 instructions a
-// logit (conversion, d, 2^d, two sums, the extremes), three quarters of the slots.
+// bits the SMs' issue slots weigh as much as the bytes: about 10 instructions a
+// logit (conversion, d, 2^d, two sums, the extremes), 72 % of the slots.
 // The rows above take 88 us (6.0 TB/s; a copy's rate is 6.8 TB/s), their gradient 178 us
 // (5.9 TB/s), and as many bytes of 32-bit logits, top 8, 102 us (5.1 TB/s).  Tried and
 // no faster: one, three or four 16-byte loads ahead instead of two, copies to a

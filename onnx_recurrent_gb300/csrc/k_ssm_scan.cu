@@ -11,7 +11,7 @@
 //     (shared memory returns 128 bytes a clock, whoever asks for the same);
 //   - channels are packed in pairs (ssm_tile.cuh): half the issue slots;
 //   - delta and delta X are formed once per channel and step, and Y's gate
-//     and rounding applied once, by elementwise passes over tiles of kSsmTile
+//     and rounding applied once, by elementwise passes over tiles of T = 16
 //     steps; the passes and the loop in between share a warp's own part of
 //     shared memory, so a tile costs the block two barriers;
 //   - the sum over a channel's lanes goes with the channels, halving the
@@ -21,7 +21,7 @@
 // The next tile's inputs are copied while a tile is computed.
 //
 // Measured (38 rows of 1024 steps, 2048 channels, M = 16, bf16: all SMs full):
-// 395 us, 3.2 updates a ns, a third of the pipes' bound.  Counters: issue slots
+// 395 us, 3200 updates a ns, a third of the pipes' bound.  Counters: issue slots
 // 59 % busy, fp32 pipe 58 %, shared memory 52 %, exponentials 38 %, DRAM 17 %; with
 // parts left out, the loop over steps takes 64 % of the time (its loads and
 // exchanges half of that), softplus and gate 9 %, copies 7 %, the rest goes to

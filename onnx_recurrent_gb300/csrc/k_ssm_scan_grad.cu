@@ -27,7 +27,7 @@
 // finds the q that each chunk passes on when none enters; with up to kFold
 // chunks a block chains those after its own, with more another launch does.
 //
-// Measured (8 rows of 2048 steps, 2048 channels, M = 16, bf16): 832 us, 0.65 updates
+// Measured (8 rows of 2048 steps, 2048 channels, M = 16, bf16): 832 us, 650 updates
 // a ns with the launch for the chunks' q; 390 instructions for 512 updates, 140 of
 // them packed fp32 ones, 43 exponentials.  Counters with the SMs full: issue slots 38 to
 // 47 % busy, the fp32 pipe 29 to 46 %, shared memory 30 to 36 %, DRAM 11 to 16 %: three warps
