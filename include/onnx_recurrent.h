@@ -631,6 +631,185 @@ typedef struct {
 } rnn_scores_grad_args;
 rnn_status rnn_scores_grad(const rnn_scores_grad_args* args);
 
+/* -------------------------------------------------- gated delta rule
+ * A recurrent layer whose state is a matrix a head, for prompts, training
+ * and single tokens.  With H heads, HK key heads (H / HK neighbouring heads
+ * share a query and a key), DK values a key and DV a value, every row n and head h
+ * run steps t = 0 .. len_n - 1 (len_n = seq_length without sequence_lens):
+ *
+ *   a    = exp(g[t,h])
+ *   u    = beta[t,h] * (V[t,h] - a * S[t-1]^T K[t,hk])      DV values
+ *   S[t] = a * S[t-1] + K[t,hk] u^T                         [DK, DV]
+ *   Y[t,h] = scale * S[t]^T Q[t,hk]
+ *
+ * where S[-1] is initial_state (zeros without one).  Queries and keys are
+ * taken as they are (layers of this kind give them length one beforehand; a key
+ * of length l and beta > 2 / l^2 makes the state grow).  g is the logarithm of the
+ * decay, at most 0 in earnest; below -1000 (-inf too) the state is forgotten.
+ *
+ * Steps t >= len_n write zeros to Y and to every gradient of a step and
+ * leave the state as it was.  Q, K, V, Y and their gradients are stored in
+ * the plan's io type (RNN_IO_*, default F32), each rounded to nearest even
+ * once; g, beta, states and their gradients are fp32, and so are all sums.
+ * Views, streams, scratch, captured calls, in-place states and lengths or slots out of
+ * range are as with rnn_ssm_*; a view's innermost part is [HK, DK] (Q, K),
+ * [H, DV] (V, Y) or [H] (g, beta).  Outputs must not overlap inputs, but for
+ * states given as the same memory. */
+typedef struct rnn_delta* rnn_delta_t;
+
+/* Create a plan (no device work).  heads H > 0; key_heads HK > 0 divides H;
+ * key_size DK in [1, 128]; value_size DV in [1, 1024]; H * DV and HK * DK below
+ * 2^31; layout 0 or 1 (dense views only); scale finite.  Anything else is
+ * RNN_ERR_INVALID_ARGUMENT. */
+rnn_status rnn_delta_create(rnn_delta_t* out, int64_t heads, int64_t key_heads, int64_t key_size, int64_t value_size,
+                            int layout, float scale);
+void rnn_delta_destroy(rnn_delta_t plan);
+rnn_status rnn_delta_set_io_type(rnn_delta_t plan, int io);
+rnn_status rnn_delta_sync(rnn_delta_t plan);
+int rnn_delta_last_launch_count(rnn_delta_t plan);
+/* Floats of `saved` for a run of this size (-1 for invalid arguments). */
+int64_t rnn_delta_saved_size(rnn_delta_t plan, int64_t seq_length, int64_t batch_size);
+
+typedef struct {
+    int64_t seq_length, batch_size;
+    rnn_view Q, K, V, g, beta;
+    const int32_t* sequence_lens;  /* [N], or NULL */
+    const float* initial_state;    /* [N, H, DK, DV], or NULL */
+    rnn_view Y;                    /* out */
+    float* final_state;            /* out [N, H, DK, DV], or NULL; may be initial_state itself */
+    float* saved;                  /* out, rnn_delta_saved_size floats for rnn_delta_rule_grad, or NULL */
+    void* stream;
+} rnn_delta_args;
+rnn_status rnn_delta_rule(rnn_delta_t plan, const rnn_delta_args* args);
+
+/* Gradients: dY (required) and d_final_state (or NULL) are the loss's slopes in
+ * the outputs, `saved` comes from rnn_delta_rule on the same inputs.  dQ, dK,
+ * dV, dg, dbeta and d_initial_state (each may be NULL) are overwritten; dQ and dK
+ * are summed over the heads that share them.  All sums are taken in a fixed
+ * order: the same inputs give the same bits.  d_initial_state may be
+ * d_final_state itself. */
+typedef struct {
+    int64_t seq_length, batch_size;
+    rnn_view dY, Q, K, V, g, beta;
+    const int32_t* sequence_lens;
+    const float* saved;
+    const float* d_final_state;
+    rnn_view dQ, dK, dV, dg, dbeta;
+    float* d_initial_state;
+    void* stream;
+} rnn_delta_grad_args;
+rnn_status rnn_delta_rule_grad(rnn_delta_t plan, const rnn_delta_grad_args* args);
+
+/* One token of each row: views hold [N, ...] (batch_stride, 0: dense).  Row n's
+ * state is state[slots[n]] ([slots, H, DK, DV]; without slots state[n]), the new one
+ * goes to the same slot of state_out, which may be state itself; slots as in
+ * rnn_ssm_conv_step. */
+typedef struct {
+    int64_t batch_size, n_slots;
+    rnn_view Q, K, V, g, beta;
+    const float* state;
+    float* state_out;
+    const int32_t* slots;
+    rnn_view Y;
+    void* stream;
+} rnn_delta_step_args;
+rnn_status rnn_delta_step(rnn_delta_t plan, const rnn_delta_step_args* args);
+
+/* ------------------------------------------------ layer normalisation
+ * Rows x[D]: Y = (x - mean) * rstd * W + bias with mean the row's mean and
+ * rstd = 1 / sqrt(mean of (x - mean)^2 + eps), and its gradients.  X, Y, dY
+ * and dX are stored in the plan's io type (rows row_stride elements apart, 0: D);
+ * W, bias, their gradients and the rows' statistics are fp32, as are all sums.
+ * A row with a NaN or an infinity is NaN throughout.  Streams, scratch and captured
+ * calls are as with rnn_ssm_*. */
+typedef struct rnn_norm* rnn_norm_t;
+/* size D in [1, 32768], eps >= 0 and finite. */
+rnn_status rnn_norm_create(rnn_norm_t* out, int64_t size, float eps);
+void rnn_norm_destroy(rnn_norm_t plan);
+rnn_status rnn_norm_set_io_type(rnn_norm_t plan, int io);
+int rnn_norm_last_launch_count(rnn_norm_t plan);
+typedef struct {
+    int64_t rows;
+    const void* X;
+    int64_t x_stride;
+    const float* W;                /* [D], or NULL: ones */
+    const float* bias;             /* [D], or NULL: zeros */
+    void* Y;                       /* out; may be X itself, with its row stride */
+    int64_t y_stride;
+    float* stats;                  /* out [rows, 2]: mean and rstd for rnn_layer_norm_grad, or NULL */
+    void* stream;
+} rnn_norm_args;
+rnn_status rnn_layer_norm(rnn_norm_t plan, const rnn_norm_args* args);
+/* dX, dW and dbias (each may be NULL) are overwritten; dX may be dY or X
+ * itself, with its row stride.  Sums over rows are taken in a fixed order. */
+typedef struct {
+    int64_t rows;
+    const void* dY;
+    int64_t dy_stride;
+    const void* X;
+    int64_t x_stride;
+    const float* stats;            /* [rows, 2] */
+    const float* W;
+    void* dX;
+    int64_t dx_stride;
+    float* dW;                     /* [D] */
+    float* dbias;                  /* [D] */
+    void* stream;
+} rnn_norm_grad_args;
+rnn_status rnn_layer_norm_grad(rnn_norm_t plan, const rnn_norm_grad_args* args);
+
+/* ------------------------------------------------------- beam search
+ * One step of a search with B beams an item.  rnn_beam_select takes logits of
+ * every beam [items, B, V] and the beams' scores so far; a beam b's
+ * candidates are all tokens v with score[b] + logits[b,v] - lse[b] (lse: the log of the sum of
+ * the beam's exponentials).  A beam that is finished has one candidate, end_id,
+ * with its score as it is, and V - 1 of -inf.  The B best of an item's B * V
+ * candidates, best first, ties to the lowest b and then the lowest v, are the new beams.  A
+ * logit of -inf is a candidate of -inf, and so is every candidate that is a NaN (a row
+ * with a NaN or +inf is all of that).  Scores are added and compared in more than
+ * fp32, and rounded once to it.
+ *
+ * rnn_beam_reorder then gives every beam its parent's states: row n * B + b of
+ * each tensor becomes row n * B + parents[n,b].  With slots, row r is at
+ * slots[r] (slots of a call must differ; -1: no row, which no beam may have for a
+ * parent).  A parent outside [0, B) or a slot outside its range is found by the kernel: that
+ * row is left as it was, and rnn_beam_sync reports RNN_ERR_INVALID_INPUT.
+ * Streams, scratch and captured calls are as with rnn_ssm_*. */
+typedef struct rnn_beam* rnn_beam_t;
+/* beams B in [1, 32]; end_id: the token that ends a beam, -1 for none. */
+rnn_status rnn_beam_create(rnn_beam_t* out, int64_t beams, int64_t end_id);
+void rnn_beam_destroy(rnn_beam_t plan);
+rnn_status rnn_beam_sync(rnn_beam_t plan);
+int rnn_beam_last_launch_count(rnn_beam_t plan);
+typedef struct {
+    int64_t items, vocab, io;      /* io: RNN_IO_* of the logits */
+    const void* logits;            /* rows of V, row_stride elements apart (0: V, RNN_SHARED_ROW: all are one) */
+    int64_t row_stride;
+    int64_t shared;                /* 0: items * B rows; 1: `items` rows, each that of all of an item's beams (a first step) */
+    const float* scores;           /* [items, B] */
+    const uint8_t* finished;       /* [items, B], or NULL */
+    int32_t* parents;              /* out [items, B] */
+    int32_t* ids;                  /* out [items, B] */
+    float* new_scores;             /* out [items, B]; may be scores itself */
+    uint8_t* new_finished;         /* out [items, B] (1 where the parent was or the token is end_id), or NULL;
+                                      may be finished itself */
+    void* stream;
+} rnn_beam_select_args;
+rnn_status rnn_beam_select(rnn_beam_t plan, const rnn_beam_select_args* args);
+typedef struct {
+    const void* in;                /* rows, row_bytes each, one after another */
+    void* out;                     /* may be in itself (an overlap in part is refused) */
+    int64_t row_bytes;
+} rnn_beam_tensor;
+typedef struct {
+    int64_t items, n_tensors, n_slots;
+    const int32_t* parents;        /* [items, B] */
+    const int32_t* slots;          /* [items * B], or NULL */
+    const rnn_beam_tensor* tensors;    /* n_tensors of them, on the host */
+    void* stream;
+} rnn_beam_reorder_args;
+rnn_status rnn_beam_reorder(rnn_beam_t plan, const rnn_beam_reorder_args* args);
+
 /* Message of the last failing call on this thread ("" if none). */
 const char* rnn_last_error(void);
 

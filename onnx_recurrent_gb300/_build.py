@@ -20,9 +20,11 @@ LIB = os.path.join(BUILD, "libonnx_recurrent_gb300.so")
 SOURCES = ["rnn_api.cpp", "k_proj.cu", "k_proj_tc.cu", "k_misc.cu", "k_recur_rnn.cu", "k_recur_gru.cu",
            "k_recur_lstm.cu", "k_recur_tc.cu", "k_cell.cu", "rnn_static.cu", "k_wave_rnn.cu", "k_wave_gru.cu",
            "k_wave_lstm.cu", "k_clus_rnn.cu", "k_clus_gru.cu", "k_clus_lstm.cu", "ssm_api.cpp", "k_ssm_conv.cu", "k_ssm_scan.cu",
-           "k_ssm_scan_grad.cu", "k_ssm_step.cu", "k_scores.cu"]
+           "k_ssm_scan_grad.cu", "k_ssm_step.cu", "k_scores.cu", "delta_api.cpp", "k_delta.cu", "k_delta_grad.cu",
+           "k_delta_step.cu", "norm_api.cpp", "k_norm.cu", "beam_api.cpp", "k_beam.cu"]
 HEADERS = ["rnn_internal.h", "exact_math.cuh", "io_types.cuh", "tma.cuh", "k_recur.cuh", "k_recur2.cuh",
-           "k_wave.cuh", "ssm_internal.h", "plan.h", "ssm_math.cuh", "ssm_tile.cuh"]
+           "k_wave.cuh", "ssm_internal.h", "plan.h", "ssm_math.cuh", "ssm_tile.cuh",
+           "delta_internal.h", "delta_tile.cuh", "norm_internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
                 "-I", os.path.join(ROOT, "include")]

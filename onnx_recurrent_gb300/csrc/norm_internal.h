@@ -1,0 +1,71 @@
+// Shared by the layer normalisation's and beam search's entry points
+// (norm_api.cpp, beam_api.cpp) and kernels.
+#pragma once
+
+#include "ssm_internal.h"
+
+namespace rnngb {
+
+constexpr int kNormMaxSize = 32768;
+constexpr int kMaxBeams = 32;
+constexpr int kReorderTensors = 32;         // of one launch
+
+struct NormParams {
+    int64_t rows;
+    int D, io, sms;
+    float eps;
+    const void* X;
+    int64_t xs;
+    const float *W, *bias;
+    void* Y;
+    int64_t ys;
+    float* stats;           // [rows][2]
+};
+
+struct NormGradParams {
+    NormParams f;           // Y and bias unused
+    const void* dY;
+    int64_t dys;
+    void* dX;
+    int64_t dxs;
+    float *dW, *dbias;
+    float* part;            // [parts][2][D]
+    int64_t parts;          // norm_grad_plan
+};
+
+struct BeamSelectParams {
+    int64_t items, V;
+    int B, io, top;         // top: alternatives a row has, min(B, V)
+    int64_t end;            // -1: none
+    int shared;             // an item's beams have one row
+    int64_t stride;         // between rows of logits
+    const void* logits;
+    const float* lse;       // [2][rows]
+    const int32_t* top_ids; // [rows][top]
+    const float* scores;
+    const uint8_t* finished;
+    int32_t *parents, *ids;
+    float* new_scores;
+    uint8_t* new_finished;
+};
+
+struct ReorderTensor {
+    const void* in;
+    void* out;
+    int64_t bytes;          // of a row
+};
+struct ReorderParams {
+    int64_t items, n_slots;
+    int B, n;
+    const int32_t *parents, *slots;
+    int* status;
+    ReorderTensor t[kReorderTensors];
+};
+
+void norm_grad_plan(NormGradParams& p);
+cudaError_t launch_norm(const NormParams& p, cudaStream_t s, int* launches);
+cudaError_t launch_norm_grad(const NormGradParams& p, cudaStream_t s, int* launches);
+cudaError_t launch_beam_select(const BeamSelectParams& p, cudaStream_t s, int* launches);
+cudaError_t launch_beam_reorder(const ReorderParams& p, cudaStream_t s, int* launches);
+
+}  // namespace rnngb
