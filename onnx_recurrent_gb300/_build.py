@@ -24,7 +24,7 @@ SOURCES = ["rnn_api.cpp", "k_proj.cu", "k_proj_tc.cu", "k_misc.cu", "k_recur_rnn
            "k_delta_step.cu", "norm_api.cpp", "k_norm.cu", "beam_api.cpp", "k_beam.cu"]
 HEADERS = ["rnn_internal.h", "exact_math.cuh", "io_types.cuh", "tma.cuh", "k_recur.cuh", "k_recur2.cuh",
            "k_wave.cuh", "ssm_internal.h", "plan.h", "ssm_math.cuh", "ssm_tile.cuh",
-           "delta_internal.h", "delta_tile.cuh", "norm_internal.h"]
+           "delta_internal.h", "delta_tile.cuh", "delta_mma.cuh", "norm_internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
                 "-I", os.path.join(ROOT, "include")]

@@ -1,0 +1,177 @@
+// Matrix products of the gated delta rule on the tensor cores: operands in
+// fp16 parts, tensor memory, and waits that end.
+//
+// An fp32 operand x is taken as two fp16 parts, hi = fp16(x / s) and lo = fp16(x / s - hi), with s
+// a power of two just above the largest |x| of its row: hi + lo has 22 bits, and
+// what a value far below its row's largest loses is below 2^-24 of that.  A product of two such operands is
+// hi hi + hi lo + lo hi (what is left out is below 2^-22 of it), summed in fp32.  Scales are applied
+// exactly, to a row of the result or, along the sum, to the other operand.  16-bit inputs are one part:
+// fp16 values, and bf16 values over their row's power of two, have no second.
+#pragma once
+
+#include "delta_tile.cuh"
+#include "tma.cuh"
+
+namespace rnngb {
+namespace delta {
+
+constexpr unsigned kBlock = 8192;            // 64 rows of 64 fp16 values, 128-byte swizzle
+
+// Byte of element c of row r in a 64-row block (c < 64).
+__device__ __forceinline__ unsigned swizzled(int r, int c) { return (unsigned)(r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2); }
+
+// A power of two above |m| (within a factor of 2), and one over it; 1 for 0, and both stay ordinary numbers.
+struct Scale {
+    float up, down;
+};
+__device__ __forceinline__ Scale scale_of(float m)
+{
+    int e = (int)((__float_as_uint(m) >> 23) & 255u) + 1;       // biased exponent of the power
+    e = m == 0.f ? 127 : e < 2 ? 2 : e > 252 ? 252 : e;
+    return Scale{__uint_as_float((unsigned)e << 23), __uint_as_float((unsigned)(254 - e) << 23)};
+}
+
+// Two neighbouring values (the first in the low half) as parts.
+__device__ __forceinline__ unsigned half_pair(float a, float b)
+{
+    unsigned v;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(b), "f"(a));
+    return v;
+}
+__device__ __forceinline__ float2 pair_value(unsigned v)
+{
+    const __half2 h = *reinterpret_cast<const __half2*>(&v);
+    return __half22float2(h);
+}
+__device__ __forceinline__ void split_pair(float a, float b, unsigned& hi, unsigned& lo)
+{
+    hi = half_pair(a, b);
+    const float2 h = pair_value(hi);
+    lo = half_pair(a - h.x, b - h.y);
+}
+
+// Shared-memory descriptors of blocks: rows along N (or M) with the sum along the row ("K-major"),
+// 1024 bytes from 8 rows to the next 8; or the sum along the rows ("MN-major"), with
+// `apart` bytes from 64 values of N to the next 64.
+__device__ __forceinline__ uint64_t desc_rows(unsigned saddr)
+{
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)1u << 16 | (uint64_t)(1024u >> 4) << 32 | (uint64_t)1u << 46 | (uint64_t)2u << 61;
+}
+__device__ __forceinline__ uint64_t desc_columns(unsigned saddr, unsigned apart)
+{
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)(apart >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 | (uint64_t)1u << 46 | (uint64_t)2u << 61;
+}
+// Instruction descriptor: fp16 operands, fp32 sums, M = 128; `columns`: B's sum runs along its rows.
+__host__ __device__ constexpr uint32_t instr(int n, bool columns) { return (1u << 4) | (columns ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | (8u << 24); }
+
+// D[128][n] (+)= A[128][16] B[n][16]^T, A in tensor memory.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot, unsigned columns)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t at, unsigned columns)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns) : "memory");
+}
+
+// 32 columns of this thread's lane, and 16 and 32 of them written.
+__device__ __forceinline__ void tmem_ld(uint32_t at, float (&v)[32])
+{
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at)
+        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const unsigned* r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 values of a row over its scale as parts: 16 columns of hi at `hi`, 16 of lo at `lo`.
+__device__ __forceinline__ void put_parts(uint32_t hi, uint32_t lo, const float* v, float down)
+{
+    unsigned h[16], l[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) split_pair(v[2 * i] * down, v[2 * i + 1] * down, h[i], l[i]);
+    tmem_st16(hi, h);
+    tmem_st16(lo, l);
+}
+
+// Waits end after this long; a kernel whose wait gave up says so in its status and returns.
+constexpr long long kWaitNs = 2000000000ll;
+__device__ __forceinline__ bool wait(uint64_t* bar, unsigned parity, volatile int* given_up)
+{
+    if (mbar_test(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer_ns();
+    unsigned it = 0;
+    while (!mbar_test(bar, parity)) {
+        if ((++it & 255u) == 0u) {
+            if (*given_up) return false;
+            if ((long long)(globaltimer_ns() - t0) > kWaitNs) {
+                *given_up = 1;
+                return false;
+            }
+        }
+    }
+    return true;
+}
+
+// Meets `threads` threads at barrier `id` and says whether all of them came with ok.
+__device__ __forceinline__ bool meet(int id, int threads, bool ok)
+{
+    int all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, %2, %3, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"((int)ok), "r"(id), "r"(threads)
+        : "memory");
+    return all != 0;
+}
+
+// A fragment of four 8 x 8 matrices from swizzled rows.
+__device__ __forceinline__ void ld_matrix(unsigned (&r)[4], unsigned saddr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(saddr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_sync(float (&c)[4], const unsigned (&a)[4], unsigned b0, unsigned b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+}  // namespace delta
+}  // namespace rnngb

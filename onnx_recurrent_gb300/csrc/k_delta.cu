@@ -11,16 +11,277 @@
 // which are the steps one after another: (1 + A) U = b (V - e^G K S0) is u's formula with
 // the state written out.  Only S0 -> S1 is a chain; T and P are formed before it
 // for all chunks at once.
-#include "delta_tile.cuh"
+#include "delta_mma.cuh"
 
 namespace rnngb {
 namespace {
 
 using namespace delta;
 
+// What the first launch leaves for the second, as it will lie in shared memory: K and Q of a chunk and key
+// head in KP parts of DKB blocks (64 steps by 64 values each), T and P of a chunk and head in two
+// parts each, and the factors of its steps.
+template <int DKB, int KP>
+struct Images {
+    static constexpr unsigned keys = 2 * KP * DKB * kBlock, mats = 4 * kBlock + 2048;
+    static constexpr int stages = 4 * (keys + mats) <= 220 * 1024 ? 4 : 3 * (keys + mats) <= 220 * 1024 ? 3 : 2;
+    static constexpr size_t smem = stages * (size_t)(keys + mats) + 1024;
+};
+// Factors: of V and of K S0 in b (V - e^G K S0), of U's columns, of U's rows for the state, of Q S0 and of P U
+// in Y (kWhole: e^G_last).  The scales of the rows of K, Q, T and P are in them.
+enum Factor { kBeta = 0, kDecayed = 64, kT = 128, kLast = 192, kQuery = 256, kP = 320, kWhole = 384 };
+
+template <int DKB, int KP>
+struct PrepSmem {
+    unsigned char K[KP * DKB * kBlock], Q[KP * DKB * kBlock];
+    unsigned char P[2 * kBlock];
+    float A[C][C + 1], T[C][C + 1], X[32][33];
+    float ek[C], eq[C], beta[C], fac[512];
+    Sums sums;
+    double carry;
+};
+
+// Rows r and values 4 l .. 4 l + 3 of a chunk of queries or keys, l the lane.
+template <typename T>
+__device__ __forceinline__ void load_four(const View& v, int64_t n, int64_t t, bool in, int64_t at, int d, bool wide, float (&x)[4])
+{
+    const int c = threadIdx.x % 32 * 4;
+    x[0] = x[1] = x[2] = x[3] = 0.f;
+    if (!in || c >= d) return;
+    const T* row = static_cast<const T*>(v.data) + n * v.bs + t * v.ss + at + c;
+    if (wide) {
+        struct alignas(4 * sizeof(T)) Four {
+            T v[4];
+        };
+        const Four q = *reinterpret_cast<const Four*>(row);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = to_f(q.v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c + i < d) x[i] = to_f(row[i]);
+    }
+}
+template <int DKB, int KP>
+__device__ __forceinline__ float put_row(unsigned char* img, int r, const float (&x)[4])
+{
+    float m = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+#pragma unroll
+    for (int o = 16; o; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const Scale s = scale_of(m);
+    const int c = threadIdx.x % 32 * 4;
+    if (c < DKB * 64) {
+        uint2 hi, lo;
+        split_pair(x[0] * s.down, x[1] * s.down, hi.x, lo.x);
+        split_pair(x[2] * s.down, x[3] * s.down, hi.y, lo.y);
+        unsigned char* at = img + c / 64 * kBlock + swizzled(r, c % 64);
+        *reinterpret_cast<uint2*>(at) = hi;
+        if (KP == 2) *reinterpret_cast<uint2*>(at + DKB * kBlock) = lo;
+    }
+    return s.up;
+}
+// Whether rows of d values start on multiples of four of them.
+template <typename T>
+__device__ __forceinline__ bool fours(const View& v, int d)
+{
+    return (uintptr_t)v.data % (4 * sizeof(T)) == 0 && (v.ss | v.bs | d) % 4 == 0;
+}
+
+// T and P, the factors, and K and Q as the second launch wants them.  A block has a chunk of a head.  The two products
+// [K; Q] K^T are small (a twentieth of all); they go through the warps' own matrix instructions.  T is
+// found by blocks: four of 16 by substitution, a thread a column, then twice T21 = -T22 (A21 T11).
+template <typename T, int DKB, int KP>
+__global__ void __launch_bounds__(kThreads) delta_prep_kernel(const DeltaParams p, unsigned char* keys, unsigned char* mats)
+{
+    extern __shared__ __align__(1024) unsigned char raw[];
+    using S = PrepSmem<DKB, KP>;
+    S& s = *reinterpret_cast<S*>(raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u));
+    const int64_t chunk = blockIdx.x, chunks = gridDim.x;
+    const int64_t nh = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
+    if (nh >= p.N * p.H) return;
+    const int64_t n = nh / p.H;
+    const int per = p.H / p.HK, h = (int)(nh - n * p.H), hk = h / per;
+    const int64_t len = row_length(p.lens, n, p.S, p.status), t0 = chunk * C;
+    if (t0 >= len) return;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    {
+        const bool kw = fours<T>(p.K, p.DK), qw = fours<T>(p.Q, p.DK);
+        float k[8][4], q[8][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t t = t0 + warp * 8 + i;
+            load_four<T>(p.K, n, t, t < len, (int64_t)hk * p.DK, p.DK, kw, k[i]);
+            load_four<T>(p.Q, n, t, t < len, (int64_t)hk * p.DK, p.DK, qw, q[i]);
+        }
+        if (tid < C) s.beta[tid] = t0 + tid < len ? static_cast<const float*>(p.beta.data)[n * p.beta.bs + (t0 + tid) * p.beta.ss + h] : 0.f;
+        form_sums(s.sums, p.g, n, h, t0, len, &s.carry);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float ek = put_row<DKB, KP>(s.K, warp * 8 + i, k[i]), eq = put_row<DKB, KP>(s.Q, warp * 8 + i, q[i]);
+            if (lane == 0) s.ek[warp * 8 + i] = ek, s.eq[warp * 8 + i] = eq;
+        }
+    }
+    __syncthreads();
+    if (h % per == 0) {
+        uint4* out = reinterpret_cast<uint4*>(keys + ((n * p.HK + hk) * chunks + chunk) * Images<DKB, KP>::keys);
+        for (int i = tid; i < (int)Images<DKB, KP>::keys / 16; i += kThreads) out[i] = reinterpret_cast<const uint4*>(s.K)[i];
+    }
+    // warps 0 .. 3: 16 rows of K K^T each; 4 .. 7: of Q K^T
+    const int rows = warp % 4 * 16;
+    float c[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
+    const unsigned a0 = smem_addr(warp < 4 ? s.K : s.Q), b0 = smem_addr(s.K);
+#pragma unroll
+    for (int ks = 0; ks < DKB * 4; ++ks) {
+        const unsigned blk = ks / 4 * kBlock;
+        const int col = ks % 4 * 16;
+        unsigned a[KP][4];
+#pragma unroll
+        for (int q = 0; q < KP; ++q)
+            ld_matrix(a[q], a0 + q * DKB * kBlock + blk + swizzled(rows + lane % 16, col + lane / 16 * 8));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {       // 16 columns
+            if (j * 16 > rows) continue;    // above the diagonal
+#pragma unroll
+            for (int q = 0; q < KP; ++q) {
+                unsigned b[4];
+                ld_matrix(b, b0 + q * DKB * kBlock + blk + swizzled(j * 16 + lane % 8 + lane / 16 * 8, col + lane / 8 % 2 * 8));
+#pragma unroll
+                for (int r = 0; r + q < KP; ++r) {
+                    mma_sync(c[2 * j], a[r], b[0], b[1]);
+                    mma_sync(c[2 * j + 1], a[r], b[2], b[3]);
+                }
+            }
+        }
+    }
+    const float* er = warp < 4 ? s.ek : s.eq;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int i = rows + lane / 4 + half * 8;
+        float m = 0.f;
+#pragma unroll
+        for (int j8 = 0; j8 < 8; ++j8)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int j = j8 * 8 + lane % 4 * 2 + e;
+                float v = 0.f;
+                if (j < i || (j == i && warp >= 4)) v = expf(s.sums.between(i, j)) * (c[j8][half * 2 + e] * (er[i] * s.ek[j]));
+                if (warp < 4 && j < i) s.A[i][j] = s.beta[i] * v;
+                c[j8][half * 2 + e] = v;
+                m = fmaxf(m, fabsf(v));
+            }
+        if (warp >= 4) {
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            const Scale sc = scale_of(m);
+            if (lane % 4 == 0) s.fac[kP + i] = p.scale * sc.up;
+#pragma unroll
+            for (int j8 = 0; j8 < 8; ++j8) {
+                unsigned hi, lo;
+                split_pair(c[j8][half * 2] * sc.down, c[j8][half * 2 + 1] * sc.down, hi, lo);
+                unsigned char* at = s.P + swizzled(i, j8 * 8 + lane % 4 * 2);
+                *reinterpret_cast<unsigned*>(at) = hi;
+                *reinterpret_cast<unsigned*>(at + kBlock) = lo;
+            }
+        }
+    }
+    if (tid < C) {
+        const float first = expf(s.sums.hi[tid] + s.sums.lo[tid]);
+        s.fac[kBeta + tid] = s.beta[tid];
+        s.fac[kDecayed + tid] = s.beta[tid] * first * s.ek[tid];
+        s.fac[kLast + tid] = expf(s.sums.between(C - 1, tid)) * s.ek[tid];
+        s.fac[kQuery + tid] = p.scale * first * s.eq[tid];
+        if (tid == C - 1) s.fac[kWhole] = first;
+    }
+    __syncthreads();
+    if (tid < C) {
+        const int b = tid / 16 * 16, j = tid % 16;
+        float t[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            t[i] = i == j ? 1.f : 0.f;
+#pragma unroll
+            for (int m = 0; m < i; ++m) t[i] = fmaf(-s.A[b + i][b + m], t[m], t[i]);
+            s.T[b + i][b + j] = t[i];
+        }
+    }
+    __syncthreads();
+    {   // two pairs of blocks of 16
+        const int at = tid / 128 * 32, i = tid % 128 / 8, j = tid % 8 * 2;
+        float x[2] = {0.f, 0.f};
+#pragma unroll
+        for (int m = 0; m < 16; ++m) {
+            const float a = s.A[at + 16 + i][at + m];
+            x[0] = fmaf(a, s.T[at + m][at + j], x[0]);
+            x[1] = fmaf(a, s.T[at + m][at + j + 1], x[1]);
+        }
+        s.X[at / 2 + i][j] = x[0];
+        s.X[at / 2 + i][j + 1] = x[1];
+        __syncthreads();
+        x[0] = x[1] = 0.f;
+#pragma unroll
+        for (int m = 0; m < 16; ++m) {
+            const float a = -s.T[at + 16 + i][at + 16 + m];
+            x[0] = fmaf(a, s.X[at / 2 + m][j], x[0]);
+            x[1] = fmaf(a, s.X[at / 2 + m][j + 1], x[1]);
+        }
+        s.T[at + 16 + i][at + j] = x[0];
+        s.T[at + 16 + i][at + j + 1] = x[1];
+        s.T[at + i][at + 16 + j] = s.T[at + i][at + 17 + j] = 0.f;
+    }
+    __syncthreads();
+    {   // the two of 32
+        const int i = tid / 8, j = tid % 8 * 4;
+        float x[4] = {};
+#pragma unroll 8
+        for (int m = 0; m < 32; ++m) {
+            const float a = s.A[32 + i][m];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = fmaf(a, s.T[m][j + e], x[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s.X[i][j + e] = x[e], x[e] = 0.f;
+        __syncthreads();
+#pragma unroll 8
+        for (int m = 0; m < 32; ++m) {
+            const float a = -s.T[32 + i][32 + m];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = fmaf(a, s.X[m][j + e], x[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s.T[32 + i][j + e] = x[e], s.T[i][32 + j + e] = 0.f;
+    }
+    __syncthreads();
+    unsigned char* out = mats + (nh * chunks + chunk) * Images<DKB, KP>::mats;
+    {   // T's parts: four threads a row, 16 values each
+        const int i = tid / 4, j = tid % 4 * 16;
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(s.T[i][j + e]));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const Scale sc = scale_of(m);
+        if (tid % 4 == 0) s.fac[kT + i] = sc.up;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            uint4 hi, lo;
+            unsigned* hs = &hi.x;
+            unsigned* ls = &lo.x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split_pair(s.T[i][j + q * 8 + 2 * e] * sc.down, s.T[i][j + q * 8 + 2 * e + 1] * sc.down, hs[e], ls[e]);
+            *reinterpret_cast<uint4*>(out + swizzled(i, j + q * 8)) = hi;
+            *reinterpret_cast<uint4*>(out + kBlock + swizzled(i, j + q * 8)) = lo;
+        }
+    }
+    for (int i = tid; i < (int)(2 * kBlock / 16); i += kThreads) reinterpret_cast<uint4*>(out + 2 * kBlock)[i] = reinterpret_cast<const uint4*>(s.P)[i];
+    __syncthreads();
+    if (tid < 128) reinterpret_cast<float4*>(out + 4 * kBlock)[tid] = reinterpret_cast<const float4*>(s.fac)[tid];
+}
+
 // T and P of every chunk: [N][H][chunks][C][C] each, transposed (for the run) or not (for its
 // gradient, with a third matrix, e^(G_i - G_j) K_i.K_j below the diagonal).
-struct PrepSmem {
+struct GradPrepSmem {
     float KT[kDeltaMaxKey][C + 4], QT[kDeltaMaxKey][C + 4];
     float A[C][C + 1];
     float T[C][C + 1];
@@ -30,10 +291,10 @@ struct PrepSmem {
 };
 
 template <typename T, bool GRAD>
-__global__ void __launch_bounds__(kThreads) delta_prep_kernel(const DeltaParams p, float* mats)
+__global__ void __launch_bounds__(kThreads) delta_grad_prep_kernel(const DeltaParams p, float* mats)
 {
-    extern __shared__ __align__(16) unsigned char raw[];
-    PrepSmem& s = *reinterpret_cast<PrepSmem*>(raw);
+    extern __shared__ __align__(1024) unsigned char raw[];
+    GradPrepSmem& s = *reinterpret_cast<GradPrepSmem*>(raw);
     const int64_t chunk = blockIdx.x, chunks = gridDim.x;
     const int64_t nh = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
     if (nh >= p.N * p.H) return;
@@ -84,129 +345,293 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const DeltaParams 
     for (int i = tid; i < C * C; i += kThreads) outT[i] = GRAD ? s.T[i / C][i % C] : s.T[i % C][i / C];
 }
 
-constexpr int kBV = 32;         // columns of the state that a block has
+// The chain.  A block has 128 columns of a head's state, a lane of tensor memory each: with S^T [value][key], U^T
+// and R^T [value][step] in tensor memory as first operands, every product of a chunk has
+// them on the left and K, Q, T or P, as they lie in shared memory, on the right.
+//   warps 0 .. 7: a thread has half the columns of a lane (32 steps, or half the keys): V, R, U, the state
+//     itself (fp32, in registers), the parts of each, and Y;
+//   warp 8, a lane: issues the products, whose order keeps the tensor cores at work while the others compute:
+//     K S0, half of Q S0, T R, the rest of Q S0, U K, P U;
+//   warp 9, a lane: copies the chunks' images, `stages` of them ahead.
+// A chunk is about 2900 clocks, of which the tensor cores work 2400 (keys of 128): the chain K S0 -> R -> T R
+// -> U -> U K -> S is what bounds it.
+constexpr int kRunThreads = 384;     // warps 10 and 11 are there for the registers' sake (warpgroups of four)
+constexpr unsigned kTmem = 512;
 
-struct RunSmem {
-    float KT[kDeltaMaxKey][C + 4], QT[kDeltaMaxKey][C + 4];
-    float K[C][kDeltaMaxKey + 4];
-    float S[kDeltaMaxKey][kBV];
-    float TT[C][C], PT[C][C];
-    float R[C][kBV], U[C][kBV];
-    Sums sums;
-    float beta[C], first[C], last[C];
-    double carry;
+template <int DKB>
+struct Columns {     // of tensor memory
+    static constexpr uint32_t dS = 0, S = DKB * 64, R = 2 * DKB * 64, U = R + 64, U2 = U + 64, QS = U2 + 64, PU = R;
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) delta_run_kernel(const DeltaParams p, const float* mats)
+template <typename T, int DKB, int KP>
+__global__ void __launch_bounds__(kRunThreads, 1) delta_run_kernel(const DeltaParams p, const unsigned char* keys, const unsigned char* mats)
 {
-    extern __shared__ __align__(16) unsigned char raw[];
-    RunSmem& s = *reinterpret_cast<RunSmem*>(raw);
+    using Im = Images<DKB, KP>;
+    using Co = Columns<DKB>;
+    constexpr int ST = Im::stages, SR = DKB * 32;
+    extern __shared__ __align__(1024) unsigned char raw[];
+    __shared__ __align__(8) uint64_t full[ST], empty[ST], s_ready, d_ready, r_ready, u_ready, up_ready, ds_ready, o_ready, done;
+    __shared__ float most[4][2][128];
+    __shared__ uint32_t slot;
+    __shared__ int given_up;
+    unsigned char* base = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
     const int64_t nh = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
     if (nh >= p.N * p.H) return;
     const int64_t n = nh / p.H, chunks = delta_chunks(p.S);
     const int h = (int)(nh - n * p.H), hk = h / (p.H / p.HK);
-    const int v0 = blockIdx.x * kBV, tid = threadIdx.x;
     const int64_t len = row_length(p.lens, n, p.S, p.status);
-    const int m0 = tid / 16 * 4, d0 = tid / 16 * 8, n0 = tid % 16 * 2;
-    const int DK = p.DK, DV = p.DV;
-    float state[8][2];
-    float* U = p.saved ? p.saved + p.N * p.H * chunks * DK * DV : nullptr;
-#pragma unroll
-    for (int a = 0; a < 8; ++a)
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int d = d0 + a, v = v0 + n0 + b;
-            state[a][b] = p.h0 && d < DK && v < DV ? p.h0[(nh * DK + d) * DV + v] : 0.f;
-            s.S[d][n0 + b] = state[a][b];
+    const int64_t live = (len + C - 1) / C;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 9);
         }
-    for (int i = tid; i < C * (kDeltaMaxKey + 4); i += kThreads) s.K[0][i] = 0.f;
-    for (int64_t chunk = 0; chunk * C < len; ++chunk) {
-        const int64_t t0 = chunk * C;
-        __syncthreads();
-        load_rows<T>(p.K, n, t0, len, (int64_t)hk * DK, DK, s.K[0], kDeltaMaxKey + 4, s.KT[0], C + 4);
-        load_rows<T>(p.Q, n, t0, len, (int64_t)hk * DK, DK, nullptr, 0, s.QT[0], C + 4);
-        const float* m = mats + (nh * chunks + chunk) * 2 * C * C;
-        for (int i = tid; i < C * C; i += kThreads) {
-            s.TT[0][i] = m[i];
-            s.PT[0][i] = m[C * C + i];
-        }
-        if (tid < C)
-            s.beta[tid] = t0 + tid < len ? static_cast<const float*>(p.beta.data)[n * p.beta.bs + (t0 + tid) * p.beta.ss + h] : 0.f;
-        form_sums(s.sums, p.g, n, h, t0, len, &s.carry);
-        if (tid < C) {
-            s.first[tid] = expf(s.sums.hi[tid]);
-            s.last[tid] = expf(s.sums.between(C - 1, tid));
-        }
-        __syncthreads();
-        if (p.saved)
-#pragma unroll
-            for (int a = 0; a < 8; ++a)
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-                    if (d0 + a < DK && v0 + n0 + b < DV)
-                        p.saved[((nh * chunks + chunk) * DK + d0 + a) * DV + v0 + n0 + b] = state[a][b];
-        float ks[4][2], qs[4][2], u[4][2];
-        clear(ks);
-        clear(qs);
-        clear(u);
-        product<4, 2>(ks, s.KT[0] + m0, C + 4, s.S[0] + n0, kBV, DK);
-        product<4, 2>(qs, s.QT[0] + m0, C + 4, s.S[0] + n0, kBV, DK);
-#pragma unroll
-        for (int a = 0; a < 4; ++a)
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int t = m0 + a, v = v0 + n0 + b;
-                const float x = t0 + t < len && v < DV
-                    ? to_f(static_cast<const T*>(p.V.data)[n * p.V.bs + (t0 + t) * p.V.ss + (int64_t)h * DV + v]) : 0.f;
-                s.R[t][n0 + b] = s.beta[t] * (x - s.first[t] * ks[a][b]);
-            }
-        __syncthreads();
-        product<4, 2>(u, s.TT[0] + m0, C, s.R[0] + n0, kBV, C);
-#pragma unroll
-        for (int a = 0; a < 4; ++a)
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                s.U[m0 + a][n0 + b] = u[a][b];
-                if (U && v0 + n0 + b < DV) U[((nh * chunks + chunk) * C + m0 + a) * DV + v0 + n0 + b] = u[a][b];
-            }
-        __syncthreads();
-        clear(ks);
-        product<4, 2>(ks, s.PT[0] + m0, C, s.U[0] + n0, kBV, C);
-#pragma unroll
-        for (int a = 0; a < 4; ++a)
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int t = m0 + a, v = v0 + n0 + b;
-                if (t0 + t < len && v < DV)
-                    static_cast<T*>(p.Y.data)[n * p.Y.bs + (t0 + t) * p.Y.ss + (int64_t)h * DV + v] =
-                        from_f<T>(p.scale * fmaf(s.first[t], qs[a][b], ks[a][b]));
-                s.R[t][n0 + b] = s.last[t] * u[a][b];
-            }
-        __syncthreads();
-        const float whole = s.first[C - 1];
-#pragma unroll
-        for (int a = 0; a < 8; ++a)
-#pragma unroll
-            for (int b = 0; b < 2; ++b) state[a][b] *= whole;
-        product<8, 2>(state, s.K[0] + d0, kDeltaMaxKey + 4, s.R[0] + n0, kBV, C);
-#pragma unroll
-        for (int a = 0; a < 8; ++a)
-#pragma unroll
-            for (int b = 0; b < 2; ++b) s.S[d0 + a][n0 + b] = state[a][b];
+        mbar_init(&s_ready, 8);
+        mbar_init(&d_ready, 1);
+        mbar_init(&r_ready, 8);
+        mbar_init(&u_ready, 1);
+        mbar_init(&up_ready, 8);
+        mbar_init(&ds_ready, 1);
+        mbar_init(&o_ready, 1);
+        mbar_init(&done, 1);
+        given_up = 0;
+        mbar_fence_init();
     }
-    if (p.hT)
+    if (warp == 8) tmem_alloc(&slot, kTmem);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tm = slot;
+    int never = 0;
+    // of 168 registers a thread at launch: 216 for the eight warps that hold the state, 72 for the rest
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 9 && lane == 0) {
+            int64_t k = 0;
+            for (; k < live; ++k) {
+                const int s = (int)(k % ST);
+                if (k >= ST && !wait(&empty[s], (unsigned)(k / ST - 1) & 1u, &given_up)) break;
+                unsigned char* st = base + (size_t)s * (Im::keys + Im::mats);
+                mbar_arrive_expect_tx(&full[s], Im::keys + Im::mats);
+                bulk_g2s(st, keys + ((n * p.HK + hk) * chunks + k) * Im::keys, Im::keys, &full[s]);
+                bulk_g2s(st + Im::keys, mats + (nh * chunks + k) * Im::mats, Im::mats, &full[s]);
+            }
+            // no copy is in flight when the block ends
+            for (int64_t i = k > ST ? k - ST : 0; i < k; ++i) wait(&full[i % ST], (unsigned)(i / ST) & 1u, &never);
+        }
+        if (warp == 8 && lane == 0) {
+            for (int64_t k = 0; k < live; ++k) {
+                const int s = (int)(k % ST);
+                const unsigned ph = (unsigned)k & 1u;
+                if (!wait(&full[s], (unsigned)(k / ST) & 1u, &given_up) || !wait(&s_ready, ph, &given_up)) break;
+                fence_after();
+                const unsigned kimg = smem_addr(base + (size_t)s * (Im::keys + Im::mats)), qimg = kimg + KP * DKB * kBlock;
+                const unsigned timg = kimg + Im::keys, pimg = timg + 2 * kBlock;
+                // parts a of S and b of K or Q, over the keys
+                auto keys_product = [&](uint32_t d, unsigned img, int a, int b, bool add) {
 #pragma unroll
-        for (int a = 0; a < 8; ++a)
+                    for (int ks = 0; ks < DKB * 4; ++ks)
+                        mma_ts(tm + d, tm + Co::S + a * SR + ks * 8, desc_rows(img + (b * DKB + ks / 4) * kBlock + ks % 4 * 32), instr(C, false), add || ks > 0);
+                };
+                // a part of R or U, and a matrix's part, over the steps
+                auto steps_product = [&](uint32_t d, uint32_t from, int a, unsigned img, int b, bool add) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
-                if (d0 + a < DK && v0 + n0 + b < DV) p.hT[(nh * DK + d0 + a) * DV + v0 + n0 + b] = state[a][b];
-    // steps past the row's end
-    for (int64_t i = tid; i < (p.S - len) * kBV; i += kThreads) {
-        const int64_t t = len + i / kBV;
-        const int v = v0 + (int)(i % kBV);
-        if (v < DV) static_cast<T*>(p.Y.data)[n * p.Y.bs + t * p.Y.ss + (int64_t)h * DV + v] = from_f<T>(0.f);
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_ts(tm + d, tm + from + ks / 2 * 32 + a * 16 + ks % 2 * 8, desc_rows(img + b * kBlock + ks * 32), instr(C, false), add || ks > 0);
+                };
+                keys_product(Co::R, kimg, 0, 0, false);
+                keys_product(Co::R, kimg, 1, 0, true);
+                if (KP == 2) keys_product(Co::R, kimg, 0, 1, true);
+                mma_commit(&d_ready);
+                keys_product(Co::QS, qimg, 0, 0, false);
+                if (!wait(&r_ready, ph, &given_up)) break;
+                fence_after();
+                steps_product(Co::U, Co::R, 0, timg, 0, false);
+                steps_product(Co::U, Co::R, 0, timg, 1, true);
+                steps_product(Co::U, Co::R, 1, timg, 0, true);
+                mma_commit(&u_ready);
+                keys_product(Co::QS, qimg, 1, 0, true);
+                if (KP == 2) keys_product(Co::QS, qimg, 0, 1, true);
+                if (!wait(&up_ready, ph, &given_up)) break;
+                fence_after();
+#pragma unroll
+                for (int q = 0; q < 1 + KP; ++q) {      // hi hi, lo hi, hi lo
+                    const int a = q == 1, b = q == 2;
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_ts(tm + Co::dS, tm + Co::U2 + ks / 2 * 32 + a * 16 + ks % 2 * 8,
+                               desc_columns(kimg + b * DKB * kBlock + ks * 2048, kBlock), instr(DKB * 64, true), q > 0 || ks > 0);
+                }
+                mma_commit(&ds_ready);
+                steps_product(Co::PU, Co::U, 0, pimg, 0, false);
+                steps_product(Co::PU, Co::U, 0, pimg, 1, true);
+                steps_product(Co::PU, Co::U, 1, pimg, 0, true);
+                mma_commit(&o_ready);
+                mma_commit(&empty[s]);
+            }
+            mma_commit(&done);
+            wait(&done, 0, &never);
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const int half = warp / 4, row = warp % 4 * 32 + lane;
+        const uint32_t my = tm + ((uint32_t)(warp % 4 * 32) << 16);
+        const int v = blockIdx.x * 128 + row;
+        const bool col = v < p.DV;
+        const int64_t at = nh * p.DK * p.DV + v;         // of this column's state
+        const int d0 = half * SR;                        // its keys: SR from here
+        float S[SR], x[32];
+        T vs[32];
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < SR; ++i) {
+            S[i] = p.h0 && col && d0 + i < p.DK ? p.h0[at + (int64_t)(d0 + i) * p.DV] : 0.f;
+            m = fmaxf(m, fabsf(S[i]));
+        }
+        auto load_v = [&](int64_t k) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const int64_t t = k * C + half * 32 + i;
+                vs[i] = col && t < len ? static_cast<const T*>(p.V.data)[n * p.V.bs + t * p.V.ss + (int64_t)h * p.DV + v] : from_f<T>(0.f);
+            }
+        };
+        // a lane's two threads share a scale; false once any wait gave up
+        auto both = [&](int i, float& m, bool ok) {
+            most[i][half][row] = m;
+            if (!meet(1, 256, ok)) return false;
+            m = fmaxf(m, most[i][1 - half][row]);
+            return true;
+        };
+        auto tell = [&](uint64_t* bar) {
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        auto put_state = [&](float down) {
+#pragma unroll
+            for (int q = 0; q < DKB; ++q)
+                put_parts(my + Co::S + d0 / 2 + q * 16, my + Co::S + SR + d0 / 2 + q * 16, S + q * 32, down);
+            tmem_st_wait();
+        };
+        auto save_state = [&](int64_t k) {
+            if (!p.saved || !col) return;
+            float* to = p.saved + (nh * chunks + k) * p.DK * p.DV + v;
+#pragma unroll
+            for (int i = 0; i < SR; ++i)
+                if (d0 + i < p.DK) to[(int64_t)(d0 + i) * p.DV] = S[i];
+        };
+        load_v(0);
+        bool ok = both(3, m, true);
+        Scale es = scale_of(m);
+        if (live > 0) {
+            put_state(es.down);
+            tell(&s_ready);
+            save_state(0);
+        }
+        for (int64_t k = 0; k < live; ++k) {
+            const int s = (int)(k % ST);
+            const unsigned ph = (unsigned)k & 1u;
+            const float* fac = reinterpret_cast<const float*>(base + (size_t)s * (Im::keys + Im::mats) + Im::keys + 4 * kBlock) + half * 32;
+            ok = __all_sync(0xffffffffu, ok && wait(&full[s], (unsigned)(k / ST) & 1u, &given_up) && wait(&d_ready, ph, &given_up));
+            m = 0.f;
+            if (ok) {
+                fence_after();
+                tmem_ld(my + Co::R + half * 32, x);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    x[i] = fac[kBeta + i] * to_f(vs[i]) - (fac[kDecayed + i] * es.up) * x[i];
+                    m = fmaxf(m, fabsf(x[i]));
+                }
+            }
+            if (!both(0, m, ok)) break;
+            const Scale er = scale_of(m);
+            put_parts(my + Co::R + half * 32, my + Co::R + half * 32 + 16, x, er.down);
+            tmem_st_wait();
+            tell(&r_ready);
+            if (k + 1 < live) load_v(k + 1);
+            ok = __all_sync(0xffffffffu, wait(&u_ready, ph, &given_up));
+            m = 0.f;
+            float m2 = 0.f;
+            if (ok) {
+                fence_after();
+                tmem_ld(my + Co::U + half * 32, x);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    x[i] *= fac[kT + i] * er.up;
+                    m = fmaxf(m, fabsf(x[i]));
+                    m2 = fmaxf(m2, fabsf(x[i] * fac[kLast + i]));
+                }
+                if (p.saved && col) {
+                    float* to = p.saved + p.N * p.H * chunks * p.DK * p.DV + ((nh * chunks + k) * C + half * 32) * p.DV + v;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) to[(int64_t)i * p.DV] = x[i];
+                }
+            }
+            most[1][half][row] = m;
+            if (!both(2, m2, ok)) break;
+            m = fmaxf(m, most[1][1 - half][row]);
+            const Scale eu = scale_of(m), e2 = scale_of(m2);
+            put_parts(my + Co::U + half * 32, my + Co::U + half * 32 + 16, x, eu.down);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] *= fac[kLast + i];
+            put_parts(my + Co::U2 + half * 32, my + Co::U2 + half * 32 + 16, x, e2.down);
+            tmem_st_wait();
+            tell(&up_ready);
+            ok = __all_sync(0xffffffffu, wait(&ds_ready, ph, &given_up));
+            m = 0.f;
+            const Scale old = es;
+            if (ok) {
+                fence_after();
+                const float w = fac[kWhole - half * 32];
+#pragma unroll
+                for (int q = 0; q < DKB; ++q) {
+                    tmem_ld(my + Co::dS + d0 + q * 32, x);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        S[q * 32 + i] = fmaf(e2.up, x[i], w * S[q * 32 + i]);
+                        m = fmaxf(m, fabsf(S[q * 32 + i]));
+                    }
+                }
+            }
+            if (!both(3, m, ok)) break;
+            es = scale_of(m);
+            if (k + 1 < live) put_state(es.down);
+            ok = __all_sync(0xffffffffu, wait(&o_ready, ph, &given_up));
+            if (ok) {
+                fence_after();
+                float y[32];
+                tmem_ld(my + Co::QS + half * 32, x);
+                tmem_ld(my + Co::PU + half * 32, y);
+                if (k + 1 < live) tell(&s_ready);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int64_t t = k * C + half * 32 + i;
+                    const float o = fac[kQuery + i] * old.up * x[i] + fac[kP + i] * eu.up * y[i];
+                    if (col && t < len) static_cast<T*>(p.Y.data)[n * p.Y.bs + t * p.Y.ss + (int64_t)h * p.DV + v] = from_f<T>(o);
+                }
+                if (k + 1 < live) save_state(k + 1);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[s]);
+        }
+        if (p.hT && col)
+#pragma unroll
+            for (int i = 0; i < SR; ++i)
+                if (d0 + i < p.DK) p.hT[at + (int64_t)(d0 + i) * p.DV] = S[i];
+        // steps past the row's end
+        if (col)
+            for (int64_t t = len + half; t < p.S; t += 2)
+                static_cast<T*>(p.Y.data)[n * p.Y.bs + t * p.Y.ss + (int64_t)h * p.DV + v] = from_f<T>(0.f);
     }
+    fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        fence_after();
+        tmem_free(tm, kTmem);
+    }
+    if (threadIdx.x == 0 && given_up) *p.status = 6;        // RNN_ERR_TIMEOUT
 }
 
 // Rows and heads over y and z of a grid.
@@ -216,30 +641,45 @@ dim3 heads_grid(int64_t x, int64_t nh)
     return dim3((unsigned)x, (unsigned)y, (unsigned)((nh + y - 1) / y));
 }
 
+int64_t keys_bytes(const DeltaParams& p)
+{
+    return p.N * p.HK * delta_chunks(p.S) * 2 * (p.io == 0 ? 2 : 1) * ((p.DK + 63) / 64) * (int64_t)kBlock;
+}
+
+template <typename T, int DKB>
+cudaError_t run(const DeltaParams& p, cudaStream_t st, int* launches)
+{
+    constexpr int KP = sizeof(T) == 4 ? 2 : 1;
+    constexpr size_t prep_smem = sizeof(PrepSmem<DKB, KP>) + 1024, run_smem = Images<DKB, KP>::smem;
+    static std::atomic<uint64_t> prep_done{0}, run_done{0};
+    cudaError_t e = allow_shared(delta_prep_kernel<T, DKB, KP>, prep_smem, prep_done);
+    if (e == cudaSuccess) e = allow_shared(delta_run_kernel<T, DKB, KP>, run_smem, run_done);
+    if (e != cudaSuccess) return e;
+    const int64_t nh = p.N * p.H;
+    unsigned char* keys = reinterpret_cast<unsigned char*>(p.scratch);
+    unsigned char* mats = keys + keys_bytes(p);
+    if (p.S > 0) {
+        delta_prep_kernel<T, DKB, KP><<<heads_grid(delta_chunks(p.S), nh), kThreads, prep_smem, st>>>(p, keys, mats);
+        ++*launches;
+    }
+    delta_run_kernel<T, DKB, KP><<<heads_grid((p.DV + 127) / 128, nh), kRunThreads, run_smem, st>>>(p, keys, mats);
+    ++*launches;
+    return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t run(const DeltaParams& p, cudaStream_t st, int* launches)
 {
-    static std::atomic<uint64_t> prep_done{0}, run_done{0};
-    cudaError_t e = allow_shared(delta_prep_kernel<T, false>, sizeof(PrepSmem), prep_done);
-    if (e == cudaSuccess) e = allow_shared(delta_run_kernel<T>, sizeof(RunSmem), run_done);
-    if (e != cudaSuccess) return e;
-    const int64_t nh = p.N * p.H;
-    if (p.S > 0) {
-        delta_prep_kernel<T, false><<<heads_grid(delta_chunks(p.S), nh), kThreads, sizeof(PrepSmem), st>>>(p, p.scratch);
-        ++*launches;
-    }
-    delta_run_kernel<T><<<heads_grid((p.DV + kBV - 1) / kBV, nh), kThreads, sizeof(RunSmem), st>>>(p, p.scratch);
-    ++*launches;
-    return cudaGetLastError();
+    return p.DK > 64 ? run<T, 2>(p, st, launches) : run<T, 1>(p, st, launches);
 }
 
 template <typename T>
 cudaError_t prep_grad(const DeltaParams& p, float* mats, cudaStream_t st, int* launches)
 {
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_shared(delta_prep_kernel<T, true>, sizeof(PrepSmem), done);
+    cudaError_t e = allow_shared(delta_grad_prep_kernel<T, true>, sizeof(GradPrepSmem), done);
     if (e != cudaSuccess) return e;
-    delta_prep_kernel<T, true><<<heads_grid(delta_chunks(p.S), p.N * p.H), kThreads, sizeof(PrepSmem), st>>>(p, mats);
+    delta_grad_prep_kernel<T, true><<<heads_grid(delta_chunks(p.S), p.N * p.H), kThreads, sizeof(GradPrepSmem), st>>>(p, mats);
     ++*launches;
     return cudaGetLastError();
 }
@@ -248,7 +688,7 @@ cudaError_t prep_grad(const DeltaParams& p, float* mats, cudaStream_t st, int* l
 
 size_t delta_scratch_bytes(const DeltaParams& p)
 {
-    return sizeof(float) * (size_t)(p.N * p.H * delta_chunks(p.S)) * 2 * C * C;
+    return (size_t)keys_bytes(p) + (size_t)(p.N * p.H * delta_chunks(p.S)) * Images<1, 1>::mats;
 }
 
 cudaError_t launch_delta(const DeltaParams& p, cudaStream_t s, int* launches)

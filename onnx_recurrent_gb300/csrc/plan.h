@@ -262,6 +262,7 @@ inline rnn_status read_status(PlanMemory* pl, const char* invalid_input)
     }
     if (current != pl->device) cudaSetDevice(current);
     if (e != cudaSuccess) return cuda_fail(e, "reading the status");
+    if (word == RNN_ERR_TIMEOUT) return fail(RNN_ERR_TIMEOUT, "a kernel gave up waiting for its own copies or products");
     if (word) return fail(RNN_ERR_INVALID_INPUT, "%s", invalid_input);
     return RNN_OK;
 }
