@@ -10,6 +10,7 @@
 #pragma once
 
 #include "delta_tile.cuh"
+#include "ssm_tile.cuh"
 #include "tma.cuh"
 
 namespace rnngb {
@@ -64,6 +65,14 @@ __device__ __forceinline__ uint64_t desc_columns(unsigned saddr, unsigned apart)
 // Instruction descriptor: fp16 operands, fp32 sums, M = 128; `columns`: B's sum runs along its rows.
 __host__ __device__ constexpr uint32_t instr(int n, bool columns) { return (1u << 4) | (columns ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | (8u << 24); }
 
+// One lane of a converged warp.  Products are issued by a whole warp of which one lane acts: operands
+// then stay in uniform registers (33 clocks a product of 128 x 64 x 16; by a lone lane, 45).
+__device__ __forceinline__ bool elected()
+{
+    unsigned v;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(v));
+    return v != 0;
+}
 // D[128][n] (+)= A[128][16] B[n][16]^T, A in tensor memory.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
 {
@@ -90,7 +99,7 @@ __device__ __forceinline__ void tmem_free(uint32_t at, unsigned columns)
 }
 
 // 32 columns of this thread's lane, and 16 and 32 of them written.
-__device__ __forceinline__ void tmem_ld(uint32_t at, float (&v)[32])
+__device__ __forceinline__ void tmem_ld(uint32_t at, f2 (&v)[16])
 {
     uint32_t r[32];
     asm volatile(
@@ -104,7 +113,7 @@ __device__ __forceinline__ void tmem_ld(uint32_t at, float (&v)[32])
         : "memory");
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < 16; ++i) v[i] = pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t at, const unsigned* r)
 {
@@ -117,12 +126,22 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const unsigned* r)
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 32 values of a row over its scale as parts: 16 columns of hi at `hi`, 16 of lo at `lo`.
-__device__ __forceinline__ void put_parts(uint32_t hi, uint32_t lo, const float* v, float down)
+// 32 values of a row over its scale, |v| down < 1, as parts: 16 columns of hi at `hi`, 16 of lo at `lo`.  hi is rounded to
+// a multiple of 2^-11 (in the last place of 1.5 2^12), which fp16 holds exactly, so pairs of values
+// take three packed operations and two conversions; lo is then off by 2^-25 at most.
+__device__ __forceinline__ void put_parts(uint32_t hi, uint32_t lo, const f2* v, float down)
 {
     unsigned h[16], l[16];
+    const f2 d = dup2(down), m = dup2(6144.f), mm = dup2(-6144.f), minus = dup2(-1.f);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) split_pair(v[2 * i] * down, v[2 * i + 1] * down, h[i], l[i]);
+    for (int i = 0; i < 16; ++i) {
+        const f2 a = add2(fma2(v[i], d, m), mm);
+        float x, y;
+        unpack2(a, x, y);
+        h[i] = half_pair(x, y);
+        unpack2(fma2(v[i], d, mul2(a, minus)), x, y);
+        l[i] = half_pair(x, y);
+    }
     tmem_st16(hi, h);
     tmem_st16(lo, l);
 }

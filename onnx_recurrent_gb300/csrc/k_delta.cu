@@ -11,6 +11,8 @@
 // which are the steps one after another: (1 + A) U = b (V - e^G K S0) is u's formula with
 // the state written out.  Only S0 -> S1 is a chain; T and P are formed before it
 // for all chunks at once.
+#include <type_traits>
+
 #include "delta_mma.cuh"
 
 namespace rnngb {
@@ -24,8 +26,6 @@ using namespace delta;
 template <int DKB, int KP>
 struct Images {
     static constexpr unsigned keys = 2 * KP * DKB * kBlock, mats = 4 * kBlock + 2048;
-    static constexpr int stages = 4 * (keys + mats) <= 220 * 1024 ? 4 : 3 * (keys + mats) <= 220 * 1024 ? 3 : 2;
-    static constexpr size_t smem = stages * (size_t)(keys + mats) + 1024;
 };
 // Factors: of V and of K S0 in b (V - e^G K S0), of U's columns, of U's rows for the state, of Q S0 and of P U
 // in Y (kWhole: e^G_last).  The scales of the rows of K, Q, T and P are in them.
@@ -350,12 +350,12 @@ __global__ void __launch_bounds__(kThreads) delta_grad_prep_kernel(const DeltaPa
 // them on the left and K, Q, T or P, as they lie in shared memory, on the right.
 //   warps 0 .. 7: a thread has half the columns of a lane (32 steps, or half the keys): V, R, U, the state
 //     itself (fp32, in registers), the parts of each, and Y;
-//   warp 8, a lane: issues the products, whose order keeps the tensor cores at work while the others compute:
+//   warp 8: issues the products, whose order keeps the tensor cores at work while the others compute:
 //     K S0, half of Q S0, T R, the rest of Q S0, U K, P U;
-//   warp 9, a lane: copies the chunks' images, `stages` of them ahead.
-// A chunk is about 2900 clocks, of which the tensor cores work 2400 (keys of 128): the chain K S0 -> R -> T R
-// -> U -> U K -> S is what bounds it.
-constexpr int kRunThreads = 384;     // warps 10 and 11 are there for the registers' sake (warpgroups of four)
+//   warp 9: copies the chunks' images, `stages` of them ahead;
+//   warps 10, 11 (16-bit types): a step a thread, lay V out by columns before it is wanted and write Y's rows, 16
+//     bytes at a time where they are aligned.
+constexpr int kRunThreads = 384;
 constexpr unsigned kTmem = 512;
 
 template <int DKB>
@@ -363,30 +363,79 @@ struct Columns {     // of tensor memory
     static constexpr uint32_t dS = 0, S = DKB * 64, R = 2 * DKB * 64, U = R + 64, U2 = U + 64, QS = U2 + 64, PU = R;
 };
 
+// V and Y of a chunk by columns: 64 steps of 16 bits and 16 bytes more, so that threads' 16-byte accesses spread over all banks.
+constexpr int kPitch = 144;
+constexpr unsigned kSheet = 128 * kPitch;
+template <typename T, int DKB, int KP>
+struct RunSmem {
+    static constexpr bool staged = sizeof(T) == 2;
+    static constexpr unsigned stage = Images<DKB, KP>::keys + Images<DKB, KP>::mats;
+    static constexpr int stages = 2;
+    static constexpr size_t bytes = stages * (size_t)stage + (staged ? 3 * kSheet : 0) + 1024;
+};
+
+template <typename T>
+__device__ __forceinline__ f2 pair_of(unsigned raw);
+template <>
+__device__ __forceinline__ f2 pair_of<__nv_bfloat16>(unsigned raw) { return pack2(__uint_as_float(raw << 16), __uint_as_float(raw & 0xffff0000u)); }
+template <>
+__device__ __forceinline__ f2 pair_of<__half>(unsigned raw)
+{
+    const float2 v = pair_value(raw);
+    return pack2(v.x, v.y);
+}
+template <typename T>
+__device__ __forceinline__ unsigned raw_pair(f2 v)
+{
+    float a, b;
+    unpack2(v, a, b);
+    if (sizeof(T) == 4) return 0;
+    unsigned r;
+    if constexpr (std::is_same_v<T, __nv_bfloat16>) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    else r = half_pair(a, b);
+    return r;
+}
+__device__ __forceinline__ float most_of(float m, f2 v)
+{
+    float a, b;
+    unpack2(v, a, b);
+    return fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+}
+
 template <typename T, int DKB, int KP>
 __global__ void __launch_bounds__(kRunThreads, 1) delta_run_kernel(const DeltaParams p, const unsigned char* keys, const unsigned char* mats)
 {
     using Im = Images<DKB, KP>;
     using Co = Columns<DKB>;
-    constexpr int ST = Im::stages, SR = DKB * 32;
+    using Sm = RunSmem<T, DKB, KP>;
+    constexpr int ST = Sm::stages, SR = DKB * 32;
     extern __shared__ __align__(1024) unsigned char raw[];
-    __shared__ __align__(8) uint64_t full[ST], empty[ST], s_ready, d_ready, r_ready, u_ready, up_ready, ds_ready, o_ready, done;
+    __shared__ __align__(8) uint64_t full[ST], empty[ST], v_full[2], v_empty[2], y_full, y_empty;
+    __shared__ __align__(8) uint64_t s_ready, d_ready, r_ready, u_ready, up_ready, ds_ready, o_ready, done;
     __shared__ float most[4][2][128];
     __shared__ uint32_t slot;
     __shared__ int given_up;
     unsigned char* base = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+    unsigned char* sheets = base + ST * Sm::stage;       // V, V, Y
     const int64_t nh = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
     if (nh >= p.N * p.H) return;
     const int64_t n = nh / p.H, chunks = delta_chunks(p.S);
     const int h = (int)(nh - n * p.H), hk = h / (p.H / p.HK);
     const int64_t len = row_length(p.lens, n, p.S, p.status);
-    const int64_t live = (len + C - 1) / C;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int live = (int)((len + C - 1) / C);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, v0 = blockIdx.x * 128;
+    const int cols = p.DV - v0 < 128 ? p.DV - v0 : 128;
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 9);
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&v_full[i], 2);
+            mbar_init(&v_empty[i], 8);
+        }
+        mbar_init(&y_full, 8);
+        mbar_init(&y_empty, 2);
         mbar_init(&s_ready, 8);
         mbar_init(&d_ready, 1);
         mbar_init(&r_ready, 8);
@@ -402,99 +451,176 @@ __global__ void __launch_bounds__(kRunThreads, 1) delta_run_kernel(const DeltaPa
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tm = slot;
+    const uint32_t tm = __shfl_sync(0xffffffffu, slot, 0);
     int never = 0;
     // of 168 registers a thread at launch: 216 for the eight warps that hold the state, 72 for the rest
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 9 && lane == 0) {
-            int64_t k = 0;
+            int k = 0;
             for (; k < live; ++k) {
-                const int s = (int)(k % ST);
+                const int s = k % ST;
                 if (k >= ST && !wait(&empty[s], (unsigned)(k / ST - 1) & 1u, &given_up)) break;
-                unsigned char* st = base + (size_t)s * (Im::keys + Im::mats);
-                mbar_arrive_expect_tx(&full[s], Im::keys + Im::mats);
+                unsigned char* st = base + s * Sm::stage;
+                mbar_arrive_expect_tx(&full[s], Sm::stage);
                 bulk_g2s(st, keys + ((n * p.HK + hk) * chunks + k) * Im::keys, Im::keys, &full[s]);
                 bulk_g2s(st + Im::keys, mats + (nh * chunks + k) * Im::mats, Im::mats, &full[s]);
             }
             // no copy is in flight when the block ends
-            for (int64_t i = k > ST ? k - ST : 0; i < k; ++i) wait(&full[i % ST], (unsigned)(i / ST) & 1u, &never);
+            for (int i = k > ST ? k - ST : 0; i < k; ++i) wait(&full[i % ST], (unsigned)(i / ST) & 1u, &never);
         }
-        if (warp == 8 && lane == 0) {
-            for (int64_t k = 0; k < live; ++k) {
-                const int s = (int)(k % ST);
+        if (warp == 8) {
+            const bool leader = elected();
+            const unsigned sbase = __shfl_sync(0xffffffffu, smem_addr(base), 0);
+            for (int k = 0; k < live; ++k) {
+                const int s = k % ST;
                 const unsigned ph = (unsigned)k & 1u;
-                if (!wait(&full[s], (unsigned)(k / ST) & 1u, &given_up) || !wait(&s_ready, ph, &given_up)) break;
+                if (!__all_sync(0xffffffffu, wait(&full[s], (unsigned)(k / ST) & 1u, &given_up) && wait(&s_ready, ph, &given_up))) break;
                 fence_after();
-                const unsigned kimg = smem_addr(base + (size_t)s * (Im::keys + Im::mats)), qimg = kimg + KP * DKB * kBlock;
+                const unsigned kimg = sbase + s * Sm::stage, qimg = kimg + KP * DKB * kBlock;
                 const unsigned timg = kimg + Im::keys, pimg = timg + 2 * kBlock;
                 // parts a of S and b of K or Q, over the keys
                 auto keys_product = [&](uint32_t d, unsigned img, int a, int b, bool add) {
 #pragma unroll
                     for (int ks = 0; ks < DKB * 4; ++ks)
-                        mma_ts(tm + d, tm + Co::S + a * SR + ks * 8, desc_rows(img + (b * DKB + ks / 4) * kBlock + ks % 4 * 32), instr(C, false), add || ks > 0);
+                        if (leader)
+                            mma_ts(tm + d, tm + Co::S + a * SR + ks * 8, desc_rows(img + (b * DKB + ks / 4) * kBlock + ks % 4 * 32), instr(C, false), add || ks > 0);
                 };
                 // a part of R or U, and a matrix's part, over the steps
                 auto steps_product = [&](uint32_t d, uint32_t from, int a, unsigned img, int b, bool add) {
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        mma_ts(tm + d, tm + from + ks / 2 * 32 + a * 16 + ks % 2 * 8, desc_rows(img + b * kBlock + ks * 32), instr(C, false), add || ks > 0);
+                        if (leader)
+                            mma_ts(tm + d, tm + from + ks / 2 * 32 + a * 16 + ks % 2 * 8, desc_rows(img + b * kBlock + ks * 32), instr(C, false), add || ks > 0);
                 };
                 keys_product(Co::R, kimg, 0, 0, false);
                 keys_product(Co::R, kimg, 1, 0, true);
                 if (KP == 2) keys_product(Co::R, kimg, 0, 1, true);
-                mma_commit(&d_ready);
+                if (leader) mma_commit(&d_ready);
                 keys_product(Co::QS, qimg, 0, 0, false);
-                if (!wait(&r_ready, ph, &given_up)) break;
+                if (!__all_sync(0xffffffffu, wait(&r_ready, ph, &given_up))) break;
                 fence_after();
                 steps_product(Co::U, Co::R, 0, timg, 0, false);
                 steps_product(Co::U, Co::R, 0, timg, 1, true);
                 steps_product(Co::U, Co::R, 1, timg, 0, true);
-                mma_commit(&u_ready);
+                if (leader) mma_commit(&u_ready);
                 keys_product(Co::QS, qimg, 1, 0, true);
                 if (KP == 2) keys_product(Co::QS, qimg, 0, 1, true);
-                if (!wait(&up_ready, ph, &given_up)) break;
+                if (!__all_sync(0xffffffffu, wait(&up_ready, ph, &given_up))) break;
                 fence_after();
 #pragma unroll
-                for (int q = 0; q < 1 + KP; ++q) {      // hi hi, lo hi, hi lo
-                    const int a = q == 1, b = q == 2;
+                for (int q = 0; q < 1 + KP; ++q)        // hi hi, lo hi, hi lo
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        mma_ts(tm + Co::dS, tm + Co::U2 + ks / 2 * 32 + a * 16 + ks % 2 * 8,
-                               desc_columns(kimg + b * DKB * kBlock + ks * 2048, kBlock), instr(DKB * 64, true), q > 0 || ks > 0);
-                }
-                mma_commit(&ds_ready);
+                        if (leader)
+                            mma_ts(tm + Co::dS, tm + Co::U2 + ks / 2 * 32 + (q == 1) * 16 + ks % 2 * 8,
+                                   desc_columns(kimg + (q == 2) * DKB * kBlock + ks * 2048, kBlock), instr(DKB * 64, true), q > 0 || ks > 0);
+                if (leader) mma_commit(&ds_ready);
                 steps_product(Co::PU, Co::U, 0, pimg, 0, false);
                 steps_product(Co::PU, Co::U, 0, pimg, 1, true);
                 steps_product(Co::PU, Co::U, 1, pimg, 0, true);
-                mma_commit(&o_ready);
-                mma_commit(&empty[s]);
+                if (leader) {
+                    mma_commit(&o_ready);
+                    mma_commit(&empty[s]);
+                }
             }
-            mma_commit(&done);
+            if (leader) mma_commit(&done);
             wait(&done, 0, &never);
+        }
+        if constexpr (Sm::staged)
+        if (warp >= 10) {
+            const int t = threadIdx.x - 320;
+            const T* from = static_cast<const T*>(p.V.data) + n * p.V.bs + (int64_t)h * p.DV + v0;
+            T* to = static_cast<T*>(p.Y.data) + n * p.Y.bs + (int64_t)h * p.DV + v0;
+            const bool vw = (uintptr_t)from % 16 == 0 && p.V.ss % 8 == 0, yw = (uintptr_t)to % 16 == 0 && p.Y.ss % 8 == 0;
+            auto load_v = [&](int k) {
+                unsigned short* sheet = reinterpret_cast<unsigned short*>(sheets + (k & 1) * kSheet) + t;
+                const int64_t step = (int64_t)k * C + t;
+                const bool in = step < len;
+                const T* row = from + step * p.V.ss;
+#pragma unroll 1
+                for (int c0 = 0; c0 < 128; c0 += 64) {
+                    uint4 x[8];         // all on their way at once
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const int c = c0 + 8 * q;
+                        x[q] = make_uint4(0, 0, 0, 0);
+                        if (in && vw && c + 8 <= cols) {
+                            x[q] = *reinterpret_cast<const uint4*>(row + c);
+                        } else if (in && c < cols) {
+                            const unsigned short* one = reinterpret_cast<const unsigned short*>(row) + c;
+                            unsigned* pairs = &x[q].x;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (c + e < cols) pairs[e / 2] |= (unsigned)one[e] << (e % 2 * 16);
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const unsigned pairs[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) sheet[(c0 + 8 * q + e) * (kPitch / 2)] = (unsigned short)(pairs[e / 2] >> (e % 2 * 16));
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&v_full[k & 1]);
+            };
+            if (live > 0) load_v(0);
+            for (int k = 0; k < live; ++k) {
+                if (k + 1 < live) {
+                    if (k >= 1 && !__all_sync(0xffffffffu, wait(&v_empty[(k + 1) & 1], (unsigned)((k - 1) / 2) & 1u, &given_up))) break;
+                    load_v(k + 1);
+                }
+                if (!__all_sync(0xffffffffu, wait(&y_full, (unsigned)k & 1u, &given_up))) break;
+                const unsigned short* sheet = reinterpret_cast<const unsigned short*>(sheets + 2 * kSheet) + t;
+                const int64_t step = (int64_t)k * C + t;
+                unsigned short* row = reinterpret_cast<unsigned short*>(to + step * p.Y.ss);
+                if (step < len)
+#pragma unroll 4
+                    for (int c = 0; c < cols; c += 8) {
+                        unsigned short x[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = sheet[(c + e) * (kPitch / 2)];
+                        if (yw && c + 8 <= cols) {
+                            *reinterpret_cast<uint4*>(row + c) = make_uint4(x[0] | (unsigned)x[1] << 16, x[2] | (unsigned)x[3] << 16,
+                                                                            x[4] | (unsigned)x[5] << 16, x[6] | (unsigned)x[7] << 16);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (c + e < cols) row[c + e] = x[e];
+                        }
+                    }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&y_empty);
+            }
         }
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int half = warp / 4, row = warp % 4 * 32 + lane;
         const uint32_t my = tm + ((uint32_t)(warp % 4 * 32) << 16);
-        const int v = blockIdx.x * 128 + row;
+        const int v = v0 + row;
         const bool col = v < p.DV;
         const int64_t at = nh * p.DK * p.DV + v;         // of this column's state
         const int d0 = half * SR;                        // its keys: SR from here
-        float S[SR], x[32];
-        T vs[32];
+        f2 S[SR / 2], x[16];
+        T vs[Sm::staged ? 1 : 32];
         float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < SR; ++i) {
-            S[i] = p.h0 && col && d0 + i < p.DK ? p.h0[at + (int64_t)(d0 + i) * p.DV] : 0.f;
-            m = fmaxf(m, fabsf(S[i]));
-        }
-        auto load_v = [&](int64_t k) {
+        for (int i = 0; i < SR / 2; ++i) {
+            float a[2];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int64_t t = k * C + half * 32 + i;
-                vs[i] = col && t < len ? static_cast<const T*>(p.V.data)[n * p.V.bs + t * p.V.ss + (int64_t)h * p.DV + v] : from_f<T>(0.f);
+            for (int e = 0; e < 2; ++e) a[e] = p.h0 && col && d0 + 2 * i + e < p.DK ? p.h0[at + (int64_t)(d0 + 2 * i + e) * p.DV] : 0.f;
+            S[i] = pack2(a[0], a[1]);
+            m = most_of(m, S[i]);
+        }
+        auto load_v = [&](int k) {
+            if constexpr (!Sm::staged) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int64_t t = (int64_t)k * C + half * 32 + i;
+                    vs[i] = col && t < len ? static_cast<const T*>(p.V.data)[n * p.V.bs + t * p.V.ss + (int64_t)h * p.DV + v] : from_f<T>(0.f);
+                }
             }
         };
         // a lane's two threads share a scale; false once any wait gave up
@@ -512,37 +638,123 @@ __global__ void __launch_bounds__(kRunThreads, 1) delta_run_kernel(const DeltaPa
         auto put_state = [&](float down) {
 #pragma unroll
             for (int q = 0; q < DKB; ++q)
-                put_parts(my + Co::S + d0 / 2 + q * 16, my + Co::S + SR + d0 / 2 + q * 16, S + q * 32, down);
+                put_parts(my + Co::S + d0 / 2 + q * 16, my + Co::S + SR + d0 / 2 + q * 16, S + q * 16, down);
             tmem_st_wait();
         };
-        auto save_state = [&](int64_t k) {
-            if (!p.saved || !col) return;
-            float* to = p.saved + (nh * chunks + k) * p.DK * p.DV + v;
+        auto write_state = [&](float* to) {
+            to += (int64_t)d0 * p.DV;
 #pragma unroll
-            for (int i = 0; i < SR; ++i)
-                if (d0 + i < p.DK) to[(int64_t)(d0 + i) * p.DV] = S[i];
+            for (int i = 0; i < SR / 2; ++i) {
+                float a[2];
+                unpack2(S[i], a[0], a[1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (d0 + 2 * i + e < p.DK) *to = a[e];
+                    to += p.DV;
+                }
+            }
         };
+        Scale es{1.f, 1.f}, eu{1.f, 1.f}, e2{1.f, 1.f};
+        bool ok = true;
         load_v(0);
-        bool ok = both(3, m, true);
-        Scale es = scale_of(m);
-        if (live > 0) {
-            put_state(es.down);
-            tell(&s_ready);
-            save_state(0);
-        }
-        for (int64_t k = 0; k < live; ++k) {
-            const int s = (int)(k % ST);
-            const unsigned ph = (unsigned)k & 1u;
-            const float* fac = reinterpret_cast<const float*>(base + (size_t)s * (Im::keys + Im::mats) + Im::keys + 4 * kBlock) + half * 32;
-            ok = __all_sync(0xffffffffu, ok && wait(&full[s], (unsigned)(k / ST) & 1u, &given_up) && wait(&d_ready, ph, &given_up));
+        // A round ends chunk k - 1 (its state, then its Y) and begins chunk k: the state's parts go out before Y is formed.
+        for (int k = 0; k <= live; ++k) {
+            const int s = k % ST, sp = (k + ST - 1) % ST;
+            const unsigned ph = (unsigned)k & 1u, php = ph ^ 1u;
+            const float* stage = reinterpret_cast<const float*>(base + s * Sm::stage + Im::keys + 4 * kBlock) + half * 32;
+            const float* before = reinterpret_cast<const float*>(base + sp * Sm::stage + Im::keys + 4 * kBlock) + half * 32;
+            auto factors = [](const float* fac, int which, int i) { return *reinterpret_cast<const ulonglong2*>(fac + which + 4 * i); };
+            f2 y[16];
+            const Scale old = es;
+            if (k > 0) {
+                ok = __all_sync(0xffffffffu, wait(&ds_ready, php, &given_up));
+                m = 0.f;
+                if (ok) {
+                    fence_after();
+                    const f2 w = dup2(before[kWhole - half * 32]), up = dup2(e2.up);
+#pragma unroll
+                    for (int q = 0; q < DKB; ++q) {
+                        tmem_ld(my + Co::dS + d0 + q * 32, x);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            S[q * 16 + i] = fma2(up, x[i], mul2(w, S[q * 16 + i]));
+                            m = most_of(m, S[q * 16 + i]);
+                        }
+                    }
+                }
+            }
+            if (k < live) {
+                if (!both(3, m, ok)) break;
+                es = scale_of(m);
+                put_state(es.down);
+            }
+            if (k > 0) {
+                ok = __all_sync(0xffffffffu, ok && wait(&o_ready, php, &given_up));
+                if (ok) {
+                    fence_after();
+                    tmem_ld(my + Co::QS + half * 32, x);
+                    tmem_ld(my + Co::PU + half * 32, y);
+                }
+            }
+            if (k < live) tell(&s_ready);
+            if (k > 0) {
+                if constexpr (Sm::staged)
+                    if (k > 1) ok = __all_sync(0xffffffffu, ok && wait(&y_empty, ph, &given_up));
+                if (ok) {
+                    const f2 qs = dup2(old.up), pu = dup2(eu.up);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const ulonglong2 a = factors(before, kQuery, i), b = factors(before, kP, i);
+                        x[2 * i] = fma2(mul2(a.x, qs), x[2 * i], mul2(mul2(b.x, pu), y[2 * i]));
+                        x[2 * i + 1] = fma2(mul2(a.y, qs), x[2 * i + 1], mul2(mul2(b.y, pu), y[2 * i + 1]));
+                    }
+                    if constexpr (Sm::staged) {
+                        uint4* sheet = reinterpret_cast<uint4*>(sheets + 2 * kSheet + row * kPitch + half * 64);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            sheet[i] = make_uint4(raw_pair<T>(x[4 * i]), raw_pair<T>(x[4 * i + 1]), raw_pair<T>(x[4 * i + 2]), raw_pair<T>(x[4 * i + 3]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int64_t t = (int64_t)(k - 1) * C + half * 32 + i;
+                            float a[2];
+                            unpack2(x[i / 2], a[0], a[1]);
+                            if (col && t < len) static_cast<T*>(p.Y.data)[n * p.Y.bs + t * p.Y.ss + (int64_t)h * p.DV + v] = from_f<T>(a[i % 2]);
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (Sm::staged) mbar_arrive(&y_full);
+                    mbar_arrive(&empty[sp]);
+                }
+            }
+            if (k == live) break;
+            if (p.saved && col) write_state(p.saved + (nh * chunks + k) * p.DK * p.DV + v);
+            ok = ok && wait(&full[s], (unsigned)(k / ST) & 1u, &given_up);
+            if constexpr (Sm::staged) ok = ok && wait(&v_full[k & 1], (unsigned)(k / 2) & 1u, &given_up);
+            ok = __all_sync(0xffffffffu, ok && wait(&d_ready, ph, &given_up));
             m = 0.f;
             if (ok) {
                 fence_after();
                 tmem_ld(my + Co::R + half * 32, x);
+                const f2 minus = dup2(-es.up);
+                const uint4* sheet = reinterpret_cast<const uint4*>(sheets + (k & 1) * kSheet + row * kPitch + half * 64);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    x[i] = fac[kBeta + i] * to_f(vs[i]) - (fac[kDecayed + i] * es.up) * x[i];
-                    m = fmaxf(m, fabsf(x[i]));
+                for (int i = 0; i < 8; ++i) {
+                    const ulonglong2 a = factors(stage, kBeta, i), b = factors(stage, kDecayed, i);
+                    f2 w0, w1;
+                    if constexpr (Sm::staged) {
+                        const uint4 raw4 = sheet[i / 2];
+                        w0 = pair_of<T>(i % 2 ? raw4.z : raw4.x);
+                        w1 = pair_of<T>(i % 2 ? raw4.w : raw4.y);
+                    } else {
+                        w0 = pack2(to_f(vs[4 * i]), to_f(vs[4 * i + 1]));
+                        w1 = pack2(to_f(vs[4 * i + 2]), to_f(vs[4 * i + 3]));
+                    }
+                    x[2 * i] = fma2(a.x, w0, mul2(mul2(b.x, minus), x[2 * i]));
+                    x[2 * i + 1] = fma2(a.y, w1, mul2(mul2(b.y, minus), x[2 * i + 1]));
+                    m = most_of(most_of(m, x[2 * i]), x[2 * i + 1]);
                 }
             }
             if (!both(0, m, ok)) break;
@@ -550,6 +762,8 @@ __global__ void __launch_bounds__(kRunThreads, 1) delta_run_kernel(const DeltaPa
             put_parts(my + Co::R + half * 32, my + Co::R + half * 32 + 16, x, er.down);
             tmem_st_wait();
             tell(&r_ready);
+            if constexpr (Sm::staged)
+                if (lane == 0) mbar_arrive(&v_empty[k & 1]);
             if (k + 1 < live) load_v(k + 1);
             ok = __all_sync(0xffffffffu, wait(&u_ready, ph, &given_up));
             m = 0.f;
@@ -557,69 +771,40 @@ __global__ void __launch_bounds__(kRunThreads, 1) delta_run_kernel(const DeltaPa
             if (ok) {
                 fence_after();
                 tmem_ld(my + Co::U + half * 32, x);
+                const f2 up = dup2(er.up);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    x[i] *= fac[kT + i] * er.up;
-                    m = fmaxf(m, fabsf(x[i]));
-                    m2 = fmaxf(m2, fabsf(x[i] * fac[kLast + i]));
-                }
-                if (p.saved && col) {
-                    float* to = p.saved + p.N * p.H * chunks * p.DK * p.DV + ((nh * chunks + k) * C + half * 32) * p.DV + v;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) to[(int64_t)i * p.DV] = x[i];
+                for (int i = 0; i < 8; ++i) {
+                    const ulonglong2 a = factors(stage, kT, i), b = factors(stage, kLast, i);
+                    x[2 * i] = mul2(x[2 * i], mul2(a.x, up));
+                    x[2 * i + 1] = mul2(x[2 * i + 1], mul2(a.y, up));
+                    y[2 * i] = mul2(x[2 * i], b.x);
+                    y[2 * i + 1] = mul2(x[2 * i + 1], b.y);
+                    m = most_of(most_of(m, x[2 * i]), x[2 * i + 1]);
+                    m2 = most_of(most_of(m2, y[2 * i]), y[2 * i + 1]);
                 }
             }
             most[1][half][row] = m;
             if (!both(2, m2, ok)) break;
             m = fmaxf(m, most[1][1 - half][row]);
-            const Scale eu = scale_of(m), e2 = scale_of(m2);
+            eu = scale_of(m), e2 = scale_of(m2);
+            put_parts(my + Co::U2 + half * 32, my + Co::U2 + half * 32 + 16, y, e2.down);
             put_parts(my + Co::U + half * 32, my + Co::U + half * 32 + 16, x, eu.down);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] *= fac[kLast + i];
-            put_parts(my + Co::U2 + half * 32, my + Co::U2 + half * 32 + 16, x, e2.down);
             tmem_st_wait();
             tell(&up_ready);
-            ok = __all_sync(0xffffffffu, wait(&ds_ready, ph, &given_up));
-            m = 0.f;
-            const Scale old = es;
-            if (ok) {
-                fence_after();
-                const float w = fac[kWhole - half * 32];
+            if (p.saved && col) {
+                float* to = p.saved + p.N * p.H * chunks * p.DK * p.DV + ((nh * chunks + k) * C + half * 32) * p.DV + v;
 #pragma unroll
-                for (int q = 0; q < DKB; ++q) {
-                    tmem_ld(my + Co::dS + d0 + q * 32, x);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        S[q * 32 + i] = fmaf(e2.up, x[i], w * S[q * 32 + i]);
-                        m = fmaxf(m, fabsf(S[q * 32 + i]));
-                    }
+                for (int i = 0; i < 16; ++i) {
+                    float a, b;
+                    unpack2(x[i], a, b);
+                    *to = a;
+                    to += p.DV;
+                    *to = b;
+                    to += p.DV;
                 }
             }
-            if (!both(3, m, ok)) break;
-            es = scale_of(m);
-            if (k + 1 < live) put_state(es.down);
-            ok = __all_sync(0xffffffffu, wait(&o_ready, ph, &given_up));
-            if (ok) {
-                fence_after();
-                float y[32];
-                tmem_ld(my + Co::QS + half * 32, x);
-                tmem_ld(my + Co::PU + half * 32, y);
-                if (k + 1 < live) tell(&s_ready);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int64_t t = k * C + half * 32 + i;
-                    const float o = fac[kQuery + i] * old.up * x[i] + fac[kP + i] * eu.up * y[i];
-                    if (col && t < len) static_cast<T*>(p.Y.data)[n * p.Y.bs + t * p.Y.ss + (int64_t)h * p.DV + v] = from_f<T>(o);
-                }
-                if (k + 1 < live) save_state(k + 1);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[s]);
         }
-        if (p.hT && col)
-#pragma unroll
-            for (int i = 0; i < SR; ++i)
-                if (d0 + i < p.DK) p.hT[at + (int64_t)(d0 + i) * p.DV] = S[i];
+        if (p.hT && col) write_state(p.hT + at);
         // steps past the row's end
         if (col)
             for (int64_t t = len + half; t < p.S; t += 2)
@@ -650,7 +835,7 @@ template <typename T, int DKB>
 cudaError_t run(const DeltaParams& p, cudaStream_t st, int* launches)
 {
     constexpr int KP = sizeof(T) == 4 ? 2 : 1;
-    constexpr size_t prep_smem = sizeof(PrepSmem<DKB, KP>) + 1024, run_smem = Images<DKB, KP>::smem;
+    constexpr size_t prep_smem = sizeof(PrepSmem<DKB, KP>) + 1024, run_smem = RunSmem<T, DKB, KP>::bytes;
     static std::atomic<uint64_t> prep_done{0}, run_done{0};
     cudaError_t e = allow_shared(delta_prep_kernel<T, DKB, KP>, prep_smem, prep_done);
     if (e == cudaSuccess) e = allow_shared(delta_run_kernel<T, DKB, KP>, run_smem, run_done);
