@@ -93,6 +93,21 @@ DeltaParams params(const rnn_delta* pl, int64_t S, int64_t N)
     return p;
 }
 
+// The parts of what a run saves.
+void place(DeltaParams& p, void* saved)
+{
+    p.keys = static_cast<unsigned char*>(saved);
+    p.mats = p.keys + delta_keys_bytes(p.S, p.N, p.HK, p.DK, p.io);
+    p.states = reinterpret_cast<float*>(p.mats + delta_mats_bytes(p.S, p.N, p.H));
+    p.us = p.states + p.N * p.H * delta_chunks(p.S) * p.DK * p.DV;
+}
+
+rnn_status check_saved(const void* saved)
+{
+    if ((uintptr_t)saved % 16) return fail(RNN_ERR_INVALID_ARGUMENT, "saved is not aligned to 16 bytes");
+    return RNN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -151,7 +166,7 @@ int rnn_delta_last_launch_count(rnn_delta_t pl) { return pl ? pl->launches : 0; 
 int64_t rnn_delta_saved_size(rnn_delta_t pl, int64_t S, int64_t N)
 {
     if (!pl || S < 0 || N < 0) return -1;
-    return delta_saved_floats(S, N, pl->H, pl->DK, pl->DV);
+    return delta_saved_floats(S, N, pl->H, pl->HK, pl->DK, pl->DV, pl->io);
 }
 
 rnn_status rnn_delta_rule(rnn_delta_t pl, const rnn_delta_args* a)
@@ -164,8 +179,8 @@ rnn_status rnn_delta_rule(rnn_delta_t pl, const rnn_delta_args* a)
     rs = check_all({{&a->Q, "Q", steps, e}, {&a->K, "K", steps, e}, {&a->V, "V", steps, e}, {&a->g, "g", steps, 4},
                     {&a->beta, "beta", steps, 4}, {&a->Y, "Y", steps, e}});
     if (rs == RNN_OK)
-        rs = check_arrays({{a->sequence_lens, "sequence_lens"}, {a->initial_state, "initial_state"}, {a->final_state, "final_state"},
-                           {a->saved, "saved"}});
+        rs = check_arrays({{a->sequence_lens, "sequence_lens"}, {a->initial_state, "initial_state"}, {a->final_state, "final_state"}});
+    if (rs == RNN_OK) rs = check_saved(a->saved);
     const int64_t S = a->seq_length, N = a->batch_size, dk = pl->HK * pl->DK, dv = pl->H * pl->DV;
     const View Y = dense(a->Y, pl, S, N, dv);
     if (rs == RNN_OK) rs = check_apart(S, N, {{Y, dv, "Y"}});
@@ -184,13 +199,13 @@ rnn_status rnn_delta_rule(rnn_delta_t pl, const rnn_delta_args* a)
     p.lens = a->sequence_lens;
     p.h0 = a->initial_state;
     p.hT = a->final_state;
-    p.saved = a->saved;
     cudaStream_t st = (cudaStream_t)a->stream;
-    const size_t bytes = delta_scratch_bytes(p);
+    const size_t bytes = a->saved ? 0 : (size_t)(delta_keys_bytes(S, N, p.HK, p.DK, p.io) + delta_mats_bytes(S, N, p.H));
     char* scratch = nullptr;
     rs = claim_scratch(pl, bytes, st, &scratch);
     if (rs != RNN_OK) return rs;
-    p.scratch = (float*)scratch;
+    place(p, a->saved ? (void*)a->saved : scratch);
+    if (!a->saved) p.states = p.us = nullptr;
     cudaError_t err = launch_delta(p, st, &pl->launches);
     if (err != cudaSuccess) return cuda_fail(err, "delta rule launch");
     return release_scratch(pl, bytes, st);
@@ -208,7 +223,8 @@ rnn_status rnn_delta_rule_grad(rnn_delta_t pl, const rnn_delta_grad_args* a)
                     {&a->dV, "dV", false, e}, {&a->dg, "dg", false, 4}, {&a->dbeta, "dbeta", false, 4}});
     if (rs != RNN_OK) return rs;
     if (steps) NEED(a->saved, "saved");
-    rs = check_arrays({{a->sequence_lens, "sequence_lens"}, {a->saved, "saved"}, {a->d_final_state, "d_final_state"}, {a->d_initial_state, "d_initial_state"}});
+    rs = check_saved(a->saved);
+    if (rs == RNN_OK) rs = check_arrays({{a->sequence_lens, "sequence_lens"}, {a->d_final_state, "d_final_state"}, {a->d_initial_state, "d_initial_state"}});
     if (rs != RNN_OK) return rs;
     const int64_t S = a->seq_length, N = a->batch_size, H = pl->H, dk = pl->HK * pl->DK, dv = H * pl->DV;
     DeltaGradParams q{};
@@ -229,16 +245,17 @@ rnn_status rnn_delta_rule_grad(rnn_delta_t pl, const rnn_delta_grad_args* a)
     q.f.g = dense(a->g, pl, S, N, H);
     q.f.beta = dense(a->beta, pl, S, N, H);
     q.f.lens = a->sequence_lens;
-    q.f.saved = const_cast<float*>(a->saved);
+    place(q.f, const_cast<float*>(a->saved));
     q.dY = dense(a->dY, pl, S, N, dv);
     q.dhT = a->d_final_state;
     q.dh0 = a->d_initial_state;
     cudaStream_t st = (cudaStream_t)a->stream;
-    const size_t bytes = delta_grad_scratch_bytes(q);
+    const size_t bytes = sizeof(float) * (size_t)delta_grad_scratch_floats(S, N, H, pl->DK, pl->DV);
     char* scratch = nullptr;
     rs = claim_scratch(pl, bytes, st, &scratch);
     if (rs != RNN_OK) return rs;
-    q.f.scratch = (float*)scratch;
+    q.ends = (float*)scratch;
+    q.drs = q.ends + N * H * delta_chunks(S) * pl->DK * pl->DV;
     cudaError_t err = launch_delta_grad(q, st, &pl->launches);
     if (err != cudaSuccess) return cuda_fail(err, "delta rule gradient launch");
     return release_scratch(pl, bytes, st);

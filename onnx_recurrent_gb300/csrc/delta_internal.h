@@ -18,8 +18,8 @@ struct DeltaParams {
     const int32_t* lens;
     const float* h0;        // [N, H, DK, DV]
     float* hT;
-    float* saved;           // delta_saved_floats, or NULL
-    float* scratch;         // delta_scratch_bytes
+    unsigned char *keys, *mats;     // what the chunks' first launch leaves (delta_mma.cuh: Images)
+    float *states, *us;     // the state before every chunk, [N, H, chunks, DK, DV], and u, [N, H, chunks, C, DV]; NULL: not kept
     int* status;
 };
 
@@ -28,6 +28,7 @@ struct DeltaGradParams {
     View dY, dQ, dK, dV, dg, dbeta;
     const float* dhT;
     float* dh0;
+    float *ends, *drs;      // scratch: the slope in the state after every chunk, and dR, as states and us
 };
 
 struct DeltaStepParams {
@@ -42,14 +43,22 @@ struct DeltaStepParams {
 };
 
 __host__ __device__ inline int64_t delta_chunks(int64_t S) { return (S + kDeltaChunk - 1) / kDeltaChunk; }
-// What a run saves for its gradient: the state before every chunk, [N][H][chunks][DK][DV],
-// then the steps' u, [N][H][chunks][kDeltaChunk][DV].
-inline int64_t delta_saved_floats(int64_t S, int64_t N, int64_t H, int64_t DK, int64_t DV)
+// The images of a run's chunks (delta_mma.cuh), and what a run saves for its gradient: them, the states
+// before the chunks, and u.
+constexpr int64_t kDeltaBlock = 8192, kDeltaMats = 4 * kDeltaBlock + 3072;
+inline int64_t delta_keys_bytes(int64_t S, int64_t N, int64_t HK, int64_t DK, int io)
+{
+    return N * HK * delta_chunks(S) * 2 * (io == 0 ? 2 : 1) * ((DK + 63) / 64) * kDeltaBlock;
+}
+inline int64_t delta_mats_bytes(int64_t S, int64_t N, int64_t H) { return N * H * delta_chunks(S) * kDeltaMats; }
+inline int64_t delta_saved_floats(int64_t S, int64_t N, int64_t H, int64_t HK, int64_t DK, int64_t DV, int io)
+{
+    return (delta_keys_bytes(S, N, HK, DK, io) + delta_mats_bytes(S, N, H)) / 4 + N * H * delta_chunks(S) * (DK + kDeltaChunk) * DV;
+}
+inline int64_t delta_grad_scratch_floats(int64_t S, int64_t N, int64_t H, int64_t DK, int64_t DV)
 {
     return N * H * delta_chunks(S) * (DK + kDeltaChunk) * DV;
 }
-size_t delta_scratch_bytes(const DeltaParams& p);
-size_t delta_grad_scratch_bytes(const DeltaGradParams& p);
 
 cudaError_t launch_delta(const DeltaParams& p, cudaStream_t s, int* launches);
 cudaError_t launch_delta_grad(const DeltaGradParams& p, cudaStream_t s, int* launches);

@@ -9,6 +9,8 @@
 // fp16 values, and bf16 values over their row's power of two, have no second.
 #pragma once
 
+#include <type_traits>
+
 #include "delta_tile.cuh"
 #include "ssm_tile.cuh"
 #include "tma.cuh"
@@ -82,6 +84,17 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
+// The same with A in shared memory (K-major).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+// What threads wrote to shared memory is read by products and copies after this and a barrier.
+__device__ __forceinline__ void fence_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void mma_commit(uint64_t* bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -114,6 +127,20 @@ __device__ __forceinline__ void tmem_ld(uint32_t at, f2 (&v)[16])
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t at, float (&v)[16])
+{
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at)
+        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void tmem_st16(uint32_t at, const unsigned* r)
 {
@@ -190,6 +217,171 @@ __device__ __forceinline__ void mma_sync(float (&c)[4], const unsigned (&a)[4], 
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+
+// What the first launch leaves for the second, as it will lie in shared memory: K and Q of a chunk and key
+// head in KP parts of DKB blocks (64 steps by 64 values each; a block of Q follows its block of K), T
+// and P of a chunk and head in two parts each, and the factors of its steps.
+template <int DKB, int KP>
+struct Images {
+    static constexpr unsigned keys = 2 * KP * DKB * kBlock, mats = kDeltaMats;
+};
+// Factors: of V and of K S0 in b (V - e^G K S0), of U's columns, of U's rows for the state, of Q S0 and of P U
+// in Y (kWhole: e^G_last).  The scales of the rows of K, Q, T and P are in them; those of K and Q also stand alone.
+enum Factor { kBeta = 0, kDecayed = 64, kT = 128, kLast = 192, kQuery = 256, kP = 320, kKeyScale = 384, kQueryScale = 448, kWhole = 512 };
+
+// Rows r and values 4 l .. 4 l + 3 of a chunk of queries or keys, l the lane.
+template <typename T>
+__device__ __forceinline__ void load_four(const View& v, int64_t n, int64_t t, bool in, int64_t at, int d, bool wide, float (&x)[4])
+{
+    const int c = threadIdx.x % 32 * 4;
+    x[0] = x[1] = x[2] = x[3] = 0.f;
+    if (!in || c >= d) return;
+    const T* row = static_cast<const T*>(v.data) + n * v.bs + t * v.ss + at + c;
+    if (wide) {
+        struct alignas(4 * sizeof(T)) Four {
+            T v[4];
+        };
+        const Four q = *reinterpret_cast<const Four*>(row);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = to_f(q.v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c + i < d) x[i] = to_f(row[i]);
+    }
+}
+// The largest of a row of 128 values, four a lane.
+__device__ __forceinline__ float row_most(const float (&x)[4])
+{
+    float m = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+#pragma unroll
+    for (int o = 16; o; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+// A row over its scale into blocks `apart` bytes from one another (the second part after the first's BLOCKS).
+template <int BLOCKS, int PARTS>
+__device__ __forceinline__ void put_row(unsigned char* img, unsigned apart, int r, const float (&x)[4], float down)
+{
+    const int c = threadIdx.x % 32 * 4;
+    if (c < BLOCKS * 64) {
+        uint2 hi, lo;
+        split_pair(x[0] * down, x[1] * down, hi.x, lo.x);
+        split_pair(x[2] * down, x[3] * down, hi.y, lo.y);
+        unsigned char* at = img + c / 64 * apart + swizzled(r, c % 64);
+        *reinterpret_cast<uint2*>(at) = hi;
+        if (PARTS == 2) *reinterpret_cast<uint2*>(at + BLOCKS * apart) = lo;
+    }
+}
+// Whether rows of d values start on multiples of four of them.
+template <typename T>
+__device__ __forceinline__ bool fours(const View& v, int d)
+{
+    return (uintptr_t)v.data % (4 * sizeof(T)) == 0 && (v.ss | v.bs | d) % 4 == 0;
+}
+
+// V and Y of a chunk by columns: 64 steps of 16 bits and 16 bytes more, so that threads' 16-byte accesses spread over all banks.
+constexpr int kPitch = 144;
+constexpr unsigned kSheet = 128 * kPitch;
+
+// A 64-step chunk of rows of 16-bit values to columns in shared memory (and back): thread t of 64 has step t; 16 bytes at
+// a time where the rows are aligned.  Rows have `cols` (at most 128) values; out of range they are 0.
+template <typename T>
+__device__ __forceinline__ void rows_to_sheet(unsigned char* sheet_at, const T* row, bool in, bool wide, int cols, int t)
+{
+    unsigned short* sheet = reinterpret_cast<unsigned short*>(sheet_at) + t;
+#pragma unroll 1
+    for (int c0 = 0; c0 < 128; c0 += 64) {
+        uint4 x[8];         // all on their way at once
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int c = c0 + 8 * q;
+            x[q] = make_uint4(0, 0, 0, 0);
+            if (in && wide && c + 8 <= cols) {
+                x[q] = *reinterpret_cast<const uint4*>(row + c);
+            } else if (in && c < cols) {
+                const unsigned short* one = reinterpret_cast<const unsigned short*>(row) + c;
+                unsigned* pairs = &x[q].x;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (c + e < cols) pairs[e / 2] |= (unsigned)one[e] << (e % 2 * 16);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const unsigned pairs[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sheet[(c0 + 8 * q + e) * (kPitch / 2)] = (unsigned short)(pairs[e / 2] >> (e % 2 * 16));
+        }
+    }
+}
+template <typename T>
+__device__ __forceinline__ void sheet_to_rows(const unsigned char* sheet_at, T* row_at, bool wide, int cols, int t)
+{
+    const unsigned short* sheet = reinterpret_cast<const unsigned short*>(sheet_at) + t;
+    unsigned short* row = reinterpret_cast<unsigned short*>(row_at);
+#pragma unroll 4
+    for (int c = 0; c < cols; c += 8) {
+        unsigned short x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = sheet[(c + e) * (kPitch / 2)];
+        if (wide && c + 8 <= cols) {
+            *reinterpret_cast<uint4*>(row + c) = make_uint4(x[0] | (unsigned)x[1] << 16, x[2] | (unsigned)x[3] << 16,
+                                                            x[4] | (unsigned)x[5] << 16, x[6] | (unsigned)x[7] << 16);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < cols) row[c + e] = x[e];
+        }
+    }
+}
+
+
+constexpr unsigned kTmem = 512;             // a block takes all of it
+constexpr int kChainThreads = 384;
+
+template <typename T>
+__device__ __forceinline__ f2 pair_of(unsigned raw);
+template <>
+__device__ __forceinline__ f2 pair_of<__nv_bfloat16>(unsigned raw) { return pack2(__uint_as_float(raw << 16), __uint_as_float(raw & 0xffff0000u)); }
+template <>
+__device__ __forceinline__ f2 pair_of<__half>(unsigned raw)
+{
+    const float2 v = pair_value(raw);
+    return pack2(v.x, v.y);
+}
+template <typename T>
+__device__ __forceinline__ unsigned raw_pair(f2 v)
+{
+    float a, b;
+    unpack2(v, a, b);
+    if (sizeof(T) == 4) return 0;
+    unsigned r;
+    if constexpr (std::is_same_v<T, __nv_bfloat16>) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    else r = half_pair(a, b);
+    return r;
+}
+__device__ __forceinline__ float most_of(float m, f2 v)
+{
+    float a, b;
+    unpack2(v, a, b);
+    return fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+}
+
+template <typename T, int DKB, int KP>
+struct ChainSmem {
+    static constexpr bool staged = sizeof(T) == 2;
+    static constexpr unsigned stage = Images<DKB, KP>::keys + Images<DKB, KP>::mats;
+    static constexpr int stages = 2;
+    static constexpr size_t bytes = stages * (size_t)stage + (staged ? 3 * kSheet : 0) + 1024;
+};
+
+// Rows and heads over y and z of a grid.
+inline dim3 heads_grid(int64_t x, int64_t nh)
+{
+    const int64_t y = nh < 65535 ? nh : 65535;
+    return dim3((unsigned)x, (unsigned)y, (unsigned)((nh + y - 1) / y));
 }
 
 }  // namespace delta

@@ -40,45 +40,5 @@ __device__ __forceinline__ void form_sums(Sums& s, const View& g, int64_t n, int
     __syncthreads();
 }
 
-// acc[i][j] += sum_k A[k][m0 + i] * B[k][n0 + j], both in shared memory.
-template <int RM, int RN>
-__device__ __forceinline__ void product(float (&acc)[RM][RN], const float* A, int lda, const float* B, int ldb, int K)
-{
-#pragma unroll 4
-    for (int k = 0; k < K; ++k) {
-        float a[RM], b[RN];
-#pragma unroll
-        for (int i = 0; i < RM; ++i) a[i] = A[k * lda + i];
-#pragma unroll
-        for (int j = 0; j < RN; ++j) b[j] = B[k * ldb + j];
-#pragma unroll
-        for (int i = 0; i < RM; ++i)
-#pragma unroll
-            for (int j = 0; j < RN; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-    }
-}
-template <int RM, int RN>
-__device__ __forceinline__ void clear(float (&acc)[RM][RN])
-{
-#pragma unroll
-    for (int i = 0; i < RM; ++i)
-#pragma unroll
-        for (int j = 0; j < RN; ++j) acc[i][j] = 0.f;
-}
-
-// A chunk's rows of one head, [C][d], in fp32: natural (row stride ldn) and transposed (ldt), either may
-// be NULL; zeros past the row's end.
-template <typename T>
-__device__ __forceinline__ void load_rows(const View& v, int64_t n, int64_t t0, int64_t len, int64_t at, int d, float* nat, int ldn,
-                                          float* tr, int ldt)
-{
-    for (int i = threadIdx.x; i < C * d; i += blockDim.x) {
-        const int t = i / d, c = i - t * d;
-        const float x = t0 + t < len ? to_f(static_cast<const T*>(v.data)[n * v.bs + (t0 + t) * v.ss + at + c]) : 0.f;
-        if (nat) nat[t * ldn + c] = x;
-        if (tr) tr[c * ldt + t] = x;
-    }
-}
-
 }  // namespace delta
 }  // namespace rnngb

@@ -11,8 +11,6 @@
 // which are the steps one after another: (1 + A) U = b (V - e^G K S0) is u's formula with
 // the state written out.  Only S0 -> S1 is a chain; T and P are formed before it
 // for all chunks at once.
-#include <type_traits>
-
 #include "delta_mma.cuh"
 
 namespace rnngb {
@@ -20,72 +18,15 @@ namespace {
 
 using namespace delta;
 
-// What the first launch leaves for the second, as it will lie in shared memory: K and Q of a chunk and key
-// head in KP parts of DKB blocks (64 steps by 64 values each), T and P of a chunk and head in two
-// parts each, and the factors of its steps.
-template <int DKB, int KP>
-struct Images {
-    static constexpr unsigned keys = 2 * KP * DKB * kBlock, mats = 4 * kBlock + 2048;
-};
-// Factors: of V and of K S0 in b (V - e^G K S0), of U's columns, of U's rows for the state, of Q S0 and of P U
-// in Y (kWhole: e^G_last).  The scales of the rows of K, Q, T and P are in them.
-enum Factor { kBeta = 0, kDecayed = 64, kT = 128, kLast = 192, kQuery = 256, kP = 320, kWhole = 384 };
-
 template <int DKB, int KP>
 struct PrepSmem {
-    unsigned char K[KP * DKB * kBlock], Q[KP * DKB * kBlock];
+    unsigned char KQ[2 * KP * DKB * kBlock];
     unsigned char P[2 * kBlock];
     float A[C][C + 1], T[C][C + 1], X[32][33];
-    float ek[C], eq[C], beta[C], fac[512];
+    float ek[C], eq[C], beta[C], fac[768];
     Sums sums;
     double carry;
 };
-
-// Rows r and values 4 l .. 4 l + 3 of a chunk of queries or keys, l the lane.
-template <typename T>
-__device__ __forceinline__ void load_four(const View& v, int64_t n, int64_t t, bool in, int64_t at, int d, bool wide, float (&x)[4])
-{
-    const int c = threadIdx.x % 32 * 4;
-    x[0] = x[1] = x[2] = x[3] = 0.f;
-    if (!in || c >= d) return;
-    const T* row = static_cast<const T*>(v.data) + n * v.bs + t * v.ss + at + c;
-    if (wide) {
-        struct alignas(4 * sizeof(T)) Four {
-            T v[4];
-        };
-        const Four q = *reinterpret_cast<const Four*>(row);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = to_f(q.v[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (c + i < d) x[i] = to_f(row[i]);
-    }
-}
-template <int DKB, int KP>
-__device__ __forceinline__ float put_row(unsigned char* img, int r, const float (&x)[4])
-{
-    float m = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-#pragma unroll
-    for (int o = 16; o; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const Scale s = scale_of(m);
-    const int c = threadIdx.x % 32 * 4;
-    if (c < DKB * 64) {
-        uint2 hi, lo;
-        split_pair(x[0] * s.down, x[1] * s.down, hi.x, lo.x);
-        split_pair(x[2] * s.down, x[3] * s.down, hi.y, lo.y);
-        unsigned char* at = img + c / 64 * kBlock + swizzled(r, c % 64);
-        *reinterpret_cast<uint2*>(at) = hi;
-        if (KP == 2) *reinterpret_cast<uint2*>(at + DKB * kBlock) = lo;
-    }
-    return s.up;
-}
-// Whether rows of d values start on multiples of four of them.
-template <typename T>
-__device__ __forceinline__ bool fours(const View& v, int d)
-{
-    return (uintptr_t)v.data % (4 * sizeof(T)) == 0 && (v.ss | v.bs | d) % 4 == 0;
-}
 
 // T and P, the factors, and K and Q as the second launch wants them.  A block has a chunk of a head.  The two products
 // [K; Q] K^T are small (a twentieth of all); they go through the warps' own matrix instructions.  T is
@@ -117,36 +58,38 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const DeltaParams 
         form_sums(s.sums, p.g, n, h, t0, len, &s.carry);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float ek = put_row<DKB, KP>(s.K, warp * 8 + i, k[i]), eq = put_row<DKB, KP>(s.Q, warp * 8 + i, q[i]);
-            if (lane == 0) s.ek[warp * 8 + i] = ek, s.eq[warp * 8 + i] = eq;
+            const Scale ek = scale_of(row_most(k[i])), eq = scale_of(row_most(q[i]));
+            put_row<DKB, KP>(s.KQ, 2 * kBlock, warp * 8 + i, k[i], ek.down);
+            put_row<DKB, KP>(s.KQ + kBlock, 2 * kBlock, warp * 8 + i, q[i], eq.down);
+            if (lane == 0) s.ek[warp * 8 + i] = ek.up, s.eq[warp * 8 + i] = eq.up;
         }
     }
     __syncthreads();
     if (h % per == 0) {
         uint4* out = reinterpret_cast<uint4*>(keys + ((n * p.HK + hk) * chunks + chunk) * Images<DKB, KP>::keys);
-        for (int i = tid; i < (int)Images<DKB, KP>::keys / 16; i += kThreads) out[i] = reinterpret_cast<const uint4*>(s.K)[i];
+        for (int i = tid; i < (int)Images<DKB, KP>::keys / 16; i += kThreads) out[i] = reinterpret_cast<const uint4*>(s.KQ)[i];
     }
     // warps 0 .. 3: 16 rows of K K^T each; 4 .. 7: of Q K^T
     const int rows = warp % 4 * 16;
     float c[8][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
-    const unsigned a0 = smem_addr(warp < 4 ? s.K : s.Q), b0 = smem_addr(s.K);
+    const unsigned a0 = smem_addr(s.KQ) + (warp < 4 ? 0 : kBlock), b0 = smem_addr(s.KQ);
 #pragma unroll
     for (int ks = 0; ks < DKB * 4; ++ks) {
-        const unsigned blk = ks / 4 * kBlock;
+        const unsigned blk = ks / 4 * 2 * kBlock;
         const int col = ks % 4 * 16;
         unsigned a[KP][4];
 #pragma unroll
         for (int q = 0; q < KP; ++q)
-            ld_matrix(a[q], a0 + q * DKB * kBlock + blk + swizzled(rows + lane % 16, col + lane / 16 * 8));
+            ld_matrix(a[q], a0 + q * DKB * 2 * kBlock + blk + swizzled(rows + lane % 16, col + lane / 16 * 8));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {       // 16 columns
             if (j * 16 > rows) continue;    // above the diagonal
 #pragma unroll
             for (int q = 0; q < KP; ++q) {
                 unsigned b[4];
-                ld_matrix(b, b0 + q * DKB * kBlock + blk + swizzled(j * 16 + lane % 8 + lane / 16 * 8, col + lane / 8 % 2 * 8));
+                ld_matrix(b, b0 + q * DKB * 2 * kBlock + blk + swizzled(j * 16 + lane % 8 + lane / 16 * 8, col + lane / 8 % 2 * 8));
 #pragma unroll
                 for (int r = 0; r + q < KP; ++r) {
                     mma_sync(c[2 * j], a[r], b[0], b[1]);
@@ -192,6 +135,8 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const DeltaParams 
         s.fac[kDecayed + tid] = s.beta[tid] * first * s.ek[tid];
         s.fac[kLast + tid] = expf(s.sums.between(C - 1, tid)) * s.ek[tid];
         s.fac[kQuery + tid] = p.scale * first * s.eq[tid];
+        s.fac[kKeyScale + tid] = s.ek[tid];
+        s.fac[kQueryScale + tid] = s.eq[tid];
         if (tid == C - 1) s.fac[kWhole] = first;
     }
     __syncthreads();
@@ -276,73 +221,7 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const DeltaParams 
     }
     for (int i = tid; i < (int)(2 * kBlock / 16); i += kThreads) reinterpret_cast<uint4*>(out + 2 * kBlock)[i] = reinterpret_cast<const uint4*>(s.P)[i];
     __syncthreads();
-    if (tid < 128) reinterpret_cast<float4*>(out + 4 * kBlock)[tid] = reinterpret_cast<const float4*>(s.fac)[tid];
-}
-
-// T and P of every chunk: [N][H][chunks][C][C] each, transposed (for the run) or not (for its
-// gradient, with a third matrix, e^(G_i - G_j) K_i.K_j below the diagonal).
-struct GradPrepSmem {
-    float KT[kDeltaMaxKey][C + 4], QT[kDeltaMaxKey][C + 4];
-    float A[C][C + 1];
-    float T[C][C + 1];
-    Sums sums;
-    float beta[C];
-    double carry;
-};
-
-template <typename T, bool GRAD>
-__global__ void __launch_bounds__(kThreads) delta_grad_prep_kernel(const DeltaParams p, float* mats)
-{
-    extern __shared__ __align__(1024) unsigned char raw[];
-    GradPrepSmem& s = *reinterpret_cast<GradPrepSmem*>(raw);
-    const int64_t chunk = blockIdx.x, chunks = gridDim.x;
-    const int64_t nh = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
-    if (nh >= p.N * p.H) return;
-    const int64_t n = nh / p.H;
-    const int h = (int)(nh - n * p.H), hk = h / (p.H / p.HK);
-    const int64_t len = row_length(p.lens, n, p.S, p.status), t0 = chunk * C;
-    if (t0 >= len) return;
-    const int tid = threadIdx.x;
-    load_rows<T>(p.K, n, t0, len, (int64_t)hk * p.DK, p.DK, nullptr, 0, s.KT[0], C + 4);
-    load_rows<T>(p.Q, n, t0, len, (int64_t)hk * p.DK, p.DK, nullptr, 0, s.QT[0], C + 4);
-    if (tid < C) s.beta[tid] = t0 + tid < len ? static_cast<const float*>(p.beta.data)[n * p.beta.bs + (t0 + tid) * p.beta.ss + h] : 0.f;
-    form_sums(s.sums, p.g, n, h, t0, len, &s.carry);
-    const int m0 = tid / 16 * 4, n0 = tid % 16 * 4;
-    float kk[4][4], qk[4][4];
-    clear(kk);
-    clear(qk);
-    product<4, 4>(kk, s.KT[0] + m0, C + 4, s.KT[0] + n0, C + 4, p.DK);
-    product<4, 4>(qk, s.QT[0] + m0, C + 4, s.KT[0] + n0, C + 4, p.DK);
-    float* outT = mats + (nh * chunks + chunk) * (GRAD ? 3 : 2) * C * C;
-    float* outP = outT + C * C;
-#pragma unroll
-    for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int i = m0 + a, j = n0 + b;
-            const float d = i >= j ? expf(s.sums.between(i, j)) : 0.f;
-            const float k = i > j ? d * kk[a][b] : 0.f;
-            s.A[i][j] = i > j ? s.beta[i] * k : 0.f;
-            const float q = i >= j ? d * qk[a][b] : 0.f;
-            if (GRAD) {
-                outP[i * C + j] = q;
-                outP[C * C + i * C + j] = k;
-            } else {
-                outP[j * C + i] = q;
-            }
-        }
-    __syncthreads();
-    // a thread has a column of T: T_ij = -(sum over j <= m < i of A_im T_mj)
-    if (tid < C) {
-        const int j = tid;
-        for (int i = 0; i < C; ++i) {
-            float v = i == j ? 1.f : 0.f;
-            for (int m = j; m < i; ++m) v = fmaf(-s.A[i][m], s.T[m][j], v);
-            s.T[i][j] = v;
-        }
-    }
-    __syncthreads();
-    for (int i = tid; i < C * C; i += kThreads) outT[i] = GRAD ? s.T[i / C][i % C] : s.T[i % C][i / C];
+    if (tid < 192) reinterpret_cast<float4*>(out + 4 * kBlock)[tid] = reinterpret_cast<const float4*>(s.fac)[tid];
 }
 
 // The chain.  A block has 128 columns of a head's state, a lane of tensor memory each: with S^T [value][key], U^T
@@ -355,59 +234,17 @@ __global__ void __launch_bounds__(kThreads) delta_grad_prep_kernel(const DeltaPa
 //   warp 9: copies the chunks' images, `stages` of them ahead;
 //   warps 10, 11 (16-bit types): a step a thread, lay V out by columns before it is wanted and write Y's rows, 16
 //     bytes at a time where they are aligned.
-constexpr int kRunThreads = 384;
-constexpr unsigned kTmem = 512;
-
 template <int DKB>
 struct Columns {     // of tensor memory
     static constexpr uint32_t dS = 0, S = DKB * 64, R = 2 * DKB * 64, U = R + 64, U2 = U + 64, QS = U2 + 64, PU = R;
 };
 
-// V and Y of a chunk by columns: 64 steps of 16 bits and 16 bytes more, so that threads' 16-byte accesses spread over all banks.
-constexpr int kPitch = 144;
-constexpr unsigned kSheet = 128 * kPitch;
 template <typename T, int DKB, int KP>
-struct RunSmem {
-    static constexpr bool staged = sizeof(T) == 2;
-    static constexpr unsigned stage = Images<DKB, KP>::keys + Images<DKB, KP>::mats;
-    static constexpr int stages = 2;
-    static constexpr size_t bytes = stages * (size_t)stage + (staged ? 3 * kSheet : 0) + 1024;
-};
-
-template <typename T>
-__device__ __forceinline__ f2 pair_of(unsigned raw);
-template <>
-__device__ __forceinline__ f2 pair_of<__nv_bfloat16>(unsigned raw) { return pack2(__uint_as_float(raw << 16), __uint_as_float(raw & 0xffff0000u)); }
-template <>
-__device__ __forceinline__ f2 pair_of<__half>(unsigned raw)
-{
-    const float2 v = pair_value(raw);
-    return pack2(v.x, v.y);
-}
-template <typename T>
-__device__ __forceinline__ unsigned raw_pair(f2 v)
-{
-    float a, b;
-    unpack2(v, a, b);
-    if (sizeof(T) == 4) return 0;
-    unsigned r;
-    if constexpr (std::is_same_v<T, __nv_bfloat16>) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-    else r = half_pair(a, b);
-    return r;
-}
-__device__ __forceinline__ float most_of(float m, f2 v)
-{
-    float a, b;
-    unpack2(v, a, b);
-    return fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
-}
-
-template <typename T, int DKB, int KP>
-__global__ void __launch_bounds__(kRunThreads, 1) delta_run_kernel(const DeltaParams p, const unsigned char* keys, const unsigned char* mats)
+__global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const DeltaParams p, const unsigned char* keys, const unsigned char* mats)
 {
     using Im = Images<DKB, KP>;
     using Co = Columns<DKB>;
-    using Sm = RunSmem<T, DKB, KP>;
+    using Sm = ChainSmem<T, DKB, KP>;
     constexpr int ST = Sm::stages, SR = DKB * 32;
     extern __shared__ __align__(1024) unsigned char raw[];
     __shared__ __align__(8) uint64_t full[ST], empty[ST], v_full[2], v_empty[2], y_full, y_empty;
@@ -477,14 +314,14 @@ __global__ void __launch_bounds__(kRunThreads, 1) delta_run_kernel(const DeltaPa
                 const unsigned ph = (unsigned)k & 1u;
                 if (!__all_sync(0xffffffffu, wait(&full[s], (unsigned)(k / ST) & 1u, &given_up) && wait(&s_ready, ph, &given_up))) break;
                 fence_after();
-                const unsigned kimg = sbase + s * Sm::stage, qimg = kimg + KP * DKB * kBlock;
+                const unsigned kimg = sbase + s * Sm::stage, qimg = kimg + kBlock;
                 const unsigned timg = kimg + Im::keys, pimg = timg + 2 * kBlock;
                 // parts a of S and b of K or Q, over the keys
                 auto keys_product = [&](uint32_t d, unsigned img, int a, int b, bool add) {
 #pragma unroll
                     for (int ks = 0; ks < DKB * 4; ++ks)
                         if (leader)
-                            mma_ts(tm + d, tm + Co::S + a * SR + ks * 8, desc_rows(img + (b * DKB + ks / 4) * kBlock + ks % 4 * 32), instr(C, false), add || ks > 0);
+                            mma_ts(tm + d, tm + Co::S + a * SR + ks * 8, desc_rows(img + (b * DKB + ks / 4) * 2 * kBlock + ks % 4 * 32), instr(C, false), add || ks > 0);
                 };
                 // a part of R or U, and a matrix's part, over the steps
                 auto steps_product = [&](uint32_t d, uint32_t from, int a, unsigned img, int b, bool add) {
@@ -514,7 +351,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) delta_run_kernel(const DeltaPa
                     for (int ks = 0; ks < 4; ++ks)
                         if (leader)
                             mma_ts(tm + Co::dS, tm + Co::U2 + ks / 2 * 32 + (q == 1) * 16 + ks % 2 * 8,
-                                   desc_columns(kimg + (q == 2) * DKB * kBlock + ks * 2048, kBlock), instr(DKB * 64, true), q > 0 || ks > 0);
+                                   desc_columns(kimg + (q == 2) * DKB * 2 * kBlock + ks * 2048, 2 * kBlock), instr(DKB * 64, true), q > 0 || ks > 0);
                 if (leader) mma_commit(&ds_ready);
                 steps_product(Co::PU, Co::U, 0, pimg, 0, false);
                 steps_product(Co::PU, Co::U, 0, pimg, 1, true);
@@ -534,34 +371,8 @@ __global__ void __launch_bounds__(kRunThreads, 1) delta_run_kernel(const DeltaPa
             T* to = static_cast<T*>(p.Y.data) + n * p.Y.bs + (int64_t)h * p.DV + v0;
             const bool vw = (uintptr_t)from % 16 == 0 && p.V.ss % 8 == 0, yw = (uintptr_t)to % 16 == 0 && p.Y.ss % 8 == 0;
             auto load_v = [&](int k) {
-                unsigned short* sheet = reinterpret_cast<unsigned short*>(sheets + (k & 1) * kSheet) + t;
                 const int64_t step = (int64_t)k * C + t;
-                const bool in = step < len;
-                const T* row = from + step * p.V.ss;
-#pragma unroll 1
-                for (int c0 = 0; c0 < 128; c0 += 64) {
-                    uint4 x[8];         // all on their way at once
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const int c = c0 + 8 * q;
-                        x[q] = make_uint4(0, 0, 0, 0);
-                        if (in && vw && c + 8 <= cols) {
-                            x[q] = *reinterpret_cast<const uint4*>(row + c);
-                        } else if (in && c < cols) {
-                            const unsigned short* one = reinterpret_cast<const unsigned short*>(row) + c;
-                            unsigned* pairs = &x[q].x;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (c + e < cols) pairs[e / 2] |= (unsigned)one[e] << (e % 2 * 16);
-                        }
-                    }
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const unsigned pairs[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) sheet[(c0 + 8 * q + e) * (kPitch / 2)] = (unsigned short)(pairs[e / 2] >> (e % 2 * 16));
-                    }
-                }
+                rows_to_sheet(sheets + (k & 1) * kSheet, from + step * p.V.ss, step < len, vw, cols, t);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&v_full[k & 1]);
             };
@@ -572,24 +383,8 @@ __global__ void __launch_bounds__(kRunThreads, 1) delta_run_kernel(const DeltaPa
                     load_v(k + 1);
                 }
                 if (!__all_sync(0xffffffffu, wait(&y_full, (unsigned)k & 1u, &given_up))) break;
-                const unsigned short* sheet = reinterpret_cast<const unsigned short*>(sheets + 2 * kSheet) + t;
                 const int64_t step = (int64_t)k * C + t;
-                unsigned short* row = reinterpret_cast<unsigned short*>(to + step * p.Y.ss);
-                if (step < len)
-#pragma unroll 4
-                    for (int c = 0; c < cols; c += 8) {
-                        unsigned short x[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = sheet[(c + e) * (kPitch / 2)];
-                        if (yw && c + 8 <= cols) {
-                            *reinterpret_cast<uint4*>(row + c) = make_uint4(x[0] | (unsigned)x[1] << 16, x[2] | (unsigned)x[3] << 16,
-                                                                            x[4] | (unsigned)x[5] << 16, x[6] | (unsigned)x[7] << 16);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (c + e < cols) row[c + e] = x[e];
-                        }
-                    }
+                if (step < len) sheet_to_rows(sheets + 2 * kSheet, to + step * p.Y.ss, yw, cols, t);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&y_empty);
             }
@@ -730,7 +525,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) delta_run_kernel(const DeltaPa
                 }
             }
             if (k == live) break;
-            if (p.saved && col) write_state(p.saved + (nh * chunks + k) * p.DK * p.DV + v);
+            if (p.states && col) write_state(p.states + (nh * chunks + k) * p.DK * p.DV + v);
             ok = ok && wait(&full[s], (unsigned)(k / ST) & 1u, &given_up);
             if constexpr (Sm::staged) ok = ok && wait(&v_full[k & 1], (unsigned)(k / 2) & 1u, &given_up);
             ok = __all_sync(0xffffffffu, ok && wait(&d_ready, ph, &given_up));
@@ -791,8 +586,8 @@ __global__ void __launch_bounds__(kRunThreads, 1) delta_run_kernel(const DeltaPa
             put_parts(my + Co::U + half * 32, my + Co::U + half * 32 + 16, x, eu.down);
             tmem_st_wait();
             tell(&up_ready);
-            if (p.saved && col) {
-                float* to = p.saved + p.N * p.H * chunks * p.DK * p.DV + ((nh * chunks + k) * C + half * 32) * p.DV + v;
+            if (p.states && col) {
+                float* to = p.us + ((nh * chunks + k) * C + half * 32) * p.DV + v;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     float a, b;
@@ -819,35 +614,22 @@ __global__ void __launch_bounds__(kRunThreads, 1) delta_run_kernel(const DeltaPa
     if (threadIdx.x == 0 && given_up) *p.status = 6;        // RNN_ERR_TIMEOUT
 }
 
-// Rows and heads over y and z of a grid.
-dim3 heads_grid(int64_t x, int64_t nh)
-{
-    const int64_t y = nh < 65535 ? nh : 65535;
-    return dim3((unsigned)x, (unsigned)y, (unsigned)((nh + y - 1) / y));
-}
-
-int64_t keys_bytes(const DeltaParams& p)
-{
-    return p.N * p.HK * delta_chunks(p.S) * 2 * (p.io == 0 ? 2 : 1) * ((p.DK + 63) / 64) * (int64_t)kBlock;
-}
-
 template <typename T, int DKB>
 cudaError_t run(const DeltaParams& p, cudaStream_t st, int* launches)
 {
     constexpr int KP = sizeof(T) == 4 ? 2 : 1;
-    constexpr size_t prep_smem = sizeof(PrepSmem<DKB, KP>) + 1024, run_smem = RunSmem<T, DKB, KP>::bytes;
+    constexpr size_t prep_smem = sizeof(PrepSmem<DKB, KP>) + 1024, run_smem = ChainSmem<T, DKB, KP>::bytes;
     static std::atomic<uint64_t> prep_done{0}, run_done{0};
     cudaError_t e = allow_shared(delta_prep_kernel<T, DKB, KP>, prep_smem, prep_done);
     if (e == cudaSuccess) e = allow_shared(delta_run_kernel<T, DKB, KP>, run_smem, run_done);
     if (e != cudaSuccess) return e;
     const int64_t nh = p.N * p.H;
-    unsigned char* keys = reinterpret_cast<unsigned char*>(p.scratch);
-    unsigned char* mats = keys + keys_bytes(p);
+    unsigned char *keys = p.keys, *mats = p.mats;
     if (p.S > 0) {
         delta_prep_kernel<T, DKB, KP><<<heads_grid(delta_chunks(p.S), nh), kThreads, prep_smem, st>>>(p, keys, mats);
         ++*launches;
     }
-    delta_run_kernel<T, DKB, KP><<<heads_grid((p.DV + 127) / 128, nh), kRunThreads, run_smem, st>>>(p, keys, mats);
+    delta_run_kernel<T, DKB, KP><<<heads_grid((p.DV + 127) / 128, nh), kChainThreads, run_smem, st>>>(p, keys, mats);
     ++*launches;
     return cudaGetLastError();
 }
@@ -858,34 +640,11 @@ cudaError_t run(const DeltaParams& p, cudaStream_t st, int* launches)
     return p.DK > 64 ? run<T, 2>(p, st, launches) : run<T, 1>(p, st, launches);
 }
 
-template <typename T>
-cudaError_t prep_grad(const DeltaParams& p, float* mats, cudaStream_t st, int* launches)
-{
-    static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_shared(delta_grad_prep_kernel<T, true>, sizeof(GradPrepSmem), done);
-    if (e != cudaSuccess) return e;
-    delta_grad_prep_kernel<T, true><<<heads_grid(delta_chunks(p.S), p.N * p.H), kThreads, sizeof(GradPrepSmem), st>>>(p, mats);
-    ++*launches;
-    return cudaGetLastError();
-}
-
 }  // namespace
-
-size_t delta_scratch_bytes(const DeltaParams& p)
-{
-    return (size_t)keys_bytes(p) + (size_t)(p.N * p.H * delta_chunks(p.S)) * Images<1, 1>::mats;
-}
 
 cudaError_t launch_delta(const DeltaParams& p, cudaStream_t s, int* launches)
 {
     return p.io == 0 ? run<float>(p, s, launches) : p.io == 1 ? run<__half>(p, s, launches) : run<__nv_bfloat16>(p, s, launches);
-}
-
-cudaError_t launch_delta_prep_grad(const DeltaParams& p, float* mats, cudaStream_t s, int* launches)
-{
-    return p.io == 0 ? prep_grad<float>(p, mats, s, launches)
-         : p.io == 1 ? prep_grad<__half>(p, mats, s, launches)
-                     : prep_grad<__nv_bfloat16>(p, mats, s, launches);
 }
 
 }  // namespace rnngb
