@@ -231,25 +231,36 @@ struct Images {
 // in Y (kWhole: e^G_last).  The scales of the rows of K, Q, T and P are in them; those of K and Q also stand alone.
 enum Factor { kBeta = 0, kDecayed = 64, kT = 128, kLast = 192, kQuery = 256, kP = 320, kKeyScale = 384, kQueryScale = 448, kWhole = 512 };
 
-// Rows r and values 4 l .. 4 l + 3 of a chunk of queries or keys, l the lane.
+// Four neighbouring values of rows of T: N rows at once, their loads together (a branch between them would make each wait
+// for the one before).  Row a is at `row + a * apart`, lanes have the values 4 l .. 4 l + 3 of `left`; rows of which
+// in(a) is false, and values past `left`, are 0.
 template <typename T>
-__device__ __forceinline__ void load_four(const View& v, int64_t n, int64_t t, bool in, int64_t at, int d, bool wide, float (&x)[4])
+struct alignas(4 * sizeof(T)) Four {
+    T v[4];
+};
+template <int N, typename T, typename In>
+__device__ __forceinline__ void load_fours(const T* row, int64_t apart, int left, bool wide, In in, float (&x)[N][4])
 {
     const int c = threadIdx.x % 32 * 4;
-    x[0] = x[1] = x[2] = x[3] = 0.f;
-    if (!in || c >= d) return;
-    const T* row = static_cast<const T*>(v.data) + n * v.bs + t * v.ss + at + c;
     if (wide) {
-        struct alignas(4 * sizeof(T)) Four {
-            T v[4];
-        };
-        const Four q = *reinterpret_cast<const Four*>(row);
+        Four<T> q[N] = {};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = to_f(q.v[i]);
+        for (int a = 0; a < N; ++a)
+            if (in(a) && c < left) q[a] = *reinterpret_cast<const Four<T>*>(row + a * apart + c);
+#pragma unroll
+        for (int a = 0; a < N; ++a)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[a][e] = to_f(q[a].v[e]);
     } else {
+        T q[N][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (c + i < d) x[i] = to_f(row[i]);
+        for (int a = 0; a < N; ++a)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) q[a][e] = in(a) && c + e < left ? row[a * apart + c + e] : from_f<T>(0.f);
+#pragma unroll
+        for (int a = 0; a < N; ++a)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[a][e] = to_f(q[a][e]);
     }
 }
 // The largest of a row of 128 values, four a lane.

@@ -48,12 +48,11 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const DeltaParams 
     {
         const bool kw = fours<T>(p.K, p.DK), qw = fours<T>(p.Q, p.DK);
         float k[8][4], q[8][4];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t t = t0 + warp * 8 + i;
-            load_four<T>(p.K, n, t, t < len, (int64_t)hk * p.DK, p.DK, kw, k[i]);
-            load_four<T>(p.Q, n, t, t < len, (int64_t)hk * p.DK, p.DK, qw, q[i]);
-        }
+        const int64_t t = t0 + warp * 8;
+        auto in = [&](int a) { return t + a < len; };
+        const int64_t at = n * p.K.bs + t * p.K.ss + (int64_t)hk * p.DK, qt = n * p.Q.bs + t * p.Q.ss + (int64_t)hk * p.DK;
+        load_fours<8>(static_cast<const T*>(p.K.data) + at, p.K.ss, p.DK, kw, in, k);
+        load_fours<8>(static_cast<const T*>(p.Q.data) + qt, p.Q.ss, p.DK, qw, in, q);
         if (tid < C) s.beta[tid] = t0 + tid < len ? static_cast<const float*>(p.beta.data)[n * p.beta.bs + (t0 + tid) * p.beta.ss + h] : 0.f;
         form_sums(s.sums, p.g, n, h, t0, len, &s.carry);
 #pragma unroll

@@ -441,19 +441,6 @@ struct RestSmem {
     static_assert(d + 128 * C * 4 <= states, "");
 };
 
-__device__ __forceinline__ void load_floats(const float* row, int v, int left, bool wide, float (&x)[4])
-{
-    x[0] = x[1] = x[2] = x[3] = 0.f;
-    if (wide && left >= 4) {
-        const float4 q = *reinterpret_cast<const float4*>(row + v);
-        x[0] = q.x, x[1] = q.y, x[2] = q.z, x[3] = q.w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < left) x[i] = row[v + i];
-    }
-}
-
 template <typename T, int DKB, int KP>
 __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const DeltaGradParams q)
 {
@@ -526,65 +513,64 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
             for (int j = tid; j < 192; j += kRestThreads)
                 reinterpret_cast<float4*>(fac)[j] = reinterpret_cast<const float4*>(p.mats + at * Im::mats + 4 * kBlock)[j];
             form_sums(sums, p.g, n, h, t0, len, &carry);
-            // row r of U, dR and dY' (r < 192), S0 (from 192), dS1 (from 192 + 128); the tile's values 4 lane ..
-            auto load = [&](int r, int v0, float (&x)[4]) {
-                const int left = DV - v0 - lane * 4;
-                if (r < 128) {
-                    load_floats((r < C ? us + r * (int64_t)DV : drs + (r - C) * (int64_t)DV) + v0, lane * 4, left, wide, x);
-                } else if (r < 192) {
-                    const int64_t t = t0 + r - 128;
-                    load_four<T>(q.dY, n, t, t < len, (int64_t)h * DV + v0, DV - v0, yw, x);
-                } else {
-                    const int d = (r - 192) % 128;
-                    x[0] = x[1] = x[2] = x[3] = 0.f;
-                    if (d < DK) load_floats((r < 320 ? states : ends) + d * (int64_t)DV + v0, lane * 4, left, wide, x);
-                }
-            };
-            // more values than a tile has: the rows' largest first
-            auto row_scale = [&](int r, const float (&x)[4]) {
+            // a row's scale; where it has more values than a tile, its others are looked through first
+            auto row_scale = [&](const auto* row, bool in, bool vec, const float (&x)[4]) {
                 float m = row_most(x);
-                if (tiles > 1) {
-                    m = 0.f;
-                    for (int v0 = 0; v0 < DV; v0 += 128) {
-                        float z[4];
-                        load(r, v0, z);
-                        m = fmaxf(m, row_most(z));
+                if (tiles > 1)
+                    for (int v = 0; v < DV; v += 128) {
+                        float z[1][4];
+                        load_fours<1>(row + v, 0, DV - v, vec, [&](int) { return in; }, z);
+                        m = fmaxf(m, row_most(z[0]));
                     }
-                }
                 return scale_of(m);
             };
             float rv_mine = 0.f, dot = 0.f;     // lane l: the sum for the warp's l-th row of dR
             for (int tile = 0; tile < tiles && ok; ++tile) {
                 const int v0 = tile * 128;
                 const bool second = DV - v0 > 64;       // two blocks of 64 values
-                constexpr int kRows = 192 + DKB * 64, kAhead = 4;
-#pragma unroll 1
-                for (int r0 = warp; r0 < kRows; r0 += 16 * kAhead) {
-                    float x[kAhead][4];
+                const int left = DV - v0;
+                // a warp's rows: every 16th of U, dR, dY' and V, then of S0
+                auto step_in = [&](int a) { return t0 + warp + 16 * a < len; };
+                auto key_in = [&](int a) { return warp + 16 * a < DK; };
+                auto always = [](int) { return true; };
+                const float *u_row = us + warp * (int64_t)DV, *r_row = drs + warp * (int64_t)DV, *s_row = states + warp * (int64_t)DV;
+                const T* y_row = static_cast<const T*>(q.dY.data) + n * q.dY.bs + (t0 + warp) * q.dY.ss + (int64_t)h * DV;
+                const T* v_row = static_cast<const T*>(p.V.data) + n * p.V.bs + (t0 + warp) * p.V.ss + (int64_t)h * DV;
+                {
+                    float x[4][4], y[4][4], z[4][4], w[4][4];
+                    load_fours<4>(u_row + v0, 16 * (int64_t)DV, left, wide, always, x);
+                    load_fours<4>(r_row + v0, 16 * (int64_t)DV, left, wide, always, y);
+                    load_fours<4>(y_row + v0, 16 * q.dY.ss, left, yw, step_in, z);
+                    load_fours<4>(v_row + v0, 16 * p.V.ss, left, vw, step_in, w);
 #pragma unroll
-                    for (int a = 0; a < kAhead; ++a)
-                        if (r0 + 16 * a < kRows) load(r0 + 16 * a, v0, x[a]);
+                    for (int a = 0; a < 4; ++a) {
+                        const int r = warp + 16 * a;
+                        const Scale su = row_scale(u_row + a * 16 * (int64_t)DV, true, wide, x[a]);
+                        const Scale sr = row_scale(r_row + a * 16 * (int64_t)DV, true, wide, y[a]);
+                        const Scale sy = row_scale(y_row + a * 16 * q.dY.ss, step_in(a), yw, z[a]);
+                        put_row<2, 2>(base + Sm::rows, Sm::row_block, r, x[a], su.down);
+                        put_row<2, 2>(base + Sm::rows, Sm::row_block, C + r, y[a], sr.down);
+                        put_row<2, 2>(base + Sm::rows, Sm::row_block, 2 * C + r, z[a], sy.down);
+                        float s = y[a][0] * w[a][0] + y[a][1] * w[a][1] + y[a][2] * w[a][2] + y[a][3] * w[a][3];
 #pragma unroll
-                    for (int a = 0; a < kAhead; ++a) {
-                        const int r = r0 + 16 * a;
-                        if (r >= kRows) continue;
-                        const Scale sc = row_scale(r, x[a]);
-                        if (r < 192) {
-                            put_row<2, 2>(base + Sm::rows, Sm::row_block, r, x[a], sc.down);
-                            if (lane == 0) scale[r] = (r < 128 ? 1.f : p.scale) * sc.up;
-                        } else {
-                            put_row<2, 2>(base + Sm::states, Sm::state_block, r - 192, x[a], sc.down);
-                            if (lane == 0) s_scale[r - 192] = sc.up;
+                        for (int o = 16; o; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+                        if (lane == a) rv_mine += s;
+                        if (lane == 0) {
+                            scale[r] = su.up;
+                            scale[C + r] = sr.up;
+                            scale[2 * C + r] = p.scale * sy.up;
                         }
-                        if (r >= C && r < 128) {        // dR . V
-                            float z[4];
-                            const int64_t t = t0 + r - C;
-                            load_four<T>(p.V, n, t, t < len, (int64_t)h * DV + v0, DV - v0, vw, z);
-                            float s = x[a][0] * z[0] + x[a][1] * z[1] + x[a][2] * z[2] + x[a][3] * z[3];
+                    }
+                }
+                {
+                    float x[DKB * 4][4];
+                    load_fours<DKB * 4>(s_row + v0, 16 * (int64_t)DV, left, wide, key_in, x);
 #pragma unroll
-                            for (int o = 16; o; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-                            if (lane == (r - C) / 16) rv_mine += s;
-                        }
+                    for (int a = 0; a < DKB * 4; ++a) {
+                        const int d = warp + 16 * a;
+                        const Scale sc = row_scale(s_row + a * 16 * (int64_t)DV, d < DK, wide, x[a]);
+                        put_row<2, 2>(base + Sm::states, Sm::state_block, d, x[a], sc.down);
+                        if (lane == 0) s_scale[d] = sc.up;
                     }
                 }
                 fence_shared();
@@ -610,8 +596,8 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                 }
                 // dS1 in the meantime, and <dS1, S0> with S0 as its parts have it
                 float g[DKB * 4][4];
-#pragma unroll
-                for (int a = 0; a < DKB * 4; ++a) load(320 + warp + 16 * a, v0, g[a]);
+                const float* e_row = ends + warp * (int64_t)DV;
+                load_fours<DKB * 4>(e_row + v0, 16 * (int64_t)DV, left, wide, key_in, g);
 #pragma unroll
                 for (int a = 0; a < DKB * 4; ++a) {
                     const int d = warp + 16 * a, c = lane * 4;
@@ -626,7 +612,7 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
 #pragma unroll
                 for (int a = 0; a < DKB * 4; ++a) {
                     const int d = warp + 16 * a;
-                    const Scale sc = row_scale(320 + d, g[a]);
+                    const Scale sc = row_scale(e_row + a * 16 * (int64_t)DV, d < DK, wide, g[a]);
                     put_row<2, 2>(base + Sm::states, Sm::state_block, d, g[a], sc.down);
                     if (lane == 0) g_scale[d] = sc.up;
                 }
@@ -847,13 +833,25 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
     if (out.data && i < steps) {
         T* row = static_cast<T*>(out.data) + n * out.bs + (t0 + i) * out.ss + (int64_t)hk * DK;
         const bool in = t0 + i < len;
+        constexpr int VEC = 16 / (int)sizeof(T);
+        const bool vec = (uintptr_t)out.data % 16 == 0 && (out.ss | out.bs | DK) % VEC == 0;
 #pragma unroll
-        for (int b = 0; b < DKB; ++b)
+        for (int b = 0; b < DKB; ++b) {
+            const int d0 = quarter * DKB * 16 + b * 16;
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const int d = quarter * DKB * 16 + b * 16 + c;
-                if (d < DK) row[d] = from_f<T>(in ? acc[b][c] : 0.f);
+            for (int c = 0; c < 16; c += VEC) {
+                __align__(16) T x[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) x[e] = from_f<T>(in ? acc[b][c + e] : 0.f);
+                if (vec) {
+                    if (d0 + c < DK) *reinterpret_cast<uint4*>(row + d0 + c) = *reinterpret_cast<const uint4*>(x);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        if (d0 + c + e < DK) row[d0 + c + e] = x[e];
+                }
             }
+        }
     }
 }
 
