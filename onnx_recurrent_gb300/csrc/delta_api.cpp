@@ -98,8 +98,7 @@ void place(DeltaParams& p, void* saved)
 {
     p.keys = static_cast<unsigned char*>(saved);
     p.mats = p.keys + delta_keys_bytes(p.S, p.N, p.HK, p.DK, p.io);
-    p.states = reinterpret_cast<float*>(p.mats + delta_mats_bytes(p.S, p.N, p.H));
-    p.us = p.states + p.N * p.H * delta_chunks(p.S) * p.DK * p.DV;
+    p.kept = p.mats + delta_mats_bytes(p.S, p.N, p.H);
 }
 
 rnn_status check_saved(const void* saved)
@@ -205,7 +204,7 @@ rnn_status rnn_delta_rule(rnn_delta_t pl, const rnn_delta_args* a)
     rs = claim_scratch(pl, bytes, st, &scratch);
     if (rs != RNN_OK) return rs;
     place(p, a->saved ? (void*)a->saved : scratch);
-    if (!a->saved) p.states = p.us = nullptr;
+    if (!a->saved) p.kept = nullptr;
     cudaError_t err = launch_delta(p, st, &pl->launches);
     if (err != cudaSuccess) return cuda_fail(err, "delta rule launch");
     return release_scratch(pl, bytes, st);
@@ -250,12 +249,11 @@ rnn_status rnn_delta_rule_grad(rnn_delta_t pl, const rnn_delta_grad_args* a)
     q.dhT = a->d_final_state;
     q.dh0 = a->d_initial_state;
     cudaStream_t st = (cudaStream_t)a->stream;
-    const size_t bytes = sizeof(float) * (size_t)delta_grad_scratch_floats(S, N, H, pl->DK, pl->DV);
+    const size_t bytes = (size_t)delta_slopes_bytes(S, N, H, pl->DK, pl->DV, pl->io);
     char* scratch = nullptr;
     rs = claim_scratch(pl, bytes, st, &scratch);
     if (rs != RNN_OK) return rs;
-    q.ends = (float*)scratch;
-    q.drs = q.ends + N * H * delta_chunks(S) * pl->DK * pl->DV;
+    q.slopes = (unsigned char*)scratch;
     cudaError_t err = launch_delta_grad(q, st, &pl->launches);
     if (err != cudaSuccess) return cuda_fail(err, "delta rule gradient launch");
     return release_scratch(pl, bytes, st);

@@ -19,7 +19,7 @@ struct DeltaParams {
     const float* h0;        // [N, H, DK, DV]
     float* hT;
     unsigned char *keys, *mats;     // what the chunks' first launch leaves (delta_mma.cuh: Images)
-    float *states, *us;     // the state before every chunk, [N, H, chunks, DK, DV], and u, [N, H, chunks, C, DV]; NULL: not kept
+    unsigned char* kept;    // the states before the chunks, and u (delta_kept_bytes); NULL: not kept
     int* status;
 };
 
@@ -28,7 +28,7 @@ struct DeltaGradParams {
     View dY, dQ, dK, dV, dg, dbeta;
     const float* dhT;
     float* dh0;
-    float *ends, *drs;      // scratch: the slope in the state after every chunk, and dR, as states and us
+    unsigned char* slopes;  // scratch (delta_slopes_bytes): the slopes in the states after the chunks, dR and dY
 };
 
 struct DeltaStepParams {
@@ -51,13 +51,18 @@ inline int64_t delta_keys_bytes(int64_t S, int64_t N, int64_t HK, int64_t DK, in
     return N * HK * delta_chunks(S) * 2 * (io == 0 ? 2 : 1) * ((DK + 63) / 64) * kDeltaBlock;
 }
 inline int64_t delta_mats_bytes(int64_t S, int64_t N, int64_t H) { return N * H * delta_chunks(S) * kDeltaMats; }
+// Of a chunk, head and 128 values: two parts each of the state (64 keys a block) and of u, and their scales.
+__host__ __device__ inline int64_t delta_kept_tile(int DK) { return (2 * ((DK + 63) / 64) + 2) * 2 * kDeltaBlock + 1024; }
+// ... of the slope in the state, of dR, and of dY (16-bit ones have one part).
+__host__ __device__ inline int64_t delta_slopes_tile(int DK, int io) { return delta_kept_tile(DK) + (io == 0 ? 2 : 1) * 2 * kDeltaBlock; }
+inline int64_t delta_tiles(int64_t S, int64_t N, int64_t H, int64_t DV) { return N * H * delta_chunks(S) * ((DV + 127) / 128); }
 inline int64_t delta_saved_floats(int64_t S, int64_t N, int64_t H, int64_t HK, int64_t DK, int64_t DV, int io)
 {
-    return (delta_keys_bytes(S, N, HK, DK, io) + delta_mats_bytes(S, N, H)) / 4 + N * H * delta_chunks(S) * (DK + kDeltaChunk) * DV;
+    return (delta_keys_bytes(S, N, HK, DK, io) + delta_mats_bytes(S, N, H) + delta_tiles(S, N, H, DV) * delta_kept_tile((int)DK)) / 4;
 }
-inline int64_t delta_grad_scratch_floats(int64_t S, int64_t N, int64_t H, int64_t DK, int64_t DV)
+inline int64_t delta_slopes_bytes(int64_t S, int64_t N, int64_t H, int64_t DK, int64_t DV, int io)
 {
-    return N * H * delta_chunks(S) * (DK + kDeltaChunk) * DV;
+    return delta_tiles(S, N, H, DV) * delta_slopes_tile((int)DK, io);
 }
 
 cudaError_t launch_delta(const DeltaParams& p, cudaStream_t s, int* launches);

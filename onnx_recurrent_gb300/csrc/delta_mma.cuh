@@ -267,9 +267,7 @@ __device__ __forceinline__ void load_fours(const T* row, int64_t apart, int left
 __device__ __forceinline__ float row_most(const float (&x)[4])
 {
     float m = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-#pragma unroll
-    for (int o = 16; o; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    return m;
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));      // not negative: its bits sort as it does
 }
 // A row over its scale into blocks `apart` bytes from one another (the second part after the first's BLOCKS).
 template <int BLOCKS, int PARTS>
@@ -394,6 +392,42 @@ inline dim3 heads_grid(int64_t x, int64_t nh)
     const int64_t y = nh < 65535 ? nh : 65535;
     return dim3((unsigned)x, (unsigned)y, (unsigned)((nh + y - 1) / y));
 }
+
+
+// What a chain keeps of a chunk for the gradient's second launch, for each tile of 128 values: [value][...] rows in two
+// parts under one scale a tile (their sums run over the values), swizzled as products take them.
+constexpr unsigned kSheetImage = 128 * 128;     // 128 values' rows of 64 steps or keys
+// N pairs of values as 16-byte pieces from `piece` on of row r of an image and of its second part.
+template <int N>
+__device__ __forceinline__ void keep_parts(unsigned char* image, unsigned second, int r, int piece, const f2* v, float down)
+{
+    const f2 d = dup2(down), m = dup2(6144.f), mm = dup2(-6144.f), minus = dup2(-1.f);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+        unsigned hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const f2 a = add2(fma2(v[4 * i + e], d, m), mm);
+            float x, y;
+            unpack2(a, x, y);
+            hi[e] = half_pair(x, y);
+            unpack2(fma2(v[4 * i + e], d, mul2(a, minus)), x, y);
+            lo[e] = half_pair(x, y);
+        }
+        unsigned char* at = image + r * 128 + (((piece + i) ^ (r & 7)) << 4);
+        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(at + second) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+}
+// The largest of a block's 256 threads' values, which their warps have left in `most`.
+__device__ __forceinline__ float most_of_warps(const float (&most)[8])
+{
+    float m = most[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = fmaxf(m, most[i]);
+    return m;
+}
+__device__ __forceinline__ float warp_most(float m) { return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m))); }
 
 }  // namespace delta
 }  // namespace rnngb

@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
     extern __shared__ __align__(1024) unsigned char raw[];
     __shared__ __align__(8) uint64_t full[ST], empty[ST], v_full[2], v_empty[2], y_full, y_empty;
     __shared__ __align__(8) uint64_t s_ready, d_ready, r_ready, u_ready, up_ready, ds_ready, o_ready, done;
-    __shared__ float most[4][2][128];
+    __shared__ float most[4][2][128], warps_most[2][8];
     __shared__ uint32_t slot;
     __shared__ int given_up;
     unsigned char* base = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
@@ -399,6 +399,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
         const int d0 = half * SR;                        // its keys: SR from here
         f2 S[SR / 2], x[16];
         T vs[Sm::staged ? 1 : 32];
+        // where a chunk's parts are kept for the gradient
+        unsigned char* kept = p.kept ? p.kept + (nh * chunks * gridDim.x + blockIdx.x) * delta_kept_tile(p.DK) : nullptr;
         float m = 0.f;
 #pragma unroll
         for (int i = 0; i < SR / 2; ++i) {
@@ -478,6 +480,10 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
                 }
             }
             if (k < live) {
+                if (kept) {
+                    const float w = warp_most(m);
+                    if (lane == 0) warps_most[0][warp] = w;
+                }
                 if (!both(3, m, ok)) break;
                 es = scale_of(m);
                 put_state(es.down);
@@ -524,7 +530,11 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
                 }
             }
             if (k == live) break;
-            if (p.states && col) write_state(p.states + (nh * chunks + k) * p.DK * p.DV + v);
+            if (kept) {
+                const Scale one = scale_of(most_of_warps(warps_most[0]));
+                keep_parts<SR / 2>(kept + (DKB == 2 ? half * kSheetImage : 0), DKB * kSheetImage, row, DKB == 2 ? 0 : half * 4, S, one.down);
+                if (threadIdx.x == 0) *reinterpret_cast<float*>(kept + (2 * DKB + 2) * kSheetImage) = one.up;
+            }
             ok = ok && wait(&full[s], (unsigned)(k / ST) & 1u, &given_up);
             if constexpr (Sm::staged) ok = ok && wait(&v_full[k & 1], (unsigned)(k / 2) & 1u, &given_up);
             ok = __all_sync(0xffffffffu, ok && wait(&d_ready, ph, &given_up));
@@ -577,6 +587,10 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
                     m2 = most_of(most_of(m2, y[2 * i]), y[2 * i + 1]);
                 }
             }
+            if (kept) {
+                const float w = warp_most(m);
+                if (lane == 0) warps_most[1][warp] = w;
+            }
             most[1][half][row] = m;
             if (!both(2, m2, ok)) break;
             m = fmaxf(m, most[1][1 - half][row]);
@@ -585,17 +599,11 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
             put_parts(my + Co::U + half * 32, my + Co::U + half * 32 + 16, x, eu.down);
             tmem_st_wait();
             tell(&up_ready);
-            if (p.states && col) {
-                float* to = p.us + ((nh * chunks + k) * C + half * 32) * p.DV + v;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float a, b;
-                    unpack2(x[i], a, b);
-                    *to = a;
-                    to += p.DV;
-                    *to = b;
-                    to += p.DV;
-                }
+            if (kept) {
+                const Scale one = scale_of(most_of_warps(warps_most[1]));
+                keep_parts<16>(kept + 2 * DKB * kSheetImage, kSheetImage, row, half * 4, x, one.down);
+                if (threadIdx.x == 0) *reinterpret_cast<float*>(kept + (2 * DKB + 2) * kSheetImage + 4) = one.up;
+                kept += gridDim.x * delta_kept_tile(p.DK);
             }
         }
         if (p.hT && col) write_state(p.hT + at);

@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_grad_chain_kernel(cons
     extern __shared__ __align__(1024) unsigned char raw[];
     __shared__ __align__(8) uint64_t full[ST], empty[ST], v_full[2], v_empty[2], y_full, y_empty;
     __shared__ __align__(8) uint64_t x_ready, g_ready, d_ready, u_told, r_ready, x2_ready, dq_ready, r_told, dg_ready, done;
-    __shared__ float most[5][2][128];
+    __shared__ float most[5][2][128], warps_most[3][8];
     __shared__ uint32_t slot;
     __shared__ int given_up;
     unsigned char* base = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
@@ -198,6 +198,10 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_grad_chain_kernel(cons
         const int64_t at = nh * p.DK * p.DV + v;
         const int d0 = half * SR;
         f2 G[SR / 2], x[16], y[16];
+        // where a chunk's parts are kept for the second launch: G's, dR's, dY's, the last chunk first
+        const int64_t tile = delta_slopes_tile(p.DK, sizeof(T) == 4 ? 0 : 1);
+        unsigned char* kept = q.slopes + ((nh * chunks + live - 1) * gridDim.x + blockIdx.x) * tile;
+        constexpr unsigned kR = 2 * DKB * kSheetImage, kY = kR + 2 * kSheetImage, kScales = kY + KP * kSheetImage;
         float m = 0.f;
 #pragma unroll
         for (int i = 0; i < SR / 2; ++i) {
@@ -235,8 +239,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_grad_chain_kernel(cons
         auto factors = [](const float* fac, int which, int i) { return *reinterpret_cast<const ulonglong2*>(fac + which + 4 * i); };
         auto stage_of = [&](int k) { return reinterpret_cast<const float*>(base + k % ST * Sm::stage + Im::keys + 4 * kBlock) + half * 32; };
         // dY of chunk k times the factors of kind `which`, into y and, in parts, to X; false once any wait gave up
-        auto put_dy = [&](int k, int which, int meeting, float& up, bool ok) {
-            float most_y = 0.f;
+        auto put_dy = [&](int k, int which, int meeting, float& up, bool ok, bool keep) {
+            float most_y = 0.f, most_raw = 0.f;
+            f2 raw_y[16];
             if (ok) {
                 const float* fac = stage_of(k);
                 const uint4* sheet = reinterpret_cast<const uint4*>(sheets + (k & 1) * kSheet + row * kPitch + half * 64);
@@ -258,16 +263,42 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_grad_chain_kernel(cons
                         w0 = pack2(w[0], w[1]);
                         w1 = pack2(w[2], w[3]);
                     }
+                    if (keep) {
+                        raw_y[2 * i] = w0;
+                        raw_y[2 * i + 1] = w1;
+                        most_raw = most_of(most_of(most_raw, w0), w1);
+                    }
                     y[2 * i] = mul2(a.x, w0);
                     y[2 * i + 1] = mul2(a.y, w1);
                     most_y = most_of(most_of(most_y, y[2 * i]), y[2 * i + 1]);
                 }
+            }
+            if (keep) {
+                const float w = warp_most(most_raw);
+                if (lane == 0) warps_most[1][warp] = w;
             }
             if (!both(meeting, most_y, ok)) return false;
             const Scale e = scale_of(most_y);
             put_parts(my + Co::X + half * 32, my + Co::X + half * 32 + 16, y, e.down);
             tmem_st_wait();
             up = e.up;
+            if (keep) {
+                tell(&x2_ready);
+                const Scale one = scale_of(most_of_warps(warps_most[1]));
+                if (threadIdx.x == 0) *reinterpret_cast<float*>(kept + kScales + 8) = one.up;
+                if constexpr (KP == 2) {
+                    keep_parts<16>(kept + kY, kSheetImage, row, half * 4, raw_y, one.down);
+                } else {
+                    const f2 d = dup2(one.down);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        unsigned v[4];
+#pragma unroll
+                        for (int e2 = 0; e2 < 4; ++e2) v[e2] = raw_pair<__half>(mul2(raw_y[4 * i + e2], d));
+                        *reinterpret_cast<uint4*>(kept + kY + row * 128 + (((half * 4 + i) ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                }
+            }
             return true;
         };
         auto arrived = [&](int k) {     // chunk k's factors and dY
@@ -282,7 +313,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_grad_chain_kernel(cons
             // dY' P's operand, ahead of all else of this chunk
             if (k < live) {
                 ok = arrived(k) && ok;
-                if (!put_dy(k, kP, 4, py_up, ok)) break;
+                if (!put_dy(k, kP, 4, py_up, ok, false)) break;
                 tell(&x_ready);
             }
             if (k > 0) {        // G of the chunk before is complete
@@ -305,6 +336,10 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_grad_chain_kernel(cons
                 if (lane == 0) mbar_arrive(&empty[(k - 1) % ST]);
             }
             if (k == live) break;
+            {
+                const float w = warp_most(m);
+                if (lane == 0) warps_most[0][warp] = w;
+            }
             if (!both(3, m, ok)) break;
             const Scale eg = scale_of(m);
 #pragma unroll
@@ -313,7 +348,11 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_grad_chain_kernel(cons
             tmem_st_wait();
             tell(&g_ready);
             const int64_t chunk = live - 1 - k;
-            if (col) write_state(q.ends + (nh * chunks + chunk) * p.DK * p.DV + v);
+            {
+                const Scale one = scale_of(most_of_warps(warps_most[0]));
+                keep_parts<SR / 2>(kept + (DKB == 2 ? half * kSheetImage : 0), DKB * kSheetImage, row, DKB == 2 ? 0 : half * 4, G, one.down);
+                if (threadIdx.x == 0) *reinterpret_cast<float*>(kept + kScales) = one.up;
+            }
             const float* fac = stage_of(k);
             ok = __all_sync(0xffffffffu, wait(&d_ready, ph, &given_up));
             m = 0.f;
@@ -335,12 +374,12 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_grad_chain_kernel(cons
             put_parts(my + Co::U + half * 32, my + Co::U + half * 32 + 16, x, eu.down);
             tmem_st_wait();
             tell(&u_told);
-            if (!put_dy(k, kQuery, 1, qy_up, ok)) break;
-            tell(&x2_ready);
+            if (!put_dy(k, kQuery, 1, qy_up, ok, true)) break;
             if constexpr (Sm::staged)
                 if (lane == 0) mbar_arrive(&v_empty[k & 1]);
             ok = __all_sync(0xffffffffu, wait(&r_ready, ph, &given_up));
             m = 0.f;
+            float most_r = 0.f;
             if (ok) {
                 fence_after();
                 tmem_ld(my + Co::R + half * 32, x);
@@ -350,10 +389,15 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_grad_chain_kernel(cons
                     const ulonglong2 a = factors(fac, kDecayed, i);
                     x[2 * i] = mul2(x[2 * i], up);
                     x[2 * i + 1] = mul2(x[2 * i + 1], up);
+                    most_r = most_of(most_of(most_r, x[2 * i]), x[2 * i + 1]);
                     y[2 * i] = mul2(mul2(a.x, minus), x[2 * i]);
                     y[2 * i + 1] = mul2(mul2(a.y, minus), x[2 * i + 1]);
                     m = most_of(most_of(m, y[2 * i]), y[2 * i + 1]);
                 }
+            }
+            {
+                const float w = warp_most(most_r);
+                if (lane == 0) warps_most[2][warp] = w;
             }
             if (!both(2, m, ok)) break;
             const Scale er = scale_of(m);
@@ -372,17 +416,11 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_grad_chain_kernel(cons
                 }
                 tell(&r_told);
             }
-            if (col) {
-                float* to = q.drs + ((nh * chunks + chunk) * C + half * 32) * p.DV + v;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float a, b;
-                    unpack2(x[i], a, b);
-                    *to = a;
-                    to += p.DV;
-                    *to = b;
-                    to += p.DV;
-                }
+            {
+                const Scale one = scale_of(most_of_warps(warps_most[2]));
+                keep_parts<16>(kept + kR, kSheetImage, row, half * 4, x, one.down);
+                if (threadIdx.x == 0) *reinterpret_cast<float*>(kept + kScales + 4) = one.up;
+                kept -= gridDim.x * tile;
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {       // dV
@@ -423,36 +461,45 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_grad_chain_kernel(cons
     if (threadIdx.x == 0 && given_up) *p.status = 6;        // RNN_ERR_TIMEOUT
 }
 
-// The rest, a chunk and key head a block.  With [U; dR; dY'] as rows of one buffer, their products with the two states and with
-// U are
-//     [dR; dY'] S0^T = [X2; X1],   [dR; dY'] U^T = [-dA; dP],   [U; dR] dS1^T = [X3; not wanted],
-// 128 rows each: a lane of tensor memory is a step, in the upper half of dR's results, in the lower of dY''s.  Then [K; Q] K^T
-// again, and [EA + EA^T; EP] K and [EP^T; 0] Q.  Everything is read from memory once, as fp32 rows that a warp
-// takes to parts (a row's values are the products' sums' direction, so its scale is the result's); the
-// reads are what bounds it: 256 KB a chunk and head of 128 x 128, at 16 bits.
+// The rest, a chunk and key head a block.  With what the chains have kept, each [value][step] or [value][key] in two parts,
+// the products over the values are
+//     [dR; dY'] S0^T = [X2; X1],   [dR; dY'] U^T = [-dA; dP],   [U; not used] dS1^T = [X3; not used],
+// 128 rows each: a lane of tensor memory is a step, dR's in the upper half and dY''s in the lower one.  Then [K; Q] K^T
+// again, [EA + EA^T; EP] K and [EP^T; not used] Q.  More values than 128 are taken one tile after the other: everything
+// below is linear in the five first products.
+//
+// With D_ij as above, sum_j D_ij = k_i.(EA K)_i + q_i.(EP K)_i and sum_j D_ji = k_i.(EA^T K + EP^T Q)_i, so the slope in G_i is
+//     q_i.dQ_i - k_i.dK_i + 2 (sum_j EA_ij K_i.K_j - b_i e^G_i k_i.X2_i)
+// and no sum runs down a column.
+//
+// Bytes bound it, 240 KB a chunk and head of 128 x 128 at 16 bits, copied as they are.
 constexpr int kRestThreads = 512;
-template <int DKB>
+template <int DKB, int KP>
 struct RestSmem {
-    static constexpr unsigned row_block = 192 * 128, state_block = DKB * kBlock;
-    static constexpr unsigned rows = 0, states = 4 * row_block, e = states + 4 * state_block, end = e + 128 * C * 4;
-    // once the rows are done with: [EA + EA^T; EP], [EP^T; 0] and D; in place of the states, K and Q
-    static constexpr unsigned a1 = 0, a2 = 4 * kBlock, d = 8 * kBlock;
+    // u's parts, then [dR; dY] of the first parts and of the second; the states; K and Q (of 32-bit types in the states' place,
+    // when these are done with)
+    static constexpr unsigned u = 0, r = 2 * kSheetImage, y = 3 * kSheetImage, states = 6 * kSheetImage;
+    static constexpr bool early = KP == 1;
+    static constexpr unsigned keys = early ? states + 2 * DKB * kSheetImage : states;
+    static constexpr unsigned end = states + 2 * DKB * kSheetImage + (early ? Images<DKB, KP>::keys : 0);
+    // once [dR; dY] and u are done with: E; [EA + EA^T; EP]; EP^T
+    static constexpr unsigned e = r, a1 = 4 * kSheetImage, a2 = u;
     static constexpr size_t bytes = end + 1024;
-    static_assert(d + 128 * C * 4 <= states, "");
+    static_assert(Images<DKB, KP>::keys <= 2 * DKB * kSheetImage, "");
 };
 
 template <typename T, int DKB, int KP>
 __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const DeltaGradParams q)
 {
     using Im = Images<DKB, KP>;
-    using Sm = RestSmem<DKB>;
-    constexpr uint32_t cX = 0, cE = 128, cX3 = 192, cK = 320, cKQ = 448;     // columns of tensor memory
+    using Sm = RestSmem<DKB, KP>;
+    constexpr uint32_t cX = 0, cX3 = 128, cK = 256, cE = 384, cKQ = 448, cKE = 384;     // columns of tensor memory
     extern __shared__ __align__(1024) unsigned char raw[];
-    __shared__ __align__(8) uint64_t bar[4], images, done;
+    __shared__ __align__(8) uint64_t first_full, g_full, k_full, x_done, x3_done, kq_done, k_done, done;
     __shared__ Sums sums;
-    __shared__ float scale[192], s_scale[128], g_scale[128], k_scale[C], q_scale[C];
-    __shared__ float fac[768];
-    __shared__ float rv[C], part[4][4][128], dots[kRestThreads / 32], slope[C], end[C];
+    __shared__ float k_scale[C], q_scale[C];
+    __shared__ float fac[768], scales[8];
+    __shared__ float rv[16][C], part[5][4][128], dots[kRestThreads / 32], slope[C], end[C], db[C];
     __shared__ double carry;
     __shared__ uint32_t slot;
     __shared__ int given_up;
@@ -473,18 +520,22 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[b][e] = 0.f;
     if (t0 >= len) {
-        for (int j = tid; j < steps * p.H; j += kRestThreads) {
-            const int t = j / p.H, h = j - t * p.H;
-            if (h / per != hk) continue;
+        for (int j = tid; j < steps * per; j += kRestThreads) {
+            const int t = j / per, h = hk * per + j % per;
             if (q.dg.data) static_cast<float*>(q.dg.data)[n * q.dg.bs + (t0 + t) * q.dg.ss + h] = 0.f;
             if (q.dbeta.data) static_cast<float*>(q.dbeta.data)[n * q.dbeta.bs + (t0 + t) * q.dbeta.ss + h] = 0.f;
         }
     } else {
         unsigned char* base = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
-        float *E = reinterpret_cast<float*>(base + Sm::e), *D = reinterpret_cast<float*>(base + Sm::d);
+        float* E = reinterpret_cast<float*>(base + Sm::e);
         if (tid == 0) {
-            for (int b = 0; b < 4; ++b) mbar_init(&bar[b], 1);
-            mbar_init(&images, 1);
+            mbar_init(&first_full, 1);
+            mbar_init(&g_full, 1);
+            mbar_init(&k_full, 1);
+            mbar_init(&x_done, 1);
+            mbar_init(&x3_done, 1);
+            mbar_init(&kq_done, 1);
+            mbar_init(&k_done, 1);
             mbar_init(&done, 1);
             given_up = 0;
             mbar_fence_init();
@@ -497,297 +548,348 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
         const unsigned sbase = __shfl_sync(0xffffffffu, smem_addr(base), 0);
         const bool leader = warp == 0 && elected();
         const int tiles = (DV + 127) / 128;
-        unsigned phase[3] = {0, 0, 0};      // of bar[0], of bar[1], of the rest (once a head)
+        const int64_t kept_tile = delta_kept_tile(DK), slopes_tile = delta_slopes_tile(DK, KP == 2 ? 0 : 1);
+        constexpr unsigned kStates = 2 * DKB * kSheetImage;
         // all threads wait, and know whether all did
-        auto await = [&](uint64_t* b, unsigned ph) {
-            const bool ok = __syncthreads_and(wait(b, ph, &given_up));
+        unsigned phase = 0;
+        float dot_all = 0.f;        // warp 0's
+        auto await = [&](uint64_t* b) {
+            fence_before();
+            const bool ok = __syncthreads_and(wait(b, phase, &given_up));
             fence_after();
             return ok;
         };
         bool ok = true;
-        for (int h = hk * per; h < (hk + 1) * per && ok; ++h) {
+        for (int round = 0; round < per * tiles; ++round) {
+            const int h = hk * per + round / tiles, tile = round % tiles, v0 = tile * 128;
             const int64_t nh = n * p.H + h, at = nh * chunks + chunk;
-            const float *us = p.us + at * C * DV, *drs = q.drs + at * C * DV, *states = p.states + at * DK * DV, *ends = q.ends + at * DK * DV;
-            const bool wide = DV % 4 == 0 && ((uintptr_t)p.us | (uintptr_t)p.states) % 16 == 0 && ((uintptr_t)q.drs | (uintptr_t)q.ends) % 16 == 0;
-            const bool yw = fours<T>(q.dY, DV), vw = fours<T>(p.V, DV);
-            for (int j = tid; j < 192; j += kRestThreads)
-                reinterpret_cast<float4*>(fac)[j] = reinterpret_cast<const float4*>(p.mats + at * Im::mats + 4 * kBlock)[j];
-            form_sums(sums, p.g, n, h, t0, len, &carry);
-            // a row's scale; where it has more values than a tile, its others are looked through first
-            auto row_scale = [&](const auto* row, bool in, bool vec, const float (&x)[4]) {
-                float m = row_most(x);
-                if (tiles > 1)
-                    for (int v = 0; v < DV; v += 128) {
-                        float z[1][4];
-                        load_fours<1>(row + v, 0, DV - v, vec, [&](int) { return in; }, z);
-                        m = fmaxf(m, row_most(z[0]));
-                    }
-                return scale_of(m);
-            };
-            float rv_mine = 0.f, dot = 0.f;     // lane l: the sum for the warp's l-th row of dR
-            for (int tile = 0; tile < tiles && ok; ++tile) {
-                const int v0 = tile * 128;
-                const bool second = DV - v0 > 64;       // two blocks of 64 values
-                const int left = DV - v0;
-                // a warp's rows: every 16th of U, dR, dY' and V, then of S0
-                auto step_in = [&](int a) { return t0 + warp + 16 * a < len; };
-                auto key_in = [&](int a) { return warp + 16 * a < DK; };
-                auto always = [](int) { return true; };
-                const float *u_row = us + warp * (int64_t)DV, *r_row = drs + warp * (int64_t)DV, *s_row = states + warp * (int64_t)DV;
-                const T* y_row = static_cast<const T*>(q.dY.data) + n * q.dY.bs + (t0 + warp) * q.dY.ss + (int64_t)h * DV;
-                const T* v_row = static_cast<const T*>(p.V.data) + n * p.V.bs + (t0 + warp) * p.V.ss + (int64_t)h * DV;
-                {
-                    float x[4][4], y[4][4], z[4][4], w[4][4];
-                    load_fours<4>(u_row + v0, 16 * (int64_t)DV, left, wide, always, x);
-                    load_fours<4>(r_row + v0, 16 * (int64_t)DV, left, wide, always, y);
-                    load_fours<4>(y_row + v0, 16 * q.dY.ss, left, yw, step_in, z);
-                    load_fours<4>(v_row + v0, 16 * p.V.ss, left, vw, step_in, w);
-#pragma unroll
-                    for (int a = 0; a < 4; ++a) {
-                        const int r = warp + 16 * a;
-                        const Scale su = row_scale(u_row + a * 16 * (int64_t)DV, true, wide, x[a]);
-                        const Scale sr = row_scale(r_row + a * 16 * (int64_t)DV, true, wide, y[a]);
-                        const Scale sy = row_scale(y_row + a * 16 * q.dY.ss, step_in(a), yw, z[a]);
-                        put_row<2, 2>(base + Sm::rows, Sm::row_block, r, x[a], su.down);
-                        put_row<2, 2>(base + Sm::rows, Sm::row_block, C + r, y[a], sr.down);
-                        put_row<2, 2>(base + Sm::rows, Sm::row_block, 2 * C + r, z[a], sy.down);
-                        float s = y[a][0] * w[a][0] + y[a][1] * w[a][1] + y[a][2] * w[a][2] + y[a][3] * w[a][3];
-#pragma unroll
-                        for (int o = 16; o; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-                        if (lane == a) rv_mine += s;
-                        if (lane == 0) {
-                            scale[r] = su.up;
-                            scale[C + r] = sr.up;
-                            scale[2 * C + r] = p.scale * sy.up;
-                        }
-                    }
-                }
-                {
-                    float x[DKB * 4][4];
-                    load_fours<DKB * 4>(s_row + v0, 16 * (int64_t)DV, left, wide, key_in, x);
-#pragma unroll
-                    for (int a = 0; a < DKB * 4; ++a) {
-                        const int d = warp + 16 * a;
-                        const Scale sc = row_scale(s_row + a * 16 * (int64_t)DV, d < DK, wide, x[a]);
-                        put_row<2, 2>(base + Sm::states, Sm::state_block, d, x[a], sc.down);
-                        if (lane == 0) s_scale[d] = sc.up;
-                    }
-                }
-                fence_shared();
-                __syncthreads();
-                const unsigned rows = sbase + Sm::rows, sts = sbase + Sm::states;
-                // parts a of the rows from `first` on, b of the other side, over the tile's values
-                auto product = [&](uint32_t d, int first, int a, unsigned other, unsigned apart, int b, int nn, bool add) {
-                    for (int blk = 0; blk < (second ? 2 : 1); ++blk)
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            if (leader)
-                                mma_ss(tm + d, desc_rows(rows + (a * 2 + blk) * Sm::row_block + first * 128 + ks * 32),
-                                       desc_rows(other + (b * 2 + blk) * apart + ks * 32), instr(nn, false), add || blk > 0 || ks > 0);
-                };
-                if (warp == 0) {
-                    product(cX, C, 0, sts, Sm::state_block, 0, DKB * 64, tile > 0);
-                    product(cX, C, 0, sts, Sm::state_block, 1, DKB * 64, true);
-                    product(cX, C, 1, sts, Sm::state_block, 0, DKB * 64, true);
-                    product(cE, C, 0, rows, Sm::row_block, 0, C, tile > 0);
-                    product(cE, C, 0, rows, Sm::row_block, 1, C, true);
-                    product(cE, C, 1, rows, Sm::row_block, 0, C, true);
-                    if (leader) mma_commit(&bar[0]);
-                }
-                // dS1 in the meantime, and <dS1, S0> with S0 as its parts have it
-                float g[DKB * 4][4];
-                const float* e_row = ends + warp * (int64_t)DV;
-                load_fours<DKB * 4>(e_row + v0, 16 * (int64_t)DV, left, wide, key_in, g);
-#pragma unroll
-                for (int a = 0; a < DKB * 4; ++a) {
-                    const int d = warp + 16 * a, c = lane * 4;
-                    const unsigned char* hi = base + Sm::states + c / 64 * Sm::state_block + swizzled(d, c % 64);
-                    const uint2 u = *reinterpret_cast<const uint2*>(hi), w = *reinterpret_cast<const uint2*>(hi + 2 * Sm::state_block);
-                    const float2 u0 = pair_value(u.x), u1 = pair_value(u.y), w0 = pair_value(w.x), w1 = pair_value(w.y);
-                    dot = fmaf(s_scale[d], g[a][0] * (u0.x + w0.x) + g[a][1] * (u0.y + w0.y) + g[a][2] * (u1.x + w1.x) + g[a][3] * (u1.y + w1.y), dot);
-                }
-                ok = await(&bar[0], phase[0]);
-                phase[0] ^= 1u;
-                if (!ok) break;
-#pragma unroll
-                for (int a = 0; a < DKB * 4; ++a) {
-                    const int d = warp + 16 * a;
-                    const Scale sc = row_scale(e_row + a * 16 * (int64_t)DV, d < DK, wide, g[a]);
-                    put_row<2, 2>(base + Sm::states, Sm::state_block, d, g[a], sc.down);
-                    if (lane == 0) g_scale[d] = sc.up;
-                }
-                fence_shared();
-                __syncthreads();
-                if (warp == 0) {
-                    product(cX3, 0, 0, sts, Sm::state_block, 0, DKB * 64, tile > 0);
-                    product(cX3, 0, 0, sts, Sm::state_block, 1, DKB * 64, true);
-                    product(cX3, 0, 1, sts, Sm::state_block, 0, DKB * 64, true);
-                    if (leader) mma_commit(&bar[1]);
-                }
-                ok = await(&bar[1], phase[1]);
-                phase[1] ^= 1u;
-            }
-            if (!ok) break;
-            if (lane < 4) rv[warp + 16 * lane] = rv_mine;
-#pragma unroll
-            for (int o = 16; o; o /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-            if (lane == 0) dots[warp] = dot;
+            const unsigned char *kept = p.kept + (at * tiles + tile) * kept_tile, *slopes = q.slopes + (at * tiles + tile) * slopes_tile;
+            const unsigned char* keys = p.keys + (nk * chunks + chunk) * Im::keys;
             if (tid == 0) {
-                mbar_arrive_expect_tx(&images, Im::keys);
-                bulk_g2s(base + Sm::states, p.keys + (nk * chunks + chunk) * Im::keys, Im::keys, &images);
+                mbar_arrive_expect_tx(&first_full, kStates + (4 + KP) * kSheetImage + (Sm::early ? Im::keys : 0));
+                bulk_g2s(base + Sm::r, slopes + kStates, kSheetImage, &first_full);
+                bulk_g2s(base + Sm::r + 2 * kSheetImage, slopes + kStates + kSheetImage, kSheetImage, &first_full);
+                bulk_g2s(base + Sm::y, slopes + kStates + 2 * kSheetImage, kSheetImage, &first_full);
+                if (KP == 2) bulk_g2s(base + Sm::y + 2 * kSheetImage, slopes + kStates + 3 * kSheetImage, kSheetImage, &first_full);
+                bulk_g2s(base + Sm::u, kept + kStates, 2 * kSheetImage, &first_full);
+                bulk_g2s(base + Sm::states, kept, kStates, &first_full);
+                if (Sm::early) bulk_g2s(base + Sm::keys, keys, Im::keys, &first_full);
             }
-            ok = await(&images, phase[2]);
-            if (!ok) break;
-            const unsigned kimg = sbase + Sm::states, qimg = kimg + kBlock;
-            if (warp == 0) {
+            if (KP == 1)            // 16-bit values have no second part
+                for (int j = tid; j < (int)kSheetImage / 16; j += kRestThreads)
+                    reinterpret_cast<uint4*>(base + Sm::y + 2 * kSheetImage)[j] = make_uint4(0, 0, 0, 0);
+            fence_shared();
+            if (tid < 192) reinterpret_cast<float4*>(fac)[tid] = reinterpret_cast<const float4*>(p.mats + at * Im::mats + 4 * kBlock)[tid];
+            if (tid == 192) {
+                const float* a = reinterpret_cast<const float*>(kept + kStates + 2 * kSheetImage);
+                const float* b = reinterpret_cast<const float*>(slopes + kStates + (2 + KP) * kSheetImage);
+                scales[0] = a[0], scales[1] = a[1], scales[2] = b[0], scales[3] = b[1], scales[4] = b[2];
+            }
+            // V at this thread's two steps and its warp's eight values
+            float vs[2][8];
+            {
+                const T* row = static_cast<const T*>(p.V.data) + n * p.V.bs + (t0 + 2 * lane) * p.V.ss + (int64_t)h * DV + v0 + warp * 8;
+                const int left = DV - v0 - warp * 8;
+                const bool vec = sizeof(T) == 2 && (uintptr_t)row % 16 == 0 && p.V.ss % 8 == 0 && left >= 8;
 #pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const bool in = t0 + 2 * lane + w < len;
+                    if (vec) {
+                        __align__(16) T x[8] = {};
+                        if (in) *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(row + w * p.V.ss);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) vs[w][e] = to_f(x[e]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) vs[w][e] = in && e < left ? to_f(row[w * p.V.ss + e]) : 0.f;
+                    }
+                }
+            }
+            form_sums(sums, p.g, n, h, t0, len, &carry);
+            const float s_up = scales[0], u_up = scales[1], g_up = scales[2], r_up = scales[3], y_up = p.scale * scales[4];
+            ok = await(&first_full);
+            if (!ok) break;
+            const unsigned kimg = sbase + Sm::keys, qimg = kimg + kBlock;
+            auto key_products = [&] {
+#pragma unroll 1
                 for (int r = 0; r < 2 * KP - 1; ++r)         // hi hi, lo hi, hi lo
 #pragma unroll
                     for (int ks = 0; ks < DKB * 4; ++ks)
                         if (leader)
                             mma_ss(tm + cKQ, desc_rows(kimg + ((r == 1) * DKB + ks / 4) * 2 * kBlock + ks % 4 * 32),
                                    desc_rows(kimg + ((r == 2) * DKB + ks / 4) * 2 * kBlock + ks % 4 * 32), instr(C, false), r > 0 || ks > 0);
-                if (leader) mma_commit(&bar[2]);
+                if (leader) mma_commit(&kq_done);
+            };
+            if (warp == 0) {
+#pragma unroll 1
+                for (int r = 0; r < 3; ++r)     // [dR; dY'] S0^T: hi hi, lo hi, hi lo
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        if (leader)
+                            mma_ss(tm + cX, desc_columns(sbase + Sm::r + (r == 1) * 2 * kSheetImage + ks * 2048, kSheetImage),
+                                   desc_columns(sbase + Sm::states + (r == 2) * DKB * kSheetImage + ks * 2048, kSheetImage), instr(DKB * 64, true) | 1u << 15,
+                                   r > 0 || ks > 0);
+#pragma unroll 1
+                for (int r = 0; r < 3; ++r)     // [dR; dY'] U^T
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        if (leader)
+                            mma_ss(tm + cE, desc_columns(sbase + Sm::r + (r == 1) * 2 * kSheetImage + ks * 2048, kSheetImage),
+                                   desc_columns(sbase + Sm::u + (r == 2) * kSheetImage + ks * 2048, kSheetImage), instr(C, true) | 1u << 15, r > 0 || ks > 0);
+                if (leader) mma_commit(&x_done);
+                if (Sm::early) key_products();
             }
-            ok = await(&bar[2], phase[2]);
-            if (!ok) break;
-            const float b_i = fac[kBeta + i];
+            // dR . V, a warp's eight values of all steps
             {
-                float e[16], kq[16], row = 0.f, db = 0.f;
+                float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int d = warp * 8 + e;
+                    const unsigned char* at_r = base + Sm::r + d * 128 + (((lane >> 2) ^ (d & 7)) << 4) + lane % 4 * 4;
+                    const float2 a = pair_value(*reinterpret_cast<const unsigned*>(at_r)), b = pair_value(*reinterpret_cast<const unsigned*>(at_r + 2 * kSheetImage));
+                    s0 = fmaf(a.x + b.x, vs[0][e], s0);
+                    s1 = fmaf(a.y + b.y, vs[1][e], s1);
+                }
+                rv[warp][2 * lane] = s0;
+                rv[warp][2 * lane + 1] = s1;
+            }
+            ok = await(&x_done);
+            if (!ok) break;
+            // S0 to registers, dS1 in its place
+            uint4 s0[DKB][4];
+#pragma unroll
+            for (int b = 0; b < DKB; ++b)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const unsigned char* from = base + Sm::states + (b * 2 + c) * (kSheetImage / 2) + tid * 16;
+                    s0[b][c] = *reinterpret_cast<const uint4*>(from);
+                    s0[b][2 + c] = *reinterpret_cast<const uint4*>(from + DKB * kSheetImage);
+                }
+            fence_shared();
+            __syncthreads();
+            if (tid == 0) {
+                mbar_arrive_expect_tx(&g_full, kStates);
+                bulk_g2s(base + Sm::states, slopes, kStates, &g_full);
+            }
+            const float b_i = fac[kBeta + i];
+            auto form_e = [&] {
+                float e[16], kq[16], row = 0.f, s = 0.f;
                 tmem_ld16(my + cE + quarter * 16, e);
                 tmem_ld16(my + cKQ + quarter * 16, kq);
-                const float mine = scale[upper ? C + i : 128 + i], es = fac[(upper ? kKeyScale : kQueryScale) + i];
+                const float mine = (upper ? -r_up : y_up) * u_up, es = fac[(upper ? kKeyScale : kQueryScale) + i];
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
                     const int j = quarter * 16 + c;
                     const bool in = upper ? j < i : j <= i;
                     const float decay = in ? expf(sums.between(i, j)) : 0.f;
-                    const float d = in ? (upper ? -e[c] : e[c]) * (mine * scale[j]) * decay : 0.f;
+                    const float d = in ? e[c] * mine * decay : 0.f;
                     const float k = in ? kq[c] * (es * fac[kKeyScale + j]) : 0.f;
                     const float v = upper ? b_i * d : d;
-                    db = fmaf(d, k, db);
+                    s = fmaf(d, k, s);
                     E[lane_row * C + (j ^ lane)] = v;
-                    D[lane_row * C + (j ^ lane)] = v * k;
                     row = fmaf(v, k, row);
                 }
                 part[0][quarter][lane_row] = row;
-                part[1][quarter][lane_row] = db;
+                part[1][quarter][lane_row] = s;
+            };
+            if (Sm::early) {
+                ok = await(&kq_done);
+                if (!ok) break;
+                form_e();
             }
-            __syncthreads();
-            // rows of [EA + EA^T; EP] and [EP^T; 0], times the scales of K's and Q's rows
-            auto pair_to = [&](unsigned img, int r, const float (&v)[2], float down) {
+            ok = await(&g_full);
+            if (!ok) break;
+            if (warp == 0) {
+#pragma unroll 1
+                for (int r = 0; r < 3; ++r)     // U dS1^T
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        if (leader)
+                            mma_ss(tm + cX3, desc_columns(sbase + Sm::u + (r == 1) * kSheetImage + ks * 2048, kSheetImage),
+                                   desc_columns(sbase + Sm::states + (r == 2) * DKB * kSheetImage + ks * 2048, kSheetImage), instr(DKB * 64, true) | 1u << 15,
+                                   r > 0 || ks > 0);
+                if (leader) mma_commit(&x3_done);
+            }
+            {   // <dS1, S0>
+                float dot = 0.f;
+#pragma unroll
+                for (int b = 0; b < DKB; ++b)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const unsigned char* from = base + Sm::states + (b * 2 + c) * (kSheetImage / 2) + tid * 16;
+                        const uint4 gh = *reinterpret_cast<const uint4*>(from), gl = *reinterpret_cast<const uint4*>(from + DKB * kSheetImage);
+                        const unsigned gs[8] = {gh.x, gh.y, gh.z, gh.w, gl.x, gl.y, gl.z, gl.w};
+                        const unsigned ss[8] = {s0[b][c].x, s0[b][c].y, s0[b][c].z, s0[b][c].w, s0[b][2 + c].x, s0[b][2 + c].y, s0[b][2 + c].z, s0[b][2 + c].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 a = pair_value(gs[e]), al = pair_value(gs[4 + e]), z = pair_value(ss[e]), zl = pair_value(ss[4 + e]);
+                            dot = fmaf(a.x + al.x, z.x + zl.x, fmaf(a.y + al.y, z.y + zl.y, dot));
+                        }
+                    }
+#pragma unroll
+                for (int o = 16; o; o /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                if (lane == 0) dots[warp] = dot * (g_up * s_up);
+            }
+            ok = await(&x3_done);
+            if (!ok) break;
+            if (!Sm::early) {
+                fence_shared();
+                __syncthreads();
+                if (tid == 0) {
+                    mbar_arrive_expect_tx(&k_full, Im::keys);
+                    bulk_g2s(base + Sm::keys, keys, Im::keys, &k_full);
+                }
+                ok = await(&k_full);
+                if (!ok) break;
+                if (warp == 0) key_products();
+                ok = await(&kq_done);
+                if (!ok) break;
+                form_e();
+                __syncthreads();
+            }
+            // rows of [EA + EA^T; EP] and EP^T, times the scales of K's and Q's rows
+            auto pair_to = [&](unsigned img, unsigned second, int r, const float (&v)[2], float down) {
                 unsigned hi, lo;
                 split_pair(v[0] * down, v[1] * down, hi, lo);
                 unsigned char* to = base + img + swizzled(r, 2 * lane);
                 *reinterpret_cast<unsigned*>(to) = hi;
-                *reinterpret_cast<unsigned*>(to + 2 * kBlock) = lo;
+                *reinterpret_cast<unsigned*>(to + second) = lo;
             };
             auto at_e = [&](int r, int j) { return E[r * C + (j ^ (r & 31))]; };
-            for (int r = warp; r < C; r += 16) {
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                const int r = warp + 16 * a;
                 float ea[2], ep[2], et[2], mk = 0.f, mq = 0.f;
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     const int j = 2 * lane + w;
-                    ea[w] = (at_e(r, j) + at_e(j, r)) * fac[kKeyScale + j];
-                    ep[w] = at_e(C + r, j) * fac[kKeyScale + j];
+                    const float ks = fac[kKeyScale + j];
+                    ea[w] = (at_e(r, j) + at_e(j, r)) * ks;
+                    ep[w] = at_e(C + r, j) * ks;
                     et[w] = at_e(C + j, r) * fac[kQueryScale + j];
                     mk = fmaxf(mk, fmaxf(fabsf(ea[w]), fabsf(et[w])));
                     mq = fmaxf(mq, fabsf(ep[w]));
                 }
-#pragma unroll
-                for (int o = 16; o; o /= 2) {
-                    mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-                    mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, o));
-                }
-                const Scale sk = scale_of(mk), sq = scale_of(mq);
-                pair_to(Sm::a1, r, ea, sk.down);
-                pair_to(Sm::a1, C + r, ep, sq.down);
-                pair_to(Sm::a2, r, et, sk.down);
-                const float zero[2] = {0.f, 0.f};
-                pair_to(Sm::a2, C + r, zero, 1.f);
+                const Scale sk = scale_of(warp_most(mk)), sq = scale_of(warp_most(mq));
+                pair_to(Sm::a1, kSheetImage, r, ea, sk.down);
+                pair_to(Sm::a1, kSheetImage, C + r, ep, sq.down);
+                pair_to(Sm::a2, kBlock, r, et, sk.down);
                 if (lane == 0) k_scale[r] = sk.up, q_scale[r] = sq.up;
             }
             fence_shared();
             __syncthreads();
             if (warp == 0) {
+#pragma unroll 1
+                for (int r = 0; r < 1 + KP; ++r)    // hi hi, lo hi, hi lo
 #pragma unroll
-                for (int w = 0; w < 2; ++w)             // with K, with Q
+                    for (int ks = 0; ks < 4; ++ks)
+                        if (leader)
+                            mma_ss(tm + cK, desc_rows(sbase + Sm::a1 + (r == 1) * kSheetImage + ks * 32),
+                                   desc_columns(kimg + (r == 2) * DKB * 2 * kBlock + ks * 2048, 2 * kBlock), instr(DKB * 64, true), r > 0 || ks > 0);
+#pragma unroll 1
+                for (int r = 0; r < 1 + KP; ++r)
 #pragma unroll
-                    for (int r = 0; r < 1 + KP; ++r)    // hi hi, lo hi, hi lo
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            if (leader)
-                                mma_ss(tm + cK, desc_rows(sbase + (w ? Sm::a2 : Sm::a1) + (r == 1) * 2 * kBlock + ks * 32),
-                                       desc_columns((w ? qimg : kimg) + (r == 2) * DKB * 2 * kBlock + ks * 2048, 2 * kBlock), instr(DKB * 64, true),
-                                       w > 0 || r > 0 || ks > 0);
-                if (leader) mma_commit(&bar[3]);
+                    for (int ks = 0; ks < 4; ++ks)
+                        if (leader)
+                            mma_ss(tm + cKE, desc_rows(sbase + Sm::a2 + (r == 1) * kBlock + ks * 32),
+                                   desc_columns(qimg + (r == 2) * DKB * 2 * kBlock + ks * 2048, 2 * kBlock), instr(DKB * 64, true), r > 0 || ks > 0);
+                if (leader) mma_commit(&k_done);
             }
             // in the meantime what the states give, and its sums with K and Q
+            const float es = fac[(upper ? kKeyScale : kQueryScale) + i];
+            const unsigned char* krow = base + Sm::keys + (upper ? 0 : kBlock);
+            auto key_values = [&](int c0, float (&k)[16]) {
+#pragma unroll
+                for (int c8 = 0; c8 < 2; ++c8) {
+                    const unsigned char* row = krow + (c0 / 64) * 2 * kBlock + swizzled(i, c0 % 64 + c8 * 8);
+                    const uint4 hi = *reinterpret_cast<const uint4*>(row);
+                    uint4 lo = make_uint4(0, 0, 0, 0);
+                    if (KP == 2) lo = *reinterpret_cast<const uint4*>(row + DKB * 2 * kBlock);
+                    const unsigned his[4] = {hi.x, hi.y, hi.z, hi.w}, los[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const float2 a = pair_value(his[c]), b = pair_value(los[c]);
+                        k[c8 * 8 + 2 * c] = KP == 2 ? a.x + b.x : a.x;
+                        k[c8 * 8 + 2 * c + 1] = KP == 2 ? a.y + b.y : a.y;
+                    }
+                }
+            };
+            float own = 0.f;            // this quarter's part of k_i.dK_i or q_i.dQ_i
             {
                 const float first = expf(sums.hi[i] + sums.lo[i]), last = expf(sums.between(C - 1, i));
-                const float mine = scale[upper ? C + i : 128 + i], own = scale[i];
-                const float es = fac[(upper ? kKeyScale : kQueryScale) + i];
-                const unsigned char* img = base + Sm::states + (upper ? 0 : kBlock);
+                const float fx = (upper ? -b_i * r_up : y_up) * s_up * first, f3 = upper ? last * (u_up * g_up) : 0.f;
                 float s1 = 0.f, s3 = 0.f;
 #pragma unroll
                 for (int b = 0; b < DKB; ++b) {
                     const int c0 = quarter * DKB * 16 + b * 16;
-                    float x1[16], x3[16];
-                    tmem_ld16(my + cX + c0, x1);
-                    tmem_ld16(my + cX3 + c0, x3);
+                    float x[16], k[16];
+                    key_values(c0, k);
+                    tmem_ld16(my + cX + c0, x);
 #pragma unroll
-                    for (int c8 = 0; c8 < 2; ++c8) {
-                        const unsigned char* row = img + (c0 / 64) * 2 * kBlock + swizzled(i, c0 % 64 + c8 * 8);
-                        const uint4 hi = *reinterpret_cast<const uint4*>(row);
-                        uint4 lo = make_uint4(0, 0, 0, 0);
-                        if (KP == 2) lo = *reinterpret_cast<const uint4*>(row + DKB * 2 * kBlock);
-                        const unsigned his[4] = {hi.x, hi.y, hi.z, hi.w}, los[4] = {lo.x, lo.y, lo.z, lo.w};
+                    for (int c = 0; c < 16; ++c) {
+                        s1 = fmaf(k[c], x[c], s1);
+                        acc[b][c] = fmaf(fx, x[c], acc[b][c]);
+                    }
+                    if (upper) {        // (whole warps are)
+                        tmem_ld16(my + cX3 + c0, x);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const int cc = c8 * 8 + c;
-                            const float2 u = pair_value(his[c / 2]), w = pair_value(los[c / 2]);
-                            const float k = (c % 2 ? u.y : u.x) + (KP == 2 ? (c % 2 ? w.y : w.x) : 0.f);
-                            const float a = x1[cc] * (mine * s_scale[c0 + cc]), z = x3[cc] * (own * g_scale[c0 + cc]);
-                            s1 = fmaf(k, a, s1);
-                            s3 = fmaf(k, z, s3);
-                            acc[b][cc] += upper ? last * z - b_i * first * a : first * a;
+                        for (int c = 0; c < 16; ++c) {
+                            s3 = fmaf(k[c], x[c], s3);
+                            acc[b][c] = fmaf(f3, x[c], acc[b][c]);
                         }
                     }
                 }
-                part[2][quarter][lane_row] = s1 * es;
-                part[3][quarter][lane_row] = s3 * es;
+                own = fx * s1 + f3 * s3;
+                part[2][quarter][lane_row] = es * (r_up * s_up * first) * s1;       // e^G k.X2 (of the upper half)
+                part[3][quarter][lane_row] = es * f3 * s3;      // e^(G_last - G) k.X3
             }
-            ok = await(&bar[3], phase[2]);
-            phase[2] ^= 1u;
+            ok = await(&k_done);
             if (!ok) break;
             {
                 const float mine = upper ? k_scale[i] : q_scale[i];
+                float s = 0.f;
 #pragma unroll
                 for (int b = 0; b < DKB; ++b) {
-                    float x[16];
-                    tmem_ld16(my + cK + quarter * DKB * 16 + b * 16, x);
+                    const int c0 = quarter * DKB * 16 + b * 16;
+                    float x[16], k[16];
+                    key_values(c0, k);
+                    tmem_ld16(my + cK + c0, x);
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) acc[b][c] = fmaf(mine, x[c], acc[b][c]);
+                    for (int c = 0; c < 16; ++c) {
+                        s = fmaf(k[c], x[c], s);
+                        acc[b][c] = fmaf(mine, x[c], acc[b][c]);
+                    }
+                    if (upper) {
+                        tmem_ld16(my + cKE + c0, x);
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            s = fmaf(k[c], x[c], s);
+                            acc[b][c] = fmaf(mine, x[c], acc[b][c]);
+                        }
+                    }
                 }
+                part[4][quarter][lane_row] = es * (own + mine * s);
             }
+            fence_before();
+            __syncthreads();
+            fence_after();
             // the decays' slopes, and their sums from each step to the chunk's end
             if (tid < C) {
-                const float first = expf(sums.hi[tid] + sums.lo[tid]), last = expf(sums.between(C - 1, tid)), b = fac[kBeta + tid];
-                float rowsum = 0.f, db = 0.f, qx1 = 0.f, kx2 = 0.f, kx3 = 0.f, column = 0.f;
+                float ea = 0.f, s = 0.f, kx2 = 0.f, kx3 = 0.f, qdq = 0.f, kdk = 0.f, v = 0.f;
+#pragma unroll
                 for (int w = 0; w < 4; ++w) {
-                    rowsum += part[0][w][tid] + part[0][w][C + tid];
-                    db += part[1][w][tid];
+                    ea += part[0][w][tid];
+                    s += part[1][w][tid];
                     kx2 += part[2][w][tid];
-                    qx1 += part[2][w][C + tid];
                     kx3 += part[3][w][tid];
+                    kdk += part[4][w][tid];
+                    qdq += part[4][w][C + tid];
                 }
-                for (int r = 0; r < 128; ++r) column += D[r * C + (tid ^ (r & 31))];
-                kx3 *= last;
-                end[tid] = kx3;
-                slope[tid] = rowsum - column + first * (qx1 - b * kx2) - kx3;
-                const bool step = t0 + tid < len;
-                if (q.dbeta.data && tid < steps)
-                    static_cast<float*>(q.dbeta.data)[n * q.dbeta.bs + (t0 + tid) * q.dbeta.ss + h] = step ? db + rv[tid] - first * kx2 : 0.f;
+#pragma unroll
+                for (int w = 0; w < 16; ++w) v += rv[w][tid];
+                slope[tid] = (tile ? slope[tid] : 0.f) + (qdq - kdk) + 2.f * (ea - fac[kBeta + tid] * kx2);
+                end[tid] = (tile ? end[tid] : 0.f) + kx3;
+                db[tid] = (tile ? db[tid] : 0.f) + s + v * r_up - kx2;
             }
             __syncthreads();
             if (tid < 32) {
@@ -796,25 +898,33 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                     all += __shfl_xor_sync(0xffffffffu, all, o);
                     d += __shfl_xor_sync(0xffffffffu, d, o);
                 }
-                all += fac[kWhole] * d;
-                float hi = slope[tid + 32], lo = slope[tid];
-                if (tid == 31) hi += all;
-                for (int o = 1; o < 32; o *= 2) {
-                    const float a = __shfl_down_sync(0xffffffffu, hi, o), b = __shfl_down_sync(0xffffffffu, lo, o);
-                    if (tid + o < 32) {
-                        hi += a;
-                        lo += b;
+                dot_all = (tile ? dot_all : 0.f) + d;
+                if (tile == tiles - 1) {
+                    float hi = slope[tid + 32], lo = slope[tid];
+                    if (tid == 31) hi += all + fac[kWhole] * dot_all;
+                    for (int o = 1; o < 32; o *= 2) {
+                        const float a = __shfl_down_sync(0xffffffffu, hi, o), b = __shfl_down_sync(0xffffffffu, lo, o);
+                        if (tid + o < 32) {
+                            hi += a;
+                            lo += b;
+                        }
+                    }
+                    lo += __shfl_sync(0xffffffffu, hi, 0);
+                    float* dg = static_cast<float*>(q.dg.data) + n * q.dg.bs + h;
+                    float* dbeta = static_cast<float*>(q.dbeta.data) + n * q.dbeta.bs + h;
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        const int t = tid + 32 * w;
+                        if (t >= steps) continue;
+                        const bool step = t0 + t < len;
+                        if (q.dg.data) dg[(t0 + t) * q.dg.ss] = step ? (w ? hi : lo) : 0.f;
+                        if (q.dbeta.data) dbeta[(t0 + t) * q.dbeta.ss] = step ? db[t] : 0.f;
                     }
                 }
-                lo += __shfl_sync(0xffffffffu, hi, 0);
-                if (q.dg.data) {
-                    float* dg = static_cast<float*>(q.dg.data) + n * q.dg.bs + h;
-                    if (tid < steps) dg[(t0 + tid) * q.dg.ss] = t0 + tid < len ? lo : 0.f;
-                    if (tid + 32 < steps) dg[(t0 + tid + 32) * q.dg.ss] = t0 + tid + 32 < len ? hi : 0.f;
-                }
             }
+            phase ^= 1u;
             fence_before();
-            __syncthreads();        // the next head's rows take the place of this one's
+            __syncthreads();        // the next round's images take the place of this one's
             fence_after();
         }
         if (!ok && warp == 0) {     // no product is in flight when the block ends
@@ -859,7 +969,7 @@ template <typename T, int DKB>
 cudaError_t run(const DeltaGradParams& q, cudaStream_t st, int* launches)
 {
     constexpr int KP = sizeof(T) == 4 ? 2 : 1;
-    constexpr size_t chain_smem = ChainSmem<T, DKB, KP>::bytes, rest_smem = RestSmem<DKB>::bytes;
+    constexpr size_t chain_smem = ChainSmem<T, DKB, KP>::bytes, rest_smem = RestSmem<DKB, KP>::bytes;
     static std::atomic<uint64_t> chain_done{0}, rest_done{0};
     cudaError_t e = allow_shared(delta_grad_chain_kernel<T, DKB, KP>, chain_smem, chain_done);
     if (e == cudaSuccess) e = allow_shared(delta_grad_rest_kernel<T, DKB, KP>, rest_smem, rest_done);
