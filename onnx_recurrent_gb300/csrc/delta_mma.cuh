@@ -394,14 +394,17 @@ inline dim3 heads_grid(int64_t x, int64_t nh)
 }
 
 
-// What a chain keeps of a chunk for the gradient's second launch, for each tile of 128 values: [value][...] rows in two
-// parts under one scale a tile (their sums run over the values), swizzled as products take them.
-constexpr unsigned kSheetImage = 128 * 128;     // 128 values' rows of 64 steps or keys
-// N pairs of values as 16-byte pieces from `piece` on of row r of an image and of its second part.
+// What a chain keeps of a chunk for the gradient's second launch, for each tile of 128 values: matrices [value][step or key] in two
+// parts under one scale a tile (the products' sums run over the values).  They lie without a swizzle, eight steps or keys (16
+// bytes) of all 128 values one after another, so that the 32 lanes of a chain's warp, a value each, write 512 bytes together
+// (rows of 128 bytes, swizzled, took a store 32 lines: 4600 clocks a chunk instead of 800).
+constexpr unsigned kSheetImage = 128 * 128;     // 128 values of 64 steps or keys
+constexpr unsigned kPiece = 128 * 16;
 template <int N>
 __device__ __forceinline__ void keep_parts(unsigned char* image, unsigned second, int r, int piece, const f2* v, float down)
 {
     const f2 d = dup2(down), m = dup2(6144.f), mm = dup2(-6144.f), minus = dup2(-1.f);
+    unsigned char* at = image + piece * kPiece + r * 16;
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
         unsigned hi[4], lo[4];
@@ -414,10 +417,15 @@ __device__ __forceinline__ void keep_parts(unsigned char* image, unsigned second
             unpack2(fma2(v[4 * i + e], d, mul2(a, minus)), x, y);
             lo[e] = half_pair(x, y);
         }
-        unsigned char* at = image + r * 128 + (((piece + i) ^ (r & 7)) << 4);
-        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(at + second) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4*>(at + i * kPiece) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(at + i * kPiece + second) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
+}
+// Descriptor of such a matrix, the sum along the values, from value 16 ks on: 128 bytes from 8 values to the next, kPiece
+// from 8 steps or keys to the next.
+__device__ __forceinline__ uint64_t desc_kept(unsigned saddr, int ks)
+{
+    return (uint64_t)(((saddr + ks * 256) >> 4) & 0x3FFFu) | (uint64_t)(128u >> 4) << 16 | (uint64_t)(kPiece >> 4) << 32 | (uint64_t)1u << 46;
 }
 // The largest of a block's 256 threads' values, which their warps have left in `most`.
 __device__ __forceinline__ float most_of_warps(const float (&most)[8])

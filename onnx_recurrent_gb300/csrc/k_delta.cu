@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
             if (k == live) break;
             if (kept) {
                 const Scale one = scale_of(most_of_warps(warps_most[0]));
-                keep_parts<SR / 2>(kept + (DKB == 2 ? half * kSheetImage : 0), DKB * kSheetImage, row, DKB == 2 ? 0 : half * 4, S, one.down);
+                keep_parts<SR / 2>(kept, DKB * kSheetImage, row, d0 / 8, S, one.down);
                 if (threadIdx.x == 0) *reinterpret_cast<float*>(kept + (2 * DKB + 2) * kSheetImage) = one.up;
             }
             ok = ok && wait(&full[s], (unsigned)(k / ST) & 1u, &given_up);

@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_grad_chain_kernel(cons
                         unsigned v[4];
 #pragma unroll
                         for (int e2 = 0; e2 < 4; ++e2) v[e2] = raw_pair<__half>(mul2(raw_y[4 * i + e2], d));
-                        *reinterpret_cast<uint4*>(kept + kY + row * 128 + (((half * 4 + i) ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                        *reinterpret_cast<uint4*>(kept + kY + (half * 4 + i) * kPiece + row * 16) = make_uint4(v[0], v[1], v[2], v[3]);
                     }
                 }
             }
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_grad_chain_kernel(cons
             const int64_t chunk = live - 1 - k;
             {
                 const Scale one = scale_of(most_of_warps(warps_most[0]));
-                keep_parts<SR / 2>(kept + (DKB == 2 ? half * kSheetImage : 0), DKB * kSheetImage, row, DKB == 2 ? 0 : half * 4, G, one.down);
+                keep_parts<SR / 2>(kept, DKB * kSheetImage, row, d0 / 8, G, one.down);
                 if (threadIdx.x == 0) *reinterpret_cast<float*>(kept + kScales) = one.up;
             }
             const float* fac = stage_of(k);
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
     __shared__ Sums sums;
     __shared__ float k_scale[C], q_scale[C];
     __shared__ float fac[768], scales[8];
-    __shared__ float rv[16][C], part[5][4][128], dots[kRestThreads / 32], slope[C], end[C], db[C];
+    __shared__ float rv[C], part[5][4][128], dots[kRestThreads / 32], slope[C], end[C], db[C];
     __shared__ double carry;
     __shared__ uint32_t slot;
     __shared__ int given_up;
@@ -585,25 +585,15 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                 const float* b = reinterpret_cast<const float*>(slopes + kStates + (2 + KP) * kSheetImage);
                 scales[0] = a[0], scales[1] = a[1], scales[2] = b[0], scales[3] = b[1], scales[4] = b[2];
             }
-            // V at this thread's two steps and its warp's eight values
-            float vs[2][8];
+            // V at the warp's four steps, four values 32 apart a lane
+            T vs[4][4];
             {
-                const T* row = static_cast<const T*>(p.V.data) + n * p.V.bs + (t0 + 2 * lane) * p.V.ss + (int64_t)h * DV + v0 + warp * 8;
-                const int left = DV - v0 - warp * 8;
-                const bool vec = sizeof(T) == 2 && (uintptr_t)row % 16 == 0 && p.V.ss % 8 == 0 && left >= 8;
+                const T* row = static_cast<const T*>(p.V.data) + n * p.V.bs + (t0 + warp * 4) * p.V.ss + (int64_t)h * DV + v0 + lane;
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const bool in = t0 + 2 * lane + w < len;
-                    if (vec) {
-                        __align__(16) T x[8] = {};
-                        if (in) *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(row + w * p.V.ss);
+                for (int t = 0; t < 4; ++t)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) vs[w][e] = to_f(x[e]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) vs[w][e] = in && e < left ? to_f(row[w * p.V.ss + e]) : 0.f;
-                    }
-                }
+                    for (int e = 0; e < 4; ++e)
+                        vs[t][e] = t0 + warp * 4 + t < len && v0 + lane + 32 * e < DV ? row[t * p.V.ss + 32 * e] : from_f<T>(0.f);
             }
             form_sums(sums, p.g, n, h, t0, len, &carry);
             const float s_up = scales[0], u_up = scales[1], g_up = scales[2], r_up = scales[3], y_up = p.scale * scales[4];
@@ -622,36 +612,70 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
             };
             if (warp == 0) {
 #pragma unroll 1
-                for (int r = 0; r < 3; ++r)     // [dR; dY'] S0^T: hi hi, lo hi, hi lo
+                for (int r = 0; r < 3; ++r)     // [dR; dY'] U^T: hi hi, lo hi, hi lo
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
                         if (leader)
-                            mma_ss(tm + cX, desc_columns(sbase + Sm::r + (r == 1) * 2 * kSheetImage + ks * 2048, kSheetImage),
-                                   desc_columns(sbase + Sm::states + (r == 2) * DKB * kSheetImage + ks * 2048, kSheetImage), instr(DKB * 64, true) | 1u << 15,
-                                   r > 0 || ks > 0);
-#pragma unroll 1
-                for (int r = 0; r < 3; ++r)     // [dR; dY'] U^T
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        if (leader)
-                            mma_ss(tm + cE, desc_columns(sbase + Sm::r + (r == 1) * 2 * kSheetImage + ks * 2048, kSheetImage),
-                                   desc_columns(sbase + Sm::u + (r == 2) * kSheetImage + ks * 2048, kSheetImage), instr(C, true) | 1u << 15, r > 0 || ks > 0);
-                if (leader) mma_commit(&x_done);
+                            mma_ss(tm + cE, desc_kept(sbase + Sm::r + (r == 1) * 2 * kSheetImage, ks), desc_kept(sbase + Sm::u + (r == 2) * kSheetImage, ks),
+                                   instr(C, true) | 1u << 15, r > 0 || ks > 0);
                 if (Sm::early) key_products();
-            }
-            // dR . V, a warp's eight values of all steps
-            {
-                float s0 = 0.f, s1 = 0.f;
+#pragma unroll 1
+                for (int r = 0; r < 3; ++r)     // [dR; dY'] S0^T
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int d = warp * 8 + e;
-                    const unsigned char* at_r = base + Sm::r + d * 128 + (((lane >> 2) ^ (d & 7)) << 4) + lane % 4 * 4;
-                    const float2 a = pair_value(*reinterpret_cast<const unsigned*>(at_r)), b = pair_value(*reinterpret_cast<const unsigned*>(at_r + 2 * kSheetImage));
-                    s0 = fmaf(a.x + b.x, vs[0][e], s0);
-                    s1 = fmaf(a.y + b.y, vs[1][e], s1);
+                    for (int ks = 0; ks < 8; ++ks)
+                        if (leader)
+                            mma_ss(tm + cX, desc_kept(sbase + Sm::r + (r == 1) * 2 * kSheetImage, ks),
+                                   desc_kept(sbase + Sm::states + (r == 2) * DKB * kSheetImage, ks), instr(DKB * 64, true) | 1u << 15, r > 0 || ks > 0);
+                if (leader) mma_commit(&x_done);
+            }
+            {   // dR . V
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const unsigned char* from = base + Sm::r + warp / 2 * kPiece + warp % 2 * 8 + lane * 16;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint2 a = *reinterpret_cast<const uint2*>(from + e * 512), b = *reinterpret_cast<const uint2*>(from + e * 512 + 2 * kSheetImage);
+                    const float2 a0 = pair_value(a.x), a1 = pair_value(a.y), b0 = pair_value(b.x), b1 = pair_value(b.y);
+                    sum[0] = fmaf(a0.x + b0.x, to_f(vs[0][e]), sum[0]);
+                    sum[1] = fmaf(a0.y + b0.y, to_f(vs[1][e]), sum[1]);
+                    sum[2] = fmaf(a1.x + b1.x, to_f(vs[2][e]), sum[2]);
+                    sum[3] = fmaf(a1.y + b1.y, to_f(vs[3][e]), sum[3]);
                 }
-                rv[warp][2 * lane] = s0;
-                rv[warp][2 * lane + 1] = s1;
+#pragma unroll
+                for (int o = 16; o; o /= 2)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) sum[t] += __shfl_xor_sync(0xffffffffu, sum[t], o);
+                if (lane < 4) rv[warp * 4 + lane] = lane == 0 ? sum[0] : lane == 1 ? sum[1] : lane == 2 ? sum[2] : sum[3];
+            }
+            const float b_i = fac[kBeta + i];
+            float e[16];
+            auto form_e = [&] {
+                float kq[16], row = 0.f, s = 0.f;
+                tmem_ld16(my + cE + quarter * 16, e);
+                tmem_ld16(my + cKQ + quarter * 16, kq);
+                const float mine = (upper ? -r_up : y_up) * u_up, es = fac[(upper ? kKeyScale : kQueryScale) + i];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const int j = quarter * 16 + c;
+                    const bool in = upper ? j < i : j <= i;
+                    const float decay = in ? expf(sums.between(i, j)) : 0.f;
+                    const float d = in ? e[c] * mine * decay : 0.f;
+                    const float k = in ? kq[c] * (es * fac[kKeyScale + j]) : 0.f;
+                    const float v = upper ? b_i * d : d;
+                    s = fmaf(d, k, s);
+                    e[c] = v;
+                    row = fmaf(v, k, row);
+                }
+                part[0][quarter][lane_row] = row;
+                part[1][quarter][lane_row] = s;
+            };
+            auto put_e = [&] {
+#pragma unroll
+                for (int c = 0; c < 16; ++c) E[lane_row * C + ((quarter * 16 + c) ^ lane)] = e[c];
+            };
+            if (Sm::early) {
+                ok = await(&kq_done);
+                if (!ok) break;
+                form_e();
             }
             ok = await(&x_done);
             if (!ok) break;
@@ -671,32 +695,7 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                 mbar_arrive_expect_tx(&g_full, kStates);
                 bulk_g2s(base + Sm::states, slopes, kStates, &g_full);
             }
-            const float b_i = fac[kBeta + i];
-            auto form_e = [&] {
-                float e[16], kq[16], row = 0.f, s = 0.f;
-                tmem_ld16(my + cE + quarter * 16, e);
-                tmem_ld16(my + cKQ + quarter * 16, kq);
-                const float mine = (upper ? -r_up : y_up) * u_up, es = fac[(upper ? kKeyScale : kQueryScale) + i];
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    const int j = quarter * 16 + c;
-                    const bool in = upper ? j < i : j <= i;
-                    const float decay = in ? expf(sums.between(i, j)) : 0.f;
-                    const float d = in ? e[c] * mine * decay : 0.f;
-                    const float k = in ? kq[c] * (es * fac[kKeyScale + j]) : 0.f;
-                    const float v = upper ? b_i * d : d;
-                    s = fmaf(d, k, s);
-                    E[lane_row * C + (j ^ lane)] = v;
-                    row = fmaf(v, k, row);
-                }
-                part[0][quarter][lane_row] = row;
-                part[1][quarter][lane_row] = s;
-            };
-            if (Sm::early) {
-                ok = await(&kq_done);
-                if (!ok) break;
-                form_e();
-            }
+            if (Sm::early) put_e();
             ok = await(&g_full);
             if (!ok) break;
             if (warp == 0) {
@@ -705,8 +704,8 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
                         if (leader)
-                            mma_ss(tm + cX3, desc_columns(sbase + Sm::u + (r == 1) * kSheetImage + ks * 2048, kSheetImage),
-                                   desc_columns(sbase + Sm::states + (r == 2) * DKB * kSheetImage + ks * 2048, kSheetImage), instr(DKB * 64, true) | 1u << 15,
+                            mma_ss(tm + cX3, desc_kept(sbase + Sm::u + (r == 1) * kSheetImage, ks),
+                                   desc_kept(sbase + Sm::states + (r == 2) * DKB * kSheetImage, ks), instr(DKB * 64, true) | 1u << 15,
                                    r > 0 || ks > 0);
                 if (leader) mma_commit(&x3_done);
             }
@@ -745,6 +744,7 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                 ok = await(&kq_done);
                 if (!ok) break;
                 form_e();
+                put_e();
                 __syncthreads();
             }
             // rows of [EA + EA^T; EP] and EP^T, times the scales of K's and Q's rows
@@ -875,7 +875,7 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
             fence_after();
             // the decays' slopes, and their sums from each step to the chunk's end
             if (tid < C) {
-                float ea = 0.f, s = 0.f, kx2 = 0.f, kx3 = 0.f, qdq = 0.f, kdk = 0.f, v = 0.f;
+                float ea = 0.f, s = 0.f, kx2 = 0.f, kx3 = 0.f, qdq = 0.f, kdk = 0.f;
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     ea += part[0][w][tid];
@@ -885,11 +885,9 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                     kdk += part[4][w][tid];
                     qdq += part[4][w][C + tid];
                 }
-#pragma unroll
-                for (int w = 0; w < 16; ++w) v += rv[w][tid];
                 slope[tid] = (tile ? slope[tid] : 0.f) + (qdq - kdk) + 2.f * (ea - fac[kBeta + tid] * kx2);
                 end[tid] = (tile ? end[tid] : 0.f) + kx3;
-                db[tid] = (tile ? db[tid] : 0.f) + s + v * r_up - kx2;
+                db[tid] = (tile ? db[tid] : 0.f) + s + rv[tid] * r_up - kx2;
             }
             __syncthreads();
             if (tid < 32) {
