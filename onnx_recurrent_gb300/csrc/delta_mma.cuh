@@ -12,7 +12,6 @@
 #include <type_traits>
 
 #include "delta_tile.cuh"
-#include "ssm_tile.cuh"
 #include "tma.cuh"
 
 namespace rnngb {

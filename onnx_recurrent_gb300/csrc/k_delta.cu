@@ -20,8 +20,10 @@ using namespace delta;
 
 template <int DKB, int KP>
 struct PrepSmem {
-    unsigned char KQ[2 * KP * DKB * kBlock];
-    unsigned char P[2 * kBlock];
+    union {
+        unsigned char KQ[2 * KP * DKB * kBlock];
+        unsigned char P[2 * kBlock];        // once K and Q are done with
+    };
     float A[C][C + 1], T[C][C + 1], X[32][33];
     float ek[C], eq[C], beta[C], fac[768];
     Sums sums;
@@ -46,6 +48,7 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const DeltaParams 
     if (t0 >= len) return;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     {
+        const float g = load_g(p.g, n, h, t0, len);
         const bool kw = fours<T>(p.K, p.DK), qw = fours<T>(p.Q, p.DK);
         float k[8][4], q[8][4];
         const int64_t t = t0 + warp * 8;
@@ -54,7 +57,7 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const DeltaParams 
         load_fours<8>(static_cast<const T*>(p.K.data) + at, p.K.ss, p.DK, kw, in, k);
         load_fours<8>(static_cast<const T*>(p.Q.data) + qt, p.Q.ss, p.DK, qw, in, q);
         if (tid < C) s.beta[tid] = t0 + tid < len ? static_cast<const float*>(p.beta.data)[n * p.beta.bs + (t0 + tid) * p.beta.ss + h] : 0.f;
-        form_sums(s.sums, p.g, n, h, t0, len, &s.carry);
+        form_sums(s.sums, g, &s.carry);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const Scale ek = scale_of(row_most(k[i])), eq = scale_of(row_most(q[i]));
@@ -97,22 +100,25 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const DeltaParams 
             }
         }
     }
+    __syncthreads();        // (and written out)
     const float* er = warp < 4 ? s.ek : s.eq;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int i = rows + lane / 4 + half * 8;
         float m = 0.f;
 #pragma unroll
-        for (int j8 = 0; j8 < 8; ++j8)
+        for (int j8 = 0; j8 < 8; ++j8) {
+            if (j8 * 8 > rows + 15) continue;       // above the diagonal, where c is 0
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int j = j8 * 8 + lane % 4 * 2 + e;
-                float v = 0.f;
-                if (j < i || (j == i && warp >= 4)) v = expf(s.sums.between(i, j)) * (c[j8][half * 2 + e] * (er[i] * s.ek[j]));
-                if (warp < 4 && j < i) s.A[i][j] = s.beta[i] * v;
+                const bool in = j < i || (j == i && warp >= 4);
+                const float v = in ? s.sums.power(i, j) * (c[j8][half * 2 + e] * (er[i] * s.ek[j])) : 0.f;
+                if (warp < 4 && in) s.A[i][j] = s.beta[i] * v;
                 c[j8][half * 2 + e] = v;
                 m = fmaxf(m, fabsf(v));
             }
+        }
         if (warp >= 4) {
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
@@ -129,10 +135,10 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const DeltaParams 
         }
     }
     if (tid < C) {
-        const float first = expf(s.sums.hi[tid] + s.sums.lo[tid]);
+        const float first = s.sums.power(tid);
         s.fac[kBeta + tid] = s.beta[tid];
         s.fac[kDecayed + tid] = s.beta[tid] * first * s.ek[tid];
-        s.fac[kLast + tid] = expf(s.sums.between(C - 1, tid)) * s.ek[tid];
+        s.fac[kLast + tid] = s.sums.power(C - 1, tid) * s.ek[tid];
         s.fac[kQuery + tid] = p.scale * first * s.eq[tid];
         s.fac[kKeyScale + tid] = s.ek[tid];
         s.fac[kQueryScale + tid] = s.eq[tid];

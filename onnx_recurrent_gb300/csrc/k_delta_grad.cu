@@ -565,6 +565,12 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
             const int64_t nh = n * p.H + h, at = nh * chunks + chunk;
             const unsigned char *kept = p.kept + (at * tiles + tile) * kept_tile, *slopes = q.slopes + (at * tiles + tile) * slopes_tile;
             const unsigned char* keys = p.keys + (nk * chunks + chunk) * Im::keys;
+            const float g = load_g(p.g, n, h, t0, len);
+            float4 fac4;
+            if (tid < 192) fac4 = reinterpret_cast<const float4*>(p.mats + at * Im::mats + 4 * kBlock)[tid];
+            float scale_one = 0.f;
+            if (tid < 2) scale_one = reinterpret_cast<const float*>(kept + kStates + 2 * kSheetImage)[tid];
+            else if (tid < 5) scale_one = reinterpret_cast<const float*>(slopes + kStates + (2 + KP) * kSheetImage)[tid - 2];
             if (tid == 0) {
                 mbar_arrive_expect_tx(&first_full, kStates + (4 + KP) * kSheetImage + (Sm::early ? Im::keys : 0));
                 bulk_g2s(base + Sm::r, slopes + kStates, kSheetImage, &first_full);
@@ -579,12 +585,6 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                 for (int j = tid; j < (int)kSheetImage / 16; j += kRestThreads)
                     reinterpret_cast<uint4*>(base + Sm::y + 2 * kSheetImage)[j] = make_uint4(0, 0, 0, 0);
             fence_shared();
-            if (tid < 192) reinterpret_cast<float4*>(fac)[tid] = reinterpret_cast<const float4*>(p.mats + at * Im::mats + 4 * kBlock)[tid];
-            if (tid == 192) {
-                const float* a = reinterpret_cast<const float*>(kept + kStates + 2 * kSheetImage);
-                const float* b = reinterpret_cast<const float*>(slopes + kStates + (2 + KP) * kSheetImage);
-                scales[0] = a[0], scales[1] = a[1], scales[2] = b[0], scales[3] = b[1], scales[4] = b[2];
-            }
             // V at the warp's four steps, four values 32 apart a lane
             T vs[4][4];
             {
@@ -595,7 +595,9 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                     for (int e = 0; e < 4; ++e)
                         vs[t][e] = t0 + warp * 4 + t < len && v0 + lane + 32 * e < DV ? row[t * p.V.ss + 32 * e] : from_f<T>(0.f);
             }
-            form_sums(sums, p.g, n, h, t0, len, &carry);
+            if (tid < 192) reinterpret_cast<float4*>(fac)[tid] = fac4;
+            if (tid < 5) scales[tid] = scale_one;
+            form_sums(sums, g, &carry);
             const float s_up = scales[0], u_up = scales[1], g_up = scales[2], r_up = scales[3], y_up = p.scale * scales[4];
             ok = await(&first_full);
             if (!ok) break;
@@ -657,7 +659,7 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                 for (int c = 0; c < 16; ++c) {
                     const int j = quarter * 16 + c;
                     const bool in = upper ? j < i : j <= i;
-                    const float decay = in ? expf(sums.between(i, j)) : 0.f;
+                    const float decay = in ? sums.power(i, j) : 0.f;
                     const float d = in ? e[c] * mine * decay : 0.f;
                     const float k = in ? kq[c] * (es * fac[kKeyScale + j]) : 0.f;
                     const float v = upper ? b_i * d : d;
@@ -816,7 +818,7 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
             };
             float own = 0.f;            // this quarter's part of k_i.dK_i or q_i.dQ_i
             {
-                const float first = expf(sums.hi[i] + sums.lo[i]), last = expf(sums.between(C - 1, i));
+                const float first = sums.power(i), last = sums.power(C - 1, i);
                 const float fx = (upper ? -b_i * r_up : y_up) * s_up * first, f3 = upper ? last * (u_up * g_up) : 0.f;
                 float s1 = 0.f, s3 = 0.f;
 #pragma unroll
