@@ -10,9 +10,9 @@ namespace delta {
 constexpr int C = kDeltaChunk;
 constexpr int kThreads = 256;
 
-// The log decays' sums within a chunk, from its first step, in units of log 2.  Formed in 64 bits and kept as two fp32 parts, so
-// that the difference of two sums is as exact as itself in fp32 however long the sums have grown.  A g below -1000 counts as
-// -1000, whose exponential is 0 as well, and whose sums have differences.
+// The log decays' sums within a chunk, from its first step, in units of log 2.  Each is two fp32 parts (48 bits), so that the
+// difference of two sums is as exact as itself in fp32 however long the sums have grown.  A g below -1000 counts as -1000,
+// whose exponential is 0 as well, and whose sums have differences.
 struct Sums {
     float hi[C], lo[C];
     __device__ __forceinline__ float power(int i, int j) const { return ex2((hi[i] - hi[j]) + (lo[i] - lo[j])); }
@@ -24,23 +24,33 @@ __device__ __forceinline__ float load_g(const View& g, int64_t n, int h, int64_t
     const int t = threadIdx.x;
     return t < C && t0 + t < len ? static_cast<const float*>(g.data)[n * g.bs + (t0 + t) * g.ss + h] : 0.f;
 }
-__device__ __forceinline__ void form_sums(Sums& s, float g, double* carry)
+// (a, b) + (c, d), each a number and what its rounding left off.
+__device__ __forceinline__ void add_pair(float& a, float& b, float c, float d)
+{
+    const float s = __fadd_rn(a, c), t = __fsub_rn(s, a);
+    const float e = __fadd_rn(__fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(c, t)), __fadd_rn(b, d));
+    a = __fadd_rn(s, e);
+    b = __fsub_rn(e, __fsub_rn(a, s));
+}
+__device__ __forceinline__ void form_sums(Sums& s, float g, float2* carry)
 {
     const int t = threadIdx.x;
-    double v = 0.0;
+    float a = 0.f, b = 0.f;
     if (t < C) {
-        v = 1.4426950408889634074 * (double)(g < -1000.f ? -1000.f : g);
+        const float x = g < -1000.f ? -1000.f : g;
+        a = __fmul_rn(x, kLog2e);
+        b = fmaf(x, 1.925963033500888e-08f, fmaf(x, kLog2e, -a));       // log2 e, and what its rounding to fp32 left off
         for (int o = 1; o < 32; o *= 2) {
-            const double w = __shfl_up_sync(0xffffffffu, v, o);
-            if ((t & 31) >= o) v += w;
+            const float c = __shfl_up_sync(0xffffffffu, a, o), d = __shfl_up_sync(0xffffffffu, b, o);
+            if ((t & 31) >= o) add_pair(a, b, c, d);
         }
-        if (t == 31) *carry = v;
+        if (t == 31) *carry = make_float2(a, b);
     }
     __syncthreads();
     if (t < C) {
-        if (t >= 32) v += *carry;
-        s.hi[t] = (float)v;
-        s.lo[t] = (float)(v - (double)s.hi[t]);
+        if (t >= 32) add_pair(a, b, carry->x, carry->y);
+        s.hi[t] = a;
+        s.lo[t] = b;
     }
     __syncthreads();
 }

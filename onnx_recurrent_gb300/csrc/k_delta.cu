@@ -27,14 +27,14 @@ struct PrepSmem {
     float A[C][C + 1], T[C][C + 1], X[32][33];
     float ek[C], eq[C], beta[C], fac[768];
     Sums sums;
-    double carry;
+    float2 carry;
 };
 
 // T and P, the factors, and K and Q as the second launch wants them.  A block has a chunk of a head.  The two products
 // [K; Q] K^T are small (a twentieth of all); they go through the warps' own matrix instructions.  T is
 // found by blocks: four of 16 by substitution, a thread a column, then twice T21 = -T22 (A21 T11).
 template <typename T, int DKB, int KP>
-__global__ void __launch_bounds__(kThreads) delta_prep_kernel(const DeltaParams p, unsigned char* keys, unsigned char* mats)
+__global__ void __launch_bounds__(kThreads, 3) delta_prep_kernel(const DeltaParams p, unsigned char* keys, unsigned char* mats)
 {
     extern __shared__ __align__(1024) unsigned char raw[];
     using S = PrepSmem<DKB, KP>;

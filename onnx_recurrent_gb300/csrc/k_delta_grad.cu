@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
     __shared__ float k_scale[C], q_scale[C];
     __shared__ float fac[768], scales[8];
     __shared__ float rv[C], part[5][4][128], dots[kRestThreads / 32], slope[C], end[C], db[C];
-    __shared__ double carry;
+    __shared__ float2 carry;
     __shared__ uint32_t slot;
     __shared__ int given_up;
     const DeltaParams& p = q.f;
@@ -601,6 +601,26 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
             const float s_up = scales[0], u_up = scales[1], g_up = scales[2], r_up = scales[3], y_up = p.scale * scales[4];
             ok = await(&first_full);
             if (!ok) break;
+            // What comes next on this multiprocessor, into L2: blocks load and compute at the same times, and their loads alone
+            // would wait for one another at the memory.
+            if (tid == 32) {
+                int64_t next_at = at * tiles + tile + 1, next_keys = -1;
+                bool there = true;
+                if (round + 1 == per * tiles) {
+                    const int64_t b = nk * chunks + chunk + p.sms, bk = b / chunks;
+                    there = bk < p.N * p.HK;
+                    next_at = ((bk / p.HK * p.H + bk % p.HK * per) * chunks + b % chunks) * tiles;
+                    next_keys = b;
+                } else if (tile + 1 == tiles) {
+                    next_at = (at + chunks) * tiles;
+                }
+                if (there) {
+                    prefetch(p.kept + next_at * kept_tile, (unsigned)kept_tile);
+                    prefetch(q.slopes + next_at * slopes_tile, (unsigned)slopes_tile);
+                    prefetch(p.mats + next_at / tiles * Im::mats + 4 * kBlock, 3072);
+                    if (next_keys >= 0) prefetch(p.keys + next_keys * Im::keys, Im::keys);
+                }
+            }
             const unsigned kimg = sbase + Sm::keys, qimg = kimg + kBlock;
             auto key_products = [&] {
 #pragma unroll 1
