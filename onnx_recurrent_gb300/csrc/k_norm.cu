@@ -6,9 +6,9 @@
 // mean) rstd and w = dY W,
 //     dX = rstd (w - mean(w) - z mean(w z)),   dW = sum over rows of dY z,   dbias = that of dY.
 //
-// Bytes bound both: each block walks rows, some at a time so that their loads are in flight together and share
-// the barriers of their sums; a thread keeps the weights of its columns (and the gradient's sums over the
-// rows, until they go to scratch as one of few parts that are added in order).
+// Bytes bound both.  Blocks walk rows; in the gradient a thread keeps the sums over rows of its columns, which go to
+// scratch as one of few parts that are added in order.  (Several rows at once, or the next row's loads ahead, were no faster:
+// the registers cost as many blocks.)
 #include "norm_internal.h"
 #include "ssm_math.cuh"
 
@@ -21,13 +21,13 @@ struct alignas(sizeof(T) * VEC) Piece {
     T v[VEC];
 };
 
-// Threads of a row, values a thread holds (NV, in pieces of VEC), rows a thread has at once (R).
-template <typename T_, int VEC_, int NV_, int TPR_, int R_>
+// Threads of a row, and values a thread holds (NV, in pieces of VEC).
+template <typename T_, int VEC_, int NV_, int TPR_>
 struct Shape {
     using T = T_;
-    static constexpr int VEC = VEC_, NV = NV_, TPR = TPR_, R = R_, PER = NV / VEC;
+    static constexpr int VEC = VEC_, NV = NV_, TPR = TPR_, PER = NV / VEC;
     static constexpr int threads = TPR < 256 ? 256 : TPR, groups = threads / TPR;
-    static constexpr bool weights = NV <= 16;       // in registers
+    static constexpr bool weights = NV <= 16;         // the columns' weights stay in registers
 };
 
 // The sums of a row's threads, in all of them.  `shared` must differ from the one of the sums before.
@@ -65,79 +65,83 @@ __device__ __forceinline__ void load_weights(float (&w)[S::NV], const float* fro
         }
 }
 
+// The weights of a piece of columns, `wide`: from a 16-byte boundary.
+template <int VEC>
+__device__ __forceinline__ void piece_weights(float (&w)[VEC], const float* from, int c, bool wide, float otherwise)
+{
+    if (VEC % 4 == 0 && from && wide) {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(from + c + e);
+            w[e] = q.x, w[e + 1] = q.y, w[e + 2] = q.z, w[e + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) w[e] = from ? from[c + e] : otherwise;
+    }
+}
+
 template <typename S>
 __global__ void __launch_bounds__(S::threads) norm_kernel(const NormParams p)
 {
     using T = typename S::T;
     using P = Piece<T, S::VEC>;
-    __shared__ float sums[2][S::threads / 32][S::R];
+    __shared__ float sums[2][S::threads / 32][1];
     const int t = threadIdx.x % S::TPR, group = threadIdx.x / S::TPR, pieces = p.D / S::VEC;
     float w[S::weights ? S::NV : 1], b[S::weights ? S::NV : 1];
     if constexpr (S::weights) {
         load_weights<S>(w, p.W, p.D, t, 1.f);
         load_weights<S>(b, p.bias, p.D, t, 0.f);
     }
-    const float per = 1.f / (float)p.D;
-    constexpr int rows = S::groups * S::R;
-    for (int64_t r0 = (int64_t)blockIdx.x * rows; r0 < p.rows; r0 += (int64_t)gridDim.x * rows) {
-        P x[S::R][S::PER] = {};
+    const bool wide = ((uintptr_t)p.W | (uintptr_t)p.bias) % 16 == 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * S::groups; r0 < p.rows; r0 += (int64_t)gridDim.x * S::groups) {
+        const int64_t r = r0 + group;
+        const bool in = r < p.rows;
+        const P* from = reinterpret_cast<const P*>(static_cast<const T*>(p.X) + r * p.xs);
+        P x[S::PER] = {};
 #pragma unroll
-        for (int a = 0; a < S::R; ++a) {
-            const int64_t r = r0 + group * S::R + a;
-            const P* from = reinterpret_cast<const P*>(static_cast<const T*>(p.X) + r * p.xs);
+        for (int i = 0; i < S::PER; ++i)
+            if (in && i * S::TPR + t < pieces) x[i] = from[i * S::TPR + t];
+        float s[1] = {0.f};
 #pragma unroll
-            for (int i = 0; i < S::PER; ++i)
-                if (r < p.rows && i * S::TPR + t < pieces) x[a][i] = from[i * S::TPR + t];
-        }
-        float s[S::R], mean[S::R], rstd[S::R];
+        for (int i = 0; i < S::PER; ++i)
 #pragma unroll
-        for (int a = 0; a < S::R; ++a) {
-            s[a] = 0.f;
-#pragma unroll
-            for (int i = 0; i < S::PER; ++i)
-#pragma unroll
-                for (int e = 0; e < S::VEC; ++e) s[a] += to_f(x[a][i].v[e]);
-        }
+            for (int e = 0; e < S::VEC; ++e) s[0] += to_f(x[i].v[e]);
         row_sums<S>(s, sums[0]);
+        const float mean = s[0] / (float)p.D;
+        s[0] = 0.f;
 #pragma unroll
-        for (int a = 0; a < S::R; ++a) {
-            mean[a] = s[a] / (float)p.D;
-            s[a] = 0.f;
-#pragma unroll
-            for (int i = 0; i < S::PER; ++i)
-                if (i * S::TPR + t < pieces)
-#pragma unroll
-                    for (int e = 0; e < S::VEC; ++e) {
-                        const float d = to_f(x[a][i].v[e]) - mean[a];
-                        s[a] = fmaf(d, d, s[a]);
-                    }
-        }
-        row_sums<S>(s, sums[1]);
-#pragma unroll
-        for (int a = 0; a < S::R; ++a) {
-            const int64_t r = r0 + group * S::R + a;
-            if (r >= p.rows) continue;
-            rstd[a] = 1.f / sqrtf(fmaf(s[a], per, p.eps));
-            if (p.stats && t == 0) {
-                p.stats[2 * r] = mean[a];
-                p.stats[2 * r + 1] = rstd[a];
-            }
-            P* to = reinterpret_cast<P*>(static_cast<T*>(p.Y) + r * p.ys);
-#pragma unroll
-            for (int i = 0; i < S::PER; ++i) {
-                const int at = i * S::TPR + t;
-                if (at >= pieces) continue;
-                P q;
+        for (int i = 0; i < S::PER; ++i)
+            if (i * S::TPR + t < pieces)
 #pragma unroll
                 for (int e = 0; e < S::VEC; ++e) {
-                    const float z = (to_f(x[a][i].v[e]) - mean[a]) * rstd[a];
-                    float wi, bi;
-                    if constexpr (S::weights) wi = w[i * S::VEC + e], bi = b[i * S::VEC + e];
-                    else wi = p.W ? p.W[at * S::VEC + e] : 1.f, bi = p.bias ? p.bias[at * S::VEC + e] : 0.f;
-                    q.v[e] = from_f<T>(fmaf(z, wi, bi));
+                    const float d = to_f(x[i].v[e]) - mean;
+                    s[0] = fmaf(d, d, s[0]);
                 }
-                to[at] = q;
+        row_sums<S>(s, sums[1]);
+        if (!in) continue;
+        const float rstd = 1.f / sqrtf(s[0] / (float)p.D + p.eps);
+        if (p.stats && t == 0) {
+            p.stats[2 * r] = mean;
+            p.stats[2 * r + 1] = rstd;
+        }
+        P* to = reinterpret_cast<P*>(static_cast<T*>(p.Y) + r * p.ys);
+#pragma unroll
+        for (int i = 0; i < S::PER; ++i) {
+            const int at = i * S::TPR + t;
+            if (at >= pieces) continue;
+            P q;
+            float pw[S::VEC], pb[S::VEC];
+            if constexpr (!S::weights) {
+                piece_weights(pw, p.W, at * S::VEC, wide, 1.f);
+                piece_weights(pb, p.bias, at * S::VEC, wide, 0.f);
             }
+#pragma unroll
+            for (int e = 0; e < S::VEC; ++e) {
+                if constexpr (S::weights) pw[e] = w[i * S::VEC + e], pb[e] = b[i * S::VEC + e];
+                q.v[e] = from_f<T>(fmaf((to_f(x[i].v[e]) - mean) * rstd, pw[e], pb[e]));
+            }
+            to[at] = q;
         }
     }
 }
@@ -148,71 +152,59 @@ __global__ void __launch_bounds__(S::threads) norm_grad_kernel(const NormGradPar
 {
     using T = typename S::T;
     using P = Piece<T, S::VEC>;
-    __shared__ float sums[2][S::threads / 32][2 * S::R];
+    __shared__ float sums[2][S::threads / 32][2];
     const NormParams& f = p.f;
     const int t = threadIdx.x % S::TPR, group = threadIdx.x / S::TPR, pieces = f.D / S::VEC;
     float w[S::weights ? S::NV : 1], dw[SUMS ? S::NV : 1] = {}, db[SUMS ? S::NV : 1] = {};
     if constexpr (S::weights) load_weights<S>(w, f.W, f.D, t, 1.f);
     const float per = 1.f / (float)f.D;
-    constexpr int rows = S::groups * S::R;
+    auto weight = [&](int i, int e) {
+        if constexpr (S::weights) return w[i * S::VEC + e];
+        else return f.W && i * S::TPR + t < pieces ? f.W[(i * S::TPR + t) * S::VEC + e] : 1.f;
+    };
     int turn = 0;
-    for (int64_t r0 = (int64_t)blockIdx.x * rows; r0 < f.rows; r0 += (int64_t)gridDim.x * rows, turn ^= 1) {
-        P x[S::R][S::PER] = {}, y[S::R][S::PER] = {};
-        float2 stat[S::R];
+    for (int64_t r0 = (int64_t)blockIdx.x * S::groups; r0 < f.rows; r0 += (int64_t)gridDim.x * S::groups, turn ^= 1) {
+        const int64_t r = r0 + group;
+        const bool in = r < f.rows;
+        const P* fx = reinterpret_cast<const P*>(static_cast<const T*>(f.X) + r * f.xs);
+        const P* fy = reinterpret_cast<const P*>(static_cast<const T*>(p.dY) + r * p.dys);
+        P x[S::PER] = {}, y[S::PER] = {};
 #pragma unroll
-        for (int a = 0; a < S::R; ++a) {
-            const int64_t r = r0 + group * S::R + a;
-            const P* fx = reinterpret_cast<const P*>(static_cast<const T*>(f.X) + r * f.xs);
-            const P* fy = reinterpret_cast<const P*>(static_cast<const T*>(p.dY) + r * p.dys);
-            stat[a] = make_float2(r < f.rows ? f.stats[2 * r] : 0.f, r < f.rows ? f.stats[2 * r + 1] : 0.f);
+        for (int i = 0; i < S::PER; ++i)
+            if (in && i * S::TPR + t < pieces) {
+                x[i] = fx[i * S::TPR + t];
+                y[i] = fy[i * S::TPR + t];
+            }
+        const float mean = in ? f.stats[2 * r] : 0.f, rstd = in ? f.stats[2 * r + 1] : 0.f;
+        float s[2] = {0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < S::PER; ++i)
-                if (r < f.rows && i * S::TPR + t < pieces) {
-                    x[a][i] = fx[i * S::TPR + t];
-                    y[a][i] = fy[i * S::TPR + t];
+        for (int i = 0; i < S::PER; ++i)
+#pragma unroll
+            for (int e = 0; e < S::VEC; ++e) {      // (past the row's end dY is 0)
+                const float z = (to_f(x[i].v[e]) - mean) * rstd, d = to_f(y[i].v[e]), g = d * weight(i, e);
+                s[0] += g;
+                s[1] = fmaf(g, z, s[1]);
+                if constexpr (SUMS) {
+                    dw[i * S::VEC + e] = fmaf(d, z, dw[i * S::VEC + e]);
+                    db[i * S::VEC + e] += d;
                 }
-        }
-        float s[2 * S::R];
-        auto weight = [&](int i, int e) {
-            if constexpr (S::weights) return w[i * S::VEC + e];
-            else return f.W && i * S::TPR + t < pieces ? f.W[(i * S::TPR + t) * S::VEC + e] : 1.f;
-        };
-#pragma unroll
-        for (int a = 0; a < S::R; ++a) {
-            s[2 * a] = s[2 * a + 1] = 0.f;
-#pragma unroll
-            for (int i = 0; i < S::PER; ++i)
-#pragma unroll
-                for (int e = 0; e < S::VEC; ++e) {      // (past the row's end dY is 0, and z is not used but with it)
-                    const float z = (to_f(x[a][i].v[e]) - stat[a].x) * stat[a].y, d = to_f(y[a][i].v[e]), g = d * weight(i, e);
-                    s[2 * a] += g;
-                    s[2 * a + 1] = fmaf(g, z, s[2 * a + 1]);
-                    if constexpr (SUMS) {
-                        dw[i * S::VEC + e] = fmaf(d, z, dw[i * S::VEC + e]);
-                        db[i * S::VEC + e] += d;
-                    }
-                }
-        }
+            }
         if (!p.dX) continue;
         row_sums<S>(s, sums[turn]);
+        if (!in) continue;
+        const float u = s[0] * per, v = s[1] * per;
+        P* to = reinterpret_cast<P*>(static_cast<T*>(p.dX) + r * p.dxs);
 #pragma unroll
-        for (int a = 0; a < S::R; ++a) {
-            const int64_t r = r0 + group * S::R + a;
-            if (r >= f.rows) continue;
-            const float u = s[2 * a] * per, v = s[2 * a + 1] * per;
-            P* to = reinterpret_cast<P*>(static_cast<T*>(p.dX) + r * p.dxs);
+        for (int i = 0; i < S::PER; ++i) {
+            const int at = i * S::TPR + t;
+            if (at >= pieces) continue;
+            P q;
 #pragma unroll
-            for (int i = 0; i < S::PER; ++i) {
-                const int at = i * S::TPR + t;
-                if (at >= pieces) continue;
-                P q;
-#pragma unroll
-                for (int e = 0; e < S::VEC; ++e) {
-                    const float z = (to_f(x[a][i].v[e]) - stat[a].x) * stat[a].y;
-                    q.v[e] = from_f<T>(stat[a].y * (to_f(y[a][i].v[e]) * weight(i, e) - u - z * v));
-                }
-                to[at] = q;
+            for (int e = 0; e < S::VEC; ++e) {
+                const float z = (to_f(x[i].v[e]) - mean) * rstd;
+                q.v[e] = from_f<T>(rstd * (to_f(y[i].v[e]) * weight(i, e) - u - z * v));
             }
+            to[at] = q;
         }
     }
     if constexpr (SUMS) {
@@ -259,22 +251,17 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormGradParams 
     }
 }
 
-// Rows of up to this many values are walked with sums in registers.
+// Rows of up to this many values have the gradient's sums in registers.
 constexpr int kWalked = 8192;
 int threads_of_row(int D) { return D <= 256 ? 32 : D <= 1024 ? 128 : D <= 4096 ? 256 : D <= kWalked ? 512 : 1024; }
-// Rows a block has at once; one a thread where there are too few to fill the multiprocessors otherwise.
-struct Split {
-    int rows;       // a thread's
-    int64_t blocks;
-};
-Split split_of(const NormParams& p, int a_multiprocessor)
+// Blocks that walk `rows` rows, `at_once` each, at most `cap` a multiprocessor.
+int64_t blocks_of(const NormParams& p, int at_once, int cap)
 {
-    const int tpr = threads_of_row(p.D), groups = tpr < 256 ? 256 / tpr : 1, most = p.D <= 2048 ? 4 : p.D <= 4096 ? 2 : 1;
-    const int r = p.rows >= (int64_t)p.sms * 4 * groups * most ? most : 1;
-    const int64_t blocks = (p.rows + groups * r - 1) / (groups * r), cap = (int64_t)p.sms * a_multiprocessor;
-    return Split{r, blocks < cap ? blocks : cap};
+    const int64_t blocks = (p.rows + at_once - 1) / at_once, most = (int64_t)p.sms * cap;
+    return blocks < most ? blocks : most;
 }
-constexpr int kRunBlocks = 8, kGradBlocks = 3;      // a multiprocessor's
+// (two rows at least a part)
+int64_t grad_blocks(const NormParams& p) { return blocks_of(p, 2 * (threads_of_row(p.D) < 256 ? 256 / threads_of_row(p.D) : 1), 4); }
 
 template <typename S>
 void go(const NormParams& p, const NormGradParams* g, int64_t blocks, cudaStream_t s)
@@ -292,16 +279,31 @@ void go(const NormParams& p, const NormGradParams* g, int64_t blocks, cudaStream
     norm_grad_kernel<S, false><<<(unsigned)blocks, S::threads, 0, s>>>(*g);
 }
 
+// A few rows: many threads a row, for its latency (96 rows of 2048: 3.2 us with 256 threads).  Many: 32 values a thread, their
+// weights from the first-level cache, in flight together (16384 x 2048 bf16: 37 us with 64 threads a row; 8 values a thread
+// with their weights in registers 42 to 50 us, whatever the rows at once and blocks; 64 values 39 us).  The gradient has 8 or 16
+// values a thread, for its sums.
 template <typename T, int VEC>
 void by_size(const NormParams& p, const NormGradParams* g, cudaStream_t s)
 {
-    const Split q = split_of(p, g ? kGradBlocks : kRunBlocks);
-    if (p.D <= 256) q.rows == 4 ? go<Shape<T, VEC, 8, 32, 4>>(p, g, q.blocks, s) : go<Shape<T, VEC, 8, 32, 1>>(p, g, q.blocks, s);
-    else if (p.D <= 1024) q.rows == 4 ? go<Shape<T, VEC, 8, 128, 4>>(p, g, q.blocks, s) : go<Shape<T, VEC, 8, 128, 1>>(p, g, q.blocks, s);
-    else if (p.D <= 2048) q.rows == 4 ? go<Shape<T, VEC, 8, 256, 4>>(p, g, q.blocks, s) : go<Shape<T, VEC, 8, 256, 1>>(p, g, q.blocks, s);
-    else if (p.D <= 4096) q.rows == 2 ? go<Shape<T, VEC, 16, 256, 2>>(p, g, q.blocks, s) : go<Shape<T, VEC, 16, 256, 1>>(p, g, q.blocks, s);
-    else if (p.D <= kWalked) go<Shape<T, VEC, 16, 512, 1>>(p, g, q.blocks, s);
-    else go<Shape<T, VEC, 32, 1024, 1>>(p, g, q.blocks, s);
+    auto walk = [&](auto shape) {
+        using S = decltype(shape);
+        go<S>(p, g, g ? grad_blocks(p) : blocks_of(p, S::groups, 8), s);
+    };
+    if (!g && p.D > 256 && p.rows >= (int64_t)p.sms * 16) {
+        if (p.D <= 1024) walk(Shape<T, VEC, 32, 32>{});
+        else if (p.D <= 2048) walk(Shape<T, VEC, 32, 64>{});
+        else if (p.D <= 4096) walk(Shape<T, VEC, 32, 128>{});
+        else if (p.D <= 8192) walk(Shape<T, VEC, 32, 256>{});
+        else walk(Shape<T, VEC, 32, 1024>{});
+        return;
+    }
+    if (p.D <= 256) walk(Shape<T, VEC, 8, 32>{});
+    else if (p.D <= 1024) walk(Shape<T, VEC, 8, 128>{});
+    else if (p.D <= 2048) walk(Shape<T, VEC, 8, 256>{});
+    else if (p.D <= 4096) walk(Shape<T, VEC, 16, 256>{});
+    else if (p.D <= kWalked) walk(Shape<T, VEC, 16, 512>{});
+    else walk(Shape<T, VEC, 32, 1024>{});
 }
 
 template <typename T>
@@ -340,8 +342,7 @@ cudaError_t launch_norm(const NormParams& p, cudaStream_t s, int* launches)
 void norm_grad_plan(NormGradParams& p)
 {
     if (p.f.D <= kWalked) {
-        const int tpr = threads_of_row(p.f.D);
-        p.parts = split_of(p.f, kGradBlocks).blocks * (tpr < 256 ? 256 / tpr : 1);
+        p.parts = grad_blocks(p.f) * (threads_of_row(p.f.D) < 256 ? 256 / threads_of_row(p.f.D) : 1);
         if (p.parts < 1) p.parts = 1;
         return;
     }
