@@ -22,8 +22,6 @@ rnn_status check_plan(rnn_beam* pl, const void* args, int64_t items)
     return RNN_OK;
 }
 
-size_t up(size_t bytes) { return (bytes + 255) / 256 * 256; }
-
 }  // namespace
 
 extern "C" {
@@ -85,7 +83,6 @@ rnn_status rnn_beam_select(rnn_beam_t pl, const rnn_beam_select_args* a)
     if (rs == RNN_OK) rs = check_in_place(a->finished, a->new_finished, beams, "finished and new_finished");
     if (rs == RNN_OK) rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
-    const int64_t rows = a->shared ? a->items : a->items * pl->B;
     BeamSelectParams p{};
     p.items = a->items;
     p.V = a->vocab;
@@ -103,24 +100,14 @@ rnn_status rnn_beam_select(rnn_beam_t pl, const rnn_beam_select_args* a)
     p.new_scores = a->new_scores;
     p.new_finished = a->new_finished;
     cudaStream_t st = (cudaStream_t)a->stream;
-    const size_t lse = up(8 * (size_t)rows), bytes = lse + 4 * (size_t)(rows * p.top);
+    p.sms = pl->sms;
+    beam_plan(p);
+    const size_t bytes = beam_scratch_bytes(p);
     char* scratch = nullptr;
     rs = claim_scratch(pl, bytes, st, &scratch);
     if (rs != RNN_OK) return rs;
-    ScoreParams q{};
-    q.rows = rows;
-    q.V = p.V;
-    q.stride = p.stride;
-    q.io = p.io;
-    q.top = p.top;
-    q.x = p.logits;
-    q.lse = (float*)scratch;
-    q.lse_rest = q.lse + rows;
-    q.top_ids = (int32_t*)(scratch + lse);
-    p.lse = q.lse;
-    p.top_ids = q.top_ids;
-    cudaError_t e = launch_scores(q, st, &pl->launches);
-    if (e == cudaSuccess) e = launch_beam_select(p, st, &pl->launches);
+    p.scratch = (unsigned char*)scratch;
+    cudaError_t e = launch_beam_select(p, st, &pl->launches);
     if (e != cudaSuccess) return cuda_fail(e, "beam selection launch");
     return release_scratch(pl, bytes, st);
 }

@@ -35,19 +35,22 @@ struct NormGradParams {
 
 struct BeamSelectParams {
     int64_t items, V;
-    int B, io, top;         // top: alternatives a row has, min(B, V)
+    int B, io, top;         // top: candidates a row has, min(B, V)
     int64_t end;            // -1: none
     int shared;             // an item's beams have one row
     int64_t stride;         // between rows of logits
     const void* logits;
-    const float* lse;       // [2][rows]
-    const int32_t* top_ids; // [rows][top]
+    int sms, parts;         // parts of a row, a block each, and their length (beam_plan)
+    int64_t length;
+    unsigned char* scratch; // beam_scratch_bytes
     const float* scores;
     const uint8_t* finished;
     int32_t *parents, *ids;
     float* new_scores;
     uint8_t* new_finished;
 };
+void beam_plan(BeamSelectParams& p);
+size_t beam_scratch_bytes(const BeamSelectParams& p);
 
 struct ReorderTensor {
     const void* in;

@@ -85,7 +85,11 @@ def test_rows_shared_by_beams_or_by_all_and_strides():
     big = torch.full((12, V + 9), 50.0)
     big[:, 2:2 + V] = wide
     c = orc.beam_select(plan, big.cuda()[:, 2:2 + V], scores.cuda())
-    assert all(torch.equal(p, q) for p, q in zip(c, b))
+    assert all(torch.equal(p, q) for p, q in zip(c[:2] + c[3:], b[:2] + b[3:]))
+    # Rows that start elsewhere in 16 bytes go to other threads, and their exponentials are added in another order.  A thread adds at
+    # most 16 pieces of 4 or 8, a warp 5 times, a block 8: 145 roundings of positive terms, so each sum is off by at most 145 *
+    # 2^-24, its logarithm by as much, and two of them by 2 * 145 * 2^-24; each score is rounded once more.
+    assert ((c.scores - b.scores).abs() <= 290 * 2.0 ** -24 + 2 * 2.0 ** -24 * b.scores.abs()).all()
     one = x[:1].cuda().expand(12, V)
     d = orc.beam_select(plan, one, scores.cuda())
     e = _check(plan, x[:1].expand(12, V).contiguous(), scores)
