@@ -299,33 +299,37 @@ constexpr int kPitch = 144;
 constexpr unsigned kSheet = 128 * kPitch;
 
 // A 64-step chunk of rows of 16-bit values to columns in shared memory (and back): thread t of 64 has step t; 16 bytes at
-// a time where the rows are aligned.  Rows have `cols` (at most 128) values; out of range they are 0.
+// a time where the rows are aligned.  Rows have `cols` (at most 128) values; out of range they are 0.  (Short loops: what a chain's
+// warps run each chunk has to stay in the instruction cache.)
 template <typename T>
 __device__ __forceinline__ void rows_to_sheet(unsigned char* sheet_at, const T* row, bool in, bool wide, int cols, int t)
 {
     unsigned short* sheet = reinterpret_cast<unsigned short*>(sheet_at) + t;
+    const unsigned short* from = reinterpret_cast<const unsigned short*>(row);
+    if (wide && cols % 8 == 0) {
 #pragma unroll 1
-    for (int c0 = 0; c0 < 128; c0 += 64) {
-        uint4 x[8];         // all on their way at once
+        for (int c0 = 0; c0 < 128; c0 += 64) {
+            uint4 x[8];         // all on their way at once
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const int c = c0 + 8 * q;
-            x[q] = make_uint4(0, 0, 0, 0);
-            if (in && wide && c + 8 <= cols) {
-                x[q] = *reinterpret_cast<const uint4*>(row + c);
-            } else if (in && c < cols) {
-                const unsigned short* one = reinterpret_cast<const unsigned short*>(row) + c;
-                unsigned* pairs = &x[q].x;
+            for (int q = 0; q < 8; ++q) {
+                x[q] = make_uint4(0, 0, 0, 0);
+                if (in && c0 + 8 * q < cols) x[q] = *reinterpret_cast<const uint4*>(from + c0 + 8 * q);
+            }
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (c + e < cols) pairs[e / 2] |= (unsigned)one[e] << (e % 2 * 16);
+            for (int q = 0; q < 8; ++q) {
+                const unsigned pairs[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sheet[(c0 + 8 * q + e) * (kPitch / 2)] = (unsigned short)(pairs[e / 2] >> (e % 2 * 16));
             }
         }
+    } else {
+#pragma unroll 1
+        for (int c0 = 0; c0 < 128; c0 += 16) {
+            unsigned short x[16];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const unsigned pairs[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+            for (int e = 0; e < 16; ++e) x[e] = in && c0 + e < cols ? from[c0 + e] : (unsigned short)0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sheet[(c0 + 8 * q + e) * (kPitch / 2)] = (unsigned short)(pairs[e / 2] >> (e % 2 * 16));
+            for (int e = 0; e < 16; ++e) sheet[(c0 + e) * (kPitch / 2)] = x[e];
         }
     }
 }
@@ -334,22 +338,20 @@ __device__ __forceinline__ void sheet_to_rows(const unsigned char* sheet_at, T* 
 {
     const unsigned short* sheet = reinterpret_cast<const unsigned short*>(sheet_at) + t;
     unsigned short* row = reinterpret_cast<unsigned short*>(row_at);
-#pragma unroll 4
-    for (int c = 0; c < cols; c += 8) {
-        unsigned short x[8];
+    if (wide && cols % 8 == 0) {
+#pragma unroll 2
+        for (int c = 0; c < cols; c += 8) {
+            unsigned short x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = sheet[(c + e) * (kPitch / 2)];
-        if (wide && c + 8 <= cols) {
+            for (int e = 0; e < 8; ++e) x[e] = sheet[(c + e) * (kPitch / 2)];
             *reinterpret_cast<uint4*>(row + c) = make_uint4(x[0] | (unsigned)x[1] << 16, x[2] | (unsigned)x[3] << 16,
                                                             x[4] | (unsigned)x[5] << 16, x[6] | (unsigned)x[7] << 16);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c + e < cols) row[c + e] = x[e];
         }
+    } else {
+#pragma unroll 4
+        for (int c = 0; c < cols; ++c) row[c] = sheet[c * (kPitch / 2)];
     }
 }
-
 
 constexpr unsigned kTmem = 512;             // a block takes all of it
 constexpr int kChainThreads = 384;

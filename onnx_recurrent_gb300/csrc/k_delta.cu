@@ -321,36 +321,39 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
                 fence_after();
                 const unsigned kimg = sbase + s * Sm::stage, qimg = kimg + kBlock;
                 const unsigned timg = kimg + Im::keys, pimg = timg + 2 * kBlock;
-                // parts a of S and b of K or Q, over the keys
-                auto keys_product = [&](uint32_t d, unsigned img, int a, int b, bool add) {
+                // parts of S (from the first on, `count` of them) and part b of K or Q, over the keys
+                auto keys_product = [&](uint32_t d, unsigned img, int first, int count, int b, bool add) {
+#pragma unroll 1
+                    for (int a = first; a < first + count; ++a)
 #pragma unroll
-                    for (int ks = 0; ks < DKB * 4; ++ks)
-                        if (leader)
-                            mma_ts(tm + d, tm + Co::S + a * SR + ks * 8, desc_rows(img + (b * DKB + ks / 4) * 2 * kBlock + ks % 4 * 32), instr(C, false), add || ks > 0);
+                        for (int ks = 0; ks < DKB * 4; ++ks)
+                            if (leader)
+                                mma_ts(tm + d, tm + Co::S + a * SR + ks * 8, desc_rows(img + (b * DKB + ks / 4) * 2 * kBlock + ks % 4 * 32), instr(C, false),
+                                       add || a > first || ks > 0);
                 };
-                // a part of R or U, and a matrix's part, over the steps
-                auto steps_product = [&](uint32_t d, uint32_t from, int a, unsigned img, int b, bool add) {
+                // R or U and a matrix, over the steps: hi hi, lo hi, hi lo
+                auto steps_product = [&](uint32_t d, uint32_t from, unsigned img) {
+#pragma unroll 1
+                    for (int q = 0; q < 3; ++q)
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        if (leader)
-                            mma_ts(tm + d, tm + from + ks / 2 * 32 + a * 16 + ks % 2 * 8, desc_rows(img + b * kBlock + ks * 32), instr(C, false), add || ks > 0);
+                        for (int ks = 0; ks < 4; ++ks)
+                            if (leader)
+                                mma_ts(tm + d, tm + from + ks / 2 * 32 + (q == 1) * 16 + ks % 2 * 8, desc_rows(img + (q == 2) * kBlock + ks * 32), instr(C, false),
+                                       q > 0 || ks > 0);
                 };
-                keys_product(Co::R, kimg, 0, 0, false);
-                keys_product(Co::R, kimg, 1, 0, true);
-                if (KP == 2) keys_product(Co::R, kimg, 0, 1, true);
+                keys_product(Co::R, kimg, 0, 2, 0, false);
+                if (KP == 2) keys_product(Co::R, kimg, 0, 1, 1, true);
                 if (leader) mma_commit(&d_ready);
-                keys_product(Co::QS, qimg, 0, 0, false);
+                keys_product(Co::QS, qimg, 0, 1, 0, false);
                 if (!__all_sync(0xffffffffu, wait(&r_ready, ph, &given_up))) break;
                 fence_after();
-                steps_product(Co::U, Co::R, 0, timg, 0, false);
-                steps_product(Co::U, Co::R, 0, timg, 1, true);
-                steps_product(Co::U, Co::R, 1, timg, 0, true);
+                steps_product(Co::U, Co::R, timg);
                 if (leader) mma_commit(&u_ready);
-                keys_product(Co::QS, qimg, 1, 0, true);
-                if (KP == 2) keys_product(Co::QS, qimg, 0, 1, true);
+                keys_product(Co::QS, qimg, 1, 1, 0, true);
+                if (KP == 2) keys_product(Co::QS, qimg, 0, 1, 1, true);
                 if (!__all_sync(0xffffffffu, wait(&up_ready, ph, &given_up))) break;
                 fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int q = 0; q < 1 + KP; ++q)        // hi hi, lo hi, hi lo
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
@@ -358,9 +361,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
                             mma_ts(tm + Co::dS, tm + Co::U2 + ks / 2 * 32 + (q == 1) * 16 + ks % 2 * 8,
                                    desc_columns(kimg + (q == 2) * DKB * 2 * kBlock + ks * 2048, 2 * kBlock), instr(DKB * 64, true), q > 0 || ks > 0);
                 if (leader) mma_commit(&ds_ready);
-                steps_product(Co::PU, Co::U, 0, pimg, 0, false);
-                steps_product(Co::PU, Co::U, 0, pimg, 1, true);
-                steps_product(Co::PU, Co::U, 1, pimg, 0, true);
+                steps_product(Co::PU, Co::U, pimg);
                 if (leader) {
                     mma_commit(&o_ready);
                     mma_commit(&empty[s]);

@@ -112,29 +112,30 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_grad_chain_kernel(cons
                 fence_after();
                 const unsigned kimg = sbase + s * Sm::stage, qimg = kimg + kBlock;
                 const unsigned timg = kimg + Im::keys, pimg = timg + 2 * kBlock;
-                // first operand's part a at `from`, a matrix's part b transposed, over the steps
-                auto steps_product = [&](uint32_t d, uint32_t from, int a, unsigned img, int b, bool add) {
+                // the operand at `from` and a matrix transposed, over the steps: hi hi, lo hi, hi lo
+                auto steps_product = [&](uint32_t d, uint32_t from, unsigned img) {
+#pragma unroll 1
+                    for (int r = 0; r < 3; ++r)
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        if (leader)
-                            mma_ts(tm + d, tm + from + ks / 2 * 32 + a * 16 + ks % 2 * 8, desc_columns(img + b * kBlock + ks * 2048, kBlock), instr(C, true), add || ks > 0);
+                        for (int ks = 0; ks < 4; ++ks)
+                            if (leader)
+                                mma_ts(tm + d, tm + from + ks / 2 * 32 + (r == 1) * 16 + ks % 2 * 8, desc_columns(img + (r == 2) * kBlock + ks * 2048, kBlock),
+                                       instr(C, true), r > 0 || ks > 0);
                 };
                 // the same with K or Q, into G's increment
                 auto state_product = [&](uint32_t from, unsigned img) {
-#pragma unroll
-                    for (int r = 0; r < 1 + KP; ++r)        // hi hi, lo hi, hi lo
+#pragma unroll 1
+                    for (int r = 0; r < 1 + KP; ++r)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
                             if (leader)
                                 mma_ts(tm + Co::dG, tm + from + ks / 2 * 32 + (r == 1) * 16 + ks % 2 * 8,
                                        desc_columns(img + (r == 2) * DKB * 2 * kBlock + ks * 2048, 2 * kBlock), instr(DKB * 64, true), r > 0 || ks > 0);
                 };
-                steps_product(Co::PY, Co::X, 0, pimg, 0, false);
-                steps_product(Co::PY, Co::X, 0, pimg, 1, true);
-                steps_product(Co::PY, Co::X, 1, pimg, 0, true);
+                steps_product(Co::PY, Co::X, pimg);
                 if (!__all_sync(0xffffffffu, wait(&g_ready, ph, &given_up))) break;
                 fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int r = 0; r < 1 + KP; ++r)
 #pragma unroll
                     for (int ks = 0; ks < DKB * 4; ++ks)
@@ -144,9 +145,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_grad_chain_kernel(cons
                 if (leader) mma_commit(&d_ready);
                 if (!__all_sync(0xffffffffu, wait(&u_told, ph, &given_up))) break;
                 fence_after();
-                steps_product(Co::R, Co::U, 0, timg, 0, false);
-                steps_product(Co::R, Co::U, 0, timg, 1, true);
-                steps_product(Co::R, Co::U, 1, timg, 0, true);
+                steps_product(Co::R, Co::U, timg);
                 if (leader) mma_commit(&r_ready);
                 if (!__all_sync(0xffffffffu, wait(&x2_ready, ph, &given_up))) break;
                 fence_after();
