@@ -199,12 +199,16 @@ rnn_status rnn_delta_rule(rnn_delta_t pl, const rnn_delta_args* a)
     p.h0 = a->initial_state;
     p.hT = a->final_state;
     cudaStream_t st = (cudaStream_t)a->stream;
-    const size_t bytes = a->saved ? 0 : (size_t)(delta_keys_bytes(S, N, p.HK, p.DK, p.io) + delta_mats_bytes(S, N, p.H));
+    delta_split(p);
+    const size_t images = a->saved ? 0 : (size_t)(delta_keys_bytes(S, N, p.HK, p.DK, p.io) + delta_mats_bytes(S, N, p.H));
+    const size_t bytes = images + sizeof(float) * (size_t)delta_split_floats(p);
     char* scratch = nullptr;
     rs = claim_scratch(pl, bytes, st, &scratch);
     if (rs != RNN_OK) return rs;
     place(p, a->saved ? (void*)a->saved : scratch);
     if (!a->saved) p.kept = nullptr;
+    p.over = (float*)(scratch + images);
+    p.starts = p.over + N * p.H * (p.cuts - 1) * (int64_t)p.DK * (p.DV + p.DK);
     cudaError_t err = launch_delta(p, st, &pl->launches);
     if (err != cudaSuccess) return cuda_fail(err, "delta rule launch");
     return release_scratch(pl, bytes, st);

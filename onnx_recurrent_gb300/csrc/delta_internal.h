@@ -21,6 +21,11 @@ struct DeltaParams {
     unsigned char *keys, *mats;     // what the chunks' first launch leaves (delta_mma.cuh: Images)
     unsigned char* kept;    // the states before the chunks, and u (delta_kept_bytes); NULL: not kept
     int* status;
+    // A run whose chain is cut into `cuts` segments of cut_chunks chunks (delta_split): what takes a state over each of them,
+    // and the states before them.
+    int cuts;
+    int64_t cut_chunks;
+    float *over, *starts;   // [N, H, cuts - 1, DK, DV + DK] and [N, H, cuts, DK, DV]
 };
 
 struct DeltaGradParams {
@@ -65,6 +70,11 @@ inline int64_t delta_slopes_bytes(int64_t S, int64_t N, int64_t H, int64_t DK, i
     return delta_tiles(S, N, H, DV) * delta_slopes_tile((int)DK, io);
 }
 
+void delta_split(DeltaParams& p);
+inline int64_t delta_split_floats(const DeltaParams& p)
+{
+    return p.cuts > 1 ? p.N * p.H * p.DK * ((p.cuts - 1) * (int64_t)(p.DV + p.DK) + p.cuts * (int64_t)p.DV) : 0;
+}
 cudaError_t launch_delta(const DeltaParams& p, cudaStream_t s, int* launches);
 cudaError_t launch_delta_grad(const DeltaGradParams& p, cudaStream_t s, int* launches);
 cudaError_t launch_delta_step(const DeltaStepParams& p, cudaStream_t s, int* launches);

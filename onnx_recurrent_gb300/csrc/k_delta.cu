@@ -244,7 +244,10 @@ struct Columns {     // of tensor memory
     static constexpr uint32_t dS = 0, S = DKB * 64, R = 2 * DKB * 64, U = R + 64, U2 = U + 64, QS = U2 + 64, PU = R;
 };
 
-template <typename T, int DKB, int KP>
+// A chain may be cut into segments, whose states come from one another by what takes a state over a segment, S -> F S + E.  SEARCH:
+// finds these, without outputs: E as the state after the segment from zeros (the first one's from initial_state), F as that
+// of a head without values from the state 1, in a block of its own.
+template <typename T, int DKB, int KP, bool SEARCH>
 __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const DeltaParams p, const unsigned char* keys, const unsigned char* mats)
 {
     using Im = Images<DKB, KP>;
@@ -259,14 +262,20 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
     __shared__ int given_up;
     unsigned char* base = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
     unsigned char* sheets = base + ST * Sm::stage;       // V, V, Y
-    const int64_t nh = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
-    if (nh >= p.N * p.H) return;
+    const int64_t nhs = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
+    const int cuts = SEARCH ? p.cuts - 1 : p.cuts;
+    if (nhs >= p.N * p.H * cuts) return;
+    const int64_t nh = nhs / cuts;
+    const int cut = (int)(nhs - nh * cuts), tiles = (p.DV + 127) / 128;
+    const bool of_one = SEARCH && (int)blockIdx.x == tiles;         // F's block
+    if (of_one && cut == 0) return;
     const int64_t n = nh / p.H, chunks = delta_chunks(p.S);
     const int h = (int)(nh - n * p.H), hk = h / (p.H / p.HK);
     const int64_t len = row_length(p.lens, n, p.S, p.status);
-    const int live = (int)((len + C - 1) / C);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, v0 = blockIdx.x * 128;
-    const int cols = p.DV - v0 < 128 ? p.DV - v0 : 128;
+    const int64_t first = cut * p.cut_chunks, all = (len + C - 1) / C;
+    const int live = (int)(all <= first ? 0 : all - first < p.cut_chunks ? all - first : p.cut_chunks);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, v0 = of_one ? 0 : blockIdx.x * 128;
+    const int width = of_one ? p.DK : p.DV, cols = width - v0 < 128 ? width - v0 : 128;
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&full[i], 1);
@@ -305,8 +314,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
                 if (k >= ST && !wait(&empty[s], (unsigned)(k / ST - 1) & 1u, &given_up)) break;
                 unsigned char* st = base + s * Sm::stage;
                 mbar_arrive_expect_tx(&full[s], Sm::stage);
-                bulk_g2s(st, keys + ((n * p.HK + hk) * chunks + k) * Im::keys, Im::keys, &full[s]);
-                bulk_g2s(st + Im::keys, mats + (nh * chunks + k) * Im::mats, Im::mats, &full[s]);
+                bulk_g2s(st, keys + ((n * p.HK + hk) * chunks + first + k) * Im::keys, Im::keys, &full[s]);
+                bulk_g2s(st + Im::keys, mats + (nh * chunks + first + k) * Im::mats, Im::mats, &full[s]);
             }
             // no copy is in flight when the block ends
             for (int i = k > ST ? k - ST : 0; i < k; ++i) wait(&full[i % ST], (unsigned)(i / ST) & 1u, &never);
@@ -344,13 +353,15 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
                 keys_product(Co::R, kimg, 0, 2, 0, false);
                 if (KP == 2) keys_product(Co::R, kimg, 0, 1, 1, true);
                 if (leader) mma_commit(&d_ready);
-                keys_product(Co::QS, qimg, 0, 1, 0, false);
+                if (!SEARCH) keys_product(Co::QS, qimg, 0, 1, 0, false);
                 if (!__all_sync(0xffffffffu, wait(&r_ready, ph, &given_up))) break;
                 fence_after();
                 steps_product(Co::U, Co::R, timg);
                 if (leader) mma_commit(&u_ready);
-                keys_product(Co::QS, qimg, 1, 1, 0, true);
-                if (KP == 2) keys_product(Co::QS, qimg, 0, 1, 1, true);
+                if (!SEARCH) {
+                    keys_product(Co::QS, qimg, 1, 1, 0, true);
+                    if (KP == 2) keys_product(Co::QS, qimg, 0, 1, 1, true);
+                }
                 if (!__all_sync(0xffffffffu, wait(&up_ready, ph, &given_up))) break;
                 fence_after();
 #pragma unroll 1
@@ -361,7 +372,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
                             mma_ts(tm + Co::dS, tm + Co::U2 + ks / 2 * 32 + (q == 1) * 16 + ks % 2 * 8,
                                    desc_columns(kimg + (q == 2) * DKB * 2 * kBlock + ks * 2048, 2 * kBlock), instr(DKB * 64, true), q > 0 || ks > 0);
                 if (leader) mma_commit(&ds_ready);
-                steps_product(Co::PU, Co::U, pimg);
+                if (!SEARCH) steps_product(Co::PU, Co::U, pimg);
                 if (leader) {
                     mma_commit(&o_ready);
                     mma_commit(&empty[s]);
@@ -377,8 +388,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
             T* to = static_cast<T*>(p.Y.data) + n * p.Y.bs + (int64_t)h * p.DV + v0;
             const bool vw = (uintptr_t)from % 16 == 0 && p.V.ss % 8 == 0, yw = (uintptr_t)to % 16 == 0 && p.Y.ss % 8 == 0;
             auto load_v = [&](int k) {
-                const int64_t step = (int64_t)k * C + t;
-                rows_to_sheet(sheets + (k & 1) * kSheet, from + step * p.V.ss, step < len, vw, cols, t);
+                const int64_t step = (first + k) * C + t;
+                rows_to_sheet(sheets + (k & 1) * kSheet, from + step * p.V.ss, step < len && !of_one, vw, cols, t);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&v_full[k & 1]);
             };
@@ -388,8 +399,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
                     if (k >= 1 && !__all_sync(0xffffffffu, wait(&v_empty[(k + 1) & 1], (unsigned)((k - 1) / 2) & 1u, &given_up))) break;
                     load_v(k + 1);
                 }
+                if (SEARCH) continue;
                 if (!__all_sync(0xffffffffu, wait(&y_full, (unsigned)k & 1u, &given_up))) break;
-                const int64_t step = (int64_t)k * C + t;
+                const int64_t step = (first + k) * C + t;
                 if (step < len) sheet_to_rows(sheets + 2 * kSheet, to + step * p.Y.ss, yw, cols, t);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&y_empty);
@@ -401,19 +413,26 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
         const int half = warp / 4, row = warp % 4 * 32 + lane;
         const uint32_t my = tm + ((uint32_t)(warp % 4 * 32) << 16);
         const int v = v0 + row;
-        const bool col = v < p.DV;
+        const bool col = v < width;
         const int64_t at = nh * p.DK * p.DV + v;         // of this column's state
         const int d0 = half * SR;                        // its keys: SR from here
         f2 S[SR / 2], x[16];
         T vs[Sm::staged ? 1 : 32];
         // where a chunk's parts are kept for the gradient
-        unsigned char* kept = p.kept ? p.kept + (nh * chunks * gridDim.x + blockIdx.x) * delta_kept_tile(p.DK) : nullptr;
+        unsigned char* kept = !SEARCH && p.kept ? p.kept + ((nh * chunks + first) * gridDim.x + blockIdx.x) * delta_kept_tile(p.DK) : nullptr;
+        const float* h0 = SEARCH || p.cuts == 1 ? (cut == 0 && p.h0 ? p.h0 + at : nullptr)
+                        : cut == 0 && !p.h0   ? nullptr
+                                              : p.starts + (nh * cuts + cut) * (int64_t)p.DK * p.DV + v;
         float m = 0.f;
 #pragma unroll
         for (int i = 0; i < SR / 2; ++i) {
             float a[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) a[e] = p.h0 && col && d0 + 2 * i + e < p.DK ? p.h0[at + (int64_t)(d0 + 2 * i + e) * p.DV] : 0.f;
+            for (int e = 0; e < 2; ++e) {
+                const int d = d0 + 2 * i + e;
+                if (of_one) a[e] = d == v ? 1.f : 0.f;
+                else a[e] = h0 && col && d < p.DK ? h0[(int64_t)d * p.DV] : 0.f;
+            }
             S[i] = pack2(a[0], a[1]);
             m = most_of(m, S[i]);
         }
@@ -421,8 +440,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
             if constexpr (!Sm::staged) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                    const int64_t t = (int64_t)k * C + half * 32 + i;
-                    vs[i] = col && t < len ? static_cast<const T*>(p.V.data)[n * p.V.bs + t * p.V.ss + (int64_t)h * p.DV + v] : from_f<T>(0.f);
+                    const int64_t t = (first + k) * C + half * 32 + i;
+                    vs[i] = col && !of_one && t < len ? static_cast<const T*>(p.V.data)[n * p.V.bs + t * p.V.ss + (int64_t)h * p.DV + v] : from_f<T>(0.f);
                 }
             }
         };
@@ -444,8 +463,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
                 put_parts(my + Co::S + d0 / 2 + q * 16, my + Co::S + SR + d0 / 2 + q * 16, S + q * 16, down);
             tmem_st_wait();
         };
-        auto write_state = [&](float* to) {
-            to += (int64_t)d0 * p.DV;
+        auto write_state = [&](float* to, int apart) {
+            to += (int64_t)d0 * apart;
 #pragma unroll
             for (int i = 0; i < SR / 2; ++i) {
                 float a[2];
@@ -453,7 +472,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     if (d0 + 2 * i + e < p.DK) *to = a[e];
-                    to += p.DV;
+                    to += apart;
                 }
             }
         };
@@ -497,7 +516,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
             }
             if (k > 0) {
                 ok = __all_sync(0xffffffffu, ok && wait(&o_ready, php, &given_up));
-                if (ok) {
+                if (ok && !SEARCH) {
                     fence_after();
                     tmem_ld(my + Co::QS + half * 32, x);
                     tmem_ld(my + Co::PU + half * 32, y);
@@ -505,9 +524,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
             }
             if (k < live) tell(&s_ready);
             if (k > 0) {
-                if constexpr (Sm::staged)
+                if constexpr (Sm::staged && !SEARCH)
                     if (k > 1) ok = __all_sync(0xffffffffu, ok && wait(&y_empty, ph, &given_up));
-                if (ok) {
+                if (ok && !SEARCH) {
                     const f2 qs = dup2(old.up), pu = dup2(eu.up);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -523,7 +542,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            const int64_t t = (int64_t)(k - 1) * C + half * 32 + i;
+                            const int64_t t = (first + k - 1) * C + half * 32 + i;
                             float a[2];
                             unpack2(x[i / 2], a[0], a[1]);
                             if (col && t < len) static_cast<T*>(p.Y.data)[n * p.Y.bs + t * p.Y.ss + (int64_t)h * p.DV + v] = from_f<T>(a[i % 2]);
@@ -532,7 +551,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
                 }
                 __syncwarp();
                 if (lane == 0) {
-                    if constexpr (Sm::staged) mbar_arrive(&y_full);
+                    if constexpr (Sm::staged && !SEARCH) mbar_arrive(&y_full);
                     mbar_arrive(&empty[sp]);
                 }
             }
@@ -613,11 +632,16 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
                 kept += gridDim.x * delta_kept_tile(p.DK);
             }
         }
-        if (p.hT && col) write_state(p.hT + at);
-        // steps past the row's end
-        if (col)
-            for (int64_t t = len + half; t < p.S; t += 2)
-                static_cast<T*>(p.Y.data)[n * p.Y.bs + t * p.Y.ss + (int64_t)h * p.DV + v] = from_f<T>(0.f);
+        if (SEARCH) {
+            float* over = p.over + (nh * cuts + cut) * p.DK * (int64_t)(p.DV + p.DK);
+            if (col) write_state(of_one ? over + (int64_t)p.DK * p.DV + v : over + v, width);
+        } else if (cut == cuts - 1) {
+            if (p.hT && col) write_state(p.hT + at, p.DV);
+            // steps past the row's end
+            if (col)
+                for (int64_t t = len + half; t < p.S; t += 2)
+                    static_cast<T*>(p.Y.data)[n * p.Y.bs + t * p.Y.ss + (int64_t)h * p.DV + v] = from_f<T>(0.f);
+        }
     }
     fence_before();
     __syncthreads();
@@ -628,14 +652,76 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
     if (threadIdx.x == 0 && given_up) *p.status = 6;        // RNN_ERR_TIMEOUT
 }
 
+// The states before the segments, one after another: S <- F S + E.  A block has 32 columns of a head's state.
+constexpr int kJoined = 32;
+struct JoinSmem {
+    float S[2][kDeltaMaxKey][kJoined];
+    float F[kDeltaMaxKey][kDeltaMaxKey + 1];
+};
+__global__ void __launch_bounds__(kThreads) delta_join_kernel(const DeltaParams p)
+{
+    extern __shared__ __align__(1024) unsigned char raw[];
+    JoinSmem& s = *reinterpret_cast<JoinSmem*>(raw);
+    const int64_t nh = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
+    if (nh >= p.N * p.H) return;
+    const int tid = threadIdx.x, DK = p.DK, DV = p.DV, v0 = blockIdx.x * kJoined, c = tid % 8 * 4, r = tid / 8;
+    // (initial_state too: final_state may be the same memory)
+    if (p.h0)
+        for (int i = tid; i < DK * kJoined; i += kThreads) {
+            const int d = i / kJoined, v = v0 + i % kJoined;
+            if (v < DV) p.starts[(nh * p.cuts * DK + d) * (int64_t)DV + v] = p.h0[(nh * DK + d) * (int64_t)DV + v];
+        }
+    for (int cut = 0; cut < p.cuts - 1; ++cut) {
+        const float* E = p.over + (nh * (p.cuts - 1) + cut) * DK * (int64_t)(DV + DK);
+        const float* F = E + (int64_t)DK * DV;
+        if (cut)
+            for (int i = tid; i < DK * DK; i += kThreads) s.F[i / DK][i % DK] = F[i];
+        __syncthreads();
+        const float(*old)[kJoined] = s.S[(cut + 1) & 1];
+        float acc[4][4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int d = r + 32 * a, v = v0 + c + e;
+                acc[a][e] = d < DK && v < DV ? E[(int64_t)d * DV + v] : 0.f;
+            }
+        if (cut)
+#pragma unroll 4
+            for (int k = 0; k < DK; ++k) {
+                const float4 x = *reinterpret_cast<const float4*>(&old[k][c]);
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                    const float f = s.F[r + 32 * a][k];      // (rows past DK are not used)
+                    acc[a][0] = fmaf(f, x.x, acc[a][0]);
+                    acc[a][1] = fmaf(f, x.y, acc[a][1]);
+                    acc[a][2] = fmaf(f, x.z, acc[a][2]);
+                    acc[a][3] = fmaf(f, x.w, acc[a][3]);
+                }
+            }
+        float* out = p.starts + (nh * p.cuts + cut + 1) * DK * (int64_t)DV;
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int d = r + 32 * a, v = v0 + c + e;
+                s.S[cut & 1][d][c + e] = acc[a][e];
+                if (d < DK && v < DV) out[(int64_t)d * DV + v] = acc[a][e];
+            }
+        __syncthreads();
+    }
+}
+
 template <typename T, int DKB>
 cudaError_t run(const DeltaParams& p, cudaStream_t st, int* launches)
 {
     constexpr int KP = sizeof(T) == 4 ? 2 : 1;
     constexpr size_t prep_smem = sizeof(PrepSmem<DKB, KP>) + 1024, run_smem = ChainSmem<T, DKB, KP>::bytes;
-    static std::atomic<uint64_t> prep_done{0}, run_done{0};
+    static std::atomic<uint64_t> prep_done{0}, run_done{0}, search_done{0}, join_done{0};
     cudaError_t e = allow_shared(delta_prep_kernel<T, DKB, KP>, prep_smem, prep_done);
-    if (e == cudaSuccess) e = allow_shared(delta_run_kernel<T, DKB, KP>, run_smem, run_done);
+    if (e == cudaSuccess) e = allow_shared(delta_run_kernel<T, DKB, KP, false>, run_smem, run_done);
+    if (e == cudaSuccess && p.cuts > 1) e = allow_shared(delta_run_kernel<T, DKB, KP, true>, run_smem, search_done);
+    if (e == cudaSuccess && p.cuts > 1) e = allow_shared(delta_join_kernel, sizeof(JoinSmem), join_done);
     if (e != cudaSuccess) return e;
     const int64_t nh = p.N * p.H;
     unsigned char *keys = p.keys, *mats = p.mats;
@@ -643,7 +729,13 @@ cudaError_t run(const DeltaParams& p, cudaStream_t st, int* launches)
         delta_prep_kernel<T, DKB, KP><<<heads_grid(delta_chunks(p.S), nh), kThreads, prep_smem, st>>>(p, keys, mats);
         ++*launches;
     }
-    delta_run_kernel<T, DKB, KP><<<heads_grid((p.DV + 127) / 128, nh), kChainThreads, run_smem, st>>>(p, keys, mats);
+    const int64_t tiles = (p.DV + 127) / 128;
+    if (p.cuts > 1) {
+        delta_run_kernel<T, DKB, KP, true><<<heads_grid(tiles + 1, nh * (p.cuts - 1)), kChainThreads, run_smem, st>>>(p, keys, mats);
+        delta_join_kernel<<<heads_grid((p.DV + kJoined - 1) / kJoined, nh), kThreads, sizeof(JoinSmem), st>>>(p);
+        *launches += 2;
+    }
+    delta_run_kernel<T, DKB, KP, false><<<heads_grid(tiles, nh * p.cuts), kChainThreads, run_smem, st>>>(p, keys, mats);
     ++*launches;
     return cudaGetLastError();
 }
@@ -655,6 +747,27 @@ cudaError_t run(const DeltaParams& p, cudaStream_t st, int* launches)
 }
 
 }  // namespace
+
+// A chain is cut where there are too few of them for the multiprocessors: the search for what takes a state over a segment costs
+// as much again, or twice that (F's blocks), at `cuts` times the blocks.  In waves of blocks times chunks; joining costs a few chunks.
+void delta_split(DeltaParams& p)
+{
+    const int64_t chunks = delta_chunks(p.S), tiles = (p.DV + 127) / 128, chains = p.N * p.H;
+    auto waves = [&](int64_t blocks) { return (blocks + p.sms - 1) / p.sms; };
+    p.cuts = 1;
+    p.cut_chunks = chunks > 0 ? chunks : 1;
+    if (p.sms <= 0 || chunks < 16 || chains * tiles * 2 > p.sms) return;
+    double best = 0.8 * (double)(waves(chains * tiles) * chunks);
+    for (int64_t cuts = 2; cuts <= 64 && cuts * 4 <= chunks; ++cuts) {
+        const int64_t per = (chunks + cuts - 1) / cuts, n = (chunks + per - 1) / per;
+        const double cost = (double)((waves(chains * (tiles + 1) * (n - 1)) + waves(chains * tiles * n)) * per) + 6.0 + 1.0 * (double)n;
+        if (n == cuts && cost < best) {
+            best = cost;
+            p.cuts = (int)n;
+            p.cut_chunks = per;
+        }
+    }
+}
 
 cudaError_t launch_delta(const DeltaParams& p, cudaStream_t s, int* launches)
 {

@@ -75,6 +75,34 @@ def test_run_and_gradient(size, io):
     Case(*size, io=io, layout=size[1] % 2, carried=size[0] > 1).check()
 
 
+# few heads and long rows, whose chain is cut into segments: whole ones, ragged ones, a last one of a few steps
+LONG = [(1, 4096, 1, 1, 16, 32), (2, 4200, 2, 1, 20, 40), (1, 4400, 1, 1, 72, 130), (1, 5121, 3, 3, 8, 8)]
+
+
+@pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("size", LONG, ids=str)
+def test_long_rows(size, io):
+    c = Case(*size, io=io, carried=True, decay=0.3)
+    c.check()
+    assert orc.rnn_delta_last_launch_count(c.plan) == 2        # the gradient's
+    orc.delta_rule(c.plan, *c.gpu)
+    assert orc.rnn_delta_last_launch_count(c.plan) == 4
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_long_rows_of_other_lengths_in_place(io):
+    lens = [4500, 0, 3, 2700, 64]
+    c = Case(5, 4500, 2, 1, 24, 48, io=io, layout=0, lens=lens, carried=True, decay=0.3)
+    Y, state, _ = c.check()
+    st, y = c.gstate.clone(), torch.full_like(Y, 7.0)
+    orc.rnn_delta_rule(c.plan, *c.gpu, c.glens, st, y, st)
+    assert torch.equal(st, state) and torch.equal(y, Y)
+    # without a state to begin with, as with zeros
+    a = orc.delta_rule(c.plan, *c.gpu, c.glens)
+    b = orc.delta_rule(c.plan, *c.gpu, c.glens, torch.zeros_like(st))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 def test_rows_of_other_lengths(io):
     c = Case(6, 150, 2, 1, 32, 48, io=io, lens=[150, 0, 1, 64, 65, 149], carried=True)
