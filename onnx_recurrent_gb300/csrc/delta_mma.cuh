@@ -66,6 +66,11 @@ __device__ __forceinline__ uint64_t desc_columns(unsigned saddr, unsigned apart)
 // Instruction descriptor: fp16 operands, fp32 sums, M = 128; `columns`: B's sum runs along its rows.
 __host__ __device__ constexpr uint32_t instr(int n, bool columns) { return (1u << 4) | (columns ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | (8u << 24); }
 
+// Asks for memory to be brought into L2 (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void prefetch(const void* at, unsigned bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
+}
 // One lane of a converged warp.  Products are issued by a whole warp of which one lane acts: operands
 // then stay in uniform registers (33 clocks a product of 128 x 64 x 16; by a lone lane, 45).
 __device__ __forceinline__ bool elected()

@@ -471,8 +471,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_grad_chain_kernel(cons
 //     q_i.dQ_i - k_i.dK_i + 2 (sum_j EA_ij K_i.K_j - b_i e^G_i k_i.X2_i)
 // and no sum runs down a column.
 //
-// A block walks through chunks; what the next one needs first is copied while this one's last products run, 240 KB a chunk and
-// head of 128 x 128 at 16 bits.
+// Bytes bound it, 240 KB a chunk and head of 128 x 128 at 16 bits, copied as they are.
 constexpr int kRestThreads = 512;
 template <int DKB, int KP>
 struct RestSmem {
@@ -495,176 +494,132 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
     using Sm = RestSmem<DKB, KP>;
     constexpr uint32_t cX = 0, cX3 = 128, cK = 256, cE = 384, cKQ = 448, cKE = 384;     // columns of tensor memory
     extern __shared__ __align__(1024) unsigned char raw[];
-    __shared__ __align__(8) uint64_t s_full, r_full, g_full, k_full, x_done, x3_done, kq_done, k_done, done;
+    __shared__ __align__(8) uint64_t first_full, g_full, k_full, x_done, x3_done, kq_done, k_done, done;
     __shared__ Sums sums;
     __shared__ float k_scale[C], q_scale[C];
-    __shared__ __align__(16) float fac[768];        // (written 16 bytes at a time)
-    __shared__ float scales[8];
+    __shared__ float fac[768], scales[8];
     __shared__ float rv[C], part[5][4][128], dots[kRestThreads / 32], slope[C], end[C], db[C];
     __shared__ float2 carry;
     __shared__ uint32_t slot;
     __shared__ int given_up;
     const DeltaParams& p = q.f;
-    const int64_t chunks = delta_chunks(p.S), items = p.N * p.HK * chunks;
-    const int per = p.H / p.HK, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int DK = p.DK, DV = p.DV, tiles = (DV + 127) / 128;
+    const int64_t chunk = blockIdx.x, chunks = gridDim.x, nk = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
+    if (nk >= p.N * p.HK) return;
+    const int64_t n = nk / p.HK, t0 = chunk * C;
+    const int hk = (int)(nk - n * p.HK), per = p.H / p.HK, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int64_t len = row_length(p.lens, n, p.S, p.status);
+    const int DK = p.DK, DV = p.DV, steps = (int)(p.S - t0 < C ? p.S - t0 : C);
     // a thread's step, whether of the upper half (dK) or the lower (dQ), and its quarter of the columns
     const int lane_row = warp % 4 * 32 + lane, i = lane_row % C, quarter = warp / 4;
     const bool upper = lane_row < C;
     const View& out = upper ? q.dK : q.dQ;
-    unsigned char* base = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
-    float* E = reinterpret_cast<float*>(base + Sm::e);
-    if (tid == 0) {
-        mbar_init(&s_full, 1);
-        mbar_init(&r_full, 1);
-        mbar_init(&g_full, 1);
-        mbar_init(&k_full, 1);
-        mbar_init(&x_done, 1);
-        mbar_init(&x3_done, 1);
-        mbar_init(&kq_done, 1);
-        mbar_init(&k_done, 2);      // both products' warps
-        mbar_init(&done, 4);
-        given_up = 0;
-        mbar_fence_init();
-    }
-    if (warp == 0) tmem_alloc(&slot, kTmem);
-    fence_before();
-    __syncthreads();
-    fence_after();
-    const uint32_t tm = __shfl_sync(0xffffffffu, slot, 0), my = tm + ((uint32_t)(warp % 4 * 32) << 16);
-    const unsigned sbase = __shfl_sync(0xffffffffu, smem_addr(base), 0);
-    const bool leader = warp < 4 && elected();       // products are issued by four warps, which keep the tensor cores busier than one
-    const int64_t kept_tile = delta_kept_tile(DK), slopes_tile = delta_slopes_tile(DK, KP == 2 ? 0 : 1);
-    constexpr unsigned kStates = 2 * DKB * kSheetImage;
-    // all threads wait, and know whether all did
-    unsigned phase = 0;
-    auto await = [&](uint64_t* b, bool so_far) {
-        fence_before();
-        const bool ok = __syncthreads_and(so_far && wait(b, phase, &given_up));
-        fence_after();
-        return ok;
-    };
-    // A chunk of a key head, and a head and tile of it; those past a row's end have nothing to load.
-    struct Place {
-        int64_t item, n, chunk, t0, len, at;        // at: of the head's chunk
-        int hk, part, tile;                         // part: of the key head's heads
-    };
-    __shared__ Place ahead;     // the next that has something to load; known from the round's first barrier on
-    // the next chunk of this block is so many rows, key heads and chunks on (divided once: 64-bit divisions are slow)
-    const int64_t step_n = gridDim.x / (p.HK * chunks), step_rest = gridDim.x - step_n * p.HK * chunks;
-    const int step_hk = (int)(step_rest / chunks);
-    const int64_t step_chunk = step_rest - step_hk * chunks;
-    auto locate = [&](Place& w) {
-        w.t0 = w.chunk * C;
-        w.part = w.tile = 0;
-        w.len = w.n < p.N ? row_length(p.lens, w.n, p.S, p.status) : 0;
-        w.at = (w.n * p.H + w.hk * per) * chunks + w.chunk;
-    };
-    auto on = [&](Place& w) {
-        w.item += gridDim.x;
-        w.n += step_n;
-        w.hk += step_hk;
-        w.chunk += step_chunk;
-        if (w.chunk >= chunks) w.chunk -= chunks, ++w.hk;
-        if (w.hk >= p.HK) w.hk -= p.HK, ++w.n;
-        locate(w);
-    };
-    auto kept_of = [&](const Place& w) { return p.kept + (w.at * tiles + w.tile) * kept_tile; };
-    auto slopes_of = [&](const Place& w) { return q.slopes + (w.at * tiles + w.tile) * slopes_tile; };
-    auto keys_of = [&](const Place& w) { return p.keys + w.item * Im::keys; };
-    // one thread's copies: of the state before the chunk, of dR, dY and u, of K and Q
-    auto copy_state = [&](const Place& w) {
-        mbar_arrive_expect_tx(&s_full, kStates);
-        bulk_g2s(base + Sm::states, kept_of(w), kStates, &s_full);
-    };
-    auto copy_rows = [&](const Place& w) {
-        const unsigned char *kept = kept_of(w), *slopes = slopes_of(w);
-        mbar_arrive_expect_tx(&r_full, (4 + KP) * kSheetImage);
-        bulk_g2s(base + Sm::r, slopes + kStates, kSheetImage, &r_full);
-        bulk_g2s(base + Sm::r + 2 * kSheetImage, slopes + kStates + kSheetImage, kSheetImage, &r_full);
-        bulk_g2s(base + Sm::y, slopes + kStates + 2 * kSheetImage, kSheetImage, &r_full);
-        if (KP == 2) bulk_g2s(base + Sm::y + 2 * kSheetImage, slopes + kStates + 3 * kSheetImage, kSheetImage, &r_full);
-        bulk_g2s(base + Sm::u, kept + kStates, 2 * kSheetImage, &r_full);
-    };
-    auto copy_keys = [&](const Place& w) {
-        mbar_arrive_expect_tx(&k_full, Im::keys);
-        bulk_g2s(base + Sm::keys, keys_of(w), Im::keys, &k_full);
-    };
-    // every thread's own loads, for the round after: g, the factors and scales
-    float g_next = 0.f, scale_next = 0.f;
-    float4 fac_next;
-    auto load_own = [&](const Place& w) {
-        const int h = w.hk * per + w.part;
-        g_next = load_g(p.g, w.n, h, w.t0, w.len);
-        if (tid < 192) fac_next = reinterpret_cast<const float4*>(p.mats + w.at * Im::mats + 4 * kBlock)[tid];
-        if (tid < 2) scale_next = reinterpret_cast<const float*>(kept_of(w) + kStates + 2 * kSheetImage)[tid];
-        else if (tid < 5) scale_next = reinterpret_cast<const float*>(slopes_of(w) + kStates + (2 + KP) * kSheetImage)[tid - 2];
-    };
-    float dot_all = 0.f;        // warp 0's
-    bool ok = true, begun = false;
-    Place w{};
-    w.item = blockIdx.x;
-    w.n = w.item / (p.HK * chunks);
-    w.hk = (int)((w.item - w.n * p.HK * chunks) / chunks);
-    w.chunk = w.item - (w.n * p.HK + w.hk) * chunks;
-    locate(w);
-    for (; w.item < items && ok; on(w)) {
-        float acc[DKB][16];
+    float acc[DKB][16];
 #pragma unroll
-        for (int b = 0; b < DKB; ++b)
+    for (int b = 0; b < DKB; ++b)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[b][e] = 0.f;
-        const int64_t n = w.n, t0 = w.t0, len = w.len;
-        const int hk = w.hk, steps = (int)(p.S - t0 < C ? p.S - t0 : C);
-        if (t0 >= len) {
-            for (int j = tid; j < steps * per; j += kRestThreads) {
-                const int t = j / per, h = hk * per + j % per;
-                if (q.dg.data) static_cast<float*>(q.dg.data)[n * q.dg.bs + (t0 + t) * q.dg.ss + h] = 0.f;
-                if (q.dbeta.data) static_cast<float*>(q.dbeta.data)[n * q.dbeta.bs + (t0 + t) * q.dbeta.ss + h] = 0.f;
-            }
+        for (int e = 0; e < 16; ++e) acc[b][e] = 0.f;
+    if (t0 >= len) {
+        for (int j = tid; j < steps * per; j += kRestThreads) {
+            const int t = j / per, h = hk * per + j % per;
+            if (q.dg.data) static_cast<float*>(q.dg.data)[n * q.dg.bs + (t0 + t) * q.dg.ss + h] = 0.f;
+            if (q.dbeta.data) static_cast<float*>(q.dbeta.data)[n * q.dbeta.bs + (t0 + t) * q.dbeta.ss + h] = 0.f;
         }
-        for (bool last = t0 >= len; !last;) {
-            const int h = hk * per + w.part, tile = w.tile;
-            last = w.part == per - 1 && tile == tiles - 1;
+    } else {
+        unsigned char* base = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+        float* E = reinterpret_cast<float*>(base + Sm::e);
+        if (tid == 0) {
+            mbar_init(&first_full, 1);
+            mbar_init(&g_full, 1);
+            mbar_init(&k_full, 1);
+            mbar_init(&x_done, 1);
+            mbar_init(&x3_done, 1);
+            mbar_init(&kq_done, 1);
+            mbar_init(&k_done, 1);
+            mbar_init(&done, 1);
+            given_up = 0;
+            mbar_fence_init();
+        }
+        if (warp == 0) tmem_alloc(&slot, kTmem);
+        fence_before();
+        __syncthreads();
+        fence_after();
+        const uint32_t tm = __shfl_sync(0xffffffffu, slot, 0), my = tm + ((uint32_t)(warp % 4 * 32) << 16);
+        const unsigned sbase = __shfl_sync(0xffffffffu, smem_addr(base), 0);
+        const bool leader = warp == 0 && elected();
+        const int tiles = (DV + 127) / 128;
+        const int64_t kept_tile = delta_kept_tile(DK), slopes_tile = delta_slopes_tile(DK, KP == 2 ? 0 : 1);
+        constexpr unsigned kStates = 2 * DKB * kSheetImage;
+        // all threads wait, and know whether all did
+        unsigned phase = 0;
+        float dot_all = 0.f;        // warp 0's
+        auto await = [&](uint64_t* b) {
+            fence_before();
+            const bool ok = __syncthreads_and(wait(b, phase, &given_up));
+            fence_after();
+            return ok;
+        };
+        bool ok = true;
+        for (int round = 0; round < per * tiles; ++round) {
+            const int h = hk * per + round / tiles, tile = round % tiles, v0 = tile * 128;
+            const int64_t nh = n * p.H + h, at = nh * chunks + chunk;
+            const unsigned char *kept = p.kept + (at * tiles + tile) * kept_tile, *slopes = q.slopes + (at * tiles + tile) * slopes_tile;
+            const unsigned char* keys = p.keys + (nk * chunks + chunk) * Im::keys;
+            const float g = load_g(p.g, n, h, t0, len);
+            float4 fac4;
+            if (tid < 192) fac4 = reinterpret_cast<const float4*>(p.mats + at * Im::mats + 4 * kBlock)[tid];
+            float scale_one = 0.f;
+            if (tid < 2) scale_one = reinterpret_cast<const float*>(kept + kStates + 2 * kSheetImage)[tid];
+            else if (tid < 5) scale_one = reinterpret_cast<const float*>(slopes + kStates + (2 + KP) * kSheetImage)[tid - 2];
             if (tid == 0) {
-                Place to = w;
-                if (!last) {
-                    if (++to.tile == tiles) to.tile = 0, ++to.part, to.at += chunks;
-                } else {
-                    do on(to);
-                    while (to.item < items && to.t0 >= to.len);
-                }
-                ahead = to;
-            }
-            if (!begun) {
-                if (tid == 0) {
-                    copy_rows(w);
-                    copy_state(w);
-                    if (Sm::early) copy_keys(w);
-                }
-                load_own(w);
-                begun = true;
-            }
-            // V at the warp's four steps, four values 32 apart a lane
-            T vs[4][4];
-            {
-                const int v0 = tile * 128 + lane;
-                const T* row = static_cast<const T*>(p.V.data) + n * p.V.bs + (t0 + warp * 4) * p.V.ss + (int64_t)h * DV + v0;
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) vs[t][e] = t0 + warp * 4 + t < len && v0 + 32 * e < DV ? row[t * p.V.ss + 32 * e] : from_f<T>(0.f);
+                mbar_arrive_expect_tx(&first_full, kStates + (4 + KP) * kSheetImage + (Sm::early ? Im::keys : 0));
+                bulk_g2s(base + Sm::r, slopes + kStates, kSheetImage, &first_full);
+                bulk_g2s(base + Sm::r + 2 * kSheetImage, slopes + kStates + kSheetImage, kSheetImage, &first_full);
+                bulk_g2s(base + Sm::y, slopes + kStates + 2 * kSheetImage, kSheetImage, &first_full);
+                if (KP == 2) bulk_g2s(base + Sm::y + 2 * kSheetImage, slopes + kStates + 3 * kSheetImage, kSheetImage, &first_full);
+                bulk_g2s(base + Sm::u, kept + kStates, 2 * kSheetImage, &first_full);
+                bulk_g2s(base + Sm::states, kept, kStates, &first_full);
+                if (Sm::early) bulk_g2s(base + Sm::keys, keys, Im::keys, &first_full);
             }
             if (KP == 1)            // 16-bit values have no second part
                 for (int j = tid; j < (int)kSheetImage / 16; j += kRestThreads)
                     reinterpret_cast<uint4*>(base + Sm::y + 2 * kSheetImage)[j] = make_uint4(0, 0, 0, 0);
             fence_shared();
-            if (tid < 192) reinterpret_cast<float4*>(fac)[tid] = fac_next;
-            if (tid < 5) scales[tid] = scale_next;
-            form_sums(sums, g_next, &carry);
+            // V at the warp's four steps, four values 32 apart a lane
+            T vs[4][4];
+            {
+                const T* row = static_cast<const T*>(p.V.data) + n * p.V.bs + (t0 + warp * 4) * p.V.ss + (int64_t)h * DV + v0 + lane;
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        vs[t][e] = t0 + warp * 4 + t < len && v0 + lane + 32 * e < DV ? row[t * p.V.ss + 32 * e] : from_f<T>(0.f);
+            }
+            if (tid < 192) reinterpret_cast<float4*>(fac)[tid] = fac4;
+            if (tid < 5) scales[tid] = scale_one;
+            form_sums(sums, g, &carry);
             const float s_up = scales[0], u_up = scales[1], g_up = scales[2], r_up = scales[3], y_up = p.scale * scales[4];
-            ok = await(&r_full, true);
+            ok = await(&first_full);
             if (!ok) break;
+            // What comes next on this multiprocessor, into L2: blocks load and compute at the same times, and their loads alone
+            // would wait for one another at the memory.
+            if (tid == 32) {
+                int64_t next_at = at * tiles + tile + 1, next_keys = -1;
+                bool there = true;
+                if (round + 1 == per * tiles) {
+                    const int64_t b = nk * chunks + chunk + p.sms, bk = b / chunks;
+                    there = bk < p.N * p.HK;
+                    next_at = ((bk / p.HK * p.H + bk % p.HK * per) * chunks + b % chunks) * tiles;
+                    next_keys = b;
+                } else if (tile + 1 == tiles) {
+                    next_at = (at + chunks) * tiles;
+                }
+                if (there) {
+                    prefetch(p.kept + next_at * kept_tile, (unsigned)kept_tile);
+                    prefetch(q.slopes + next_at * slopes_tile, (unsigned)slopes_tile);
+                    prefetch(p.mats + next_at / tiles * Im::mats + 4 * kBlock, 3072);
+                    if (next_keys >= 0) prefetch(p.keys + next_keys * Im::keys, Im::keys);
+                }
+            }
             const unsigned kimg = sbase + Sm::keys, qimg = kimg + kBlock;
             auto key_products = [&] {
 #pragma unroll 1
@@ -684,12 +639,7 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                         if (leader)
                             mma_ss(tm + cE, desc_kept(sbase + Sm::r + (r == 1) * 2 * kSheetImage, ks), desc_kept(sbase + Sm::u + (r == 2) * kSheetImage, ks),
                                    instr(C, true) | 1u << 15, r > 0 || ks > 0);
-                if (Sm::early) {
-                    ok = __all_sync(0xffffffffu, wait(&k_full, phase, &given_up));
-                    key_products();
-                }
-            } else if (warp == 1) {
-                ok = __all_sync(0xffffffffu, wait(&s_full, phase, &given_up));
+                if (Sm::early) key_products();
 #pragma unroll 1
                 for (int r = 0; r < 3; ++r)     // [dR; dY'] S0^T
 #pragma unroll
@@ -724,10 +674,6 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                 tmem_ld16(my + cE + quarter * 16, e);
                 tmem_ld16(my + cKQ + quarter * 16, kq);
                 const float mine = (upper ? -r_up : y_up) * u_up, es = fac[(upper ? kKeyScale : kQueryScale) + i];
-                if (quarter * 16 > warp % 2 * 32 + 31) {        // all above the diagonal
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) e[c] = 0.f;
-                } else
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
                     const int j = quarter * 16 + c;
@@ -747,13 +693,12 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
 #pragma unroll
                 for (int c = 0; c < 16; ++c) E[lane_row * C + ((quarter * 16 + c) ^ lane)] = e[c];
             };
-            if (Sm::early) {        // (each warp by itself: the first is issuing products still)
-                ok = ok && wait(&k_full, phase, &given_up) && wait(&s_full, phase, &given_up) && wait(&kq_done, phase, &given_up);
-                __syncwarp();
-                fence_after();
+            if (Sm::early) {
+                ok = await(&kq_done);
+                if (!ok) break;
                 form_e();
             }
-            ok = await(&x_done, ok && wait(&s_full, phase, &given_up));
+            ok = await(&x_done);
             if (!ok) break;
             // S0 to registers, dS1 in its place
             uint4 s0[DKB][4];
@@ -769,12 +714,12 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
             __syncthreads();
             if (tid == 0) {
                 mbar_arrive_expect_tx(&g_full, kStates);
-                bulk_g2s(base + Sm::states, slopes_of(w), kStates, &g_full);
+                bulk_g2s(base + Sm::states, slopes, kStates, &g_full);
             }
             if (Sm::early) put_e();
-            ok = await(&g_full, true);
+            ok = await(&g_full);
             if (!ok) break;
-            if (warp == 2) {
+            if (warp == 0) {
 #pragma unroll 1
                 for (int r = 0; r < 3; ++r)     // U dS1^T
 #pragma unroll
@@ -805,18 +750,19 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                 for (int o = 16; o; o /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, o);
                 if (lane == 0) dots[warp] = dot * (g_up * s_up);
             }
-            ok = await(&x3_done, true);
+            ok = await(&x3_done);
             if (!ok) break;
-            if (Sm::early) {
-                if (tid == 0 && ahead.item < items) copy_state(ahead);
-            } else {
+            if (!Sm::early) {
                 fence_shared();
                 __syncthreads();
-                if (tid == 0) copy_keys(w);
-                ok = await(&k_full, true);
+                if (tid == 0) {
+                    mbar_arrive_expect_tx(&k_full, Im::keys);
+                    bulk_g2s(base + Sm::keys, keys, Im::keys, &k_full);
+                }
+                ok = await(&k_full);
                 if (!ok) break;
                 if (warp == 0) key_products();
-                ok = await(&kq_done, true);
+                ok = await(&kq_done);
                 if (!ok) break;
                 form_e();
                 put_e();
@@ -853,7 +799,7 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
             }
             fence_shared();
             __syncthreads();
-            if (warp == 3) {
+            if (warp == 0) {
 #pragma unroll 1
                 for (int r = 0; r < 1 + KP; ++r)    // hi hi, lo hi, hi lo
 #pragma unroll
@@ -861,8 +807,6 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                         if (leader)
                             mma_ss(tm + cK, desc_rows(sbase + Sm::a1 + (r == 1) * kSheetImage + ks * 32),
                                    desc_columns(kimg + (r == 2) * DKB * 2 * kBlock + ks * 2048, 2 * kBlock), instr(DKB * 64, true), r > 0 || ks > 0);
-                if (leader) mma_commit(&k_done);
-            } else if (warp == 0) {
 #pragma unroll 1
                 for (int r = 0; r < 1 + KP; ++r)
 #pragma unroll
@@ -920,13 +864,8 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                 part[2][quarter][lane_row] = es * (r_up * s_up * first) * s1;       // e^G k.X2 (of the upper half)
                 part[3][quarter][lane_row] = es * f3 * s3;      // e^(G_last - G) k.X3
             }
-            ok = await(&k_done, true);
+            ok = await(&k_done);
             if (!ok) break;
-            const bool more = ahead.item < items;
-            if (more) {
-                if (tid == 0) copy_rows(ahead);
-                load_own(ahead);
-            }
             {
                 const float mine = upper ? k_scale[i] : q_scale[i];
                 float s = 0.f;
@@ -1006,57 +945,43 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
             fence_before();
             __syncthreads();        // the next round's images take the place of this one's
             fence_after();
-            if (tid == 0 && more) {
-                if (Sm::early) copy_keys(ahead);
-                else copy_state(ahead);
-            }
-            if (!last) {
-                if (++w.tile == tiles) w.tile = 0, ++w.part, w.at += chunks;
-            }
         }
-        if (!ok) break;
-        if (out.data && i < steps) {
-            T* row = static_cast<T*>(out.data) + n * out.bs + (t0 + i) * out.ss + (int64_t)hk * DK;
-            const bool in = t0 + i < len;
-            constexpr int VEC = 16 / (int)sizeof(T);
-            const bool vec = (uintptr_t)out.data % 16 == 0 && (out.ss | out.bs | DK) % VEC == 0;
+        if (!ok && warp == 0) {     // no product is in flight when the block ends
+            int never = 0;
+            if (leader) mma_commit(&done);
+            wait(&done, 0, &never);
+        }
+        fence_before();
+        __syncthreads();
+        if (warp == 0) {
+            fence_after();
+            tmem_free(tm, kTmem);
+        }
+        if (tid == 0 && given_up) *p.status = 6;        // RNN_ERR_TIMEOUT
+    }
+    if (out.data && i < steps) {
+        T* row = static_cast<T*>(out.data) + n * out.bs + (t0 + i) * out.ss + (int64_t)hk * DK;
+        const bool in = t0 + i < len;
+        constexpr int VEC = 16 / (int)sizeof(T);
+        const bool vec = (uintptr_t)out.data % 16 == 0 && (out.ss | out.bs | DK) % VEC == 0;
 #pragma unroll
-            for (int b = 0; b < DKB; ++b) {
-                const int d0 = quarter * DKB * 16 + b * 16;
+        for (int b = 0; b < DKB; ++b) {
+            const int d0 = quarter * DKB * 16 + b * 16;
 #pragma unroll
-                for (int c = 0; c < 16; c += VEC) {
-                    __align__(16) T x[VEC];
+            for (int c = 0; c < 16; c += VEC) {
+                __align__(16) T x[VEC];
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) x[e] = from_f<T>(in ? acc[b][c + e] : 0.f);
-                    if (vec) {
-                        if (d0 + c < DK) *reinterpret_cast<uint4*>(row + d0 + c) = *reinterpret_cast<const uint4*>(x);
-                    } else {
+                for (int e = 0; e < VEC; ++e) x[e] = from_f<T>(in ? acc[b][c + e] : 0.f);
+                if (vec) {
+                    if (d0 + c < DK) *reinterpret_cast<uint4*>(row + d0 + c) = *reinterpret_cast<const uint4*>(x);
+                } else {
 #pragma unroll
-                        for (int e = 0; e < VEC; ++e)
-                            if (d0 + c + e < DK) row[d0 + c + e] = x[e];
-                    }
+                    for (int e = 0; e < VEC; ++e)
+                        if (d0 + c + e < DK) row[d0 + c + e] = x[e];
                 }
             }
         }
     }
-    if (!ok && leader) mma_commit(&done);
-    if (!ok && warp == 0) {     // no product or copy is in flight when the block ends
-        int never = 0;
-        wait(&done, 0, &never);
-        for (unsigned ph = 0; ph < 2; ++ph) {
-            wait(&s_full, ph, &never);
-            wait(&r_full, ph, &never);
-            wait(&g_full, ph, &never);
-            wait(&k_full, ph, &never);
-        }
-    }
-    fence_before();
-    __syncthreads();
-    if (warp == 0) {
-        fence_after();
-        tmem_free(tm, kTmem);
-    }
-    if (tid == 0 && given_up) *p.status = 6;        // RNN_ERR_TIMEOUT
 }
 
 template <typename T, int DKB>
@@ -1072,8 +997,7 @@ cudaError_t run(const DeltaGradParams& q, cudaStream_t st, int* launches)
     delta_grad_chain_kernel<T, DKB, KP><<<heads_grid((p.DV + 127) / 128, p.N * p.H), kChainThreads, chain_smem, st>>>(q);
     ++*launches;
     if (p.S > 0 && (q.dQ.data || q.dK.data || q.dg.data || q.dbeta.data)) {
-        const int64_t items = p.N * p.HK * delta_chunks(p.S);
-        delta_grad_rest_kernel<T, DKB, KP><<<(unsigned)(items < p.sms ? items : p.sms), kRestThreads, rest_smem, st>>>(q);
+        delta_grad_rest_kernel<T, DKB, KP><<<heads_grid(delta_chunks(p.S), p.N * p.HK), kRestThreads, rest_smem, st>>>(q);
         ++*launches;
     }
     return cudaGetLastError();
