@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
     __shared__ __align__(8) uint64_t first_full, g_full, k_full, x_done, x3_done, kq_done, k_done, done;
     __shared__ Sums sums;
     __shared__ float k_scale[C], q_scale[C];
-    __shared__ float fac[768], scales[8];
+    __shared__ __align__(16) float fac[768], scales[8];      // (copied 16 bytes at a time)
     __shared__ float rv[C], part[5][4][128], dots[kRestThreads / 32], slope[C], end[C], db[C];
     __shared__ float2 carry;
     __shared__ uint32_t slot;
