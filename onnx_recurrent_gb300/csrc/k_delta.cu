@@ -652,11 +652,13 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
     if (threadIdx.x == 0 && given_up) *p.status = 6;        // RNN_ERR_TIMEOUT
 }
 
-// The states before the segments, one after another: S <- F S + E.  A block has 32 columns of a head's state.
-constexpr int kJoined = 32;
+// The states before the segments, one after another: S <- F S + E.  A block has 16 columns of a head's state, a thread two
+// rows by four columns of it, and the next segment's F and E are on their way while this one's product runs: the launch is as
+// long as the segments' products in a row, each DK^2 x 16 multiplications a block, and what it reads lies in L2.
+constexpr int kJoined = 16;
 struct JoinSmem {
     float S[2][kDeltaMaxKey][kJoined];
-    float F[kDeltaMaxKey][kDeltaMaxKey + 1];
+    float F[kDeltaMaxKey][kDeltaMaxKey + 4];
 };
 __global__ void __launch_bounds__(kThreads) delta_join_kernel(const DeltaParams p)
 {
@@ -664,50 +666,71 @@ __global__ void __launch_bounds__(kThreads) delta_join_kernel(const DeltaParams 
     JoinSmem& s = *reinterpret_cast<JoinSmem*>(raw);
     const int64_t nh = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
     if (nh >= p.N * p.H) return;
-    const int tid = threadIdx.x, DK = p.DK, DV = p.DV, v0 = blockIdx.x * kJoined, c = tid % 8 * 4, r = tid / 8;
+    constexpr int kRows = kDeltaMaxKey / 2, kF = kDeltaMaxKey / (kThreads / 32);
+    static_assert(kThreads == kRows * kJoined / 4, "a thread for two rows by four columns");
+    const int tid = threadIdx.x, warp = tid / 32, DK = p.DK, DV = p.DV, v0 = blockIdx.x * kJoined, c = tid % 4 * 4, r = tid / 4;
+    const bool wide = DK % 4 == 0 && ((uintptr_t)p.over & 15) == 0;
     // (initial_state too: final_state may be the same memory)
     if (p.h0)
         for (int i = tid; i < DK * kJoined; i += kThreads) {
             const int d = i / kJoined, v = v0 + i % kJoined;
             if (v < DV) p.starts[(nh * p.cuts * DK + d) * (int64_t)DV + v] = p.h0[(nh * DK + d) * (int64_t)DV + v];
         }
-    for (int cut = 0; cut < p.cuts - 1; ++cut) {
+    float f[kF][4], acc[2][4], next[2][4] = {};
+    auto load = [&](int cut) {
         const float* E = p.over + (nh * (p.cuts - 1) + cut) * DK * (int64_t)(DV + DK);
-        const float* F = E + (int64_t)DK * DV;
-        if (cut)
-            for (int i = tid; i < DK * DK; i += kThreads) s.F[i / DK][i % DK] = F[i];
-        __syncthreads();
-        const float(*old)[kJoined] = s.S[(cut + 1) & 1];
-        float acc[4][4];
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
+        for (int a = 0; a < 2; ++a)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int d = r + 32 * a, v = v0 + c + e;
-                acc[a][e] = d < DK && v < DV ? E[(int64_t)d * DV + v] : 0.f;
+                const int d = r + kRows * a, v = v0 + c + e;
+                next[a][e] = d < DK && v < DV ? E[(int64_t)d * DV + v] : 0.f;
             }
+        // (the first segment has no F: its E begins with the initial state)
+        if (cut)
+            load_fours<kF>(E + (int64_t)DK * DV + (int64_t)warp * DK, (int64_t)(kThreads / 32) * DK, DK, wide,
+                           [&](int a) { return warp + kThreads / 32 * a < DK; }, f);
+    };
+    load(0);
+    for (int cut = 0; cut < p.cuts - 1; ++cut) {
+        if (cut)
+#pragma unroll
+            for (int a = 0; a < kF; ++a)
+                *reinterpret_cast<float4*>(&s.F[warp + kThreads / 32 * a][tid % 32 * 4]) = make_float4(f[a][0], f[a][1], f[a][2], f[a][3]);
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[a][e] = next[a][e];
+        __syncthreads();
+        if (cut + 1 < p.cuts - 1) load(cut + 1);
+        const float(*old)[kJoined] = s.S[(cut + 1) & 1];
         if (cut)
 #pragma unroll 4
-            for (int k = 0; k < DK; ++k) {
-                const float4 x = *reinterpret_cast<const float4*>(&old[k][c]);
+            for (int k = 0; k < DK; k += 4) {       // (past DK both are 0)
+                const float4 f0 = *reinterpret_cast<const float4*>(&s.F[r][k]), f1 = *reinterpret_cast<const float4*>(&s.F[r + kRows][k]);
+                const float fs[2][4] = {{f0.x, f0.y, f0.z, f0.w}, {f1.x, f1.y, f1.z, f1.w}};
 #pragma unroll
-                for (int a = 0; a < 4; ++a) {
-                    const float f = s.F[r + 32 * a][k];      // (rows past DK are not used)
-                    acc[a][0] = fmaf(f, x.x, acc[a][0]);
-                    acc[a][1] = fmaf(f, x.y, acc[a][1]);
-                    acc[a][2] = fmaf(f, x.z, acc[a][2]);
-                    acc[a][3] = fmaf(f, x.w, acc[a][3]);
+                for (int w = 0; w < 4; ++w) {
+                    const float4 x = *reinterpret_cast<const float4*>(&old[k + w][c]);
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) {
+                        acc[a][0] = fmaf(fs[a][w], x.x, acc[a][0]);
+                        acc[a][1] = fmaf(fs[a][w], x.y, acc[a][1]);
+                        acc[a][2] = fmaf(fs[a][w], x.z, acc[a][2]);
+                        acc[a][3] = fmaf(fs[a][w], x.w, acc[a][3]);
+                    }
                 }
             }
         float* out = p.starts + (nh * p.cuts + cut + 1) * DK * (int64_t)DV;
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
+        for (int a = 0; a < 2; ++a) {
+            const int d = r + kRows * a;
+            *reinterpret_cast<float4*>(&s.S[cut & 1][d][c]) = d < DK ? make_float4(acc[a][0], acc[a][1], acc[a][2], acc[a][3])
+                                                                     : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int d = r + 32 * a, v = v0 + c + e;
-                s.S[cut & 1][d][c + e] = acc[a][e];
-                if (d < DK && v < DV) out[(int64_t)d * DV + v] = acc[a][e];
-            }
+            for (int e = 0; e < 4; ++e)
+                if (d < DK && v0 + c + e < DV) out[(int64_t)d * DV + v0 + c + e] = acc[a][e];
+        }
         __syncthreads();
     }
 }
