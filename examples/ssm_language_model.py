@@ -1,14 +1,17 @@
 """A small recurrent language model on the state space operators.
 
-    python examples/ssm_language_model.py [--steps 60] [--tokens 48] [--io bf16]
+    python examples/ssm_language_model.py [--steps 60] [--tokens 48] [--io bf16] [--layers scan,scan] [--beams 0]
 
-Two layers of projection -> causal convolution -> selective scan -> projection
-learn the sentences of a small grammar (bracketed words whose brackets close
-in order).  Training takes whole sentences (convolution, scan and scores with
-their gradients, an entropy bonus in the loss); generation reads a prompt with
-the same operators and then continues it a token at a time from the layers'
-states, printing each token's log probability and the alternatives that the
-model saw.  The matrix products are torch's.
+Two layers of normalisation -> projection -> causal convolution -> selective
+scan -> projection (with --layers delta: the gated delta rule in the scan's and
+the convolution's place) learn the sentences of a small grammar (bracketed words
+whose brackets close in order).  Training takes whole sentences (the operators
+and the scores with their gradients, an entropy bonus in the loss); generation
+reads a prompt with the same operators and then continues it a token at a time
+from the layers' states, printing each token's log probability and the
+alternatives that the model saw; with --beams it also searches for likely
+continuations, the layers' states following the beams.  The matrix products are
+torch's.
 """
 import argparse
 import os
@@ -42,13 +45,26 @@ def sentence(rng, length):
     return out
 
 
+class Norm(torch.nn.Module):
+    """Layer normalisation of rows in the model's own type (fp32)."""
+
+    def __init__(self, width):
+        super().__init__()
+        self.plan = orc.rnn_norm_create(width)
+        self.weight = torch.nn.Parameter(torch.ones(width))
+        self.bias = torch.nn.Parameter(torch.zeros(width))
+
+    def forward(self, h):
+        return autograd.layer_norm(self.plan, h, self.weight, self.bias)
+
+
 class Layer(torch.nn.Module):
     def __init__(self, width, inner, state, io):
         super().__init__()
         self.plan = orc.rnn_ssm_create(inner, state_size=state, groups=1, conv_width=4, layout=1)
         orc.rnn_ssm_set_io_type(self.plan, io)
         self.inner, self.state = inner, state
-        self.norm = torch.nn.LayerNorm(width)
+        self.norm = Norm(width)
         self.into = torch.nn.Linear(width, 2 * inner, bias=False)
         self.to_bc = torch.nn.Linear(inner, 2 * state, bias=False)
         self.to_dt = torch.nn.Linear(inner, inner, bias=False)
@@ -86,12 +102,50 @@ class Layer(torch.nn.Module):
         return h + self.out(y.to(h.dtype))
 
 
+class DeltaLayer(torch.nn.Module):
+    """Heads of 32 values, two to a query and key head of 16."""
+
+    def __init__(self, width, inner, io):
+        super().__init__()
+        self.heads, self.key_heads, self.key, self.value = inner // 32, max(inner // 64, 1), 16, 32
+        self.plan = orc.rnn_delta_create(self.heads, self.key, self.value, self.key_heads, layout=1)
+        orc.rnn_delta_set_io_type(self.plan, io)
+        self.norm = Norm(width)
+        self.sizes = (self.key_heads * self.key, self.key_heads * self.key, self.heads * self.value)
+        self.into = torch.nn.Linear(width, sum(self.sizes), bias=False)
+        self.to_gates = torch.nn.Linear(width, 2 * self.heads)
+        self.out = torch.nn.Linear(self.heads * self.value, width, bias=False)
+
+    def project(self, h):
+        """Q, K, V, g and beta of inputs [..., width]."""
+        h, dtype = self.norm(h), self.plan.dtype
+        q, k, v = self.into(h).split(self.sizes, -1)
+        q, k = (torch.nn.functional.normalize(t.unflatten(-1, (self.key_heads, self.key)), dim=-1) for t in (q, k))
+        a, b = self.to_gates(h).split(self.heads, -1)
+        return (q.to(dtype), k.to(dtype), v.unflatten(-1, (self.heads, self.value)).to(dtype),
+                torch.nn.functional.logsigmoid(a + 3), torch.sigmoid(b))
+
+    def forward(self, h, states=None):
+        q, k, v, g, beta = self.project(h)
+        y, state = autograd.delta_rule(self.plan, q, k, v, g.contiguous(), beta, None, *(states or ()))
+        return h + self.out(y.flatten(-2).to(h.dtype)), (state,)
+
+    def step(self, h, states):
+        q, k, v, g, beta = self.project(h)
+        y = torch.empty_like(v, memory_format=torch.contiguous_format)
+        orc.rnn_delta_step(self.plan, q, k, v, g, beta, states[0], y)
+        return h + self.out(y.flatten(-2).to(h.dtype))
+
+
 class Model(torch.nn.Module):
     def __init__(self, width=64, inner=128, state=16, layers=2, io="bf16"):
+        """layers: their number, or their kinds ("scan" or "delta")."""
         super().__init__()
+        kinds = ["scan"] * layers if isinstance(layers, int) else layers
         self.embed = torch.nn.Embedding(len(WORDS), width)
-        self.layers = torch.nn.ModuleList(Layer(width, inner, state, io) for _ in range(layers))
-        self.norm = torch.nn.LayerNorm(width)
+        self.layers = torch.nn.ModuleList(DeltaLayer(width, inner, io) if kind == "delta" else Layer(width, inner, state, io)
+                                          for kind in kinds)
+        self.norm = Norm(width)
         self.head = torch.nn.Linear(width, len(WORDS), bias=False)
 
     def forward(self, ids):
@@ -140,20 +194,47 @@ def generate(model, prompt, tokens):
     return ids, logps, others
 
 
+@torch.no_grad()
+def search(model, prompt, tokens, beams):
+    """Likely continuations of the prompt, best first: (ids [beams, tokens], scores [beams])."""
+    plan = orc.rnn_beam_create(beams, end_id=WORDS.index("."))
+    logits, states = model(torch.tensor([prompt], device="cuda"))
+    # every beam starts from the prompt's states, and the first alone has a score
+    states = [tuple(t.expand(beams, *t.shape[1:]).contiguous() for t in s) for s in states]
+    scores = torch.full((1, beams), -torch.inf, device="cuda")
+    scores[0, 0] = 0
+    logits, finished = logits[:, -1].contiguous(), None
+    ids = torch.zeros((beams, tokens), dtype=torch.int32, device="cuda")
+    for t in range(tokens):
+        r = orc.beam_select(plan, logits, scores, finished)
+        orc.rnn_beam_reorder(plan, r.parents, [ids, *(x for s in states for x in s)])
+        ids[:, t] = r.ids[0]
+        scores, finished = r.scores, r.finished
+        if t + 1 < tokens:
+            logits = model.step(r.ids[0].long(), states)
+    orc.rnn_beam_sync(plan)
+    return ids, scores[0]
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--steps", type=int, default=60)
     ap.add_argument("--tokens", type=int, default=48)
     ap.add_argument("--io", choices=sorted(DTYPES), default="bf16")
+    ap.add_argument("--layers", default="scan,scan", help="the layers' kinds: scan or delta, with commas between")
+    ap.add_argument("--beams", type=int, default=0)
     a = ap.parse_args()
     torch.manual_seed(0)
-    model = Model(io=a.io).cuda()
+    model = Model(layers=a.layers.split(","), io=a.io).cuda()
     losses = train(model, a.steps)
     print(f"loss {losses[0]:.3f} -> {losses[-1]:.3f} in {a.steps} steps")
     ids, logps, others = generate(model, [0, 1, 3], a.tokens)
     print(" ".join(WORDS[i] for i in ids))
     for i, lp, alt in list(zip(ids[3:], logps, others))[:8]:
         print(f"  {WORDS[i]:4} log p {lp:6.2f}   else {alt}")
+    if a.beams:
+        for ids, score in zip(*search(model, [0, 1, 3], 12, a.beams)):
+            print(f"  {float(score):7.2f}  " + " ".join(WORDS[i] for i in ids.tolist()))
 
 
 if __name__ == "__main__":

@@ -1,16 +1,19 @@
-"""The state space operators and token scores as differentiable functions.
+"""The state space operators, the gated delta rule, layer normalisation and token
+scores as differentiable functions.
 
-Thin torch.autograd wrappers of ``ssm``: each forward and each gradient is one
+Thin torch.autograd wrappers of ``ssm``, ``delta`` and ``norm``: each forward and each gradient is one
 entry point of the CUDA library.  Gradients are those of one backward pass:
 differentiating them again raises an error.  Only the gradients that are asked
-for are formed, and a scan that needs none saves nothing for them.
+for are formed, and a scan or a delta rule that needs none saves nothing for
+them.  A backward pass that is to be captured needs leaves that no graph built
+outside the capture still holds.
 """
 from __future__ import annotations
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import ssm
+from . import delta, norm, ssm
 
 
 def _dense(slope):
@@ -87,6 +90,44 @@ class _Scores(torch.autograd.Function):
         return dlogits, None, None
 
 
+class _Delta(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, plan, Q, K, V, g, beta, sequence_lens, initial_state):
+        ctx.set_materialize_grads(False)
+        args = (Q, K, V, g, beta, sequence_lens, initial_state)
+        Y, state, saved = delta.delta_rule(plan, *args, save=True)
+        ctx.plan = plan
+        ctx.save_for_backward(saved, *args)
+        return Y, state
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dY, d_state):
+        saved, *args = ctx.saved_tensors
+        dY = torch.zeros_like(args[2], memory_format=torch.contiguous_format) if dY is None else dY.contiguous()
+        names = ("dQ", "dK", "dV", "dg", "dbeta", None, "d_initial_state")
+        g = _wanted(ctx, zip(names, args))
+        delta.rnn_delta_rule_grad(ctx.plan, dY, saved, *args[:6], _dense(d_state), **g)
+        return (None, *(g.get(name) for name in names))
+
+
+class _Norm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, plan, X, W, bias):
+        Y, stats = norm.layer_norm(plan, X, W, bias)
+        ctx.plan = plan
+        ctx.save_for_backward(X, stats, W, bias)
+        return Y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dY):
+        X, stats, W, bias = ctx.saved_tensors
+        g = _wanted(ctx, (("dX", X), ("dW", W), ("dbias", bias)))
+        norm.rnn_layer_norm_grad(ctx.plan, dY.contiguous(), X, stats, W, **g)
+        return None, g.get("dX"), g.get("dW"), g.get("dbias")
+
+
 def conv(plan, X, W, bias=None, sequence_lens=None, initial_state=None):
     """(Y, final_state) of the causal convolution, as ``ssm_conv``."""
     return _Conv.apply(plan, X, W, bias, sequence_lens, initial_state)
@@ -98,6 +139,19 @@ def scan(plan, X, dt, A, B, C, D=None, Z=None, dt_bias=None, sequence_lens=None,
     if not torch.is_grad_enabled() or not any(t is not None and t.requires_grad for t in args):
         return ssm.ssm_scan(plan, *args)[:2]
     return _Scan.apply(plan, *args)
+
+
+def delta_rule(plan, Q, K, V, g, beta, sequence_lens=None, initial_state=None):
+    """(Y, final_state) of the gated delta rule, as ``delta.delta_rule``."""
+    args = (Q, K, V, g, beta, sequence_lens, initial_state)
+    if not torch.is_grad_enabled() or not any(t is not None and t.requires_grad for t in args):
+        return delta.delta_rule(plan, *args)[:2]
+    return _Delta.apply(plan, *args)
+
+
+def layer_norm(plan, X, W=None, bias=None):
+    """Y of the layer normalisation, as ``norm.layer_norm``."""
+    return _Norm.apply(plan, X, W, bias)
 
 
 def scores(logits, ids=None, top=0):
