@@ -330,47 +330,47 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_run_kernel(const Delta
                 fence_after();
                 const unsigned kimg = sbase + s * Sm::stage, qimg = kimg + kBlock;
                 const unsigned timg = kimg + Im::keys, pimg = timg + 2 * kBlock;
-                // parts of S (from the first on, `count` of them) and part b of K or Q, over the keys
-                auto keys_product = [&](uint32_t d, unsigned img, int first, int count, int b, bool add) {
+                // parts of S (from the last down, `count` of them) and part b of K or Q, over the keys
+                auto keys_product = [&](uint32_t d, unsigned img, int last, int count, int b, bool add) {
 #pragma unroll 1
-                    for (int a = first; a < first + count; ++a)
+                    for (int a = last; a > last - count; --a)
 #pragma unroll
                         for (int ks = 0; ks < DKB * 4; ++ks)
                             if (leader)
                                 mma_ts(tm + d, tm + Co::S + a * SR + ks * 8, desc_rows(img + (b * DKB + ks / 4) * 2 * kBlock + ks % 4 * 32), instr(C, false),
-                                       add || a > first || ks > 0);
+                                       add || a < last || ks > 0);
                 };
-                // R or U and a matrix, over the steps: hi hi, lo hi, hi lo
+                // R or U and a matrix, over the steps: hi lo, lo hi, hi hi
                 auto steps_product = [&](uint32_t d, uint32_t from, unsigned img) {
 #pragma unroll 1
-                    for (int q = 0; q < 3; ++q)
+                    for (int q = 2; q >= 0; --q)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
                             if (leader)
                                 mma_ts(tm + d, tm + from + ks / 2 * 32 + (q == 1) * 16 + ks % 2 * 8, desc_rows(img + (q == 2) * kBlock + ks * 32), instr(C, false),
-                                       q > 0 || ks > 0);
+                                       q < 2 || ks > 0);
                 };
-                keys_product(Co::R, kimg, 0, 2, 0, false);
-                if (KP == 2) keys_product(Co::R, kimg, 0, 1, 1, true);
+                if (KP == 2) keys_product(Co::R, kimg, 0, 1, 1, false);
+                keys_product(Co::R, kimg, 1, 2, 0, KP == 2);
                 if (leader) mma_commit(&d_ready);
-                if (!SEARCH) keys_product(Co::QS, qimg, 0, 1, 0, false);
+                if (!SEARCH) keys_product(Co::QS, qimg, 1, 1, 0, false);
                 if (!__all_sync(0xffffffffu, wait(&r_ready, ph, &given_up))) break;
                 fence_after();
                 steps_product(Co::U, Co::R, timg);
                 if (leader) mma_commit(&u_ready);
                 if (!SEARCH) {
-                    keys_product(Co::QS, qimg, 1, 1, 0, true);
                     if (KP == 2) keys_product(Co::QS, qimg, 0, 1, 1, true);
+                    keys_product(Co::QS, qimg, 0, 1, 0, true);
                 }
                 if (!__all_sync(0xffffffffu, wait(&up_ready, ph, &given_up))) break;
                 fence_after();
 #pragma unroll 1
-                for (int q = 0; q < 1 + KP; ++q)        // hi hi, lo hi, hi lo
+                for (int q = KP; q >= 0; --q)        // hi lo, lo hi, hi hi
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         if (leader)
                             mma_ts(tm + Co::dS, tm + Co::U2 + ks / 2 * 32 + (q == 1) * 16 + ks % 2 * 8,
-                                   desc_columns(kimg + (q == 2) * DKB * 2 * kBlock + ks * 2048, 2 * kBlock), instr(DKB * 64, true), q > 0 || ks > 0);
+                                   desc_columns(kimg + (q == 2) * DKB * 2 * kBlock + ks * 2048, 2 * kBlock), instr(DKB * 64, true), q < KP || ks > 0);
                 if (leader) mma_commit(&ds_ready);
                 if (!SEARCH) steps_product(Co::PU, Co::U, pimg);
                 if (leader) {

@@ -112,36 +112,36 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_grad_chain_kernel(cons
                 fence_after();
                 const unsigned kimg = sbase + s * Sm::stage, qimg = kimg + kBlock;
                 const unsigned timg = kimg + Im::keys, pimg = timg + 2 * kBlock;
-                // the operand at `from` and a matrix transposed, over the steps: hi hi, lo hi, hi lo
+                // the operand at `from` and a matrix transposed, over the steps: hi lo, lo hi, hi hi
                 auto steps_product = [&](uint32_t d, uint32_t from, unsigned img) {
 #pragma unroll 1
-                    for (int r = 0; r < 3; ++r)
+                    for (int r = 2; r >= 0; --r)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
                             if (leader)
                                 mma_ts(tm + d, tm + from + ks / 2 * 32 + (r == 1) * 16 + ks % 2 * 8, desc_columns(img + (r == 2) * kBlock + ks * 2048, kBlock),
-                                       instr(C, true), r > 0 || ks > 0);
+                                       instr(C, true), r < 2 || ks > 0);
                 };
                 // the same with K or Q, into G's increment
                 auto state_product = [&](uint32_t from, unsigned img) {
 #pragma unroll 1
-                    for (int r = 0; r < 1 + KP; ++r)
+                    for (int r = KP; r >= 0; --r)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
                             if (leader)
                                 mma_ts(tm + Co::dG, tm + from + ks / 2 * 32 + (r == 1) * 16 + ks % 2 * 8,
-                                       desc_columns(img + (r == 2) * DKB * 2 * kBlock + ks * 2048, 2 * kBlock), instr(DKB * 64, true), r > 0 || ks > 0);
+                                       desc_columns(img + (r == 2) * DKB * 2 * kBlock + ks * 2048, 2 * kBlock), instr(DKB * 64, true), r < KP || ks > 0);
                 };
                 steps_product(Co::PY, Co::X, pimg);
                 if (!__all_sync(0xffffffffu, wait(&g_ready, ph, &given_up))) break;
                 fence_after();
 #pragma unroll 1
-                for (int r = 0; r < 1 + KP; ++r)
+                for (int r = KP; r >= 0; --r)
 #pragma unroll
                     for (int ks = 0; ks < DKB * 4; ++ks)
                         if (leader)
                             mma_ts(tm + Co::U, tm + Co::G + (r == 1) * SR + ks * 8, desc_rows(kimg + ((r == 2) * DKB + ks / 4) * 2 * kBlock + ks % 4 * 32),
-                                   instr(C, false), r > 0 || ks > 0);
+                                   instr(C, false), r < KP || ks > 0);
                 if (leader) mma_commit(&d_ready);
                 if (!__all_sync(0xffffffffu, wait(&u_told, ph, &given_up))) break;
                 fence_after();
@@ -467,9 +467,11 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_grad_chain_kernel(cons
 // again, [EA + EA^T; EP] K and [EP^T; not used] Q.  More values than 128 are taken one tile after the other: everything
 // below is linear in the five first products.
 //
-// With D_ij as above, sum_j D_ij = k_i.(EA K)_i + q_i.(EP K)_i and sum_j D_ji = k_i.(EA^T K + EP^T Q)_i, so the slope in G_i is
-//     q_i.dQ_i - k_i.dK_i + 2 (sum_j EA_ij K_i.K_j - b_i e^G_i k_i.X2_i)
-// and no sum runs down a column.
+// What decays between two steps i > j, D_ij = EA_ij K_i.K_j + EP_ij Q_i.K_j, has g_t in it for j < t <= i, so that
+//     dg_t = sum_{i >= t > j} D_ij + sum_{i >= t} e^G_i (q_i.X1_i - b_i k_i.X2_i) + sum_{j < t} e^(G_last - G_j) k_j.X3_j + e^G_last <dS1, S0>.
+// (Sums of the slopes in G_i over i >= t are the same, but hold each D_ij of two later steps twice, with either sign:
+// where decays are strong the little that is left had lost three bits.)  The first sum comes from sums along the rows, in
+// a thread's 16 columns and those before, added down the rows i >= t.
 //
 // Bytes bound it, 240 KB a chunk and head of 128 x 128 at 16 bits, copied as they are.
 constexpr int kRestThreads = 512;
@@ -498,7 +500,7 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
     __shared__ Sums sums;
     __shared__ float k_scale[C], q_scale[C];
     __shared__ __align__(16) float fac[768], scales[8];      // (copied 16 bytes at a time)
-    __shared__ float rv[C], part[5][4][128], dots[kRestThreads / 32], slope[C], end[C], db[C];
+    __shared__ float rv[C], part[5][4][128], dots[kRestThreads / 32], scans[5][C], slope[C], db[C];
     __shared__ float2 carry;
     __shared__ uint32_t slot;
     __shared__ int given_up;
@@ -551,7 +553,6 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
         constexpr unsigned kStates = 2 * DKB * kSheetImage;
         // all threads wait, and know whether all did
         unsigned phase = 0;
-        float dot_all = 0.f;        // warp 0's
         auto await = [&](uint64_t* b) {
             fence_before();
             const bool ok = __syncthreads_and(wait(b, phase, &given_up));
@@ -623,30 +624,30 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
             const unsigned kimg = sbase + Sm::keys, qimg = kimg + kBlock;
             auto key_products = [&] {
 #pragma unroll 1
-                for (int r = 0; r < 2 * KP - 1; ++r)         // hi hi, lo hi, hi lo
+                for (int r = 2 * KP - 2; r >= 0; --r)         // hi lo, lo hi, hi hi
 #pragma unroll
                     for (int ks = 0; ks < DKB * 4; ++ks)
                         if (leader)
                             mma_ss(tm + cKQ, desc_rows(kimg + ((r == 1) * DKB + ks / 4) * 2 * kBlock + ks % 4 * 32),
-                                   desc_rows(kimg + ((r == 2) * DKB + ks / 4) * 2 * kBlock + ks % 4 * 32), instr(C, false), r > 0 || ks > 0);
+                                   desc_rows(kimg + ((r == 2) * DKB + ks / 4) * 2 * kBlock + ks % 4 * 32), instr(C, false), r < 2 * KP - 2 || ks > 0);
                 if (leader) mma_commit(&kq_done);
             };
             if (warp == 0) {
 #pragma unroll 1
-                for (int r = 0; r < 3; ++r)     // [dR; dY'] U^T: hi hi, lo hi, hi lo
+                for (int r = 2; r >= 0; --r)     // [dR; dY'] U^T: hi lo, lo hi, hi hi
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
                         if (leader)
                             mma_ss(tm + cE, desc_kept(sbase + Sm::r + (r == 1) * 2 * kSheetImage, ks), desc_kept(sbase + Sm::u + (r == 2) * kSheetImage, ks),
-                                   instr(C, true) | 1u << 15, r > 0 || ks > 0);
+                                   instr(C, true) | 1u << 15, r < 2 || ks > 0);
                 if (Sm::early) key_products();
 #pragma unroll 1
-                for (int r = 0; r < 3; ++r)     // [dR; dY'] S0^T
+                for (int r = 2; r >= 0; --r)     // [dR; dY'] S0^T
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
                         if (leader)
                             mma_ss(tm + cX, desc_kept(sbase + Sm::r + (r == 1) * 2 * kSheetImage, ks),
-                                   desc_kept(sbase + Sm::states + (r == 2) * DKB * kSheetImage, ks), instr(DKB * 64, true) | 1u << 15, r > 0 || ks > 0);
+                                   desc_kept(sbase + Sm::states + (r == 2) * DKB * kSheetImage, ks), instr(DKB * 64, true) | 1u << 15, r < 2 || ks > 0);
                 if (leader) mma_commit(&x_done);
             }
             {   // dR . V
@@ -685,9 +686,23 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                     s = fmaf(d, k, s);
                     e[c] = v;
                     row = fmaf(v, k, row);
+                    kq[c] = j < i ? row : 0.f;      // of D_i., up to column j, where step j + 1 is not past i
                 }
                 part[0][quarter][lane_row] = row;
                 part[1][quarter][lane_row] = s;
+                // added over the warp's rows: each round halves the columns that a lane has
+#pragma unroll
+                for (int o = 16, left = 8; o > 1; o /= 2, left /= 2) {
+                    const bool high = lane & o;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        if (c < left) {
+                            const float keep = high ? kq[c + left] : kq[c], give = high ? kq[c] : kq[c + left];
+                            kq[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                        }
+                }
+                kq[0] += __shfl_xor_sync(0xffffffffu, kq[0], 1);
+                if (lane % 2 == 0) part[4][warp % 4][quarter * 16 + lane / 2] = kq[0];
             };
             auto put_e = [&] {
 #pragma unroll
@@ -721,13 +736,13 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
             if (!ok) break;
             if (warp == 0) {
 #pragma unroll 1
-                for (int r = 0; r < 3; ++r)     // U dS1^T
+                for (int r = 2; r >= 0; --r)     // U dS1^T
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
                         if (leader)
                             mma_ss(tm + cX3, desc_kept(sbase + Sm::u + (r == 1) * kSheetImage, ks),
                                    desc_kept(sbase + Sm::states + (r == 2) * DKB * kSheetImage, ks), instr(DKB * 64, true) | 1u << 15,
-                                   r > 0 || ks > 0);
+                                   r < 2 || ks > 0);
                 if (leader) mma_commit(&x3_done);
             }
             {   // <dS1, S0>
@@ -801,19 +816,19 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
             __syncthreads();
             if (warp == 0) {
 #pragma unroll 1
-                for (int r = 0; r < 1 + KP; ++r)    // hi hi, lo hi, hi lo
+                for (int r = KP; r >= 0; --r)    // hi lo, lo hi, hi hi
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         if (leader)
                             mma_ss(tm + cK, desc_rows(sbase + Sm::a1 + (r == 1) * kSheetImage + ks * 32),
-                                   desc_columns(kimg + (r == 2) * DKB * 2 * kBlock + ks * 2048, 2 * kBlock), instr(DKB * 64, true), r > 0 || ks > 0);
+                                   desc_columns(kimg + (r == 2) * DKB * 2 * kBlock + ks * 2048, 2 * kBlock), instr(DKB * 64, true), r < KP || ks > 0);
 #pragma unroll 1
-                for (int r = 0; r < 1 + KP; ++r)
+                for (int r = KP; r >= 0; --r)
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         if (leader)
                             mma_ss(tm + cKE, desc_rows(sbase + Sm::a2 + (r == 1) * kBlock + ks * 32),
-                                   desc_columns(qimg + (r == 2) * DKB * 2 * kBlock + ks * 2048, 2 * kBlock), instr(DKB * 64, true), r > 0 || ks > 0);
+                                   desc_columns(qimg + (r == 2) * DKB * 2 * kBlock + ks * 2048, 2 * kBlock), instr(DKB * 64, true), r < KP || ks > 0);
                 if (leader) mma_commit(&k_done);
             }
             // in the meantime what the states give, and its sums with K and Q
@@ -835,7 +850,6 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                     }
                 }
             };
-            float own = 0.f;            // this quarter's part of k_i.dK_i or q_i.dQ_i
             {
                 const float first = sums.power(i), last = sums.power(C - 1, i);
                 const float fx = (upper ? -b_i * r_up : y_up) * s_up * first, f3 = upper ? last * (u_up * g_up) : 0.f;
@@ -860,85 +874,90 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                         }
                     }
                 }
-                own = fx * s1 + f3 * s3;
-                part[2][quarter][lane_row] = es * (r_up * s_up * first) * s1;       // e^G k.X2 (of the upper half)
+                part[2][quarter][lane_row] = es * ((upper ? r_up : y_up) * s_up * first) * s1;      // e^G k.X2 and e^G q.X1
                 part[3][quarter][lane_row] = es * f3 * s3;      // e^(G_last - G) k.X3
             }
             ok = await(&k_done);
             if (!ok) break;
             {
                 const float mine = upper ? k_scale[i] : q_scale[i];
-                float s = 0.f;
 #pragma unroll
                 for (int b = 0; b < DKB; ++b) {
                     const int c0 = quarter * DKB * 16 + b * 16;
-                    float x[16], k[16];
-                    key_values(c0, k);
+                    float x[16];
                     tmem_ld16(my + cK + c0, x);
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        s = fmaf(k[c], x[c], s);
-                        acc[b][c] = fmaf(mine, x[c], acc[b][c]);
-                    }
+                    for (int c = 0; c < 16; ++c) acc[b][c] = fmaf(mine, x[c], acc[b][c]);
                     if (upper) {
                         tmem_ld16(my + cKE + c0, x);
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            s = fmaf(k[c], x[c], s);
-                            acc[b][c] = fmaf(mine, x[c], acc[b][c]);
-                        }
+                        for (int c = 0; c < 16; ++c) acc[b][c] = fmaf(mine, x[c], acc[b][c]);
                     }
                 }
-                part[4][quarter][lane_row] = es * (own + mine * s);
             }
             fence_before();
             __syncthreads();
             fence_after();
-            // the decays' slopes, and their sums from each step to the chunk's end
-            if (tid < C) {
-                float ea = 0.f, s = 0.f, kx2 = 0.f, kx3 = 0.f, qdq = 0.f, kdk = 0.f;
+            // a warp's sum over the steps: of each quarter's D from a step on, of what the states before give from a step
+            // on, and of what goes into the state after before a step
+            if (warp < 5) {
+                float x[2];
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    ea += part[0][w][tid];
-                    s += part[1][w][tid];
-                    kx2 += part[2][w][tid];
-                    kx3 += part[3][w][tid];
-                    kdk += part[4][w][tid];
-                    qdq += part[4][w][C + tid];
-                }
-                slope[tid] = (tile ? slope[tid] : 0.f) + (qdq - kdk) + 2.f * (ea - fac[kBeta + tid] * kx2);
-                end[tid] = (tile ? end[tid] : 0.f) + kx3;
-                db[tid] = (tile ? db[tid] : 0.f) + s + rv[tid] * r_up - kx2;
-            }
-            __syncthreads();
-            if (tid < 32) {
-                float all = end[tid] + end[tid + 32], d = tid < kRestThreads / 32 ? dots[tid] : 0.f;
-                for (int o = 16; o; o /= 2) {
-                    all += __shfl_xor_sync(0xffffffffu, all, o);
-                    d += __shfl_xor_sync(0xffffffffu, d, o);
-                }
-                dot_all = (tile ? dot_all : 0.f) + d;
-                if (tile == tiles - 1) {
-                    float hi = slope[tid + 32], lo = slope[tid];
-                    if (tid == 31) hi += all + fac[kWhole] * dot_all;
-                    for (int o = 1; o < 32; o *= 2) {
-                        const float a = __shfl_down_sync(0xffffffffu, hi, o), b = __shfl_down_sync(0xffffffffu, lo, o);
-                        if (tid + o < 32) {
-                            hi += a;
-                            lo += b;
-                        }
+                for (int w = 0; w < 2; ++w) {
+                    const int t = lane + 32 * w;
+                    float a = 0.f, b = 0.f;
+                    if (warp < 4) {
+                        if (warp < 3) a = part[0][warp][t], b = part[0][warp][C + t];
+                        else
+                            for (int o = 0; o < 4; ++o) a -= part[2][o][t], b += part[2][o][C + t];
+                        x[w] = warp < 3 ? a + b : fmaf(fac[kBeta + t], a, b);
+                    } else {
+                        for (int o = 0; o < 4; ++o) a += part[3][o][t];
+                        x[w] = a;
                     }
-                    lo += __shfl_sync(0xffffffffu, hi, 0);
-                    float* dg = static_cast<float*>(q.dg.data) + n * q.dg.bs + h;
-                    float* dbeta = static_cast<float*>(q.dbeta.data) + n * q.dbeta.bs + h;
+                }
+                const bool back = warp < 4;
+#pragma unroll
+                for (int o = 1; o < 32; o *= 2)
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
-                        const int t = tid + 32 * w;
-                        if (t >= steps) continue;
-                        const bool step = t0 + t < len;
-                        if (q.dg.data) dg[(t0 + t) * q.dg.ss] = step ? (w ? hi : lo) : 0.f;
-                        if (q.dbeta.data) dbeta[(t0 + t) * q.dbeta.ss] = step ? db[t] : 0.f;
+                        const float a = back ? __shfl_down_sync(0xffffffffu, x[w], o) : __shfl_up_sync(0xffffffffu, x[w], o);
+                        if (back ? lane + o < 32 : lane >= o) x[w] += a;
                     }
+                if (back) {
+                    x[0] += __shfl_sync(0xffffffffu, x[1], 0);
+                    scans[warp][lane] = x[0];
+                    scans[warp][lane + 32] = x[1];
+                } else {
+                    const float all = __shfl_sync(0xffffffffu, x[0], 31);
+                    const float a = __shfl_up_sync(0xffffffffu, x[0], 1), b = __shfl_up_sync(0xffffffffu, x[1], 1);
+                    scans[4][lane] = lane ? a : 0.f;
+                    scans[4][lane + 32] = all + (lane ? b : 0.f);
+                }
+            } else if (warp < 7) {
+                const int t = tid - 5 * 32;
+                float s = 0.f, kx2 = 0.f;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) s += part[1][w][t], kx2 += part[2][w][t];
+                db[t] = (tile ? db[t] : 0.f) + s + rv[t] * r_up - kx2;
+            } else if (warp == 7) {
+                float d = lane < kRestThreads / 32 ? dots[lane] : 0.f;
+                for (int o = 16; o; o /= 2) d += __shfl_xor_sync(0xffffffffu, d, o);
+                if (lane == 0) carry.x = fac[kWhole] * d;
+            }
+            __syncthreads();
+            if (tid < C) {
+                float x = carry.x + scans[4][tid] + scans[3][tid];
+                if (tid)
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) x += part[4][w][tid - 1] + (w < (tid - 1) / 16 ? scans[w][tid] : 0.f);
+                if (tile) x += slope[tid];
+                slope[tid] = x;
+                if (tile == tiles - 1 && tid < steps) {
+                    const bool step = t0 + tid < len;
+                    const int64_t t = t0 + tid;
+                    if (q.dg.data) static_cast<float*>(q.dg.data)[n * q.dg.bs + t * q.dg.ss + h] = step ? x : 0.f;
+                    if (q.dbeta.data) static_cast<float*>(q.dbeta.data)[n * q.dbeta.bs + t * q.dbeta.ss + h] = step ? db[tid] : 0.f;
                 }
             }
             phase ^= 1u;
