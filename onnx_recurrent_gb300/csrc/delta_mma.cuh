@@ -409,19 +409,16 @@ constexpr unsigned kPiece = 128 * 16;
 template <int N>
 __device__ __forceinline__ void keep_parts(unsigned char* image, unsigned second, int r, int piece, const f2* v, float down)
 {
-    const f2 d = dup2(down), m = dup2(6144.f), mm = dup2(-6144.f), minus = dup2(-1.f);
+    const f2 d = dup2(down);
     unsigned char* at = image + piece * kPiece + r * 16;
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
         unsigned hi[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const f2 a = add2(fma2(v[4 * i + e], d, m), mm);
             float x, y;
-            unpack2(a, x, y);
-            hi[e] = half_pair(x, y);
-            unpack2(fma2(v[4 * i + e], d, mul2(a, minus)), x, y);
-            lo[e] = half_pair(x, y);
+            unpack2(mul2(v[4 * i + e], d), x, y);
+            split_pair(x, y, hi[e], lo[e]);
         }
         *reinterpret_cast<uint4*>(at + i * kPiece) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(at + i * kPiece + second) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
