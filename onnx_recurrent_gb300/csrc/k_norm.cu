@@ -82,7 +82,7 @@ __device__ __forceinline__ void piece_weights(float (&w)[VEC], const float* from
 }
 
 template <typename S>
-__global__ void __launch_bounds__(S::threads) norm_kernel(const NormParams p)
+__global__ void __launch_bounds__(S::threads, S::NV == 32 && S::VEC > 1 && S::threads == 256 ? 4 : 1) norm_kernel(const NormParams p)
 {
     using T = typename S::T;
     using P = Piece<T, S::VEC>;
