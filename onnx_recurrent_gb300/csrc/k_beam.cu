@@ -350,7 +350,9 @@ __global__ void __launch_bounds__(kItemThreads) beam_select_kernel(const BeamSel
 constexpr int kThreads = 128;
 
 // A thread has one unit of a row's bytes of all B rows of an item: it has read them all before it
-// writes, so a tensor may be reordered in place.
+// writes, so a tensor may be reordered in place.  Eight rows' loads are in flight together; more rows wait in shared memory.
+// (A row that is to become itself is left.)
+constexpr int kAtOnce = 8;
 template <typename U>
 __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const ReorderParams p)
 {
@@ -375,15 +377,29 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const ReorderPar
         } else if (!good) {
             *p.status = 2;
         }
-        from[threadIdx.x] = good ? from_ : -1;
+        from[threadIdx.x] = good && !(t.in == t.out && from_ == to_) ? from_ : -1;
         to[threadIdx.x] = to_;
     }
     __syncthreads();
     for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < units; u += (int64_t)gridDim.x * kThreads) {
-        for (int b = 0; b < B; ++b)
-            if (from[b] >= 0) held[b * kThreads] = static_cast<const U*>(t.in)[from[b] * units + u];
-        for (int b = 0; b < B; ++b)
-            if (from[b] >= 0) static_cast<U*>(t.out)[to[b] * units + u] = held[b * kThreads];
+        U v[kAtOnce] = {};
+        for (int b0 = 0; b0 < B; b0 += kAtOnce) {
+#pragma unroll
+            for (int b = 0; b < kAtOnce; ++b)
+                if (b0 + b < B && from[b0 + b] >= 0) v[b] = static_cast<const U*>(t.in)[from[b0 + b] * units + u];
+            if (B > kAtOnce)
+#pragma unroll
+                for (int b = 0; b < kAtOnce; ++b)
+                    if (b0 + b < B) held[(b0 + b) * kThreads] = v[b];
+        }
+        if (B > kAtOnce) {
+            for (int b = 0; b < B; ++b)
+                if (from[b] >= 0) static_cast<U*>(t.out)[to[b] * units + u] = held[b * kThreads];
+        } else {
+#pragma unroll
+            for (int b = 0; b < kAtOnce; ++b)
+                if (b < B && from[b] >= 0) static_cast<U*>(t.out)[to[b] * units + u] = v[b];
+        }
     }
 }
 
@@ -391,7 +407,7 @@ template <typename U>
 cudaError_t reorder(const ReorderParams& p, cudaStream_t s, int* launches)
 {
     static std::atomic<uint64_t> done{0};
-    const size_t bytes = sizeof(U) * kThreads * (size_t)p.B;
+    const size_t bytes = p.B > kAtOnce ? sizeof(U) * kThreads * (size_t)p.B : 0;
     cudaError_t e = allow_shared(beam_reorder_kernel<U>, sizeof(U) * kThreads * (size_t)kMaxBeams, done);
     if (e != cudaSuccess) return e;
     int64_t most = 1;

@@ -8,7 +8,7 @@
 // Bytes bound it: the states, read and written once (DK * DV * 8 bytes a row and head).  A warp has 16 columns of a head's
 // state to itself, a lane 4 columns of up to 16 neighbouring keys: all its loads are in flight together and the sums over the
 // keys are three rounds of shuffles, so no warp waits for another.  (Blocks of 256 threads for 32 columns, whose
-// sums met in shared memory, executed five times the instructions: 512 rows, 8 heads of 128 x 128, bf16: 110 us; this 84.5, of which the bytes take 79.5.)
+// sums met in shared memory, executed five times the instructions: 256 rows, 16 heads of 128 x 128, bf16: 110 us; this 84.5, of which the bytes take 79.5.)
 #include "delta_internal.h"
 #include "ssm_tile.cuh"
 
