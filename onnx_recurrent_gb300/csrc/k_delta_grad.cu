@@ -514,7 +514,6 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
     // a thread's step, whether of the upper half (dK) or the lower (dQ), and its quarter of the columns
     const int lane_row = warp % 4 * 32 + lane, i = lane_row % C, quarter = warp / 4;
     const bool upper = lane_row < C;
-    const View& out = upper ? q.dK : q.dQ;
     float acc[DKB][16];
 #pragma unroll
     for (int b = 0; b < DKB; ++b)
@@ -978,28 +977,36 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
         }
         if (tid == 0 && given_up) *p.status = 6;        // RNN_ERR_TIMEOUT
     }
-    if (out.data && i < steps) {
-        T* row = static_cast<T*>(out.data) + n * out.bs + (t0 + i) * out.ss + (int64_t)hk * DK;
-        const bool in = t0 + i < len;
-        constexpr int VEC = 16 / (int)sizeof(T);
-        const bool vec = (uintptr_t)out.data % 16 == 0 && (out.ss | out.bs | DK) % VEC == 0;
+    // Rows of dK and then of dQ through shared memory (nothing reads the first images any more), so that a warp's stores are
+    // whole rows: a lane a row, they took 32 lines each.
+    constexpr int VEC = 16 / (int)sizeof(T), kUnits = DKB * 64 / VEC, kRowBytes = kUnits * 16 + 16;
+    static_assert(128 * kRowBytes <= Sm::states, "");
+    unsigned char* rows = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
 #pragma unroll
-        for (int b = 0; b < DKB; ++b) {
-            const int d0 = quarter * DKB * 16 + b * 16;
+    for (int b = 0; b < DKB; ++b)
 #pragma unroll
-            for (int c = 0; c < 16; c += VEC) {
-                __align__(16) T x[VEC];
+        for (int c = 0; c < 16; c += VEC) {
+            __align__(16) T x[VEC];
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) x[e] = from_f<T>(in ? acc[b][c + e] : 0.f);
-                if (vec) {
-                    if (d0 + c < DK) *reinterpret_cast<uint4*>(row + d0 + c) = *reinterpret_cast<const uint4*>(x);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        if (d0 + c + e < DK) row[d0 + c + e] = x[e];
-                }
-            }
+            for (int e = 0; e < VEC; ++e) x[e] = from_f<T>(t0 + i < len ? acc[b][c + e] : 0.f);
+            *reinterpret_cast<uint4*>(rows + lane_row * kRowBytes + (quarter * DKB * 16 + b * 16 + c) * (int)sizeof(T)) = *reinterpret_cast<const uint4*>(x);
         }
+    __syncthreads();
+    constexpr int kEach = 128 / (kRestThreads / 32);        // rows of a warp
+    const int first = warp * kEach, t1 = first % C;
+    const View& to = first < C ? q.dK : q.dQ;
+    if (!to.data) return;
+    T* at = static_cast<T*>(to.data) + n * to.bs + (t0 + t1) * to.ss + (int64_t)hk * DK;
+    if ((uintptr_t)to.data % 16 == 0 && (to.ss | to.bs | DK) % VEC == 0) {
+#pragma unroll
+        for (int k = 0; k < kEach * kUnits / 32; ++k) {
+            const int r = (k * 32 + lane) / kUnits, u = (k * 32 + lane) % kUnits;
+            if (t1 + r < steps && u * VEC < DK)
+                *reinterpret_cast<uint4*>(at + r * to.ss + u * VEC) = *reinterpret_cast<const uint4*>(rows + (first + r) * kRowBytes + u * 16);
+        }
+    } else {
+        for (int r = 0; r < kEach && t1 + r < steps; ++r)
+            for (int d = lane; d < DK; d += 32) at[r * to.ss + d] = reinterpret_cast<const T*>(rows + (first + r) * kRowBytes)[d];
     }
 }
 
