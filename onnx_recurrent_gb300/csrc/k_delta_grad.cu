@@ -964,10 +964,14 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
             __syncthreads();        // the next round's images take the place of this one's
             fence_after();
         }
-        if (!ok && warp == 0) {     // no product is in flight when the block ends
+        if (!ok && warp == 0) {     // no product and no copy is in flight when the block ends
             int never = 0;
             if (leader) mma_commit(&done);
             wait(&done, 0, &never);
+            for (uint64_t* b : {&first_full, &g_full, &k_full}) {
+                never = 0;
+                wait(b, phase, &never);
+            }
         }
         fence_before();
         __syncthreads();
