@@ -27,6 +27,13 @@ View dense(const rnn_view& v, const rnn_delta* pl, int64_t S, int64_t N, int64_t
 
 View dense_row(const rnn_view& v, int64_t inner) { return View{v.data, 0, v.batch_stride ? v.batch_stride : inner}; }
 
+// Whether the images and states of all chunks and heads, at most 2^20 bytes each and a tile of 128 values, are counted in 64 bits.
+bool countable(const rnn_delta* pl, int64_t S, int64_t N)
+{
+    return S <= 0x7fffff00LL && N <= 0x7fffff00LL && N * pl->H <= 0x7fffff00LL &&
+           (S + 63) / 64 <= ((int64_t)1 << 42) / ((pl->DV + 127) / 128) / (N * pl->H > 0 ? N * pl->H : 1);
+}
+
 rnn_status check_sizes(rnn_delta* pl, const void* args, int64_t S, int64_t N)
 {
     if (!pl) return fail(RNN_ERR_INVALID_ARGUMENT, "plan is NULL");
@@ -35,8 +42,7 @@ rnn_status check_sizes(rnn_delta* pl, const void* args, int64_t S, int64_t N)
     if (S < 0 || N < 0)
         return fail(RNN_ERR_INVALID_ARGUMENT, "seq_length %lld, batch_size %lld", (long long)S, (long long)N);
     // heads of all rows are counted over two dimensions of a grid
-    if (S > 0x7fffff00LL || N > 0x7fffff00LL || N * pl->H > 0x7fffff00LL)
-        return fail(RNN_ERR_UNSUPPORTED, "a size of 2^31 or more");
+    if (!countable(pl, S, N)) return fail(RNN_ERR_UNSUPPORTED, "a size of 2^31 or more");
     return RNN_OK;
 }
 
@@ -164,7 +170,7 @@ int rnn_delta_last_launch_count(rnn_delta_t pl) { return pl ? pl->launches : 0; 
 
 int64_t rnn_delta_saved_size(rnn_delta_t pl, int64_t S, int64_t N)
 {
-    if (!pl || S < 0 || N < 0) return -1;
+    if (!pl || S < 0 || N < 0 || !countable(pl, S, N)) return -1;
     return delta_saved_floats(S, N, pl->H, pl->HK, pl->DK, pl->DV, pl->io);
 }
 

@@ -146,3 +146,13 @@ def test_the_binding_checks_shapes_and_types():
         orc.layer_norm(orc.rnn_norm_create(4), torch.zeros(3, 4))
     with pytest.raises(TypeError):
         orc.beam_select(orc.rnn_beam_create(2), torch.zeros(2, 4), torch.zeros(1, 2))
+
+
+def test_sizes_past_counting(lib):
+    """Sizes whose images would not be counted in 64 bits, each of which is in range by itself."""
+    p = orc.rnn_delta_create(1024, 128, 1024)
+    assert orc.rnn_delta_saved_size(p, 2 ** 30, 2 ** 20) == -1
+    assert orc.rnn_delta_saved_size(p, 2 ** 20, 2 ** 10) > 0
+    a = delta_run()
+    a[0], a[1] = 2 ** 30, 2 ** 20
+    assert _run(lib.rnn_delta_rule, p, a) != 0 and "2^31 or more" in orc.rnn_last_error()
