@@ -654,20 +654,34 @@ rnn_status rnn_scores_grad(const rnn_scores_grad_args* args);
  * Views, streams, scratch, captured calls, in-place states and lengths or slots out of
  * range are as with rnn_ssm_*; a view's innermost part is [HK, DK] (Q, K),
  * [H, DV] (V, Y) or [H] (g, beta).  Outputs must not overlap inputs, but for
- * states given as the same memory. */
+ * states given as the same memory.
+ *
+ * Runs and gradients take 64 steps at a time, as products of matrices whose
+ * fp32 operands are the sum of two fp16 numbers over a power of two (22 bits of
+ * a row's largest value; what a run saves, of the largest of 128 values'
+ * rows): errors are those of fp32 sums, within a small factor.  An infinity or a NaN in an
+ * input is found again in every output that depends on it, and may be in those of
+ * the other steps, too, that are among the same 64 of its row and head; other rows
+ * and heads keep theirs.  A call takes 2 launches (4 where few heads have many
+ * steps), a gradient 2, a token 1.  A kernel that waits two seconds for its own copies or
+ * products gives up, and rnn_delta_sync reports RNN_ERR_TIMEOUT. */
 typedef struct rnn_delta* rnn_delta_t;
 
 /* Create a plan (no device work).  heads H > 0; key_heads HK > 0 divides H;
  * key_size DK in [1, 128]; value_size DV in [1, 1024]; H * DV and HK * DK below
  * 2^31; layout 0 or 1 (dense views only); scale finite.  Anything else is
- * RNN_ERR_INVALID_ARGUMENT. */
+ * RNN_ERR_INVALID_ARGUMENT.  A run that does not save takes 35 KB of scratch a
+ * head and 64 steps and 16 KB (fp32: 32) a key head, 64 steps and 64 values of a
+ * key; a gradient 113 KB (fp32: 129) a head, 64 steps and 128 values for keys of
+ * more than 64 values, 32 KB less for others. */
 rnn_status rnn_delta_create(rnn_delta_t* out, int64_t heads, int64_t key_heads, int64_t key_size, int64_t value_size,
                             int layout, float scale);
 void rnn_delta_destroy(rnn_delta_t plan);
 rnn_status rnn_delta_set_io_type(rnn_delta_t plan, int io);
 rnn_status rnn_delta_sync(rnn_delta_t plan);
 int rnn_delta_last_launch_count(rnn_delta_t plan);
-/* Floats of `saved` for a run of this size (-1 for invalid arguments). */
+/* Floats of `saved` for a run of this size in the plan's io type (-1 for
+ * invalid arguments). */
 int64_t rnn_delta_saved_size(rnn_delta_t plan, int64_t seq_length, int64_t batch_size);
 
 typedef struct {
@@ -683,7 +697,8 @@ typedef struct {
 rnn_status rnn_delta_rule(rnn_delta_t plan, const rnn_delta_args* args);
 
 /* Gradients: dY (required) and d_final_state (or NULL) are the loss's slopes in
- * the outputs, `saved` comes from rnn_delta_rule on the same inputs.  dQ, dK,
+ * the outputs, `saved` comes from rnn_delta_rule on the same inputs in the
+ * same io type, and starts on 16 bytes.  dQ, dK,
  * dV, dg, dbeta and d_initial_state (each may be NULL) are overwritten; dQ and dK
  * are summed over the heads that share them.  All sums are taken in a fixed
  * order: the same inputs give the same bits.  d_initial_state may be
