@@ -24,8 +24,9 @@ struct PrepSmem {
         unsigned char KQ[2 * KP * DKB * kBlock];
         unsigned char P[2 * kBlock];        // once K and Q are done with
     };
-    float A[C][C + 1], T[C][C + 1], X[32][33];
-    float ek[C], eq[C], beta[C], fac[768];
+    alignas(16) float A[C][C + 4], T[C][C + 4];     // (X, a product amid T's, lies above A's diagonal)
+    float ek[C], eq[C], beta[C];
+    alignas(16) float fac[768];
     Sums sums;
     float2 carry;
 };
@@ -157,58 +158,74 @@ __global__ void __launch_bounds__(kThreads, 3) delta_prep_kernel(const DeltaPara
         }
     }
     __syncthreads();
+    auto X = [&](int i, int j) { return &s.A[i][32 + j]; };
     {   // two pairs of blocks of 16
         const int at = tid / 128 * 32, i = tid % 128 / 8, j = tid % 8 * 2;
         float x[2] = {0.f, 0.f};
 #pragma unroll
-        for (int m = 0; m < 16; ++m) {
-            const float a = s.A[at + 16 + i][at + m];
-            x[0] = fmaf(a, s.T[at + m][at + j], x[0]);
-            x[1] = fmaf(a, s.T[at + m][at + j + 1], x[1]);
+        for (int m = 0; m < 16; m += 4) {
+            const float4 a4 = *reinterpret_cast<const float4*>(&s.A[at + 16 + i][at + m]);
+            const float a[4] = {a4.x, a4.y, a4.z, a4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 t = *reinterpret_cast<const float2*>(&s.T[at + m + e][at + j]);
+                x[0] = fmaf(a[e], t.x, x[0]);
+                x[1] = fmaf(a[e], t.y, x[1]);
+            }
         }
-        s.X[at / 2 + i][j] = x[0];
-        s.X[at / 2 + i][j + 1] = x[1];
+        *reinterpret_cast<float2*>(X(at / 2 + i, j)) = make_float2(x[0], x[1]);
         __syncthreads();
         x[0] = x[1] = 0.f;
 #pragma unroll
-        for (int m = 0; m < 16; ++m) {
-            const float a = -s.T[at + 16 + i][at + 16 + m];
-            x[0] = fmaf(a, s.X[at / 2 + m][j], x[0]);
-            x[1] = fmaf(a, s.X[at / 2 + m][j + 1], x[1]);
+        for (int m = 0; m < 16; m += 4) {
+            const float4 a4 = *reinterpret_cast<const float4*>(&s.T[at + 16 + i][at + 16 + m]);
+            const float a[4] = {-a4.x, -a4.y, -a4.z, -a4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 t = *reinterpret_cast<const float2*>(X(at / 2 + m + e, j));
+                x[0] = fmaf(a[e], t.x, x[0]);
+                x[1] = fmaf(a[e], t.y, x[1]);
+            }
         }
-        s.T[at + 16 + i][at + j] = x[0];
-        s.T[at + 16 + i][at + j + 1] = x[1];
-        s.T[at + i][at + 16 + j] = s.T[at + i][at + 17 + j] = 0.f;
+        *reinterpret_cast<float2*>(&s.T[at + 16 + i][at + j]) = make_float2(x[0], x[1]);
+        *reinterpret_cast<float2*>(&s.T[at + i][at + 16 + j]) = make_float2(0.f, 0.f);
     }
     __syncthreads();
     {   // the two of 32
         const int i = tid / 8, j = tid % 8 * 4;
         float x[4] = {};
-#pragma unroll 8
-        for (int m = 0; m < 32; ++m) {
-            const float a = s.A[32 + i][m];
+        auto add = [&](const float4& a4, float sign, auto row) {
+            const float a[4] = {sign * a4.x, sign * a4.y, sign * a4.z, sign * a4.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = fmaf(a, s.T[m][j + e], x[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s.X[i][j + e] = x[e], x[e] = 0.f;
+            for (int e = 0; e < 4; ++e) {
+                const float4 t = *reinterpret_cast<const float4*>(row(e));
+                x[0] = fmaf(a[e], t.x, x[0]);
+                x[1] = fmaf(a[e], t.y, x[1]);
+                x[2] = fmaf(a[e], t.z, x[2]);
+                x[3] = fmaf(a[e], t.w, x[3]);
+            }
+        };
+#pragma unroll 2
+        for (int m = 0; m < 32; m += 4) add(*reinterpret_cast<const float4*>(&s.A[32 + i][m]), 1.f, [&](int e) { return &s.T[m + e][j]; });
+        *reinterpret_cast<float4*>(X(i, j)) = make_float4(x[0], x[1], x[2], x[3]);
+        x[0] = x[1] = x[2] = x[3] = 0.f;
         __syncthreads();
-#pragma unroll 8
-        for (int m = 0; m < 32; ++m) {
-            const float a = -s.T[32 + i][32 + m];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = fmaf(a, s.X[m][j + e], x[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s.T[32 + i][j + e] = x[e], s.T[i][32 + j + e] = 0.f;
+#pragma unroll 2
+        for (int m = 0; m < 32; m += 4) add(*reinterpret_cast<const float4*>(&s.T[32 + i][32 + m]), -1.f, [&](int e) { return X(m + e, j); });
+        *reinterpret_cast<float4*>(&s.T[32 + i][j]) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4*>(&s.T[i][32 + j]) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     __syncthreads();
     unsigned char* out = mats + (nh * chunks + chunk) * Images<DKB, KP>::mats;
     {   // T's parts: four threads a row, 16 values each
         const int i = tid / 4, j = tid % 4 * 16;
         float m = 0.f;
+        float4 t4[4];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(s.T[i][j + e]));
+        for (int e = 0; e < 4; ++e) {
+            t4[e] = *reinterpret_cast<const float4*>(&s.T[i][j + 4 * e]);
+            m = fmaxf(m, fmaxf(fmaxf(fabsf(t4[e].x), fabsf(t4[e].y)), fmaxf(fabsf(t4[e].z), fabsf(t4[e].w))));
+        }
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
         const Scale sc = scale_of(m);
@@ -219,7 +236,11 @@ __global__ void __launch_bounds__(kThreads, 3) delta_prep_kernel(const DeltaPara
             unsigned* hs = &hi.x;
             unsigned* ls = &lo.x;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) split_pair(s.T[i][j + q * 8 + 2 * e] * sc.down, s.T[i][j + q * 8 + 2 * e + 1] * sc.down, hs[e], ls[e]);
+            for (int e = 0; e < 2; ++e) {
+                const float4 t = t4[2 * q + e];
+                split_pair(t.x * sc.down, t.y * sc.down, hs[2 * e], ls[2 * e]);
+                split_pair(t.z * sc.down, t.w * sc.down, hs[2 * e + 1], ls[2 * e + 1]);
+            }
             *reinterpret_cast<uint4*>(out + swizzled(i, j + q * 8)) = hi;
             *reinterpret_cast<uint4*>(out + kBlock + swizzled(i, j + q * 8)) = lo;
         }
