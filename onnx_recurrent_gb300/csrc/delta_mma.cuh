@@ -4,7 +4,8 @@
 // An fp32 operand x is taken as two fp16 parts, hi = fp16(x / s) and lo = fp16(x / s - hi), with s
 // a power of two just above the largest |x| of its row: hi + lo has 22 bits, and
 // what a value far below its row's largest loses is below 2^-24 of that.  A product of two such operands is
-// hi hi + hi lo + lo hi (what is left out is below 2^-22 of it), summed in fp32.  Scales are applied
+// hi lo + lo hi + hi hi (what is left out is below 2^-22 of it), summed in fp32 in this order: every instruction of 16
+// products rounds its sum towards zero, so the large ones come last (first, results were off by twice as much).  Scales are applied
 // exactly, to a row of the result or, along the sum, to the other operand.  16-bit inputs are one part:
 // fp16 values, and bf16 values over their row's power of two, have no second.
 #pragma once
