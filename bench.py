@@ -308,6 +308,7 @@ def measure_l2_gbs(torch, nbytes=32 << 20, reps=10, trials=5):
 # kernel's code is unchanged.
 _COMMON = ["tma.cuh", "exact_math.cuh", "io_types.cuh", "rnn_internal.h"]
 _SSM = ["ssm_math.cuh", "ssm_internal.h"]
+_DELTA = ["delta_internal.h", "delta_tile.cuh", "delta_mma.cuh", "ssm_tile.cuh", "tma.cuh", "delta_api.cpp", "plan.h"] + _SSM
 KERNEL_SOURCES = {
     "rnn_recurrent_kernel": ["k_recur.cuh", "k_recur_rnn.cu", "k_recur_gru.cu", "k_recur_lstm.cu"] + _COMMON,
     "rnn_dataflow_kernel": ["k_recur.cuh", "k_recur2.cuh", "k_recur_rnn.cu", "k_recur_gru.cu", "k_recur_lstm.cu",
@@ -323,6 +324,11 @@ KERNEL_SOURCES = {
     "ssm_scan_grad_kernel": ["k_ssm_scan_grad.cu", "ssm_tile.cuh", "ssm_api.cpp"] + _SSM,
     "ssm_scan_step_kernel": ["k_ssm_step.cu", "ssm_tile.cuh", "ssm_api.cpp"] + _SSM,
     "scores_kernel": ["k_scores.cu", "ssm_tile.cuh", "tma.cuh", "ssm_api.cpp"] + _SSM,
+    "delta_run_kernel": ["k_delta.cu"] + _DELTA,
+    "delta_grad_rest_kernel": ["k_delta_grad.cu"] + _DELTA,
+    "delta_step_kernel": ["k_delta_step.cu"] + _DELTA,
+    "norm_kernel": ["k_norm.cu", "norm_internal.h", "norm_api.cpp", "plan.h"] + _SSM,
+    "beam_rows_kernel": ["k_beam.cu", "norm_internal.h", "ssm_tile.cuh", "beam_api.cpp", "plan.h"] + _SSM,
 }
 
 
