@@ -475,8 +475,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) delta_grad_chain_kernel(cons
 // a thread's 16 columns and those before, added down the rows i >= t.
 //
 // 240 KB come in a chunk and head of 128 x 128 at 16 bits, copied as they are.  Its phases bound it, five rounds of products
-// and what forms their operands, with one block a multiprocessor (197 KB of shared memory): 4096 chunks take 470 us, 1.24 GB at
-// 2.6 TB/s, the tensor cores at 15 %.
+// and what forms their operands, with one block a multiprocessor (197 KB of shared memory): 4096 chunks take 457 us, 1.24 GB at
+// 2.7 TB/s, the tensor cores at 15 %.
 constexpr int kRestThreads = 512;
 template <int DKB, int KP>
 struct RestSmem {
@@ -484,10 +484,13 @@ struct RestSmem {
     // when these are done with)
     static constexpr unsigned u = 0, r = 2 * kSheetImage, y = 3 * kSheetImage, states = 6 * kSheetImage;
     static constexpr bool early = KP == 1;
-    static constexpr unsigned keys = early ? states + 2 * DKB * kSheetImage : states;
-    static constexpr unsigned end = states + 2 * DKB * kSheetImage + (early ? Images<DKB, KP>::keys : 0);
-    // once [dR; dY] and u are done with: E; [EA + EA^T; EP]; EP^T
-    static constexpr unsigned e = r, a1 = 4 * kSheetImage, a2 = u;
+    // once [dR; dY] are done with: E; [EA + EA^T; EP].  EP^T has a place of its own, or u's once that is done with
+    static constexpr unsigned after = states + 2 * DKB * kSheetImage;
+    static constexpr unsigned e = r, a1 = 4 * kSheetImage, a2 = early ? after : u;
+    static constexpr unsigned keys = early ? after + 2 * kBlock : states;
+    static constexpr unsigned end = early ? keys + Images<DKB, KP>::keys : after;
+    // (the products read 128 rows of EP^T's parts, of which 64 are there: what lies behind them must be the block's, too)
+    static_assert(a2 + kBlock + 2 * kBlock <= end, "");
     static constexpr size_t bytes = end + 1024;
     static_assert(Images<DKB, KP>::keys <= 2 * DKB * kSheetImage, "");
 };
@@ -733,7 +736,60 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                 mbar_arrive_expect_tx(&g_full, kStates);
                 bulk_g2s(base + Sm::states, slopes, kStates, &g_full);
             }
-            if (Sm::early) put_e();
+            // rows of [EA + EA^T; EP] and EP^T, times the scales of K's and Q's rows
+            auto pair_to = [&](unsigned img, unsigned second, int r, const float (&v)[2], float down) {
+                unsigned hi, lo;
+                split_pair(v[0] * down, v[1] * down, hi, lo);
+                unsigned char* to = base + img + swizzled(r, 2 * lane);
+                *reinterpret_cast<unsigned*>(to) = hi;
+                *reinterpret_cast<unsigned*>(to + second) = lo;
+            };
+            auto at_e = [&](int r, int j) { return E[r * C + (j ^ (r & 31))]; };
+            auto convert = [&] {
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                    const int r = warp + 16 * a;
+                    float ea[2], ep[2], et[2], mk = 0.f, mq = 0.f;
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        const int j = 2 * lane + w;
+                        const float ks = fac[kKeyScale + j];
+                        ea[w] = (at_e(r, j) + at_e(j, r)) * ks;
+                        ep[w] = at_e(C + r, j) * ks;
+                        et[w] = at_e(C + j, r) * fac[kQueryScale + j];
+                        mk = fmaxf(mk, fmaxf(fabsf(ea[w]), fabsf(et[w])));
+                        mq = fmaxf(mq, fabsf(ep[w]));
+                    }
+                    const Scale sk = scale_of(warp_most(mk)), sq = scale_of(warp_most(mq));
+                    pair_to(Sm::a1, kSheetImage, r, ea, sk.down);
+                    pair_to(Sm::a1, kSheetImage, C + r, ep, sq.down);
+                    pair_to(Sm::a2, kBlock, r, et, sk.down);
+                    if (lane == 0) k_scale[r] = sk.up, q_scale[r] = sq.up;
+                }
+            };
+            auto step_products = [&] {
+#pragma unroll 1
+                for (int r = KP; r >= 0; --r)    // hi lo, lo hi, hi hi
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        if (leader)
+                            mma_ss(tm + cK, desc_rows(sbase + Sm::a1 + (r == 1) * kSheetImage + ks * 32),
+                                   desc_columns(kimg + (r == 2) * DKB * 2 * kBlock + ks * 2048, 2 * kBlock), instr(DKB * 64, true), r < KP || ks > 0);
+#pragma unroll 1
+                for (int r = KP; r >= 0; --r)
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        if (leader)
+                            mma_ss(tm + cKE, desc_rows(sbase + Sm::a2 + (r == 1) * kBlock + ks * 32),
+                                   desc_columns(qimg + (r == 2) * DKB * 2 * kBlock + ks * 2048, 2 * kBlock), instr(DKB * 64, true), r < KP || ks > 0);
+                if (leader) mma_commit(&k_done);
+            };
+            if (Sm::early) {        // while dS1 is on its way
+                put_e();
+                __syncthreads();
+                convert();
+                fence_shared();
+            }
             ok = await(&g_full);
             if (!ok) break;
             if (warp == 0) {
@@ -746,6 +802,7 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                                    desc_kept(sbase + Sm::states + (r == 2) * DKB * kSheetImage, ks), instr(DKB * 64, true) | 1u << 15,
                                    r < 2 || ks > 0);
                 if (leader) mma_commit(&x3_done);
+                if (Sm::early) step_products();
             }
             {   // <dS1, S0>
                 float dot = 0.f;
@@ -784,54 +841,10 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                 form_e();
                 put_e();
                 __syncthreads();
-            }
-            // rows of [EA + EA^T; EP] and EP^T, times the scales of K's and Q's rows
-            auto pair_to = [&](unsigned img, unsigned second, int r, const float (&v)[2], float down) {
-                unsigned hi, lo;
-                split_pair(v[0] * down, v[1] * down, hi, lo);
-                unsigned char* to = base + img + swizzled(r, 2 * lane);
-                *reinterpret_cast<unsigned*>(to) = hi;
-                *reinterpret_cast<unsigned*>(to + second) = lo;
-            };
-            auto at_e = [&](int r, int j) { return E[r * C + (j ^ (r & 31))]; };
-#pragma unroll
-            for (int a = 0; a < 4; ++a) {
-                const int r = warp + 16 * a;
-                float ea[2], ep[2], et[2], mk = 0.f, mq = 0.f;
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const int j = 2 * lane + w;
-                    const float ks = fac[kKeyScale + j];
-                    ea[w] = (at_e(r, j) + at_e(j, r)) * ks;
-                    ep[w] = at_e(C + r, j) * ks;
-                    et[w] = at_e(C + j, r) * fac[kQueryScale + j];
-                    mk = fmaxf(mk, fmaxf(fabsf(ea[w]), fabsf(et[w])));
-                    mq = fmaxf(mq, fabsf(ep[w]));
-                }
-                const Scale sk = scale_of(warp_most(mk)), sq = scale_of(warp_most(mq));
-                pair_to(Sm::a1, kSheetImage, r, ea, sk.down);
-                pair_to(Sm::a1, kSheetImage, C + r, ep, sq.down);
-                pair_to(Sm::a2, kBlock, r, et, sk.down);
-                if (lane == 0) k_scale[r] = sk.up, q_scale[r] = sq.up;
-            }
-            fence_shared();
-            __syncthreads();
-            if (warp == 0) {
-#pragma unroll 1
-                for (int r = KP; r >= 0; --r)    // hi lo, lo hi, hi hi
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        if (leader)
-                            mma_ss(tm + cK, desc_rows(sbase + Sm::a1 + (r == 1) * kSheetImage + ks * 32),
-                                   desc_columns(kimg + (r == 2) * DKB * 2 * kBlock + ks * 2048, 2 * kBlock), instr(DKB * 64, true), r < KP || ks > 0);
-#pragma unroll 1
-                for (int r = KP; r >= 0; --r)
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        if (leader)
-                            mma_ss(tm + cKE, desc_rows(sbase + Sm::a2 + (r == 1) * kBlock + ks * 32),
-                                   desc_columns(qimg + (r == 2) * DKB * 2 * kBlock + ks * 2048, 2 * kBlock), instr(DKB * 64, true), r < KP || ks > 0);
-                if (leader) mma_commit(&k_done);
+                convert();
+                fence_shared();
+                __syncthreads();
+                if (warp == 0) step_products();
             }
             // in the meantime what the states give, and its sums with K and Q
             const float es = fac[(upper ? kKeyScale : kQueryScale) + i];
