@@ -108,10 +108,10 @@ def _count(plan, X):
 def rnn_layer_norm(plan: Norm, X, W=None, bias=None, Y=None, stats=None, stream=None):
     """Y = (X - mean) rstd W + bias over the last dimension; stats [rows, 2] takes mean and rstd.  Y may be X."""
     dev = _device(X, "X")
-    rows, d = _count(plan, X), (plan.size,)
+    rows, d, shape = _count(plan, X), (plan.size,), X.shape
     args = struct.pack(
-        "9q", rows, *_rows(plan, X, "X", X.shape, dev), _dense(W, d, _f32, dev, "W"), _dense(bias, d, _f32, dev, "bias"),
-        *_rows(plan, Y, "Y", X.shape, dev), _dense(stats, (rows, 2), _f32, dev, "stats"),
+        "9q", rows, *_rows(plan, X, "X", shape, dev), _dense(W, d, _f32, dev, "W"), _dense(bias, d, _f32, dev, "bias"),
+        *_rows(plan, Y, "Y", shape, dev), _dense(stats, (rows, 2), _f32, dev, "stats"),
         _ssm._raw_stream(dev) if stream is None else _handle(stream))
     _call(dev, _lib.rnn_layer_norm, plan.handle, args)
 
@@ -121,7 +121,7 @@ def layer_norm(plan: Norm, X, W=None, bias=None, stream=None):
     if stream is not None:
         with _onto(stream, X.device):
             return layer_norm(plan, X, W, bias)
-    Y = torch.empty(X.shape, dtype=plan.dtype, device=X.device)
+    Y = torch.empty_like(X, memory_format=torch.contiguous_format)      # (of the plan's type, or the call refuses X)
     stats = torch.empty((_count(plan, X), 2), dtype=_f32, device=X.device)
     rnn_layer_norm(plan, X, W, bias, Y, stats)
     return Y, stats
@@ -143,7 +143,7 @@ def layer_norm_grad(plan: Norm, dY, X, stats, W=None, bias=None, stream=None):
     if stream is not None:
         with _onto(stream, X.device):
             return layer_norm_grad(plan, dY, X, stats, W, bias)
-    out = {"dX": torch.empty(X.shape, dtype=plan.dtype, device=X.device)}
+    out = {"dX": torch.empty_like(X, memory_format=torch.contiguous_format)}
     if W is not None:
         out["dW"] = torch.empty_like(W)
     if bias is not None:
