@@ -813,7 +813,8 @@ typedef struct {
 rnn_status rnn_beam_select(rnn_beam_t plan, const rnn_beam_select_args* args);
 typedef struct {
     const void* in;                /* rows, row_bytes each, one after another */
-    void* out;                     /* may be in itself (an overlap in part is refused) */
+    void* out;                     /* may be in itself (an overlap in part is refused, as is one with another
+                                      tensor, parents or slots) */
     int64_t row_bytes;
 } rnn_beam_tensor;
 typedef struct {

@@ -134,6 +134,24 @@ rnn_status rnn_beam_reorder(rnn_beam_t pl, const rnn_beam_reorder_args* a)
         rs = check_in_place(t.in, t.out, (size_t)(rows * t.row_bytes), "a tensor's in and out");
         if (rs != RNN_OK) return rs;
     }
+    // Blocks of all tensors run side by side: none may write where another reads or writes.
+    auto meet = [](const void* a, uint64_t an, const void* b, uint64_t bn) {
+        return (uintptr_t)a < (uintptr_t)b + bn && (uintptr_t)b < (uintptr_t)a + an;
+    };
+    const uint64_t beams = 4 * (uint64_t)(a->items * pl->B);
+    for (int64_t i = 0; i < a->n_tensors; ++i) {
+        const rnn_beam_tensor& t = a->tensors[i];
+        const uint64_t bytes = (uint64_t)(rows * t.row_bytes);
+        if (!bytes) continue;
+        if (meet(t.out, bytes, a->parents, beams) || (a->slots && meet(t.out, bytes, a->slots, beams)))
+            return fail(RNN_ERR_INVALID_ARGUMENT, "tensor %lld's out overlaps parents or slots", (long long)i);
+        for (int64_t j = 0; j < i; ++j) {
+            const rnn_beam_tensor& o = a->tensors[j];
+            const uint64_t others = (uint64_t)(rows * o.row_bytes);
+            if (others && (meet(t.out, bytes, o.out, others) || meet(t.out, bytes, o.in, others) || meet(t.in, bytes, o.out, others)))
+                return fail(RNN_ERR_INVALID_ARGUMENT, "tensors %lld and %lld overlap", (long long)j, (long long)i);
+        }
+    }
     rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
     ReorderParams p{};

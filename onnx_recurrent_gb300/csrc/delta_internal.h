@@ -50,7 +50,7 @@ struct DeltaStepParams {
 __host__ __device__ inline int64_t delta_chunks(int64_t S) { return (S + kDeltaChunk - 1) / kDeltaChunk; }
 // The images of a run's chunks (delta_mma.cuh), and what a run saves for its gradient: them, the states
 // before the chunks, and u.
-constexpr int64_t kDeltaBlock = 8192, kDeltaMats = 4 * kDeltaBlock + 3072;
+constexpr int64_t kDeltaBlock = 8192, kDeltaFactors = 768 * 4, kDeltaMats = 4 * kDeltaBlock + kDeltaFactors;
 inline int64_t delta_keys_bytes(int64_t S, int64_t N, int64_t HK, int64_t DK, int io)
 {
     return N * HK * delta_chunks(S) * 2 * (io == 0 ? 2 : 1) * ((DK + 63) / 64) * kDeltaBlock;

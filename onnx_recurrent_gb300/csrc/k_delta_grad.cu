@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                 if (there) {
                     prefetch(p.kept + next_at * kept_tile, (unsigned)kept_tile);
                     prefetch(q.slopes + next_at * slopes_tile, (unsigned)slopes_tile);
-                    prefetch(p.mats + next_at / tiles * Im::mats + 4 * kBlock, 3072);
+                    prefetch(p.mats + next_at / tiles * Im::mats + 4 * kBlock, (unsigned)kDeltaFactors);
                     if (next_keys >= 0) prefetch(p.keys + next_keys * Im::keys, Im::keys);
                 }
             }

@@ -156,3 +156,18 @@ def test_sizes_past_counting(lib):
     a = delta_run()
     a[0], a[1] = 2 ** 30, 2 ** 20
     assert _run(lib.rnn_delta_rule, p, a) != 0 and "2^31 or more" in orc.rnn_last_error()
+
+
+def test_tensors_reordered_at_once_lie_apart(lib):
+    """Blocks of all tensors run side by side: a tensor given twice would be reordered while it is read."""
+    p = orc.rnn_beam_create(4)
+    r = lib.rnn_beam_reorder
+    table = lambda *rows: ctypes.create_string_buffer(struct.pack(f"{3 * len(rows)}q", *[x for t in rows for x in t]))  # noqa: E731
+    # 8 rows of 16 bytes each: 128 bytes a tensor; parents 32 bytes at AT
+    for second in [(FAR, FAR, 16), (FAR, 2 * FAR, 16), (2 * FAR, FAR, 16), (FAR + 64, FAR + 64, 16), (2 * FAR, FAR + 127, 16)]:
+        both = table((FAR, FAR, 16), second)
+        _refused(r, p, [2, 2, 0, AT, 0, ctypes.addressof(both), 0], "tensors 0 and 1 overlap")
+    one = table((FAR, AT + 16, 16))
+    _refused(r, p, [2, 1, 0, AT, 0, ctypes.addressof(one), 0], "overlaps parents")
+    one = table((FAR, 2 * FAR, 16))
+    _refused(r, p, [2, 1, 100, AT, 2 * FAR + 1596, ctypes.addressof(one), 0], "overlaps parents or slots")
