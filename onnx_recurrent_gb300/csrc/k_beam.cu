@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kItemThreads) beam_select_kernel(const BeamSel
         const bool done = p.finished && p.finished[item * B + b];
         const Part* parts = reinterpret_cast<const Part*>(p.scratch) + (p.shared ? item : item * B + b) * p.parts;
         bool dead = !(fabsf(s) < CUDART_INF_F);
-        double lse = 0.0;
+        double most = 0.0, rest = 0.0;      // lse = most + rest, apart: of a row of nothing but a mask's lowest value, 3e38, the sum would be `most` again
         Key list = 0;
         if (!dead && !done) {
             float m = -CUDART_INF_F, sum = 0.f;
@@ -300,7 +300,8 @@ __global__ void __launch_bounds__(kItemThreads) beam_select_kernel(const BeamSel
                     if (i == 0) list = some;
                     else join(list, some);
                 }
-                lse = (double)m + log((double)sum);
+                most = (double)m;
+                rest = log((double)sum);
             }
         }
         // Candidates of -inf alone come by token; a finished beam's first is its end, then the others.
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(kItemThreads) beam_select_kernel(const BeamSel
             if (lane == 0) total = (double)s;
         } else if (!dead) {
             id = (int)~(unsigned)list;
-            total = (double)s + ((double)logit_of(list) - lse);
+            total = (double)s + (((double)logit_of(list) - most) - rest);
             if (!(total == total)) total = none;
         }
         const long long bits = __double_as_longlong(total + 0.0);

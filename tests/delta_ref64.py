@@ -93,7 +93,7 @@ def beam(logits, scores, finished, end):
             elif done:
                 lp[end] = s
             elif bool(lse.isfinite()):
-                lp = s + (logits[i, b] - lse)
+                lp = s + torch.log_softmax(logits[i, b], 0)         # (logits - lse loses log V where all are -3e38)
             cand.append(lp)
         total, order = torch.sort(torch.cat(cand), descending=True, stable=True)
         parent, token = order[:B] // V, order[:B] % V
