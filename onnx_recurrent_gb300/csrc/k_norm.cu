@@ -2,8 +2,11 @@
 // include/onnx_recurrent.h).
 //
 // A row is read once and held in registers: its mean first, then the mean square of what is left
-// of each value (no difference of large sums, so rows far from zero lose nothing).  With z = (x -
-// mean) rstd and w = dY W,
+// of each value, d = x - mean (no difference of large sums).  That mean is a number of 24 bits, and the sum that it came from
+// has rounded: c, the mean of d, is what it is off by, and comes with the squares in one more reduction's second value.  d - c
+// is then off by a few units of itself, however far the row is from zero, and so are the variance, mean(d^2) - c^2, and z
+// = (d - c) rstd.  (A constant row of 2048 times 1000.1: the mean is off by 6e-5, Y was 0.02 at eps 1e-5.)  The gradient
+// has mean + c, rounded, of the statistics, and finds what that is off by where it may matter (off_matters).  With w = dY W,
 //     dX = rstd (w - mean(w) - z mean(w z)),   dW = sum over rows of dY z,   dbias = that of dY.
 //
 // Bytes bound both.  Blocks walk rows; in the gradient a thread keeps the sums over rows of its columns, which go to
@@ -34,26 +37,56 @@ struct Shape {
 template <typename S, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float (*shared)[N])
 {
+    static_assert(N == 1 || N == 2, "a value, or one a half of a warp");
+    const int lane = threadIdx.x % 32;
+    if constexpr (S::TPR == 32) {
 #pragma unroll
-    for (int o = 16; o; o /= 2)
+        for (int o = 16; o; o /= 2)
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-    if constexpr (S::TPR > 32) {
-        const int warp = threadIdx.x / 32, first = warp / (S::TPR / 32) * (S::TPR / 32);
-        if (threadIdx.x % 32 == 0)
+            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    } else {
+        // Two values' first round leaves one each half of the warp: 5 exchanges in place of 10.
+        float x = v[0];
+        if constexpr (N == 1) {
+            x += __shfl_xor_sync(0xffffffffu, x, 16);
+        } else {
+            const float give = lane < 16 ? v[1] : v[0];
+            x = (lane < 16 ? v[0] : v[1]) + __shfl_xor_sync(0xffffffffu, give, 16);
+        }
 #pragma unroll
-            for (int i = 0; i < N; ++i) shared[warp][i] = v[i];
+        for (int o = 8; o; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
+        constexpr int warps = S::TPR / 32;
+        const int warp = threadIdx.x / 32, first = warp / warps * warps;
+        if (lane % 16 == 0 && lane / 16 < N) shared[warp][lane / 16] = x;
         // (rows of a block do not wait for each other)
         if constexpr (S::groups > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / S::TPR), "n"(S::TPR) : "memory");
         else __syncthreads();
+        if constexpr (warps == 32) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            v[i] = 0.f;
+            for (int i = 0; i < N; ++i) v[i] = shared[lane][i];
 #pragma unroll
-            for (int w = 0; w < S::TPR / 32; ++w) v[i] += shared[first + w][i];
+            for (int o = 16; o; o /= 2)
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = 0.f;
+#pragma unroll
+            for (int w = 0; w < warps; ++w) {
+                if constexpr (N == 1) {
+                    v[0] += shared[first + w][0];
+                } else {
+                    const float2 both = *reinterpret_cast<const float2*>(shared[first + w]);
+                    v[0] += both.x;
+                    v[1] += both.y;
+                }
+            }
         }
     }
 }
+
+// Whether what a mean that is held as one fp32 number is off by, at most 2^-24 of itself, may be more than 16 of 2^-24 in z.
+__device__ __forceinline__ bool off_matters(float mean, float rstd) { return fabsf(mean) * rstd > 16.f; }
 
 template <typename S>
 __device__ __forceinline__ void load_weights(float (&w)[S::NV], const float* from, int D, int t, float otherwise)
@@ -83,12 +116,13 @@ __device__ __forceinline__ void piece_weights(float (&w)[VEC], const float* from
     }
 }
 
+// (Blocks a multiprocessor: without a bound the registers of what the mean is off by cost the fourth.)
 template <typename S>
-__global__ void __launch_bounds__(S::threads, S::NV == 32 && S::VEC > 1 && S::threads == 256 ? 4 : 1) norm_kernel(const NormParams p)
+__global__ void __launch_bounds__(S::threads, S::NV == 8 || (S::NV == 32 && S::VEC > 1 && S::threads == 256) ? 4 : 1) norm_kernel(const NormParams p)
 {
     using T = typename S::T;
     using P = Piece<T, S::VEC>;
-    __shared__ float sums[2][S::threads / 32][1];
+    __shared__ __align__(8) float sums[S::threads / 32][1], more[S::threads / 32][2];
     const int t = threadIdx.x % S::TPR, group = threadIdx.x / S::TPR, pieces = p.D / S::VEC;
     float w[S::weights ? S::NV : 1], b[S::weights ? S::NV : 1];
     if constexpr (S::weights) {
@@ -109,22 +143,24 @@ __global__ void __launch_bounds__(S::threads, S::NV == 32 && S::VEC > 1 && S::th
         for (int i = 0; i < S::PER; ++i)
 #pragma unroll
             for (int e = 0; e < S::VEC; ++e) s[0] += to_f(x[i].v[e]);
-        row_sums<S>(s, sums[0]);
+        row_sums<S>(s, sums);
         const float mean = s[0] / (float)p.D;
-        s[0] = 0.f;
+        float left[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < S::PER; ++i)
             if (i * S::TPR + t < pieces)
 #pragma unroll
                 for (int e = 0; e < S::VEC; ++e) {
                     const float d = to_f(x[i].v[e]) - mean;
-                    s[0] = fmaf(d, d, s[0]);
+                    left[0] += d;
+                    left[1] = fmaf(d, d, left[1]);
                 }
-        row_sums<S>(s, sums[1]);
+        row_sums<S>(left, more);
         if (!in) continue;
-        const float rstd = 1.f / sqrtf(s[0] / (float)p.D + p.eps);
+        const float c = left[0] / (float)p.D, var = left[1] / (float)p.D - c * c;
+        const float rstd = 1.f / sqrtf((var < 0.f ? 0.f : var) + p.eps);      // (a NaN stays)
         if (p.stats && t == 0) {
-            p.stats[2 * r] = mean;
+            p.stats[2 * r] = mean + c;
             p.stats[2 * r + 1] = rstd;
         }
         P* to = reinterpret_cast<P*>(static_cast<T*>(p.Y) + r * p.ys);
@@ -141,20 +177,22 @@ __global__ void __launch_bounds__(S::threads, S::NV == 32 && S::VEC > 1 && S::th
 #pragma unroll
             for (int e = 0; e < S::VEC; ++e) {
                 if constexpr (S::weights) pw[e] = w[i * S::VEC + e], pb[e] = b[i * S::VEC + e];
-                q.v[e] = from_f<T>(fmaf((to_f(x[i].v[e]) - mean) * rstd, pw[e], pb[e]));
+                q.v[e] = from_f<T>(fmaf(((to_f(x[i].v[e]) - mean) - c) * rstd, pw[e], pb[e]));
             }
             to[at] = q;
         }
     }
 }
 
-// SUMS: dW and dbias too.
+// SUMS: dW and dbias too.  (Blocks a multiprocessor as above: with three in place of four 16384 rows of 2048 in bf16 took 95 us
+// for 67, with one in place of two 8192 rows of 4096 110 for 83.)
 template <typename S, bool SUMS>
-__global__ void __launch_bounds__(S::threads) norm_grad_kernel(const NormGradParams p)
+__global__ void __launch_bounds__(S::threads, S::NV == 8 ? 4 : S::NV == 16 && S::threads == 256 ? 2 : 1) norm_grad_kernel(const NormGradParams p)
 {
     using T = typename S::T;
     using P = Piece<T, S::VEC>;
-    __shared__ float sums[2][S::threads / 32][2];
+    __shared__ __align__(8) float sums[2][S::threads / 32][2];
+    __shared__ float offs[2][S::threads / 32][1];
     const NormParams& f = p.f;
     const int t = threadIdx.x % S::TPR, group = threadIdx.x / S::TPR, pieces = f.D / S::VEC;
     float w[S::weights ? S::NV : 1], dw[SUMS ? S::NV : 1] = {}, db[SUMS ? S::NV : 1] = {};
@@ -164,10 +202,11 @@ __global__ void __launch_bounds__(S::threads) norm_grad_kernel(const NormGradPar
         if constexpr (S::weights) return w[i * S::VEC + e];
         else return f.W && i * S::TPR + t < pieces ? f.W[(i * S::TPR + t) * S::VEC + e] : 1.f;
     };
-    int turn = 0;
+    int turn = 0, found = 0;
     for (int64_t r0 = (int64_t)blockIdx.x * S::groups; r0 < f.rows; r0 += (int64_t)gridDim.x * S::groups, turn ^= 1) {
         const int64_t r = r0 + group;
         const bool in = r < f.rows;
+        const float mean = in ? f.stats[2 * r] : 0.f, rstd = in ? f.stats[2 * r + 1] : 0.f;
         const P* fx = reinterpret_cast<const P*>(static_cast<const T*>(f.X) + r * f.xs);
         const P* fy = reinterpret_cast<const P*>(static_cast<const T*>(p.dY) + r * p.dys);
         P x[S::PER] = {}, y[S::PER] = {};
@@ -177,13 +216,24 @@ __global__ void __launch_bounds__(S::threads) norm_grad_kernel(const NormGradPar
                 x[i] = fx[i * S::TPR + t];
                 y[i] = fy[i * S::TPR + t];
             }
-        const float mean = in ? f.stats[2 * r] : 0.f, rstd = in ? f.stats[2 * r + 1] : 0.f;
+        float c = 0.f;
+        if (off_matters(mean, rstd)) {      // (all of a row's threads, which meet here)
+            float s[1] = {0.f};
+#pragma unroll
+            for (int i = 0; i < S::PER; ++i)
+                if (i * S::TPR + t < pieces)
+#pragma unroll
+                    for (int e = 0; e < S::VEC; ++e) s[0] += to_f(x[i].v[e]) - mean;
+            row_sums<S>(s, offs[found]);
+            found ^= 1;
+            c = s[0] * per;
+        }
         float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < S::PER; ++i)
 #pragma unroll
             for (int e = 0; e < S::VEC; ++e) {      // (past the row's end dY is 0)
-                const float z = (to_f(x[i].v[e]) - mean) * rstd, d = to_f(y[i].v[e]), g = d * weight(i, e);
+                const float z = ((to_f(x[i].v[e]) - mean) - c) * rstd, d = to_f(y[i].v[e]), g = d * weight(i, e);
                 s[0] += g;
                 s[1] = fmaf(g, z, s[1]);
                 if constexpr (SUMS) {
@@ -203,7 +253,7 @@ __global__ void __launch_bounds__(S::threads) norm_grad_kernel(const NormGradPar
             P q;
 #pragma unroll
             for (int e = 0; e < S::VEC; ++e) {
-                const float z = (to_f(x[i].v[e]) - mean) * rstd;
+                const float z = ((to_f(x[i].v[e]) - mean) - c) * rstd;
                 q.v[e] = from_f<T>(rstd * (to_f(y[i].v[e]) * weight(i, e) - u - z * v));
             }
             to[at] = q;
@@ -225,6 +275,32 @@ __global__ void __launch_bounds__(S::threads) norm_grad_kernel(const NormGradPar
     }
 }
 
+// What the statistics' mean of a row is off by (c above), for the sums below: a block a row.
+template <typename T>
+__global__ void __launch_bounds__(256) norm_off_kernel(const NormGradParams p)
+{
+    __shared__ float sums[8];
+    for (int64_t r = blockIdx.x; r < p.f.rows; r += gridDim.x) {
+        const T* x = static_cast<const T*>(p.f.X) + r * p.f.xs;
+        const float mean = p.f.stats[2 * r];
+        if (!off_matters(mean, p.f.stats[2 * r + 1])) {
+            if (threadIdx.x == 0) p.off[r] = 0.f;
+            continue;
+        }
+        float s = 0.f;
+        for (int c = threadIdx.x; c < p.f.D; c += 256) s += to_f(x[c]) - mean;
+#pragma unroll
+        for (int o = 16; o; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = s;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < 8; ++w) s += sums[w];
+            p.off[r] = s / (float)p.f.D;
+        }
+        __syncthreads();
+    }
+}
+
 // Sums over a part of the rows, for rows too long to keep a thread's: a block has 32 columns and 8 rows at a time.
 template <typename T>
 __global__ void __launch_bounds__(256) norm_columns_kernel(const NormGradParams p)
@@ -237,7 +313,7 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormGradParams 
     if (at < D)
         for (int64_t r = r0 + lane; r < r1; r += 8) {
             const float dy = to_f(static_cast<const T*>(p.dY)[r * p.dys + at]), x = to_f(static_cast<const T*>(p.f.X)[r * p.f.xs + at]);
-            w = fmaf(dy, (x - p.f.stats[2 * r]) * p.f.stats[2 * r + 1], w);
+            w = fmaf(dy, ((x - p.f.stats[2 * r]) - p.off[r]) * p.f.stats[2 * r + 1], w);
             b += dy;
         }
     sw[lane][c] = w;
@@ -342,6 +418,11 @@ cudaError_t launch_norm(const NormParams& p, cudaStream_t s, int* launches)
     return cudaGetLastError();
 }
 
+size_t norm_grad_floats(const NormGradParams& p)
+{
+    return 2 * (size_t)(p.parts * p.f.D) + (p.f.D > kWalked ? (size_t)p.f.rows : 0);
+}
+
 void norm_grad_plan(NormGradParams& p)
 {
     if (p.f.D <= kWalked) {
@@ -359,11 +440,17 @@ cudaError_t launch_norm_grad(const NormGradParams& p, cudaStream_t s, int* launc
     cudaError_t e = cudaSuccess;
     if (p.part && p.f.rows && p.f.D > kWalked) {
         // (first: dX may be X or dY)
+        const unsigned rows = (unsigned)blocks_of(p.f, 1, 8);
         const dim3 grid((unsigned)((p.f.D + 31) / 32), (unsigned)p.parts);
-        if (p.f.io == 0) norm_columns_kernel<float><<<grid, 256, 0, s>>>(p);
-        else if (p.f.io == 1) norm_columns_kernel<__half><<<grid, 256, 0, s>>>(p);
-        else norm_columns_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
-        ++*launches;
+        auto sums = [&](auto one) {
+            using T = decltype(one);
+            norm_off_kernel<T><<<rows, 256, 0, s>>>(p);
+            norm_columns_kernel<T><<<grid, 256, 0, s>>>(p);
+        };
+        if (p.f.io == 0) sums(0.f);
+        else if (p.f.io == 1) sums(__half());
+        else sums(__nv_bfloat16());
+        *launches += 2;
     }
     if (p.f.rows && (p.dX || (p.part && p.f.D <= kWalked))) {
         by_type(p.f, &p, s);

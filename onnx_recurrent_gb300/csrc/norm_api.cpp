@@ -157,12 +157,13 @@ rnn_status rnn_layer_norm_grad(rnn_norm_t pl, const rnn_norm_grad_args* a)
     q.dbias = a->dbias;
     if (!q.dX && !q.dW && !q.dbias) return RNN_OK;
     norm_grad_plan(q);
-    const size_t bytes = q.dW || q.dbias ? sizeof(float) * 2 * (size_t)(q.parts * pl->D) : 0;
+    const size_t bytes = q.dW || q.dbias ? sizeof(float) * norm_grad_floats(q) : 0;
     cudaStream_t st = (cudaStream_t)a->stream;
     char* scratch = nullptr;
     rs = claim_scratch(pl, bytes, st, &scratch);
     if (rs != RNN_OK) return rs;
     q.part = (float*)scratch;
+    q.off = q.part + 2 * q.parts * pl->D;
     cudaError_t e = launch_norm_grad(q, st, &pl->launches);
     if (e != cudaSuccess) return cuda_fail(e, "normalisation gradient launch");
     return release_scratch(pl, bytes, st);

@@ -31,6 +31,7 @@ struct NormGradParams {
     float *dW, *dbias;
     float* part;            // [parts][2][D]
     int64_t parts;          // norm_grad_plan
+    float* off;             // [rows], behind the parts (norm_grad_floats): for rows too long to keep a thread's sums
 };
 
 struct BeamSelectParams {
@@ -66,6 +67,7 @@ struct ReorderParams {
 };
 
 void norm_grad_plan(NormGradParams& p);
+size_t norm_grad_floats(const NormGradParams& p);      // of scratch, where dW or dbias is wanted
 cudaError_t launch_norm(const NormParams& p, cudaStream_t s, int* launches);
 cudaError_t launch_norm_grad(const NormGradParams& p, cudaStream_t s, int* launches);
 cudaError_t launch_beam_select(const BeamSelectParams& p, cudaStream_t s, int* launches);
