@@ -657,9 +657,11 @@ rnn_status rnn_scores_grad(const rnn_scores_grad_args* args);
  * states given as the same memory.
  *
  * Runs and gradients take 64 steps at a time, as products of matrices whose
- * fp32 operands are the sum of two fp16 numbers over a power of two (22 bits of
- * a row's largest value; what a run saves, of the largest of 128 values'
- * rows): errors are those of fp32 sums, within a small factor.  An infinity or a NaN in an
+ * fp32 operands are the sum of two fp16 numbers over a power of two: 22 bits of
+ * every value down to 2^-17 of the largest of its row (of 64 steps or 128 keys; in
+ * what a run and its gradient keep, of 64 steps or keys by 128 values), one fewer for each power of two below, and
+ * nothing below 2^-40.  Errors are those of fp32 sums, within a small factor, for
+ * steps, keys and values that do not differ by more.  An infinity or a NaN in an
  * input is found again in every output that depends on it, and may be in those of
  * the other steps, too, that are among the same 64 of its row and head; other rows
  * and heads keep theirs.  A call takes 2 launches (4 where few heads have many

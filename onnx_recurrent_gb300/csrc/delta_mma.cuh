@@ -2,12 +2,15 @@
 // fp16 parts, tensor memory, and waits that end.
 //
 // An fp32 operand x is taken as two fp16 parts, hi = fp16(x / s) and lo = fp16(x / s - hi), with s
-// a power of two just above the largest |x| of its row: hi + lo has 22 bits, and
-// what a value far below its row's largest loses is below 2^-24 of that.  A product of two such operands is
+// a power of two that brings the largest |x| of its row to between 2^14 and 2^15: nearly all of fp16's exponents then lie
+// below it.  hi + lo has 22 bits (off by 2^-23 of x at most) of every value down to 2^-17 of the row's power of two, and what a smaller one
+// loses is below 2^-40 of that.  (With the largest at 1, that floor was 2^-25: a step whose slopes are a millionth of its
+// neighbours' kept five bits of them.)  A product of two such operands is
 // hi lo + lo hi + hi hi (what is left out is below 2^-22 of it), summed in fp32 in this order: every instruction of 16
 // products rounds its sum towards zero, so the large ones come last (first, results were off by twice as much).  Scales are applied
 // exactly, to a row of the result or, along the sum, to the other operand.  16-bit inputs are one part:
-// fp16 values, and bf16 values over their row's power of two, have no second.
+// bf16 values down to 2^-32 of their row's power of two have no second, nor have fp16 values, but for subnormal ones beside
+// 2^15 or more.
 #pragma once
 
 #include <type_traits>
@@ -23,14 +26,15 @@ constexpr unsigned kBlock = 8192;            // 64 rows of 64 fp16 values, 128-b
 // Byte of element c of row r in a 64-row block (c < 64).
 __device__ __forceinline__ unsigned swizzled(int r, int c) { return (unsigned)(r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2); }
 
-// A power of two above |m| (within a factor of 2), and one over it; 1 for 0, and both stay ordinary numbers.
+// The power of two s of a row whose largest is m, |m| / s below 2^15, and one over it; 1 for 0, and both stay ordinary numbers.
 struct Scale {
     float up, down;
 };
+constexpr int kTop = 15;
 __device__ __forceinline__ Scale scale_of(float m)
 {
-    int e = (int)((__float_as_uint(m) >> 23) & 255u) + 1;       // biased exponent of the power
-    e = m == 0.f ? 127 : e < 2 ? 2 : e > 252 ? 252 : e;
+    int e = (int)((__float_as_uint(m) >> 23) & 255u) + 1 - kTop;        // biased exponent of s
+    e = m == 0.f ? 127 : e < 2 ? 2 : e;                                  // (at most 241)
     return Scale{__uint_as_float((unsigned)e << 23), __uint_as_float((unsigned)(254 - e) << 23)};
 }
 
@@ -158,20 +162,19 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const unsigned* r)
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 32 values of a row over its scale, |v| down < 1, as parts: 16 columns of hi at `hi`, 16 of lo at `lo`.  hi is rounded to
-// a multiple of 2^-11 (in the last place of 1.5 2^12), which fp16 holds exactly, so pairs of values
-// take three packed operations and two conversions; lo is then off by 2^-25 at most.
+// 32 values of a row over its scale as parts: 16 columns of hi at `hi`, 16 of lo at `lo`.
 __device__ __forceinline__ void put_parts(uint32_t hi, uint32_t lo, const f2* v, float down)
 {
     unsigned h[16], l[16];
-    const f2 d = dup2(down), m = dup2(6144.f), mm = dup2(-6144.f), minus = dup2(-1.f);
+    const f2 d = dup2(down), minus = dup2(-1.f);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        const f2 a = add2(fma2(v[i], d, m), mm);
+        const f2 a = mul2(v[i], d);
         float x, y;
         unpack2(a, x, y);
         h[i] = half_pair(x, y);
-        unpack2(fma2(v[i], d, mul2(a, minus)), x, y);
+        const float2 b = pair_value(h[i]);
+        unpack2(fma2(pack2(b.x, b.y), minus, a), x, y);
         l[i] = half_pair(x, y);
     }
     tmem_st16(hi, h);

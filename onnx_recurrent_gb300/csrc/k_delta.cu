@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 3) delta_prep_kernel(const DeltaPara
             for (int e = 0; e < 2; ++e) {
                 const int j = j8 * 8 + lane % 4 * 2 + e;
                 const bool in = j < i || (j == i && warp >= 4);
-                const float v = in ? s.sums.power(i, j) * (c[j8][half * 2 + e] * (er[i] * s.ek[j])) : 0.f;
+                const float v = in ? s.sums.power(i, j) * (c[j8][half * 2 + e] * er[i] * s.ek[j]) : 0.f;
                 if (warp < 4 && in) s.A[i][j] = s.beta[i] * v;
                 c[j8][half * 2 + e] = v;
                 m = fmaxf(m, fabsf(v));

@@ -686,7 +686,7 @@ __global__ void __launch_bounds__(kRestThreads, 1) delta_grad_rest_kernel(const 
                     const bool in = upper ? j < i : j <= i;
                     const float decay = in ? sums.power(i, j) : 0.f;
                     const float d = in ? e[c] * mine * decay : 0.f;
-                    const float k = in ? kq[c] * (es * fac[kKeyScale + j]) : 0.f;
+                    const float k = in ? kq[c] * es * fac[kKeyScale + j] : 0.f;
                     const float v = upper ? b_i * d : d;
                     s = fmaf(d, k, s);
                     e[c] = v;
