@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 3) delta_prep_kernel(const DeltaPara
         s.fac[kQuery + tid] = p.scale * first * s.eq[tid];
         s.fac[kKeyScale + tid] = s.ek[tid];
         s.fac[kQueryScale + tid] = s.eq[tid];
-        if (tid == C - 1) s.fac[kWhole] = first;
+        if (tid == C - 1) s.fac[kWhole] = s.sums.whole();
     }
     __syncthreads();
     if (tid < C) {

@@ -71,3 +71,34 @@ def test_slopes_of_very_different_steps(up, io):
 def test_values_and_betas_of_very_different_sizes(io):
     Case(2, 150, 2, 1, 24, 40, io, columns=10.0 ** -(torch.arange(40) % 6).float()).check(64)
     Case(2, 150, 2, 1, 24, 40, io, betas=10.0 ** -(torch.arange(150) % 7).float()).check(64)
+
+
+def test_slow_decays_over_many_chunks():
+    """Nothing but decays (betas of 0) over 16384 steps: each of 256 chunks rounds its decay, a product and a sum.  Roundings of
+    at most u that err to both sides alike have a root mean square of u / sqrt(3), so 768 of them add up to 16 u; five times that for
+    the worst of 80 heads."""
+    N, S, H, D = 40, 16384, 2, 4
+    g = torch.Generator(device="cuda").manual_seed(0)
+    r = lambda *s: torch.rand(*s, generator=g, device="cuda")  # noqa: E731
+    rate = torch.linspace(5e-5, 3e-4, N * H, device="cuda").view(N, 1, H)
+    decay, state = -rate * (0.5 + r(N, S, H)), 1 + r(N, H, D, D)
+    k, v = r(N, S, H, D), r(N, S, H, D)
+    plan = orc.rnn_delta_create(H, D, D, layout=1)
+    end = orc.delta_rule(plan, k, k, v, decay, torch.zeros_like(decay), None, state)[1]
+    off = end.double() / (state.double() * decay.double().sum(1).exp()[..., None, None]) - 1
+    assert float(off.mean((-1, -2)).abs().max()) <= 80 * U
+
+
+def test_slow_decays_over_many_tokens():
+    """The same a token at a time: 1500 tokens round a decay and a product each, 32 u; five times that for the worst of 64 heads."""
+    N, S, H, D = 32, 1500, 2, 8
+    g = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *s: torch.rand(*s, generator=g, device="cuda")  # noqa: E731
+    decay, state = -(0.003 + 0.003 * r(S, N, H)), 1 + r(N, H, D, D)
+    want = state.double() * decay.double().sum(0).exp()[..., None, None]
+    plan, x, Y = orc.rnn_delta_create(H, D, D), r(N, H, D), torch.empty(N, H, D, device="cuda")
+    beta = torch.zeros(N, H, device="cuda")
+    for t in range(S):
+        orc.rnn_delta_step(plan, x, x, x, decay[t], beta, state, Y)
+    off = state.double() / want - 1
+    assert float(off.mean((-1, -2)).abs().max()) <= 160 * U
