@@ -782,9 +782,11 @@ rnn_status rnn_layer_norm_grad(rnn_norm_t plan, const rnn_norm_grad_args* args);
  * the beam's exponentials).  A beam that is finished has one candidate, end_id,
  * with its score as it is, and V - 1 of -inf.  The B best of an item's B * V
  * candidates, best first, ties to the lowest b and then the lowest v, are the new beams.  A
- * logit of -inf is a candidate of -inf, and so is every candidate that is a NaN (a row
- * with a NaN or +inf is all of that).  Scores are added and compared in more than
- * fp32, and rounded once to it.
+ * logit of -inf is a candidate of -inf, and so is every candidate of a row with a NaN or +inf
+ * and of a beam whose score is not finite (finished or not; a score of +inf is no log
+ * probability).  Scores are added and compared in more than
+ * fp32, and rounded once to it; lse, whose exponentials are fp32, is off by some 10^-7, and beams whose candidates lie closer may change
+ * places.
  *
  * rnn_beam_reorder then gives every beam its parent's states: row n * B + b of
  * each tensor becomes row n * B + parents[n,b].  With slots, row r is at

@@ -30,3 +30,17 @@ def test_a_row_of_a_masks_lowest_value_is_uniform(io, V):
     u = math.log(V)
     want = torch.tensor([[-1.0, -2.0, -u], [-1.0 - u] * 3], dtype=torch.float64)
     assert ((step.scores.cpu().double() - want).abs() <= 2.0 ** -24 * want.abs() + 1e-12).all()
+
+
+def test_beams_whose_score_is_not_finite_have_no_candidates():
+    B, V = 4, 30
+    plan = orc.rnn_beam_create(B, end_id=3)
+    x = torch.randn(B, V)
+    scores = torch.tensor([[float("inf"), -1.0, float("nan"), float("inf")]])
+    done = torch.tensor([[False, False, True, True]])
+    step = orc.beam_select(plan, x.cuda(), scores.cuda(), done.cuda())
+    assert step.parents.tolist() == [[1] * 4]
+    assert step.ids[0].tolist() == x[1].topk(4).indices.tolist()
+    x[1] = NEG              # all are -inf: the lowest beam's lowest tokens
+    step = orc.beam_select(plan, x.cuda(), scores.cuda(), done.cuda())
+    assert step.parents.tolist() == [[0] * 4] and step.ids.tolist() == [[0, 1, 2, 3]] and (step.scores == NEG).all()
