@@ -653,8 +653,8 @@ rnn_status rnn_scores_grad(const rnn_scores_grad_args* args);
  * once; g, beta, states and their gradients are fp32, and so are all sums.
  * Views, streams, scratch, captured calls, in-place states and lengths or slots out of
  * range are as with rnn_ssm_*; a view's innermost part is [HK, DK] (Q, K),
- * [H, DV] (V, Y) or [H] (g, beta).  Outputs must not overlap inputs, but for
- * states given as the same memory.
+ * [H, DV] (V, Y) or [H] (g, beta).  Outputs must not overlap inputs or one another, but for
+ * states given as the same memory (what is sure to overlap is refused).
  *
  * Runs and gradients take 64 steps at a time, as products of matrices whose
  * fp32 operands are the sum of two fp16 numbers over a power of two: 22 bits of

@@ -83,6 +83,83 @@ rnn_status check_apart(int64_t S, int64_t N, const OutView (&views)[K])
     return RNN_OK;
 }
 
+// A call's array: S steps of N rows of `inner` elements (a state or another dense array: one of each).
+struct Laid {
+    const void* data;
+    int64_t ss, bs, S, N, inner;
+    int64_t elem;
+    const char* name;
+};
+Laid laid(const View& v, int64_t S, int64_t N, int64_t inner, size_t elem, const char* name)
+{
+    return Laid{v.data, v.ss, v.bs, S, N, inner, (int64_t)elem, name};
+}
+Laid laid(const void* p, int64_t count, const char* name) { return Laid{p, 0, 0, 1, 1, count, 4, name}; }
+
+// Whether two arrays are certain to share memory.  Arrays without gaps are told apart from any other one, and others from those of
+// the same strides (parts of wider rows, side by side); of the rest nothing is said.
+using wide = __int128;
+struct Nested {             // an array's strides and counts, the wider stride first, in bytes
+    wide far, near, inner;
+    int64_t fars, nears;
+};
+Nested nested(const Laid& x)
+{
+    const bool rows_far = x.bs > x.ss;
+    return Nested{(wide)(rows_far ? x.bs : x.ss) * x.elem, (wide)(rows_far ? x.ss : x.bs) * x.elem, (wide)x.inner * x.elem,
+                  rows_far ? x.N : x.S, rows_far ? x.S : x.N};
+}
+// Whether any of off + i stride, lo <= i <= hi, that lies between -left and right is what is looked for.
+template <typename F>
+bool any_between(wide off, wide stride, int64_t lo, int64_t hi, wide left, wide right, F&& found)
+{
+    if (stride == 0) lo = hi = 0;
+    wide i = stride == 0 ? 0 : (-left - off) / stride - 1;
+    if (i < lo) i = lo;
+    for (int tries = 0; tries < 8 && i <= hi && off + i * stride < right; ++i)
+        if (off + i * stride > -left) {
+            ++tries;
+            if (found(off + i * stride)) return true;
+        }
+    return false;
+}
+// Whether a block of `len` bytes meets items of b that begin `off` from it, or (both) that many strides before.
+bool block_meets(wide off, wide len, const Nested& b, bool both)
+{
+    return any_between(off, b.far, both ? 1 - b.fars : 0, b.fars - 1, b.near * (b.nears - 1) + b.inner, len + (both ? b.near * (b.nears - 1) : 0),
+                       [&](wide o) { return any_between(o, b.near, both ? 1 - b.nears : 0, b.nears - 1, b.inner, len, [](wide) { return true; }); });
+}
+bool share(const Laid& a, const Laid& b)
+{
+    auto empty = [](const Laid& x) { return !x.data || x.S < 1 || x.N < 1 || x.inner < 1; };
+    if (empty(a) || empty(b)) return false;
+    const Nested na = nested(a), nb = nested(b);
+    auto span = [](const Nested& x) { return x.far * (x.fars - 1) + x.near * (x.nears - 1) + x.inner; };
+    const wide off = (wide)(uintptr_t)b.data - (wide)(uintptr_t)a.data;
+    if (off >= span(na) || -off >= span(nb)) return false;
+    auto gapless = [](const Nested& x) {
+        return (x.nears == 1 || x.near <= x.inner) && (x.fars == 1 || x.far <= x.near * (x.nears - 1) + x.inner);
+    };
+    if (gapless(na)) return block_meets(off, span(na), nb, false);
+    if (gapless(nb)) return block_meets(-off, span(nb), na, false);
+    if (a.S != b.S || a.N != b.N || (a.S > 1 && a.ss * a.elem != b.ss * b.elem) || (a.N > 1 && a.bs * a.elem != b.bs * b.elem)) return false;
+    return block_meets(off, na.inner, nb, true);
+}
+
+// Outputs lie on no input and on no other output.  The first of either is a state and where it goes, which may be the same
+// memory (check_in_place).
+template <int I, int O>
+rnn_status check_shared(const Laid (&in)[I], const Laid (&out)[O])
+{
+    for (int o = 0; o < O; ++o) {
+        for (int i = 0; i < I; ++i)
+            if (!(o == 0 && i == 0) && share(out[o], in[i])) return fail(RNN_ERR_INVALID_ARGUMENT, "%s overlaps %s", out[o].name, in[i].name);
+        for (int i = 0; i < o; ++i)
+            if (share(out[o], out[i])) return fail(RNN_ERR_INVALID_ARGUMENT, "%s overlaps %s", out[o].name, out[i].name);
+    }
+    return RNN_OK;
+}
+
 DeltaParams params(const rnn_delta* pl, int64_t S, int64_t N)
 {
     DeltaParams p{};
@@ -93,9 +170,7 @@ DeltaParams params(const rnn_delta* pl, int64_t S, int64_t N)
     p.DK = pl->DK;
     p.DV = pl->DV;
     p.io = pl->io;
-    p.sms = pl->sms;
     p.scale = pl->scale;
-    p.status = pl->status;
     return p;
 }
 
@@ -192,7 +267,6 @@ rnn_status rnn_delta_rule(rnn_delta_t pl, const rnn_delta_args* a)
     const size_t states = sizeof(float) * (size_t)(N * dv * pl->DK);
     // the same memory: the block that writes a part of a state has read it
     if (rs == RNN_OK) rs = check_in_place(a->initial_state, a->final_state, states, "initial_state and final_state");
-    if (rs == RNN_OK) rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
     DeltaParams p = params(pl, S, N);
     p.Q = dense(a->Q, pl, S, N, dk);
@@ -201,6 +275,15 @@ rnn_status rnn_delta_rule(rnn_delta_t pl, const rnn_delta_args* a)
     p.g = dense(a->g, pl, S, N, pl->H);
     p.beta = dense(a->beta, pl, S, N, pl->H);
     p.Y = Y;
+    const int64_t saved = a->saved ? delta_saved_floats(S, N, p.H, p.HK, p.DK, p.DV, p.io) : 0;
+    rs = check_shared({laid(a->initial_state, N * dv * pl->DK, "initial_state"), laid(p.Q, S, N, dk, e, "Q"), laid(p.K, S, N, dk, e, "K"),
+                       laid(p.V, S, N, dv, e, "V"), laid(p.g, S, N, pl->H, 4, "g"), laid(p.beta, S, N, pl->H, 4, "beta"),
+                       laid(a->sequence_lens, N, "sequence_lens")},
+                      {laid(a->final_state, N * dv * pl->DK, "final_state"), laid(Y, S, N, dv, e, "Y"), laid(a->saved, saved, "saved")});
+    if (rs == RNN_OK) rs = ensure_status(pl);
+    if (rs != RNN_OK) return rs;
+    p.sms = pl->sms;
+    p.status = pl->status;
     p.lens = a->sequence_lens;
     p.h0 = a->initial_state;
     p.hT = a->final_state;
@@ -245,7 +328,6 @@ rnn_status rnn_delta_rule_grad(rnn_delta_t pl, const rnn_delta_grad_args* a)
     rs = check_apart(S, N, {{q.dQ, dk, "dQ"}, {q.dK, dk, "dK"}, {q.dV, dv, "dV"}, {q.dg, H, "dg"}, {q.dbeta, H, "dbeta"}});
     const size_t states = sizeof(float) * (size_t)(N * dv * pl->DK);
     if (rs == RNN_OK) rs = check_in_place(a->d_final_state, a->d_initial_state, states, "d_final_state and d_initial_state");
-    if (rs == RNN_OK) rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
     q.f = params(pl, S, N);
     q.f.Q = dense(a->Q, pl, S, N, dk);
@@ -258,6 +340,16 @@ rnn_status rnn_delta_rule_grad(rnn_delta_t pl, const rnn_delta_grad_args* a)
     q.dY = dense(a->dY, pl, S, N, dv);
     q.dhT = a->d_final_state;
     q.dh0 = a->d_initial_state;
+    const int64_t saved = steps ? delta_saved_floats(S, N, H, pl->HK, pl->DK, pl->DV, pl->io) : 0;
+    rs = check_shared({laid(a->d_final_state, N * dv * pl->DK, "d_final_state"), laid(q.dY, S, N, dv, e, "dY"), laid(q.f.Q, S, N, dk, e, "Q"),
+                       laid(q.f.K, S, N, dk, e, "K"), laid(q.f.V, S, N, dv, e, "V"), laid(q.f.g, S, N, H, 4, "g"),
+                       laid(q.f.beta, S, N, H, 4, "beta"), laid(a->sequence_lens, N, "sequence_lens"), laid(a->saved, saved, "saved")},
+                      {laid(a->d_initial_state, N * dv * pl->DK, "d_initial_state"), laid(q.dQ, S, N, dk, e, "dQ"), laid(q.dK, S, N, dk, e, "dK"),
+                       laid(q.dV, S, N, dv, e, "dV"), laid(q.dg, S, N, H, 4, "dg"), laid(q.dbeta, S, N, H, 4, "dbeta")});
+    if (rs == RNN_OK) rs = ensure_status(pl);
+    if (rs != RNN_OK) return rs;
+    q.f.sms = pl->sms;
+    q.f.status = pl->status;
     cudaStream_t st = (cudaStream_t)a->stream;
     const size_t bytes = (size_t)delta_slopes_bytes(S, N, H, pl->DK, pl->DV, pl->io);
     char* scratch = nullptr;
@@ -287,7 +379,6 @@ rnn_status rnn_delta_step(rnn_delta_t pl, const rnn_delta_step_args* a)
     if (rs == RNN_OK) rs = check_in_place(a->state, a->state_out, states, "state and state_out");
     const View Y = dense_row(a->Y, dv);
     if (rs == RNN_OK) rs = check_outputs(1, a->batch_size, {{Y, dv, "Y"}});
-    if (rs == RNN_OK) rs = ensure_status(pl);
     if (rs != RNN_OK) return rs;
     DeltaStepParams p{};
     p.N = a->batch_size;
@@ -297,7 +388,6 @@ rnn_status rnn_delta_step(rnn_delta_t pl, const rnn_delta_step_args* a)
     p.DK = pl->DK;
     p.DV = pl->DV;
     p.io = pl->io;
-    p.sms = pl->sms;
     p.scale = pl->scale;
     p.Q = dense_row(a->Q, dk);
     p.K = dense_row(a->K, dk);
@@ -308,6 +398,13 @@ rnn_status rnn_delta_step(rnn_delta_t pl, const rnn_delta_step_args* a)
     p.state = a->state;
     p.state_out = a->state_out;
     p.slots = a->slots;
+    const int64_t N = a->batch_size, values = (a->slots ? a->n_slots : N) * dv * pl->DK;
+    rs = check_shared({laid(a->state, values, "state"), laid(p.Q, 1, N, dk, e, "Q"), laid(p.K, 1, N, dk, e, "K"), laid(p.V, 1, N, dv, e, "V"),
+                       laid(p.g, 1, N, p.H, 4, "g"), laid(p.beta, 1, N, p.H, 4, "beta"), laid(a->slots, N, "slots")},
+                      {laid(a->state_out, values, "state_out"), laid(Y, 1, N, dv, e, "Y")});
+    if (rs == RNN_OK) rs = ensure_status(pl);
+    if (rs != RNN_OK) return rs;
+    p.sms = pl->sms;
     p.status = pl->status;
     cudaError_t err = launch_delta_step(p, (cudaStream_t)a->stream, &pl->launches);
     return err == cudaSuccess ? RNN_OK : cuda_fail(err, "delta rule step launch");
