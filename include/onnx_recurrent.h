@@ -735,7 +735,8 @@ rnn_status rnn_delta_step(rnn_delta_t plan, const rnn_delta_step_args* args);
 /* ------------------------------------------------ layer normalisation
  * Rows x[D]: Y = (x - mean) * rstd * W + bias with mean the row's mean and
  * rstd = 1 / sqrt(mean of (x - mean)^2 + eps), and its gradients.  X, Y, dY
- * and dX are stored in the plan's io type (rows row_stride elements apart, 0: D);
+ * and dX are stored in the plan's io type (rows row_stride elements apart, 0: D, and RNN_SHARED_ROW for X and dY:
+ * every row is the same one);
  * W, bias, their gradients and the rows' statistics are fp32, as are all sums.
  * A row with a NaN or an infinity is NaN throughout.  Streams, scratch and captured
  * calls are as with rnn_ssm_*. */

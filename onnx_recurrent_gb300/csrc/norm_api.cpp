@@ -14,11 +14,12 @@ struct rnn_norm : PlanMemory {
 
 namespace {
 
-// Rows of D values: *stride in elements.  Output rows must lie apart.
+// Rows of D values: *stride in elements.  Output rows must lie apart; an input's may all be one.
 rnn_status check_rows(const rnn_norm* pl, const void* data, int64_t rows, int64_t* stride, const char* name, bool out)
 {
-    if (*stride < 0) return fail(RNN_ERR_INVALID_ARGUMENT, "%s has a negative stride", name);
-    if (*stride == 0) *stride = pl->D;
+    const bool one = !out && *stride == RNN_SHARED_ROW;
+    if (*stride < 0 && !one) return fail(RNN_ERR_INVALID_ARGUMENT, "%s has a negative stride", name);
+    *stride = one ? 0 : *stride == 0 ? pl->D : *stride;
     if (out && data && rows > 1 && *stride < pl->D) return fail(RNN_ERR_INVALID_ARGUMENT, "%s: its rows share memory", name);
     if ((uintptr_t)data % element(pl->io)) return fail(RNN_ERR_INVALID_ARGUMENT, "%s is not aligned to its elements", name);
     return RNN_OK;

@@ -8,7 +8,7 @@ import struct
 
 from . import ssm as _ssm
 from .rnn import IO_TYPES, _check
-from .ssm import _bad, _call, _dense, _device, _handle, _onto
+from .ssm import _SHARED_ROW, _bad, _call, _dense, _device, _handle, _onto
 
 _lib = None
 torch = _f32 = None
@@ -74,8 +74,8 @@ def rnn_norm_last_launch_count(plan: Norm) -> int:
     return int(_load().rnn_norm_last_launch_count(plan.handle))
 
 
-def _rows(plan, t, name, shape, dev):
-    """(address, row stride) of a [..., size] tensor whose rows are dense and evenly apart."""
+def _rows(plan, t, name, shape, dev, out=False):
+    """(address, row stride) of a [..., size] tensor whose rows are dense and evenly apart; an input's may all be one."""
     if t is None:
         return 0, 0
     if t.dtype is not plan.dtype or t.get_device() != dev or t.shape != shape:
@@ -95,7 +95,9 @@ def _rows(plan, t, name, shape, dev):
             raise ValueError(f"{name}: rows must be evenly apart")
         count *= size[i]
     if stride == 0:
-        raise ValueError(f"{name}: rows must not share memory")
+        if out:
+            raise ValueError(f"{name}: rows must not share memory")
+        stride = _SHARED_ROW
     return t.data_ptr(), stride or 0
 
 
@@ -111,7 +113,7 @@ def rnn_layer_norm(plan: Norm, X, W=None, bias=None, Y=None, stats=None, stream=
     rows, d, shape = _count(plan, X), (plan.size,), X.shape
     args = struct.pack(
         "9q", rows, *_rows(plan, X, "X", shape, dev), _dense(W, d, _f32, dev, "W"), _dense(bias, d, _f32, dev, "bias"),
-        *_rows(plan, Y, "Y", shape, dev), _dense(stats, (rows, 2), _f32, dev, "stats"),
+        *_rows(plan, Y, "Y", shape, dev, True), _dense(stats, (rows, 2), _f32, dev, "stats"),
         _ssm._raw_stream(dev) if stream is None else _handle(stream))
     _call(dev, _lib.rnn_layer_norm, plan.handle, args)
 
@@ -132,7 +134,7 @@ def rnn_layer_norm_grad(plan: Norm, dY, X, stats, W=None, dX=None, dW=None, dbia
     rows, d = _count(plan, X), (plan.size,)
     args = struct.pack(
         "12q", rows, *_rows(plan, dY, "dY", X.shape, dev), *_rows(plan, X, "X", X.shape, dev),
-        _dense(stats, (rows, 2), _f32, dev, "stats"), _dense(W, d, _f32, dev, "W"), *_rows(plan, dX, "dX", X.shape, dev),
+        _dense(stats, (rows, 2), _f32, dev, "stats"), _dense(W, d, _f32, dev, "W"), *_rows(plan, dX, "dX", X.shape, dev, True),
         _dense(dW, d, _f32, dev, "dW"), _dense(dbias, d, _f32, dev, "dbias"),
         _ssm._raw_stream(dev) if stream is None else _handle(stream))
     _call(dev, _lib.rnn_layer_norm_grad, plan.handle, args)

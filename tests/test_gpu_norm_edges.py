@@ -113,3 +113,22 @@ def test_many_rows_in_place_and_of_wider_rows():
         assert ((X - want).abs() <= 200 * U * (1 + want.abs())).all()
         keep[:, D + off:2 * D + off] = X
         assert torch.equal(big, keep)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [96, 8200])
+def test_inputs_whose_rows_are_one(D, io):
+    X, W, b, dY = _inputs(1, D, io)
+    plan = orc.rnn_norm_create(D)
+    orc.rnn_norm_set_io_type(plan, io)
+    many = X.expand(50, D)
+    want, stats = orc.layer_norm(plan, many.contiguous(), W, b)
+    Y, st = orc.layer_norm(plan, many, W, b)
+    assert torch.equal(Y, want) and torch.equal(st, stats)
+    slopes = dY.expand(5, 10, D)
+    full = orc.layer_norm_grad(plan, slopes.reshape(50, D).contiguous(), many.contiguous(), stats, W, b)
+    out = orc.layer_norm_grad(plan, slopes, X.expand(5, 10, D), stats, W, b)
+    for name in full:
+        assert torch.equal(out[name].view_as(full[name]), full[name]), name
+    with pytest.raises(ValueError):
+        orc.rnn_layer_norm(plan, many, W, b, many)
