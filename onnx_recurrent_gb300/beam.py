@@ -127,8 +127,8 @@ def rnn_beam_reorder(plan: BeamPlan, parents, tensors, outs=None, slots=None, st
     fields, n_slots = [], 0
     for i, t in enumerate(tensors):
         o = t if outs is None else outs[i]
-        if i == 0:
-            n_slots = t.shape[0] if slots is not None else 0
+        if i == 0 and slots is not None and t.dim():
+            n_slots = t.shape[0]
         count = rows if slots is None else n_slots
         if t.dim() < 1 or t.shape[0] != count:
             raise ValueError(f"a tensor has shape {tuple(t.shape)}, expected {count} rows")

@@ -108,3 +108,11 @@ def test_a_row_shared_by_beams_and_cut_in_parts(V, io):
     wide = orc.beam_select(plan, x.repeat_interleave(B, 0).cuda(), scores.cuda())
     one = orc.beam_select(plan, x.cuda(), scores.cuda())
     assert torch.equal(one.ids, wide.ids) and torch.equal(one.parents, wide.parents)
+
+
+def test_a_tensor_without_rows_is_refused():
+    plan = orc.rnn_beam_create(2)
+    parents, slots = torch.zeros(1, 2, dtype=torch.int32, device="cuda"), torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    for kw in (dict(), dict(slots=slots)):
+        with pytest.raises(ValueError):
+            orc.rnn_beam_reorder(plan, parents, [torch.zeros((), device="cuda")], **kw)
