@@ -130,6 +130,9 @@ __global__ void __launch_bounds__(S::threads, S::NV == 8 || (S::NV == 32 && S::V
         load_weights<S>(b, p.bias, p.D, t, 0.f);
     }
     const bool wide = ((uintptr_t)p.W | (uintptr_t)p.bias) % 16 == 0;
+    // (32 values a thread leave no register for it: they divide)
+    const float per = 1.f / (float)p.D;
+    auto over_d = [&](float v) { return S::weights ? v * per : v / (float)p.D; };
     for (int64_t r0 = (int64_t)blockIdx.x * S::groups; r0 < p.rows; r0 += (int64_t)gridDim.x * S::groups) {
         const int64_t r = r0 + group;
         const bool in = r < p.rows;
@@ -144,7 +147,7 @@ __global__ void __launch_bounds__(S::threads, S::NV == 8 || (S::NV == 32 && S::V
 #pragma unroll
             for (int e = 0; e < S::VEC; ++e) s[0] += to_f(x[i].v[e]);
         row_sums<S>(s, sums);
-        const float mean = s[0] / (float)p.D;
+        const float mean = over_d(s[0]);
         float left[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < S::PER; ++i)
@@ -157,8 +160,8 @@ __global__ void __launch_bounds__(S::threads, S::NV == 8 || (S::NV == 32 && S::V
                 }
         row_sums<S>(left, more);
         if (!in) continue;
-        const float c = left[0] / (float)p.D, var = left[1] / (float)p.D - c * c;
-        const float rstd = 1.f / sqrtf((var < 0.f ? 0.f : var) + p.eps);      // (a NaN stays)
+        const float c = over_d(left[0]), var = over_d(left[1]) - c * c;
+        const float rstd = 1.f / sqrtf((var < 0.f ? 0.f : var) + p.eps), off = -c * rstd;      // (a NaN stays)
         if (p.stats && t == 0) {
             p.stats[2 * r] = mean + c;
             p.stats[2 * r + 1] = rstd;
@@ -177,7 +180,7 @@ __global__ void __launch_bounds__(S::threads, S::NV == 8 || (S::NV == 32 && S::V
 #pragma unroll
             for (int e = 0; e < S::VEC; ++e) {
                 if constexpr (S::weights) pw[e] = w[i * S::VEC + e], pb[e] = b[i * S::VEC + e];
-                q.v[e] = from_f<T>(fmaf(((to_f(x[i].v[e]) - mean) - c) * rstd, pw[e], pb[e]));
+                q.v[e] = from_f<T>(fmaf(fmaf(to_f(x[i].v[e]) - mean, rstd, off), pw[e], pb[e]));
             }
             to[at] = q;
         }
@@ -216,7 +219,7 @@ __global__ void __launch_bounds__(S::threads, S::NV == 8 ? 4 : S::NV == 16 && S:
                 x[i] = fx[i * S::TPR + t];
                 y[i] = fy[i * S::TPR + t];
             }
-        float c = 0.f;
+        float left = 0.f;       // -c rstd
         if (off_matters(mean, rstd)) {      // (all of a row's threads, which meet here)
             float s[1] = {0.f};
 #pragma unroll
@@ -226,14 +229,14 @@ __global__ void __launch_bounds__(S::threads, S::NV == 8 ? 4 : S::NV == 16 && S:
                     for (int e = 0; e < S::VEC; ++e) s[0] += to_f(x[i].v[e]) - mean;
             row_sums<S>(s, offs[found]);
             found ^= 1;
-            c = s[0] * per;
+            left = -(s[0] * per) * rstd;
         }
         float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < S::PER; ++i)
 #pragma unroll
             for (int e = 0; e < S::VEC; ++e) {      // (past the row's end dY is 0)
-                const float z = ((to_f(x[i].v[e]) - mean) - c) * rstd, d = to_f(y[i].v[e]), g = d * weight(i, e);
+                const float z = fmaf(to_f(x[i].v[e]) - mean, rstd, left), d = to_f(y[i].v[e]), g = d * weight(i, e);
                 s[0] += g;
                 s[1] = fmaf(g, z, s[1]);
                 if constexpr (SUMS) {
@@ -253,7 +256,7 @@ __global__ void __launch_bounds__(S::threads, S::NV == 8 ? 4 : S::NV == 16 && S:
             P q;
 #pragma unroll
             for (int e = 0; e < S::VEC; ++e) {
-                const float z = ((to_f(x[i].v[e]) - mean) - c) * rstd;
+                const float z = fmaf(to_f(x[i].v[e]) - mean, rstd, left);
                 q.v[e] = from_f<T>(rstd * (to_f(y[i].v[e]) * weight(i, e) - u - z * v));
             }
             to[at] = q;
