@@ -793,7 +793,9 @@ rnn_status rnn_layer_norm_grad(rnn_norm_t plan, const rnn_norm_grad_args* args);
  * each tensor becomes row n * B + parents[n,b].  With slots, row r is at
  * slots[r] (slots of a call must differ; -1: no row, which no beam may have for a
  * parent).  A parent outside [0, B) or a slot outside its range is found by the kernel: that
- * row is left as it was, and rnn_beam_sync reports RNN_ERR_INVALID_INPUT.
+ * row is left as it was, and rnn_beam_sync reports RNN_ERR_INVALID_INPUT.  Rows are copied in the largest of
+ * 16, 4 and 1 bytes that every address and row_bytes of a call's tensors are multiples of: a small tensor of odd
+ * rows is better given to a call of its own.
  * Streams, scratch and captured calls are as with rnn_ssm_*. */
 typedef struct rnn_beam* rnn_beam_t;
 /* beams B in [1, 32]; end_id: the token that ends a beam, -1 for none. */

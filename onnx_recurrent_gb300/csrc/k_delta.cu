@@ -34,7 +34,7 @@ struct PrepSmem {
 // T and P, the factors, and K and Q as the second launch wants them.  A block has a chunk of a head.  The two products
 // [K; Q] K^T are small (a twentieth of all); they go through the warps' own matrix instructions.  T is
 // found by blocks: four of 16 by substitution, a thread a column, then twice T21 = -T22 (A21 T11).
-// Instruction issue bounds it, and its eight barriers: 4096 chunks of 64 x 128 in bf16 take 159 us, 0.36 GB at 2.3 TB/s, with
+// Instruction issue bounds it, and its eight barriers: 4096 chunks of 64 x 128 in bf16 take 157 us, 0.36 GB at 2.3 TB/s, with
 // three blocks a multiprocessor (75 KB of shared memory each).
 template <typename T, int DKB, int KP>
 __global__ void __launch_bounds__(kThreads, 3) delta_prep_kernel(const DeltaParams p, unsigned char* keys, unsigned char* mats)
@@ -263,8 +263,8 @@ __global__ void __launch_bounds__(kThreads, 3) delta_prep_kernel(const DeltaPara
 //   warps 10, 11 (16-bit types): a step a thread, lay V out by columns before it is wanted and write Y's rows, 16
 //     bytes at a time where they are aligned.
 // The latency of a chunk's chain bounds it: products, tensor memory to registers, parts, and back, some 8200 clocks a chunk of
-// 128 x 128, of which the tensor cores work 15 %.  128 chains of 32 chunks that keep for their gradient take 209 us (0.77 GB
-// at 3.7 TB/s), 144 segments of 29 that do not 142 us.
+// 128 x 128, of which the tensor cores work 15 %.  128 chains of 32 chunks that keep for their gradient take 220 us (0.77 GB
+// at 3.5 TB/s; 209 with first parts on a grid of 2^-11, which are cheaper to form and lose small values), 144 segments of 29 that do not 151 us.
 template <int DKB>
 struct Columns {     // of tensor memory
     static constexpr uint32_t dS = 0, S = DKB * 64, R = 2 * DKB * 64, U = R + 64, U2 = U + 64, QS = U2 + 64, PU = R;

@@ -360,11 +360,11 @@ void go(const NormParams& p, const NormGradParams* g, int64_t blocks, cudaStream
     norm_grad_kernel<S, false><<<(unsigned)blocks, S::threads, 0, s>>>(*g);
 }
 
-// A few rows: many threads a row, for its latency (96 rows of 2048: 3.2 us with 256 threads).  Many: 32 values a thread, their
-// weights from the first-level cache, in flight together, four blocks a multiprocessor (16384 x 2048 bf16: 29 us with 64
-// threads a row, 33 with three blocks; 8 values a thread with their weights in registers 42 to 50 us, whatever the rows at
-// once and blocks; 64 values 39 us).  The gradient has 8 or 16
-// values a thread, for its sums (the same case 51 us; 16 values and 128 threads a row, two rows a block, 86).
+// A few rows: many threads a row, for its latency (96 rows of 2048: 3.6 us with 256 threads).  Many: 32 values a thread, their
+// weights from the first-level cache, in flight together, four blocks a multiprocessor (16384 x 2048 bf16: 30.5 us with 64
+// threads a row; 8 values a thread with their weights in registers took 1.4 to 1.7 times as long, whatever the rows at
+// once and blocks, 64 values 1.3 times, three blocks 1.1 times).  The gradient has 8 or 16
+// values a thread, for its sums (the same case 52.5 us; 16 values and 128 threads a row, two rows a block, 1.7 times that).
 template <typename T, int VEC>
 void by_size(const NormParams& p, const NormGradParams* g, cudaStream_t s)
 {
