@@ -83,7 +83,7 @@ def chunks(Q, K, V, g, beta, state, dY, d_state, scale):
     return out
 
 
-def plain_errors(ins, want, size, orders=4):
+def plain_errors(ins, want, size, orders=4, forms=(steps, chunks)):
     """Of each output, the error of its groups in norm; `ins` are the eight tensors of `steps`, and the scale."""
     *tensors, scale = ins
     total = {}
@@ -93,7 +93,7 @@ def plain_errors(ins, want, size, orders=4):
         Q, K, V, decay, beta, state, dY, d_state = (t.float() for t in tensors)
         turned = (Q[..., keys], K[..., keys], V[..., values], decay, beta, state[..., keys, :][..., values], dY[..., values],
                   d_state[..., keys, :][..., values], scale)
-        for f in (steps, chunks):
+        for f in forms:
             for name, t in f(*turned).items():
                 w = want[name]
                 if name in ("dQ", "dK"):
@@ -104,7 +104,7 @@ def plain_errors(ins, want, size, orders=4):
                     w = w[..., keys, :][..., values]
                 e = (groups(name, t.double(), size) - groups(name, w, size)).square().sum(1) / orders
                 total[f, name] = total.get((f, name), 0) + e
-    return {name: torch.maximum(total[steps, name], total[chunks, name]).sqrt() for name in want}
+    return {name: torch.stack([total[f, name] for f in forms]).amax(0).sqrt() for name in want}
 
 
 def like_plain(name, got, want, plain, io_u=0.0, floor=0.0):

@@ -9,7 +9,7 @@ import torch
 
 import delta_ref64 as ref
 import onnx_recurrent_gb300 as orc
-from delta_plain32 import groups, like_plain, plain_errors, steps
+from delta_plain32 import chunks, groups, like_plain, plain_errors, steps
 
 pytestmark = pytest.mark.gpu
 DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
@@ -44,10 +44,10 @@ class Case:
         orc.rnn_delta_sync(self.plan)
         return {n: t.cpu() for n, t in dict(Y=Y, state=end, **out).items()}
 
-    def check(self, size, floor=0.0):
+    def check(self, size, floor=0.0, forms=(steps, chunks)):
         ins = [*self.ins, self.state, self.dY, self.d_state]
-        got, want = self.run(), steps(*(t.double() for t in ins), self.plan.scale)
-        plain = plain_errors([*ins, self.plan.scale], want, size)
+        got, want = self.run(), forms[-1](*(t.double() for t in ins), self.plan.scale)
+        plain = plain_errors([*ins, self.plan.scale], want, size, forms=forms)
         for name in want:
             io = self.io if name in ("Y", "dQ", "dK", "dV") else "f32"
             like_plain(name, groups(name, got[name].double(), size), groups(name, want[name], size), plain[name], ref.IO_U[io], floor)
@@ -57,6 +57,13 @@ class Case:
 @pytest.mark.parametrize("size", [(2, 200, 4, 2, 128, 128), (3, 130, 2, 2, 40, 72), (1, 300, 3, 1, 64, 200)], ids=str)
 def test_every_row_head_and_chunk_as_the_plain_form(size, io):
     Case(*size, io).check(64)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [(1, 4200, 2, 1, 24, 40), (1, 4400, 1, 1, 72, 130), (2, 5121, 3, 3, 8, 8)], ids=str)
+def test_every_chunk_of_long_rows_as_the_plain_form(size, io):
+    """Rows that are cut into segments (the plain form by chunks alone: its steps would take minutes)."""
+    Case(*size, io, decay=0.02).check(64, forms=(chunks,))
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
