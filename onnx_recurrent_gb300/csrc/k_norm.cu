@@ -12,6 +12,8 @@
 // Bytes bound both.  Blocks walk rows; in the gradient a thread keeps the sums over rows of its columns, which go to
 // scratch as one of few parts that are added in order.  (Several rows at once, or the next row's loads ahead, were no faster:
 // the registers cost as many blocks.)
+#include <cfloat>
+
 #include "norm_internal.h"
 #include "ssm_math.cuh"
 
@@ -160,8 +162,10 @@ __global__ void __launch_bounds__(S::threads, S::NV == 8 || (S::NV == 32 && S::V
                 }
         row_sums<S>(left, more);
         if (!in) continue;
-        const float c = over_d(left[0]), var = over_d(left[1]) - c * c;
-        const float rstd = 1.f / sqrtf((var < 0.f ? 0.f : var) + p.eps), off = -c * rstd;      // (a NaN stays)
+        const float c = over_d(left[0]), square = over_d(left[1]);
+        // (squares past fp32's range: an infinite variance, as it would be without c, and z = 0; a NaN stays)
+        const float var = square <= FLT_MAX ? fmaxf(square - c * c, 0.f) : square;
+        const float rstd = 1.f / sqrtf(var + p.eps), off = -c * rstd;
         if (p.stats && t == 0) {
             p.stats[2 * r] = mean + c;
             p.stats[2 * r + 1] = rstd;
