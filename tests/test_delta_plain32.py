@@ -6,6 +6,15 @@ import torch
 from delta_plain32 import chunks, groups, like_plain, plain_errors, steps
 
 
+@pytest.fixture(autouse=True)
+def one_thread():
+    """Thousands of small operations: threads of several test processes would wait for one another."""
+    threads = torch.get_num_threads()
+    torch.set_num_threads(1)
+    yield
+    torch.set_num_threads(threads)
+
+
 def _inputs(dY=1.0):
     g = torch.Generator().manual_seed(0)
     r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
