@@ -131,8 +131,6 @@ bool block_meets(wide off, wide len, const Nested& b, bool both)
 }
 bool share(const Laid& a, const Laid& b)
 {
-    auto empty = [](const Laid& x) { return !x.data || x.S < 1 || x.N < 1 || x.inner < 1; };
-    if (empty(a) || empty(b)) return false;
     const Nested na = nested(a), nb = nested(b);
     auto span = [](const Nested& x) { return x.far * (x.fars - 1) + x.near * (x.nears - 1) + x.inner; };
     const wide off = (wide)(uintptr_t)b.data - (wide)(uintptr_t)a.data;
@@ -151,11 +149,30 @@ bool share(const Laid& a, const Laid& b)
 template <int I, int O>
 rnn_status check_shared(const Laid (&in)[I], const Laid (&out)[O])
 {
+    // what nearly all calls come to: ranges that do not meet (an empty array's is empty)
+    struct Range {
+        uintptr_t lo, hi;
+    };
+    auto range = [](const Laid& x) {
+        if (!x.data || x.S < 1 || x.N < 1 || x.inner < 1) return Range{0, 0};
+        int64_t rows, steps, bytes;
+        uintptr_t end;
+        const bool past = __builtin_mul_overflow(x.bs, x.N - 1, &rows) || __builtin_mul_overflow(x.ss, x.S - 1, &steps) ||
+                          __builtin_add_overflow(rows, steps, &bytes) || __builtin_add_overflow(bytes, x.inner, &bytes) ||
+                          __builtin_mul_overflow(bytes, x.elem, &bytes) || __builtin_add_overflow((uintptr_t)x.data, (uintptr_t)bytes, &end);
+        return Range{(uintptr_t)x.data, past ? UINTPTR_MAX : end};
+    };
+    auto meet = [](const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; };
+    Range ins[I], outs[O];
+    for (int i = 0; i < I; ++i) ins[i] = range(in[i]);
     for (int o = 0; o < O; ++o) {
-        for (int i = 0; i < I; ++i)
-            if (!(o == 0 && i == 0) && share(out[o], in[i])) return fail(RNN_ERR_INVALID_ARGUMENT, "%s overlaps %s", out[o].name, in[i].name);
+        outs[o] = range(out[o]);
+        for (int i = o == 0; i < I; ++i)
+            if (meet(outs[o], ins[i]) && share(out[o], in[i]))
+                return fail(RNN_ERR_INVALID_ARGUMENT, "%s overlaps %s", out[o].name, in[i].name);
         for (int i = 0; i < o; ++i)
-            if (share(out[o], out[i])) return fail(RNN_ERR_INVALID_ARGUMENT, "%s overlaps %s", out[o].name, out[i].name);
+            if (meet(outs[o], outs[i]) && share(out[o], out[i]))
+                return fail(RNN_ERR_INVALID_ARGUMENT, "%s overlaps %s", out[o].name, out[i].name);
     }
     return RNN_OK;
 }
